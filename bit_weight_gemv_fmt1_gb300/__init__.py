@@ -36,6 +36,11 @@ class _Stats(ctypes.Structure):
     _fields_ = [("calls", ctypes.c_uint64), ("launches", ctypes.c_uint64), ("weight_bytes", ctypes.c_uint64)]
 
 
+class _MlaCache(ctypes.Structure):
+    _fields_ = [("dtype", _int), ("latent", _int), ("rope", _int), ("page_size", _int), ("n_pages", ctypes.c_int64),
+                ("rows", _vp), ("scales", _vp)]
+
+
 class _Expert(ctypes.Structure):
     _fields_ = [("gate", _vp), ("up", _vp), ("down", _vp)]
 
@@ -60,6 +65,13 @@ _lib.coli_expert_table_free.restype = None
 _lib.coli_moe_block_t.argtypes = [_vp, _int, _vp, _vp, _vp, _int, _vp, _vp]
 _lib.coli_moe_topk.argtypes = [_vp, _vp, _int, _int, _int, ctypes.c_float, _int, ctypes.c_float, _vp, _vp, _vp]
 _lib.coli_moe_router.argtypes = [_vp, _int, _vp, _vp, _int, ctypes.c_float, _int, ctypes.c_float, _vp, _vp, _vp]
+_f = ctypes.c_float
+_lib.coli_mla_query.argtypes = [_vp, _i64, _int, _int, _int, _int, _vp, _vp, _int, _int, _int, _vp, _i64, _int, _vp, _i64, _vp]
+_lib.coli_mla_append.argtypes = [_vp, _vp, _i64, _int, _vp, _f, _vp, _vp, _int, _int, _vp, _vp]
+_lib.coli_mla_read.argtypes = [_vp, _vp, _i64, _int, _vp, _int, _int, _vp, _i64, _vp]
+_lib.coli_mla_attend.argtypes = [_vp, _int, _vp, _vp, _int, _int, _int, _vp, _i64, _vp, _f, _int, _vp, _vp, _vp]
+_lib.coli_mla_prefill.argtypes = [_int, _vp, _i64, _vp, _i64, _vp, _i64, _int, _int, _int, _vp, _vp, _int, _int, _int, _int, _f,
+                                  _int, _vp, _vp, _vp]
 _lib.coli_sync_check.argtypes = [_vp]
 _lib.coli_get_stats.argtypes = [ctypes.POINTER(_Stats)]
 _lib.coli_get_stats.restype = None
@@ -71,6 +83,7 @@ EXPORTS = ("coli_tensor_upload", "coli_tensor_upload_host", "coli_tensor_free", 
            "coli_matmul_rows", "coli_matmul_rows_t",
            "coli_moe_route", "coli_moe_topk", "coli_moe_router", "coli_moe_block", "coli_moe_block_noalloc",
            "coli_expert_table_create", "coli_expert_table_free", "coli_moe_block_t",
+           "coli_mla_query", "coli_mla_append", "coli_mla_read", "coli_mla_attend", "coli_mla_prefill",
            "coli_sync_check", "coli_last_error", "coli_get_stats", "coli_reset_stats", "coli_set_fail_after",
            "coli_version")
 
@@ -265,6 +278,167 @@ def moe_block_noalloc(x, table: ExpertTable, ids, w, y, dev_error, stream=None):
     _check(_lib.coli_moe_block_noalloc(_ptr(x), int(S), table.arr, len(table), _ptr(ids), _ptr(w), int(K), _ptr(y),
                                        _ptr(dev_error), _stream(stream)))
     return y
+
+
+COLI_F32, COLI_BF16, COLI_E4M3 = 0, 1, 2
+
+
+def _refuse(msg: str):
+    raise ColiError(COLI_EINVAL, msg)
+
+
+_DTYPES: dict = {}
+
+
+def _dtype(t) -> int:
+    """The library's element type of a tensor (COLI_EFMT for one it has not)."""
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: COLI_F32, torch.bfloat16: COLI_BF16, torch.float8_e4m3fn: COLI_E4M3})
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ColiError(COLI_EFMT, f"no element type for {t.dtype}")
+    return d
+
+
+def _typed(t, kind: str, name: str):
+    """t is a contiguous CUDA tensor of torch type `kind`."""
+    if str(t.dtype) != kind or not t.is_cuda or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous {kind} CUDA tensor")
+
+
+def _rows3(t, name: str) -> int:
+    """Stride of the rows of t [T, heads, n]: rows of one stride over tokens and heads, elements packed."""
+    T, H, n = t.shape
+    s = t.stride()
+    ld = s[1] if H > 1 else s[0] if T > 1 else n
+    if not t.is_cuda or (n > 1 and s[2] != 1) or (T > 1 and H > 0 and s[0] != H * ld):
+        _refuse(f"{name} must be a CUDA tensor whose [tokens, heads] rows have one stride")
+    return ld
+
+
+def _tokens(t, name: str) -> int:
+    """Token stride of t [T, ...] whose tokens are packed."""
+    if not t.is_cuda:
+        _refuse(f"{name} must be a CUDA tensor")
+    n = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != n:
+            _refuse(f"a token of {name} must be packed")
+        n *= size
+    return t.stride(0) if t.shape[0] > 1 else n
+
+
+class MlaCache:
+    """The paged latent cache of coli.h's coli_mla_cache over the caller's
+    tensors: rows [n_pages, page_size, latent + rope] bfloat16, or float8_e4m3fn
+    with scales float32 [n_pages, page_size].  Keeps the tensors alive."""
+
+    def __init__(self, rows, latent: int, rope: int, scales=None):
+        if rows.dim() != 3 or not rows.is_contiguous() or not rows.is_cuda or rows.shape[2] != latent + rope:
+            _refuse("rows must be a contiguous CUDA tensor [n_pages, page_size, latent + rope]")
+        d = _dtype(rows)
+        if d == COLI_E4M3:
+            if scales is None or tuple(scales.shape) != tuple(rows.shape[:2]):
+                _refuse("an e4m3 cache needs scales [n_pages, page_size]")
+            _typed(scales, "torch.float32", "scales")
+        elif scales is not None:
+            _refuse("only an e4m3 cache has scales")
+        self.rows, self.scales = rows, scales
+        self.latent, self.rope, self.page_size, self.n_pages = int(latent), int(rope), rows.shape[1], rows.shape[0]
+        self._c = _MlaCache(d, self.latent, self.rope, self.page_size, self.n_pages, rows.data_ptr(), _ptr(scales))
+        self._p = ctypes.addressof(self._c)
+
+
+def mla_query(q, pos, rot, out_nope, out_rope, interleaved: bool = False, stream=None):
+    """Split q [T, heads, nope + rope] into out_nope [T, heads, nope] and the rotated out_rope [T, heads, rope]
+    (f32 or bf16 each, possibly two parts of one tensor; out_nope None: nope = 0).  rot [n_pos, rope] = cos | sin."""
+    T, H, n = q.shape
+    R = out_rope.shape[2]
+    N = n - R
+    if str(q.dtype) != "torch.float32" or tuple(out_rope.shape[:2]) != (T, H) or pos.shape[0] != T or rot.shape[1] != R or \
+            (N if out_nope is None else tuple(out_nope.shape) != (T, H, N)):
+        _refuse("mla_query: q must be float32 [T, heads, nope + rope] and the others must match it")
+    _typed(pos, "torch.int32", "pos")
+    _typed(rot, "torch.float32", "rot")
+    _check(_lib.coli_mla_query(_ptr(q), _tokens(q, "q"), T, H, N, R, _ptr(pos), _ptr(rot), rot.shape[0], int(interleaved),
+                               0 if out_nope is None else _dtype(out_nope), _ptr(out_nope),
+                               0 if out_nope is None else _rows3(out_nope, "out_nope"),
+                               _dtype(out_rope), _ptr(out_rope), _rows3(out_rope, "out_rope"), _stream(stream)))
+    return out_nope, out_rope
+
+
+def mla_append(cache: MlaCache, kv, norm, eps: float, pos, rot, slots, interleaved: bool = False, stream=None):
+    """Norm (norm None: none), rotate, quantise and store kv [T, latent + rope] at slots [T] of the cache."""
+    T, n = kv.shape
+    if str(kv.dtype) != "torch.float32" or n != cache.latent + cache.rope or pos.shape[0] != T or slots.shape[0] != T or \
+            rot.shape[1] != cache.rope or (norm is not None and norm.shape[0] != cache.latent):
+        _refuse("mla_append: kv must be float32 [T, latent + rope] and the others must match it and the cache")
+    _typed(pos, "torch.int32", "pos")
+    _typed(slots, "torch.int64", "slots")
+    _typed(rot, "torch.float32", "rot")
+    if norm is not None:
+        _typed(norm, "torch.float32", "norm")
+    _check(_lib.coli_mla_append(cache._p, _ptr(kv), _tokens(kv, "kv"), T, _ptr(norm), float(eps), _ptr(pos), _ptr(rot),
+                                rot.shape[0], int(interleaved), _ptr(slots), _stream(stream)))
+
+
+def _pages(pages, n_seq: int) -> int:
+    if str(pages.dtype) != "torch.int32" or not pages.is_cuda or pages.shape[0] != n_seq or \
+            (pages.shape[1] > 1 and pages.stride(1) != 1):
+        _refuse("pages must be an int32 CUDA tensor [n_seq, n] with packed rows")
+    return pages.stride(0) if n_seq > 1 else pages.shape[1]
+
+
+def mla_read(cache: MlaCache, pages, cu, out, stream=None):
+    """Read the first cu[b+1] - cu[b] tokens of each sequence b back into out [T, latent + rope] (f32 or bf16)."""
+    n_seq = cu.shape[0] - 1
+    T, n = out.shape
+    if n != cache.latent + cache.rope:
+        _refuse("mla_read: out must have latent + rope columns")
+    _typed(cu, "torch.int32", "cu")
+    _check(_lib.coli_mla_read(cache._p, _ptr(pages), _pages(pages, n_seq), n_seq, _ptr(cu), T, _dtype(out), _ptr(out),
+                              _tokens(out, "out"), _stream(stream)))
+    return out
+
+
+def mla_attend(cache: MlaCache, q_latent, q_rope, pages, lens, scale: float, out, lse=None, stream=None):
+    """Absorbed attention of q_latent [n_seq, n_q, heads, latent] and q_rope [n_seq, n_q, heads, rope] over the cached
+    tokens (lens [n_seq] int32, the new ones included) into out [n_seq, n_q, heads, latent]; lse f32 [n_seq, n_q, heads]."""
+    B, n_q, H, n = q_latent.shape
+    if n != cache.latent or tuple(q_rope.shape) != (B, n_q, H, cache.rope) or out.shape != q_latent.shape or \
+            q_rope.dtype != q_latent.dtype or lens.shape[0] != B or (lse is not None and tuple(lse.shape) != (B, n_q, H)):
+        _refuse("mla_attend: q_latent, q_rope, lens, out and lse must match one another and the cache")
+    if not (q_latent.is_contiguous() and q_rope.is_contiguous() and out.is_contiguous() and out.is_cuda and q_latent.is_cuda):
+        _refuse("mla_attend: q_latent, q_rope and out must be contiguous CUDA tensors")
+    _typed(lens, "torch.int32", "lens")
+    if lse is not None:
+        _typed(lse, "torch.float32", "lse")
+    _check(_lib.coli_mla_attend(cache._p, _dtype(q_latent), _ptr(q_latent), _ptr(q_rope), B, n_q, H, _ptr(pages),
+                                _pages(pages, B), _ptr(lens), float(scale), _dtype(out), _ptr(out), _ptr(lse), _stream(stream)))
+    return out
+
+
+def mla_prefill(q, kv, k_rope, cu_q, cu_k, scale: float, out, lse=None, stream=None):
+    """Causal attention of packed sequences: q [Tq, heads, nope + rope], kv [Tk, heads, nope + v], k_rope [Tk, rope]
+    (all bf16 or all f32) into out [Tq, heads, v]; cu_q, cu_k int32 [n_seq + 1]; lse f32 [Tq, heads]."""
+    Tq, H, dk = q.shape
+    Tk, R, V = kv.shape[0], k_rope.shape[1], out.shape[2]
+    N = dk - R
+    if tuple(kv.shape[1:]) != (H, N + V) or k_rope.shape[0] != Tk or tuple(out.shape[:2]) != (Tq, H) or \
+            cu_q.shape != cu_k.shape or kv.dtype != q.dtype or k_rope.dtype != q.dtype or \
+            (lse is not None and tuple(lse.shape) != (Tq, H)):
+        _refuse("mla_prefill: q, kv, k_rope, cu_q, cu_k, out and lse must match one another")
+    if not (out.is_contiguous() and out.is_cuda):
+        _refuse("mla_prefill: out must be a contiguous CUDA tensor")
+    _typed(cu_q, "torch.int32", "cu_q")
+    _typed(cu_k, "torch.int32", "cu_k")
+    if lse is not None:
+        _typed(lse, "torch.float32", "lse")
+    _check(_lib.coli_mla_prefill(_dtype(q), _ptr(q), _tokens(q, "q"), _ptr(kv), _tokens(kv, "kv"), _ptr(k_rope),
+                                 _tokens(k_rope, "k_rope"), Tq, Tk, cu_q.shape[0] - 1, _ptr(cu_q), _ptr(cu_k), H, N, R, V,
+                                 float(scale), _dtype(out), _ptr(out), _ptr(lse), _stream(stream)))
+    return out
 
 
 def sync_check(stream=None):

@@ -254,6 +254,20 @@ int set_last_error(int code, const char *msg) { return fail(code, "%s", msg); }
 void clear_last_error() { g_msg[0] = 0; }
 int injected_gate() { return injected(); }
 void count_call(int launches, uint64_t weight_bytes) { count(launches, weight_bytes); }
+
+int device_info(cudaStream_t st, size_t bytes, DevInfo *out) {
+    DeviceState *ds = nullptr;
+    if (int rc = device_state(&ds)) return rc;
+    out->err = ds->err;
+    out->n_sm = ds->n_sm;
+    out->scratch = nullptr;
+    if (bytes) {
+        Workspace *ws = nullptr;
+        if (int rc = workspace(ds, st, bytes, &ws)) return rc;
+        out->scratch = ws->buf;
+    }
+    return COLI_OK;
+}
 }  // namespace coli
 
 // =================================================================== ABI
@@ -1382,9 +1396,11 @@ int coli_sync_check(void *stream) {
         std::lock_guard<std::mutex> lk(ds->mu);
         for (auto &kv : ds->ws)
             if (kv.second.bar) cudaMemset(kv.second.bar, 0, kBarrierBytes);
-        return fail(COLI_ETIMEOUT, "a grid-wide wait in the expert block ran out of time");
+        return fail(COLI_ETIMEOUT, "a bounded device-side wait ran out of time");
     }
     if (word == DEV_ERR_BAD_ID) return fail(COLI_EINVAL, "a routing id was outside [-1, n_experts)");
+    if (word == DEV_ERR_BAD_INDEX)
+        return fail(COLI_EINVAL, "latent attention: a page, slot, position, length or offset was out of range");
     return fail(COLI_ECUDA, "device error word %d", word);
 }
 

@@ -47,7 +47,7 @@ namespace coli {
 
 // ------------------------------------------------------------------ errors
 // Device-side error codes recorded in the per-device error word.
-enum : int { DEV_ERR_NONE = 0, DEV_ERR_TIMEOUT = 1, DEV_ERR_BAD_ID = 2 };
+enum : int { DEV_ERR_NONE = 0, DEV_ERR_TIMEOUT = 1, DEV_ERR_BAD_ID = 2, DEV_ERR_BAD_INDEX = 3 };
 
 // ------------------------------------------------------------------ traits
 template <int FMT> struct Fmt;
@@ -777,6 +777,14 @@ void clear_last_error();
 int injected_gate();
 // Count one compute call with its launches and weight bytes (coli_get_stats).
 void count_call(int launches, uint64_t weight_bytes);
+// What the latent-attention entry points need of the device's state: the error
+// word, the SM count, and `bytes` of the stream's scratch (none for bytes = 0).
+struct DevInfo {
+    int *err;
+    int n_sm;
+    void *scratch;
+};
+int device_info(cudaStream_t st, size_t bytes, DevInfo *out);
 // Copy n expert descriptors, passed by value in kernel parameters, to the
 // device table dst (stream-ordered, no host memory involved).
 cudaError_t launch_table_fill(ExpertDesc *dst, const ExpertDesc *src, int n, cudaStream_t st);

@@ -345,10 +345,169 @@ int coli_moe_block_noalloc(const float *x, int S, const coli_expert *experts, in
                            const int32_t *ids, const float *w, int K, float *y, int32_t *dev_error,
                            void *stream);
 
+/*
+ * Latent attention (MLA): what a decoder layer computes between its q / kv_a
+ * projections (coli_matmul) with the kv_b absorption products (coli_matmul_rows
+ * and coli_matmul_rows_t above; PR #298 page, commit message on qt_addrow /
+ * qt_matvec_rows) and its o projection.  A token's keys and values of all heads
+ * are one cached row of latent + rope elements:
+ *   row = [ c (latent dims, normed) | k (rope dims, rotated, shared by the heads) ]
+ * In the absorbed form a head's query is q_latent (its no-position part times
+ * the key rows of kv_b: coli_matmul_rows_t) and q_rope (rotated):
+ *   s_t = scale * (q_latent . c_t + q_rope . k_t),  p = softmax(s),
+ *   out = sum_t p_t c_t, which coli_matmul_rows takes to the head's values.
+ * In the expanded form (prompts) every head has keys and values of its own,
+ * computed from the rows with kv_b.
+ */
+
+/* Element types of activations and caches. */
+enum {
+    COLI_F32 = 0,
+    COLI_BF16 = 1,
+    COLI_E4M3 = 2         /* FP8 E4M3 with one f32 scale per cached row */
+};
+
+/*
+ * A paged cache of latent rows in the caller's device memory.  Row `slot`
+ * (= page * page_size + offset) holds latent + rope elements; with COLI_E4M3 its
+ * values are e4m3(code) * scales[slot].
+ *   dtype      COLI_BF16 or COLI_E4M3.
+ *   latent     128, 256, 384 or 512.
+ *   rope       a multiple of 16 in 16..64.
+ *   page_size  tokens per page, a multiple of 16 in 16..65536.
+ *   n_pages    >= 1, n_pages * page_size <= 2^31 - 1.
+ *   rows       device [n_pages][page_size][latent + rope], 16-byte aligned.
+ *   scales     device f32 [n_pages][page_size] (COLI_E4M3; else ignored); finite, >= 0.
+ */
+typedef struct {
+    int dtype, latent, rope, page_size;
+    int64_t n_pages;
+    void *rows;
+    float *scales;
+} coli_mla_cache;
+
+/*
+ * The queries' split and rotation: q[t][h] = [ nope | rope ] ->
+ * out_nope[t][h] = the first part, out_rope[t][h] = the second part turned by
+ * the angles of position pos[t]: each pair (a, b) becomes
+ * (a*cos - b*sin, a*sin + b*cos), with the pairs (i, i + rope/2), or
+ * (2i, 2i+1) if interleaved != 0, i < rope/2.
+ *   q          device f32, token t at q + t * q_stride, [n_heads][nope + rope].
+ *   nope, rope multiples of 8 >= 0 and of 16 in 16..256.
+ *   pos        device int32 [T], each in [0, n_pos).
+ *   rot        device f32 [n_pos][rope]: cos of the rope/2 angles, then sin.
+ *   out_nope   device COLI_F32 or COLI_BF16 (dtype_nope); row r = t * n_heads + h
+ *              at element r * ld_nope.  Ignored when nope = 0.
+ *   out_rope   the same with dtype_rope, ld_rope.  The two may be parts of one
+ *              row [nope | rope] (ld_nope = ld_rope = nope + rope): the expanded form's q.
+ * f32 outputs are exact copies / one rounding per operation; bf16 rounds to nearest.
+ * All pointers 16-byte aligned, strides multiples of 8 elements.  T >= 0.  A
+ * position out of range is recorded for coli_sync_check and its rows are zero.
+ * Errors: COLI_EINVAL, COLI_EFMT (a dtype), COLI_ECUDA, COLI_EINJECTED.
+ */
+int coli_mla_query(const float *q, int64_t q_stride, int T, int n_heads, int nope, int rope,
+                   const int32_t *pos, const float *rot, int n_pos, int interleaved,
+                   int dtype_nope, void *out_nope, int64_t ld_nope,
+                   int dtype_rope, void *out_rope, int64_t ld_rope, void *stream);
+
+/*
+ * Write tokens into the cache: norm of the latent part, rotation of the shared
+ * key part and quantisation in one pass.  kv[t] = [ c | k ] (kv_a's output) ->
+ *   row = [ c * rsqrt(mean(c^2) + eps) * norm | k turned as in coli_mla_query ]
+ * stored at slots[t].  COLI_BF16 rounds each element to nearest.  COLI_E4M3
+ * stores scale = max|row| / 448 and code = e4m3(row / scale), to nearest; a row
+ * of zeros gets scale 0 and codes 0.
+ *   kv      device f32, token t at kv + t * kv_stride, [latent + rope].
+ *   norm    device f32 [latent], or NULL: the latent part is stored as it is.
+ *   eps     > 0 (ignored without norm).
+ *   pos, rot, n_pos, interleaved  as in coli_mla_query, with the cache's rope.
+ *   slots   device int64 [T]; -1 skips the token.  Equal slots in one call race.
+ * Pointers 16-byte aligned (pos: 4, slots: 8), kv_stride a multiple of 4.  T >= 0.
+ * A slot or position out of range is recorded for coli_sync_check and the token
+ * is not written.
+ * Errors: COLI_EINVAL, COLI_EFMT (the cache's dtype), COLI_ECUDA, COLI_EINJECTED.
+ */
+int coli_mla_append(const coli_mla_cache *cache, const float *kv, int64_t kv_stride, int T,
+                    const float *norm, float eps, const int32_t *pos, const float *rot, int n_pos,
+                    int interleaved, const int64_t *slots, void *stream);
+
+/*
+ * Read the first tokens of n_seq sequences back, one after another (e.g. to
+ * expand a cached prefix with kv_b): out row cu[b] + i = token i of sequence b,
+ * i < cu[b+1] - cu[b].
+ *   pages   device int32, sequence b's page ids at pages + b * pages_stride
+ *           (pages_stride >= 1 entries; only those its tokens need are read).
+ *   cu      device int32 [n_seq + 1], cu[0] = 0, ascending; rows >= cu[n_seq] are left alone.
+ *   T       rows of out, >= 0.
+ *   dtype   COLI_F32 (exact) or COLI_BF16 (rounded to nearest); out_stride in
+ *           elements, a multiple of 8, >= latent + rope; out 16-byte aligned.
+ * A page id outside [0, n_pages), or a sequence longer than its page list, is
+ * recorded for coli_sync_check and its rows are zero.
+ * Errors: COLI_EINVAL, COLI_EFMT, COLI_ECUDA, COLI_EINJECTED.
+ */
+int coli_mla_read(const coli_mla_cache *cache, const int32_t *pages, int64_t pages_stride, int n_seq,
+                  const int32_t *cu, int T, int dtype, void *out, int64_t out_stride, void *stream);
+
+/*
+ * Attention over the cache in the absorbed form, for the n_q newest tokens of
+ * each of n_seq sequences (n_q = 1: a decode step).  Query token j of sequence
+ * b sees the cached tokens t < lens[b] - (n_q - 1 - j) (lens counts the new
+ * tokens, whose rows are in the cache already).
+ *   out[b][j][h] = sum_t p_t c_t   (formulas above),  lse[b][j][h] = ln sum_t exp(s_t)
+ * A query that sees no token gives zeros and lse = -infinity.
+ *   q_latent  device [n_seq][n_q][n_heads][latent], COLI_F32 or COLI_BF16 (dtype_q).
+ *   q_rope    device [n_seq][n_q][n_heads][rope], same type.
+ *   pages     as in coli_mla_read; lens[b] <= pages_stride * page_size.
+ *   lens      device int32 [n_seq], >= 0.
+ *   out       device [n_seq][n_q][n_heads][latent], COLI_F32 or COLI_BF16.
+ *   lse       device f32 [n_seq][n_q][n_heads], or NULL.
+ * The products take 16-bit operands, as the cache holds no more: q and the
+ * probabilities are rounded to bf16 for a COLI_BF16 cache, to f16 (q scaled by
+ * a power of two per head) for a COLI_E4M3 one; sums, maxima and the
+ * softmax's denominator are f32.  Rows past a sequence's length, and pages
+ * past its last, are never used: they may hold anything.
+ * Pointers 16-byte aligned (pages, lens, lse: 4).  n_seq >= 0, n_q >= 1, 1 <= n_heads <= 1024,
+ * n_q * n_heads <= 65536.  A page id outside [0, n_pages) among the needed ones, or a length out
+ * of range, is recorded for coli_sync_check; that sequence's output is unspecified.
+ * Errors: COLI_EINVAL, COLI_EFMT, COLI_ENOMEM (scratch), COLI_ECUDA, COLI_EINJECTED.
+ */
+int coli_mla_attend(const coli_mla_cache *cache, int dtype_q, const void *q_latent, const void *q_rope,
+                    int n_seq, int n_q, int n_heads, const int32_t *pages, int64_t pages_stride,
+                    const int32_t *lens, float scale, int dtype_out, void *out, float *lse, void *stream);
+
+/*
+ * Causal attention of whole prompts in the expanded form, over n_seq sequences
+ * packed one after another.  Sequence b has query rows cu_q[b] .. cu_q[b+1] and
+ * key rows cu_k[b] .. cu_k[b+1]; its last query lines up with its last key:
+ * query i sees the keys j <= i + n_k - n_q (earlier keys: a cached prefix).
+ *   s_ij = scale * (q_nope_i . k_nope_j + q_rope_i . k_rope_j), out_i = sum_j softmax(s_i)_j v_j
+ * A query that sees no key gives zeros and lse = -infinity.
+ *   q       device [Tq][n_heads][nope + rope], rotated (coli_mla_query); token stride q_stride.
+ *   kv      device [Tk][n_heads][nope + v]: kv_b's product, a head's key part then its
+ *           values; token stride kv_stride.
+ *   k_rope  device [Tk][rope], rotated, shared by the heads; token stride kr_stride.
+ *   dtype   COLI_BF16, or COLI_F32: the three are then rounded to bf16 in scratch first.
+ *   nope, rope, v   64 or 128; a multiple of 16 in 16..64; 64 or 128.
+ *   cu_q, cu_k      device int32 [n_seq + 1], ascending from 0 to Tq / Tk.
+ *   out     device [Tq][n_heads][v], COLI_F32 or COLI_BF16; lse device f32 [Tq][n_heads] or NULL.
+ * Products have bf16 operands (the probabilities are rounded to bf16) and f32
+ * sums; maxima and denominators are f32.  A value of another sequence never
+ * reaches the result; a non-finite v row that a query's own sequence masks may.
+ * Pointers 16-byte aligned (cu, lse: 4); strides in elements, multiples of 8.
+ * Tq, Tk >= 0, n_seq >= 0, 1 <= n_heads <= 1024.  Offsets outside [0, Tq] / [0, Tk] or descending are
+ * recorded for coli_sync_check; those sequences' outputs are unspecified.
+ * Errors: COLI_EINVAL, COLI_EFMT, COLI_ENOMEM, COLI_ECUDA, COLI_EINJECTED.
+ */
+int coli_mla_prefill(int dtype, const void *q, int64_t q_stride, const void *kv, int64_t kv_stride,
+                     const void *k_rope, int64_t kr_stride, int Tq, int Tk, int n_seq,
+                     const int32_t *cu_q, const int32_t *cu_k, int n_heads, int nope, int rope, int v,
+                     float scale, int dtype_out, void *out, float *lse, void *stream);
+
 /* Synchronize `stream`, then report (and clear) any error the library's
  * kernels recorded on this device: COLI_ETIMEOUT for a bounded wait that ran
- * out, COLI_EINVAL for an out-of-range routing id, COLI_ECUDA for a CUDA
- * error.  Returns COLI_OK otherwise. */
+ * out, COLI_EINVAL for an out-of-range routing id or an out-of-range page,
+ * slot, position, length or offset of the latent attention, COLI_ECUDA for a
+ * CUDA error.  Returns COLI_OK otherwise. */
 int coli_sync_check(void *stream);
 
 /* Message for the last error on the calling thread ("" if none). */
