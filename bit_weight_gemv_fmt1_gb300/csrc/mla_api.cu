@@ -172,7 +172,10 @@ int attend(const coli_mla_cache *cache, int dtype_q, const void *q_latent, const
     if (n_seq < 0 || n_q < 1 || H < 1 || H > 1024 || (int64_t)n_q * H > 65536)
         return bad(COLI_EINVAL, "need n_seq >= 0, n_q >= 1, 1 <= n_heads <= 1024, n_q * n_heads <= 65536 (got %d, %d, %d)", n_seq, n_q, H);
     if ((int64_t)n_seq * n_q * H > (1LL << 31) - 1) return bad(COLI_EINVAL, "n_seq * n_q * n_heads is too large");
-    if (pages_stride < 1) return bad(COLI_EINVAL, "pages_stride must be >= 1 (got %lld)", (long long)pages_stride);
+    if (pages_stride < 1 || pages_stride > (1LL << 31) - 1)
+        return bad(COLI_EINVAL, "pages_stride must be in 1..2^31-1 (got %lld)", (long long)pages_stride);
+    if ((pages_stride * a.c.page / 128 + 1) * n_seq > (1LL << 31) - 1)
+        return bad(COLI_EINVAL, "n_seq * pages_stride * page_size is too large");
     if (!(scale == scale)) return bad(COLI_EINVAL, "scale must not be NaN");
     if (n_seq) {
         if (int rc = need(q_latent, 16, "q_latent")) return rc;
@@ -185,8 +188,6 @@ int attend(const coli_mla_cache *cache, int dtype_q, const void *q_latent, const
     }
     if (int rc = injected_gate()) return rc;
     if (!n_seq) return COLI_OK;
-    DevInfo d;
-    if (int rc = device_info((cudaStream_t)stream, 0, &d)) return rc;
     a.q_latent = q_latent;
     a.q_rope = q_rope;
     a.q_bf16 = dtype_q == COLI_BF16;
@@ -200,8 +201,14 @@ int attend(const coli_mla_cache *cache, int dtype_q, const void *q_latent, const
     a.scale = scale;
     a.out = out;
     a.lse = lse;
+    DevInfo d;
+    if (int rc = device_info((cudaStream_t)stream, 0, &d)) return rc;
+    if (const size_t bytes = mla_attend_scratch(a, d.n_sm))
+        if (int rc = device_info((cudaStream_t)stream, bytes, &d)) return rc;
     a.err = d.err;
-    return launched(launch_mla_attend(a, (cudaStream_t)stream), "coli_mla_attend", 1);
+    int n = 0;
+    const cudaError_t e = launch_mla_attend(a, d.scratch, d.n_sm, (cudaStream_t)stream, &n);
+    return launched(e, "coli_mla_attend", n);
 }
 
 int prefill(int dtype, const void *q, int64_t q_stride, const void *kv, int64_t kv_stride, const void *k_rope, int64_t kr_stride,
