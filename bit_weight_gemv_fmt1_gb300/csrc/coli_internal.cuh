@@ -171,6 +171,12 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
     return D.f;
 }
 
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+    F2U A{a}, B{b}, D;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(D.u) : "l"(A.u), "l"(B.u));
+    return D.f;
+}
+
 __device__ __forceinline__ void ffma2(float2 &acc, float2 a, float2 b) {
     F2U A{a}, B{b}, C{acc};
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(C.u) : "l"(A.u), "l"(B.u));

@@ -51,7 +51,7 @@ int check_cache(const coli_mla_cache *c, MlaCache *out) {
     if (int rc = need(c->rows, 16, "cache rows")) return rc;
     out->e4m3 = c->dtype == COLI_E4M3;
     if (out->e4m3)
-        if (int rc = need(c->scales, 4, "cache scales")) return rc;
+        if (int rc = need(c->scales, 16, "cache scales")) return rc;
     out->rows = (uint8_t *)c->rows;
     out->scales = out->e4m3 ? c->scales : nullptr;
     out->L = c->latent;

@@ -1,0 +1,164 @@
+// mla_attend.cuh -- what the two kernels of the absorbed attention share: how
+// the work is cut, the walk over a CTA's tiles, token slots and query rows.
+#pragma once
+
+#include "mla.cuh"
+#include "tcgen05.cuh"
+
+namespace coli {
+
+constexpr int kTile = 128;               // tokens per tile
+constexpr int kSoft = 256;               // softmax threads
+constexpr float kNone = -3e38f;          // reference of a column that has none yet
+
+struct AttendPlan {
+    int cols;              // query rows (columns) of a CTA
+    int n_rows;            // query rows of a sequence: n_q * H
+    int nrb;               // blocks of `cols` rows
+    int n_groups, n_slots; // pieces of the line of tiles; CTAs of a group
+    float *part;           // [n_groups * nrb * 2][cols][L] partial O, then [..][cols][2] m, l
+    float *part_ml;
+    int *prefix;           // [n_seq + 1] tiles before each sequence
+    int pbox;              // tokens per copy box
+    long long timeout_ns;
+};
+
+// The piece of a CTA's group: tiles [u0, u1), beginning in sequence b0 with p0 tiles before it.
+struct Piece {
+    int u0, u1, b0, p0;
+};
+
+__device__ __forceinline__ int seq_len(const MlaAttendArgs &a, int b) {
+    const int n = a.lens[b];
+    return n < 0 || n > a.pages_stride * a.c.page ? 0 : n;
+}
+__device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTile - 1) / kTile : 1; }
+
+// The tiles of a CTA's piece, for each of its row blocks, in order.
+struct Walk {
+    const MlaAttendArgs &a;
+    const AttendPlan &g;
+    const Piece &s;
+    int rb, u, b, p, T, len;
+    __device__ Walk(const MlaAttendArgs &a_, const AttendPlan &g_, const Piece &s_, int slot) : a(a_), g(g_), s(s_), rb(slot) { start(); }
+    __device__ void start() {
+        u = s.u0;
+        b = s.b0;
+        p = s.p0;
+        if (u < s.u1) {
+            len = seq_len(a, b);
+            T = tiles_of(len);
+        }
+    }
+    __device__ bool valid() const { return rb < g.nrb && u < s.u1; }
+    __device__ int tile() const { return u - p; }
+    __device__ bool first() const { return u == s.u0 || u == p; }              // of this CTA's part of the sequence
+    __device__ bool last() const { return u + 1 == s.u1 || u + 1 == p + T; }
+    __device__ bool whole() const { return p >= s.u0 && p + T <= s.u1; }       // the piece holds all of the sequence
+    __device__ int which() const { return p < s.u0 ? 0 : 1; }                  // which of the piece's two partial results
+    __device__ void next() {
+        if (++u == s.u1) {
+            rb += g.n_slots;
+            start();
+        } else if (u == p + T) {
+            p += T;
+            len = seq_len(a, ++b);
+            T = tiles_of(len);
+        }
+    }
+};
+
+// Slot of a token, -1 past the length or for a bad page.
+__device__ __forceinline__ int token_slot(const MlaAttendArgs &a, int b, int t, int len) {
+    if (t >= len) return -1;
+    const int pi = t / a.c.page;
+    const int id = a.pages[(long long)b * a.pages_stride + pi];
+    if (id < 0 || id >= a.c.n_pages) {
+        mla_bad_index(a.err);
+        return -1;
+    }
+    return id * a.c.page + (t - pi * a.c.page);
+}
+
+// Order-preserving map of floats to ints (its own inverse up to the sign rule).
+__device__ __forceinline__ int float_key(float f) {
+    const int i = __float_as_int(f);
+    return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+
+__device__ __forceinline__ void store_out(const MlaAttendArgs &a, long long e, float v) {
+    if (a.out_bf16) reinterpret_cast<__nv_bfloat16 *>(a.out)[e] = __float2bfloat16_rn(v);
+    else reinterpret_cast<float *>(a.out)[e] = v;
+}
+
+// Query row r of sequence b, as this lane's units of 8 elements: lane and lane
+// + 32 of the latent part, lane of the rope part (zeros where there are none).
+template <bool QB>
+struct QueryRow {
+    static constexpr int W = QB ? 1 : 2;   // 16-byte words per unit
+    uint4 x[3][W];
+    __device__ __forceinline__ void load(const MlaAttendArgs &a, long long row, bool live, int lane) {
+        const int nu = a.c.L / 8, nr = a.c.R / 8;
+#pragma unroll
+        for (int k = 0; k < 3; k++) {
+            const int u = lane + 32 * (k == 1);
+            const bool ok = live && (k < 2 ? u < nu : lane < nr);
+            const long long e = k < 2 ? row * a.c.L + 8 * u : row * a.c.R + 8 * lane;
+            const uint8_t *src = reinterpret_cast<const uint8_t *>(k < 2 ? a.q_latent : a.q_rope) + e * (QB ? 2 : 4);
+#pragma unroll
+            for (int w = 0; w < W; w++) x[k][w] = ok ? __ldg(reinterpret_cast<const uint4 *>(src) + w) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    __device__ __forceinline__ void unit(int k, float (&v)[8]) const {
+        const uint32_t w[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w, x[k][W - 1].x, x[k][W - 1].y, x[k][W - 1].z, x[k][W - 1].w};
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const float2 t = QB ? bf16x2_f32x2(w[q]) : make_float2(__uint_as_float(w[2 * q]), __uint_as_float(w[2 * q + 1]));
+            v[2 * q] = t.x;
+            v[2 * q + 1] = t.y;
+        }
+    }
+};
+
+// Warp 0: the tiles of all sequences, this group's piece of them, and (block 0) the prefix table.
+__device__ __forceinline__ void find_piece(const MlaAttendArgs &a, const AttendPlan &g, int group, int lane, Piece &out) {
+    int total = 0;
+    for (int b = lane; b < a.n_seq; b += 32) {
+        const int n = a.lens[b];
+        if (n < 0 || n > a.pages_stride * a.c.page) mla_bad_index(a.err);
+        total += tiles_of(seq_len(a, b));
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    const int chunk = (total + g.n_groups - 1) / g.n_groups;
+    const int u0 = min(total, group * chunk), u1 = min(total, u0 + chunk);
+    int run = 0;
+    for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
+        const int b = b0 + lane;
+        const int T = b < a.n_seq ? tiles_of(seq_len(a, b)) : 0;
+        int incl = T;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const int p = run + incl - T;
+        if (b < a.n_seq && p <= u0 && u0 < p + T) {
+            out.b0 = b;
+            out.p0 = p;
+        }
+        if (g.prefix && blockIdx.x == 0 && b < a.n_seq) g.prefix[b] = p;
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+        out.u0 = u0;
+        out.u1 = u1;
+        if (g.prefix && blockIdx.x == 0) g.prefix[a.n_seq] = total;
+    }
+}
+
+// The E4M3 kernel (mla_attend_e4m3.cu).
+cudaError_t launch_mla_attend_e4m3(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t st);
+// Tensor map of the cache's rows: boxes of `inner` elements x `pbox` rows, with that swizzle.
+cudaError_t mla_row_map(const MlaCache &c, int inner, int pbox, CUtensorMapSwizzle swizzle, CUtensorMap *out);
+
+}  // namespace coli

@@ -1,0 +1,444 @@
+// mla_attend_e4m3.cu -- attention over a paged E4M3 latent cache (absorbed
+// form).  mla_attend.cu explains the products, the softmax with its running
+// reference and how the work is cut; this kernel differs in that the codes are
+// never converted.
+//
+// The tensor cores multiply E4M3 by E4M3, exactly, into f32.  What faces the
+// codes is split into E4M3 terms, each 2^5 finer than the one before:
+//   q  (times a power of two per row)  = q0 + 2^-5 q1             (a bf16 value exactly)
+//   P  = weight * row scale            = p0 + 2^-5 p1 + 2^-10 p2  (to 2^-13 of the value)
+// Terms are columns side by side, S^T [128 tokens][2 NH] and O^T [128 dims][3 NH]
+// for NH = 16 or 32 query rows, and are added in f32 when they leave TMEM.  An
+// MMA reads 4 KB of codes for 128 x 32 values whatever its N, so the terms cost
+// little: at NH = 32 a tile takes 18 MMAs of N = 64 and 16 of N = 96, about 1760
+// cycles, and its bytes enter shared memory once (converting to f16 instead read
+// and wrote them twice more and was bound by that: 10400 cycles for 64 rows).
+//
+// Tiles are 73 KB, so two fit: the scores of tile i + 1 are computed while the
+// softmax of tile i runs.  Warps: 0-7 softmax and output (two threads per
+// token, each half the rows), 8 MMA issue, 9 bulk copies of codes and scales.
+#include "mla_attend.cuh"
+
+namespace coli {
+
+namespace {
+
+constexpr uint32_t kBlk8 = kTile * 128;  // 128 tokens x 128 codes, 128-byte swizzle
+constexpr uint32_t kRope8 = kTile * 64;  // 128 tokens x 64 codes, 64-byte swizzle
+constexpr uint32_t kP8 = kTile * 128;    // P [128 tokens][3 NH], rows of 128 bytes
+constexpr float kHead8 = 4.f;            // log2 of the largest weight of a fresh reference
+constexpr float kLimit8 = 8.f;           // log2 of the weight that moves the reference (E4M3 ends at 448)
+constexpr float kFine = 32.f;            // a term's step against the next
+
+struct Shared8 {
+    uint64_t k_full[2], k_empty[2], s_full[2], p_full[2];
+    uint32_t tmem;
+    int abort;
+    Piece piece;
+    alignas(16) float scale[2][kTile];   // written by bulk copies
+    alignas(16) float f[32];
+    alignas(16) float m[2][32];          // minus the reference
+    float linv[32], r[32];
+    int limit[32];
+    float red[4][32];
+};
+
+// 64-byte swizzled K-major operand: atoms of 8 rows x 64 bytes.
+__device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(512 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)4 << 61;
+}
+__device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ float2 e4m3x2_f32x2(uint32_t two) {
+    const uint32_t h = e4m3x2_f16x2(two);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+// v -> its E4M3 pair (16 bits); v becomes the remainder times 2^5.
+__device__ __forceinline__ uint32_t take_term(float2 &v) {
+    const uint32_t u = pack_e4m3(v.x, v.y);
+    float2 r = fmul2(v, make_float2(kFine, kFine));
+    ffma2(r, e4m3x2_f32x2(u), make_float2(-kFine, -kFine));
+    v = r;
+    return u;
+}
+
+// This warp's query rows of a block -> E4M3 terms [L/128 blocks][2 NH][128], then [2 NH][64] (rope).
+template <int NH, bool QB>
+__device__ __forceinline__ void load_queries8(const MlaAttendArgs &a, const AttendPlan &g, Shared8 &s, uint8_t *qsm, int b, int rb,
+                                              int len, int warp, int lane) {
+    constexpr int RB = QB ? 4 : 2;
+    const int nu = a.c.L / 8, nru = (a.c.R + 31) / 32 * 4;
+    uint8_t *rope = qsm + (a.c.L / 128) * (2 * NH * 128);
+#pragma unroll 1
+    for (int c0 = warp; c0 < NH; c0 += 8 * RB) {
+        QueryRow<QB> x[RB];
+#pragma unroll
+        for (int i = 0; i < RB; i++) {
+            const int r = rb * NH + c0 + 8 * i;
+            x[i].load(a, (long long)b * g.n_rows + r, c0 + 8 * i < NH && r < g.n_rows, lane);
+        }
+#pragma unroll
+        for (int i = 0; i < RB; i++) {
+            const int c = c0 + 8 * i, r = rb * NH + c;
+            if (c >= NH) break;
+            float v[3][8], mx = 0.f;
+#pragma unroll
+            for (int k = 0; k < 3; k++) {
+                x[i].unit(k, v[k]);
+#pragma unroll
+                for (int q = 0; q < 8; q++) mx = fmaxf(mx, fabsf(v[k][q]));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            // times 2^k2: the largest magnitude in [2^7, 2^8)
+            const int ex = (int)((__float_as_uint(mx) >> 23) & 0xFF) - 127;
+            const int k2 = mx > 0.f && ex < 128 ? min(7 - ex, 120) : 0;
+            const float up = __int_as_float((k2 + 127) << 23);
+#pragma unroll
+            for (int k = 0; k < 3; k++) {
+                uint32_t t[2][2];
+#pragma unroll
+                for (int q = 0; q < 2; q++) {
+                    float2 y0 = make_float2(v[k][4 * q] * up, v[k][4 * q + 1] * up), y1 = make_float2(v[k][4 * q + 2] * up, v[k][4 * q + 3] * up);
+                    t[0][q] = take_term(y0);
+                    t[0][q] |= take_term(y1) << 16;
+                    t[1][q] = pack_e4m3(y0.x, y0.y) | pack_e4m3(y1.x, y1.y) << 16;
+                }
+                const int u = k < 2 ? lane + 32 * k : lane;
+                if (k < 2 ? u >= nu : u >= nru) continue;
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    const int row = j * NH + c, ch = (u & 15) >> 1;
+                    uint8_t *d = k < 2 ? qsm + (u >> 4) * (2 * NH * 128) + row * 128 + ((ch ^ (row & 7)) << 4)
+                                       : rope + row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
+                    *reinterpret_cast<uint2 *>(d + 8 * (u & 1)) = make_uint2(t[j][0], t[j][1]);
+                }
+            }
+            if (lane == 0) {
+                s.f[c] = a.scale * 1.4426950408889634f * __int_as_float((127 - k2) << 23);
+                s.limit[c] = r < g.n_rows ? len - (a.n_q - 1 - r / a.H) : 0;
+            }
+        }
+    }
+}
+
+template <int NH>
+__global__ void __launch_bounds__(320, 1)
+    mla_attend_e4m3_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap rope_map, const MlaAttendArgs a,
+                           const AttendPlan g) {
+    constexpr int HC = NH / 2;             // rows per softmax thread
+    extern __shared__ uint8_t raw[];
+    __shared__ Shared8 s;
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    uint8_t *sm = raw + (base - smem_addr(raw));
+    // the shuffles tell the compiler that these are the same in a whole warp, so that MMA operands live in uniform registers
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int np = a.c.L / 128;
+    const uint32_t stage = np * kBlk8 + kRope8;
+    const uint32_t q_off = 2 * stage, p_off = q_off + np * (2 * NH * 128) + 2 * NH * 64;
+    constexpr uint32_t kCols = 16 * NH, kO = 4 * NH;   // TMEM: two S of 2 NH columns, L/128 O of 3 NH
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 0) tmem_alloc(&s.tmem, kCols);
+    if (tid == 0) {
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&s.k_full[i], 1);
+            mbar_init(&s.k_empty[i], 1);
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.p_full[i], 8);
+        }
+        s.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    const int group = blockIdx.x / g.n_slots, slot = blockIdx.x - group * g.n_slots;
+    if (warp == 0) find_piece(a, g, group, lane, s.piece);
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
+    const uint64_t deadline = global_ns() + (uint64_t)g.timeout_ns;
+    volatile int *abort = &s.abort;
+    bool ok = true;                        // this thread's waits have all ended well
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!ok) return;
+        if (!warp_wait(bar, parity, deadline, abort, lane)) {
+            ok = false;
+            *abort = 1;
+            atomicCAS(a.err, 0, (int)DEV_ERR_TIMEOUT);
+        }
+    };
+
+    if (warp < 8) {
+        // ---------------------------------------------------------- softmax and output
+        const int wq = warp & 3, grp = warp >> 2;
+        const int t = 32 * wq + lane;                                   // token of the tile, and dim of an O block
+        const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
+        const int col0 = grp * HC;
+        float2 l[HC / 2];
+        int it = 0, cur = 0;
+        for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), it++) {
+            const int buf = it & 1;
+            if (w.first()) {
+                if (a.q_bf16) load_queries8<NH, true>(a, g, s, sm + q_off, w.b, w.rb, w.len, warp, lane);
+                else load_queries8<NH, false>(a, g, s, sm + q_off, w.b, w.rb, w.len, warp, lane);
+                if (tid < NH) s.m[cur][tid] = -kNone;
+#pragma unroll
+                for (int c = 0; c < HC / 2; c++) l[c] = make_float2(0.f, 0.f);
+                fence_async_smem();
+                named_sync(1, kSoft);
+                named_arrive(3, kSoft + 32);
+            }
+            const int tok = w.tile() * kTile + t;
+            // every row sees the whole tile: the first query's limit is the lowest
+            const bool full = (w.tile() + 1) * kTile <= w.len - (a.n_q - 1) && (w.rb + 1) * NH <= g.n_rows;
+            wait(&s.k_full[buf], (it >> 1) & 1);                        // the scales
+            wait(&s.s_full[buf], (it >> 1) & 1);
+            tc_after_sync();
+            const float st = tok < w.len ? s.scale[buf][t] : 0.f;
+            if ((w.tile() + 1) * kTile > w.len && tok >= w.len) {
+                // rows past the length may hold anything, and 0 * NaN is NaN
+                for (int k = grp; k < np; k += 2)
+#pragma unroll
+                    for (int u = 0; u < 8; u++) *reinterpret_cast<uint4 *>(sm + buf * stage + k * kBlk8 + t * 128 + 16 * u) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            // log2 of the row's scale; the floor gives rows of scale 0, which weigh in l alone, a reference too
+            const float lg = fmaxf(__log2f(st), -90.f);
+            const uint32_t s_at = lanes + buf * (2 * NH) + col0;
+            // l += sign * weights 2^min(x - m, 100), and P for sign > 0; true if a weight has outgrown P
+            auto add = [&](float sign) {
+                uint32_t v0[HC], v1[HC], pk[3][HC / 4];
+                tmem_ld(s_at, v0);
+                tmem_ld(s_at + NH, v1);
+                tmem_ld_wait();
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < HC; c += 2) {
+                    const float2 f = *reinterpret_cast<const float2 *>(&s.f[col0 + c]);
+                    float2 x = *reinterpret_cast<const float2 *>(&s.m[cur][col0 + c]);
+                    float2 y = make_float2(__uint_as_float(v0[c]), __uint_as_float(v0[c + 1]));
+                    ffma2(y, make_float2(__uint_as_float(v1[c]), __uint_as_float(v1[c + 1])), make_float2(1.f / kFine, 1.f / kFine));
+                    ffma2(x, fmul2(y, make_float2(st, st)), f);
+                    if (!full) {
+                        if (tok >= s.limit[col0 + c]) x.x = -INFINITY;
+                        if (tok >= s.limit[col0 + c + 1]) x.y = -INFINITY;
+                    }
+                    top = fmaxf(top, fmaxf(x.x, x.y));
+                    x = make_float2(ex2(fminf(x.x, 100.f)), ex2(fminf(x.y, 100.f)));
+                    l[c / 2] = fadd2(l[c / 2], sign > 0.f ? x : make_float2(-x.x, -x.y));
+                    if (sign > 0.f) {
+                        float2 p = fmul2(x, make_float2(st, st));
+                        const uint32_t p0 = take_term(p), p1 = take_term(p), p2 = pack_e4m3(p.x, p.y);
+                        const int sh = 8 * (c & 2), i = c / 4;
+                        pk[0][i] = c & 2 ? pk[0][i] | p0 << sh : p0;
+                        pk[1][i] = c & 2 ? pk[1][i] | p1 << sh : p1;
+                        pk[2][i] = c & 2 ? pk[2][i] | p2 << sh : p2;
+                    }
+                }
+                if (sign > 0.f)
+#pragma unroll
+                    for (int j = 0; j < 3; j++) {
+                        uint8_t *d = sm + p_off + buf * kP8 + t * 128;
+                        if constexpr (HC == 16)
+                            *reinterpret_cast<uint4 *>(d + (((2 * j + grp) ^ (t & 7)) << 4)) = make_uint4(pk[j][0], pk[j][1], pk[j][2], pk[j][3]);
+                        else
+                            *reinterpret_cast<uint2 *>(d + ((j ^ (t & 7)) << 4) + 8 * grp) = make_uint2(pk[j][0], pk[j][1]);
+                    }
+                return top + lg > kLimit8;
+            };
+            bool move = w.first();
+            if (!move) {
+                move = named_or(1, kSoft, add(1.f));
+                // taking the weights off again is exact to an ulp of the sums with them, which the new reference
+                // scales to 2^-24 of its own weights or less
+                if (move) add(-1.f);
+            }
+            if (move) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < HC; c0 += 8) {
+                    uint32_t v0[8], v1[8];
+                    tmem_ld(s_at + c0, v0);
+                    tmem_ld(s_at + NH + c0, v1);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 8; c++) {
+                        float x = fmaf(__uint_as_float(v1[c]), 1.f / kFine, __uint_as_float(v0[c]));
+                        x = fmaf(x * st, s.f[col0 + c0 + c], lg);
+                        if (!full && tok >= s.limit[col0 + c0 + c]) x = -INFINITY;
+                        const int k = __reduce_max_sync(0xffffffffu, float_key(x));
+                        if (lane == 0) s.red[wq][col0 + c0 + c] = __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF));
+                    }
+                }
+                named_sync(1, kSoft);
+                if (tid < NH) {
+                    const float old = -s.m[cur][tid];
+                    const float x = fmaxf(fmaxf(s.red[0][tid], s.red[1][tid]), fmaxf(s.red[2][tid], s.red[3][tid]));
+                    const float now = fmaxf(old, x - kHead8);
+                    s.m[cur ^ 1][tid] = -now;
+                    s.r[tid] = ex2(old - now);
+                }
+                named_sync(1, kSoft);
+                cur ^= 1;
+                if (!w.first()) {
+#pragma unroll
+                    for (int c = 0; c < HC / 2; c++) l[c] = fmul2(l[c], make_float2(s.r[col0 + 2 * c], s.r[col0 + 2 * c + 1]));
+                    wait(&s.k_empty[buf ^ 1], ((it - 1) >> 1) & 1);      // the products of the tile before are in O
+                    tc_after_sync();
+#pragma unroll 1
+                    for (int k = 0; k < np * 3 * (HC / 8); k++) {
+                        const int c0 = col0 + 8 * (k % (HC / 8));
+                        const uint32_t at = lanes + kO + NH * (k / (HC / 8)) + c0;
+                        uint32_t o[8];
+                        tmem_ld(at, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 8; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * s.r[c0 + c]);
+                        tmem_st(at, o);
+                    }
+                    tmem_st_wait();
+                }
+                add(1.f);
+            }
+            fence_async_smem();
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0 && ok) mbar_arrive(&s.p_full[buf]);
+            if (!w.last()) continue;
+
+            // ------------------------------------------------------ this part of the sequence is done
+#pragma unroll
+            for (int c = 0; c < HC; c++) {
+                const float z = warp_sum(c & 1 ? l[c / 2].y : l[c / 2].x);
+                if (lane == 0) s.red[wq][col0 + c] = z;
+            }
+            named_sync(1, kSoft);
+            const bool whole = w.whole();
+            const long long pidx = ((long long)group * g.nrb + w.rb) * 2 + w.which();
+            if (tid < NH) {
+                const float z = s.red[0][tid] + s.red[1][tid] + s.red[2][tid] + s.red[3][tid];
+                const float m = -s.m[cur][tid];
+                s.linv[tid] = whole ? (z != 0.f ? 1.f / z : 0.f) : 1.f;
+                const int r = w.rb * NH + tid;
+                if (!whole) {
+                    g.part_ml[(pidx * NH + tid) * 2] = m;
+                    g.part_ml[(pidx * NH + tid) * 2 + 1] = z;
+                } else if (a.lse && r < g.n_rows) {
+                    a.lse[(long long)w.b * g.n_rows + r] = z != 0.f ? (m + log2f(z)) * 0.6931471805599453f : -INFINITY;
+                }
+            }
+            named_sync(1, kSoft);
+            wait(&s.k_empty[buf], (it >> 1) & 1);
+            tc_after_sync();
+#pragma unroll 1
+            for (int k = 0; k < np * (HC / 8); k++) {
+                const int c0 = col0 + 8 * (k % (HC / 8)), blk = k / (HC / 8), d = 128 * blk + t;
+                uint32_t o0[8], o1[8], o2[8];
+                tmem_ld(lanes + kO + 3 * NH * blk + c0, o0);
+                tmem_ld(lanes + kO + 3 * NH * blk + NH + c0, o1);
+                tmem_ld(lanes + kO + 3 * NH * blk + 2 * NH + c0, o2);
+                tmem_ld_wait();
+                const long long row = (long long)w.b * g.n_rows + w.rb * NH + c0;
+#pragma unroll
+                for (int c = 0; c < 8; c++) {
+                    if (w.rb * NH + c0 + c >= g.n_rows) break;
+                    const float v = fmaf(fmaf(__uint_as_float(o2[c]), 1.f / kFine, __uint_as_float(o1[c])), 1.f / kFine, __uint_as_float(o0[c])) *
+                                    s.linv[c0 + c];
+                    if (!whole) g.part[(pidx * NH + c0 + c) * a.c.L + d] = v;
+                    else store_out(a, (row + c) * a.c.L + d, v);
+                }
+            }
+            tc_before_sync();
+            named_sync(1, kSoft);
+        }
+    } else if (warp == 8) {
+        // ---------------------------------------------------------- MMA issue
+        constexpr uint32_t id_s = f16_idesc(0, false, false, kTile, 2 * NH), id_o = f16_idesc(0, true, true, 128, 3 * NH);
+        const uint64_t dk = sw128_desc(base, 16, 1024), dr = sw64_desc(base + np * kBlk8);
+        const uint64_t dq = sw128_desc(base + q_off, 16, 1024), dqr = sw64_desc(base + q_off + np * (2 * NH * 128));
+        const uint64_t dv = sw128_desc(base, 16, 1024), dp = sw128_desc(base + p_off, 16, 1024);
+        auto scores = [&](int it) {
+            const uint32_t buf = it & 1, so = (buf * stage) >> 4, d = tmem + buf * (2 * NH);
+            wait(&s.k_full[buf], (it >> 1) & 1);
+            tc_after_sync();
+            if (!ok) return;
+            for (int p = 0; p < np; p++)
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    mma8_ss(d, dk + so + ((p * kBlk8) >> 4) + 2 * k, dq + ((p * 2 * NH * 128) >> 4) + 2 * k, id_s, p || k);
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+                if (32 * k < a.c.R) mma8_ss(d, dr + so + 2 * k, dqr + 2 * k, id_s, true);
+            tc_commit(&s.s_full[buf]);
+        };
+        int it = 0;
+        for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), it++) {
+            if (w.first()) {
+                named_sync(3, kSoft + 32);
+                scores(it);
+            }
+            if (!w.last()) scores(it + 1);
+            const uint32_t buf = it & 1, so = (buf * stage) >> 4, po = (buf * kP8) >> 4;
+            wait(&s.p_full[buf], (it >> 1) & 1);
+            tc_after_sync();
+            if (ok) {
+                for (int p = 0; p < np; p++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        mma8_ss(tmem + kO + 3 * NH * p, dv + so + ((p * kBlk8 + k * 4096) >> 4), dp + po + ((k * 4096) >> 4), id_o, k || !w.first());
+                tc_commit(&s.k_empty[buf]);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- bulk copies
+        const int nbox = kTile / g.pbox;
+        int it = 0;
+        for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), it++) {
+            const int buf = it & 1;
+            const int sl = lane < nbox ? token_slot(a, w.b, w.tile() * kTile + lane * g.pbox, w.len) : -1;
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, sl >= 0));
+            if (it > 1) wait(&s.k_empty[buf], ((it - 2) >> 1) & 1);
+            if (lane == 0 && ok) mbar_expect_tx(&s.k_full[buf], boxes * g.pbox * (np * 128 + 64 + 4));
+            __syncwarp();
+            if (sl >= 0 && ok) {
+                const uint32_t dst = base + buf * stage, row = lane * g.pbox;
+                for (int p = 0; p < np; p++) tma_box(dst + p * kBlk8 + row * 128, &map, 128 * p, sl, &s.k_full[buf]);
+                tma_box(dst + np * kBlk8 + row * 64, &rope_map, a.c.L, sl, &s.k_full[buf]);
+                bulk_load(&s.scale[buf][row], a.c.scales + sl, g.pbox * 4, &s.k_full[buf]);
+            }
+        }
+        // every copy has landed before the CTA may end
+        const uint64_t late = global_ns() + 200000000ull;
+        volatile int none = 0;
+        for (int k = it > 1 ? it - 2 : 0; k < it; k++) warp_wait(&s.k_full[k & 1], (k >> 1) & 1, late, &none, lane);
+    }
+    tc_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+        tc_after_sync();
+        tmem_free(tmem, kCols);
+    }
+}
+
+template <int NH>
+cudaError_t run(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t st) {
+    CUtensorMap map, rope;
+    if (cudaError_t e = mla_row_map(a.c, 128, g.pbox, CU_TENSOR_MAP_SWIZZLE_128B, &map)) return e;
+    if (cudaError_t e = mla_row_map(a.c, 64, g.pbox, CU_TENSOR_MAP_SWIZZLE_64B, &rope)) return e;
+    const size_t np = a.c.L / 128;
+    const size_t smem = 2 * (np * kBlk8 + kRope8) + np * (2 * NH * 128) + 2 * NH * 64 + 2 * kP8 + 1024;
+    auto kern = mla_attend_e4m3_kernel<NH>;
+    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+    return launch_pdl(kern, dim3(g.n_groups * g.n_slots), dim3(320), smem, st, map, rope, a, g);
+}
+
+}  // namespace
+
+cudaError_t launch_mla_attend_e4m3(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t st) {
+    return g.cols == 16 ? run<16>(a, g, st) : run<32>(a, g, st);
+}
+
+}  // namespace coli

@@ -377,7 +377,7 @@ enum {
  *   page_size  tokens per page, a multiple of 16 in 16..65536.
  *   n_pages    >= 1, n_pages * page_size <= 2^31 - 1.
  *   rows       device [n_pages][page_size][latent + rope], 16-byte aligned.
- *   scales     device f32 [n_pages][page_size] (COLI_E4M3; else ignored); finite, >= 0.
+ *   scales     device f32 [n_pages][page_size] (COLI_E4M3; else ignored), 16-byte aligned; finite, >= 0.
  */
 typedef struct {
     int dtype, latent, rope, page_size;
@@ -461,10 +461,11 @@ int coli_mla_read(const coli_mla_cache *cache, const int32_t *pages, int64_t pag
  *   lens      device int32 [n_seq], >= 0.
  *   out       device [n_seq][n_q][n_heads][latent], COLI_F32 or COLI_BF16.
  *   lse       device f32 [n_seq][n_q][n_heads], or NULL.
- * The products take 16-bit operands, as the cache holds no more: q and the
- * probabilities are rounded to bf16 for a COLI_BF16 cache, to f16 (q scaled by
- * a power of two per head) for a COLI_E4M3 one; sums, maxima and the
- * softmax's denominator are f32.  Rows past a sequence's length, and pages
+ * The products take operands of the cache's kind: for a COLI_BF16 cache q and
+ * the probabilities are rounded to bf16; for a COLI_E4M3 one q becomes two E4M3
+ * terms (scaled by a power of two per query row; a bf16 value exactly, others
+ * to 2^-8 of them) and the probabilities three (to 2^-12).  Sums, maxima and
+ * the softmax's denominator are f32.  Rows past a sequence's length, and pages
  * past its last, are never used: they may hold anything.
  * Pointers 16-byte aligned (pages, lens, lse: 4).  n_seq >= 0, n_q >= 1, 1 <= n_heads <= 1024,
  * n_q * n_heads <= 65536.  A page id outside [0, n_pages) among the needed ones, or a length out
