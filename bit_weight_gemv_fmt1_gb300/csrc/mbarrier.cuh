@@ -37,6 +37,15 @@ __device__ __forceinline__ bool mbar_try(uint64_t *b, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(smem_addr(b)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
 // One thread's bounded wait: false once `deadline` has passed or the CTA aborted.
 __device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity, uint64_t deadline, volatile int *abort) {
     while (!mbar_try(b, parity)) {

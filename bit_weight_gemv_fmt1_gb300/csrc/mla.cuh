@@ -113,6 +113,12 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// The same to E5M2.
+__device__ __forceinline__ uint32_t pack_e5m2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 // Two E4M3 bytes -> two f16 in one register (exact).
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
     uint32_t r;

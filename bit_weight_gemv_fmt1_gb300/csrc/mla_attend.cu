@@ -25,9 +25,9 @@
 // hold part of a sequence leave (O, m, l) in f32 in scratch, and
 // mla_join_kernel adds them up; the rest is written directly.
 //
-// Warps: 0-7 softmax and output (two threads per token, each half the columns;
-// warp 0 issues the MMAs, which alternate with the softmax anyway), then for E4M3 eight warps that load codes into registers one
-// whole tile ahead, convert and store them; for bf16 one warp of tiled bulk copies.
+// Warps: 0-7 softmax and output (two threads per token, each half the columns), 8
+// MMA issue, 9-10 tiled bulk copies.  The E4M3 cache has a kernel of its own
+// (mla_attend_e4m3.cu).
 // Every wait is bounded; after one has run out all waits return at once, no
 // further MMA or copy is issued, and the kernel records DEV_ERR_TIMEOUT.
 #include <cudaTypedefs.h>
@@ -91,7 +91,7 @@ __device__ __forceinline__ void load_queries(const MlaAttendArgs &a, const Atten
 }
 
 template <int N>
-__global__ void __launch_bounds__(320, 1) mla_attend_bf16_kernel(const __grid_constant__ CUtensorMap map, const MlaAttendArgs a, const AttendPlan g) {
+__global__ void __launch_bounds__(352, 1) mla_attend_bf16_kernel(const __grid_constant__ CUtensorMap map, const MlaAttendArgs a, const AttendPlan g) {
     constexpr int NC = N / 2;              // columns per softmax thread
     extern __shared__ uint8_t raw[];
     __shared__ Shared s;
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(320, 1) mla_attend_bf16_kernel(const __grid_co
                     // s.m holds minus the reference
                     const float old = -s.m[cur][tid];
                     const float x = fmaxf(fmaxf(s.red[0][tid], s.red[1][tid]), fmaxf(s.red[2][tid], s.red[3][tid]));
-                    const float now = fmaxf(old, x - kHead);
+                    const float now = x > old + kLimit ? x - kHead : old;   // only the columns that need it
                     s.m[cur ^ 1][tid] = -now;
                     s.r[tid] = ex2(old - now);
                 }
@@ -300,11 +300,19 @@ __global__ void __launch_bounds__(320, 1) mla_attend_bf16_kernel(const __grid_co
 #pragma unroll 1
                     for (int k = 0; k < npair * (NC / 8); k++) {
                         const uint32_t at = lanes + N * (1 + k / (NC / 8)) + col0 + 8 * (k % (NC / 8));
+                        float r[8];
+                        bool same = true;
+#pragma unroll
+                        for (int c = 0; c < 8; c++) {
+                            r[c] = s.r[col0 + 8 * (k % (NC / 8)) + c];
+                            same = same && r[c] == 1.f;
+                        }
+                        if (same) continue;
                         uint32_t o[8];
                         tmem_ld(at, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int c = 0; c < 8; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * s.r[col0 + 8 * (k % (NC / 8)) + c]);
+                        for (int c = 0; c < 8; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * r[c]);
                         tmem_st(at, o);
                     }
                     tmem_st_wait();
@@ -371,23 +379,14 @@ __global__ void __launch_bounds__(320, 1) mla_attend_bf16_kernel(const __grid_co
         }
     } else {
         // ---------------------------------------------------------- bulk copies of bf16 rows
-        // A block's buffer comes free only 1500 cycles or so before the next tile's is needed, less than HBM's
-        // latency under load, so the rows are asked into L2 a whole tile earlier (shared among the group's CTAs).
-        const int nbox = kTile / g.pbox;
+        // two warps, which share a tile's pairs of blocks
+        const int who = warp - kMmaWarp - 1;
+        BoxAhead box(a, g, s.piece, slot, lane, who == 0);
         int it = 0;
-        auto slot_of = [&](const Walk &w) {
-            return lane < nbox && w.valid() ? token_slot(a, w.b, w.tile() * kTile + lane * g.pbox, w.len) : -1;
-        };
-        Walk w(a, g, s.piece, slot);
-        int next = slot_of(w);
-        for (; w.valid(); it++) {
-            const int sl = next;
+        for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), box.next(), it++) {
+            const int sl = box.slot[0];
             const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, sl >= 0));
-            w.next();
-            next = slot_of(w);
-            if (next >= 0)
-                for (int k = slot; k < nblk; k += g.n_slots) tma_prefetch(&map, 64 * k, next);
-            for (int p = 0; p <= npair; p++) {
+            for (int p = who; p <= npair; p += 2) {
                 if (it > 0) wait(&s.empty[p], (it - 1) & 1);
                 const int nb = p < npair ? 2 : 1;
                 if (lane == 0 && ok) mbar_expect_tx(&s.full[p], boxes * g.pbox * 128 * nb);
@@ -401,7 +400,7 @@ __global__ void __launch_bounds__(320, 1) mla_attend_bf16_kernel(const __grid_co
         if (it > 0) {
             const uint64_t late = global_ns() + 200000000ull;
             volatile int none = 0;
-            for (int p = 0; p <= npair; p++) warp_wait(&s.full[p], (it - 1) & 1, late, &none, lane);
+            for (int p = who; p <= npair; p += 2) warp_wait(&s.full[p], (it - 1) & 1, late, &none, lane);
         }
     }
     tc_before_sync();
@@ -412,69 +411,78 @@ __global__ void __launch_bounds__(320, 1) mla_attend_bf16_kernel(const __grid_co
     }
 }
 
-// Joins the partial results of the sequences that more than one group worked on:
-// weights 2^(m - max m), four slices of the parts per row, in a fixed order.
-__global__ void __launch_bounds__(512) mla_join_kernel(const MlaAttendArgs a, const AttendPlan g) {
-    __shared__ float s_w[512];
-    __shared__ float4 s_o[4][128];
-    __shared__ float s_m[16], s_l[16];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Joins the partial results of the sequences that more than one group worked on, with weights 2^(m - max m).
+// wpr warps (a power of two up to 16) share a row's parts, each lane with 4 dims of every 128; their sums meet in
+// shared memory in a fixed order.  Many rows (a batch): one warp each; few rows of many parts (a long context): 16.
+__global__ void __launch_bounds__(512) mla_join_kernel(const MlaAttendArgs a, const AttendPlan g, int wpr) {
+    __shared__ float4 s_o[16][128];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp & (wpr - 1), rpb = 16 / wpr;
     pdl_wait();
     pdl_trigger();
-    const int total = g.prefix[a.n_seq], chunk = (total + g.n_groups - 1) / g.n_groups;
-    for (long long row = blockIdx.x; row < (long long)a.n_seq * g.n_rows; row += gridDim.x) {
-        const int b = (int)(row / g.n_rows), r = (int)(row - (long long)b * g.n_rows);
-        const int p = g.prefix[b], g0 = p / chunk, g1 = (g.prefix[b + 1] - 1) / chunk;
-        if (g0 == g1) continue;
-        const int rb = r / g.cols, c = r - rb * g.cols, n = g1 - g0 + 1;
+    const int total = g.prefix[a.n_seq], chunk = (total + g.n_groups - 1) / g.n_groups, nd = a.c.L / 128;
+    const int rows = a.n_seq * g.n_rows;
+    for (int row0 = blockIdx.x * rpb; row0 < rows; row0 += gridDim.x * rpb) {
+        const int row = row0 + warp / wpr;
+        int b = 0, r = 0, g0 = 0, g1 = 0;
+        if (row < rows) {
+            b = row / g.n_rows;
+            r = row - b * g.n_rows;
+            g0 = g.prefix[b] / chunk;
+            g1 = (g.prefix[b + 1] - 1) / chunk;
+        }
+        const int n = g1 - g0 + 1, rb = r / g.cols, c = r - rb * g.cols;
         auto part = [&](int k) { return (((long long)(g0 + k) * g.nrb + rb) * 2 + (k == 0 ? 1 : 0)) * g.cols + c; };
-        float m = -INFINITY, z = 0.f;
-        if (tid < n) {
-            const float2 ml = *reinterpret_cast<const float2 *>(g.part_ml + part(tid) * 2);
-            m = ml.x;
-            z = ml.y;
-        }
-        float M = m;
+        float4 o[4];
+        float M = -INFINITY, z = 0.f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        if (lane == 0) s_m[warp] = M;
-        __syncthreads();
-        M = s_m[0];
-        for (int w = 1; w < 16; w++) M = fmaxf(M, s_m[w]);
-        const float f = m == -INFINITY ? 0.f : ex2(m - M);
-        s_w[tid] = f;
-        z = warp_sum(z * f);
-        if (lane == 0) s_l[warp] = z;
-        __syncthreads();
-        z = 0.f;
-        for (int w = 0; w < 16; w++) z += s_l[w];
-        const int slice = tid >> 7, q = tid & 127;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (4 * q < a.c.L) {
-#pragma unroll 8
-            for (int k = slice; k < n; k += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(g.part + part(k) * a.c.L + 4 * q);
-                const float f = s_w[k];
-                o = make_float4(fmaf(v.x, f, o.x), fmaf(v.y, f, o.y), fmaf(v.z, f, o.z), fmaf(v.w, f, o.w));
+        for (int d = 0; d < 4; d++) o[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (n > 1) {
+            for (int k = lane; k < n; k += 32) M = fmaxf(M, g.part_ml[part(k) * 2]);
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+            for (int k = lane; k < n; k += 32) {
+                const float2 ml = *reinterpret_cast<const float2 *>(g.part_ml + part(k) * 2);
+                z = fmaf(ml.y, ex2(ml.x - M), z);
+            }
+            z = warp_sum(z);
+#pragma unroll 2
+            for (int k = sub; k < n; k += wpr) {
+                const float f = ex2(g.part_ml[part(k) * 2] - M);
+                const float *src = g.part + part(k) * a.c.L + 4 * lane;
+#pragma unroll
+                for (int d = 0; d < 4; d++) {
+                    if (d >= nd) break;
+                    const float4 v = __ldcs(reinterpret_cast<const float4 *>(src + 128 * d));
+                    o[d] = make_float4(fmaf(v.x, f, o[d].x), fmaf(v.y, f, o[d].y), fmaf(v.z, f, o[d].z), fmaf(v.w, f, o[d].w));
+                }
             }
         }
-        s_o[slice][q] = o;
-        __syncthreads();
-        if (slice == 0 && 4 * q < a.c.L) {
-            const float inv = z != 0.f ? 1.f / z : 0.f;
-            for (int k = 1; k < 4; k++) {
-                const float4 v = s_o[k][q];
-                o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
-            }
-            o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (wpr > 1) {
+#pragma unroll
+            for (int d = 0; d < 4; d++) s_o[warp][32 * d + lane] = o[d];
+            __syncthreads();
+            if (sub == 0)
+                for (int w = 1; w < wpr; w++)
+#pragma unroll
+                    for (int d = 0; d < 4; d++) {
+                        const float4 v = s_o[warp + w][32 * d + lane];
+                        o[d] = make_float4(o[d].x + v.x, o[d].y + v.y, o[d].z + v.z, o[d].w + v.w);
+                    }
+            __syncthreads();
+        }
+        if (n == 1 || sub != 0) continue;
+        const float inv = z != 0.f ? 1.f / z : 0.f;
+#pragma unroll
+        for (int d = 0; d < 4; d++) {
+            if (d >= nd) break;
+            const long long e = (long long)row * a.c.L + 128 * d + 4 * lane;
+            const float4 v = make_float4(o[d].x * inv, o[d].y * inv, o[d].z * inv, o[d].w * inv);
             if (a.out_bf16)
-                *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + row * a.c.L + 4 * q) =
-                    make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+                *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + e) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
             else
-                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + row * a.c.L + 4 * q) = o;
+                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + e) = v;
         }
-        if (a.lse && tid == 0) a.lse[row] = z != 0.f ? (M + log2f(z)) * 0.6931471805599453f : -INFINITY;
-        __syncthreads();
+        if (a.lse && lane == 0) a.lse[row] = z != 0.f ? (M + log2f(z)) * 0.6931471805599453f : -INFINITY;
     }
 }
 
@@ -517,7 +525,7 @@ cudaError_t run_bf16(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t s
     const size_t smem = (size_t)nblk * kBlk + (size_t)nblk * N * 128 + 1024;
     auto kern = mla_attend_bf16_kernel<N>;
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
-    return launch_pdl(kern, dim3(g.n_groups * g.n_slots), dim3(320), smem, st, map, a, g);
+    return launch_pdl(kern, dim3(g.n_groups * g.n_slots), dim3(352), smem, st, map, a, g);
 }
 
 }  // namespace
@@ -561,8 +569,12 @@ cudaError_t launch_mla_attend(const MlaAttendArgs &a, void *scratch, int n_sm, c
     if (a.c.e4m3) e = launch_mla_attend_e4m3(a, g, st);
     else e = g.cols == 16 ? run_bf16<16>(a, g, st) : g.cols == 32 ? run_bf16<32>(a, g, st) : run_bf16<64>(a, g, st);
     if (e != cudaSuccess || g.n_groups == 1) return e;
-    const long long rows = (long long)a.n_seq * g.n_rows;
-    return launch_pdl(mla_join_kernel, dim3((unsigned)(rows < 4LL * n_sm ? rows : 4LL * n_sm)), dim3(512), 0, st, a, g);
+    // enough warps for the device, a block of 16 at a time
+    const int rows = a.n_seq * g.n_rows;
+    int wpr = 16;
+    while (wpr > 1 && (long long)rows * wpr > 32LL * n_sm) wpr /= 2;
+    const int blocks = (rows + 16 / wpr - 1) / (16 / wpr);
+    return launch_pdl(mla_join_kernel, dim3(blocks < 4 * n_sm ? blocks : 4 * n_sm), dim3(512), 0, st, a, g, wpr);
 }
 
 }  // namespace coli

@@ -38,7 +38,7 @@ __device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTile
 struct Walk {
     const MlaAttendArgs &a;
     const AttendPlan &g;
-    const Piece &s;
+    const Piece s;
     int rb, u, b, p, T, len;
     __device__ Walk(const MlaAttendArgs &a_, const AttendPlan &g_, const Piece &s_, int slot) : a(a_), g(g_), s(s_), rb(slot) { start(); }
     __device__ void start() {
@@ -55,6 +55,8 @@ struct Walk {
     __device__ bool first() const { return u == s.u0 || u == p; }              // of this CTA's part of the sequence
     __device__ bool last() const { return u + 1 == s.u1 || u + 1 == p + T; }
     __device__ bool whole() const { return p >= s.u0 && p + T <= s.u1; }       // the piece holds all of the sequence
+    __device__ int rest() const { return min(s.u1, p + T) - u; }               // tiles left of this part
+    __device__ void skip(int n) { u += n; }                                    // within this part
     __device__ int which() const { return p < s.u0 ? 0 : 1; }                  // which of the piece's two partial results
     __device__ void next() {
         if (++u == s.u1) {
@@ -155,6 +157,39 @@ __device__ __forceinline__ void find_piece(const MlaAttendArgs &a, const AttendP
         if (g.prefix && blockIdx.x == 0) g.prefix[a.n_seq] = total;
     }
 }
+
+// A copy warp's lanes: the slot of this lane's box of pbox tokens in the current
+// tile, looked up two tiles ahead, whose rows are then asked into L2 (each of the
+// group's CTAs asks for a share).  A tile's buffers come free only about 1000
+// cycles before they are needed again, less than HBM's latency under load.
+struct BoxAhead {
+    Walk w;                // two tiles ahead of the current one
+    int lane, nbox, pbox, share;
+    bool fetch;
+    int slot[3];
+    __device__ BoxAhead(const MlaAttendArgs &a, const AttendPlan &g, const Piece &s, int slot_, int lane_, bool fetch_)
+        : w(a, g, s, slot_), lane(lane_), nbox(kTile / g.pbox), pbox(g.pbox), share(slot_), fetch(fetch_) {
+        slot[0] = look();
+        slot[1] = look();
+        slot[2] = look();
+    }
+    __device__ int look() {
+        if (!w.valid()) return -1;
+        const int sl = lane < nbox ? token_slot(w.a, w.b, w.tile() * kTile + lane * pbox, w.len) : -1;
+        if (fetch && sl >= 0) {
+            // this CTA's share of the box's rows
+            const int per = (pbox + w.g.n_slots - 1) / w.g.n_slots, r0 = min(pbox, share * per), r1 = min(pbox, r0 + per);
+            if (r1 > r0) bulk_prefetch(mla_row(w.a.c, sl + r0), (r1 - r0) * w.a.c.row_bytes);
+        }
+        w.next();
+        return sl;
+    }
+    __device__ void next() {
+        slot[0] = slot[1];
+        slot[1] = slot[2];
+        slot[2] = look();
+    }
+};
 
 // The E4M3 kernel (mla_attend_e4m3.cu).
 cudaError_t launch_mla_attend_e4m3(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t st);

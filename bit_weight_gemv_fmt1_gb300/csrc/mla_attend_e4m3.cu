@@ -3,10 +3,14 @@
 // reference and how the work is cut; this kernel differs in that the codes are
 // never converted.
 //
-// The tensor cores multiply E4M3 by E4M3, exactly, into f32.  What faces the
-// codes is split into E4M3 terms, each 2^5 finer than the one before:
-//   q  (times a power of two per row)  = q0 + 2^-5 q1             (a bf16 value exactly)
-//   P  = weight * row scale            = p0 + 2^-5 p1 + 2^-10 p2  (to 2^-13 of the value)
+// The tensor cores multiply 8-bit floats exactly into f32.  What faces the codes
+// is split into 8-bit terms:
+//   q  (times a power of two per row)  = q0 + 2^-5 q1             E4M3 (a bf16 value exactly)
+//   P  = weight * row scale            = p0 + 2^-3 p1 + 2^-7 p2   E5M2 (to 2^-11, as f16 has it)
+// P's terms are E5M2 for its range: the reference starts 6 below the first tile's maximum and
+// weights may grow by 2^8 before it has to move, while those down to 2^-18 of the
+// largest keep all 11 bits.  (Three E4M3 terms have 14 bits but a 2^-20 floor under
+// a 2^8 ceiling: the reference moved every second tile, 6000 cycles each time.)
 // Terms are columns side by side, S^T [128 tokens][2 NH] and O^T [128 dims][3 NH]
 // for NH = 16 or 32 query rows, and are added in f32 when they leave TMEM.  An
 // MMA reads 4 KB of codes for 128 x 32 values whatever its N, so the terms cost
@@ -16,7 +20,7 @@
 //
 // Tiles are 73 KB, so two fit: the scores of tile i + 1 are computed while the
 // softmax of tile i runs.  Warps: 0-7 softmax and output (two threads per
-// token, each half the rows), 8 MMA issue, 9 bulk copies of codes and scales.
+// token, each half the rows), 8 MMA issue, 9-10 bulk copies of codes and scales.
 #include "mla_attend.cuh"
 
 namespace coli {
@@ -26,16 +30,18 @@ namespace {
 constexpr uint32_t kBlk8 = kTile * 128;  // 128 tokens x 128 codes, 128-byte swizzle
 constexpr uint32_t kRope8 = kTile * 64;  // 128 tokens x 64 codes, 64-byte swizzle
 constexpr uint32_t kP8 = kTile * 128;    // P [128 tokens][3 NH], rows of 128 bytes
-constexpr float kHead8 = 4.f;            // log2 of the largest weight of a fresh reference
-constexpr float kLimit8 = 8.f;           // log2 of the weight that moves the reference (E4M3 ends at 448)
-constexpr float kFine = 32.f;            // a term's step against the next
+constexpr float kHead8 = 6.f;            // log2 of the largest weight of a fresh reference
+constexpr float kLimit8 = 14.f;          // log2 of the weight that moves the reference (E5M2 ends at 57344)
+constexpr float kQ1 = 32.f;              // q's second term against the first
+constexpr float kP1 = 8.f, kP2 = 16.f;   // P's second term against the first, third against the second
 
 struct Shared8 {
-    uint64_t k_full[2], k_empty[2], s_full[2], p_full[2];
+    uint64_t k_full[2][5], k_empty[2][5];   // blocks of 128 dims; last: rope part and scales
+    uint64_t s_full[2], p_full[2];
     uint32_t tmem;
     int abort;
     Piece piece;
-    alignas(16) float scale[2][kTile];   // written by bulk copies
+    alignas(16) float scale[4][kTile];   // of tile it & 3, written by bulk copies
     alignas(16) float f[32];
     alignas(16) float m[2][32];          // minus the reference
     float linv[32], r[32];
@@ -43,6 +49,11 @@ struct Shared8 {
     float red[4][32];
 };
 
+// Instruction descriptor of kind::f8f6f4 with f32 accumulators; types: 0 = E4M3, 1 = E5M2.
+__host__ __device__ constexpr uint32_t f8_idesc(int a_type, int b_type, bool a_mn_major, bool b_mn_major, int M, int N) {
+    return (1u << 4) | ((uint32_t)a_type << 7) | ((uint32_t)b_type << 10) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
 // 64-byte swizzled K-major operand: atoms of 8 rows x 64 bytes.
 __device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(512 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)4 << 61;
@@ -54,15 +65,13 @@ __device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
-__device__ __forceinline__ float2 e4m3x2_f32x2(uint32_t two) {
-    const uint32_t h = e4m3x2_f16x2(two);
-    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
-}
-// v -> its E4M3 pair (16 bits); v becomes the remainder times 2^5.
-__device__ __forceinline__ uint32_t take_term(float2 &v) {
-    const uint32_t u = pack_e4m3(v.x, v.y);
-    float2 r = fmul2(v, make_float2(kFine, kFine));
-    ffma2(r, e4m3x2_f32x2(u), make_float2(-kFine, -kFine));
+// v -> its 8-bit pair; v becomes the remainder times `step`.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t take_term(float2 &v, float step) {
+    const uint32_t u = E5M2 ? pack_e5m2(v.x, v.y) : pack_e4m3(v.x, v.y);
+    const uint32_t h = E5M2 ? __byte_perm(u, 0u, 0x1404) : e4m3x2_f16x2(u);   // E5M2 is the high byte of f16
+    float2 r = fmul2(v, make_float2(step, step));
+    ffma2(r, __half22float2(*reinterpret_cast<const __half2 *>(&h)), make_float2(-step, -step));
     v = r;
     return u;
 }
@@ -105,8 +114,8 @@ __device__ __forceinline__ void load_queries8(const MlaAttendArgs &a, const Atte
 #pragma unroll
                 for (int q = 0; q < 2; q++) {
                     float2 y0 = make_float2(v[k][4 * q] * up, v[k][4 * q + 1] * up), y1 = make_float2(v[k][4 * q + 2] * up, v[k][4 * q + 3] * up);
-                    t[0][q] = take_term(y0);
-                    t[0][q] |= take_term(y1) << 16;
+                    t[0][q] = take_term<false>(y0, kQ1);
+                    t[0][q] |= take_term<false>(y1, kQ1) << 16;
                     t[1][q] = pack_e4m3(y0.x, y0.y) | pack_e4m3(y1.x, y1.y) << 16;
                 }
                 const int u = k < 2 ? lane + 32 * k : lane;
@@ -128,7 +137,7 @@ __device__ __forceinline__ void load_queries8(const MlaAttendArgs &a, const Atte
 }
 
 template <int NH>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(352, 1)
     mla_attend_e4m3_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap rope_map, const MlaAttendArgs a,
                            const AttendPlan g) {
     constexpr int HC = NH / 2;             // rows per softmax thread
@@ -147,8 +156,10 @@ __global__ void __launch_bounds__(320, 1)
     if (warp == 0) tmem_alloc(&s.tmem, kCols);
     if (tid == 0) {
         for (int i = 0; i < 2; i++) {
-            mbar_init(&s.k_full[i], 1);
-            mbar_init(&s.k_empty[i], 1);
+            for (int p = 0; p < 5; p++) {
+                mbar_init(&s.k_full[i][p], 1);
+                mbar_init(&s.k_empty[i][p], 1);
+            }
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_full[i], 8);
         }
@@ -196,10 +207,10 @@ __global__ void __launch_bounds__(320, 1)
             const int tok = w.tile() * kTile + t;
             // every row sees the whole tile: the first query's limit is the lowest
             const bool full = (w.tile() + 1) * kTile <= w.len - (a.n_q - 1) && (w.rb + 1) * NH <= g.n_rows;
-            wait(&s.k_full[buf], (it >> 1) & 1);                        // the scales
+            wait(&s.k_full[buf][np], (it >> 1) & 1);                    // the scales
             wait(&s.s_full[buf], (it >> 1) & 1);
             tc_after_sync();
-            const float st = tok < w.len ? s.scale[buf][t] : 0.f;
+            const float st = tok < w.len ? s.scale[it & 3][t] : 0.f;
             if ((w.tile() + 1) * kTile > w.len && tok >= w.len) {
                 // rows past the length may hold anything, and 0 * NaN is NaN
                 for (int k = grp; k < np; k += 2)
@@ -221,7 +232,7 @@ __global__ void __launch_bounds__(320, 1)
                     const float2 f = *reinterpret_cast<const float2 *>(&s.f[col0 + c]);
                     float2 x = *reinterpret_cast<const float2 *>(&s.m[cur][col0 + c]);
                     float2 y = make_float2(__uint_as_float(v0[c]), __uint_as_float(v0[c + 1]));
-                    ffma2(y, make_float2(__uint_as_float(v1[c]), __uint_as_float(v1[c + 1])), make_float2(1.f / kFine, 1.f / kFine));
+                    ffma2(y, make_float2(__uint_as_float(v1[c]), __uint_as_float(v1[c + 1])), make_float2(1.f / kQ1, 1.f / kQ1));
                     ffma2(x, fmul2(y, make_float2(st, st)), f);
                     if (!full) {
                         if (tok >= s.limit[col0 + c]) x.x = -INFINITY;
@@ -232,7 +243,7 @@ __global__ void __launch_bounds__(320, 1)
                     l[c / 2] = fadd2(l[c / 2], sign > 0.f ? x : make_float2(-x.x, -x.y));
                     if (sign > 0.f) {
                         float2 p = fmul2(x, make_float2(st, st));
-                        const uint32_t p0 = take_term(p), p1 = take_term(p), p2 = pack_e4m3(p.x, p.y);
+                        const uint32_t p0 = take_term<true>(p, kP1), p1 = take_term<true>(p, kP2), p2 = pack_e5m2(p.x, p.y);
                         const int sh = 8 * (c & 2), i = c / 4;
                         pk[0][i] = c & 2 ? pk[0][i] | p0 << sh : p0;
                         pk[1][i] = c & 2 ? pk[1][i] | p1 << sh : p1;
@@ -266,7 +277,7 @@ __global__ void __launch_bounds__(320, 1)
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < 8; c++) {
-                        float x = fmaf(__uint_as_float(v1[c]), 1.f / kFine, __uint_as_float(v0[c]));
+                        float x = fmaf(__uint_as_float(v1[c]), 1.f / kQ1, __uint_as_float(v0[c]));
                         x = fmaf(x * st, s.f[col0 + c0 + c], lg);
                         if (!full && tok >= s.limit[col0 + c0 + c]) x = -INFINITY;
                         const int k = __reduce_max_sync(0xffffffffu, float_key(x));
@@ -277,7 +288,7 @@ __global__ void __launch_bounds__(320, 1)
                 if (tid < NH) {
                     const float old = -s.m[cur][tid];
                     const float x = fmaxf(fmaxf(s.red[0][tid], s.red[1][tid]), fmaxf(s.red[2][tid], s.red[3][tid]));
-                    const float now = fmaxf(old, x - kHead8);
+                    const float now = x > old + kLimit8 ? x - kHead8 : old;   // only the columns that need it
                     s.m[cur ^ 1][tid] = -now;
                     s.r[tid] = ex2(old - now);
                 }
@@ -286,17 +297,25 @@ __global__ void __launch_bounds__(320, 1)
                 if (!w.first()) {
 #pragma unroll
                     for (int c = 0; c < HC / 2; c++) l[c] = fmul2(l[c], make_float2(s.r[col0 + 2 * c], s.r[col0 + 2 * c + 1]));
-                    wait(&s.k_empty[buf ^ 1], ((it - 1) >> 1) & 1);      // the products of the tile before are in O
+                    wait(&s.k_empty[buf ^ 1][np - 1], ((it - 1) >> 1) & 1);      // the products of the tile before are in O
                     tc_after_sync();
 #pragma unroll 1
                     for (int k = 0; k < np * 3 * (HC / 8); k++) {
                         const int c0 = col0 + 8 * (k % (HC / 8));
                         const uint32_t at = lanes + kO + NH * (k / (HC / 8)) + c0;
+                        float r[8];
+                        bool same = true;
+#pragma unroll
+                        for (int c = 0; c < 8; c++) {
+                            r[c] = s.r[c0 + c];
+                            same = same && r[c] == 1.f;
+                        }
+                        if (same) continue;
                         uint32_t o[8];
                         tmem_ld(at, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int c = 0; c < 8; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * s.r[c0 + c]);
+                        for (int c = 0; c < 8; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * r[c]);
                         tmem_st(at, o);
                     }
                     tmem_st_wait();
@@ -331,7 +350,7 @@ __global__ void __launch_bounds__(320, 1)
                 }
             }
             named_sync(1, kSoft);
-            wait(&s.k_empty[buf], (it >> 1) & 1);
+            wait(&s.k_empty[buf][np - 1], (it >> 1) & 1);
             tc_after_sync();
 #pragma unroll 1
             for (int k = 0; k < np * (HC / 8); k++) {
@@ -345,7 +364,7 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
                 for (int c = 0; c < 8; c++) {
                     if (w.rb * NH + c0 + c >= g.n_rows) break;
-                    const float v = fmaf(fmaf(__uint_as_float(o2[c]), 1.f / kFine, __uint_as_float(o1[c])), 1.f / kFine, __uint_as_float(o0[c])) *
+                    const float v = fmaf(fmaf(__uint_as_float(o2[c]), 1.f / kP2, __uint_as_float(o1[c])), 1.f / kP1, __uint_as_float(o0[c])) *
                                     s.linv[c0 + c];
                     if (!whole) g.part[(pidx * NH + c0 + c) * a.c.L + d] = v;
                     else store_out(a, (row + c) * a.c.L + d, v);
@@ -356,64 +375,102 @@ __global__ void __launch_bounds__(320, 1)
         }
     } else if (warp == 8) {
         // ---------------------------------------------------------- MMA issue
-        constexpr uint32_t id_s = f16_idesc(0, false, false, kTile, 2 * NH), id_o = f16_idesc(0, true, true, 128, 3 * NH);
+        constexpr uint32_t id_s = f8_idesc(0, 0, false, false, kTile, 2 * NH), id_o = f8_idesc(0, 1, true, true, 128, 3 * NH);
         const uint64_t dk = sw128_desc(base, 16, 1024), dr = sw64_desc(base + np * kBlk8);
         const uint64_t dq = sw128_desc(base + q_off, 16, 1024), dqr = sw64_desc(base + q_off + np * (2 * NH * 128));
         const uint64_t dv = sw128_desc(base, 16, 1024), dp = sw128_desc(base + p_off, 16, 1024);
         auto scores = [&](int it) {
             const uint32_t buf = it & 1, so = (buf * stage) >> 4, d = tmem + buf * (2 * NH);
-            wait(&s.k_full[buf], (it >> 1) & 1);
-            tc_after_sync();
-            if (!ok) return;
-            for (int p = 0; p < np; p++)
+            for (int p = 0; p < np; p++) {
+                wait(&s.k_full[buf][p], (it >> 1) & 1);
+                tc_after_sync();
+                if (!ok) return;
 #pragma unroll
                 for (int k = 0; k < 4; k++)
                     mma8_ss(d, dk + so + ((p * kBlk8) >> 4) + 2 * k, dq + ((p * 2 * NH * 128) >> 4) + 2 * k, id_s, p || k);
+            }
+            wait(&s.k_full[buf][np], (it >> 1) & 1);
+            tc_after_sync();
+            if (!ok) return;
 #pragma unroll
             for (int k = 0; k < 2; k++)
                 if (32 * k < a.c.R) mma8_ss(d, dr + so + 2 * k, dqr + 2 * k, id_s, true);
             tc_commit(&s.s_full[buf]);
+            tc_commit(&s.k_empty[buf][np]);    // the scales' buffers turn over every fourth tile, which is later than their use
         };
-        int it = 0;
-        for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), it++) {
-            if (w.first()) {
-                named_sync(3, kSoft + 32);
-                scores(it);
-            }
-            if (!w.last()) scores(it + 1);
+        auto output = [&](int it, bool first) {
             const uint32_t buf = it & 1, so = (buf * stage) >> 4, po = (buf * kP8) >> 4;
             wait(&s.p_full[buf], (it >> 1) & 1);
             tc_after_sync();
-            if (ok) {
-                for (int p = 0; p < np; p++)
+            if (!ok) return;
+            for (int p = 0; p < np; p++) {
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        mma8_ss(tmem + kO + 3 * NH * p, dv + so + ((p * kBlk8 + k * 4096) >> 4), dp + po + ((k * 4096) >> 4), id_o, k || !w.first());
-                tc_commit(&s.k_empty[buf]);
+                for (int k = 0; k < 4; k++)
+                    mma8_ss(tmem + kO + 3 * NH * p, dv + so + ((p * kBlk8 + k * 4096) >> 4), dp + po + ((k * 4096) >> 4), id_o, k || !first);
+                tc_commit(&s.k_empty[buf][p]);
             }
+        };
+        auto ready = [&](uint64_t *bar, int it) { return __all_sync(0xffffffffu, mbar_test(bar, (it >> 1) & 1)); };
+        auto tile_ready = [&](int it) {
+            for (int p = np; p >= 0; p--)
+                if (!ready(&s.k_full[it & 1][p], it)) return false;
+            return true;
+        };
+        // Scores of tile q and outputs of tile v, in whichever order their inputs come: scores first where the
+        // softmax would run dry (q = v + 1), outputs first otherwise, since they free the buffers.
+        int it = 0;
+        for (Walk w(a, g, s.piece, slot); w.valid(); w.next()) {
+            const int n = w.rest();
+            named_sync(3, kSoft + 32);
+            int q = 0, v = 0;
+            while (v < n) {
+                if (!ok) break;
+                if (q == v) {
+                    scores(it + q++);
+                } else if (q < n && q == v + 1 && tile_ready(it + q)) {
+                    scores(it + q++);
+                } else if (ready(&s.p_full[(it + v) & 1], it + v)) {
+                    output(it + v, v == 0);
+                    v++;
+                } else if (q == n || q == v + 2) {
+                    output(it + v, v == 0);                             // nothing else to do: waits
+                    v++;
+                } else if (*abort || global_ns() > deadline) {
+                    wait(&s.p_full[(it + v) & 1], ((it + v) >> 1) & 1); // records the expiry
+                }
+            }
+            it += n;
+            w.skip(n - 1);
         }
     } else {
         // ---------------------------------------------------------- bulk copies
-        const int nbox = kTile / g.pbox;
+        // two warps, which share a tile's blocks
+        const int who = warp - 9;
+        BoxAhead box(a, g, s.piece, slot, lane, who == 0);
         int it = 0;
-        for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), it++) {
-            const int buf = it & 1;
-            const int sl = lane < nbox ? token_slot(a, w.b, w.tile() * kTile + lane * g.pbox, w.len) : -1;
-            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, sl >= 0));
-            if (it > 1) wait(&s.k_empty[buf], ((it - 2) >> 1) & 1);
-            if (lane == 0 && ok) mbar_expect_tx(&s.k_full[buf], boxes * g.pbox * (np * 128 + 64 + 4));
-            __syncwarp();
-            if (sl >= 0 && ok) {
-                const uint32_t dst = base + buf * stage, row = lane * g.pbox;
-                for (int p = 0; p < np; p++) tma_box(dst + p * kBlk8 + row * 128, &map, 128 * p, sl, &s.k_full[buf]);
-                tma_box(dst + np * kBlk8 + row * 64, &rope_map, a.c.L, sl, &s.k_full[buf]);
-                bulk_load(&s.scale[buf][row], a.c.scales + sl, g.pbox * 4, &s.k_full[buf]);
+        for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), box.next(), it++) {
+            const int buf = it & 1, sl = box.slot[0];
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, sl >= 0)), row = lane * g.pbox;
+            for (int p = who; p <= np; p += 2) {
+                if (it > 1) wait(&s.k_empty[buf][p], ((it - 2) >> 1) & 1);
+                if (lane == 0 && ok) mbar_expect_tx(&s.k_full[buf][p], boxes * g.pbox * (p < np ? 128 : 64 + 4));
+                __syncwarp();
+                if (sl < 0 || !ok) continue;
+                const uint32_t dst = base + buf * stage + p * kBlk8;
+                if (p < np) {
+                    tma_box(dst + row * 128, &map, 128 * p, sl, &s.k_full[buf][p]);
+                } else {
+                    tma_box(dst + row * 64, &rope_map, a.c.L, sl, &s.k_full[buf][p]);
+                    bulk_load(&s.scale[it & 3][row], a.c.scales + sl, g.pbox * 4, &s.k_full[buf][p]);
+                }
             }
+            __syncwarp();
         }
         // every copy has landed before the CTA may end
         const uint64_t late = global_ns() + 200000000ull;
         volatile int none = 0;
-        for (int k = it > 1 ? it - 2 : 0; k < it; k++) warp_wait(&s.k_full[k & 1], (k >> 1) & 1, late, &none, lane);
+        for (int k = it > 1 ? it - 2 : 0; k < it; k++)
+            for (int p = who; p <= np; p += 2) warp_wait(&s.k_full[k & 1][p], (k >> 1) & 1, late, &none, lane);
     }
     tc_before_sync();
     __syncthreads();
@@ -432,7 +489,7 @@ cudaError_t run(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t st) {
     const size_t smem = 2 * (np * kBlk8 + kRope8) + np * (2 * NH * 128) + 2 * NH * 64 + 2 * kP8 + 1024;
     auto kern = mla_attend_e4m3_kernel<NH>;
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
-    return launch_pdl(kern, dim3(g.n_groups * g.n_slots), dim3(320), smem, st, map, rope, a, g);
+    return launch_pdl(kern, dim3(g.n_groups * g.n_slots), dim3(352), smem, st, map, rope, a, g);
 }
 
 }  // namespace

@@ -116,9 +116,9 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, in
                  "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y)
                  : "memory");
 }
-// The same box into L2 only.
-__device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int y) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+// Contiguous bytes (16-byte aligned, a multiple of 16) into L2 only.
+__device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
