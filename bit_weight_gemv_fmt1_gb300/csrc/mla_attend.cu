@@ -26,7 +26,7 @@
 // mla_join_kernel adds them up; the rest is written directly.
 //
 // Warps: 0-7 softmax and output (two threads per token, each half the columns), 8
-// MMA issue, 9-10 tiled bulk copies.  The E4M3 cache has a kernel of its own
+// MMA issue, the others tiled bulk copies.  The E4M3 cache has a kernel of its own
 // (mla_attend_e4m3.cu).
 // Every wait is bounded; after one has run out all waits return at once, no
 // further MMA or copy is issued, and the kernel records DEV_ERR_TIMEOUT.
@@ -39,6 +39,8 @@ namespace coli {
 namespace {
 
 constexpr uint32_t kBlk = kTile * 128;   // 128 tokens x 64 dims of 16 bits, 128-byte swizzle
+constexpr int kCopyWarps = 3;            // a warp's copy takes some 500 cycles to issue, so several share a tile
+constexpr int kThreads = 32 * (9 + kCopyWarps);
 constexpr int kMaxPairs = 4;             // pairs of blocks: L / 128
 constexpr float kHead = 6.f;             // log2 of the largest weight of a fresh reference
 constexpr float kLimit = 14.f;           // log2 of the weight that moves the reference
@@ -91,7 +93,7 @@ __device__ __forceinline__ void load_queries(const MlaAttendArgs &a, const Atten
 }
 
 template <int N>
-__global__ void __launch_bounds__(352, 1) mla_attend_bf16_kernel(const __grid_constant__ CUtensorMap map, const MlaAttendArgs a, const AttendPlan g) {
+__global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __grid_constant__ CUtensorMap map, const MlaAttendArgs a, const AttendPlan g) {
     constexpr int NC = N / 2;              // columns per softmax thread
     extern __shared__ uint8_t raw[];
     __shared__ Shared s;
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(352, 1) mla_attend_bf16_kernel(const __grid_co
     bool ok = true;                        // this thread's waits have all ended well
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (!ok) return;
-        if (!warp_wait(bar, parity, deadline, abort, lane)) {
+        if (!warp_wait_now(bar, parity, deadline, abort, lane)) {
             ok = false;
             *abort = 1;
             atomicCAS(a.err, 0, (int)DEV_ERR_TIMEOUT);
@@ -379,28 +381,30 @@ __global__ void __launch_bounds__(352, 1) mla_attend_bf16_kernel(const __grid_co
         }
     } else {
         // ---------------------------------------------------------- bulk copies of bf16 rows
-        // two warps, which share a tile's pairs of blocks
         const int who = warp - kMmaWarp - 1;
         BoxAhead box(a, g, s.piece, slot, lane, who == 0);
         int it = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), box.next(), it++) {
-            const int sl = box.slot[0];
-            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, sl >= 0));
-            for (int p = who; p <= npair; p += 2) {
+            const int sl = box.slot[0], nbox = kTile / g.pbox;
+            const uint32_t live = __ballot_sync(0xffffffffu, sl >= 0), boxes = __popc(live);
+            for (int p = who; p <= npair; p += kCopyWarps) {
                 if (it > 0) wait(&s.empty[p], (it - 1) & 1);
+                if (!ok) continue;
                 const int nb = p < npair ? 2 : 1;
-                if (lane == 0 && ok) mbar_expect_tx(&s.full[p], boxes * g.pbox * 128 * nb);
-                __syncwarp();
-                if (sl >= 0 && ok)
-                    for (int k = 0; k < nb; k++)
-                        tma_box(base + (2 * p + k) * kBlk + lane * g.pbox * 128, &map, 64 * (2 * p + k), sl, &s.full[p]);
+                expect_bytes(&s.full[p], boxes * g.pbox * 128 * nb);
+                for (int j = 0; j < nbox; j++) {
+                    const int y = __shfl_sync(0xffffffffu, sl, j);
+                    if (!(live >> j & 1)) continue;
+                    for (int k = 0; k < nb; k++) tma_box(base + (2 * p + k) * kBlk + j * g.pbox * 128, &map, 64 * (2 * p + k), y, &s.full[p]);
+                }
             }
+            __syncwarp();
         }
         // every copy has landed before the CTA may end
         if (it > 0) {
             const uint64_t late = global_ns() + 200000000ull;
             volatile int none = 0;
-            for (int p = who; p <= npair; p += 2) warp_wait(&s.full[p], (it - 1) & 1, late, &none, lane);
+            for (int p = who; p <= npair; p += kCopyWarps) warp_wait(&s.full[p], (it - 1) & 1, late, &none, lane);
         }
     }
     tc_before_sync();
@@ -525,7 +529,7 @@ cudaError_t run_bf16(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t s
     const size_t smem = (size_t)nblk * kBlk + (size_t)nblk * N * 128 + 1024;
     auto kern = mla_attend_bf16_kernel<N>;
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
-    return launch_pdl(kern, dim3(g.n_groups * g.n_slots), dim3(352), smem, st, map, a, g);
+    return launch_pdl(kern, dim3(g.n_groups * g.n_slots), dim3(kThreads), smem, st, map, a, g);
 }
 
 }  // namespace

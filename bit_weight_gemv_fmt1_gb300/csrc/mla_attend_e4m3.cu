@@ -20,7 +20,7 @@
 //
 // Tiles are 73 KB, so two fit: the scores of tile i + 1 are computed while the
 // softmax of tile i runs.  Warps: 0-7 softmax and output (two threads per
-// token, each half the rows), 8 MMA issue, 9-10 bulk copies of codes and scales.
+// token, each half the rows), 8 MMA issue, 9-13 bulk copies of codes and scales.
 #include "mla_attend.cuh"
 
 namespace coli {
@@ -30,18 +30,21 @@ namespace {
 constexpr uint32_t kBlk8 = kTile * 128;  // 128 tokens x 128 codes, 128-byte swizzle
 constexpr uint32_t kRope8 = kTile * 64;  // 128 tokens x 64 codes, 64-byte swizzle
 constexpr uint32_t kP8 = kTile * 128;    // P [128 tokens][3 NH], rows of 128 bytes
+constexpr int kCopyWarps = 5;            // a warp's copy takes some 500 cycles to issue, so each block has its warp
+constexpr int kThreads = 32 * (9 + kCopyWarps);
 constexpr float kHead8 = 6.f;            // log2 of the largest weight of a fresh reference
 constexpr float kLimit8 = 14.f;          // log2 of the weight that moves the reference (E5M2 ends at 57344)
 constexpr float kQ1 = 32.f;              // q's second term against the first
 constexpr float kP1 = 8.f, kP2 = 16.f;   // P's second term against the first, third against the second
 
 struct Shared8 {
-    uint64_t k_full[2][5], k_empty[2][5];   // blocks of 128 dims; last: rope part and scales
+    uint64_t k_full[2][5], k_empty[2][5];   // blocks of 128 dims; last: rope part
+    uint64_t sc_full[4];                    // row scales
     uint64_t s_full[2], p_full[2];
     uint32_t tmem;
     int abort;
     Piece piece;
-    alignas(16) float scale[4][kTile];   // of tile it & 3, written by bulk copies
+    alignas(16) float scale[4][kTile];   // of tile it & 3: a row's codes are freed by the scores, its scale is used after them
     alignas(16) float f[32];
     alignas(16) float m[2][32];          // minus the reference
     float linv[32], r[32];
@@ -137,7 +140,7 @@ __device__ __forceinline__ void load_queries8(const MlaAttendArgs &a, const Atte
 }
 
 template <int NH>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     mla_attend_e4m3_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap rope_map, const MlaAttendArgs a,
                            const AttendPlan g) {
     constexpr int HC = NH / 2;             // rows per softmax thread
@@ -155,6 +158,7 @@ __global__ void __launch_bounds__(352, 1)
     pdl_trigger();
     if (warp == 0) tmem_alloc(&s.tmem, kCols);
     if (tid == 0) {
+        for (int i = 0; i < 4; i++) mbar_init(&s.sc_full[i], 1);
         for (int i = 0; i < 2; i++) {
             for (int p = 0; p < 5; p++) {
                 mbar_init(&s.k_full[i][p], 1);
@@ -177,7 +181,7 @@ __global__ void __launch_bounds__(352, 1)
     bool ok = true;                        // this thread's waits have all ended well
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (!ok) return;
-        if (!warp_wait(bar, parity, deadline, abort, lane)) {
+        if (!warp_wait_now(bar, parity, deadline, abort, lane)) {
             ok = false;
             *abort = 1;
             atomicCAS(a.err, 0, (int)DEV_ERR_TIMEOUT);
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(352, 1)
             const int tok = w.tile() * kTile + t;
             // every row sees the whole tile: the first query's limit is the lowest
             const bool full = (w.tile() + 1) * kTile <= w.len - (a.n_q - 1) && (w.rb + 1) * NH <= g.n_rows;
-            wait(&s.k_full[buf][np], (it >> 1) & 1);                    // the scales
+            wait(&s.sc_full[it & 3], (it >> 2) & 1);
             wait(&s.s_full[buf], (it >> 1) & 1);
             tc_after_sync();
             const float st = tok < w.len ? s.scale[it & 3][t] : 0.f;
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(352, 1)
             for (int k = 0; k < 2; k++)
                 if (32 * k < a.c.R) mma8_ss(d, dr + so + 2 * k, dqr + 2 * k, id_s, true);
             tc_commit(&s.s_full[buf]);
-            tc_commit(&s.k_empty[buf][np]);    // the scales' buffers turn over every fourth tile, which is later than their use
+            tc_commit(&s.k_empty[buf][np]);
         };
         auto output = [&](int it, bool first) {
             const uint32_t buf = it & 1, so = (buf * stage) >> 4, po = (buf * kP8) >> 4;
@@ -444,24 +448,27 @@ __global__ void __launch_bounds__(352, 1)
         }
     } else {
         // ---------------------------------------------------------- bulk copies
-        // two warps, which share a tile's blocks
         const int who = warp - 9;
         BoxAhead box(a, g, s.piece, slot, lane, who == 0);
         int it = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), box.next(), it++) {
-            const int buf = it & 1, sl = box.slot[0];
-            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, sl >= 0)), row = lane * g.pbox;
-            for (int p = who; p <= np; p += 2) {
+            const int buf = it & 1, sl = box.slot[0], nbox = kTile / g.pbox;
+            const uint32_t live = __ballot_sync(0xffffffffu, sl >= 0), boxes = __popc(live);
+            for (int p = who; p <= np; p += kCopyWarps) {
                 if (it > 1) wait(&s.k_empty[buf][p], ((it - 2) >> 1) & 1);
-                if (lane == 0 && ok) mbar_expect_tx(&s.k_full[buf][p], boxes * g.pbox * (p < np ? 128 : 64 + 4));
-                __syncwarp();
-                if (sl < 0 || !ok) continue;
+                if (!ok) continue;
+                expect_bytes(&s.k_full[buf][p], boxes * g.pbox * (p < np ? 128 : 64));
+                if (p == np) expect_bytes(&s.sc_full[it & 3], boxes * g.pbox * 4);
                 const uint32_t dst = base + buf * stage + p * kBlk8;
-                if (p < np) {
-                    tma_box(dst + row * 128, &map, 128 * p, sl, &s.k_full[buf][p]);
-                } else {
-                    tma_box(dst + row * 64, &rope_map, a.c.L, sl, &s.k_full[buf][p]);
-                    bulk_load(&s.scale[it & 3][row], a.c.scales + sl, g.pbox * 4, &s.k_full[buf][p]);
+                for (int j = 0; j < nbox; j++) {
+                    const int y = __shfl_sync(0xffffffffu, sl, j), row = j * g.pbox;
+                    if (!(live >> j & 1)) continue;
+                    if (p < np) {
+                        tma_box(dst + row * 128, &map, 128 * p, y, &s.k_full[buf][p]);
+                    } else {
+                        tma_box(dst + row * 64, &rope_map, a.c.L, y, &s.k_full[buf][p]);
+                        bulk_copy(smem_addr(&s.scale[it & 3][row]), a.c.scales + y, g.pbox * 4, &s.sc_full[it & 3]);
+                    }
                 }
             }
             __syncwarp();
@@ -470,7 +477,10 @@ __global__ void __launch_bounds__(352, 1)
         const uint64_t late = global_ns() + 200000000ull;
         volatile int none = 0;
         for (int k = it > 1 ? it - 2 : 0; k < it; k++)
-            for (int p = who; p <= np; p += 2) warp_wait(&s.k_full[k & 1][p], (k >> 1) & 1, late, &none, lane);
+            for (int p = who; p <= np; p += kCopyWarps) {
+                warp_wait(&s.k_full[k & 1][p], (k >> 1) & 1, late, &none, lane);
+                if (p == np) warp_wait(&s.sc_full[k & 3], (k >> 2) & 1, late, &none, lane);
+            }
     }
     tc_before_sync();
     __syncthreads();
@@ -489,7 +499,7 @@ cudaError_t run(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t st) {
     const size_t smem = 2 * (np * kBlk8 + kRope8) + np * (2 * NH * 128) + 2 * NH * 64 + 2 * kP8 + 1024;
     auto kern = mla_attend_e4m3_kernel<NH>;
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
-    return launch_pdl(kern, dim3(g.n_groups * g.n_slots), dim3(352), smem, st, map, rope, a, g);
+    return launch_pdl(kern, dim3(g.n_groups * g.n_slots), dim3(kThreads), smem, st, map, rope, a, g);
 }
 
 }  // namespace

@@ -110,11 +110,29 @@ __device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&v)[32]) {
         "r"(v[31])
         : "memory");
 }
-// A box of a 2-D tensor map to shared memory; its bytes are counted on `bar`.
+// A box of a 2-D tensor map to shared memory; its bytes are counted on `bar`.  A whole warp with uniform arguments, one
+// thread issues: with per-lane arguments a copy costs the warp some 250 cycles, this way a tenth.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-                 "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y)
-                 : "memory");
+    asm volatile(
+        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+        " @q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n}\n" ::"r"(dst),
+        "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y)
+        : "memory");
+}
+// Contiguous bytes (16-byte aligned, a multiple of 16), likewise.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+        " @q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n}\n" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint64_t *bar, uint32_t bytes) {
+    asm volatile(
+        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+        " @q mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(smem_addr(bar)),
+        "r"(bytes)
+        : "memory");
 }
 // Contiguous bytes (16-byte aligned, a multiple of 16) into L2 only.
 __device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
