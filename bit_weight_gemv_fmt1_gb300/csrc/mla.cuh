@@ -91,7 +91,8 @@ cudaError_t launch_mla_read(const MlaReadArgs &a, bool out_bf16, cudaStream_t st
 // Scratch of a call, and the call (scratch: that many bytes, NULL if none).
 size_t mla_attend_scratch(const MlaAttendArgs &a, int n_sm);
 cudaError_t launch_mla_attend(const MlaAttendArgs &a, void *scratch, int n_sm, cudaStream_t st, int *n_launch);
-cudaError_t launch_mla_prefill(const MlaPrefillArgs &a, cudaStream_t st);
+size_t mla_prefill_scratch(const MlaPrefillArgs &a);
+cudaError_t launch_mla_prefill(const MlaPrefillArgs &a, void *scratch, int n_sm, cudaStream_t st, int *n_launch);
 
 __device__ __forceinline__ void mla_bad_index(int *err) { atomicCAS(err, 0, (int)DEV_ERR_BAD_INDEX); }
 

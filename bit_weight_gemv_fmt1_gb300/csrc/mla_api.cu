@@ -222,7 +222,8 @@ int prefill(int dtype, const void *q, int64_t q_stride, const void *kv, int64_t 
     if (rope < 16 || rope > 64 || rope % 16) return bad(COLI_EINVAL, "rope must be a multiple of 16 in 16..64 (got %d)", rope);
     if (Tq < 0 || Tk < 0 || n_seq < 0 || H < 1 || H > 1024)
         return bad(COLI_EINVAL, "need Tq, Tk, n_seq >= 0 and 1 <= n_heads <= 1024 (got %d, %d, %d, %d)", Tq, Tk, n_seq, H);
-    if ((int64_t)Tq * H > (1LL << 31) - 1) return bad(COLI_EINVAL, "Tq * n_heads is too large");
+    if ((int64_t)Tq * H > (1LL << 31) - 1 || ((int64_t)Tq / 256 + 1 + n_seq) * H > (1LL << 31) - 1)
+        return bad(COLI_EINVAL, "Tq * n_heads or n_seq * n_heads is too large");
     if (q_stride < (int64_t)H * (nope + rope) || kv_stride < (int64_t)H * (nope + v) || kr_stride < rope || q_stride % 8 ||
         kv_stride % 8 || kr_stride % 8)
         return bad(COLI_EINVAL, "strides must be multiples of 8 that hold a token (got %lld, %lld, %lld)", (long long)q_stride,
@@ -242,8 +243,6 @@ int prefill(int dtype, const void *q, int64_t q_stride, const void *kv, int64_t 
     }
     if (int rc = injected_gate()) return rc;
     if (!Tq || !n_seq) return COLI_OK;
-    DevInfo d;
-    if (int rc = device_info((cudaStream_t)stream, 0, &d)) return rc;
     MlaPrefillArgs a{};
     a.q = q;
     a.kv = kv;
@@ -265,8 +264,12 @@ int prefill(int dtype, const void *q, int64_t q_stride, const void *kv, int64_t 
     a.scale = scale;
     a.out = out;
     a.lse = lse;
+    DevInfo d;
+    if (int rc = device_info((cudaStream_t)stream, mla_prefill_scratch(a), &d)) return rc;
     a.err = d.err;
-    return launched(launch_mla_prefill(a, (cudaStream_t)stream), "coli_mla_prefill", 1);
+    int n = 0;
+    const cudaError_t e = launch_mla_prefill(a, d.scratch, d.n_sm, (cudaStream_t)stream, &n);
+    return launched(e, "coli_mla_prefill", n);
 }
 
 // No C++ exception leaves the library.

@@ -1,80 +1,440 @@
-// mla_prefill.cu -- causal attention of packed sequences in the expanded form.
+// mla_prefill.cu -- causal attention of packed sequences in the expanded form,
+// on the 5th-generation tensor cores.
 //
-// One warp per (query row, head): lanes over the dims, one warp-wide dot
-// product a key, the running maximum and sum of the softmax, the weighted sum
-// of the values in registers.  Everything is f32.
+// A CTA takes one head and 256 query rows of one sequence as two tiles A and B
+// of 128, and walks over the keys in tiles of 128:
+//   S = Q K^T   M = 128 queries, N = 128 keys, K = nope + rope (K-major operands in shared memory)
+//   O += P V    M = 128 queries, N = v, K = 128 keys (P in TMEM, V as stored: N-major)
+// The two tiles alternate: while the softmax of one runs, the tensor cores work
+// on the other.  One thread holds one query row; P overwrites S in TMEM.
+//
+// Softmax: x = log2(e) * scale * score, e = 2^(x - m), l += e, P = bf16(e).  m is
+// the row's running maximum, moved (and O and l rescaled) only when a tile's
+// maximum passes it by 8: weights up to 2^8 lose nothing in bf16.  m, l and O are
+// f32; rounding P to bf16 is within 2^-8 of each weight, as the values' own.
+//
+// Bound: the tensor cores, 1280 cycles for 128 x 128 scores (nope + rope = 192, v = 128), of which the
+// exponentials' unit takes up to 1024.  Shared memory holds Q (96 KB), two K tiles (96 KB) and one V
+// tile (32 KB); a V tile is needed a whole softmax later than it is asked for.
+//
+// Keys past a causal row's limit are masked by selection; value rows past the
+// sequence's end belong to its neighbours and are zeroed in shared memory.
+// Warps: 0-3 and 4-7 softmax of A and B, 8 MMA issue, 9 and 10 bulk copies.
+// Every wait is bounded; after one has run out all waits return at once, no
+// further MMA or copy is issued, and the kernel records DEV_ERR_TIMEOUT.
+#include <cudaTypedefs.h>
+
 #include "mla.cuh"
+#include "tcgen05.cuh"
 
 namespace coli {
 
 namespace {
 
-template <bool F32>
-__device__ __forceinline__ float ld(const void *p, long long e) {
-    if constexpr (F32) return reinterpret_cast<const float *>(p)[e];
-    else return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[e]);
-}
+constexpr int kRows = 128;               // rows of a query or key tile
+constexpr uint32_t kBlk = kRows * 128;   // 128 rows x 64 bf16, 128-byte swizzle
+constexpr float kGrow = 8.f;             // log2 of the weight that moves the reference
+constexpr float kNone = -3e38f;          // reference of a row that has seen no key
 
-template <bool F32>
-__global__ void __launch_bounds__(128) mla_prefill_kernel(const MlaPrefillArgs a) {
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);   // query * H + head
+struct Shared {
+    uint64_t q_full[2], k_full[2], k_empty[2], v_full, v_empty, s_full[2], p_full[2], o_full[2];
+    uint32_t tmem;
+    int abort;
+    int b, q0, nq, nk, qrow, krow;       // sequence, first query of the pair in it, its sizes, first rows
+};
+
+template <int V>
+__global__ void __launch_bounds__(352, 1)
+    mla_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
+                       const __grid_constant__ CUtensorMap kr_map, const MlaPrefillArgs a, int max_pairs, long long timeout_ns) {
+    extern __shared__ uint8_t raw[];
+    __shared__ Shared s;
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    uint8_t *sm = raw + (base - smem_addr(raw));
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int nn = a.nope / 64, nb = nn + 1;             // blocks of a query or key tile: no-position part, rotary part
+    const uint32_t k_off = 2 * nb * kBlk, v_off = k_off + 2 * nb * kBlk;
+    const int head = blockIdx.x / max_pairs, idx = blockIdx.x - head * max_pairs;
     pdl_wait();
     pdl_trigger();
-    if (row >= (long long)a.Tq * a.H) return;
-    const int i = (int)(row / a.H), h = (int)(row - (long long)i * a.H);
-    int lo = 0, hi = a.n_seq;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu_q[mid] <= i) lo = mid;
-        else hi = mid;
-    }
-    const int k0 = a.cu_k[lo], nk = a.cu_k[lo + 1] - k0, nq = a.cu_q[lo + 1] - a.cu_q[lo];
-    if (k0 < 0 || nk < 0 || k0 > a.Tk - nk) {
-        if (lane == 0) mla_bad_index(a.err);
-        return;
-    }
-    const int limit = i - a.cu_q[lo] + nk - nq + 1;
-    const int dk = a.nope + a.rope;
-    float q[6], o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < 6; k++) q[k] = 32 * k + lane < dk ? ld<F32>(a.q, i * a.q_stride + (long long)h * dk + 32 * k + lane) : 0.f;
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < limit; j++) {
-        const long long kb = (k0 + j) * a.kv_stride + (long long)h * (a.nope + a.v);
-        float dot = 0.f;
-#pragma unroll
-        for (int k = 0; k < 6; k++) {
-            const int d = 32 * k + lane;
-            if (d < a.nope) dot = fmaf(q[k], ld<F32>(a.kv, kb + d), dot);
-            else if (d < dk) dot = fmaf(q[k], ld<F32>(a.k_rope, (k0 + j) * a.kr_stride + d - a.nope), dot);
+    if (warp == 1) {
+        // this CTA's pair: the last pairs of the sequences, whose rows see most keys, come first
+        int total = 0;
+        for (int b = lane; b < a.n_seq; b += 32) {
+            const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+            const bool good = q0 >= 0 && q1 >= q0 && q1 <= a.Tq && k0 >= 0 && k1 >= k0 && k1 <= a.Tk;
+            if (!good) mla_bad_index(a.err);
+            total += good ? (q1 - q0 + 2 * kRows - 1) / (2 * kRows) : 0;
         }
-        const float s = warp_sum(dot) * a.scale;
-        const float mn = fmaxf(m, s);
-        const float f = mn == -INFINITY ? 1.f : expf(m - mn), p = mn == -INFINITY ? 0.f : expf(s - mn);
-        l = fmaf(l, f, p);
+        total = __reduce_add_sync(0xffffffffu, total);
+        int p = total - 1 - idx, run = 0;
+        if (lane == 0) s.b = -1;
+        __syncwarp();
+        for (int b0 = 0; b0 < a.n_seq && p >= 0; b0 += 32) {
+            const int b = b0 + lane;
+            int n = 0, q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+            if (b < a.n_seq) {
+                q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+                const bool good = q0 >= 0 && q1 >= q0 && q1 <= a.Tq && k0 >= 0 && k1 >= k0 && k1 <= a.Tk;
+                n = good ? (q1 - q0 + 2 * kRows - 1) / (2 * kRows) : 0;
+            }
+            int incl = n;
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-            if (32 * k + lane < a.v) o[k] = fmaf(o[k], f, p * ld<F32>(a.kv, kb + a.nope + 32 * k + lane));
-        m = mn;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const int before = run + incl - n;
+            if (n > 0 && before <= p && p < before + n) {
+                s.b = b;
+                s.q0 = (p - before) * 2 * kRows;
+                s.nq = q1 - q0;
+                s.nk = k1 - k0;
+                s.qrow = q0;
+                s.krow = k0;
+            }
+            run += __shfl_sync(0xffffffffu, incl, 31);
+        }
     }
+    if (warp == 0) tmem_alloc(&s.tmem, 512);
+    if (tid == 0) {
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&s.q_full[i], 1);
+            mbar_init(&s.k_full[i], 1);
+            mbar_init(&s.k_empty[i], 1);
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.p_full[i], 4);
+            mbar_init(&s.o_full[i], 1);
+        }
+        mbar_init(&s.v_full, 1);
+        mbar_init(&s.v_empty, 1);
+        s.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
+    const uint64_t deadline = global_ns() + (uint64_t)timeout_ns;
+    volatile int *abort = &s.abort;
+    bool ok = true;                      // this thread's waits have all ended well
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!ok) return;
+        if (!warp_wait_now(bar, parity, deadline, abort, lane)) {
+            ok = false;
+            *abort = 1;
+            atomicCAS(a.err, 0, (int)DEV_ERR_TIMEOUT);
+        }
+    };
+    // key tiles that the rows of tile x see: the last live row's limit
+    const bool live = s.b >= 0;
+    const int q0 = s.q0, nq = s.nq, nk = s.nk;
+    auto tiles = [&](int x) {
+        const int rows = live ? min(kRows, nq - q0 - x * kRows) : 0;
+        const int limit = rows > 0 ? q0 + x * kRows + rows - 1 + nk - nq + 1 : 0;
+        return limit > 0 ? (min(limit, nk) + kRows - 1) / kRows : 0;
+    };
+    const int nt[2] = {tiles(0), tiles(1)}, n = max(nt[0], nt[1]);
+
+    if (warp < 8) {
+        // ---------------------------------------------------------- softmax and output
+        const int x = warp >> 2, t = tid & 127, row = q0 + x * kRows + t;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), S = lanes + x * 128, O = lanes + 256 + x * V;
+        const int limit = row + nk - nq + 1;             // keys this row sees
+        const int first_limit = q0 + x * kRows + nk - nq + 1;
+        const float f = a.scale * 1.4426950408889634f;
+        float m = kNone;
+        float2 l2 = make_float2(0.f, 0.f);
+        for (int j = 0; j < nt[x]; j++) {
+            wait(&s.s_full[x], j & 1);
+            tc_after_sync();
+            const int k0 = j * kRows;
+            const bool full = k0 + kRows <= first_limit && k0 + kRows <= nk;   // every row sees the whole tile
+            const int seen = full ? kRows : min(limit, nk) - k0;              // this row's keys in the tile
+            // the tile's maximum (minimum for a negative scale) of the raw scores
+            float top = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-        const int d = 32 * k + lane;
-        if (d >= a.v) continue;
-        const float r = l != 0.f ? o[k] / l : 0.f;
-        if (a.out_bf16) reinterpret_cast<__nv_bfloat16 *>(a.out)[row * a.v + d] = __float2bfloat16_rn(r);
-        else reinterpret_cast<float *>(a.out)[row * a.v + d] = r;
+            for (int c0 = 0; c0 < kRows; c0 += 32) {
+                uint32_t v[32];
+                tmem_ld(S + c0, v);
+                tmem_ld_wait();
+                if (!full)
+#pragma unroll
+                    for (int c = 0; c < 32; c++)
+                        if (c0 + c >= seen) v[c] = f < 0.f ? 0x7F800000u : 0xFF800000u;
+                if (f < 0.f)
+#pragma unroll
+                    for (int c = 0; c < 32; c++) v[c] ^= 0x80000000u;
+                float t4[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) t4[k] = __uint_as_float(v[k]);
+#pragma unroll
+                for (int c = 4; c < 32; c += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        t4[k] = fmaxf(t4[k], c + 4 + k < 32 ? fmaxf(__uint_as_float(v[c + k]), __uint_as_float(v[c + 4 + k])) : __uint_as_float(v[c + k]));
+                top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+            }
+            const float now = top * fabsf(f);
+            const bool move = now > m + kGrow;
+            if (__any_sync(0xffffffffu, move)) {
+                const float r = move ? ex2(m - now) : 1.f;
+                if (move) m = now;
+                l2 = fmul2(l2, make_float2(r, r));
+                if (j > 0) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < V; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld(O + c0, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 32; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * r);
+                        tmem_st(O + c0, o);
+                    }
+                    tmem_st_wait();
+                }
+            }
+            const float2 f2 = make_float2(f, f), m2 = make_float2(-m, -m);
+#pragma unroll
+            for (int c0 = 0; c0 < kRows; c0 += 32) {
+                uint32_t v[32], p[16];
+                tmem_ld(S + c0, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    float2 y = m2;
+                    ffma2(y, make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f2);
+                    y = make_float2(ex2(y.x), ex2(y.y));
+                    if (!full) {
+                        if (c0 + c >= seen) y.x = 0.f;
+                        if (c0 + c + 1 >= seen) y.y = 0.f;
+                    }
+                    l2 = fadd2(l2, y);
+                    p[c / 2] = pack_bf16(y.x, y.y);
+                }
+                tmem_st(S + c0 / 2, p);                  // over scores that have been read
+            }
+            if (k0 + kRows > nk) {
+                // value rows of other sequences may hold anything, and 0 * NaN is NaN
+                wait(&s.v_full, j & 1);
+                if (k0 + t >= nk)
+#pragma unroll
+                    for (int k = 0; k < V / 64; k++)
+#pragma unroll
+                        for (int u = 0; u < 8; u++) *reinterpret_cast<uint4 *>(sm + v_off + k * kBlk + t * 128 + 16 * u) = make_uint4(0u, 0u, 0u, 0u);
+                fence_async_smem();
+            }
+            tmem_st_wait();
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0 && ok) mbar_arrive(&s.p_full[x]);
+        }
+        const bool store = live && row < nq;
+        const float l = l2.x + l2.y;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        const long long orow = ((long long)(s.qrow + row) * a.H + head);
+        if (nt[x] > 0) {
+            wait(&s.o_full[x], 0);
+            tc_after_sync();
+        }
+#pragma unroll 1
+        for (int c0 = 0; c0 < V; c0 += 32) {
+            uint32_t o[32];
+            if (nt[x] > 0) {
+                tmem_ld(O + c0, o);
+                tmem_ld_wait();
+            } else {
+#pragma unroll
+                for (int c = 0; c < 32; c++) o[c] = 0u;
+            }
+            if (!store) continue;
+#pragma unroll
+            for (int c = 0; c < 32; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
+            if (a.out_bf16) {
+                uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * V + c0);
+#pragma unroll
+                for (int c = 0; c < 32; c += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; k++) w[k] = pack_bf16(__uint_as_float(o[c + 2 * k]), __uint_as_float(o[c + 2 * k + 1]));
+                    d[c / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            } else {
+                uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<float *>(a.out) + orow * V + c0);
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) d[c / 4] = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+            }
+        }
+        if (store && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    } else if (warp == 8) {
+        // ---------------------------------------------------------- MMA issue
+        constexpr uint32_t id_s = f16_idesc(1, false, false, kRows, kRows), id_o = f16_idesc(1, false, true, kRows, V);
+        const uint64_t dq = sw128_desc(base, 16, 1024), dk = sw128_desc(base + k_off, 16, 1024), dv = sw128_desc(base + v_off, kBlk, 1024);
+        auto scores = [&](int x, int j) {
+            if (!ok) return;
+            const uint64_t qa = dq + ((x * nb * kBlk) >> 4), ka = dk + (((j & 1) * nb * kBlk) >> 4);
+            for (int b = 0; b < nn; b++)
+#pragma unroll
+                for (int k = 0; k < 4; k++) mma_ss(tmem + x * 128, qa + ((b * kBlk) >> 4) + 2 * k, ka + ((b * kBlk) >> 4) + 2 * k, id_s, b || k);
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                if (16 * k < a.rope) mma_ss(tmem + x * 128, qa + ((nn * kBlk) >> 4) + 2 * k, ka + ((nn * kBlk) >> 4) + 2 * k, id_s, true);
+            tc_commit(&s.s_full[x]);
+        };
+        auto output = [&](int x, int j) {
+            if (!ok) return;
+#pragma unroll
+            for (int k = 0; k < 8; k++) mma_ts(tmem + 256 + x * V, tmem + x * 128 + 8 * k, dv + ((k * 2048) >> 4), id_o, j || k);
+        };
+        if (n > 0) wait(&s.k_full[0], 0);
+        for (int x = 0; x < 2; x++)
+            if (nt[x] > 0) {
+                wait(&s.q_full[x], 0);
+                tc_after_sync();
+                scores(x, 0);
+            }
+        if (n > 0 && ok) tc_commit(&s.k_empty[0]);
+        for (int j = 0; j < n; j++) {
+            wait(&s.v_full, j & 1);
+            if (j + 1 < n) wait(&s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
+            for (int x = 0; x < 2; x++) {
+                if (j >= nt[x]) continue;
+                wait(&s.p_full[x], j & 1);
+                tc_after_sync();
+                output(x, j);
+                if (j + 1 < nt[x]) scores(x, j + 1);
+                else if (ok) tc_commit(&s.o_full[x]);
+            }
+            if (!ok) continue;
+            tc_commit(&s.v_empty);
+            if (j + 1 < n) tc_commit(&s.k_empty[(j + 1) & 1]);
+        }
+    } else {
+        // ---------------------------------------------------------- bulk copies: queries and keys, values
+        const int hk = head * (a.nope + V), hq = head * (a.nope + a.rope);
+        if (warp == 9) {
+            for (int j = 0; j < n; j++) {
+                const int buf = j & 1;
+                if (j > 1) wait(&s.k_empty[buf], ((j - 2) >> 1) & 1);
+                if (!ok) break;
+                const uint32_t dst = base + k_off + buf * nb * kBlk;
+                expect_bytes(&s.k_full[buf], nb * kBlk);
+                for (int b = 0; b < nn; b++) tma_box(dst + b * kBlk, &kv_map, hk + 64 * b, s.krow + j * kRows, &s.k_full[buf]);
+                tma_box(dst + nn * kBlk, &kr_map, 0, s.krow + j * kRows, &s.k_full[buf]);
+                if (j == 0)
+                    for (int x = 0; x < 2; x++) {
+                        if (nt[x] == 0) continue;
+                        expect_bytes(&s.q_full[x], nb * kBlk);
+                        for (int b = 0; b < nb; b++) tma_box(base + (x * nb + b) * kBlk, &q_map, hq + 64 * b, s.qrow + q0 + x * kRows, &s.q_full[x]);
+                    }
+            }
+        } else {
+            for (int j = 0; j < n; j++) {
+                if (j > 0) wait(&s.v_empty, (j - 1) & 1);
+                if (!ok) break;
+                expect_bytes(&s.v_full, (V / 64) * kBlk);
+                for (int b = 0; b < V / 64; b++) tma_box(base + v_off + b * kBlk, &kv_map, hk + a.nope + 64 * b, s.krow + j * kRows, &s.v_full);
+            }
+        }
+        // every copy has landed before the CTA may end (those not waited for by an MMA that was issued: after a timeout)
+        if (!ok || *abort) {
+            const uint64_t late = global_ns() + 200000000ull;
+            while (global_ns() < late) __nanosleep(1000);
+        }
     }
-    if (a.lse && lane == 0) a.lse[row] = l != 0.f ? m + logf(l) : -INFINITY;
+    tc_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+        tc_after_sync();
+        tmem_free(tmem, 512);
+    }
 }
+
+// f32 -> bf16, rows of `cols` (a multiple of 8) at `stride` to packed ones.
+__global__ void __launch_bounds__(256) mla_round_kernel(const float *src, long long stride, long long rows, int cols, __nv_bfloat16 *dst) {
+    pdl_wait();
+    pdl_trigger();
+    const int units = cols / 8;
+    const long long n = rows * units;
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
+        const long long r = i / units;
+        const int u = (int)(i - r * units);
+        const float4 x = *reinterpret_cast<const float4 *>(src + r * stride + 8 * u), y = *reinterpret_cast<const float4 *>(src + r * stride + 8 * u + 4);
+        reinterpret_cast<uint4 *>(dst)[i] = make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+    }
+}
+
+cudaError_t matrix_map(const void *p, long long cols, long long rows, long long stride, CUtensorMap *out) {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return (PFN_cuTensorMapEncodeTiled_v12000)f;
+    }();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {64, kRows}, estr[2] = {1, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+template <int V>
+cudaError_t run(const MlaPrefillArgs &a, cudaStream_t st) {
+    CUtensorMap q, kv, kr;
+    if (cudaError_t e = matrix_map(a.q, (long long)a.H * (a.nope + a.rope), a.Tq, a.q_stride, &q)) return e;
+    kv = kr = q;                         // no keys: never read
+    if (a.Tk > 0) {
+        if (cudaError_t e = matrix_map(a.kv, (long long)a.H * (a.nope + V), a.Tk, a.kv_stride, &kv)) return e;
+        if (cudaError_t e = matrix_map(a.k_rope, a.rope, a.Tk, a.kr_stride, &kr)) return e;
+    }
+    const int nb = a.nope / 64 + 1, max_pairs = (a.Tq + 2 * kRows - 1) / (2 * kRows) + a.n_seq - 1;
+    const size_t smem = (size_t)(4 * nb + V / 64) * kBlk + 1024;
+    auto kern = mla_prefill_kernel<V>;
+    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+    return launch_pdl(kern, dim3((unsigned)max_pairs * a.H), dim3(352), smem, st, q, kv, kr, a, max_pairs, 2000000000LL);
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-cudaError_t launch_mla_prefill(const MlaPrefillArgs &a, cudaStream_t st) {
-    const dim3 grid((unsigned)(((long long)a.Tq * a.H + 3) / 4));
-    return a.in_f32 ? launch_pdl(mla_prefill_kernel<true>, grid, dim3(128), 0, st, a)
-                    : launch_pdl(mla_prefill_kernel<false>, grid, dim3(128), 0, st, a);
+size_t mla_prefill_scratch(const MlaPrefillArgs &a) {
+    if (!a.in_f32) return 0;
+    return round256((size_t)a.Tq * a.H * (a.nope + a.rope) * 2) + round256((size_t)a.Tk * a.H * (a.nope + a.v) * 2) +
+           round256((size_t)a.Tk * a.rope * 2);
+}
+
+cudaError_t launch_mla_prefill(const MlaPrefillArgs &a0, void *scratch, int n_sm, cudaStream_t st, int *n_launch) {
+    MlaPrefillArgs a = a0;
+    *n_launch = 1;
+    if (a.in_f32) {
+        const int cols[3] = {a.H * (a.nope + a.rope), a.H * (a.nope + a.v), a.rope};
+        const long long rows[3] = {a.Tq, a.Tk, a.Tk}, strides[3] = {a.q_stride, a.kv_stride, a.kr_stride};
+        const void *src[3] = {a.q, a.kv, a.k_rope};
+        __nv_bfloat16 *dst[3];
+        char *at = (char *)scratch;
+        for (int i = 0; i < 3; i++) {
+            dst[i] = (__nv_bfloat16 *)at;
+            at += round256((size_t)rows[i] * cols[i] * 2);
+            const long long want = (rows[i] * (cols[i] / 8) + 255) / 256;
+            if (want == 0) continue;
+            if (cudaError_t e = launch_pdl(mla_round_kernel, dim3((unsigned)(want < 32LL * n_sm ? want : 32LL * n_sm)), dim3(256), 0, st,
+                                           (const float *)src[i], strides[i], rows[i], cols[i], dst[i]))
+                return e;
+            ++*n_launch;
+        }
+        a.q = dst[0];
+        a.kv = dst[1];
+        a.k_rope = dst[2];
+        a.q_stride = cols[0];
+        a.kv_stride = cols[1];
+        a.kr_stride = cols[2];
+    }
+    return a.v == 64 ? run<64>(a, st) : run<128>(a, st);
 }
 
 }  // namespace coli
