@@ -99,10 +99,26 @@ def _check(rc: int):
         raise ColiError(rc, _lib.coli_last_error().decode())
 
 
+_torch = None
+_raw_stream = None
+
+
+def _load_torch():
+    """torch, imported at first use (uploads and the host calls do without it)."""
+    global _torch, _raw_stream
+    import torch
+    _torch = torch
+    # the handle of the current stream without building a Stream object (3 us a call), where torch has it
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _DTYPES.update({torch.float32: COLI_F32, torch.bfloat16: COLI_BF16, torch.float8_e4m3fn: COLI_E4M3})
+    return torch
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        torch = _torch or _load_torch()
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -281,38 +297,36 @@ def moe_block_noalloc(x, table: ExpertTable, ids, w, y, dev_error, stream=None):
 
 
 COLI_F32, COLI_BF16, COLI_E4M3 = 0, 1, 2
+_DTYPES: dict = {}
 
 
 def _refuse(msg: str):
     raise ColiError(COLI_EINVAL, msg)
 
 
-_DTYPES: dict = {}
-
-
 def _dtype(t) -> int:
     """The library's element type of a tensor (COLI_EFMT for one it has not)."""
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: COLI_F32, torch.bfloat16: COLI_BF16, torch.float8_e4m3fn: COLI_E4M3})
+    if _torch is None:
+        _load_torch()
     d = _DTYPES.get(t.dtype)
     if d is None:
         raise ColiError(COLI_EFMT, f"no element type for {t.dtype}")
     return d
 
 
-def _typed(t, kind: str, name: str):
-    """t is a contiguous CUDA tensor of torch type `kind`."""
-    if str(t.dtype) != kind or not t.is_cuda or not t.is_contiguous():
+def _packed(t, kind, name: str) -> int:
+    """Address of t, a contiguous CUDA tensor of torch type `kind`."""
+    if t.dtype is not kind or not t.is_cuda or not t.is_contiguous():
         _refuse(f"{name} must be a contiguous {kind} CUDA tensor")
+    return t.data_ptr()
 
 
 def _rows3(t, name: str) -> int:
     """Stride of the rows of t [T, heads, n]: rows of one stride over tokens and heads, elements packed."""
     T, H, n = t.shape
-    s = t.stride()
-    ld = s[1] if H > 1 else s[0] if T > 1 else n
-    if not t.is_cuda or (n > 1 and s[2] != 1) or (T > 1 and H > 0 and s[0] != H * ld):
+    s0, s1, s2 = t.stride()
+    ld = s1 if H > 1 else s0 if T > 1 else n
+    if not t.is_cuda or (n > 1 and s2 != 1) or (T > 1 and s0 != H * ld):
         _refuse(f"{name} must be a CUDA tensor whose [tokens, heads] rows have one stride")
     return ld
 
@@ -321,12 +335,19 @@ def _tokens(t, name: str) -> int:
     """Token stride of t [T, ...] whose tokens are packed."""
     if not t.is_cuda:
         _refuse(f"{name} must be a CUDA tensor")
-    n = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != n:
+    shape, stride, n = t.shape, t.stride(), 1
+    for i in range(len(shape) - 1, 0, -1):
+        if stride[i] != n and shape[i] != 1:
             _refuse(f"a token of {name} must be packed")
-        n *= size
-    return t.stride(0) if t.shape[0] > 1 else n
+        n *= shape[i]
+    return stride[0] if shape[0] > 1 else n
+
+
+def _pages(pages, n_seq: int) -> int:
+    n, width = pages.shape
+    if pages.dtype is not _torch.int32 or not pages.is_cuda or n != n_seq or (width > 1 and pages.stride(1) != 1):
+        _refuse("pages must be an int32 CUDA tensor [n_seq, n] with packed rows")
+    return pages.stride(0) if n > 1 else width
 
 
 class MlaCache:
@@ -335,13 +356,13 @@ class MlaCache:
     with scales float32 [n_pages, page_size].  Keeps the tensors alive."""
 
     def __init__(self, rows, latent: int, rope: int, scales=None):
+        d = _dtype(rows)
         if rows.dim() != 3 or not rows.is_contiguous() or not rows.is_cuda or rows.shape[2] != latent + rope:
             _refuse("rows must be a contiguous CUDA tensor [n_pages, page_size, latent + rope]")
-        d = _dtype(rows)
         if d == COLI_E4M3:
-            if scales is None or tuple(scales.shape) != tuple(rows.shape[:2]):
+            if scales is None or scales.shape != rows.shape[:2]:
                 _refuse("an e4m3 cache needs scales [n_pages, page_size]")
-            _typed(scales, "torch.float32", "scales")
+            _packed(scales, _torch.float32, "scales")
         elif scales is not None:
             _refuse("only an e4m3 cache has scales")
         self.rows, self.scales = rows, scales
@@ -353,91 +374,92 @@ class MlaCache:
 def mla_query(q, pos, rot, out_nope, out_rope, interleaved: bool = False, stream=None):
     """Split q [T, heads, nope + rope] into out_nope [T, heads, nope] and the rotated out_rope [T, heads, rope]
     (f32 or bf16 each, possibly two parts of one tensor; out_nope None: nope = 0).  rot [n_pos, rope] = cos | sin."""
+    torch = _torch or _load_torch()
     T, H, n = q.shape
-    R = out_rope.shape[2]
+    T2, H2, R = out_rope.shape
+    n_pos, R2 = rot.shape
     N = n - R
-    if str(q.dtype) != "torch.float32" or tuple(out_rope.shape[:2]) != (T, H) or pos.shape[0] != T or rot.shape[1] != R or \
-            (N if out_nope is None else tuple(out_nope.shape) != (T, H, N)):
+    if q.dtype is not torch.float32 or T2 != T or H2 != H or pos.shape[0] != T or R2 != R or \
+            (N != 0 if out_nope is None else out_nope.shape != (T, H, N)):
         _refuse("mla_query: q must be float32 [T, heads, nope + rope] and the others must match it")
-    _typed(pos, "torch.int32", "pos")
-    _typed(rot, "torch.float32", "rot")
-    _check(_lib.coli_mla_query(_ptr(q), _tokens(q, "q"), T, H, N, R, _ptr(pos), _ptr(rot), rot.shape[0], int(interleaved),
-                               0 if out_nope is None else _dtype(out_nope), _ptr(out_nope),
-                               0 if out_nope is None else _rows3(out_nope, "out_nope"),
-                               _dtype(out_rope), _ptr(out_rope), _rows3(out_rope, "out_rope"), _stream(stream)))
+    if out_nope is None:
+        dn = pn = ln = 0
+    else:
+        dn, pn, ln = _dtype(out_nope), out_nope.data_ptr(), _rows3(out_nope, "out_nope")
+    rc = _lib.coli_mla_query(q.data_ptr(), _tokens(q, "q"), T, H, N, R, _packed(pos, torch.int32, "pos"),
+                             _packed(rot, torch.float32, "rot"), n_pos, interleaved, dn, pn, ln, _dtype(out_rope),
+                             out_rope.data_ptr(), _rows3(out_rope, "out_rope"), _stream(stream))
+    if rc:
+        _check(rc)
     return out_nope, out_rope
 
 
 def mla_append(cache: MlaCache, kv, norm, eps: float, pos, rot, slots, interleaved: bool = False, stream=None):
     """Norm (norm None: none), rotate, quantise and store kv [T, latent + rope] at slots [T] of the cache."""
+    torch = _torch or _load_torch()
     T, n = kv.shape
-    if str(kv.dtype) != "torch.float32" or n != cache.latent + cache.rope or pos.shape[0] != T or slots.shape[0] != T or \
-            rot.shape[1] != cache.rope or (norm is not None and norm.shape[0] != cache.latent):
+    n_pos, R = rot.shape
+    if kv.dtype is not torch.float32 or n != cache.latent + R or R != cache.rope or pos.shape[0] != T or \
+            slots.shape[0] != T or (norm is not None and norm.shape[0] != cache.latent):
         _refuse("mla_append: kv must be float32 [T, latent + rope] and the others must match it and the cache")
-    _typed(pos, "torch.int32", "pos")
-    _typed(slots, "torch.int64", "slots")
-    _typed(rot, "torch.float32", "rot")
-    if norm is not None:
-        _typed(norm, "torch.float32", "norm")
-    _check(_lib.coli_mla_append(cache._p, _ptr(kv), _tokens(kv, "kv"), T, _ptr(norm), float(eps), _ptr(pos), _ptr(rot),
-                                rot.shape[0], int(interleaved), _ptr(slots), _stream(stream)))
-
-
-def _pages(pages, n_seq: int) -> int:
-    if str(pages.dtype) != "torch.int32" or not pages.is_cuda or pages.shape[0] != n_seq or \
-            (pages.shape[1] > 1 and pages.stride(1) != 1):
-        _refuse("pages must be an int32 CUDA tensor [n_seq, n] with packed rows")
-    return pages.stride(0) if n_seq > 1 else pages.shape[1]
+    rc = _lib.coli_mla_append(cache._p, kv.data_ptr(), _tokens(kv, "kv"), T,
+                              None if norm is None else _packed(norm, torch.float32, "norm"), eps,
+                              _packed(pos, torch.int32, "pos"), _packed(rot, torch.float32, "rot"), n_pos, interleaved,
+                              _packed(slots, torch.int64, "slots"), _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def mla_read(cache: MlaCache, pages, cu, out, stream=None):
     """Read the first cu[b+1] - cu[b] tokens of each sequence b back into out [T, latent + rope] (f32 or bf16)."""
+    torch = _torch or _load_torch()
     n_seq = cu.shape[0] - 1
     T, n = out.shape
     if n != cache.latent + cache.rope:
         _refuse("mla_read: out must have latent + rope columns")
-    _typed(cu, "torch.int32", "cu")
-    _check(_lib.coli_mla_read(cache._p, _ptr(pages), _pages(pages, n_seq), n_seq, _ptr(cu), T, _dtype(out), _ptr(out),
-                              _tokens(out, "out"), _stream(stream)))
+    rc = _lib.coli_mla_read(cache._p, pages.data_ptr(), _pages(pages, n_seq), n_seq, _packed(cu, torch.int32, "cu"), T,
+                            _dtype(out), out.data_ptr(), _tokens(out, "out"), _stream(stream))
+    if rc:
+        _check(rc)
     return out
 
 
 def mla_attend(cache: MlaCache, q_latent, q_rope, pages, lens, scale: float, out, lse=None, stream=None):
     """Absorbed attention of q_latent [n_seq, n_q, heads, latent] and q_rope [n_seq, n_q, heads, rope] over the cached
     tokens (lens [n_seq] int32, the new ones included) into out [n_seq, n_q, heads, latent]; lse f32 [n_seq, n_q, heads]."""
+    torch = _torch or _load_torch()
     B, n_q, H, n = q_latent.shape
-    if n != cache.latent or tuple(q_rope.shape) != (B, n_q, H, cache.rope) or out.shape != q_latent.shape or \
-            q_rope.dtype != q_latent.dtype or lens.shape[0] != B or (lse is not None and tuple(lse.shape) != (B, n_q, H)):
+    kind = q_latent.dtype
+    if n != cache.latent or q_rope.shape != (B, n_q, H, cache.rope) or out.shape != q_latent.shape or \
+            lens.shape[0] != B or (lse is not None and lse.shape != (B, n_q, H)):
         _refuse("mla_attend: q_latent, q_rope, lens, out and lse must match one another and the cache")
-    if not (q_latent.is_contiguous() and q_rope.is_contiguous() and out.is_contiguous() and out.is_cuda and q_latent.is_cuda):
-        _refuse("mla_attend: q_latent, q_rope and out must be contiguous CUDA tensors")
-    _typed(lens, "torch.int32", "lens")
-    if lse is not None:
-        _typed(lse, "torch.float32", "lse")
-    _check(_lib.coli_mla_attend(cache._p, _dtype(q_latent), _ptr(q_latent), _ptr(q_rope), B, n_q, H, _ptr(pages),
-                                _pages(pages, B), _ptr(lens), float(scale), _dtype(out), _ptr(out), _ptr(lse), _stream(stream)))
+    rc = _lib.coli_mla_attend(cache._p, _dtype(q_latent), _packed(q_latent, kind, "q_latent"), _packed(q_rope, kind, "q_rope"),
+                              B, n_q, H, pages.data_ptr(), _pages(pages, B), _packed(lens, torch.int32, "lens"), scale,
+                              _dtype(out), _packed(out, out.dtype, "out"),
+                              None if lse is None else _packed(lse, torch.float32, "lse"), _stream(stream))
+    if rc:
+        _check(rc)
     return out
 
 
 def mla_prefill(q, kv, k_rope, cu_q, cu_k, scale: float, out, lse=None, stream=None):
     """Causal attention of packed sequences: q [Tq, heads, nope + rope], kv [Tk, heads, nope + v], k_rope [Tk, rope]
     (all bf16 or all f32) into out [Tq, heads, v]; cu_q, cu_k int32 [n_seq + 1]; lse f32 [Tq, heads]."""
+    torch = _torch or _load_torch()
     Tq, H, dk = q.shape
-    Tk, R, V = kv.shape[0], k_rope.shape[1], out.shape[2]
+    Tk, R = k_rope.shape
+    V = out.shape[2]
     N = dk - R
-    if tuple(kv.shape[1:]) != (H, N + V) or k_rope.shape[0] != Tk or tuple(out.shape[:2]) != (Tq, H) or \
-            cu_q.shape != cu_k.shape or kv.dtype != q.dtype or k_rope.dtype != q.dtype or \
-            (lse is not None and tuple(lse.shape) != (Tq, H)):
+    if kv.shape != (Tk, H, N + V) or out.shape != (Tq, H, V) or cu_q.shape != cu_k.shape or kv.dtype is not q.dtype or \
+            k_rope.dtype is not q.dtype or (lse is not None and lse.shape != (Tq, H)):
         _refuse("mla_prefill: q, kv, k_rope, cu_q, cu_k, out and lse must match one another")
-    if not (out.is_contiguous() and out.is_cuda):
-        _refuse("mla_prefill: out must be a contiguous CUDA tensor")
-    _typed(cu_q, "torch.int32", "cu_q")
-    _typed(cu_k, "torch.int32", "cu_k")
-    if lse is not None:
-        _typed(lse, "torch.float32", "lse")
-    _check(_lib.coli_mla_prefill(_dtype(q), _ptr(q), _tokens(q, "q"), _ptr(kv), _tokens(kv, "kv"), _ptr(k_rope),
-                                 _tokens(k_rope, "k_rope"), Tq, Tk, cu_q.shape[0] - 1, _ptr(cu_q), _ptr(cu_k), H, N, R, V,
-                                 float(scale), _dtype(out), _ptr(out), _ptr(lse), _stream(stream)))
+    rc = _lib.coli_mla_prefill(_dtype(q), q.data_ptr(), _tokens(q, "q"), kv.data_ptr(), _tokens(kv, "kv"), k_rope.data_ptr(),
+                               _tokens(k_rope, "k_rope"), Tq, Tk, cu_q.shape[0] - 1, _packed(cu_q, torch.int32, "cu_q"),
+                               _packed(cu_k, torch.int32, "cu_k"), H, N, R, V, scale, _dtype(out),
+                               _packed(out, out.dtype, "out"), None if lse is None else _packed(lse, torch.float32, "lse"),
+                               _stream(stream))
+    if rc:
+        _check(rc)
     return out
 
 
