@@ -57,37 +57,40 @@ struct Shared {
     float red[4][64];
 };
 
-// This warp's query rows of a block of N -> bf16 operand [L/64 + 1][N][64], 128-byte swizzle.
+// The query rows of a block of N -> bf16 operand [L/64 + 1][N][64], 128-byte swizzle.  The softmax threads share
+// the block's units of 8 elements, nine loads in flight each.
 template <int N, bool QB>
 __device__ __forceinline__ void load_queries(const MlaAttendArgs &a, const AttendPlan &g, Shared &s, uint8_t *qsm, int b, int rb, int len,
-                                             int warp, int lane) {
-    constexpr int RB = QB ? 4 : 2;         // rows in flight per warp
-    const int nu = a.c.L / 8, nr = a.c.R / 8;
+                                             int tid) {
+    constexpr int F = QB ? 9 : 5, W = QB ? 1 : 2;
+    const int upr = (a.c.L + a.c.R) / 8, total = N * upr;
+    if (tid < N) {
+        const int r = rb * N + tid;
+        s.f[tid] = a.scale * 1.4426950408889634f;
+        s.limit[tid] = r < g.n_rows ? len - (a.n_q - 1 - r / a.H) : 0;
+    }
 #pragma unroll 1
-    for (int c0 = warp; c0 < N; c0 += 8 * RB) {
-        QueryRow<QB> x[RB];
+    for (int i0 = tid; i0 < total; i0 += F * kSoft) {
+        uint4 x[F][W];
 #pragma unroll
-        for (int i = 0; i < RB; i++) {
-            const int r = rb * N + c0 + 8 * i;
-            x[i].load(a, (long long)b * g.n_rows + r, c0 + 8 * i < N && r < g.n_rows, lane);
+        for (int f = 0; f < F; f++) {
+            const int i = i0 + f * kSoft, c = i / upr, u = i - c * upr, r = rb * N + c;
+            const bool live = i < total && r < g.n_rows;
+            const uint4 *src = query_unit<QB>(a, (long long)b * g.n_rows + (live ? r : 0), live ? u : 0);
+#pragma unroll
+            for (int w = 0; w < W; w++) x[f][w] = live ? __ldg(src + w) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int i = 0; i < RB; i++) {
-            const int c = c0 + 8 * i, r = rb * N + c;
-            if (c >= N) break;
-#pragma unroll
-            for (int k = 0; k < 3; k++) {
-                const int u = k < 2 ? lane + 32 * k : nu + lane;
-                float v[8];
-                x[i].unit(k, v);
-                if (k < 2 ? u >= nu : lane >= nr) continue;
-                *reinterpret_cast<uint4 *>(qsm + (u >> 3) * (N * 128) + c * 128 + (((u & 7) ^ (c & 7)) << 4)) =
-                    make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        for (int f = 0; f < F; f++) {
+            const int i = i0 + f * kSoft, c = i / upr, u = i - c * upr;
+            if (i >= total) break;
+            uint4 v = x[f][0];
+            if constexpr (!QB) {
+                auto pack = [](uint32_t lo, uint32_t hi) { return pack_bf16(__uint_as_float(lo), __uint_as_float(hi)); };
+                const uint4 y = x[f][W - 1];
+                v = make_uint4(pack(v.x, v.y), pack(v.z, v.w), pack(y.x, y.y), pack(y.z, y.w));
             }
-            if (lane == 0) {
-                s.f[c] = a.scale * 1.4426950408889634f;
-                s.limit[c] = r < g.n_rows ? len - (a.n_q - 1 - r / a.H) : 0;
-            }
+            *reinterpret_cast<uint4 *>(qsm + (u >> 3) * (N * 128) + c * 128 + (((u & 7) ^ (c & 7)) << 4)) = v;
         }
     }
 }
@@ -188,8 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
         int it = 0, seg = 0, cur = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), it++) {
             if (w.first()) {
-                if (a.q_bf16) load_queries<N, true>(a, g, s, sm + q_off, w.b, w.rb, w.len, warp, lane);
-                else load_queries<N, false>(a, g, s, sm + q_off, w.b, w.rb, w.len, warp, lane);
+                if (a.q_bf16) load_queries<N, true>(a, g, s, sm + q_off, w.b, w.rb, w.len, tid);
+                else load_queries<N, false>(a, g, s, sm + q_off, w.b, w.rb, w.len, tid);
                 if (tid < N) s.m[cur][tid] = -kNone;
 #pragma unroll
                 for (int c = 0; c < NC / 2; c++) l[c] = make_float2(0.f, 0.f);
@@ -272,19 +275,17 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
                 if (move) add(-1.f);
             }
             if (move) {
-#pragma unroll 1
-                for (int c0 = 0; c0 < NC; c0 += 8) {
-                    uint32_t v[8];
-                    tmem_ld(lanes + col0 + c0, v);
-                    tmem_ld_wait();
+                uint32_t v[NC];
+                float x[NC];
+                tmem_ld(lanes + col0, v);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < 8; c++) {
-                        float x = __uint_as_float(v[c]) * s.f[col0 + c0 + c];
-                        if (!full && tok >= s.limit[col0 + c0 + c]) x = -INFINITY;
-                        const int k = __reduce_max_sync(0xffffffffu, float_key(x));
-                        if (lane == 0) s.red[wq][col0 + c0 + c] = __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF));
-                    }
+                for (int c = 0; c < NC; c++) {
+                    x[c] = __uint_as_float(v[c]) * s.f[col0 + c];
+                    if (!full && tok >= s.limit[col0 + c]) x[c] = -INFINITY;
                 }
+                const float top = reduce_columns(x, lane, [](float p, float q) { return fmaxf(p, q); });
+                if (lane % (32 / NC) == 0) s.red[wq][col0 + lane / (32 / NC)] = top;
                 named_sync(1, kSoft);
                 if (tid < N) {
                     // s.m holds minus the reference
@@ -328,10 +329,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
             if (!w.last()) continue;
 
             // ------------------------------------------------------ this part of the sequence is done
+            {
+                float z[NC];
 #pragma unroll
-            for (int c = 0; c < NC; c++) {
-                const float z = warp_sum(c & 1 ? l[c / 2].y : l[c / 2].x);
-                if (lane == 0) s.red[wq][col0 + c] = z;
+                for (int c = 0; c < NC; c++) z[c] = c & 1 ? l[c / 2].y : l[c / 2].x;
+                const float sum = reduce_columns(z, lane, [](float p, float q) { return p + q; });
+                if (lane % (32 / NC) == 0) s.red[wq][col0 + lane / (32 / NC)] = sum;
             }
             named_sync(1, kSoft);
             const bool whole = w.whole();
@@ -351,19 +354,23 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
             named_sync(1, kSoft);
             wait(&s.o_full, seg & 1);
             tc_after_sync();
+            const long long row = (long long)w.b * g.n_rows + w.rb * N + col0;
+            const int rows = min(NC, g.n_rows - w.rb * N - (int)col0);
 #pragma unroll 1
-            for (int k = 0; k < npair * (NC / 8); k++) {
-                const int c0 = col0 + 8 * (k % (NC / 8)), d = 128 * (k / (NC / 8)) + t;
-                uint32_t o[8];
-                tmem_ld(lanes + N * (1 + k / (NC / 8)) + c0, o);
+            for (int k = 0; k < npair; k++) {
+                uint32_t o[NC];
+                tmem_ld(lanes + N * (1 + k) + col0, o);
                 tmem_ld_wait();
-                const long long row = (long long)w.b * g.n_rows + w.rb * N + c0;
+                const int d = 128 * k + t;
+                if (!whole) {
+                    float *dst = g.part + (pidx * N + col0) * a.c.L + d;
 #pragma unroll
-                for (int c = 0; c < 8; c++) {
-                    const float v = __uint_as_float(o[c]) * s.linv[c0 + c];
-                    if (w.rb * N + c0 + c >= g.n_rows) break;
-                    if (!whole) g.part[(pidx * N + c0 + c) * a.c.L + d] = v;
-                    else store_out(a, (row + c) * a.c.L + d, v);
+                    for (int c = 0; c < NC; c++)
+                        if (c < rows) dst[c * a.c.L] = __uint_as_float(o[c]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < NC; c++)
+                        if (c < rows) store_out(a, (row + c) * a.c.L + d, __uint_as_float(o[c]) * s.linv[col0 + c]);
                 }
             }
             tc_before_sync();
@@ -441,23 +448,45 @@ __global__ void __launch_bounds__(512) mla_join_kernel(const MlaAttendArgs a, co
 #pragma unroll
         for (int d = 0; d < 4; d++) o[d] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (n > 1) {
-            for (int k = lane; k < n; k += 32) M = fmaxf(M, g.part_ml[part(k) * 2]);
+            // the first two parts are asked for before the maxima are known: one round trip for both
+            float4 v[2][4];
+            float mk[2];
+            auto load = [&](int k, float4 (&x)[4], float &m) {
+                const float *src = g.part + part(k) * a.c.L + 4 * lane;
+                m = g.part_ml[part(k) * 2];
+#pragma unroll
+                for (int d = 0; d < 4; d++)
+                    if (d < nd) x[d] = __ldcs(reinterpret_cast<const float4 *>(src + 128 * d));
+            };
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+                if (sub + i * wpr < n) load(sub + i * wpr, v[i], mk[i]);
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (lane < n) ml = *reinterpret_cast<const float2 *>(g.part_ml + part(lane) * 2);
+            M = ml.x;
+            for (int k = lane + 32; k < n; k += 32) M = fmaxf(M, g.part_ml[part(k) * 2]);
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-            for (int k = lane; k < n; k += 32) {
-                const float2 ml = *reinterpret_cast<const float2 *>(g.part_ml + part(k) * 2);
+            z = lane < n ? ml.y * ex2(ml.x - M) : 0.f;
+            for (int k = lane + 32; k < n; k += 32) {
+                ml = *reinterpret_cast<const float2 *>(g.part_ml + part(k) * 2);
                 z = fmaf(ml.y, ex2(ml.x - M), z);
             }
             z = warp_sum(z);
-#pragma unroll 2
-            for (int k = sub; k < n; k += wpr) {
-                const float f = ex2(g.part_ml[part(k) * 2] - M);
-                const float *src = g.part + part(k) * a.c.L + 4 * lane;
+            for (int k0 = sub; k0 < n; k0 += 2 * wpr) {
 #pragma unroll
-                for (int d = 0; d < 4; d++) {
-                    if (d >= nd) break;
-                    const float4 v = __ldcs(reinterpret_cast<const float4 *>(src + 128 * d));
-                    o[d] = make_float4(fmaf(v.x, f, o[d].x), fmaf(v.y, f, o[d].y), fmaf(v.z, f, o[d].z), fmaf(v.w, f, o[d].w));
+                for (int i = 0; i < 2; i++) {
+                    const int k = k0 + i * wpr;
+                    if (k >= n) break;
+                    if (k0 != sub) load(k, v[i], mk[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    if (k0 + i * wpr >= n) break;
+                    const float f = ex2(mk[i] - M);
+#pragma unroll
+                    for (int d = 0; d < 4; d++)
+                        if (d < nd) o[d] = make_float4(fmaf(v[i][d].x, f, o[d].x), fmaf(v[i][d].y, f, o[d].y), fmaf(v[i][d].z, f, o[d].z), fmaf(v[i][d].w, f, o[d].w));
                 }
             }
         }

@@ -82,61 +82,37 @@ __device__ __forceinline__ int token_slot(const MlaAttendArgs &a, int b, int t, 
     return id * a.c.page + (t - pi * a.c.page);
 }
 
-// Order-preserving map of floats to ints (its own inverse up to the sign rule).
-__device__ __forceinline__ int float_key(float f) {
-    const int i = __float_as_int(f);
-    return i ^ ((i >> 31) & 0x7FFFFFFF);
-}
-
 __device__ __forceinline__ void store_out(const MlaAttendArgs &a, long long e, float v) {
     if (a.out_bf16) reinterpret_cast<__nv_bfloat16 *>(a.out)[e] = __float2bfloat16_rn(v);
     else reinterpret_cast<float *>(a.out)[e] = v;
 }
 
-// Query row r of sequence b, as this lane's units of 8 elements: lane and lane
-// + 32 of the latent part, lane of the rope part (zeros where there are none).
+// Address of unit u (8 elements) of query row `row`: latent units first, then rope ones.
 template <bool QB>
-struct QueryRow {
-    static constexpr int W = QB ? 1 : 2;   // 16-byte words per unit
-    uint4 x[3][W];
-    __device__ __forceinline__ void load(const MlaAttendArgs &a, long long row, bool live, int lane) {
-        const int nu = a.c.L / 8, nr = a.c.R / 8;
-#pragma unroll
-        for (int k = 0; k < 3; k++) {
-            const int u = lane + 32 * (k == 1);
-            const bool ok = live && (k < 2 ? u < nu : lane < nr);
-            const long long e = k < 2 ? row * a.c.L + 8 * u : row * a.c.R + 8 * lane;
-            const uint8_t *src = reinterpret_cast<const uint8_t *>(k < 2 ? a.q_latent : a.q_rope) + e * (QB ? 2 : 4);
-#pragma unroll
-            for (int w = 0; w < W; w++) x[k][w] = ok ? __ldg(reinterpret_cast<const uint4 *>(src) + w) : make_uint4(0u, 0u, 0u, 0u);
-        }
-    }
-    __device__ __forceinline__ void unit(int k, float (&v)[8]) const {
-        const uint32_t w[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w, x[k][W - 1].x, x[k][W - 1].y, x[k][W - 1].z, x[k][W - 1].w};
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            const float2 t = QB ? bf16x2_f32x2(w[q]) : make_float2(__uint_as_float(w[2 * q]), __uint_as_float(w[2 * q + 1]));
-            v[2 * q] = t.x;
-            v[2 * q + 1] = t.y;
-        }
-    }
-};
+__device__ __forceinline__ const uint4 *query_unit(const MlaAttendArgs &a, long long row, int u) {
+    const int nu = a.c.L / 8;
+    const long long e = u < nu ? row * a.c.L + 8 * u : row * a.c.R + 8 * (u - nu);
+    return reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(u < nu ? a.q_latent : a.q_rope) + e * (QB ? 2 : 4));
+}
 
 // Warp 0: the tiles of all sequences, this group's piece of them, and (block 0) the prefix table.
 __device__ __forceinline__ void find_piece(const MlaAttendArgs &a, const AttendPlan &g, int group, int lane, Piece &out) {
-    int total = 0;
-    for (int b = lane; b < a.n_seq; b += 32) {
+    auto tiles = [&](int b, bool check) {
+        if (b >= a.n_seq) return 0;
         const int n = a.lens[b];
-        if (n < 0 || n > a.pages_stride * a.c.page) mla_bad_index(a.err);
-        total += tiles_of(seq_len(a, b));
-    }
+        const bool good = n >= 0 && n <= a.pages_stride * a.c.page;
+        if (check && !good) mla_bad_index(a.err);
+        return tiles_of(good ? n : 0);
+    };
+    const int mine = tiles(lane, true);   // the first 32 sequences' lengths are read once
+    int total = mine;
+    for (int b = lane + 32; b < a.n_seq; b += 32) total += tiles(b, true);
     total = __reduce_add_sync(0xffffffffu, total);
     const int chunk = (total + g.n_groups - 1) / g.n_groups;
     const int u0 = min(total, group * chunk), u1 = min(total, u0 + chunk);
     int run = 0;
     for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
-        const int b = b0 + lane;
-        const int T = b < a.n_seq ? tiles_of(seq_len(a, b)) : 0;
+        const int b = b0 + lane, T = b0 ? tiles(b, false) : mine;
         int incl = T;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -156,6 +132,24 @@ __device__ __forceinline__ void find_piece(const MlaAttendArgs &a, const AttendP
         out.u1 = u1;
         if (g.prefix && blockIdx.x == 0) g.prefix[a.n_seq] = total;
     }
+}
+
+// Reduces each of a thread's NC columns over the warp's lanes by halving: 31 exchanges for 32 columns instead of 160.
+// Lane i returns column i / (32 / NC).
+template <int NC, class Op>
+__device__ __forceinline__ float reduce_columns(float (&v)[NC], int lane, Op op) {
+    int o = 16;
+#pragma unroll
+    for (int w = NC / 2; w >= 1; w /= 2, o /= 2) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < w; i++) {
+            const float keep = up ? v[i + w] : v[i], send = up ? v[i] : v[i + w];
+            v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        }
+    }
+    for (; o >= 1; o /= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    return v[0];
 }
 
 // A copy warp's lanes: the slot of this lane's box of pbox tokens in the current

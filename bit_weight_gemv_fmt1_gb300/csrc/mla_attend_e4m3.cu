@@ -79,56 +79,93 @@ __device__ __forceinline__ uint32_t take_term(float2 &v, float step) {
     return u;
 }
 
-// This warp's query rows of a block -> E4M3 terms [L/128 blocks][2 NH][128], then [2 NH][64] (rope).
+// A unit of 8 query elements times `up` -> its two E4M3 terms, in f16 pairs (of f32 or bf16 input; f16 holds the
+// scaled values' 8 and the remainders' 4 bits exactly).
+template <bool QB>
+__device__ __forceinline__ void query_terms(const uint4 (&x)[QB ? 1 : 2], float up, uint2 (&t)[2]) {
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[QB ? 0 : 1].x, x[QB ? 0 : 1].y, x[QB ? 0 : 1].z, x[QB ? 0 : 1].w};
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        float2 y = QB ? bf16x2_f32x2(w[q]) : make_float2(__uint_as_float(w[2 * q]), __uint_as_float(w[2 * q + 1]));
+        y = fmul2(y, make_float2(up, up));
+        const uint32_t h = pack_f16(y.x, y.y);
+        uint16_t e;
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e) : "r"(h));
+        const uint32_t b = e4m3x2_f16x2(e);
+        const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&b)), __float2half2_rn(kQ1));
+        uint16_t f;
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(f) : "r"(*reinterpret_cast<const uint32_t *>(&r)));
+        hi[q] = e;
+        lo[q] = f;
+    }
+    t[0] = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    t[1] = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+}
+template <bool QB>
+__device__ __forceinline__ float largest(const uint4 (&x)[QB ? 1 : 2]) {
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[QB ? 0 : 1].x, x[QB ? 0 : 1].y, x[QB ? 0 : 1].z, x[QB ? 0 : 1].w};
+    float m = 0.f;
+#pragma unroll
+    for (int q = 0; q < (QB ? 4 : 8); q++) {
+        if constexpr (QB) {
+            const float2 y = bf16x2_f32x2(w[q]);
+            m = fmaxf(m, fmaxf(fabsf(y.x), fabsf(y.y)));
+        } else {
+            m = fmaxf(m, fabsf(__uint_as_float(w[q])));
+        }
+    }
+    return m;
+}
+
+// The query rows of a block -> E4M3 terms [L/128 blocks][2 NH][128], then [2 NH][64] (rope).  A warp takes four rows
+// at a time: lane l holds units l and l + 32 of each, and unit l % 8 of the rope part of row l / 8.
 template <int NH, bool QB>
 __device__ __forceinline__ void load_queries8(const MlaAttendArgs &a, const AttendPlan &g, Shared8 &s, uint8_t *qsm, int b, int rb,
                                               int len, int warp, int lane) {
-    constexpr int RB = QB ? 4 : 2;
-    const int nu = a.c.L / 8, nru = (a.c.R + 31) / 32 * 4;
+    constexpr int W = QB ? 1 : 2;
+    const int nu = a.c.L / 8, nr = a.c.R / 8, nru = (a.c.R + 31) / 32 * 4;
     uint8_t *rope = qsm + (a.c.L / 128) * (2 * NH * 128);
 #pragma unroll 1
-    for (int c0 = warp; c0 < NH; c0 += 8 * RB) {
-        QueryRow<QB> x[RB];
+    for (int c0 = 4 * warp; c0 < NH; c0 += 32) {
+        uint4 x[4][2][W], xr[W];
+        auto fetch = [&](int c, int u, bool ok, uint4 (&v)[W]) {
+            const int r = rb * NH + c;
+            ok = ok && r < g.n_rows;
+            const uint4 *src = query_unit<QB>(a, (long long)b * g.n_rows + (ok ? r : 0), ok ? u : 0);
 #pragma unroll
-        for (int i = 0; i < RB; i++) {
-            const int r = rb * NH + c0 + 8 * i;
-            x[i].load(a, (long long)b * g.n_rows + r, c0 + 8 * i < NH && r < g.n_rows, lane);
-        }
+            for (int w = 0; w < W; w++) v[w] = ok ? __ldg(src + w) : make_uint4(0u, 0u, 0u, 0u);
+        };
 #pragma unroll
-        for (int i = 0; i < RB; i++) {
-            const int c = c0 + 8 * i, r = rb * NH + c;
-            if (c >= NH) break;
-            float v[3][8], mx = 0.f;
+        for (int i = 0; i < 4; i++)
 #pragma unroll
-            for (int k = 0; k < 3; k++) {
-                x[i].unit(k, v[k]);
+            for (int k = 0; k < 2; k++) fetch(c0 + i, lane + 32 * k, lane + 32 * k < nu, x[i][k]);
+        fetch(c0 + lane / 8, nu + lane % 8, lane % 8 < nr, xr);
+        float mr = largest<QB>(xr), up_r = 0.f;
 #pragma unroll
-                for (int q = 0; q < 8; q++) mx = fmaxf(mx, fabsf(v[k][q]));
-            }
+        for (int o = 4; o > 0; o >>= 1) mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, o));
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int c = c0 + i, r = rb * NH + c;
+            float mx = fmaxf(largest<QB>(x[i][0]), largest<QB>(x[i][1]));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            mx = fmaxf(mx, __shfl_sync(0xffffffffu, mr, 8 * i));
             // times 2^k2: the largest magnitude in [2^7, 2^8)
             const int ex = (int)((__float_as_uint(mx) >> 23) & 0xFF) - 127;
             const int k2 = mx > 0.f && ex < 128 ? min(7 - ex, 120) : 0;
             const float up = __int_as_float((k2 + 127) << 23);
+            if (lane / 8 == i) up_r = up;
 #pragma unroll
-            for (int k = 0; k < 3; k++) {
-                uint32_t t[2][2];
-#pragma unroll
-                for (int q = 0; q < 2; q++) {
-                    float2 y0 = make_float2(v[k][4 * q] * up, v[k][4 * q + 1] * up), y1 = make_float2(v[k][4 * q + 2] * up, v[k][4 * q + 3] * up);
-                    t[0][q] = take_term<false>(y0, kQ1);
-                    t[0][q] |= take_term<false>(y1, kQ1) << 16;
-                    t[1][q] = pack_e4m3(y0.x, y0.y) | pack_e4m3(y1.x, y1.y) << 16;
-                }
-                const int u = k < 2 ? lane + 32 * k : lane;
-                if (k < 2 ? u >= nu : u >= nru) continue;
+            for (int k = 0; k < 2; k++) {
+                const int u = lane + 32 * k;
+                uint2 t[2];
+                query_terms<QB>(x[i][k], up, t);
+                if (u >= nu) continue;
 #pragma unroll
                 for (int j = 0; j < 2; j++) {
-                    const int row = j * NH + c, ch = (u & 15) >> 1;
-                    uint8_t *d = k < 2 ? qsm + (u >> 4) * (2 * NH * 128) + row * 128 + ((ch ^ (row & 7)) << 4)
-                                       : rope + row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
-                    *reinterpret_cast<uint2 *>(d + 8 * (u & 1)) = make_uint2(t[j][0], t[j][1]);
+                    const int row = j * NH + c;
+                    *reinterpret_cast<uint2 *>(qsm + (u >> 4) * (2 * NH * 128) + row * 128 + ((((u & 15) >> 1) ^ (row & 7)) << 4) + 8 * (u & 1)) = t[j];
                 }
             }
             if (lane == 0) {
@@ -136,6 +173,15 @@ __device__ __forceinline__ void load_queries8(const MlaAttendArgs &a, const Atte
                 s.limit[c] = r < g.n_rows ? len - (a.n_q - 1 - r / a.H) : 0;
             }
         }
+        uint2 t[2];
+        query_terms<QB>(xr, up_r, t);
+        const int u = lane % 8;
+        if (u < nru)
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int row = j * NH + c0 + lane / 8;
+                *reinterpret_cast<uint2 *>(rope + row * 64 + (((u >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (u & 1)) = t[j];
+            }
     }
 }
 
@@ -273,21 +319,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (move) add(-1.f);
             }
             if (move) {
-#pragma unroll 1
-                for (int c0 = 0; c0 < HC; c0 += 8) {
-                    uint32_t v0[8], v1[8];
-                    tmem_ld(s_at + c0, v0);
-                    tmem_ld(s_at + NH + c0, v1);
-                    tmem_ld_wait();
+                uint32_t v0[HC], v1[HC];
+                float x[HC];
+                tmem_ld(s_at, v0);
+                tmem_ld(s_at + NH, v1);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < 8; c++) {
-                        float x = fmaf(__uint_as_float(v1[c]), 1.f / kQ1, __uint_as_float(v0[c]));
-                        x = fmaf(x * st, s.f[col0 + c0 + c], lg);
-                        if (!full && tok >= s.limit[col0 + c0 + c]) x = -INFINITY;
-                        const int k = __reduce_max_sync(0xffffffffu, float_key(x));
-                        if (lane == 0) s.red[wq][col0 + c0 + c] = __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF));
-                    }
+                for (int c = 0; c < HC; c++) {
+                    x[c] = fmaf(fmaf(__uint_as_float(v1[c]), 1.f / kQ1, __uint_as_float(v0[c])) * st, s.f[col0 + c], lg);
+                    if (!full && tok >= s.limit[col0 + c]) x[c] = -INFINITY;
                 }
+                const float top = reduce_columns(x, lane, [](float p, float q) { return fmaxf(p, q); });
+                if (lane % (32 / HC) == 0) s.red[wq][col0 + lane / (32 / HC)] = top;
                 named_sync(1, kSoft);
                 if (tid < NH) {
                     const float old = -s.m[cur][tid];
@@ -333,10 +376,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!w.last()) continue;
 
             // ------------------------------------------------------ this part of the sequence is done
+            {
+                float z[HC];
 #pragma unroll
-            for (int c = 0; c < HC; c++) {
-                const float z = warp_sum(c & 1 ? l[c / 2].y : l[c / 2].x);
-                if (lane == 0) s.red[wq][col0 + c] = z;
+                for (int c = 0; c < HC; c++) z[c] = c & 1 ? l[c / 2].y : l[c / 2].x;
+                const float sum = reduce_columns(z, lane, [](float p, float q) { return p + q; });
+                if (lane % (32 / HC) == 0) s.red[wq][col0 + lane / (32 / HC)] = sum;
             }
             named_sync(1, kSoft);
             const bool whole = w.whole();
@@ -356,22 +401,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_sync(1, kSoft);
             wait(&s.k_empty[buf][np - 1], (it >> 1) & 1);
             tc_after_sync();
+            const long long row = (long long)w.b * g.n_rows + w.rb * NH + col0;
+            const int rows = min(HC, g.n_rows - w.rb * NH - col0);
 #pragma unroll 1
-            for (int k = 0; k < np * (HC / 8); k++) {
-                const int c0 = col0 + 8 * (k % (HC / 8)), blk = k / (HC / 8), d = 128 * blk + t;
-                uint32_t o0[8], o1[8], o2[8];
-                tmem_ld(lanes + kO + 3 * NH * blk + c0, o0);
-                tmem_ld(lanes + kO + 3 * NH * blk + NH + c0, o1);
-                tmem_ld(lanes + kO + 3 * NH * blk + 2 * NH + c0, o2);
+            for (int k = 0; k < np; k++) {
+                uint32_t o0[HC], o1[HC], o2[HC];
+                tmem_ld(lanes + kO + 3 * NH * k + col0, o0);
+                tmem_ld(lanes + kO + 3 * NH * k + NH + col0, o1);
+                tmem_ld(lanes + kO + 3 * NH * k + 2 * NH + col0, o2);
                 tmem_ld_wait();
-                const long long row = (long long)w.b * g.n_rows + w.rb * NH + c0;
+                const int d = 128 * k + t;
+                float *dst = g.part + (pidx * NH + col0) * a.c.L + d;
 #pragma unroll
-                for (int c = 0; c < 8; c++) {
-                    if (w.rb * NH + c0 + c >= g.n_rows) break;
-                    const float v = fmaf(fmaf(__uint_as_float(o2[c]), 1.f / kP2, __uint_as_float(o1[c])), 1.f / kP1, __uint_as_float(o0[c])) *
-                                    s.linv[c0 + c];
-                    if (!whole) g.part[(pidx * NH + c0 + c) * a.c.L + d] = v;
-                    else store_out(a, (row + c) * a.c.L + d, v);
+                for (int c = 0; c < HC; c++) {
+                    if (c >= rows) continue;
+                    const float v = fmaf(fmaf(__uint_as_float(o2[c]), 1.f / kP2, __uint_as_float(o1[c])), 1.f / kP1, __uint_as_float(o0[c]));
+                    if (!whole) dst[c * a.c.L] = v;
+                    else store_out(a, (row + c) * a.c.L + d, v * s.linv[col0 + c]);
                 }
             }
             tc_before_sync();
