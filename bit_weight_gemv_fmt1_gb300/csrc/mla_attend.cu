@@ -393,16 +393,23 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
         int it = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), box.next(), it++) {
             const int sl = box.slot[0], nbox = kTile / g.pbox;
-            const uint32_t live = __ballot_sync(0xffffffffu, sl >= 0), boxes = __popc(live);
+            const uint32_t live = __ballot_sync(0xffffffffu, sl >= 0), n = __popc(live) * g.pbox;
+            const int y0 = __shfl_sync(0xffffffffu, sl, 0);
             for (int p = who; p <= npair; p += kCopyWarps) {
+                const uint32_t dst = base + 2 * p * kBlk;
                 if (it > 0) wait(&s.empty[p], (it - 1) & 1);
                 if (!ok) continue;
-                const int nb = p < npair ? 2 : 1;
-                expect_bytes(&s.full[p], boxes * g.pbox * 128 * nb);
-                for (int j = 0; j < nbox; j++) {
+                const bool two = p < npair;
+                expect_bytes(&s.full[p], n * (two ? 256 : 128));
+                if (live & 1) {
+                    tma_box(dst, &map, 128 * p, y0, &s.full[p]);
+                    if (two) tma_box(dst + kBlk, &map, 128 * p + 64, y0, &s.full[p]);
+                }
+                for (int j = 1; j < nbox; j++) {
                     const int y = __shfl_sync(0xffffffffu, sl, j);
                     if (!(live >> j & 1)) continue;
-                    for (int k = 0; k < nb; k++) tma_box(base + (2 * p + k) * kBlk + j * g.pbox * 128, &map, 64 * (2 * p + k), y, &s.full[p]);
+                    tma_box(dst + j * g.pbox * 128, &map, 128 * p, y, &s.full[p]);
+                    if (two) tma_box(dst + kBlk + j * g.pbox * 128, &map, 128 * p + 64, y, &s.full[p]);
                 }
             }
             __syncwarp();

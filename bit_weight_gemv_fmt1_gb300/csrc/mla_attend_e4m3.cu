@@ -30,7 +30,7 @@ namespace {
 constexpr uint32_t kBlk8 = kTile * 128;  // 128 tokens x 128 codes, 128-byte swizzle
 constexpr uint32_t kRope8 = kTile * 64;  // 128 tokens x 64 codes, 64-byte swizzle
 constexpr uint32_t kP8 = kTile * 128;    // P [128 tokens][3 NH], rows of 128 bytes
-constexpr int kCopyWarps = 5;            // a warp's copy takes some 500 cycles to issue, so each block has its warp
+constexpr int kCopyWarps = 5;            // one for each block of a tile
 constexpr int kThreads = 32 * (9 + kCopyWarps);
 constexpr float kHead8 = 6.f;            // log2 of the largest weight of a fresh reference
 constexpr float kLimit8 = 14.f;          // log2 of the weight that moves the reference (E5M2 ends at 57344)
@@ -494,39 +494,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------------------------------------------------- bulk copies
-        const int who = warp - 9;
-        BoxAhead box(a, g, s.piece, slot, lane, who == 0);
+        // A block's buffer is asked for as soon as it is free, so what stands between the wait and the copies is kept
+        // short: each warp has one block of the tile (the last one: rope part and scales).
+        const int who = warp - 9, nbox = kTile / g.pbox;
+        const int p = who < 4 ? who : np;
+        const bool mine = who == 4 || who < np;
+        BoxAhead box(a, g, s.piece, slot, lane, who == 4);
         int it = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), box.next(), it++) {
-            const int buf = it & 1, sl = box.slot[0], nbox = kTile / g.pbox;
-            const uint32_t live = __ballot_sync(0xffffffffu, sl >= 0), boxes = __popc(live);
-            for (int p = who; p <= np; p += kCopyWarps) {
-                if (it > 1) wait(&s.k_empty[buf][p], ((it - 2) >> 1) & 1);
-                if (!ok) continue;
-                expect_bytes(&s.k_full[buf][p], boxes * g.pbox * (p < np ? 128 : 64));
-                if (p == np) expect_bytes(&s.sc_full[it & 3], boxes * g.pbox * 4);
-                const uint32_t dst = base + buf * stage + p * kBlk8;
+            if (!mine) continue;
+            const int buf = it & 1, sl = box.slot[0];
+            const uint32_t live = __ballot_sync(0xffffffffu, sl >= 0), n = __popc(live) * g.pbox;
+            const int y0 = __shfl_sync(0xffffffffu, sl, 0);
+            const uint32_t dst = base + buf * stage + p * kBlk8;
+            uint64_t *bar = &s.k_full[buf][p];
+            if (it > 1) wait(&s.k_empty[buf][p], ((it - 2) >> 1) & 1);
+            if (!ok) continue;
+            if (who < 4) {
+                expect_bytes(bar, n * 128);
+                if (live & 1) tma_box(dst, &map, 128 * p, y0, bar);
+                for (int j = 1; j < nbox; j++) {
+                    const int y = __shfl_sync(0xffffffffu, sl, j);
+                    if (live >> j & 1) tma_box(dst + j * g.pbox * 128, &map, 128 * p, y, bar);
+                }
+            } else {
+                expect_bytes(bar, n * 64);
+                expect_bytes(&s.sc_full[it & 3], n * 4);
                 for (int j = 0; j < nbox; j++) {
-                    const int y = __shfl_sync(0xffffffffu, sl, j), row = j * g.pbox;
+                    const int y = __shfl_sync(0xffffffffu, sl, j);
                     if (!(live >> j & 1)) continue;
-                    if (p < np) {
-                        tma_box(dst + row * 128, &map, 128 * p, y, &s.k_full[buf][p]);
-                    } else {
-                        tma_box(dst + row * 64, &rope_map, a.c.L, y, &s.k_full[buf][p]);
-                        bulk_copy(smem_addr(&s.scale[it & 3][row]), a.c.scales + y, g.pbox * 4, &s.sc_full[it & 3]);
-                    }
+                    tma_box(dst + j * g.pbox * 64, &rope_map, a.c.L, y, bar);
+                    bulk_copy(smem_addr(&s.scale[it & 3][j * g.pbox]), a.c.scales + y, g.pbox * 4, &s.sc_full[it & 3]);
                 }
             }
-            __syncwarp();
         }
         // every copy has landed before the CTA may end
         const uint64_t late = global_ns() + 200000000ull;
         volatile int none = 0;
-        for (int k = it > 1 ? it - 2 : 0; k < it; k++)
-            for (int p = who; p <= np; p += kCopyWarps) {
-                warp_wait(&s.k_full[k & 1][p], (k >> 1) & 1, late, &none, lane);
-                if (p == np) warp_wait(&s.sc_full[k & 3], (k >> 2) & 1, late, &none, lane);
-            }
+        for (int k = it > 1 ? it - 2 : 0; k < it && mine; k++) {
+            warp_wait(&s.k_full[k & 1][p], (k >> 1) & 1, late, &none, lane);
+            if (who == 4) warp_wait(&s.sc_full[k & 3], (k >> 2) & 1, late, &none, lane);
+        }
     }
     tc_before_sync();
     __syncthreads();
