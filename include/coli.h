@@ -401,6 +401,7 @@ typedef struct {
  *   out_rope   the same with dtype_rope, ld_rope.  The two may be parts of one
  *              row [nope | rope] (ld_nope = ld_rope = nope + rope): the expanded form's q.
  * f32 outputs are exact copies / one rounding per operation; bf16 rounds to nearest.
+ * f32 outputs may be q itself, part by part (in place).
  * All pointers 16-byte aligned, strides multiples of 8 elements.  T >= 0.  A
  * position out of range is recorded for coli_sync_check and its rows are zero.
  * Errors: COLI_EINVAL, COLI_EFMT (a dtype), COLI_ECUDA, COLI_EINJECTED.
