@@ -36,6 +36,12 @@ constexpr uint32_t kBlk = kRows * 128;   // 128 rows x 64 bf16, 128-byte swizzle
 constexpr float kGrow = 8.f;             // log2 of the weight that moves the reference
 constexpr float kNone = -3e38f;          // reference of a row that has seen no key
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 struct Shared {
     uint64_t q_full[2], k_full[2], k_empty[2], v_full, v_empty, s_full[2], p_full[2], o_full[2];
     uint32_t tmem;
@@ -142,75 +148,67 @@ __global__ void __launch_bounds__(352, 1)
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), S = lanes + x * 128, O = lanes + 256 + x * V;
         const int limit = row + nk - nq + 1;             // keys this row sees
         const int first_limit = q0 + x * kRows + nk - nq + 1;
-        const float f = a.scale * 1.4426950408889634f;
+        // a negative scale turns the scores' sign; a zero one must still send masked scores (-inf) to -inf
+        const bool negative = a.scale < 0.f;
+        const float f = a.scale == 0.f ? 1e-37f : fabsf(a.scale) * 1.4426950408889634f;
         float m = kNone;
-        float2 l2 = make_float2(0.f, 0.f);
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
         for (int j = 0; j < nt[x]; j++) {
             wait(&s.s_full[x], j & 1);
             tc_after_sync();
             const int k0 = j * kRows;
             const bool full = k0 + kRows <= first_limit && k0 + kRows <= nk;   // every row sees the whole tile
             const int seen = full ? kRows : min(limit, nk) - k0;              // this row's keys in the tile
-            // the tile's maximum (minimum for a negative scale) of the raw scores
-            float top = -INFINITY;
+            // the row's scores, all at once: every wait for TMEM costs more than the arithmetic on a quarter of them
+            uint32_t v[kRows];
 #pragma unroll
-            for (int c0 = 0; c0 < kRows; c0 += 32) {
-                uint32_t v[32];
-                tmem_ld(S + c0, v);
-                tmem_ld_wait();
-                if (!full)
+            for (int c0 = 0; c0 < kRows; c0 += 32) tmem_ld(S + c0, *reinterpret_cast<uint32_t(*)[32]>(v + c0));
+            tmem_ld_wait();
+            if (negative)
 #pragma unroll
-                    for (int c = 0; c < 32; c++)
-                        if (c0 + c >= seen) v[c] = f < 0.f ? 0x7F800000u : 0xFF800000u;
-                if (f < 0.f)
+                for (int c = 0; c < kRows; c++) v[c] ^= 0x80000000u;
+            if (!full)
 #pragma unroll
-                    for (int c = 0; c < 32; c++) v[c] ^= 0x80000000u;
-                float t4[4];
+                for (int c = 0; c < kRows; c++)
+                    if (c >= seen) v[c] = 0xFF800000u;
+            float t4[4];
 #pragma unroll
-                for (int k = 0; k < 4; k++) t4[k] = __uint_as_float(v[k]);
+            for (int k = 0; k < 4; k++) t4[k] = max3(__uint_as_float(v[k]), __uint_as_float(v[4 + k]), __uint_as_float(v[8 + k]));
 #pragma unroll
-                for (int c = 4; c < 32; c += 8)
+            for (int c = 12; c + 8 <= kRows; c += 8)
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        t4[k] = fmaxf(t4[k], c + 4 + k < 32 ? fmaxf(__uint_as_float(v[c + k]), __uint_as_float(v[c + 4 + k])) : __uint_as_float(v[c + k]));
-                top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
-            }
-            const float now = top * fabsf(f);
+                for (int k = 0; k < 4; k++) t4[k] = max3(t4[k], __uint_as_float(v[c + k]), __uint_as_float(v[c + 4 + k]));
+#pragma unroll
+            for (int k = 0; k < 4; k++) t4[k] = fmaxf(t4[k], __uint_as_float(v[kRows - 4 + k]));
+            const float now = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f;
             const bool move = now > m + kGrow;
             if (__any_sync(0xffffffffu, move)) {
                 const float r = move ? ex2(m - now) : 1.f;
                 if (move) m = now;
-                l2 = fmul2(l2, make_float2(r, r));
+#pragma unroll
+                for (int k = 0; k < 4; k++) l4[k] *= r;
                 if (j > 0) {
 #pragma unroll 1
-                    for (int c0 = 0; c0 < V; c0 += 32) {
-                        uint32_t o[32];
+                    for (int c0 = 0; c0 < V; c0 += 8) {
+                        uint32_t o[8];
                         tmem_ld(O + c0, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int c = 0; c < 32; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * r);
+                        for (int c = 0; c < 8; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * r);
                         tmem_st(O + c0, o);
                     }
-                    tmem_st_wait();
                 }
             }
-            const float2 f2 = make_float2(f, f), m2 = make_float2(-m, -m);
+            const float m0 = -m;
 #pragma unroll
             for (int c0 = 0; c0 < kRows; c0 += 32) {
-                uint32_t v[32], p[16];
-                tmem_ld(S + c0, v);
-                tmem_ld_wait();
+                uint32_t p[16];
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
-                    float2 y = m2;
-                    ffma2(y, make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f2);
-                    y = make_float2(ex2(y.x), ex2(y.y));
-                    if (!full) {
-                        if (c0 + c >= seen) y.x = 0.f;
-                        if (c0 + c + 1 >= seen) y.y = 0.f;
-                    }
-                    l2 = fadd2(l2, y);
-                    p[c / 2] = pack_bf16(y.x, y.y);
+                    const float x = ex2(fmaf(__uint_as_float(v[c0 + c]), f, m0)), y = ex2(fmaf(__uint_as_float(v[c0 + c + 1]), f, m0));
+                    l4[c & 3] += x;
+                    l4[(c + 1) & 3] += y;
+                    p[c / 2] = pack_bf16(x, y);
                 }
                 tmem_st(S + c0 / 2, p);                  // over scores that have been read
             }
@@ -230,7 +228,7 @@ __global__ void __launch_bounds__(352, 1)
             if (lane == 0 && ok) mbar_arrive(&s.p_full[x]);
         }
         const bool store = live && row < nq;
-        const float l = l2.x + l2.y;
+        const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
         const float inv = l != 0.f ? 1.f / l : 0.f;
         const long long orow = ((long long)(s.qrow + row) * a.H + head);
         if (nt[x] > 0) {
