@@ -15,11 +15,12 @@
 //
 // Bound: the tensor cores, 1280 cycles for 128 x 128 scores (nope + rope = 192, v = 128), of which the
 // exponentials' unit takes up to 1024.  Shared memory holds Q (96 KB), two K tiles (96 KB) and one V
-// tile (32 KB); a V tile is needed a whole softmax later than it is asked for.
+// tile (32 KB), whose two halves of 64 keys are freed and asked for one by one: each comes back
+// before its next use 1024 cycles later (asked for whole, at the end of a round, V cost 1900 of 4500 cycles).
 //
 // Keys past a causal row's limit are masked by selection; value rows past the
 // sequence's end belong to its neighbours and are zeroed in shared memory.
-// Warps: 0-3 and 4-7 softmax of A and B, 8 MMA issue, 9 and 10 bulk copies.
+// Warps: 0-3 and 4-7 softmax of A and B, 8 MMA issue, 9 copies of queries and keys, 10 and 11 of values.
 // Every wait is bounded; after one has run out all waits return at once, no
 // further MMA or copy is issued, and the kernel records DEV_ERR_TIMEOUT.
 #include <cudaTypedefs.h>
@@ -43,16 +44,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 struct Shared {
-    uint64_t q_full[2], k_full[2], k_empty[2], v_full, v_empty, s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
     uint32_t tmem;
     int abort;
     int b, q0, nq, nk, qrow, krow;       // sequence, first query of the pair in it, its sizes, first rows
 };
 
 template <int V>
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(384, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
-                       const __grid_constant__ CUtensorMap kr_map, const MlaPrefillArgs a, int max_pairs, long long timeout_ns) {
+                       const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap v_map, const MlaPrefillArgs a, int max_pairs, long long timeout_ns) {
     extern __shared__ uint8_t raw[];
     __shared__ Shared s;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
@@ -111,9 +112,9 @@ __global__ void __launch_bounds__(352, 1)
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_full[i], 4);
             mbar_init(&s.o_full[i], 1);
+            mbar_init(&s.v_full[i], 1);
+            mbar_init(&s.v_empty[i], 1);
         }
-        mbar_init(&s.v_full, 1);
-        mbar_init(&s.v_empty, 1);
         s.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -214,7 +215,8 @@ __global__ void __launch_bounds__(352, 1)
             }
             if (k0 + kRows > nk) {
                 // value rows of other sequences may hold anything, and 0 * NaN is NaN
-                wait(&s.v_full, j & 1);
+                wait(&s.v_full[0], j & 1);
+                wait(&s.v_full[1], j & 1);
                 if (k0 + t >= nk)
 #pragma unroll
                     for (int k = 0; k < V / 64; k++)
@@ -279,10 +281,16 @@ __global__ void __launch_bounds__(352, 1)
                 if (16 * k < a.rope) mma_ss(tmem + x * 128, qa + ((nn * kBlk) >> 4) + 2 * k, ka + ((nn * kBlk) >> 4) + 2 * k, id_s, true);
             tc_commit(&s.s_full[x]);
         };
-        auto output = [&](int x, int j) {
-            if (!ok) return;
+        // the value tile's halves of 64 keys are freed one by one after their last use
+        auto output = [&](int x, int j, bool last) {
 #pragma unroll
-            for (int k = 0; k < 8; k++) mma_ts(tmem + 256 + x * V, tmem + x * 128 + 8 * k, dv + ((k * 2048) >> 4), id_o, j || k);
+            for (int h = 0; h < 2; h++) {
+                wait(&s.v_full[h], j & 1);
+                if (!ok) return;
+#pragma unroll
+                for (int k = 4 * h; k < 4 * h + 4; k++) mma_ts(tmem + 256 + x * V, tmem + x * 128 + 8 * k, dv + ((k * 2048) >> 4), id_o, j || k);
+                if (last) tc_commit(&s.v_empty[h]);
+            }
         };
         if (n > 0) wait(&s.k_full[0], 0);
         for (int x = 0; x < 2; x++)
@@ -293,19 +301,19 @@ __global__ void __launch_bounds__(352, 1)
             }
         if (n > 0 && ok) tc_commit(&s.k_empty[0]);
         for (int j = 0; j < n; j++) {
-            wait(&s.v_full, j & 1);
-            if (j + 1 < n) wait(&s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
             for (int x = 0; x < 2; x++) {
                 if (j >= nt[x]) continue;
                 wait(&s.p_full[x], j & 1);
                 tc_after_sync();
-                output(x, j);
-                if (j + 1 < nt[x]) scores(x, j + 1);
-                else if (ok) tc_commit(&s.o_full[x]);
+                output(x, j, x == 1 || j >= nt[1]);
+                if (j + 1 < nt[x]) {
+                    wait(&s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
+                    scores(x, j + 1);
+                } else if (ok) {
+                    tc_commit(&s.o_full[x]);
+                }
             }
-            if (!ok) continue;
-            tc_commit(&s.v_empty);
-            if (j + 1 < n) tc_commit(&s.k_empty[(j + 1) & 1]);
+            if (ok && j + 1 < n) tc_commit(&s.k_empty[(j + 1) & 1]);
         }
     } else {
         // ---------------------------------------------------------- bulk copies: queries and keys, values
@@ -327,11 +335,13 @@ __global__ void __launch_bounds__(352, 1)
                     }
             }
         } else {
+            const int h = warp - 10;
             for (int j = 0; j < n; j++) {
-                if (j > 0) wait(&s.v_empty, (j - 1) & 1);
+                if (j > 0) wait(&s.v_empty[h], (j - 1) & 1);
                 if (!ok) break;
-                expect_bytes(&s.v_full, (V / 64) * kBlk);
-                for (int b = 0; b < V / 64; b++) tma_box(base + v_off + b * kBlk, &kv_map, hk + a.nope + 64 * b, s.krow + j * kRows, &s.v_full);
+                expect_bytes(&s.v_full[h], (V / 64) * kBlk / 2);
+                for (int b = 0; b < V / 64; b++)
+                    tma_box(base + v_off + b * kBlk + h * (kBlk / 2), &v_map, hk + a.nope + 64 * b, s.krow + j * kRows + 64 * h, &s.v_full[h]);
             }
         }
         // every copy has landed before the CTA may end (those not waited for by an MMA that was issued: after a timeout)
@@ -362,7 +372,7 @@ __global__ void __launch_bounds__(256) mla_round_kernel(const float *src, long l
     }
 }
 
-cudaError_t matrix_map(const void *p, long long cols, long long rows, long long stride, CUtensorMap *out) {
+cudaError_t matrix_map(const void *p, long long cols, long long rows, long long stride, int box_rows, CUtensorMap *out) {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void *f = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -373,7 +383,7 @@ cudaError_t matrix_map(const void *p, long long cols, long long rows, long long 
     }();
     if (!fn) return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {64, kRows}, estr[2] = {1, 1};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, estr[2] = {1, 1};
     return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
@@ -382,18 +392,19 @@ cudaError_t matrix_map(const void *p, long long cols, long long rows, long long 
 
 template <int V>
 cudaError_t run(const MlaPrefillArgs &a, cudaStream_t st) {
-    CUtensorMap q, kv, kr;
-    if (cudaError_t e = matrix_map(a.q, (long long)a.H * (a.nope + a.rope), a.Tq, a.q_stride, &q)) return e;
-    kv = kr = q;                         // no keys: never read
+    CUtensorMap q, kv, kr, vm;
+    if (cudaError_t e = matrix_map(a.q, (long long)a.H * (a.nope + a.rope), a.Tq, a.q_stride, kRows, &q)) return e;
+    kv = kr = vm = q;                         // no keys: never read
     if (a.Tk > 0) {
-        if (cudaError_t e = matrix_map(a.kv, (long long)a.H * (a.nope + V), a.Tk, a.kv_stride, &kv)) return e;
-        if (cudaError_t e = matrix_map(a.k_rope, a.rope, a.Tk, a.kr_stride, &kr)) return e;
+        if (cudaError_t e = matrix_map(a.kv, (long long)a.H * (a.nope + V), a.Tk, a.kv_stride, kRows, &kv)) return e;
+        if (cudaError_t e = matrix_map(a.kv, (long long)a.H * (a.nope + V), a.Tk, a.kv_stride, kRows / 2, &vm)) return e;
+        if (cudaError_t e = matrix_map(a.k_rope, a.rope, a.Tk, a.kr_stride, kRows, &kr)) return e;
     }
     const int nb = a.nope / 64 + 1, max_pairs = (a.Tq + 2 * kRows - 1) / (2 * kRows) + a.n_seq - 1;
     const size_t smem = (size_t)(4 * nb + V / 64) * kBlk + 1024;
     auto kern = mla_prefill_kernel<V>;
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
-    return launch_pdl(kern, dim3((unsigned)max_pairs * a.H), dim3(352), smem, st, q, kv, kr, a, max_pairs, 2000000000LL);
+    return launch_pdl(kern, dim3((unsigned)max_pairs * a.H), dim3(384), smem, st, q, kv, kr, vm, a, max_pairs, 2000000000LL);
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
