@@ -46,7 +46,7 @@ constexpr float kHead = 6.f;             // log2 of the largest weight of a fres
 constexpr float kLimit = 14.f;           // log2 of the weight that moves the reference
 
 struct Shared {
-    uint64_t full[kMaxPairs + 1], empty[kMaxPairs + 1], s_full, o_full;
+    uint64_t full[kMaxPairs + 1], empty[kMaxPairs + 1], s_full, o_full, q_full, q_empty;
     uint32_t tmem;
     int abort;
     Piece piece;
@@ -57,46 +57,37 @@ struct Shared {
     float red[4][64];
 };
 
-// The query rows of a block of N -> bf16 operand [L/64 + 1][N][64], 128-byte swizzle.  The softmax threads share
-// the block's units of 8 elements, nine loads in flight each.
-template <int N, bool QB>
-__device__ __forceinline__ void load_queries(const MlaAttendArgs &a, const AttendPlan &g, Shared &s, uint8_t *qsm, int b, int rb, int len,
-                                             int tid) {
-    constexpr int F = QB ? 9 : 5, W = QB ? 1 : 2;
+// f32 query rows of a block of N -> bf16 operand [L/64 + 1][N][64], 128-byte swizzle (bf16 ones are copied as boxes).
+// The softmax threads share the block's units of 8 elements, five in flight each.
+template <int N>
+__device__ __forceinline__ void load_queries(const MlaAttendArgs &a, const AttendPlan &g, uint8_t *qsm, int b, int rb, int tid) {
+    constexpr int F = 5;
     const int upr = (a.c.L + a.c.R) / 8, total = N * upr;
-    if (tid < N) {
-        const int r = rb * N + tid;
-        s.f[tid] = a.scale * 1.4426950408889634f;
-        s.limit[tid] = r < g.n_rows ? len - (a.n_q - 1 - r / a.H) : 0;
-    }
 #pragma unroll 1
     for (int i0 = tid; i0 < total; i0 += F * kSoft) {
-        uint4 x[F][W];
+        uint4 x[F][2];
 #pragma unroll
         for (int f = 0; f < F; f++) {
             const int i = i0 + f * kSoft, c = i / upr, u = i - c * upr, r = rb * N + c;
             const bool live = i < total && r < g.n_rows;
-            const uint4 *src = query_unit<QB>(a, (long long)b * g.n_rows + (live ? r : 0), live ? u : 0);
+            const uint4 *src = query_unit<false>(a, (long long)b * g.n_rows + (live ? r : 0), live ? u : 0);
 #pragma unroll
-            for (int w = 0; w < W; w++) x[f][w] = live ? __ldg(src + w) : make_uint4(0u, 0u, 0u, 0u);
+            for (int w = 0; w < 2; w++) x[f][w] = live ? __ldg(src + w) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int f = 0; f < F; f++) {
             const int i = i0 + f * kSoft, c = i / upr, u = i - c * upr;
             if (i >= total) break;
-            uint4 v = x[f][0];
-            if constexpr (!QB) {
-                auto pack = [](uint32_t lo, uint32_t hi) { return pack_bf16(__uint_as_float(lo), __uint_as_float(hi)); };
-                const uint4 y = x[f][W - 1];
-                v = make_uint4(pack(v.x, v.y), pack(v.z, v.w), pack(y.x, y.y), pack(y.z, y.w));
-            }
-            *reinterpret_cast<uint4 *>(qsm + (u >> 3) * (N * 128) + c * 128 + (((u & 7) ^ (c & 7)) << 4)) = v;
+            auto pack = [](uint32_t lo, uint32_t hi) { return pack_bf16(__uint_as_float(lo), __uint_as_float(hi)); };
+            *reinterpret_cast<uint4 *>(qsm + (u >> 3) * (N * 128) + c * 128 + (((u & 7) ^ (c & 7)) << 4)) =
+                make_uint4(pack(x[f][0].x, x[f][0].y), pack(x[f][0].z, x[f][0].w), pack(x[f][1].x, x[f][1].y), pack(x[f][1].z, x[f][1].w));
         }
     }
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __grid_constant__ CUtensorMap map, const MlaAttendArgs a, const AttendPlan g) {
+__global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap q_map,
+                                                                              const __grid_constant__ CUtensorMap qr_map, const MlaAttendArgs a, const AttendPlan g) {
     constexpr int NC = N / 2;              // columns per softmax thread
     extern __shared__ uint8_t raw[];
     __shared__ Shared s;
@@ -119,6 +110,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
         }
         mbar_init(&s.s_full, 1);
         mbar_init(&s.o_full, 1);
+        mbar_init(&s.q_full, 1);
+        mbar_init(&s.q_empty, 1);
         s.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -191,14 +184,18 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
         int it = 0, seg = 0, cur = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), it++) {
             if (w.first()) {
-                if (a.q_bf16) load_queries<N, true>(a, g, s, sm + q_off, w.b, w.rb, w.len, tid);
-                else load_queries<N, false>(a, g, s, sm + q_off, w.b, w.rb, w.len, tid);
+                if (!a.q_bf16) load_queries<N>(a, g, sm + q_off, w.b, w.rb, tid);
+                if (tid < N) {
+                    const int r = w.rb * N + tid;
+                    s.f[tid] = a.scale * 1.4426950408889634f;
+                    s.limit[tid] = r < g.n_rows ? w.len - (a.n_q - 1 - r / a.H) : 0;
+                }
                 if (tid < N) s.m[cur][tid] = -kNone;
 #pragma unroll
                 for (int c = 0; c < NC / 2; c++) l[c] = make_float2(0.f, 0.f);
                 fence_async_smem();
                 named_sync(1, kSoft);
-                named_arrive(3, kSoft + 32);
+                if (!a.q_bf16) named_arrive(3, kSoft + 32);
             }
             const int tok = w.tile() * kTile + t;
             // every column sees the whole tile: the first query's limit is the lowest
@@ -379,22 +376,37 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------- MMA issue
-        int it = 0;
+        int it = 0, seg = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), it++) {
-            if (w.first()) named_sync(3, kSoft + 32);
+            if (w.first()) {
+                if (a.q_bf16) wait(&s.q_full, seg++ & 1);
+                else named_sync(3, kSoft + 32);
+            }
             issue_scores(it);
+            if (w.last() && ok) tc_commit(&s.q_empty);
             named_sync(4, kSoft + 32);
             issue_output(w.first(), w.last());
         }
     } else {
         // ---------------------------------------------------------- bulk copies of bf16 rows
         const int who = warp - kMmaWarp - 1;
-        BoxAhead box(a, g, s.piece, slot, lane, who == 0);
-        int it = 0;
+        BoxAhead box(a, g, s.piece, slot, lane, who == kCopyWarps - 1);
+        int it = 0, seg = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), box.next(), it++) {
             const int sl = box.slot[0], nbox = kTile / g.pbox;
             const uint32_t live = __ballot_sync(0xffffffffu, sl >= 0), n = __popc(live) * g.pbox;
             const int y0 = __shfl_sync(0xffffffffu, sl, 0);
+            if (who == 0 && a.q_bf16 && w.first()) {
+                // the block's queries; rows past the sequence's are its neighbour's or zero, and masked
+                if (seg > 0) wait(&s.q_empty, (seg - 1) & 1);
+                seg++;
+                if (ok) {
+                    const int y = w.b * g.n_rows + w.rb * N;
+                    expect_bytes(&s.q_full, nblk * N * 128);
+                    for (int k = 0; k < nblk - 1; k++) tma_box(base + q_off + k * (N * 128), &q_map, 64 * k, y, &s.q_full);
+                    tma_box(base + q_off + (nblk - 1) * (N * 128), &qr_map, 0, y, &s.q_full);
+                }
+            }
             for (int p = who; p <= npair; p += kCopyWarps) {
                 const uint32_t dst = base + 2 * p * kBlk;
                 if (it > 0) wait(&s.empty[p], (it - 1) & 1);
@@ -418,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
         if (it > 0) {
             const uint64_t late = global_ns() + 200000000ull;
             volatile int none = 0;
+            if (seg > 0) warp_wait(&s.q_full, (seg - 1) & 1, late, &none, lane);
             for (int p = who; p <= npair; p += kCopyWarps) warp_wait(&s.full[p], (it - 1) & 1, late, &none, lane);
         }
     }
@@ -437,18 +450,18 @@ __global__ void __launch_bounds__(512) mla_join_kernel(const MlaAttendArgs a, co
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp & (wpr - 1), rpb = 16 / wpr;
     pdl_wait();
     pdl_trigger();
-    const int total = g.prefix[a.n_seq], chunk = (total + g.n_groups - 1) / g.n_groups, nd = a.c.L / 128;
+    const int nd = a.c.L / 128;
     const int rows = a.n_seq * g.n_rows;
     for (int row0 = blockIdx.x * rpb; row0 < rows; row0 += gridDim.x * rpb) {
         const int row = row0 + warp / wpr;
-        int b = 0, r = 0, g0 = 0, g1 = 0;
+        int r = 0;
+        int2 piece = make_int2(0, 1);
         if (row < rows) {
-            b = row / g.n_rows;
+            const int b = row / g.n_rows;
             r = row - b * g.n_rows;
-            g0 = g.prefix[b] / chunk;
-            g1 = (g.prefix[b + 1] - 1) / chunk;
+            piece = g.pieces[b];
         }
-        const int n = g1 - g0 + 1, rb = r / g.cols, c = r - rb * g.cols;
+        const int g0 = piece.x, n = piece.y, rb = r / g.cols, c = r - rb * g.cols;
         auto part = [&](int k) { return (((long long)(g0 + k) * g.nrb + rb) * 2 + (k == 0 ? 1 : 0)) * g.cols + c; };
         float4 o[4];
         float M = -INFINITY, z = 0.f;
@@ -530,7 +543,7 @@ __global__ void __launch_bounds__(512) mla_join_kernel(const MlaAttendArgs a, co
 // bandwidth for nothing, up to what TMEM and shared memory allow.
 int columns_of(bool e4m3, int n_rows) { return n_rows <= 16 ? 16 : n_rows <= 32 || e4m3 ? 32 : 64; }
 
-// The pieces and scratch of a call: part, part_ml and prefix are offsets from NULL until placed.
+// The pieces and scratch of a call: part, part_ml and pieces are offsets from NULL until placed.
 AttendPlan plan(const MlaAttendArgs &a, int n_sm, size_t *bytes) {
     AttendPlan g{};
     g.n_rows = a.n_q * a.H;
@@ -547,8 +560,8 @@ AttendPlan plan(const MlaAttendArgs &a, int n_sm, size_t *bytes) {
         at += parts * a.c.L * sizeof(float);
         g.part_ml = (float *)at;
         at += parts * 2 * sizeof(float);
-        g.prefix = (int *)at;
-        at += ((size_t)a.n_seq + 1) * sizeof(int);
+        g.pieces = (int2 *)at;
+        at += (size_t)a.n_seq * sizeof(int2);
     }
     g.pbox = kTile;
     while (a.c.page % g.pbox) g.pbox /= 2;
@@ -557,37 +570,51 @@ AttendPlan plan(const MlaAttendArgs &a, int n_sm, size_t *bytes) {
     return g;
 }
 
+// Tensor map of packed rows: boxes of `inner` elements x `box_rows`.
+cudaError_t encode(const void *p, CUtensorMapDataType type, long long cols, long long rows, long long row_bytes, int inner, int box_rows,
+                   CUtensorMapSwizzle swizzle, CUtensorMap *out) {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return (PFN_cuTensorMapEncodeTiled_v12000)f;
+    }();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {(cuuint32_t)inner, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+    return fn(out, type, 2, const_cast<void *>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+cudaError_t bf16_map(const void *p, int cols, long long rows, int box_rows, CUtensorMap *out) {
+    return encode(p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cols, rows, 2LL * cols, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B, out);
+}
+
 template <int N>
 cudaError_t run_bf16(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t st) {
-    CUtensorMap map;
+    CUtensorMap map, q, qr;
     if (cudaError_t e = mla_row_map(a.c, 64, g.pbox, CU_TENSOR_MAP_SWIZZLE_128B, &map)) return e;
+    q = qr = map;                        // f32 queries: never read
+    if (a.q_bf16) {
+        const long long rows = (long long)a.n_seq * g.n_rows;
+        if (cudaError_t e = bf16_map(a.q_latent, a.c.L, rows, N, &q)) return e;
+        if (cudaError_t e = bf16_map(a.q_rope, a.c.R, rows, N, &qr)) return e;
+    }
     const int nblk = a.c.L / 64 + 1;
     const size_t smem = (size_t)nblk * kBlk + (size_t)nblk * N * 128 + 1024;
     auto kern = mla_attend_bf16_kernel<N>;
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
-    return launch_pdl(kern, dim3(g.n_groups * g.n_slots), dim3(kThreads), smem, st, map, a, g);
+    return launch_pdl(kern, dim3(g.n_groups * g.n_slots), dim3(kThreads), smem, st, map, q, qr, a, g);
 }
 
 }  // namespace
 
 cudaError_t mla_row_map(const MlaCache &c, int inner, int pbox, CUtensorMapSwizzle swizzle, CUtensorMap *out) {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return (PFN_cuTensorMapEncodeTiled_v12000)p;
-    }();
-    if (!fn) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {(cuuint64_t)(c.L + c.R), (cuuint64_t)c.n_pages * c.page};
-    const cuuint64_t strides[1] = {(cuuint64_t)c.row_bytes};
-    const cuuint32_t box[2] = {(cuuint32_t)inner, (cuuint32_t)pbox}, estr[2] = {1, 1};
-    return fn(out, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.rows, dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? cudaSuccess
-               : cudaErrorInvalidValue;
+    return encode(c.rows, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, c.L + c.R, (long long)c.n_pages * c.page,
+                  c.row_bytes, inner, pbox, swizzle, out);
 }
 
 size_t mla_attend_scratch(const MlaAttendArgs &a, int n_sm) {
@@ -602,7 +629,7 @@ cudaError_t launch_mla_attend(const MlaAttendArgs &a, void *scratch, int n_sm, c
     if (bytes) {
         g.part = (float *)((char *)scratch + (size_t)g.part);
         g.part_ml = (float *)((char *)scratch + (size_t)g.part_ml);
-        g.prefix = (int *)((char *)scratch + (size_t)g.prefix);
+        g.pieces = (int2 *)((char *)scratch + (size_t)g.pieces);
     }
     *n_launch = g.n_groups > 1 ? 2 : 1;
     cudaError_t e;

@@ -18,7 +18,7 @@ struct AttendPlan {
     int n_groups, n_slots; // pieces of the line of tiles; CTAs of a group
     float *part;           // [n_groups * nrb * 2][cols][L] partial O, then [..][cols][2] m, l
     float *part_ml;
-    int *prefix;           // [n_seq + 1] tiles before each sequence
+    int2 *pieces;          // [n_seq] first group and number of groups of each sequence
     int pbox;              // tokens per copy box
     long long timeout_ns;
 };
@@ -95,7 +95,9 @@ __device__ __forceinline__ const uint4 *query_unit(const MlaAttendArgs &a, long 
     return reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(u < nu ? a.q_latent : a.q_rope) + e * (QB ? 2 : 4));
 }
 
-// Warp 0: the tiles of all sequences, this group's piece of them, and (block 0) the prefix table.
+// Warp 0: this group's piece of the line of all sequences' tiles, and (block 0) the table of the sequences' groups.
+// As many groups as sequences or more: each sequence gets one group and its share of the others, so that no piece
+// straddles two sequences (which would cost a second start and end). Fewer groups: equal contiguous pieces.
 __device__ __forceinline__ void find_piece(const MlaAttendArgs &a, const AttendPlan &g, int group, int lane, Piece &out) {
     auto tiles = [&](int b, bool check) {
         if (b >= a.n_seq) return 0;
@@ -104,33 +106,46 @@ __device__ __forceinline__ void find_piece(const MlaAttendArgs &a, const AttendP
         if (check && !good) mla_bad_index(a.err);
         return tiles_of(good ? n : 0);
     };
+    auto scan = [&](int v) {              // inclusive prefix sum over the warp
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += w;
+        }
+        return v;
+    };
     const int mine = tiles(lane, true);   // the first 32 sequences' lengths are read once
     int total = mine;
     for (int b = lane + 32; b < a.n_seq; b += 32) total += tiles(b, true);
     total = __reduce_add_sync(0xffffffffu, total);
-    const int chunk = (total + g.n_groups - 1) / g.n_groups;
-    const int u0 = min(total, group * chunk), u1 = min(total, u0 + chunk);
-    int run = 0;
-    for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
-        const int b = b0 + lane, T = b0 ? tiles(b, false) : mine;
-        int incl = T;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        const int p = run + incl - T;
-        if (b < a.n_seq && p <= u0 && u0 < p + T) {
-            out.b0 = b;
-            out.p0 = p;
-        }
-        if (g.prefix && blockIdx.x == 0 && b < a.n_seq) g.prefix[b] = p;
-        run += __shfl_sync(0xffffffffu, incl, 31);
-    }
+    const bool shares = g.n_groups >= a.n_seq;
+    const int chunk = (total + g.n_groups - 1) / g.n_groups, spare = g.n_groups - a.n_seq;
+    int u0 = shares ? 0 : min(total, group * chunk), u1 = shares ? 0 : min(total, u0 + chunk);
     if (lane == 0) {
         out.u0 = u0;
         out.u1 = u1;
-        if (g.prefix && blockIdx.x == 0) g.prefix[a.n_seq] = total;
+    }
+    __syncwarp();
+    int run_t = 0, run_g = 0;
+    for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
+        const int b = b0 + lane, T = b0 ? tiles(b, false) : mine;
+        const int n = shares && b < a.n_seq ? min(T, 1 + (int)((long long)spare * T / total)) : 0;
+        const int incl_t = scan(T), incl_g = shares ? scan(n) : 0;
+        const int p = run_t + incl_t - T, g0 = shares ? run_g + incl_g - n : p / chunk;
+        if (b < a.n_seq) {
+            if (shares ? g0 <= group && group < g0 + n : p <= u0 && u0 < p + T) {
+                out.b0 = b;
+                out.p0 = p;
+                if (shares) {
+                    const int k = group - g0;
+                    out.u0 = p + (int)((long long)T * k / n);
+                    out.u1 = p + (int)((long long)T * (k + 1) / n);
+                }
+            }
+            if (g.pieces && blockIdx.x == 0) g.pieces[b] = make_int2(g0, shares ? n : (p + T - 1) / chunk - g0 + 1);
+        }
+        run_t += __shfl_sync(0xffffffffu, incl_t, 31);
+        run_g += __shfl_sync(0xffffffffu, incl_g, 31);
     }
 }
 

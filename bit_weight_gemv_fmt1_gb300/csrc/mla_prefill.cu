@@ -20,7 +20,7 @@
 //
 // Keys past a causal row's limit are masked by selection; value rows past the
 // sequence's end belong to its neighbours and are zeroed in shared memory.
-// Warps: 0-3 and 4-7 softmax of A and B, 8 MMA issue, 9 copies of queries and keys, 10 and 11 of values.
+// Warps: 0-3 and 4-7 softmax of A and B, 8 MMA issue, 9 copies of keys, 10 and 11 of queries and values.
 // Every wait is bounded; after one has run out all waits return at once, no
 // further MMA or copy is issued, and the kernel records DEV_ERR_TIMEOUT.
 #include <cudaTypedefs.h>
@@ -327,15 +327,13 @@ __global__ void __launch_bounds__(384, 1)
                 expect_bytes(&s.k_full[buf], nb * kBlk);
                 for (int b = 0; b < nn; b++) tma_box(dst + b * kBlk, &kv_map, hk + 64 * b, s.krow + j * kRows, &s.k_full[buf]);
                 tma_box(dst + nn * kBlk, &kr_map, 0, s.krow + j * kRows, &s.k_full[buf]);
-                if (j == 0)
-                    for (int x = 0; x < 2; x++) {
-                        if (nt[x] == 0) continue;
-                        expect_bytes(&s.q_full[x], nb * kBlk);
-                        for (int b = 0; b < nb; b++) tma_box(base + (x * nb + b) * kBlk, &q_map, hq + 64 * b, s.qrow + q0 + x * kRows, &s.q_full[x]);
-                    }
             }
         } else {
-            const int h = warp - 10;
+            const int h = warp - 10;         // also the query tile whose rows this warp copies
+            if (nt[h] > 0) {
+                expect_bytes(&s.q_full[h], nb * kBlk);
+                for (int b = 0; b < nb; b++) tma_box(base + (h * nb + b) * kBlk, &q_map, hq + 64 * b, s.qrow + q0 + h * kRows, &s.q_full[h]);
+            }
             for (int j = 0; j < n; j++) {
                 if (j > 0) wait(&s.v_empty[h], (j - 1) & 1);
                 if (!ok) break;
