@@ -390,13 +390,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
     } else {
         // ---------------------------------------------------------- bulk copies of bf16 rows
         const int who = warp - kMmaWarp - 1;
-        BoxAhead box(a, g, s.piece, slot, lane, who == kCopyWarps - 1);
+        BoxAhead box(a, g, s.piece, slot, lane, who == 1);
         int it = 0, seg = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), box.next(), it++) {
             const int sl = box.slot[0], nbox = kTile / g.pbox;
             const uint32_t live = __ballot_sync(0xffffffffu, sl >= 0), n = __popc(live) * g.pbox;
             const int y0 = __shfl_sync(0xffffffffu, sl, 0);
-            if (who == 0 && a.q_bf16 && w.first()) {
+            if (who == kCopyWarps - 1 && a.q_bf16 && w.first()) {
                 // the block's queries; rows past the sequence's are its neighbour's or zero, and masked
                 if (seg > 0) wait(&s.q_empty, (seg - 1) & 1);
                 seg++;
@@ -539,18 +539,23 @@ __global__ void __launch_bounds__(512) mla_join_kernel(const MlaAttendArgs a, co
     }
 }
 
-// Columns of a CTA: the fewest that hold the sequence's rows, as small products cost less shared-memory
-// bandwidth for nothing, up to what TMEM and shared memory allow.
-int columns_of(bool e4m3, int n_rows) { return n_rows <= 16 ? 16 : n_rows <= 32 || e4m3 ? 32 : 64; }
+// Columns of a CTA: the fewest that hold the sequence's rows, as small products cost less shared-memory bandwidth
+// for nothing, up to what TMEM and shared memory allow; and half as many while the tiles that there can be leave half
+// the SMs without work (1 x 1000 tokens, 128 heads, E4M3: 32 CTAs of 32 columns 14.8 us, 64 of 16 columns 12.4 us).
+int columns_of(bool e4m3, int n_rows, long long tiles, int n_sm) {
+    int n = n_rows <= 16 ? 16 : n_rows <= 32 || e4m3 ? 32 : 64;
+    while (n > 16 && tiles * ((n_rows + n - 1) / n) * 2 <= n_sm) n /= 2;
+    return n;
+}
 
 // The pieces and scratch of a call: part, part_ml and pieces are offsets from NULL until placed.
 AttendPlan plan(const MlaAttendArgs &a, int n_sm, size_t *bytes) {
     AttendPlan g{};
     g.n_rows = a.n_q * a.H;
-    g.cols = columns_of(a.c.e4m3, g.n_rows);
+    const long long tiles = (long long)a.n_seq * ((a.pages_stride * a.c.page + kTile - 1) / kTile);
+    g.cols = columns_of(a.c.e4m3, g.n_rows, tiles, n_sm);
     g.nrb = (g.n_rows + g.cols - 1) / g.cols;
     g.n_slots = g.nrb < n_sm ? g.nrb : n_sm;
-    const long long tiles = (long long)a.n_seq * (a.pages_stride * a.c.page / kTile + 1);
     const long long ng = n_sm / g.n_slots;
     g.n_groups = (int)(ng < tiles ? ng : tiles);
     size_t at = 0;

@@ -70,18 +70,6 @@ struct Walk {
     }
 };
 
-// Slot of a token, -1 past the length or for a bad page.
-__device__ __forceinline__ int token_slot(const MlaAttendArgs &a, int b, int t, int len) {
-    if (t >= len) return -1;
-    const int pi = t / a.c.page;
-    const int id = a.pages[(long long)b * a.pages_stride + pi];
-    if (id < 0 || id >= a.c.n_pages) {
-        mla_bad_index(a.err);
-        return -1;
-    }
-    return id * a.c.page + (t - pi * a.c.page);
-}
-
 __device__ __forceinline__ void store_out(const MlaAttendArgs &a, long long e, float v) {
     if (a.out_bf16) reinterpret_cast<__nv_bfloat16 *>(a.out)[e] = __float2bfloat16_rn(v);
     else reinterpret_cast<float *>(a.out)[e] = v;
@@ -176,27 +164,49 @@ struct BoxAhead {
     int lane, nbox, pbox, share;
     bool fetch;
     int slot[3];
+    struct Asked {
+        int id, off;
+        bool live;
+    };
     __device__ BoxAhead(const MlaAttendArgs &a, const AttendPlan &g, const Piece &s, int slot_, int lane_, bool fetch_)
         : w(a, g, s, slot_), lane(lane_), nbox(kTile / g.pbox), pbox(g.pbox), share(slot_), fetch(fetch_) {
-        slot[0] = look();
-        slot[1] = look();
-        slot[2] = look();
+        // one round trip for the first three tiles' page ids
+        const Asked a0 = ask(), a1 = ask(), a2 = ask();
+        slot[0] = answer(a0);
+        slot[1] = answer(a1);
+        slot[2] = answer(a2);
     }
-    __device__ int look() {
-        if (!w.valid()) return -1;
-        const int sl = lane < nbox ? token_slot(w.a, w.b, w.tile() * kTile + lane * pbox, w.len) : -1;
-        if (fetch && sl >= 0) {
+    __device__ Asked ask() {
+        Asked q{-1, 0, false};
+        if (!w.valid()) return q;
+        const int t = w.tile() * kTile + lane * pbox;
+        if (lane < nbox && t < w.len) {
+            const int pi = t / w.a.c.page;
+            q.off = t - pi * w.a.c.page;
+            q.id = w.a.pages[(long long)w.b * w.a.pages_stride + pi];
+            q.live = true;
+        }
+        w.next();
+        return q;
+    }
+    __device__ int answer(const Asked &q) {
+        if (!q.live) return -1;
+        if (q.id < 0 || q.id >= w.a.c.n_pages) {
+            mla_bad_index(w.a.err);
+            return -1;
+        }
+        const int sl = q.id * w.a.c.page + q.off;
+        if (fetch) {
             // this CTA's share of the box's rows
             const int per = (pbox + w.g.n_slots - 1) / w.g.n_slots, r0 = min(pbox, share * per), r1 = min(pbox, r0 + per);
             if (r1 > r0) bulk_prefetch(mla_row(w.a.c, sl + r0), (r1 - r0) * w.a.c.row_bytes);
         }
-        w.next();
         return sl;
     }
     __device__ void next() {
         slot[0] = slot[1];
         slot[1] = slot[2];
-        slot[2] = look();
+        slot[2] = answer(ask());
     }
 };
 

@@ -118,17 +118,17 @@ __device__ __forceinline__ float largest(const uint4 (&x)[QB ? 1 : 2]) {
     return m;
 }
 
-// The query rows of a block -> E4M3 terms [L/128 blocks][2 NH][128], then [2 NH][64] (rope).  A warp takes four rows
-// at a time: lane l holds units l and l + 32 of each, and unit l % 8 of the rope part of row l / 8.
+// The query rows of a block -> E4M3 terms [L/128 blocks][2 NH][128], then [2 NH][64] (rope).  A warp takes NH / 8
+// rows: lane l holds units l and l + 32 of each, and unit l % 8 of the rope part of row l / 8.
 template <int NH, bool QB>
 __device__ __forceinline__ void load_queries8(const MlaAttendArgs &a, const AttendPlan &g, Shared8 &s, uint8_t *qsm, int b, int rb,
                                               int len, int warp, int lane) {
-    constexpr int W = QB ? 1 : 2;
+    constexpr int W = QB ? 1 : 2, RW = NH / 8;
     const int nu = a.c.L / 8, nr = a.c.R / 8, nru = (a.c.R + 31) / 32 * 4;
     uint8_t *rope = qsm + (a.c.L / 128) * (2 * NH * 128);
-#pragma unroll 1
-    for (int c0 = 4 * warp; c0 < NH; c0 += 32) {
-        uint4 x[4][2][W], xr[W];
+    const int c0 = RW * warp;
+    {
+        uint4 x[RW][2][W], xr[W];
         auto fetch = [&](int c, int u, bool ok, uint4 (&v)[W]) {
             const int r = rb * NH + c;
             ok = ok && r < g.n_rows;
@@ -137,15 +137,15 @@ __device__ __forceinline__ void load_queries8(const MlaAttendArgs &a, const Atte
             for (int w = 0; w < W; w++) v[w] = ok ? __ldg(src + w) : make_uint4(0u, 0u, 0u, 0u);
         };
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < RW; i++)
 #pragma unroll
             for (int k = 0; k < 2; k++) fetch(c0 + i, lane + 32 * k, lane + 32 * k < nu, x[i][k]);
-        fetch(c0 + lane / 8, nu + lane % 8, lane % 8 < nr, xr);
+        fetch(c0 + lane / 8, nu + lane % 8, lane / 8 < RW && lane % 8 < nr, xr);
         float mr = largest<QB>(xr), up_r = 0.f;
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, o));
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < RW; i++) {
             const int c = c0 + i, r = rb * NH + c;
             float mx = fmaxf(largest<QB>(x[i][0]), largest<QB>(x[i][1]));
 #pragma unroll
@@ -176,7 +176,7 @@ __device__ __forceinline__ void load_queries8(const MlaAttendArgs &a, const Atte
         uint2 t[2];
         query_terms<QB>(xr, up_r, t);
         const int u = lane % 8;
-        if (u < nru)
+        if (u < nru && lane / 8 < RW)
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 const int row = j * NH + c0 + lane / 8;

@@ -95,22 +95,25 @@ __global__ void __launch_bounds__(128) mla_append_kernel(const MlaAppendArgs a) 
     pdl_wait();
     pdl_trigger();
     if (t >= a.T) return;
+    const int L = a.c.L, R = a.c.R, half = R / 2, nk = L / 128;
+    const float *src = a.kv + t * a.kv_stride;
+    const bool pair = lane < half;
+    const int e0 = a.interleaved ? 2 * lane : lane, e1 = a.interleaved ? 2 * lane + 1 : half + lane;
+    // everything that needs no index first: one round trip, then one for the rotation
     const long long slot = a.slots[t];
     const int p = a.pos[t];
-    const int L = a.c.L, R = a.c.R, half = R / 2, nk = L / 128;
+    float4 x[4], wn[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        x[k] = k < nk ? __ldcs(reinterpret_cast<const float4 *>(src + 128 * k + 4 * lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        wn[k] = k < nk && a.norm ? *reinterpret_cast<const float4 *>(a.norm + 128 * k + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float xa = pair ? src[L + e0] : 0.f, xb = pair ? src[L + e1] : 0.f;
     if (slot == -1) return;
     if (slot < -1 || slot >= (long long)a.c.n_pages * a.c.page || p < 0 || p >= a.n_pos) {
         if (lane == 0) mla_bad_index(a.err);
         return;
     }
-    const float *src = a.kv + t * a.kv_stride;
-    float4 x[4];
-#pragma unroll
-    for (int k = 0; k < 4; k++)
-        x[k] = k < nk ? *reinterpret_cast<const float4 *>(src + 128 * k + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool pair = lane < half;
-    const int e0 = a.interleaved ? 2 * lane : lane, e1 = a.interleaved ? 2 * lane + 1 : half + lane;
-    const float xa = pair ? src[L + e0] : 0.f, xb = pair ? src[L + e1] : 0.f;
     const float *rot = a.rot + (long long)p * R;
     const float2 r = pair ? turn(xa, xb, rot[lane], rot[half + lane]) : make_float2(0.f, 0.f);
     if (a.norm) {
@@ -121,8 +124,7 @@ __global__ void __launch_bounds__(128) mla_append_kernel(const MlaAppendArgs a) 
 #pragma unroll
         for (int k = 0; k < 4; k++) {
             if (k >= nk) break;
-            const float4 w = *reinterpret_cast<const float4 *>(a.norm + 128 * k + 4 * lane);
-            x[k] = make_float4(x[k].x * f * w.x, x[k].y * f * w.y, x[k].z * f * w.z, x[k].w * f * w.w);
+            x[k] = make_float4(x[k].x * f * wn[k].x, x[k].y * f * wn[k].y, x[k].z * f * wn[k].z, x[k].w * f * wn[k].w);
         }
     }
     uint8_t *dst = a.c.rows + slot * a.c.row_bytes;
