@@ -9,6 +9,7 @@ namespace coli {
 
 constexpr int kTile = 128;               // tokens per tile
 constexpr int kSoft = 256;               // softmax threads
+constexpr int kStraddle = 3;              // tiles that a piece's second sequence costs
 constexpr float kNone = -3e38f;          // reference of a column that has none yet
 
 struct AttendPlan {
@@ -84,8 +85,10 @@ __device__ __forceinline__ const uint4 *query_unit(const MlaAttendArgs &a, long 
 }
 
 // Warp 0: this group's piece of the line of all sequences' tiles, and (block 0) the table of the sequences' groups.
-// As many groups as sequences or more: each sequence gets one group and its share of the others, so that no piece
-// straddles two sequences (which would cost a second start and end). Fewer groups: equal contiguous pieces.
+// Where that leaves no piece more than kStraddle tiles longer than an even cut, each sequence gets one group and its
+// share of the others, so that no piece straddles two sequences; otherwise the line is cut evenly.  A second start and
+// end cost a CTA about as much as kStraddle tiles (4 x 9000 tokens, 16 heads x 3 queries, bf16: 31.5 us cut evenly, 28.4
+// by sequences; 24 sequences of 3000 to 12000 tokens on 38 groups: 180 us by sequences, 98 cut evenly).
 __device__ __forceinline__ void find_piece(const MlaAttendArgs &a, const AttendPlan &g, int group, int lane, Piece &out) {
     auto tiles = [&](int b, bool check) {
         if (b >= a.n_seq) return 0;
@@ -106,8 +109,17 @@ __device__ __forceinline__ void find_piece(const MlaAttendArgs &a, const AttendP
     int total = mine;
     for (int b = lane + 32; b < a.n_seq; b += 32) total += tiles(b, true);
     total = __reduce_add_sync(0xffffffffu, total);
-    const bool shares = g.n_groups >= a.n_seq;
     const int chunk = (total + g.n_groups - 1) / g.n_groups, spare = g.n_groups - a.n_seq;
+    auto groups_of = [&](int T) { return min(T, 1 + (int)((long long)spare * T / total)); };
+    bool shares = spare >= 0;
+    if (shares) {
+        int longest = 0;
+        for (int b = lane; b < a.n_seq; b += 32) {
+            const int T = b < 32 ? mine : tiles(b, false), n = groups_of(T);
+            longest = max(longest, (T + n - 1) / n);
+        }
+        shares = __reduce_max_sync(0xffffffffu, longest) <= chunk + kStraddle;
+    }
     int u0 = shares ? 0 : min(total, group * chunk), u1 = shares ? 0 : min(total, u0 + chunk);
     if (lane == 0) {
         out.u0 = u0;
@@ -117,7 +129,7 @@ __device__ __forceinline__ void find_piece(const MlaAttendArgs &a, const AttendP
     int run_t = 0, run_g = 0;
     for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
         const int b = b0 + lane, T = b0 ? tiles(b, false) : mine;
-        const int n = shares && b < a.n_seq ? min(T, 1 + (int)((long long)spare * T / total)) : 0;
+        const int n = shares && b < a.n_seq ? groups_of(T) : 0;
         const int incl_t = scan(T), incl_g = shares ? scan(n) : 0;
         const int p = run_t + incl_t - T, g0 = shares ? run_g + incl_g - n : p / chunk;
         if (b < a.n_seq) {
