@@ -92,7 +92,7 @@ struct CachedTable {
 struct DeviceState {
     std::mutex mu;
     int *err = nullptr;           // device error word
-    int n_sm = 0;
+    int n_sm = 0, device = 0;
     size_t smem_optin = 0;
     std::map<cudaStream_t, Workspace> ws;
     std::unordered_map<uint64_t, CachedTable> tables;
@@ -118,6 +118,7 @@ int device_state(DeviceState **out) {
     int optin = 0;
     CU(cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev), "cudaDeviceGetAttribute");
     d->smem_optin = (size_t)optin;
+    d->device = dev;
     g_dev[dev] = d;
     *out = d;
     return COLI_OK;
@@ -255,17 +256,21 @@ void clear_last_error() { g_msg[0] = 0; }
 int injected_gate() { return injected(); }
 void count_call(int launches, uint64_t weight_bytes) { count(launches, weight_bytes); }
 
-int device_info(cudaStream_t st, size_t bytes, DevInfo *out) {
+int device_info(DevInfo *out) {
     DeviceState *ds = nullptr;
     if (int rc = device_state(&ds)) return rc;
     out->err = ds->err;
     out->n_sm = ds->n_sm;
+    out->device = ds->device;
     out->scratch = nullptr;
-    if (bytes) {
-        Workspace *ws = nullptr;
-        if (int rc = workspace(ds, st, bytes, &ws)) return rc;
-        out->scratch = ws->buf;
-    }
+    out->state = ds;
+    return COLI_OK;
+}
+
+int device_scratch(DevInfo *d, cudaStream_t st, size_t bytes) {
+    Workspace *ws = nullptr;
+    if (int rc = workspace((DeviceState *)d->state, st, bytes, &ws)) return rc;
+    d->scratch = ws->buf;
     return COLI_OK;
 }
 }  // namespace coli

@@ -23,6 +23,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "coli.h"
@@ -787,10 +788,21 @@ void count_call(int launches, uint64_t weight_bytes);
 // word, the SM count, and `bytes` of the stream's scratch (none for bytes = 0).
 struct DevInfo {
     int *err;
-    int n_sm;
+    int n_sm, device;
     void *scratch;
+    void *state;              // the library's own
 };
-int device_info(cudaStream_t st, size_t bytes, DevInfo *out);
+int device_info(DevInfo *out);
+int device_scratch(DevInfo *d, cudaStream_t st, size_t bytes);
+// Raise a kernel's shared-memory limit, once per device (`done`: one bit each, devices past 63 every time).
+template <class K>
+cudaError_t allow_smem(K kern, size_t bytes, int device, std::atomic<uint64_t> &done) {
+    const uint64_t bit = device < 64 ? 1ull << device : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
+}
 // Copy n expert descriptors, passed by value in kernel parameters, to the
 // device table dst (stream-ordered, no host memory involved).
 cudaError_t launch_table_fill(ExpertDesc *dst, const ExpertDesc *src, int n, cudaStream_t st);

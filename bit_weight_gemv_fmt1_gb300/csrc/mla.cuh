@@ -88,11 +88,11 @@ struct MlaPrefillArgs {
 cudaError_t launch_mla_query(const MlaQueryArgs &a, bool nope_bf16, bool rope_bf16, int n_sm, cudaStream_t st);
 cudaError_t launch_mla_append(const MlaAppendArgs &a, cudaStream_t st);
 cudaError_t launch_mla_read(const MlaReadArgs &a, bool out_bf16, cudaStream_t st);
-// Scratch of a call, and the call (scratch: that many bytes, NULL if none).
+// Scratch of a call, and the call (d.scratch: that many bytes, NULL if none).
 size_t mla_attend_scratch(const MlaAttendArgs &a, int n_sm);
-cudaError_t launch_mla_attend(const MlaAttendArgs &a, void *scratch, int n_sm, cudaStream_t st, int *n_launch);
+cudaError_t launch_mla_attend(const MlaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch);
 size_t mla_prefill_scratch(const MlaPrefillArgs &a);
-cudaError_t launch_mla_prefill(const MlaPrefillArgs &a, void *scratch, int n_sm, cudaStream_t st, int *n_launch);
+cudaError_t launch_mla_prefill(const MlaPrefillArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch);
 
 __device__ __forceinline__ void mla_bad_index(int *err) { atomicCAS(err, 0, (int)DEV_ERR_BAD_INDEX); }
 

@@ -92,7 +92,7 @@ int query(const float *q, int64_t q_stride, int T, int H, int nope, int rope, co
     if (int rc = injected_gate()) return rc;
     if (!T) return COLI_OK;
     DevInfo d;
-    if (int rc = device_info((cudaStream_t)stream, 0, &d)) return rc;
+    if (int rc = device_info(&d)) return rc;
     const MlaQueryArgs a{q, q_stride, T, H, nope, rope, pos, rot, n_pos, interleaved, out_nope, out_rope, ld_nope, ld_rope, d.err};
     return launched(launch_mla_query(a, dn == COLI_BF16, dr == COLI_BF16, d.n_sm, (cudaStream_t)stream), "coli_mla_query", 1);
 }
@@ -116,7 +116,7 @@ int append(const coli_mla_cache *cache, const float *kv, int64_t kv_stride, int 
     if (int rc = injected_gate()) return rc;
     if (!T) return COLI_OK;
     DevInfo d;
-    if (int rc = device_info((cudaStream_t)stream, 0, &d)) return rc;
+    if (int rc = device_info(&d)) return rc;
     a.kv = kv;
     a.kv_stride = kv_stride;
     a.T = T;
@@ -149,7 +149,7 @@ int read(const coli_mla_cache *cache, const int32_t *pages, int64_t pages_stride
     if (int rc = injected_gate()) return rc;
     if (!T || !n_seq) return COLI_OK;
     DevInfo d;
-    if (int rc = device_info((cudaStream_t)stream, 0, &d)) return rc;
+    if (int rc = device_info(&d)) return rc;
     a.pages = pages;
     a.pages_stride = pages_stride;
     a.n_seq = n_seq;
@@ -202,12 +202,12 @@ int attend(const coli_mla_cache *cache, int dtype_q, const void *q_latent, const
     a.out = out;
     a.lse = lse;
     DevInfo d;
-    if (int rc = device_info((cudaStream_t)stream, 0, &d)) return rc;
+    if (int rc = device_info(&d)) return rc;
     if (const size_t bytes = mla_attend_scratch(a, d.n_sm))
-        if (int rc = device_info((cudaStream_t)stream, bytes, &d)) return rc;
+        if (int rc = device_scratch(&d, (cudaStream_t)stream, bytes)) return rc;
     a.err = d.err;
     int n = 0;
-    const cudaError_t e = launch_mla_attend(a, d.scratch, d.n_sm, (cudaStream_t)stream, &n);
+    const cudaError_t e = launch_mla_attend(a, d, (cudaStream_t)stream, &n);
     return launched(e, "coli_mla_attend", n);
 }
 
@@ -265,10 +265,12 @@ int prefill(int dtype, const void *q, int64_t q_stride, const void *kv, int64_t 
     a.out = out;
     a.lse = lse;
     DevInfo d;
-    if (int rc = device_info((cudaStream_t)stream, mla_prefill_scratch(a), &d)) return rc;
+    if (int rc = device_info(&d)) return rc;
+    if (const size_t bytes = mla_prefill_scratch(a))
+        if (int rc = device_scratch(&d, (cudaStream_t)stream, bytes)) return rc;
     a.err = d.err;
     int n = 0;
-    const cudaError_t e = launch_mla_prefill(a, d.scratch, d.n_sm, (cudaStream_t)stream, &n);
+    const cudaError_t e = launch_mla_prefill(a, d, (cudaStream_t)stream, &n);
     return launched(e, "coli_mla_prefill", n);
 }
 

@@ -559,7 +559,8 @@ AttendPlan plan(const MlaAttendArgs &a, int n_sm, size_t *bytes) {
     const long long ng = n_sm / g.n_slots;
     g.n_groups = (int)(ng < tiles ? ng : tiles);
     size_t at = 0;
-    if (g.n_groups > 1) {
+    // sequences of one tile at most are never split
+    if (g.n_groups > 1 && a.pages_stride * a.c.page > kTile) {
         const size_t parts = (size_t)g.n_groups * g.nrb * 2 * g.cols;
         g.part = (float *)at;
         at += parts * a.c.L * sizeof(float);
@@ -599,7 +600,7 @@ cudaError_t bf16_map(const void *p, int cols, long long rows, int box_rows, CUte
 }
 
 template <int N>
-cudaError_t run_bf16(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t st) {
+cudaError_t run_bf16(const MlaAttendArgs &a, const AttendPlan &g, int device, cudaStream_t st) {
     CUtensorMap map, q, qr;
     if (cudaError_t e = mla_row_map(a.c, 64, g.pbox, CU_TENSOR_MAP_SWIZZLE_128B, &map)) return e;
     q = qr = map;                        // f32 queries: never read
@@ -611,7 +612,8 @@ cudaError_t run_bf16(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t s
     const int nblk = a.c.L / 64 + 1;
     const size_t smem = (size_t)nblk * kBlk + (size_t)nblk * N * 128 + 1024;
     auto kern = mla_attend_bf16_kernel<N>;
-    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+    static std::atomic<uint64_t> done{0};
+    if (cudaError_t e = allow_smem(kern, (size_t)9 * (kBlk + N * 128) + 1024, device, done)) return e;   // the largest latent's
     return launch_pdl(kern, dim3(g.n_groups * g.n_slots), dim3(kThreads), smem, st, map, q, qr, a, g);
 }
 
@@ -628,19 +630,21 @@ size_t mla_attend_scratch(const MlaAttendArgs &a, int n_sm) {
     return bytes;
 }
 
-cudaError_t launch_mla_attend(const MlaAttendArgs &a, void *scratch, int n_sm, cudaStream_t st, int *n_launch) {
+cudaError_t launch_mla_attend(const MlaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch) {
     size_t bytes;
+    const int n_sm = d.n_sm;
     AttendPlan g = plan(a, n_sm, &bytes);
+    void *scratch = d.scratch;
     if (bytes) {
         g.part = (float *)((char *)scratch + (size_t)g.part);
         g.part_ml = (float *)((char *)scratch + (size_t)g.part_ml);
         g.pieces = (int2 *)((char *)scratch + (size_t)g.pieces);
     }
-    *n_launch = g.n_groups > 1 ? 2 : 1;
+    *n_launch = g.pieces ? 2 : 1;
     cudaError_t e;
-    if (a.c.e4m3) e = launch_mla_attend_e4m3(a, g, st);
-    else e = g.cols == 16 ? run_bf16<16>(a, g, st) : g.cols == 32 ? run_bf16<32>(a, g, st) : run_bf16<64>(a, g, st);
-    if (e != cudaSuccess || g.n_groups == 1) return e;
+    if (a.c.e4m3) e = launch_mla_attend_e4m3(a, g, d.device, st);
+    else e = g.cols == 16 ? run_bf16<16>(a, g, d.device, st) : g.cols == 32 ? run_bf16<32>(a, g, d.device, st) : run_bf16<64>(a, g, d.device, st);
+    if (e != cudaSuccess || !g.pieces) return e;
     // enough warps for the device, a block of 16 at a time
     const int rows = a.n_seq * g.n_rows;
     int wpr = 16;

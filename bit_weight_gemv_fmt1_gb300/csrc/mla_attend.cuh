@@ -223,7 +223,7 @@ struct BoxAhead {
 };
 
 // The E4M3 kernel (mla_attend_e4m3.cu).
-cudaError_t launch_mla_attend_e4m3(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t st);
+cudaError_t launch_mla_attend_e4m3(const MlaAttendArgs &a, const AttendPlan &g, int device, cudaStream_t st);
 // Tensor map of the cache's rows: boxes of `inner` elements x `pbox` rows, with that swizzle.
 cudaError_t mla_row_map(const MlaCache &c, int inner, int pbox, CUtensorMapSwizzle swizzle, CUtensorMap *out);
 

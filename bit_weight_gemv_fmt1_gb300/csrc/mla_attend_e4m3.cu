@@ -544,22 +544,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+constexpr size_t smem_bytes(size_t np, size_t cols) {
+    return 2 * (np * kBlk8 + kRope8) + np * (2 * cols * 128) + 2 * cols * 64 + 2 * kP8 + 1024;
+}
+
 template <int NH>
-cudaError_t run(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t st) {
+cudaError_t run(const MlaAttendArgs &a, const AttendPlan &g, int device, cudaStream_t st) {
     CUtensorMap map, rope;
     if (cudaError_t e = mla_row_map(a.c, 128, g.pbox, CU_TENSOR_MAP_SWIZZLE_128B, &map)) return e;
     if (cudaError_t e = mla_row_map(a.c, 64, g.pbox, CU_TENSOR_MAP_SWIZZLE_64B, &rope)) return e;
-    const size_t np = a.c.L / 128;
-    const size_t smem = 2 * (np * kBlk8 + kRope8) + np * (2 * NH * 128) + 2 * NH * 64 + 2 * kP8 + 1024;
+    const size_t smem = smem_bytes(a.c.L / 128, NH);
     auto kern = mla_attend_e4m3_kernel<NH>;
-    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+    static std::atomic<uint64_t> done{0};
+    if (cudaError_t e = allow_smem(kern, smem_bytes(4, NH), device, done)) return e;   // the largest latent's
     return launch_pdl(kern, dim3(g.n_groups * g.n_slots), dim3(kThreads), smem, st, map, rope, a, g);
 }
 
 }  // namespace
 
-cudaError_t launch_mla_attend_e4m3(const MlaAttendArgs &a, const AttendPlan &g, cudaStream_t st) {
-    return g.cols == 16 ? run<16>(a, g, st) : run<32>(a, g, st);
+cudaError_t launch_mla_attend_e4m3(const MlaAttendArgs &a, const AttendPlan &g, int device, cudaStream_t st) {
+    return g.cols == 16 ? run<16>(a, g, device, st) : run<32>(a, g, device, st);
 }
 
 }  // namespace coli

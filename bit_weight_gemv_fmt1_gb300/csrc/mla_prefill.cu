@@ -389,7 +389,7 @@ cudaError_t matrix_map(const void *p, long long cols, long long rows, long long 
 }
 
 template <int V>
-cudaError_t run(const MlaPrefillArgs &a, cudaStream_t st) {
+cudaError_t run(const MlaPrefillArgs &a, int device, cudaStream_t st) {
     CUtensorMap q, kv, kr, vm;
     if (cudaError_t e = matrix_map(a.q, (long long)a.H * (a.nope + a.rope), a.Tq, a.q_stride, kRows, &q)) return e;
     kv = kr = vm = q;                         // no keys: never read
@@ -401,7 +401,9 @@ cudaError_t run(const MlaPrefillArgs &a, cudaStream_t st) {
     const int nb = a.nope / 64 + 1, max_pairs = (a.Tq + 2 * kRows - 1) / (2 * kRows) + a.n_seq - 1;
     const size_t smem = (size_t)(4 * nb + V / 64) * kBlk + 1024;
     auto kern = mla_prefill_kernel<V>;
-    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+    static std::atomic<uint64_t> done{0};
+    if (cudaError_t e = allow_smem(kern, (size_t)(12 + V / 64) * kBlk + 1024, device, done)) return e;   // nope = 128
+
     return launch_pdl(kern, dim3((unsigned)max_pairs * a.H), dim3(384), smem, st, q, kv, kr, vm, a, max_pairs, 2000000000LL);
 }
 
@@ -415,7 +417,7 @@ size_t mla_prefill_scratch(const MlaPrefillArgs &a) {
            round256((size_t)a.Tk * a.rope * 2);
 }
 
-cudaError_t launch_mla_prefill(const MlaPrefillArgs &a0, void *scratch, int n_sm, cudaStream_t st, int *n_launch) {
+cudaError_t launch_mla_prefill(const MlaPrefillArgs &a0, const DevInfo &d, cudaStream_t st, int *n_launch) {
     MlaPrefillArgs a = a0;
     *n_launch = 1;
     if (a.in_f32) {
@@ -423,13 +425,13 @@ cudaError_t launch_mla_prefill(const MlaPrefillArgs &a0, void *scratch, int n_sm
         const long long rows[3] = {a.Tq, a.Tk, a.Tk}, strides[3] = {a.q_stride, a.kv_stride, a.kr_stride};
         const void *src[3] = {a.q, a.kv, a.k_rope};
         __nv_bfloat16 *dst[3];
-        char *at = (char *)scratch;
+        char *at = (char *)d.scratch;
         for (int i = 0; i < 3; i++) {
             dst[i] = (__nv_bfloat16 *)at;
             at += round256((size_t)rows[i] * cols[i] * 2);
             const long long want = (rows[i] * (cols[i] / 8) + 255) / 256;
             if (want == 0) continue;
-            if (cudaError_t e = launch_pdl(mla_round_kernel, dim3((unsigned)(want < 32LL * n_sm ? want : 32LL * n_sm)), dim3(256), 0, st,
+            if (cudaError_t e = launch_pdl(mla_round_kernel, dim3((unsigned)(want < 32LL * d.n_sm ? want : 32LL * d.n_sm)), dim3(256), 0, st,
                                            (const float *)src[i], strides[i], rows[i], cols[i], dst[i]))
                 return e;
             ++*n_launch;
@@ -441,7 +443,7 @@ cudaError_t launch_mla_prefill(const MlaPrefillArgs &a0, void *scratch, int n_sm
         a.kv_stride = cols[1];
         a.kr_stride = cols[2];
     }
-    return a.v == 64 ? run<64>(a, st) : run<128>(a, st);
+    return a.v == 64 ? run<64>(a, d.device, st) : run<128>(a, d.device, st);
 }
 
 }  // namespace coli
