@@ -1,8 +1,14 @@
 // mla_prefill.cu -- causal attention of packed sequences in the expanded form,
 // on the 5th-generation tensor cores.
 //
-// A CTA takes one head and 256 query rows of one sequence as two tiles A and B
-// of 128, and walks over the keys in tiles of 128:
+// A unit of work is one head and 256 query rows of one sequence, two tiles A and
+// B of 128, and a walk over the keys in tiles of 128.  The grid has a CTA per unit, longest first; a CTA that nears its
+// unit's end takes over one that has not started (cluster launch control), so that the next queries, keys and
+// scores come while the last output is written.  Only the key warp looks units up; it hands them on through a ring of
+// two, and every warp spreads them from lane 0: MMA and copy operands that the compiler cannot prove uniform cost 300 of
+// 2900 cycles a tile.  Times of 8192 tokens x 32 heads / 4 x 2048 x 32 / 3 x 4000 with 4000 cached x 8, us: a CTA per
+// unit in the order of heads 515 / 124 / 236; units of a fixed share 485 / 120 / 235; this 474 / 96 / 233.  Taking heads in groups
+// whose keys fit L2: 494 / 105 / 238; keys and values asked into L2 four tiles ahead: slower by 2 %.
 //   S = Q K^T   M = 128 queries, N = 128 keys, K = nope + rope (K-major operands in shared memory)
 //   O += P V    M = 128 queries, N = v, K = 128 keys (P in TMEM, V as stored: N-major)
 // The two tiles alternate: while the softmax of one runs, the tensor cores work
@@ -20,10 +26,12 @@
 //
 // Keys past a causal row's limit are masked by selection; value rows past the
 // sequence's end belong to its neighbours and are zeroed in shared memory.
-// Warps: 0-3 and 4-7 softmax of A and B, 8 MMA issue, 9 copies of keys, 10 and 11 of queries and values.
+// Warps: 0-3 and 4-7 softmax of A and B, 8 MMA issue, 9 units and copies of keys, 10 and 11 of queries and values.
 // Every wait is bounded; after one has run out all waits return at once, no
 // further MMA or copy is issued, and the kernel records DEV_ERR_TIMEOUT.
 #include <cudaTypedefs.h>
+
+#include <algorithm>
 
 #include "mla.cuh"
 #include "tcgen05.cuh"
@@ -43,17 +51,142 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// One unit of work: a head's pair of query tiles.
+struct Unit {
+    int head, q0, nq, nk, qrow, krow;    // first query of the pair in its sequence, the sequence's sizes and first rows
+    int nt[2], n;                        // key tiles that each query tile sees, the larger of them; n < 0: no more units
+};
+
 struct Shared {
-    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], u_full[2], u_empty[2];
+    uint64_t next_full;
+    Unit unit[2];
+    alignas(16) uint32_t next[4];        // the answer to the last request for a CTA's work
     uint32_t tmem;
     int abort;
-    int b, q0, nq, nk, qrow, krow;       // sequence, first query of the pair in it, its sizes, first rows
 };
+
+
+// Sequence b's offsets (all 0 where they are bad) and its number of pairs.
+__device__ __forceinline__ int pairs_of(const MlaPrefillArgs &a, int b, bool report, int4 &c) {
+    c = make_int4(0, 0, 0, 0);
+    if (b >= a.n_seq) return 0;
+    const int4 d = make_int4(a.cu_q[b], a.cu_q[b + 1], a.cu_k[b], a.cu_k[b + 1]);
+    const bool good = d.x >= 0 && d.y >= d.x && d.y <= a.Tq && d.z >= 0 && d.w >= d.z && d.w <= a.Tk;
+    if (report && !good) mla_bad_index(a.err);
+    if (good) c = d;
+    return (c.y - c.x + 2 * kRows - 1) / (2 * kRows);
+}
+// How many of a sequence's n pairs see v key tiles or more: the last pair sees all nk keys, each one before it 256
+// fewer rows' worth.
+__device__ __forceinline__ int pairs_with(int n, int4 c, int v) {
+    if (v <= 0) return n;
+    const int spare = c.w - c.z - ((v - 1) * kRows + 1);   // rows that may lie behind the pair's last
+    if (spare < 0) return 0;
+    const int need = max(1, (c.y - c.x - spare + 2 * kRows - 1) / (2 * kRows));
+    return min(n, max(0, n - need + 1));
+}
+// Whole warp: the pairs of all sequences, and the most key tiles that one sees.
+__device__ __forceinline__ int all_pairs(const MlaPrefillArgs &a, int lane, bool report, int &most) {
+    int total = 0;
+    most = 0;
+    for (int b = lane; b < a.n_seq; b += 32) {
+        int4 c;
+        total += pairs_of(a, b, report, c);
+        most = max(most, (c.w - c.z + kRows - 1) / kRows);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    return __reduce_add_sync(0xffffffffu, total);
+}
+// Whole warp: unit i, in the order of key tiles, most first, all heads of a pair together.
+__device__ __forceinline__ Unit unit_of(const MlaPrefillArgs &a, int i, int most, int lane) {
+    Unit u;
+    const int p = i / a.H;
+    u.head = i - p * a.H;
+    int4 first;
+    const int n0 = pairs_of(a, lane, false, first);
+    auto count = [&](int v) {
+        int t = pairs_with(n0, first, v);
+        for (int b = lane + 32; b < a.n_seq; b += 32) {
+            int4 c;
+            const int n = pairs_of(a, b, false, c);
+            t += pairs_with(n, c, v);
+        }
+        return __reduce_add_sync(0xffffffffu, t);
+    };
+    int v = 0, hi = most + 1;                 // count(v) > p >= count(hi)
+    while (hi - v > 1) {
+        const int mid = (v + hi) / 2;
+        if (count(mid) > p) v = mid;
+        else hi = mid;
+    }
+    int run = count(v + 1);                   // then the pairs that see v tiles, sequence by sequence
+    u.q0 = u.nq = u.nk = u.qrow = u.krow = 0;
+    for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
+        int4 c = first;
+        const int n = b0 ? pairs_of(a, b0 + lane, false, c) : n0;
+        const int above = pairs_with(n, c, v + 1), here = pairs_with(n, c, v) - above;
+        int incl = here;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += w;
+        }
+        const int before = run + incl - here;
+        const uint32_t hit = __ballot_sync(0xffffffffu, before <= p && p < before + here);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            u.q0 = __shfl_sync(0xffffffffu, (n - 1 - above - (p - before)) * 2 * kRows, src);
+            u.qrow = __shfl_sync(0xffffffffu, c.x, src);
+            u.nq = __shfl_sync(0xffffffffu, c.y, src) - u.qrow;
+            u.krow = __shfl_sync(0xffffffffu, c.z, src);
+            u.nk = __shfl_sync(0xffffffffu, c.w, src) - u.krow;
+            break;
+        }
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; x++) {
+        // the last live row's limit
+        const int rows = min(kRows, u.nq - u.q0 - x * kRows);
+        const int limit = rows > 0 ? u.q0 + x * kRows + rows + u.nk - u.nq : 0;
+        u.nt[x] = limit > 0 ? (min(limit, u.nk) + kRows - 1) / kRows : 0;
+    }
+    u.n = max(u.nt[0], u.nt[1]);
+    return u;
+}
+
+// The same values, all from lane 0: the compiler then keeps them, and the operands of MMAs and copies that derive from
+// them, in uniform registers.
+__device__ __forceinline__ Unit uniform(Unit u) {
+    for (int *p : {&u.head, &u.q0, &u.nq, &u.nk, &u.qrow, &u.krow, &u.nt[0], &u.nt[1], &u.n}) *p = __shfl_sync(0xffffffffu, *p, 0);
+    return u;
+}
+
+// Asks for the work of a CTA that has not started yet, in its stead; the answer (16 bytes) comes to `next`.
+__device__ __forceinline__ void ask_next(Shared &s) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_addr(s.next)),
+                 "r"(smem_addr(&s.next_full))
+                 : "memory");
+}
+// That CTA's index; -1: all have started, and no further request may be made.
+__device__ __forceinline__ int read_next(Shared &s) {
+    int i;
+    asm volatile(
+        "{\n .reg .b128 r;\n .reg .pred p;\n mov.s32 %0, -1;\n ld.shared.b128 r, [%1];\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n"
+        " fence.proxy.async.shared::cta;\n}\n"
+        : "=&r"(i)
+        : "r"(smem_addr(s.next))
+        : "memory");
+    return i;
+}
 
 template <int V>
 __global__ void __launch_bounds__(384, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
-                       const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap v_map, const MlaPrefillArgs a, int max_pairs, long long timeout_ns) {
+                       const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap v_map, const MlaPrefillArgs a, long long timeout_ns) {
     extern __shared__ uint8_t raw[];
     __shared__ Shared s;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
@@ -61,52 +194,13 @@ __global__ void __launch_bounds__(384, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int nn = a.nope / 64, nb = nn + 1;             // blocks of a query or key tile: no-position part, rotary part
     const uint32_t k_off = 2 * nb * kBlk, v_off = k_off + 2 * nb * kBlk;
-    const int head = blockIdx.x / max_pairs, idx = blockIdx.x - head * max_pairs;
     pdl_wait();
     pdl_trigger();
-    if (warp == 1) {
-        // this CTA's pair: the last pairs of the sequences, whose rows see most keys, come first
-        int total = 0;
-        for (int b = lane; b < a.n_seq; b += 32) {
-            const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
-            const bool good = q0 >= 0 && q1 >= q0 && q1 <= a.Tq && k0 >= 0 && k1 >= k0 && k1 <= a.Tk;
-            if (!good) mla_bad_index(a.err);
-            total += good ? (q1 - q0 + 2 * kRows - 1) / (2 * kRows) : 0;
-        }
-        total = __reduce_add_sync(0xffffffffu, total);
-        int p = total - 1 - idx, run = 0;
-        if (lane == 0) s.b = -1;
-        __syncwarp();
-        for (int b0 = 0; b0 < a.n_seq && p >= 0; b0 += 32) {
-            const int b = b0 + lane;
-            int n = 0, q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-            if (b < a.n_seq) {
-                q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
-                const bool good = q0 >= 0 && q1 >= q0 && q1 <= a.Tq && k0 >= 0 && k1 >= k0 && k1 <= a.Tk;
-                n = good ? (q1 - q0 + 2 * kRows - 1) / (2 * kRows) : 0;
-            }
-            int incl = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            const int before = run + incl - n;
-            if (n > 0 && before <= p && p < before + n) {
-                s.b = b;
-                s.q0 = (p - before) * 2 * kRows;
-                s.nq = q1 - q0;
-                s.nk = k1 - k0;
-                s.qrow = q0;
-                s.krow = k0;
-            }
-            run += __shfl_sync(0xffffffffu, incl, 31);
-        }
-    }
     if (warp == 0) tmem_alloc(&s.tmem, 512);
     if (tid == 0) {
         for (int i = 0; i < 2; i++) {
             mbar_init(&s.q_full[i], 1);
+            mbar_init(&s.q_empty[i], 1);
             mbar_init(&s.k_full[i], 1);
             mbar_init(&s.k_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
@@ -114,7 +208,10 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&s.o_full[i], 1);
             mbar_init(&s.v_full[i], 1);
             mbar_init(&s.v_empty[i], 1);
+            mbar_init(&s.u_full[i], 1);
+            mbar_init(&s.u_empty[i], 11);
         }
+        mbar_init(&s.next_full, 1);
         s.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -133,146 +230,154 @@ __global__ void __launch_bounds__(384, 1)
             atomicCAS(a.err, 0, (int)DEV_ERR_TIMEOUT);
         }
     };
-    // key tiles that the rows of tile x see: the last live row's limit
-    const bool live = s.b >= 0;
-    const int q0 = s.q0, nq = s.nq, nk = s.nk;
-    auto tiles = [&](int x) {
-        const int rows = live ? min(kRows, nq - q0 - x * kRows) : 0;
-        const int limit = rows > 0 ? q0 + x * kRows + rows - 1 + nk - nq + 1 : 0;
-        return limit > 0 ? (min(limit, nk) + kRows - 1) / kRows : 0;
+    // Unit r of this CTA as the key warp has found it; the warp that has read it says so.
+    auto take = [&](int r) {
+        wait(&s.u_full[r & 1], (r >> 1) & 1);
+        Unit u = s.unit[r & 1];
+        if (!ok) u.n = -1;
+        u = uniform(u);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.u_empty[r & 1]);
+        return u;
     };
-    const int nt[2] = {tiles(0), tiles(1)}, n = max(nt[0], nt[1]);
 
     if (warp < 8) {
         // ---------------------------------------------------------- softmax and output
-        const int x = warp >> 2, t = tid & 127, row = q0 + x * kRows + t;
+        const int x = warp >> 2, t = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), S = lanes + x * 128, O = lanes + 256 + x * V;
-        const int limit = row + nk - nq + 1;             // keys this row sees
-        const int first_limit = q0 + x * kRows + nk - nq + 1;
         // a negative scale turns the scores' sign; a zero one must still send masked scores (-inf) to -inf
         const bool negative = a.scale < 0.f;
         const float f = a.scale == 0.f ? 1e-37f : fabsf(a.scale) * 1.4426950408889634f;
-        float m = kNone;
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int j = 0; j < nt[x]; j++) {
-            wait(&s.s_full[x], j & 1);
-            tc_after_sync();
-            const int k0 = j * kRows;
-            const bool full = k0 + kRows <= first_limit && k0 + kRows <= nk;   // every row sees the whole tile
-            const int seen = full ? kRows : min(limit, nk) - k0;              // this row's keys in the tile
-            // the row's scores, all at once: every wait for TMEM costs more than the arithmetic on a quarter of them
-            uint32_t v[kRows];
+        int k_tiles = 0, s_tiles = 0, outs = 0;          // key tiles, this tile's score tiles and outputs so far
+        for (int r = 0;; r++) {
+            const Unit u = take(r);
+            if (u.n < 0) break;
+            const int row = u.q0 + x * kRows + t, nk = u.nk, nt = x ? u.nt[1] : u.nt[0];
+            const int limit = min(row + nk - u.nq + 1, nk);  // keys this row sees
+            const int all = min(row - t + nk - u.nq + 1, nk);   // keys every row of the tile sees
+            const long long orow = row < u.nq ? (long long)(u.qrow + row) * a.H + u.head : -1;
+            float m = kNone;
+            float l4[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < nt; j++) {
+                wait(&s.s_full[x], s_tiles++ & 1);
+                tc_after_sync();
+                const int k0 = j * kRows;
+                const bool full = k0 + kRows <= all;
+                const int seen = limit - k0;                 // this row's keys in the tile
+                // the row's scores, all at once: every wait for TMEM costs more than the arithmetic on a quarter of them
+                uint32_t v[kRows];
 #pragma unroll
-            for (int c0 = 0; c0 < kRows; c0 += 32) tmem_ld(S + c0, *reinterpret_cast<uint32_t(*)[32]>(v + c0));
-            tmem_ld_wait();
-            if (negative)
+                for (int c0 = 0; c0 < kRows; c0 += 32) tmem_ld(S + c0, *reinterpret_cast<uint32_t(*)[32]>(v + c0));
+                tmem_ld_wait();
+                if (negative)
 #pragma unroll
-                for (int c = 0; c < kRows; c++) v[c] ^= 0x80000000u;
-            if (!full)
+                    for (int c = 0; c < kRows; c++) v[c] ^= 0x80000000u;
+                if (!full)
 #pragma unroll
-                for (int c = 0; c < kRows; c++)
-                    if (c >= seen) v[c] = 0xFF800000u;
-            float t4[4];
+                    for (int c = 0; c < kRows; c++)
+                        if (c >= seen) v[c] = 0xFF800000u;
+                float t4[4];
 #pragma unroll
-            for (int k = 0; k < 4; k++) t4[k] = max3(__uint_as_float(v[k]), __uint_as_float(v[4 + k]), __uint_as_float(v[8 + k]));
+                for (int k = 0; k < 4; k++) t4[k] = max3(__uint_as_float(v[k]), __uint_as_float(v[4 + k]), __uint_as_float(v[8 + k]));
 #pragma unroll
-            for (int c = 12; c + 8 <= kRows; c += 8)
+                for (int c = 12; c + 8 <= kRows; c += 8)
 #pragma unroll
-                for (int k = 0; k < 4; k++) t4[k] = max3(t4[k], __uint_as_float(v[c + k]), __uint_as_float(v[c + 4 + k]));
+                    for (int k = 0; k < 4; k++) t4[k] = max3(t4[k], __uint_as_float(v[c + k]), __uint_as_float(v[c + 4 + k]));
 #pragma unroll
-            for (int k = 0; k < 4; k++) t4[k] = fmaxf(t4[k], __uint_as_float(v[kRows - 4 + k]));
-            const float now = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f;
-            const bool move = now > m + kGrow;
-            if (__any_sync(0xffffffffu, move)) {
-                const float r = move ? ex2(m - now) : 1.f;
-                if (move) m = now;
+                for (int k = 0; k < 4; k++) t4[k] = fmaxf(t4[k], __uint_as_float(v[kRows - 4 + k]));
+                const float now = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f;
+                const bool move = now > m + kGrow;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float r = move ? ex2(m - now) : 1.f;
+                    if (move) m = now;
 #pragma unroll
-                for (int k = 0; k < 4; k++) l4[k] *= r;
-                if (j > 0) {
+                    for (int k = 0; k < 4; k++) l4[k] *= r;
+                    if (j > 0) {
 #pragma unroll 1
-                    for (int c0 = 0; c0 < V; c0 += 8) {
-                        uint32_t o[8];
-                        tmem_ld(O + c0, o);
-                        tmem_ld_wait();
+                        for (int c0 = 0; c0 < V; c0 += 8) {
+                            uint32_t o[8];
+                            tmem_ld(O + c0, o);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int c = 0; c < 8; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * r);
-                        tmem_st(O + c0, o);
+                            for (int c = 0; c < 8; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * r);
+                            tmem_st(O + c0, o);
+                        }
                     }
                 }
-            }
-            const float m0 = -m;
+                const float m0 = -m;
 #pragma unroll
-            for (int c0 = 0; c0 < kRows; c0 += 32) {
-                uint32_t p[16];
+                for (int c0 = 0; c0 < kRows; c0 += 32) {
+                    uint32_t p[16];
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    const float x = ex2(fmaf(__uint_as_float(v[c0 + c]), f, m0)), y = ex2(fmaf(__uint_as_float(v[c0 + c + 1]), f, m0));
-                    l4[c & 3] += x;
-                    l4[(c + 1) & 3] += y;
-                    p[c / 2] = pack_bf16(x, y);
+                    for (int c = 0; c < 32; c += 2) {
+                        const float x = ex2(fmaf(__uint_as_float(v[c0 + c]), f, m0)), y = ex2(fmaf(__uint_as_float(v[c0 + c + 1]), f, m0));
+                        l4[c & 3] += x;
+                        l4[(c + 1) & 3] += y;
+                        p[c / 2] = pack_bf16(x, y);
+                    }
+                    tmem_st(S + c0 / 2, p);                  // over scores that have been read
                 }
-                tmem_st(S + c0 / 2, p);                  // over scores that have been read
-            }
-            if (k0 + kRows > nk) {
-                // value rows of other sequences may hold anything, and 0 * NaN is NaN
-                wait(&s.v_full[0], j & 1);
-                wait(&s.v_full[1], j & 1);
-                if (k0 + t >= nk)
+                if (k0 + kRows > nk) {
+                    // value rows of other sequences may hold anything, and 0 * NaN is NaN
+                    wait(&s.v_full[0], (k_tiles + j) & 1);
+                    wait(&s.v_full[1], (k_tiles + j) & 1);
+                    if (k0 + t >= nk)
 #pragma unroll
-                    for (int k = 0; k < V / 64; k++)
+                        for (int k = 0; k < V / 64; k++)
 #pragma unroll
-                        for (int u = 0; u < 8; u++) *reinterpret_cast<uint4 *>(sm + v_off + k * kBlk + t * 128 + 16 * u) = make_uint4(0u, 0u, 0u, 0u);
-                fence_async_smem();
+                            for (int c = 0; c < 8; c++) *reinterpret_cast<uint4 *>(sm + v_off + k * kBlk + t * 128 + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_async_smem();
+                }
+                tmem_st_wait();
+                tc_before_sync();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(&s.p_full[x]);
             }
-            tmem_st_wait();
-            tc_before_sync();
-            __syncwarp();
-            if (lane == 0 && ok) mbar_arrive(&s.p_full[x]);
-        }
-        const bool store = live && row < nq;
-        const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        const float inv = l != 0.f ? 1.f / l : 0.f;
-        const long long orow = ((long long)(s.qrow + row) * a.H + head);
-        if (nt[x] > 0) {
-            wait(&s.o_full[x], 0);
-            tc_after_sync();
-        }
+            k_tiles += u.n;
+            const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            if (nt > 0) {
+                wait(&s.o_full[x], outs++ & 1);
+                tc_after_sync();
+            }
 #pragma unroll 1
-        for (int c0 = 0; c0 < V; c0 += 32) {
-            uint32_t o[32];
-            if (nt[x] > 0) {
-                tmem_ld(O + c0, o);
-                tmem_ld_wait();
-            } else {
+            for (int c0 = 0; c0 < V; c0 += 32) {
+                uint32_t o[32];
+                if (nt > 0) {
+                    tmem_ld(O + c0, o);
+                    tmem_ld_wait();
+                } else {
 #pragma unroll
-                for (int c = 0; c < 32; c++) o[c] = 0u;
-            }
-            if (!store) continue;
-#pragma unroll
-            for (int c = 0; c < 32; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
-            if (a.out_bf16) {
-                uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * V + c0);
-#pragma unroll
-                for (int c = 0; c < 32; c += 8) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; k++) w[k] = pack_bf16(__uint_as_float(o[c + 2 * k]), __uint_as_float(o[c + 2 * k + 1]));
-                    d[c / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int c = 0; c < 32; c++) o[c] = 0u;
                 }
-            } else {
-                uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<float *>(a.out) + orow * V + c0);
+                if (orow < 0) continue;
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) d[c / 4] = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                for (int c = 0; c < 32; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
+                if (a.out_bf16) {
+                    uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * V + c0);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; k++) w[k] = pack_bf16(__uint_as_float(o[c + 2 * k]), __uint_as_float(o[c + 2 * k + 1]));
+                        d[c / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<float *>(a.out) + orow * V + c0);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) d[c / 4] = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                }
             }
+            if (orow >= 0 && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            tc_before_sync();
         }
-        if (store && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     } else if (warp == 8) {
         // ---------------------------------------------------------- MMA issue
         constexpr uint32_t id_s = f16_idesc(1, false, false, kRows, kRows), id_o = f16_idesc(1, false, true, kRows, V);
         const uint64_t dq = sw128_desc(base, 16, 1024), dk = sw128_desc(base + k_off, 16, 1024), dv = sw128_desc(base + v_off, kBlk, 1024);
-        auto scores = [&](int x, int j) {
+        auto scores = [&](int x, int buf) {
             if (!ok) return;
-            const uint64_t qa = dq + ((x * nb * kBlk) >> 4), ka = dk + (((j & 1) * nb * kBlk) >> 4);
+            const uint64_t qa = dq + ((x * nb * kBlk) >> 4), ka = dk + ((buf * nb * kBlk) >> 4);
             for (int b = 0; b < nn; b++)
 #pragma unroll
                 for (int k = 0; k < 4; k++) mma_ss(tmem + x * 128, qa + ((b * kBlk) >> 4) + 2 * k, ka + ((b * kBlk) >> 4) + 2 * k, id_s, b || k);
@@ -281,72 +386,124 @@ __global__ void __launch_bounds__(384, 1)
                 if (16 * k < a.rope) mma_ss(tmem + x * 128, qa + ((nn * kBlk) >> 4) + 2 * k, ka + ((nn * kBlk) >> 4) + 2 * k, id_s, true);
             tc_commit(&s.s_full[x]);
         };
+        int kt = 0, st[2] = {0, 0}, qs[2] = {0, 0};      // key tiles, score tiles and query tiles before this unit
         // the value tile's halves of 64 keys are freed one by one after their last use
         auto output = [&](int x, int j, bool last) {
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-                wait(&s.v_full[h], j & 1);
+                wait(&s.v_full[h], (kt + j) & 1);
                 if (!ok) return;
 #pragma unroll
                 for (int k = 4 * h; k < 4 * h + 4; k++) mma_ts(tmem + 256 + x * V, tmem + x * 128 + 8 * k, dv + ((k * 2048) >> 4), id_o, j || k);
                 if (last) tc_commit(&s.v_empty[h]);
             }
         };
-        if (n > 0) wait(&s.k_full[0], 0);
-        for (int x = 0; x < 2; x++)
-            if (nt[x] > 0) {
-                wait(&s.q_full[x], 0);
-                tc_after_sync();
-                scores(x, 0);
-            }
-        if (n > 0 && ok) tc_commit(&s.k_empty[0]);
-        for (int j = 0; j < n; j++) {
-            for (int x = 0; x < 2; x++) {
-                if (j >= nt[x]) continue;
-                wait(&s.p_full[x], j & 1);
-                tc_after_sync();
-                output(x, j, x == 1 || j >= nt[1]);
-                if (j + 1 < nt[x]) {
-                    wait(&s.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
-                    scores(x, j + 1);
-                } else if (ok) {
-                    tc_commit(&s.o_full[x]);
+        for (int r = 0;; r++) {
+            const Unit u = take(r);
+            if (u.n < 0) break;
+            if (u.n == 0) continue;
+            wait(&s.k_full[kt & 1], (kt >> 1) & 1);
+#pragma unroll
+            for (int x = 0; x < 2; x++)
+                if (u.nt[x] > 0) {
+                    wait(&s.q_full[x], qs[x]++ & 1);
+                    tc_after_sync();
+                    scores(x, kt & 1);
+                    if (ok && u.nt[x] == 1) tc_commit(&s.q_empty[x]);
                 }
+            if (ok) tc_commit(&s.k_empty[kt & 1]);
+            for (int j = 0; j < u.n; j++) {
+                const int next = kt + j + 1;
+#pragma unroll
+                for (int x = 0; x < 2; x++) {
+                    if (j >= u.nt[x]) continue;
+                    wait(&s.p_full[x], (st[x] + j) & 1);
+                    tc_after_sync();
+                    output(x, j, x == 1 || j >= u.nt[1]);
+                    if (j + 1 < u.nt[x]) {
+                        wait(&s.k_full[next & 1], (next >> 1) & 1);
+                        scores(x, next & 1);
+                        if (ok && j + 2 == u.nt[x]) tc_commit(&s.q_empty[x]);
+                    } else if (ok) {
+                        tc_commit(&s.o_full[x]);
+                    }
+                }
+                if (ok && j + 1 < u.n) tc_commit(&s.k_empty[next & 1]);
             }
-            if (ok && j + 1 < n) tc_commit(&s.k_empty[(j + 1) & 1]);
+            kt += u.n;
+            st[0] += u.nt[0];
+            st[1] += u.nt[1];
         }
-    } else {
-        // ---------------------------------------------------------- bulk copies: queries and keys, values
-        const int hk = head * (a.nope + V), hq = head * (a.nope + a.rope);
-        if (warp == 9) {
-            for (int j = 0; j < n; j++) {
-                const int buf = j & 1;
-                if (j > 1) wait(&s.k_empty[buf], ((j - 2) >> 1) & 1);
+    } else if (warp == 9) {
+        // ---------------------------------------------------------- units and bulk copies of keys
+        int most, kt = 0, i = blockIdx.x, asked = 0;
+        const int units = all_pairs(a, lane, blockIdx.x == 0, most) * a.H;
+        for (int r = 0;; r++) {
+            Unit u;
+            u.n = -1;
+            u.nt[0] = u.nt[1] = u.head = u.q0 = u.nq = u.nk = u.qrow = u.krow = 0;
+            if (i >= 0 && i < units) u = uniform(unit_of(a, i, most, lane));
+            if (i < 0 || u.n >= 0) {
+                if (r > 1) wait(&s.u_empty[r & 1], ((r >> 1) - 1) & 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    s.unit[r & 1] = u;
+                    mbar_arrive(&s.u_full[r & 1]);
+                }
+                if (i < 0) break;
+            } else {
+                r--;                     // more CTAs than units: nothing to do for this one
+            }
+            if (lane == 0) {
+                mbar_expect_tx(&s.next_full, 16);
+                ask_next(s);
+            }
+            __syncwarp();
+            const int hk = u.head * (a.nope + V);
+            for (int j = 0; j < u.n; j++) {
+                const int t = kt + j, buf = t & 1;
+                if (t > 1) wait(&s.k_empty[buf], ((t - 2) >> 1) & 1);
                 if (!ok) break;
                 const uint32_t dst = base + k_off + buf * nb * kBlk;
                 expect_bytes(&s.k_full[buf], nb * kBlk);
-                for (int b = 0; b < nn; b++) tma_box(dst + b * kBlk, &kv_map, hk + 64 * b, s.krow + j * kRows, &s.k_full[buf]);
-                tma_box(dst + nn * kBlk, &kr_map, 0, s.krow + j * kRows, &s.k_full[buf]);
+                for (int b = 0; b < nn; b++) tma_box(dst + b * kBlk, &kv_map, hk + 64 * b, u.krow + j * kRows, &s.k_full[buf]);
+                tma_box(dst + nn * kBlk, &kr_map, 0, u.krow + j * kRows, &s.k_full[buf]);
             }
-        } else {
-            const int h = warp - 10;         // also the query tile whose rows this warp copies
-            if (nt[h] > 0) {
-                expect_bytes(&s.q_full[h], nb * kBlk);
-                for (int b = 0; b < nb; b++) tma_box(base + (h * nb + b) * kBlk, &q_map, hq + 64 * b, s.qrow + q0 + h * kRows, &s.q_full[h]);
+            kt += max(u.n, 0);
+            wait(&s.next_full, asked++ & 1);
+            if (!ok) break;
+            i = read_next(s);
+            __syncwarp();                // all lanes have read before the next request
+        }
+    } else {
+        // ---------------------------------------------------------- bulk copies of a query tile and of half the values
+        const int h = warp - 10;
+        int kt = 0, qs = 0;
+        for (int r = 0;; r++) {
+            const Unit u = take(r);
+            if (u.n < 0) break;
+            const int hk = u.head * (a.nope + V), hq = u.head * (a.nope + a.rope);
+            if ((h ? u.nt[1] : u.nt[0]) > 0) {
+                if (qs > 0) wait(&s.q_empty[h], (qs - 1) & 1);
+                qs++;
+                if (ok) expect_bytes(&s.q_full[h], nb * kBlk);
+                for (int b = 0; b < nb && ok; b++) tma_box(base + (h * nb + b) * kBlk, &q_map, hq + 64 * b, u.qrow + u.q0 + h * kRows, &s.q_full[h]);
             }
-            for (int j = 0; j < n; j++) {
-                if (j > 0) wait(&s.v_empty[h], (j - 1) & 1);
+            for (int j = 0; j < u.n; j++) {
+                const int t = kt + j;
+                if (t > 0) wait(&s.v_empty[h], (t - 1) & 1);
                 if (!ok) break;
                 expect_bytes(&s.v_full[h], (V / 64) * kBlk / 2);
                 for (int b = 0; b < V / 64; b++)
-                    tma_box(base + v_off + b * kBlk + h * (kBlk / 2), &v_map, hk + a.nope + 64 * b, s.krow + j * kRows + 64 * h, &s.v_full[h]);
+                    tma_box(base + v_off + b * kBlk + h * (kBlk / 2), &v_map, hk + a.nope + 64 * b, u.krow + j * kRows + 64 * h, &s.v_full[h]);
             }
+            kt += u.n;
         }
-        // every copy has landed before the CTA may end (those not waited for by an MMA that was issued: after a timeout)
-        if (!ok || *abort) {
-            const uint64_t late = global_ns() + 200000000ull;
-            while (global_ns() < late) __nanosleep(1000);
-        }
+    }
+    // every copy has landed before the CTA may end (those not waited for by an MMA that was issued: after a timeout)
+    if (warp > 8 && (!ok || *abort)) {
+        const uint64_t late = global_ns() + 200000000ull;
+        while (global_ns() < late) __nanosleep(1000);
     }
     tc_before_sync();
     __syncthreads();
@@ -398,13 +555,15 @@ cudaError_t run(const MlaPrefillArgs &a, int device, cudaStream_t st) {
         if (cudaError_t e = matrix_map(a.kv, (long long)a.H * (a.nope + V), a.Tk, a.kv_stride, kRows / 2, &vm)) return e;
         if (cudaError_t e = matrix_map(a.k_rope, a.rope, a.Tk, a.kr_stride, kRows, &kr)) return e;
     }
-    const int nb = a.nope / 64 + 1, max_pairs = (a.Tq + 2 * kRows - 1) / (2 * kRows) + a.n_seq - 1;
+    const int nb = a.nope / 64 + 1;
+    // at most; every unit that is not empty has a row of its own
+    const long long units = std::min((long long)a.Tq, (long long)(a.Tq + 2 * kRows - 1) / (2 * kRows) + a.n_seq - 1) * a.H;
     const size_t smem = (size_t)(4 * nb + V / 64) * kBlk + 1024;
     auto kern = mla_prefill_kernel<V>;
     static std::atomic<uint64_t> done{0};
     if (cudaError_t e = allow_smem(kern, (size_t)(12 + V / 64) * kBlk + 1024, device, done)) return e;   // nope = 128
 
-    return launch_pdl(kern, dim3((unsigned)max_pairs * a.H), dim3(384), smem, st, q, kv, kr, vm, a, max_pairs, 2000000000LL);
+    return launch_pdl(kern, dim3((unsigned)units), dim3(384), smem, st, q, kv, kr, vm, a, 2000000000LL);
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
