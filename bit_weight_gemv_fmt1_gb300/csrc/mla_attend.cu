@@ -1,33 +1,38 @@
 // mla_attend.cu -- attention over the paged latent cache (absorbed form), on
-// the 5th-generation tensor cores.
+// the 5th-generation tensor cores: the kernel for bf16 caches, the join of partial
+// results, and the plan for both kinds of cache (E4M3: mla_attend_e4m3.cu).
 //
 // All heads of a token read the same cached rows, so the rows [t][L + R] of a
-// tile of 128 tokens are brought into shared memory once, as 16-bit values, and
-// serve both products of every head:
+// tile of 128 tokens are brought into shared memory once and serve both products of
+// every head:
 //   S^T[t][c] = sum_d row[t][d] q[c][d]      M = 128 tokens, N = columns, K = L + R
 //   O^T[d][c] += sum_t row[t][d] P^T[t][c]   M = 128 dims (L/128 times), N = columns, K = 128 tokens
 // The rows are the A operand of both: K-major (a token's dims along a row) for S,
 // MN-major (the same bytes read across) for O.  A column c is one query row
 // (query token j, head h); a CTA has N = 16, 32 or 64 of them.  Tokens are the
-// lanes of S^T in TMEM, so one thread holds one token's scores of all columns.
+// lanes of S^T in TMEM, so one thread holds one token's scores of half the columns.
 //
-// Softmax.  With x = log2(e) * scale * score, m_c a running reference and s_t
-// the row's scale (1 for bf16): e = 2^(x - m_c), l_c += e, P = 16-bit(e * s_t).
-// m_c starts 6 below the first tile's maximum of x + log2(s_t) and moves only
-// when some e * s_t passes 2^14 (f16 holds 65504): most tiles need no maximum
-// and no rescaling of O, and weights down to 2^-20 of the largest keep f16's full
-// precision.  l and O are f32; P is rounded to the cache's 16-bit type (E4M3 codes
-// are exact in f16, the row scale rides on P), q to the same type.
+// Softmax.  With x = log2(e) * scale * score and m_c a running reference:
+// e = 2^(x - m_c), l_c += e, P = bf16(e).  m_c starts 6 below the first tile's
+// maximum and moves only when some e passes 2^14: most tiles need no maximum over
+// the lanes and no rescaling of O, and bf16 has its full 8 bits at every e down to
+// 2^-126.  l, m and O are f32.  P and q are rounded to bf16, as the cached rows are,
+// because the tensor cores multiply equal types.
 //
-// Work.  The tiles of all sequences form one line that is cut into equal
+// Work.  The tiles of all sequences form one line that is cut into
 // contiguous pieces, one for each group of CTAs; the CTAs of a group take the
 // piece's row blocks side by side, so each row comes from HBM once.  Pieces that
 // hold part of a sequence leave (O, m, l) in f32 in scratch, and
 // mla_join_kernel adds them up; the rest is written directly.
 //
+// Bound, L + R = 576: the MMAs' reads of the rows from shared memory, 4 KB each whatever N is.  A tile of 64 columns
+// takes 68 MMAs of 45 cycles, 3060 (N = 128: 59 each, but O would fill TMEM and leave no room for S); one tile is in
+// shared memory at a time (147 KB), and each block of 64 dims is asked for again when its last product is done.
+// Measured: 48 x 12000 tokens, 128 heads: 134 us (1.2 PFLOP/s, 0.63 of measured bf16); 1 x 100000: 54 us with the join's 7;
+// 4 x 9000, 16 heads x 3 queries: 28 us, of which launch, first copies and the join are 17.
+//
 // Warps: 0-7 softmax and output (two threads per token, each half the columns), 8
-// MMA issue, the others tiled bulk copies.  The E4M3 cache has a kernel of its own
-// (mla_attend_e4m3.cu).
+// MMA issue, 9-11 tiled bulk copies.
 // Every wait is bounded; after one has run out all waits return at once, no
 // further MMA or copy is issued, and the kernel records DEV_ERR_TIMEOUT.
 #include <cudaTypedefs.h>
@@ -539,8 +544,8 @@ __global__ void __launch_bounds__(512) mla_join_kernel(const MlaAttendArgs a, co
     }
 }
 
-// Columns of a CTA: the fewest that hold the sequence's rows, as small products cost less shared-memory bandwidth
-// for nothing, up to what TMEM and shared memory allow; and half as many while the tiles that there can be leave half
+// Columns of a CTA: the fewest that hold the sequence's rows, up to what TMEM and shared memory allow (64, E4M3 with its
+// terms 32), as a tile costs nearly the same for any N; and half as many while the tiles that there can be leave half
 // the SMs without work (1 x 1000 tokens, 128 heads, E4M3: 32 CTAs of 32 columns 14.8 us, 64 of 16 columns 12.4 us).
 int columns_of(bool e4m3, int n_rows, long long tiles, int n_sm) {
     int n = n_rows <= 16 ? 16 : n_rows <= 32 || e4m3 ? 32 : 64;

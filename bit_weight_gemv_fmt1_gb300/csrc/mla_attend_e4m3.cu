@@ -19,7 +19,8 @@
 // and wrote them twice more and was bound by that: 10400 cycles for 64 rows).
 //
 // Tiles are 73 KB, so two fit: the scores of tile i + 1 are computed while the
-// softmax of tile i runs.  Warps: 0-7 softmax and output (two threads per
+// softmax of tile i runs.  Measured: 48 x 12000 tokens, 128 heads: 160 us (1.0 PFLOP/s of the formula's work; 2.1
+// with the terms'), 1 x 1000: 12.4 us, of which two thirds are launch, the first copies and the join.  Warps: 0-7 softmax and output (two threads per
 // token, each half the rows), 8 MMA issue, 9-13 bulk copies of codes and scales.
 #include "mla_attend.cuh"
 
