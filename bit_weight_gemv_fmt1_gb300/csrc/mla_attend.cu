@@ -25,11 +25,12 @@
 // hold part of a sequence leave (O, m, l) in f32 in scratch, and
 // mla_join_kernel adds them up; the rest is written directly.
 //
-// Bound, L + R = 576: the MMAs' reads of the rows from shared memory, 4 KB each whatever N is.  A tile of 64 columns
-// takes 68 MMAs of 45 cycles, 3060 (N = 128: 59 each, but O would fill TMEM and leave no room for S); one tile is in
-// shared memory at a time (147 KB), and each block of 64 dims is asked for again when its last product is done.
-// Measured: 48 x 12000 tokens, 128 heads: 134 us (1.2 PFLOP/s, 0.63 of measured bf16); 1 x 100000: 54 us with the join's 7;
-// 4 x 9000, 16 heads x 3 queries: 28 us, of which launch, first copies and the join are 17.
+// Bound, L + R = 576, 64 columns: a tile's MMAs read 4 KB of rows each whatever N is, 68 of 45 cycles, 3060 (N = 128: 59
+// each, but O would fill TMEM and leave no room for S).  One tile is in shared memory at a time (147 KB beside 74 KB of
+// queries), so scores, softmax and outputs follow one another and only the copies overlap, each block of 64 dims being
+// asked for again when its last product is done: 7700 cycles a tile.
+// Measured: 48 sequences of up to 12000 tokens (320000 in all), 128 heads: 134 us, 0.66 PFLOP/s, 2.8 TB/s of the cache; 1 x
+// 100000: 55 us with the join's 7; 4 x 9000, 16 heads x 3 queries: 29 us, of which launch, first copies and join are 17.
 //
 // Warps: 0-7 softmax and output (two threads per token, each half the columns), 8
 // MMA issue, 9-11 tiled bulk copies.

@@ -14,14 +14,20 @@
 // Terms are columns side by side, S^T [128 tokens][2 NH] and O^T [128 dims][3 NH]
 // for NH = 16 or 32 query rows, and are added in f32 when they leave TMEM.  An
 // MMA reads 4 KB of codes for 128 x 32 values whatever its N, so the terms cost
-// little: at NH = 32 a tile takes 18 MMAs of N = 64 and 16 of N = 96, about 1760
+// little: at NH = 32 a tile takes 18 MMAs of N = 64 (45 cycles) and 16 of N = 96 (52), 1640
 // cycles, and its bytes enter shared memory once (converting to f16 instead read
 // and wrote them twice more and was bound by that: 10400 cycles for 64 rows).
 //
-// Tiles are 73 KB, so two fit: the scores of tile i + 1 are computed while the
-// softmax of tile i runs.  Measured: 48 x 12000 tokens, 128 heads: 160 us (1.0 PFLOP/s of the formula's work; 2.1
-// with the terms'), 1 x 1000: 12.4 us, of which two thirds are launch, the first copies and the join.  Warps: 0-7 softmax and output (two threads per
-// token, each half the rows), 8 MMA issue, 9-13 bulk copies of codes and scales.
+// Bound: tiles are 73 KB, so two fit beside q and P: the scores of tile i + 1 are computed while the
+// softmax of tile i runs.  What a buffer goes through in turn is longer than two tiles' MMAs: scores 1150 cycles, softmax
+// 1250, the wait for the other tile's MMAs 1200, outputs 1100 to 1450, release to next copy's arrival 2000 (issue 600,
+// L2 700), 7300 in all, so a tile takes 3650 to 4400.  What shortened it: one barrier for all blocks of a
+// tile and one look at it and at P's (162 -> 157 us), bytes announced ahead of the release (-> 155).
+// Measured: 48 sequences of up to 12000 tokens (320000 in all), 128 heads: 155 us, 0.57 PFLOP/s of the formula's work;
+// 1 x 1000: 13 us, of which two thirds are launch, the first copies and the join.
+//
+// Warps: 0-7 softmax and output (two threads per token, each half the rows), 8 MMA issue, 9-13 bulk
+// copies of codes and scales.
 #include "mla_attend.cuh"
 
 namespace coli {
@@ -39,7 +45,7 @@ constexpr float kQ1 = 32.f;              // q's second term against the first
 constexpr float kP1 = 8.f, kP2 = 16.f;   // P's second term against the first, third against the second
 
 struct Shared8 {
-    uint64_t k_full[2][5], k_empty[2][5];   // blocks of 128 dims; last: rope part
+    uint64_t k_full[2], k_empty[2][5];      // all of a tile; its blocks of 128 dims, last the rope part
     uint64_t sc_full[4];                    // row scales
     uint64_t s_full[2], p_full[2];
     uint32_t tmem;
@@ -207,10 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < 4; i++) mbar_init(&s.sc_full[i], 1);
         for (int i = 0; i < 2; i++) {
-            for (int p = 0; p < 5; p++) {
-                mbar_init(&s.k_full[i][p], 1);
-                mbar_init(&s.k_empty[i][p], 1);
-            }
+            mbar_init(&s.k_full[i], np + 1);
+            for (int p = 0; p < 5; p++) mbar_init(&s.k_empty[i][p], 1);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_full[i], 8);
         }
@@ -258,8 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tok = w.tile() * kTile + t;
             // every row sees the whole tile: the first query's limit is the lowest
             const bool full = (w.tile() + 1) * kTile <= w.len - (a.n_q - 1) && (w.rb + 1) * NH <= g.n_rows;
-            wait(&s.sc_full[it & 3], (it >> 2) & 1);
-            wait(&s.s_full[buf], (it >> 1) & 1);
+            wait(lane & 1 ? &s.sc_full[it & 3] : &s.s_full[buf], (lane & 1 ? it >> 2 : it >> 1) & 1);   // both at once
             tc_after_sync();
             const float st = tok < w.len ? s.scale[it & 3][t] : 0.f;
             if ((w.tile() + 1) * kTile > w.len && tok >= w.len) {
@@ -431,18 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dq = sw128_desc(base + q_off, 16, 1024), dqr = sw64_desc(base + q_off + np * (2 * NH * 128));
         const uint64_t dv = sw128_desc(base, 16, 1024), dp = sw128_desc(base + p_off, 16, 1024);
         auto scores = [&](int it) {
-            const uint32_t buf = it & 1, so = (buf * stage) >> 4, d = tmem + buf * (2 * NH);
-            for (int p = 0; p < np; p++) {
-                wait(&s.k_full[buf][p], (it >> 1) & 1);
-                tc_after_sync();
-                if (!ok) return;
+            const uint32_t buf = __shfl_sync(0xffffffffu, it & 1, 0), so = (buf * stage) >> 4, d = tmem + buf * (2 * NH);
+            tc_after_sync();
+            for (int p = 0; p < np; p++)
 #pragma unroll
                 for (int k = 0; k < 4; k++)
                     mma8_ss(d, dk + so + ((p * kBlk8) >> 4) + 2 * k, dq + ((p * 2 * NH * 128) >> 4) + 2 * k, id_s, p || k);
-            }
-            wait(&s.k_full[buf][np], (it >> 1) & 1);
-            tc_after_sync();
-            if (!ok) return;
 #pragma unroll
             for (int k = 0; k < 2; k++)
                 if (32 * k < a.c.R) mma8_ss(d, dr + so + 2 * k, dqr + 2 * k, id_s, true);
@@ -450,44 +447,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit(&s.k_empty[buf][np]);
         };
         auto output = [&](int it, bool first) {
-            const uint32_t buf = it & 1, so = (buf * stage) >> 4, po = (buf * kP8) >> 4;
-            wait(&s.p_full[buf], (it >> 1) & 1);
+            const uint32_t buf = __shfl_sync(0xffffffffu, it & 1, 0), so = (buf * stage) >> 4, po = (buf * kP8) >> 4;
+            const uint32_t more = __shfl_sync(0xffffffffu, first ? 0u : 1u, 0);
             tc_after_sync();
-            if (!ok) return;
             for (int p = 0; p < np; p++) {
 #pragma unroll
                 for (int k = 0; k < 4; k++)
-                    mma8_ss(tmem + kO + 3 * NH * p, dv + so + ((p * kBlk8 + k * 4096) >> 4), dp + po + ((k * 4096) >> 4), id_o, k || !first);
+                    mma8_ss(tmem + kO + 3 * NH * p, dv + so + ((p * kBlk8 + k * 4096) >> 4), dp + po + ((k * 4096) >> 4), id_o, k || more);
                 tc_commit(&s.k_empty[buf][p]);
             }
         };
-        auto ready = [&](uint64_t *bar, int it) { return __all_sync(0xffffffffu, mbar_test(bar, (it >> 1) & 1)); };
-        auto tile_ready = [&](int it) {
-            for (int p = np; p >= 0; p--)
-                if (!ready(&s.k_full[it & 1][p], it)) return false;
-            return true;
-        };
-        // Scores of tile q and outputs of tile v, in whichever order their inputs come: scores first where the
-        // softmax would run dry (q = v + 1), outputs first otherwise, since they free the buffers.
+        // Scores of tile q and outputs of tile v, in whichever order their inputs come, scores first, as the softmax
+        // would run dry.  A look at a barrier takes some 250 cycles while the MMAs read shared memory at its full rate, so
+        // a tile has one for all of its blocks, and one instruction looks at both: odd lanes at tile q, even ones at P of v.
         int it = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next()) {
             const int n = w.rest();
             named_sync(3, kSoft + 32);
-            int q = 0, v = 0;
-            while (v < n) {
-                if (!ok) break;
-                if (q == v) {
+            int q = 0, v = 0, spins = 0;
+            while (v < n && ok) {
+                const int i = lane & 1 ? it + q : it + v;
+                const uint32_t ready = __ballot_sync(0xffffffffu, mbar_test(lane & 1 ? &s.k_full[i & 1] : &s.p_full[i & 1], (i >> 1) & 1));
+                if (q < n && q <= v + 1 && (ready & 2)) {
                     scores(it + q++);
-                } else if (q < n && q == v + 1 && tile_ready(it + q)) {
-                    scores(it + q++);
-                } else if (ready(&s.p_full[(it + v) & 1], it + v)) {
+                } else if (q > v && (ready & 1)) {
                     output(it + v, v == 0);
                     v++;
-                } else if (q == n || q == v + 2) {
-                    output(it + v, v == 0);                             // nothing else to do: waits
-                    v++;
-                } else if (*abort || global_ns() > deadline) {
-                    wait(&s.p_full[(it + v) & 1], ((it + v) >> 1) & 1); // records the expiry
+                } else if ((++spins & 63) == 0 && __any_sync(0xffffffffu, *abort || global_ns() > deadline)) {
+                    ok = false;
+                    *abort = 1;
+                    atomicCAS(a.err, 0, (int)DEV_ERR_TIMEOUT);
                 }
             }
             it += n;
@@ -508,18 +497,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t live = __ballot_sync(0xffffffffu, sl >= 0), n = __popc(live) * g.pbox;
             const int y0 = __shfl_sync(0xffffffffu, sl, 0);
             const uint32_t dst = base + buf * stage + p * kBlk8;
-            uint64_t *bar = &s.k_full[buf][p];
+            uint64_t *bar = &s.k_full[buf];
+            // the bytes are announced once the tile before in this buffer has landed, ahead of the buffer's release
+            if (it > 1) wait(bar, ((it - 2) >> 1) & 1);
+            if (ok) expect_bytes(bar, n * (who < 4 ? 128 : 64));
             if (it > 1) wait(&s.k_empty[buf][p], ((it - 2) >> 1) & 1);
             if (!ok) continue;
             if (who < 4) {
-                expect_bytes(bar, n * 128);
                 if (live & 1) tma_box(dst, &map, 128 * p, y0, bar);
                 for (int j = 1; j < nbox; j++) {
                     const int y = __shfl_sync(0xffffffffu, sl, j);
                     if (live >> j & 1) tma_box(dst + j * g.pbox * 128, &map, 128 * p, y, bar);
                 }
             } else {
-                expect_bytes(bar, n * 64);
                 expect_bytes(&s.sc_full[it & 3], n * 4);
                 for (int j = 0; j < nbox; j++) {
                     const int y = __shfl_sync(0xffffffffu, sl, j);
@@ -533,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t late = global_ns() + 200000000ull;
         volatile int none = 0;
         for (int k = it > 1 ? it - 2 : 0; k < it && mine; k++) {
-            warp_wait(&s.k_full[k & 1][p], (k >> 1) & 1, late, &none, lane);
+            warp_wait(&s.k_full[k & 1], (k >> 1) & 1, late, &none, lane);
             if (who == 4) warp_wait(&s.sc_full[k & 3], (k >> 2) & 1, late, &none, lane);
         }
     }
