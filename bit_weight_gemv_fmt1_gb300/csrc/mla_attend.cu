@@ -27,8 +27,8 @@
 //
 // Bound, L + R = 576, 64 columns: a tile's MMAs read 4 KB of rows each whatever N is, 68 of 45 cycles, 3060 (N = 128: 59
 // each, but O would fill TMEM and leave no room for S).  One tile is in shared memory at a time (147 KB beside 74 KB of
-// queries), so scores, softmax and outputs follow one another and only the copies overlap, each block of 64 dims being
-// asked for again when its last product is done: 7700 cycles a tile.
+// queries), so its scores (2000 cycles), softmax (1240) and outputs (1760) follow one another, 5500 cycles a tile with the
+// hand-overs; the copies are hidden, each block of 64 dims being asked for again when its last product is done.
 // Measured: 48 sequences of up to 12000 tokens (320000 in all), 128 heads: 134 us, 0.66 PFLOP/s, 2.8 TB/s of the cache; 1 x
 // 100000: 55 us with the join's 7; 4 x 9000, 16 heads x 3 queries: 29 us, of which launch, first copies and join are 17.
 //
@@ -474,9 +474,10 @@ __global__ void __launch_bounds__(512) mla_join_kernel(const MlaAttendArgs a, co
 #pragma unroll
         for (int d = 0; d < 4; d++) o[d] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (n > 1) {
-            // the first two parts are asked for before the maxima are known: one round trip for both
-            float4 v[2][4];
-            float mk[2];
+            // the first two parts are asked for before the maxima are known: one round trip for both (four: the same times)
+            constexpr int F = 2;
+            float4 v[F][4];
+            float mk[F];
             auto load = [&](int k, float4 (&x)[4], float &m) {
                 const float *src = g.part + part(k) * a.c.L + 4 * lane;
                 m = g.part_ml[part(k) * 2];
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(512) mla_join_kernel(const MlaAttendArgs a, co
                     if (d < nd) x[d] = __ldcs(reinterpret_cast<const float4 *>(src + 128 * d));
             };
 #pragma unroll
-            for (int i = 0; i < 2; i++)
+            for (int i = 0; i < F; i++)
                 if (sub + i * wpr < n) load(sub + i * wpr, v[i], mk[i]);
             float2 ml = make_float2(-INFINITY, 0.f);
             if (lane < n) ml = *reinterpret_cast<const float2 *>(g.part_ml + part(lane) * 2);
@@ -499,15 +500,15 @@ __global__ void __launch_bounds__(512) mla_join_kernel(const MlaAttendArgs a, co
                 z = fmaf(ml.y, ex2(ml.x - M), z);
             }
             z = warp_sum(z);
-            for (int k0 = sub; k0 < n; k0 += 2 * wpr) {
+            for (int k0 = sub; k0 < n; k0 += F * wpr) {
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
+                for (int i = 0; i < F; i++) {
                     const int k = k0 + i * wpr;
                     if (k >= n) break;
                     if (k0 != sub) load(k, v[i], mk[i]);
                 }
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
+                for (int i = 0; i < F; i++) {
                     if (k0 + i * wpr >= n) break;
                     const float f = ex2(mk[i] - M);
 #pragma unroll
