@@ -20,9 +20,12 @@
 // f32; rounding P to bf16 is within 2^-8 of each weight, as the values' own.
 //
 // Bound: the tensor cores, 1280 cycles for 128 x 128 scores (nope + rope = 192, v = 128), of which the
-// exponentials' unit takes up to 1024.  Shared memory holds Q (96 KB), two K tiles (96 KB) and one V
-// tile (32 KB), whose two halves of 64 keys are freed and asked for one by one: each comes back
-// before its next use 1024 cycles later (asked for whole, at the end of a round, V cost 1900 of 4500 cycles).
+// exponentials' unit takes up to 1024.  Shared memory holds Q (96 KB), a ring of 5 key blocks of 128 keys x 64 dims (80 KB) and a
+// ring of 3 value halves of 64 keys (48 KB), each freed and asked for by itself after its last use.  In a round of 2560
+// cycles the values lie idle for 770 and the keys for 500, less than a copy takes (1000 to 1500): what the rings hold
+// beyond a tile covers that.  Two whole key tiles and one value tile, of the same size: 474 / 96 / 233 us against
+// 452 / 96 / 231 (8 x 1000 x 16 heads: 40 against 41, the price of more barriers); all blocks of a key tile waited for at once: 471.
+// 8192 tokens x 32 heads: 1.5 PFLOP/s, 0.79 of the measured bf16 rate.
 //
 // Keys past a causal row's limit are masked by selection; value rows past the
 // sequence's end belong to its neighbours and are zeroed in shared memory.
@@ -58,7 +61,7 @@ struct Unit {
 };
 
 struct Shared {
-    uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], u_full[2], u_empty[2];
+    uint64_t q_full[2], q_empty[2], k_full[5], k_empty[5], v_full[3], v_empty[3], s_full[2], p_full[2], o_full[2], u_full[2], u_empty[2];
     uint64_t next_full;
     Unit unit[2];
     alignas(16) uint32_t next[4];        // the answer to the last request for a CTA's work
@@ -66,6 +69,18 @@ struct Shared {
     int abort;
 };
 
+
+// A place in a ring of n buffers and the parity of its use.
+struct Ring {
+    int slot, par;
+    __device__ __forceinline__ void step(int by, int n) {
+        slot += by;
+        if (slot >= n) {
+            slot -= n;
+            par ^= 1;
+        }
+    }
+};
 
 // Sequence b's offsets (all 0 where they are bad) and its number of pairs.
 __device__ __forceinline__ int pairs_of(const MlaPrefillArgs &a, int b, bool report, int4 &c) {
@@ -193,7 +208,9 @@ __global__ void __launch_bounds__(384, 1)
     uint8_t *sm = raw + (base - smem_addr(raw));
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int nn = a.nope / 64, nb = nn + 1;             // blocks of a query or key tile: no-position part, rotary part
-    const uint32_t k_off = 2 * nb * kBlk, v_off = k_off + 2 * nb * kBlk;
+    const int nk_ring = 2 * nb - 1;                      // key blocks of 64 dims
+    constexpr uint32_t kHalf = V / 64 * (kBlk / 2);      // 64 value rows
+    const uint32_t k_off = 2 * nb * kBlk, v_off = k_off + nk_ring * kBlk;
     pdl_wait();
     pdl_trigger();
     if (warp == 0) tmem_alloc(&s.tmem, 512);
@@ -201,15 +218,19 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < 2; i++) {
             mbar_init(&s.q_full[i], 1);
             mbar_init(&s.q_empty[i], 1);
-            mbar_init(&s.k_full[i], 1);
-            mbar_init(&s.k_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_full[i], 4);
             mbar_init(&s.o_full[i], 1);
-            mbar_init(&s.v_full[i], 1);
-            mbar_init(&s.v_empty[i], 1);
             mbar_init(&s.u_full[i], 1);
             mbar_init(&s.u_empty[i], 11);
+        }
+        for (int i = 0; i < 5; i++) {
+            mbar_init(&s.k_full[i], 1);
+            mbar_init(&s.k_empty[i], 1);
+        }
+        for (int i = 0; i < 3; i++) {
+            mbar_init(&s.v_full[i], 1);
+            mbar_init(&s.v_empty[i], 1);
         }
         mbar_init(&s.next_full, 1);
         s.abort = 0;
@@ -248,7 +269,7 @@ __global__ void __launch_bounds__(384, 1)
         // a negative scale turns the scores' sign; a zero one must still send masked scores (-inf) to -inf
         const bool negative = a.scale < 0.f;
         const float f = a.scale == 0.f ? 1e-37f : fabsf(a.scale) * 1.4426950408889634f;
-        int k_tiles = 0, s_tiles = 0, outs = 0;          // key tiles, this tile's score tiles and outputs so far
+        int k3 = 0, s_tiles = 0, outs = 0;               // key tiles so far mod 3, this tile's score tiles and outputs so far
         for (int r = 0;; r++) {
             const Unit u = take(r);
             if (u.n < 0) break;
@@ -258,7 +279,7 @@ __global__ void __launch_bounds__(384, 1)
             const long long orow = row < u.nq ? (long long)(u.qrow + row) * a.H + u.head : -1;
             float m = kNone;
             float l4[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int j = 0; j < nt; j++) {
+            for (int j = 0; j < nt; j++, k3 = k3 == 2 ? 0 : k3 + 1) {
                 wait(&s.s_full[x], s_tiles++ & 1);
                 tc_after_sync();
                 const int k0 = j * kRows;
@@ -319,13 +340,14 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 if (k0 + kRows > nk) {
                     // value rows of other sequences may hold anything, and 0 * NaN is NaN
-                    wait(&s.v_full[0], (k_tiles + j) & 1);
-                    wait(&s.v_full[1], (k_tiles + j) & 1);
+                    const int half = 2 * k3 + (t >> 6), slot = half < 3 ? half : half - 3;
+                    wait(&s.v_full[slot], half >= 3);
                     if (k0 + t >= nk)
 #pragma unroll
                         for (int k = 0; k < V / 64; k++)
 #pragma unroll
-                            for (int c = 0; c < 8; c++) *reinterpret_cast<uint4 *>(sm + v_off + k * kBlk + t * 128 + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+                            for (int c = 0; c < 8; c++)
+                                *reinterpret_cast<uint4 *>(sm + v_off + slot * kHalf + k * (kBlk / 2) + (t & 63) * 128 + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
                     fence_async_smem();
                 }
                 tmem_st_wait();
@@ -333,7 +355,7 @@ __global__ void __launch_bounds__(384, 1)
                 __syncwarp();
                 if (lane == 0 && ok) mbar_arrive(&s.p_full[x]);
             }
-            k_tiles += u.n;
+            k3 = (k3 + u.n - nt) % 3;
             const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
             const float inv = l != 0.f ? 1.f / l : 0.f;
             if (nt > 0) {
@@ -374,69 +396,89 @@ __global__ void __launch_bounds__(384, 1)
     } else if (warp == 8) {
         // ---------------------------------------------------------- MMA issue
         constexpr uint32_t id_s = f16_idesc(1, false, false, kRows, kRows), id_o = f16_idesc(1, false, true, kRows, V);
-        const uint64_t dq = sw128_desc(base, 16, 1024), dk = sw128_desc(base + k_off, 16, 1024), dv = sw128_desc(base + v_off, kBlk, 1024);
-        auto scores = [&](int x, int buf) {
-            if (!ok) return;
-            const uint64_t qa = dq + ((x * nb * kBlk) >> 4), ka = dk + ((buf * nb * kBlk) >> 4);
-            for (int b = 0; b < nn; b++)
+        const uint64_t dq = sw128_desc(base, 16, 1024), dk = sw128_desc(base + k_off, 16, 1024), dv = sw128_desc(base + v_off, kBlk / 2, 1024);
+        // scores of query tile x with the keys at c; fresh: nobody has waited for them yet, last: nobody uses them after
+        auto scores = [&](int x, Ring c, bool fresh, bool last) {
+            const uint64_t qa = dq + ((x * nb * kBlk) >> 4);
+            for (int b = 0; b < nn; b++) {
+                if (fresh) {
+                    wait(&s.k_full[c.slot], c.par);
+                    tc_after_sync();
+                }
+                if (!ok) return;
+                const uint64_t ka = dk + ((c.slot * kBlk) >> 4);
 #pragma unroll
-                for (int k = 0; k < 4; k++) mma_ss(tmem + x * 128, qa + ((b * kBlk) >> 4) + 2 * k, ka + ((b * kBlk) >> 4) + 2 * k, id_s, b || k);
+                for (int k = 0; k < 4; k++) mma_ss(tmem + x * 128, qa + ((b * kBlk) >> 4) + 2 * k, ka + 2 * k, id_s, b || k);
+                if (last) tc_commit(&s.k_empty[c.slot]);
+                c.step(1, nk_ring);
+            }
+            if (fresh) {
+                wait(&s.k_full[c.slot], c.par);
+                tc_after_sync();
+            }
+            if (!ok) return;
+            const uint64_t ka = dk + ((c.slot * kBlk) >> 4);
 #pragma unroll
             for (int k = 0; k < 4; k++)
-                if (16 * k < a.rope) mma_ss(tmem + x * 128, qa + ((nn * kBlk) >> 4) + 2 * k, ka + ((nn * kBlk) >> 4) + 2 * k, id_s, true);
+                if (16 * k < a.rope) mma_ss(tmem + x * 128, qa + ((nn * kBlk) >> 4) + 2 * k, ka + 2 * k, id_s, true);
+            if (last) tc_commit(&s.k_empty[c.slot]);
             tc_commit(&s.s_full[x]);
         };
-        int kt = 0, st[2] = {0, 0}, qs[2] = {0, 0};      // key tiles, score tiles and query tiles before this unit
-        // the value tile's halves of 64 keys are freed one by one after their last use
-        auto output = [&](int x, int j, bool last) {
+        // the products of query tile x with the values at c, in halves of 64 keys
+        auto output = [&](int x, bool more, Ring c, bool fresh, bool last) {
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-                wait(&s.v_full[h], (kt + j) & 1);
+                if (fresh) {
+                    wait(&s.v_full[c.slot], c.par);
+                    tc_after_sync();
+                }
                 if (!ok) return;
+                const uint64_t va = dv + ((c.slot * kHalf) >> 4);
 #pragma unroll
-                for (int k = 4 * h; k < 4 * h + 4; k++) mma_ts(tmem + 256 + x * V, tmem + x * 128 + 8 * k, dv + ((k * 2048) >> 4), id_o, j || k);
-                if (last) tc_commit(&s.v_empty[h]);
+                for (int k = 0; k < 4; k++) mma_ts(tmem + 256 + x * V, tmem + x * 128 + 8 * (4 * h + k), va + ((k * 2048) >> 4), id_o, more || h || k);
+                if (last) tc_commit(&s.v_empty[c.slot]);
+                c.step(1, 3);
             }
         };
+        Ring kr{0, 0}, vr{0, 0};                         // this unit's next keys and values
+        int st[2] = {0, 0}, qs[2] = {0, 0};              // score tiles and query tiles before this unit
         for (int r = 0;; r++) {
             const Unit u = take(r);
             if (u.n < 0) break;
             if (u.n == 0) continue;
-            wait(&s.k_full[kt & 1], (kt >> 1) & 1);
 #pragma unroll
             for (int x = 0; x < 2; x++)
                 if (u.nt[x] > 0) {
                     wait(&s.q_full[x], qs[x]++ & 1);
                     tc_after_sync();
-                    scores(x, kt & 1);
+                    scores(x, kr, x == 0 || u.nt[0] == 0, x == 1 || u.nt[1] == 0);
                     if (ok && u.nt[x] == 1) tc_commit(&s.q_empty[x]);
                 }
-            if (ok) tc_commit(&s.k_empty[kt & 1]);
+            kr.step(nb, nk_ring);
             for (int j = 0; j < u.n; j++) {
-                const int next = kt + j + 1;
 #pragma unroll
                 for (int x = 0; x < 2; x++) {
                     if (j >= u.nt[x]) continue;
                     wait(&s.p_full[x], (st[x] + j) & 1);
                     tc_after_sync();
-                    output(x, j, x == 1 || j >= u.nt[1]);
+                    output(x, j > 0, vr, x == 0 || j >= u.nt[0], x == 1 || j >= u.nt[1]);
                     if (j + 1 < u.nt[x]) {
-                        wait(&s.k_full[next & 1], (next >> 1) & 1);
-                        scores(x, next & 1);
+                        scores(x, kr, x == 0 || j + 1 >= u.nt[0], x == 1 || j + 1 >= u.nt[1]);
                         if (ok && j + 2 == u.nt[x]) tc_commit(&s.q_empty[x]);
                     } else if (ok) {
                         tc_commit(&s.o_full[x]);
                     }
                 }
-                if (ok && j + 1 < u.n) tc_commit(&s.k_empty[next & 1]);
+                vr.step(2, 3);
+                if (j + 1 < u.n) kr.step(nb, nk_ring);
             }
-            kt += u.n;
             st[0] += u.nt[0];
             st[1] += u.nt[1];
         }
     } else if (warp == 9) {
         // ---------------------------------------------------------- units and bulk copies of keys
-        int most, kt = 0, i = blockIdx.x, asked = 0;
+        int most, blocks = 0, i = blockIdx.x, asked = 0;
+        Ring c{0, 0};
         const int units = all_pairs(a, lane, blockIdx.x == 0, most) * a.H;
         for (int r = 0;; r++) {
             Unit u;
@@ -460,16 +502,14 @@ __global__ void __launch_bounds__(384, 1)
             }
             __syncwarp();
             const int hk = u.head * (a.nope + V);
-            for (int j = 0; j < u.n; j++) {
-                const int t = kt + j, buf = t & 1;
-                if (t > 1) wait(&s.k_empty[buf], ((t - 2) >> 1) & 1);
-                if (!ok) break;
-                const uint32_t dst = base + k_off + buf * nb * kBlk;
-                expect_bytes(&s.k_full[buf], nb * kBlk);
-                for (int b = 0; b < nn; b++) tma_box(dst + b * kBlk, &kv_map, hk + 64 * b, u.krow + j * kRows, &s.k_full[buf]);
-                tma_box(dst + nn * kBlk, &kr_map, 0, u.krow + j * kRows, &s.k_full[buf]);
-            }
-            kt += max(u.n, 0);
+            for (int j = 0; j < u.n; j++)
+                for (int b = 0; b < nb; b++) {
+                    if (blocks++ >= nk_ring) wait(&s.k_empty[c.slot], c.par ^ 1);
+                    if (!ok) break;
+                    expect_bytes(&s.k_full[c.slot], kBlk);
+                    tma_box(base + k_off + c.slot * kBlk, b < nn ? &kv_map : &kr_map, b < nn ? hk + 64 * b : 0, u.krow + j * kRows, &s.k_full[c.slot]);
+                    c.step(1, nk_ring);
+                }
             wait(&s.next_full, asked++ & 1);
             if (!ok) break;
             i = read_next(s);
@@ -478,7 +518,8 @@ __global__ void __launch_bounds__(384, 1)
     } else {
         // ---------------------------------------------------------- bulk copies of a query tile and of half the values
         const int h = warp - 10;
-        int kt = 0, qs = 0;
+        int tiles = 0, qs = 0;
+        Ring c{h, 0};
         for (int r = 0;; r++) {
             const Unit u = take(r);
             if (u.n < 0) break;
@@ -490,14 +531,13 @@ __global__ void __launch_bounds__(384, 1)
                 for (int b = 0; b < nb && ok; b++) tma_box(base + (h * nb + b) * kBlk, &q_map, hq + 64 * b, u.qrow + u.q0 + h * kRows, &s.q_full[h]);
             }
             for (int j = 0; j < u.n; j++) {
-                const int t = kt + j;
-                if (t > 0) wait(&s.v_empty[h], (t - 1) & 1);
+                if (2 * tiles++ + h >= 3) wait(&s.v_empty[c.slot], c.par ^ 1);
                 if (!ok) break;
-                expect_bytes(&s.v_full[h], (V / 64) * kBlk / 2);
+                expect_bytes(&s.v_full[c.slot], kHalf);
                 for (int b = 0; b < V / 64; b++)
-                    tma_box(base + v_off + b * kBlk + h * (kBlk / 2), &v_map, hk + a.nope + 64 * b, u.krow + j * kRows + 64 * h, &s.v_full[h]);
+                    tma_box(base + v_off + c.slot * kHalf + b * (kBlk / 2), &v_map, hk + a.nope + 64 * b, u.krow + j * kRows + 64 * h, &s.v_full[c.slot]);
+                c.step(2, 3);
             }
-            kt += u.n;
         }
     }
     // every copy has landed before the CTA may end (those not waited for by an MMA that was issued: after a timeout)
@@ -558,10 +598,11 @@ cudaError_t run(const MlaPrefillArgs &a, int device, cudaStream_t st) {
     const int nb = a.nope / 64 + 1;
     // at most; every unit that is not empty has a row of its own
     const long long units = std::min((long long)a.Tq, (long long)(a.Tq + 2 * kRows - 1) / (2 * kRows) + a.n_seq - 1) * a.H;
-    const size_t smem = (size_t)(4 * nb + V / 64) * kBlk + 1024;
+    auto bytes = [](int nb) { return (size_t)(4 * nb - 1) * kBlk + 3 * (V / 64) * (kBlk / 2) + 1024; };
+    const size_t smem = bytes(nb);
     auto kern = mla_prefill_kernel<V>;
     static std::atomic<uint64_t> done{0};
-    if (cudaError_t e = allow_smem(kern, (size_t)(12 + V / 64) * kBlk + 1024, device, done)) return e;   // nope = 128
+    if (cudaError_t e = allow_smem(kern, bytes(3), device, done)) return e;   // nope = 128
 
     return launch_pdl(kern, dim3((unsigned)units), dim3(384), smem, st, q, kv, kr, vm, a, 2000000000LL);
 }
