@@ -12,6 +12,7 @@ at most d = r * scale * max_t sum_i |q_i| |k_ti| and with them every p_t by at
 most a factor exp(2 d), f32 sums, exp and the f32 score add 1e-4 at most for
 the lengths used here, and a bf16 output rounds once more."""
 import math
+import random
 
 import numpy as np
 import pytest
@@ -503,6 +504,18 @@ def test_prefill_score_ranges(q_scale):
 def test_prefill_long():
     torch, coli = setup()
     prefill_case(torch, coli, [2500, 1100], [2500, 1500], 2, 128, 64, 128, 33)
+
+
+@pytest.mark.parametrize("N,R,V", [(128, 64, 128), (64, 32, 64), (128, 64, 64)])
+def test_prefill_many_units(N, R, V):
+    """Several units of work per SM, of every mix of sizes, from more sequences than a warp has lanes; equal calls give equal bits."""
+    torch, coli = setup()
+    r = random.Random(7)
+    n_qs = [r.choice((0, 1, 100, 128, 129, 256, 257, 300, 513)) for _ in range(70)]
+    n_ks = [max(0, n + r.choice((-200, -1, 0, 0, 1, 127, 128, 300))) for n in n_qs]
+    one = prefill_case(torch, coli, n_qs, n_ks, 8, N, R, V, 34)
+    two = prefill_case(torch, coli, n_qs, n_ks, 8, N, R, V, 34)
+    assert torch.equal(one, two)
 
 
 def test_prefill_isolates_sequences():
