@@ -19,13 +19,16 @@
 // maximum passes it by 8: weights up to 2^8 lose nothing in bf16.  m, l and O are
 // f32; rounding P to bf16 is within 2^-8 of each weight, as the values' own.
 //
-// Bound: the tensor cores, 1280 cycles for 128 x 128 scores (nope + rope = 192, v = 128), of which the
-// exponentials' unit takes up to 1024.  Shared memory holds Q (96 KB), a ring of 5 key blocks of 128 keys x 64 dims (80 KB) and a
-// ring of 3 value halves of 64 keys (48 KB), each freed and asked for by itself after its last use.  In a round of 2560
-// cycles the values lie idle for 770 and the keys for 500, less than a copy takes (1000 to 1500): what the rings hold
+// Bound: shared memory, close to the tensor cores.  A round (128 keys, nope + rope = 192, v = 128) is 24 score MMAs that read 8 KB,
+// 16 output MMAs that read 4 KB and 82 KB of copies coming in, 342 KB or 2670 cycles at 128 bytes each; the tensor cores
+// alone need 2340.  Measured: 3300, in which the MMA warp issues without a pause (scores 86 cycles each, 59 alone) and
+// either softmax (1300) has 2000 to spare.  Q from TMEM would spare a third of the reads, but S and O fill TMEM.
+// Shared memory holds Q (96 KB), a ring of 5 key blocks of 128 keys x 64 dims (80 KB) and a
+// ring of 3 value halves of 64 keys (48 KB), each freed and asked for by itself after its last use.  In a round
+// the values lie idle for 770 cycles and the keys for 500, less than a copy takes (1000 to 1500): what the rings hold
 // beyond a tile covers that.  Two whole key tiles and one value tile, of the same size: 474 / 96 / 233 us against
 // 452 / 96 / 231 (8 x 1000 x 16 heads: 40 against 41, the price of more barriers); all blocks of a key tile waited for at once: 471.
-// 8192 tokens x 32 heads: 1.5 PFLOP/s, 0.79 of the measured bf16 rate.
+// 8192 tokens x 32 heads: 1.5 PFLOP/s, 0.79 of the measured bf16 rate (0.75 with L2 flushed between calls).
 //
 // Keys past a causal row's limit are masked by selection; value rows past the
 // sequence's end belong to its neighbours and are zeroed in shared memory.
