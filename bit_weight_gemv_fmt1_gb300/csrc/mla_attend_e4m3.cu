@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tok = w.tile() * kTile + t;
             // every row sees the whole tile: the first query's limit is the lowest
             const bool full = (w.tile() + 1) * kTile <= w.len - (a.n_q - 1) && (w.rb + 1) * NH <= g.n_rows;
-            wait(lane & 1 ? &s.sc_full[it & 3] : &s.s_full[buf], (lane & 1 ? it >> 2 : it >> 1) & 1);   // both at once
+            wait(&s.sc_full[it & 3], (it >> 2) & 1);
+            wait(&s.s_full[buf], (it >> 1) & 1);
             tc_after_sync();
             const float st = tok < w.len ? s.scale[it & 3][t] : 0.f;
             if ((w.tile() + 1) * kTile > w.len && tok >= w.len) {
@@ -468,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (v < n && ok) {
                 const int i = lane & 1 ? it + q : it + v;
                 const uint32_t ready = __ballot_sync(0xffffffffu, mbar_test(lane & 1 ? &s.k_full[i & 1] : &s.p_full[i & 1], (i >> 1) & 1));
+                __syncwarp();                                          // passes on what the other lanes have seen
                 if (q < n && q <= v + 1 && (ready & 2)) {
                     scores(it + q++);
                 } else if (q > v && (ready & 1)) {
