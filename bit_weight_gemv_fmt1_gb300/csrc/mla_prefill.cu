@@ -116,33 +116,51 @@ __device__ __forceinline__ int all_pairs(const MlaPrefillArgs &a, int lane, bool
     most = __reduce_max_sync(0xffffffffu, most);
     return __reduce_add_sync(0xffffffffu, total);
 }
+// How far a CTA has come in the order of units: the pairs that see v tiles have the numbers below..upto - 1, and those
+// of sequences before b0 end at run.  A CTA's units rise, so most of them are found from here in one look at 32
+// sequences (512 sequences of up to 200 rows x 16 heads: 333 us, with a search from the start each time 853; 8192 x 32 heads,
+// which needs none of it, 459 against 452, or 472 with the count unrolled at five places: it is one loop for its size).
+struct Place {
+    int v, below, upto, b0, run;
+};
 // Whole warp: unit i, in the order of key tiles, most first, all heads of a pair together.
-__device__ __forceinline__ Unit unit_of(const MlaPrefillArgs &a, int i, int most, int lane) {
+__device__ __forceinline__ Unit unit_of(const MlaPrefillArgs &a, int i, int pairs, Place &at, int lane) {
     Unit u;
     const int p = i / a.H;
     u.head = i - p * a.H;
-    int4 first;
-    const int n0 = pairs_of(a, lane, false, first);
-    auto count = [&](int v) {
-        int t = pairs_with(n0, first, v);
-        for (int b = lane + 32; b < a.n_seq; b += 32) {
-            int4 c;
-            const int n = pairs_of(a, b, false, c);
-            t += pairs_with(n, c, v);
+    if (p >= at.upto) {
+        // count(lo) > p >= count(hi), the pairs that see so many tiles or more; first the next number of tiles, then halves
+        int lo = 0, hi = at.v, above = pairs, below = at.upto, v = hi - 1;
+        while (hi - lo > 1) {
+            int t = 0;
+#pragma unroll 2
+            for (int b = lane; b < a.n_seq; b += 32) {
+                int4 c;
+                const int n = pairs_of(a, b, false, c);
+                t += pairs_with(n, c, v);
+            }
+            t = __reduce_add_sync(0xffffffffu, t);
+            if (t > p) {
+                lo = v;
+                above = t;
+            } else {
+                hi = v;
+                below = t;
+            }
+            v = (lo + hi) / 2;
         }
-        return __reduce_add_sync(0xffffffffu, t);
-    };
-    int v = 0, hi = most + 1;                 // count(v) > p >= count(hi)
-    while (hi - v > 1) {
-        const int mid = (v + hi) / 2;
-        if (count(mid) > p) v = mid;
-        else hi = mid;
+        at.v = lo;
+        at.below = below;
+        at.upto = above;
+        at.b0 = 0;
+        at.run = below;
     }
-    int run = count(v + 1);                   // then the pairs that see v tiles, sequence by sequence
+    const int v = at.v;
+    int run = at.run;
     u.q0 = u.nq = u.nk = u.qrow = u.krow = 0;
-    for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
-        int4 c = first;
-        const int n = b0 ? pairs_of(a, b0 + lane, false, c) : n0;
+    for (int b0 = at.b0; b0 < a.n_seq; b0 += 32) {
+        int4 c;
+        const int n = pairs_of(a, b0 + lane, false, c);
         const int above = pairs_with(n, c, v + 1), here = pairs_with(n, c, v) - above;
         int incl = here;
 #pragma unroll
@@ -153,6 +171,8 @@ __device__ __forceinline__ Unit unit_of(const MlaPrefillArgs &a, int i, int most
         const int before = run + incl - here;
         const uint32_t hit = __ballot_sync(0xffffffffu, before <= p && p < before + here);
         if (hit) {
+            at.b0 = b0;
+            at.run = run;
             const int src = __ffs(hit) - 1;
             u.q0 = __shfl_sync(0xffffffffu, (n - 1 - above - (p - before)) * 2 * kRows, src);
             u.qrow = __shfl_sync(0xffffffffu, c.x, src);
@@ -482,12 +502,13 @@ __global__ void __launch_bounds__(384, 1)
         // ---------------------------------------------------------- units and bulk copies of keys
         int most, blocks = 0, i = blockIdx.x, asked = 0;
         Ring c{0, 0};
-        const int units = all_pairs(a, lane, blockIdx.x == 0, most) * a.H;
+        const int pairs = all_pairs(a, lane, blockIdx.x == 0, most), units = pairs * a.H;
+        Place at{most + 1, 0, 0, 0, 0};
         for (int r = 0;; r++) {
             Unit u;
             u.n = -1;
             u.nt[0] = u.nt[1] = u.head = u.q0 = u.nq = u.nk = u.qrow = u.krow = 0;
-            if (i >= 0 && i < units) u = uniform(unit_of(a, i, most, lane));
+            if (i >= 0 && i < units) u = uniform(unit_of(a, i, pairs, at, lane));
             if (i < 0 || u.n >= 0) {
                 if (r > 1) wait(&s.u_empty[r & 1], ((r >> 1) - 1) & 1);
                 if (!ok) break;
