@@ -16,8 +16,9 @@
 // e = 2^(x - m_c), l_c += e, P = bf16(e).  m_c starts 6 below the first tile's
 // maximum and moves only when some e passes 2^14: most tiles need no maximum over
 // the lanes and no rescaling of O, and bf16 has its full 8 bits at every e down to
-// 2^-126.  l, m and O are f32.  P and q are rounded to bf16, as the cached rows are,
-// because the tensor cores multiply equal types.
+// 2^-126.  A NaN score makes e, and with it l and O, NaN; a score of +infinity does
+// so by x - m.  l, m and O are f32.  P and q are rounded to bf16, as the cached rows
+// are, because the tensor cores multiply equal types.
 //
 // Work.  The tiles of all sequences form one line that is cut into
 // contiguous pieces, one for each group of CTAs; the CTAs of a group take the
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
 #pragma unroll
                 for (int c = 0; c < CH / 2; c++) {
                     top = fmaxf(top, fmaxf(x[c].x, x[c].y));
-                    x[c] = make_float2(ex2(fminf(x[c].x, 100.f)), ex2(fminf(x[c].y, 100.f)));
+                    x[c] = make_float2(ex2(min_nan(x[c].x, 100.f)), ex2(min_nan(x[c].y, 100.f)));
                 }
             };
             auto add = [&](float sign) {       // l += sign * weights, and P for sign > 0; true if a weight has outgrown P

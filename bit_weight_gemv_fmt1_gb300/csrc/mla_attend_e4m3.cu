@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (tok >= s.limit[col0 + c + 1]) x.y = -INFINITY;
                     }
                     top = fmaxf(top, fmaxf(x.x, x.y));
-                    x = make_float2(ex2(fminf(x.x, 100.f)), ex2(fminf(x.y, 100.f)));
+                    x = make_float2(ex2(min_nan(x.x, 100.f)), ex2(min_nan(x.y, 100.f)));
                     l[c / 2] = fadd2(l[c / 2], sign > 0.f ? x : make_float2(-x.x, -x.y));
                     if (sign > 0.f) {
                         float2 p = fmul2(x, make_float2(st, st));

@@ -143,6 +143,12 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The smaller one, or NaN if either is (fminf would drop it).
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float c;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+    return c;
+}
 // Named barrier of n threads that ORs a predicate over them.
 __device__ __forceinline__ bool named_or(int id, int n, bool p) {
     uint32_t r;

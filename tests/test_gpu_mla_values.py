@@ -1,0 +1,116 @@
+"""Latent attention on the GPU where values are special: NaN and infinities in operands that count and in places that a
+query does not see, rows of scale 0, queries of widely spread magnitudes, more query rows than a launch has columns.
+
+Tolerances.  out = sum_t p_t c_t: rounding p to 16 bits moves it by r * sum_t p_t |c_t| (r = 2^-8 for a bf16 cache; 2^-11
+for the E4M3 one's three terms), scores off by d by expm1(2 d) of the same, f32 sums and exp by 1e-4 of it for these
+lengths, a bf16 output by 2^-8 of itself.  d = scale * max_t sum_i e_i |k_ti| + 2^-21 of the same sum with |q_i|, where e_i is
+what the operand of element q_i is off by.  bf16 cache: 0 for bf16 queries, 2^-8 |q_i| for f32 ones.  E4M3 cache: the row
+is scaled so that its largest element M lies in [2^7, 2^8); the first E4M3 term leaves 2^-4 of an element or 2^-10, the
+second 2^-4 of that or 2^-10 / 32: 2^-8 |q_i|, and no less than 2^-15, at most 2^-22 M unscaled; for f32 queries the
+f16 in between adds 2^-11 |q_i|; a bf16 element has 8 bits, which the two terms hold, so 2^-22 M alone is left."""
+import math
+
+import pytest
+
+from test_gpu_mla import U16, UF16, filled, gen, new_cache, rotation, sequence, setup, values
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(torch, coli, c, table, lens, ql, qr, scale, out_bf16=False, stream=None):
+    out = torch.full(ql.shape, 7.0, device="cuda", dtype=torch.bfloat16 if out_bf16 else torch.float32)
+    ls = torch.full(ql.shape[:3], 7.0, device="cuda")
+    coli.mla_attend(c, ql.cuda(), qr.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), scale, out, ls)
+    coli.sync_check()
+    return out.cpu(), ls.cpu()
+
+
+def check(torch, c, table, lens, ql, qr, scale, out, ls, skip=lambda b, j: None):
+    """Every row against the definition in 64 bits, but for the heads that skip(b, j) names."""
+    B, n_q, H, L = ql.shape
+    e4m3 = c.scales is not None
+    r = UF16 if e4m3 else U16
+    vals = values(torch, c)
+    for b in range(B):
+        rows = sequence(torch, vals, table, b, lens[b], c.page_size)
+        for j in range(n_q):
+            n = lens[b] - (n_q - 1 - j)
+            heads = torch.tensor([h for h in range(H) if h not in (skip(b, j) or ())], dtype=torch.long)
+            if not len(heads):
+                continue
+            o, l = out[b, j, heads].double(), ls[b, j, heads].double()
+            if n <= 0:
+                assert (o == 0).all() and (l == -math.inf).all()
+                continue
+            q, k = torch.cat([ql[b, j, heads], qr[b, j, heads]], -1).double(), rows[:n]
+            s = q @ k.T * scale
+            p = torch.softmax(s, -1)
+            ref, size = p @ k[:, :L], p @ k[:, :L].abs()
+            e = torch.zeros_like(q)
+            if ql.dtype == torch.float32:
+                e += U16 * q.abs() + (UF16 * q.abs() if e4m3 else 0.0)
+            if e4m3:
+                e += 2.0 ** -22 * q.abs().amax(-1, keepdim=True)
+            d = abs(scale) * ((e + 2.0 ** -21 * q.abs()) @ k.abs().T).amax(-1, keepdim=True)
+            tol = (r + torch.expm1(2 * d) + 1e-4) * size + (U16 if out.dtype == torch.bfloat16 else 0.0) * ref.abs() + 1e-30
+            assert ((o - ref).abs() <= tol).all(), (b, j, float(((o - ref).abs() / tol).max()))
+            want = torch.logsumexp(s, -1)
+            assert ((l - want).abs() <= 1e-4 + d[:, 0] + 2e-6 * want.abs()).all(), (b, j, float((l - want).abs().max()))
+
+
+def queries(torch, g, B, n_q, H, L, R, bf16, scale=1.0):
+    t = torch.bfloat16 if bf16 else torch.float32
+    return (torch.randn(B, n_q, H, L, generator=g) * scale).to(t), (torch.randn(B, n_q, H, R, generator=g) * scale).to(t)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_nan_query(e4m3, bf16):
+    """A NaN in a head's query makes that head's output and lse NaN, and nothing else."""
+    torch, coli = setup()
+    g = gen(torch, 1)
+    lens, L, R = [300, 40, 1], 256, 32
+    c, table = filled(torch, coli, e4m3, L, R, 16, lens, g)
+    ql, qr = queries(torch, g, 3, 1, 40, L, R, bf16)
+    ql[0, 0, 3, 7] = qr[1, 0, 5, 2] = ql[2, 0, 39, 255] = float("nan")
+    bad = {0: [3], 1: [5], 2: [39]}
+    out, ls = attend(torch, coli, c, table, lens, ql, qr, 0.06)
+    for b, (h,) in bad.items():
+        assert torch.isnan(out[b, 0, h]).all() and torch.isnan(ls[b, 0, h])
+    check(torch, c, table, lens, ql, qr, 0.06, out, ls, lambda b, j: bad[b])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("token", [0, 200, 1000, 2999])
+@pytest.mark.parametrize("where", [3, 255, 270])
+def test_nan_row(e4m3, token, where):
+    """A NaN in a cached row that counts, in its latent or its rotary part, makes its sequence's outputs NaN, and no other's."""
+    torch, coli = setup()
+    g = gen(torch, 2)
+    lens, L, R, page, H = [3000, 90], 256, 32, 16, 1024      # many heads: few CTAs share the tokens, several tiles each
+    c, table = filled(torch, coli, e4m3, L, R, page, lens, g)
+    c.rows[int(table[0, token // page]), token % page].view(torch.uint8 if e4m3 else torch.int16)[where] = 0x7F if e4m3 else 0x7FC0
+    ql, qr = queries(torch, g, 2, 1, H, L, R, True)
+    out, ls = attend(torch, coli, c, table, lens, ql, qr, 0.06)
+    assert torch.isnan(out[0]).all() and torch.isnan(ls[0]).all()
+    check(torch, c, table, lens, ql, qr, 0.06, out, ls, lambda b, j: range(H) if b == 0 else ())
+
+
+@pytest.mark.parametrize("token", [5, 130, 1000, 2999])
+def test_infinite_row(token):
+    """An infinity in the rotary part of a bf16 row: the heads that it gives a score of +inf are NaN, those of -inf do not see it."""
+    torch, coli = setup()
+    g = gen(torch, 3)
+    L, R, page, H, lens = 256, 32, 16, 1024, [3000]
+    c, table = filled(torch, coli, False, L, R, page, lens, g)
+    at = (int(table[0, token // page]), token % page, L + 4)
+    c.rows[at] = float("inf")
+    ql, qr = queries(torch, g, 1, 1, H, L, R, True)
+    up = [h for h in range(H) if qr[0, 0, h, 4] > 0]
+    out, ls = attend(torch, coli, c, table, lens, ql, qr, 0.06)
+    assert 0 < len(up) < H
+    assert torch.isnan(out[0, 0, up]).all() and torch.isnan(ls[0, 0, up]).all()
+    c.rows[at] = 1e30                     # as good as +inf for a negative factor
+    down = [h for h in range(H) if h not in up]
+    again, ls2 = attend(torch, coli, c, table, lens, ql, qr, 0.06)
+    assert torch.equal(out[0, 0, down], again[0, 0, down]) and torch.equal(ls[0, 0, down], ls2[0, 0, down])
