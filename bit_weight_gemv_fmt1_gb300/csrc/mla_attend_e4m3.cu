@@ -158,7 +158,7 @@ __device__ __forceinline__ void load_queries8(const MlaAttendArgs &a, const Atte
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             mx = fmaxf(mx, __shfl_sync(0xffffffffu, mr, 8 * i));
-            // times 2^k2: the largest magnitude in [2^7, 2^8)
+            // times 2^k2: the largest magnitude in [2^7, 2^8); E4M3 has no infinity, so a row with one has NaN for its factor
             const int ex = (int)((__float_as_uint(mx) >> 23) & 0xFF) - 127;
             const int k2 = mx > 0.f && ex < 128 ? min(7 - ex, 120) : 0;
             const float up = __int_as_float((k2 + 127) << 23);
@@ -176,7 +176,7 @@ __device__ __forceinline__ void load_queries8(const MlaAttendArgs &a, const Atte
                 }
             }
             if (lane == 0) {
-                s.f[c] = a.scale * 1.4426950408889634f * __int_as_float((127 - k2) << 23);
+                s.f[c] = ex < 128 ? a.scale * 1.4426950408889634f * __int_as_float((127 - k2) << 23) : __int_as_float(0x7FC00000);
                 s.limit[c] = r < g.n_rows ? len - (a.n_q - 1 - r / a.H) : 0;
             }
         }

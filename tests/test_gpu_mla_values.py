@@ -114,3 +114,21 @@ def test_infinite_row(token):
     down = [h for h in range(H) if h not in up]
     again, ls2 = attend(torch, coli, c, table, lens, ql, qr, 0.06)
     assert torch.equal(out[0, 0, down], again[0, 0, down]) and torch.equal(ls[0, 0, down], ls2[0, 0, down])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_infinite_query(e4m3, bf16, sign):
+    """An infinite query element gives scores of +inf and -inf: that head is NaN, and nothing else."""
+    torch, coli = setup()
+    g = gen(torch, 4)
+    lens, L, R = [300, 140], 256, 32
+    c, table = filled(torch, coli, e4m3, L, R, 16, lens, g)
+    ql, qr = queries(torch, g, 2, 1, 40, L, R, bf16)
+    ql[0, 0, 3, 7] = qr[1, 0, 5, 2] = sign * float("inf")
+    bad = {0: [3], 1: [5]}
+    out, ls = attend(torch, coli, c, table, lens, ql, qr, 0.06)
+    for b, (h,) in bad.items():
+        assert torch.isnan(out[b, 0, h]).all() and torch.isnan(ls[b, 0, h])
+    check(torch, c, table, lens, ql, qr, 0.06, out, ls, lambda b, j: bad[b])
