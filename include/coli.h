@@ -417,7 +417,8 @@ int coli_mla_query(const float *q, int64_t q_stride, int T, int n_heads, int nop
  *   row = [ c * rsqrt(mean(c^2) + eps) * norm | k turned as in coli_mla_query ]
  * stored at slots[t].  COLI_BF16 rounds each element to nearest.  COLI_E4M3
  * stores scale = max|row| / 448 and code = e4m3(row / scale), to nearest; a row
- * of zeros gets scale 0 and codes 0.
+ * of zeros gets scale 0 and codes 0.  A NaN element is passed over by the
+ * maximum and stored as NaN.
  *   kv      device f32, token t at kv + t * kv_stride, [latent + rope].
  *   norm    device f32 [latent], or NULL: the latent part is stored as it is.
  *   eps     > 0 (ignored without norm).

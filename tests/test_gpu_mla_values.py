@@ -132,3 +132,27 @@ def test_infinite_query(e4m3, bf16, sign):
     for b, (h,) in bad.items():
         assert torch.isnan(out[b, 0, h]).all() and torch.isnan(ls[b, 0, h])
     check(torch, c, table, lens, ql, qr, 0.06, out, ls, lambda b, j: bad[b])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("fill", [0.0, 1.0, float("nan")])
+def test_append_keeps_nan(interleaved, norm, fill):
+    """A token with a NaN leaves NaN in its E4M3 row (all of its latent part under a norm), whatever stands beside it, zeros included."""
+    torch, coli = setup()
+    L, R = 128, 16
+    c = new_cache(torch, coli, True, L, R, 16, 1, junk=False)
+    kv = torch.full((3, L + R), fill)
+    kv[0, 5] = kv[1, L + 3] = float("nan")      # latent, rotary
+    kv[2, :] = 2.0
+    w = torch.ones(L).cuda() if norm else None
+    pos = torch.full((3,), 2, dtype=torch.int32).cuda()
+    coli.mla_append(c, kv.cuda(), w, 1e-6, pos, rotation(torch, 4, R).cuda(), torch.arange(3).cuda(), interleaved)
+    coli.sync_check()
+    got = values(torch, c)
+    pair = (2, 3) if interleaved else (3, 3 + R // 2)
+    assert torch.isnan(got[0, :L]).all() if norm else torch.isnan(got[0, 5])
+    assert torch.isnan(got[1, L + pair[0]]) and torch.isnan(got[1, L + pair[1]])
+    assert not torch.isnan(got[2]).any()
+    if fill == fill and not norm:
+        assert not torch.isnan(got[0, :5]).any() and not torch.isnan(got[1, :L]).any()
