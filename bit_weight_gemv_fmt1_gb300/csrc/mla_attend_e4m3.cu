@@ -41,6 +41,7 @@ constexpr int kCopyWarps = 5;            // one for each block of a tile
 constexpr int kThreads = 32 * (9 + kCopyWarps);
 constexpr float kHead8 = 6.f;            // log2 of the largest weight of a fresh reference
 constexpr float kLimit8 = 14.f;          // log2 of the weight that moves the reference (E5M2 ends at 57344)
+constexpr float kFloor8 = -90.f;         // log2 of a row's scale, at least
 constexpr float kQ1 = 32.f;              // q's second term against the first
 constexpr float kP1 = 8.f, kP2 = 16.f;   // P's second term against the first, third against the second
 
@@ -273,9 +274,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int u = 0; u < 8; u++) *reinterpret_cast<uint4 *>(sm + buf * stage + k * kBlk8 + t * 128 + 16 * u) = make_uint4(0u, 0u, 0u, 0u);
             }
             // log2 of the row's scale; the floor gives rows of scale 0, which weigh in l alone, a reference too
-            const float lg = fmaxf(__log2f(st), -90.f);
+            const float lg = fmaxf(__log2f(st), kFloor8);
             const uint32_t s_at = lanes + buf * (2 * NH) + col0;
-            // l += sign * weights 2^min(x - m, 100), and P for sign > 0; true if a weight has outgrown P
+            // l += sign * weights 2^min(x - m, kLimit8 - kFloor8), which the largest that moves no reference reaches, and P for
+            // sign > 0; true if a weight has outgrown P
             auto add = [&](float sign) {
                 uint32_t v0[HC], v1[HC], pk[3][HC / 4];
                 tmem_ld(s_at, v0);
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (tok >= s.limit[col0 + c + 1]) x.y = -INFINITY;
                     }
                     top = fmaxf(top, fmaxf(x.x, x.y));
-                    x = make_float2(ex2(min_nan(x.x, 100.f)), ex2(min_nan(x.y, 100.f)));
+                    x = make_float2(ex2(min_nan(x.x, kLimit8 - kFloor8)), ex2(min_nan(x.y, kLimit8 - kFloor8)));
                     l[c / 2] = fadd2(l[c / 2], sign > 0.f ? x : make_float2(-x.x, -x.y));
                     if (sign > 0.f) {
                         float2 p = fmul2(x, make_float2(st, st));

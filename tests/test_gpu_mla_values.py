@@ -156,3 +156,20 @@ def test_append_keeps_nan(interleaved, norm, fill):
     assert not torch.isnan(got[2]).any()
     if fill == fill and not norm:
         assert not torch.isnan(got[0, :5]).any() and not torch.isnan(got[1, :L]).any()
+
+
+@pytest.mark.parametrize("below", [94.5, 96.0, 97.5, 99.0, 140.0])
+def test_rows_of_scale_0_outweigh(below):
+    """Rows of scale 0 (value 0, score 0) after tiles whose scores lie far below: they take all the weight."""
+    torch, coli = setup()
+    L, R, page, n, H = 128, 16, 64, 1500, 1024    # many heads: few CTAs share the tokens, three tiles each
+    c = new_cache(torch, coli, True, L, R, page, 24, junk=False)
+    c.rows.view(-1, L + R)[:128, :2] = 1.0
+    c.scales.view(-1)[:128] = 1.0               # the first tile: scores of -below log2 units; the others: scale 0
+    ql, qr = torch.zeros(1, 1, H, L), torch.zeros(1, 1, H, R)
+    ql[..., 0] = -below * math.log(2.0)
+    table = torch.arange(24, dtype=torch.int32)[None]
+    out, ls = attend(torch, coli, c, table, [n], ql, qr, 1.0)
+    # lse = ln(1372 + 128 2^-below); out = 128 2^-below / 1372 of the first tile's rows
+    assert ((ls - math.log(1372.0)).abs() <= 1e-4).all()
+    assert (out.abs() <= 2.0 ** (1 - below)).all()
