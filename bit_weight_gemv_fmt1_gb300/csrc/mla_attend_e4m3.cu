@@ -267,11 +267,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(&s.s_full[buf], (it >> 1) & 1);
             tc_after_sync();
             const float st = tok < w.len ? s.scale[it & 3][t] : 0.f;
-            if ((w.tile() + 1) * kTile > w.len && tok >= w.len) {
-                // rows past the length may hold anything, and 0 * NaN is NaN
+            // what P takes of it: a row with no finite scale has it in its scores, and 0 * NaN is NaN
+            const float sp = fabsf(st) < INFINITY ? st : 0.f;
+            if (tok > w.len - a.n_q) {
+                // Likewise the codes.  Rows past the length may hold anything: zero.  Of the newest tokens' rows, which not
+                // every query sees, the NaN: the queries that see it have it in their scores.
                 for (int k = grp; k < np; k += 2)
 #pragma unroll
-                    for (int u = 0; u < 8; u++) *reinterpret_cast<uint4 *>(sm + buf * stage + k * kBlk8 + t * 128 + 16 * u) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int u = 0; u < 8; u++) {
+                        uint4 *at = reinterpret_cast<uint4 *>(sm + buf * stage + k * kBlk8 + t * 128 + 16 * u);
+                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                        if (tok < w.len) {
+                            x = *at;
+                            for (uint32_t *e : {&x.x, &x.y, &x.z, &x.w}) *e &= ~__vcmpeq4(*e & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                        }
+                        *at = x;
+                    }
             }
             // log2 of the row's scale; the floor gives rows of scale 0, which weigh in l alone, a reference too
             const float lg = fmaxf(__log2f(st), kFloor8);
@@ -299,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     x = make_float2(ex2(min_nan(x.x, kLimit8 - kFloor8)), ex2(min_nan(x.y, kLimit8 - kFloor8)));
                     l[c / 2] = fadd2(l[c / 2], sign > 0.f ? x : make_float2(-x.x, -x.y));
                     if (sign > 0.f) {
-                        float2 p = fmul2(x, make_float2(st, st));
+                        float2 p = fmul2(x, make_float2(sp, sp));
                         const uint32_t p0 = take_term<true>(p, kP1), p1 = take_term<true>(p, kP2), p2 = pack_e5m2(p.x, p.y);
                         const int sh = 8 * (c & 2), i = c / 4;
                         pk[0][i] = c & 2 ? pk[0][i] | p0 << sh : p0;

@@ -468,7 +468,8 @@ int coli_mla_read(const coli_mla_cache *cache, const int32_t *pages, int64_t pag
  * terms (scaled by a power of two per query row; a bf16 value exactly, others
  * to 2^-8 of them) and the probabilities three E5M2 ones (to 2^-11).  Sums,
  * maxima and the softmax's denominator are f32.  Rows past a sequence's length, and pages
- * past its last, are never used: they may hold anything.
+ * past its last, are never used: they may hold anything.  A NaN in a query, or in a row
+ * that a query sees, makes its output and lse NaN; a row that it does not see leaves it alone.
  * Pointers 16-byte aligned (pages, lens, lse: 4).  n_seq >= 0, n_q >= 1, 1 <= n_heads <= 1024,
  * n_q * n_heads <= 65536.  A page id outside [0, n_pages) among the needed ones, or a length out
  * of range, is recorded for coli_sync_check; that sequence's output is unspecified.

@@ -173,3 +173,29 @@ def test_rows_of_scale_0_outweigh(below):
     # lse = ln(1372 + 128 2^-below); out = 128 2^-below / 1372 of the first tile's rows
     assert ((ls - math.log(1372.0)).abs() <= 1e-4).all()
     assert (out.abs() <= 2.0 ** (1 - below)).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("n_q,n", [(2, 200), (3, 129), (4, 257), (130, 140)])
+def test_tokens_that_some_queries_do_not_see(e4m3, value, n_q, n):
+    """A newest token's row that is not finite leaves the queries before it alone."""
+    torch, coli = setup()
+    g = gen(torch, 5)
+    L, R, page, H = 256, 32, 16, 5
+    c, table = filled(torch, coli, e4m3, L, R, page, [n, 70], g)
+    at = (int(table[0, (n - 1) // page]), (n - 1) % page)
+    if e4m3:
+        c.scales[at] = value
+        c.rows[at].view(torch.uint8)[::3] = 0x7F
+    else:
+        c.rows[at[0], at[1], ::3] = value
+    ql, qr = queries(torch, g, 2, n_q, H, L, R, True)
+    out, ls = attend(torch, coli, c, table, [n, 70], ql, qr, 0.06)
+    vals = c.rows[at].view(torch.uint8 if e4m3 else torch.int16)
+    vals.zero_()                                # for the reference alone: no query that is checked sees the row
+    if e4m3:
+        c.scales[at] = 0.0
+    check(torch, c, table, [n, 70], ql, qr, 0.06, out, ls, lambda b, j: range(H) if b == 0 and j == n_q - 1 else ())
+    if value != value or e4m3:
+        assert torch.isnan(out[0, n_q - 1]).all()
