@@ -76,6 +76,8 @@ __device__ __forceinline__ void store_out(const MlaAttendArgs &a, long long e, f
     else reinterpret_cast<float *>(a.out)[e] = v;
 }
 
+__device__ __forceinline__ bool finite_bits(uint32_t v) { return (v & 0x7F800000u) != 0x7F800000u; }
+
 // Address of unit u (8 elements) of query row `row`: latent units first, then rope ones.
 template <bool QB>
 __device__ __forceinline__ const uint4 *query_unit(const MlaAttendArgs &a, long long row, int u) {
