@@ -78,6 +78,8 @@ _lib.coli_get_stats.restype = None
 _lib.coli_reset_stats.restype = None
 _lib.coli_set_fail_after.argtypes = [_i64]
 _lib.coli_set_fail_after.restype = None
+_lib.coli_set_wait_limit.argtypes = [_i64]
+_lib.coli_set_wait_limit.restype = None
 
 EXPORTS = ("coli_tensor_upload", "coli_tensor_upload_host", "coli_tensor_free", "coli_tensor_info", "coli_matmul", "coli_matmul_multi",
            "coli_matmul_rows", "coli_matmul_rows_t",
@@ -85,7 +87,7 @@ EXPORTS = ("coli_tensor_upload", "coli_tensor_upload_host", "coli_tensor_free", 
            "coli_expert_table_create", "coli_expert_table_free", "coli_moe_block_t",
            "coli_mla_query", "coli_mla_append", "coli_mla_read", "coli_mla_attend", "coli_mla_prefill",
            "coli_sync_check", "coli_last_error", "coli_get_stats", "coli_reset_stats", "coli_set_fail_after",
-           "coli_version")
+           "coli_set_wait_limit", "coli_version")
 
 
 class ColiError(RuntimeError):
@@ -479,6 +481,11 @@ def reset_stats():
 
 def set_fail_after(n: int):
     _lib.coli_set_fail_after(int(n))
+
+
+def set_wait_limit(ns: int):
+    """Bound of each device-side wait of the latent attention's kernels (ns <= 0: the default, 2 s)."""
+    _lib.coli_set_wait_limit(int(ns))
 
 
 def last_error() -> str:

@@ -66,6 +66,9 @@ int injected() {
     return COLI_OK;
 }
 
+constexpr int64_t kWaitNs = 2000000000;
+std::atomic<int64_t> g_wait_ns{kWaitNs};   // bound of the latent attention's device-side waits
+
 void count(int launches, uint64_t wbytes) {
     g_calls++;
     g_launches += launches;
@@ -262,6 +265,7 @@ int device_info(DevInfo *out) {
     out->err = ds->err;
     out->n_sm = ds->n_sm;
     out->device = ds->device;
+    out->wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     out->scratch = nullptr;
     out->state = ds;
     return COLI_OK;
@@ -296,6 +300,8 @@ void coli_reset_stats(void) {
 }
 
 void coli_set_fail_after(int64_t n) { fail_after().store(n < 0 ? -1 : n); }
+
+void coli_set_wait_limit(int64_t ns) { g_wait_ns.store(ns > 0 ? ns : kWaitNs); }
 
 // Argument checks shared by both uploads.
 static int check_upload(int fmt, int gs, int64_t O, int64_t I, const void *data, const float *scales,

@@ -35,8 +35,9 @@
 //
 // Warps: 0-7 softmax and output (two threads per token, each half the columns), 8
 // MMA issue, 9-11 tiled bulk copies.
-// Every wait is bounded; after one has run out all waits return at once, no
-// further MMA or copy is issued, and the kernel records DEV_ERR_TIMEOUT.
+// Every wait for another role is bounded; after one has run out all of them return at
+// once, no further MMA or copy is issued, and the kernel records DEV_ERR_TIMEOUT.  Named
+// barriers join the softmax warps alone, which pass the same ones whatever has run out.
 #include <cudaTypedefs.h>
 
 #include "mla_attend.cuh"
@@ -53,7 +54,7 @@ constexpr float kHead = 6.f;             // log2 of the largest weight of a fres
 constexpr float kLimit = 14.f;           // log2 of the weight that moves the reference
 
 struct Shared {
-    uint64_t full[kMaxPairs + 1], empty[kMaxPairs + 1], s_full, o_full, q_full, q_empty;
+    uint64_t full[kMaxPairs + 1], empty[kMaxPairs + 1], s_full, p_full, o_full, q_full, q_empty;   // q_full: by copies or by a softmax thread
     uint32_t tmem;
     int abort;
     Piece piece;
@@ -116,6 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
             mbar_init(&s.empty[p], 1);
         }
         mbar_init(&s.s_full, 1);
+        mbar_init(&s.p_full, 1);
         mbar_init(&s.o_full, 1);
         mbar_init(&s.q_full, 1);
         mbar_init(&s.q_empty, 1);
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
     };
 
     if (warp < 8) {
-        // ---------------------------------------------------------- softmax and output; warp 0 also issues the MMAs
+        // ---------------------------------------------------------- softmax and output
         const int wq = warp & 3, grp = warp >> 2;
         const int t = 32 * wq + lane;                                   // token of the tile, and dim of an O block
         const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
                 for (int c = 0; c < NC / 2; c++) l[c] = make_float2(0.f, 0.f);
                 fence_async_smem();
                 named_sync(1, kSoft);
-                if (!a.q_bf16) named_arrive(3, kSoft + 32);
+                if (!a.q_bf16 && tid == 0 && ok) mbar_arrive(&s.q_full);   // behind the barrier: for all of them
             }
             const int tok = w.tile() * kTile + t;
             // every column sees the whole tile: the first query's limit is the lowest
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
                 tc_before_sync();
                 named_sync(1, kSoft);
             }
-            named_arrive(4, kSoft + 32);
+            if (tid == 0 && ok) mbar_arrive(&s.p_full);                    // likewise
             if (!w.last()) continue;
 
             // ------------------------------------------------------ this part of the sequence is done
@@ -403,13 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
         // ---------------------------------------------------------- MMA issue
         int it = 0, seg = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), it++) {
-            if (w.first()) {
-                if (a.q_bf16) wait(&s.q_full, seg++ & 1);
-                else named_sync(3, kSoft + 32);
-            }
+            if (w.first()) wait(&s.q_full, seg++ & 1);
             issue_scores(it);
             if (w.last() && ok) tc_commit(&s.q_empty);
-            named_sync(4, kSoft + 32);
+            wait(&s.p_full, it & 1);
             issue_output(w.first(), w.last());
         }
     } else {
@@ -462,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
     tc_before_sync();
     __syncthreads();
     if (warp == 0) {
+        if (*abort) settle();
         tc_after_sync();
         tmem_free(tmem, kCols);
     }
@@ -597,7 +597,6 @@ AttendPlan plan(const MlaAttendArgs &a, int n_sm, size_t *bytes) {
     }
     g.pbox = kTile;
     while (a.c.page % g.pbox) g.pbox /= 2;
-    g.timeout_ns = 2000000000LL;
     *bytes = at;
     return g;
 }
@@ -660,6 +659,7 @@ cudaError_t launch_mla_attend(const MlaAttendArgs &a, const DevInfo &d, cudaStre
     size_t bytes;
     const int n_sm = d.n_sm;
     AttendPlan g = plan(a, n_sm, &bytes);
+    g.timeout_ns = d.wait_ns;
     void *scratch = d.scratch;
     if (bytes) {
         g.part = (float *)((char *)scratch + (size_t)g.part);

@@ -48,7 +48,7 @@ constexpr float kP1 = 8.f, kP2 = 16.f;   // P's second term against the first, t
 struct Shared8 {
     uint64_t k_full[2], k_empty[2][5];      // all of a tile; its blocks of 128 dims, last the rope part
     uint64_t sc_full[4];                    // row scales
-    uint64_t s_full[2], p_full[2];
+    uint64_t s_full[2], p_full[2], q_full;
     uint32_t tmem;
     int abort;
     Piece piece;
@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) tmem_alloc(&s.tmem, kCols);
     if (tid == 0) {
         for (int i = 0; i < 4; i++) mbar_init(&s.sc_full[i], 1);
+        mbar_init(&s.q_full, 1);
         for (int i = 0; i < 2; i++) {
             mbar_init(&s.k_full[i], np + 1);
             for (int p = 0; p < 5; p++) mbar_init(&s.k_empty[i][p], 1);
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < HC / 2; c++) l[c] = make_float2(0.f, 0.f);
                 fence_async_smem();
                 named_sync(1, kSoft);
-                named_arrive(3, kSoft + 32);
+                if (tid == 0 && ok) mbar_arrive(&s.q_full);             // behind the barrier: for all of them
             }
             const int tok = w.tile() * kTile + t;
             // every row sees the whole tile: the first query's limit is the lowest
@@ -482,10 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Scores of tile q and outputs of tile v, in whichever order their inputs come, scores first, as the softmax
         // would run dry.  A look at a barrier takes some 250 cycles while the MMAs read shared memory at its full rate, so
         // a tile has one for all of its blocks, and one instruction looks at both: odd lanes at tile q, even ones at P of v.
-        int it = 0;
+        int it = 0, seg = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next()) {
             const int n = w.rest();
-            named_sync(3, kSoft + 32);
+            wait(&s.q_full, seg++ & 1);
             int q = 0, v = 0, spins = 0;
             while (v < n && ok) {
                 const int i = lane & 1 ? it + q : it + v;
@@ -553,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_before_sync();
     __syncthreads();
     if (warp == 0) {
+        if (*abort) settle();
         tc_after_sync();
         tmem_free(tmem, kCols);
     }

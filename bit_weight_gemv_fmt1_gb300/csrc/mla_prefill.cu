@@ -564,14 +564,10 @@ __global__ void __launch_bounds__(384, 1)
             }
         }
     }
-    // every copy has landed before the CTA may end (those not waited for by an MMA that was issued: after a timeout)
-    if (warp > 8 && (!ok || *abort)) {
-        const uint64_t late = global_ns() + 200000000ull;
-        while (global_ns() < late) __nanosleep(1000);
-    }
     tc_before_sync();
     __syncthreads();
     if (warp == 0) {
+        if (*abort) settle();
         tc_after_sync();
         tmem_free(tmem, 512);
     }
@@ -610,7 +606,7 @@ cudaError_t matrix_map(const void *p, long long cols, long long rows, long long 
 }
 
 template <int V>
-cudaError_t run(const MlaPrefillArgs &a, int device, cudaStream_t st) {
+cudaError_t run(const MlaPrefillArgs &a, const DevInfo &d, cudaStream_t st) {
     CUtensorMap q, kv, kr, vm;
     if (cudaError_t e = matrix_map(a.q, (long long)a.H * (a.nope + a.rope), a.Tq, a.q_stride, kRows, &q)) return e;
     kv = kr = vm = q;                         // no keys: never read
@@ -626,9 +622,9 @@ cudaError_t run(const MlaPrefillArgs &a, int device, cudaStream_t st) {
     const size_t smem = bytes(nb);
     auto kern = mla_prefill_kernel<V>;
     static std::atomic<uint64_t> done{0};
-    if (cudaError_t e = allow_smem(kern, bytes(3), device, done)) return e;   // nope = 128
+    if (cudaError_t e = allow_smem(kern, bytes(3), d.device, done)) return e;   // nope = 128
 
-    return launch_pdl(kern, dim3((unsigned)units), dim3(384), smem, st, q, kv, kr, vm, a, 2000000000LL);
+    return launch_pdl(kern, dim3((unsigned)units), dim3(384), smem, st, q, kv, kr, vm, a, d.wait_ns);
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -667,7 +663,7 @@ cudaError_t launch_mla_prefill(const MlaPrefillArgs &a0, const DevInfo &d, cudaS
         a.kv_stride = cols[1];
         a.kr_stride = cols[2];
     }
-    return a.v == 64 ? run<64>(a, d.device, st) : run<128>(a, d.device, st);
+    return a.v == 64 ? run<64>(a, d, st) : run<128>(a, d, st);
 }
 
 }  // namespace coli

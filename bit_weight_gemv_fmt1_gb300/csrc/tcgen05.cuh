@@ -54,6 +54,11 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
         " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar))
         : "memory");
 }
+// After a wait has run out: time for every copy and MMA that was issued to end, before the CTA gives up its memory.
+__device__ __forceinline__ void settle() {
+    const uint64_t until = global_ns() + 200000000ull;
+    while (global_ns() < until) __nanosleep(1000);
+}
 // Whole warp: allocate / free `cols` TMEM columns (a power of two >= 32).
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t cols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(cols) : "memory");

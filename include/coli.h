@@ -527,6 +527,13 @@ void coli_reset_stats(void);
  * load time. */
 void coli_set_fail_after(int64_t n);
 
+/* How long, in nanoseconds, a kernel of the latent attention waits for one of its own
+ * steps before it gives up, records COLI_ETIMEOUT for coli_sync_check and returns; its
+ * outputs are then unspecified.  ns <= 0: the default, 2 s.  Applies to calls made
+ * after it.  A step takes microseconds: the limit is there for a kernel that has
+ * gone wrong, and a short one for tests of the error's way back. */
+void coli_set_wait_limit(int64_t ns);
+
 /* Library version string. */
 const char *coli_version(void);
 
