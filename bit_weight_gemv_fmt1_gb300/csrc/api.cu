@@ -66,7 +66,7 @@ int injected() {
     return COLI_OK;
 }
 
-constexpr int64_t kWaitNs = 2000000000;
+constexpr int64_t kWaitNs = 2000000000, kMaxWaitNs = 3600000000000;
 std::atomic<int64_t> g_wait_ns{kWaitNs};   // bound of the latent attention's device-side waits
 
 void count(int launches, uint64_t wbytes) {
@@ -301,7 +301,7 @@ void coli_reset_stats(void) {
 
 void coli_set_fail_after(int64_t n) { fail_after().store(n < 0 ? -1 : n); }
 
-void coli_set_wait_limit(int64_t ns) { g_wait_ns.store(ns > 0 ? ns : kWaitNs); }
+void coli_set_wait_limit(int64_t ns) { g_wait_ns.store(ns > 0 ? std::min(ns, kMaxWaitNs) : kWaitNs); }
 
 // Argument checks shared by both uploads.
 static int check_upload(int fmt, int gs, int64_t O, int64_t I, const void *data, const float *scales,

@@ -789,7 +789,7 @@ void count_call(int launches, uint64_t weight_bytes);
 struct DevInfo {
     int *err;
     int n_sm, device;
-    long long wait_ns;        // bound of a device-side wait
+    long long wait_ns;        // bound of the device-side waits (see deadline_after)
     void *scratch;
     void *state;              // the library's own
 };

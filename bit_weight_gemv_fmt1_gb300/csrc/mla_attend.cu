@@ -35,8 +35,8 @@
 //
 // Warps: 0-7 softmax and output (two threads per token, each half the columns), 8
 // MMA issue, 9-11 tiled bulk copies.
-// Every wait for another role is bounded; after one has run out all of them return at
-// once, no further MMA or copy is issued, and the kernel records DEV_ERR_TIMEOUT.  Named
+// Every wait for another role is bounded, by a limit that each part of a sequence
+// renews; after one has run out all of them return at once, no further MMA or copy is issued, and the kernel records DEV_ERR_TIMEOUT.  Named
 // barriers join the softmax warps alone, which pass the same ones whatever has run out.
 #include <cudaTypedefs.h>
 
@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
-    const uint64_t deadline = global_ns() + (uint64_t)g.timeout_ns;
     volatile int *abort = &s.abort;
+    uint64_t deadline = deadline_after(g.wait_ns, 0);
     bool ok = true;                        // this thread's waits have all ended well
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (!ok) return;
@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
         int it = 0, seg = 0, cur = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), it++) {
             if (w.first()) {
+                deadline = deadline_after(g.wait_ns, w.rest());
                 if (!a.q_bf16) load_queries<N>(a, g, sm + q_off, w.b, w.rb, tid);
                 if (tid < N) {
                     const int r = w.rb * N + tid;
@@ -405,7 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
         // ---------------------------------------------------------- MMA issue
         int it = 0, seg = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), it++) {
-            if (w.first()) wait(&s.q_full, seg++ & 1);
+            if (w.first()) {
+                deadline = deadline_after(g.wait_ns, w.rest());
+                wait(&s.q_full, seg++ & 1);
+            }
             issue_scores(it);
             if (w.last() && ok) tc_commit(&s.q_empty);
             wait(&s.p_full, it & 1);
@@ -417,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
         BoxAhead box(a, g, s.piece, slot, lane, who == 1);
         int it = 0, seg = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), box.next(), it++) {
+            if (w.first()) deadline = deadline_after(g.wait_ns, w.rest());
             const int sl = box.slot[0], nbox = kTile / g.pbox;
             const uint32_t live = __ballot_sync(0xffffffffu, sl >= 0), n = __popc(live) * g.pbox;
             const int y0 = __shfl_sync(0xffffffffu, sl, 0);
@@ -659,7 +664,7 @@ cudaError_t launch_mla_attend(const MlaAttendArgs &a, const DevInfo &d, cudaStre
     size_t bytes;
     const int n_sm = d.n_sm;
     AttendPlan g = plan(a, n_sm, &bytes);
-    g.timeout_ns = d.wait_ns;
+    g.wait_ns = d.wait_ns;
     void *scratch = d.scratch;
     if (bytes) {
         g.part = (float *)((char *)scratch + (size_t)g.part);

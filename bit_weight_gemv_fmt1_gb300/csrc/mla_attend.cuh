@@ -21,7 +21,7 @@ struct AttendPlan {
     float *part_ml;
     int2 *pieces;          // [n_seq] first group and number of groups of each sequence
     int pbox;              // tokens per copy box
-    long long timeout_ns;
+    long long wait_ns;     // bound of the waits (deadline_after)
 };
 
 // The piece of a CTA's group: tiles [u0, u1), beginning in sequence b0 with p0 tiles before it.

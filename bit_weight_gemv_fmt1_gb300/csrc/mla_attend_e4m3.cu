@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
-    const uint64_t deadline = global_ns() + (uint64_t)g.timeout_ns;
     volatile int *abort = &s.abort;
+    uint64_t deadline = deadline_after(g.wait_ns, 0);
     bool ok = true;                        // this thread's waits have all ended well
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (!ok) return;
@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), it++) {
             const int buf = it & 1;
             if (w.first()) {
+                deadline = deadline_after(g.wait_ns, w.rest());
                 if (a.q_bf16) load_queries8<NH, true>(a, g, s, sm + q_off, w.b, w.rb, w.len, warp, lane);
                 else load_queries8<NH, false>(a, g, s, sm + q_off, w.b, w.rb, w.len, warp, lane);
                 if (tid < NH) s.m[cur][tid] = -kNone;
@@ -486,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0, seg = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next()) {
             const int n = w.rest();
+            deadline = deadline_after(g.wait_ns, n);
             wait(&s.q_full, seg++ & 1);
             int q = 0, v = 0, spins = 0;
             while (v < n && ok) {
@@ -517,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0;
         for (Walk w(a, g, s.piece, slot); w.valid(); w.next(), box.next(), it++) {
             if (!mine) continue;
+            if (w.first()) deadline = deadline_after(g.wait_ns, w.rest());
             const int buf = it & 1, sl = box.slot[0];
             const uint32_t live = __ballot_sync(0xffffffffu, sl >= 0), n = __popc(live) * g.pbox;
             const int y0 = __shfl_sync(0xffffffffu, sl, 0);

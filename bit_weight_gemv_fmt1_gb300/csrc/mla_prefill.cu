@@ -33,8 +33,9 @@
 // Keys past a causal row's limit are masked by selection; value rows past the
 // sequence's end belong to its neighbours and are zeroed in shared memory.
 // Warps: 0-3 and 4-7 softmax of A and B, 8 MMA issue, 9 units and copies of keys, 10 and 11 of queries and values.
-// Every wait is bounded; after one has run out all waits return at once, no
-// further MMA or copy is issued, and the kernel records DEV_ERR_TIMEOUT.
+// Every wait is bounded, by a limit that each unit renews: a CTA that takes over units lives as
+// long as the call.  After one has run out all waits return at once, no further MMA or copy is
+// issued, and the kernel records DEV_ERR_TIMEOUT.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -224,7 +225,7 @@ __device__ __forceinline__ int read_next(Shared &s) {
 template <int V>
 __global__ void __launch_bounds__(384, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
-                       const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap v_map, const MlaPrefillArgs a, long long timeout_ns) {
+                       const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap v_map, const MlaPrefillArgs a, long long wait_ns) {
     extern __shared__ uint8_t raw[];
     __shared__ Shared s;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
@@ -263,9 +264,9 @@ __global__ void __launch_bounds__(384, 1)
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem, 0);
-    const uint64_t deadline = global_ns() + (uint64_t)timeout_ns;
     volatile int *abort = &s.abort;
     bool ok = true;                      // this thread's waits have all ended well
+    uint64_t deadline = deadline_after(wait_ns, 0);
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (!ok) return;
         if (!warp_wait_now(bar, parity, deadline, abort, lane)) {
@@ -274,12 +275,14 @@ __global__ void __launch_bounds__(384, 1)
             atomicCAS(a.err, 0, (int)DEV_ERR_TIMEOUT);
         }
     };
-    // Unit r of this CTA as the key warp has found it; the warp that has read it says so.
+    // Unit r of this CTA as the key warp has found it; the warp that has read it says so.  It comes when the keys of the unit
+    // before have been asked for: a warp with no tile in that one waits for all of its time.
     auto take = [&](int r) {
         wait(&s.u_full[r & 1], (r >> 1) & 1);
         Unit u = s.unit[r & 1];
         if (!ok) u.n = -1;
         u = uniform(u);
+        deadline = deadline_after(wait_ns, max(u.n, 0));
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.u_empty[r & 1]);
         return u;
@@ -525,6 +528,7 @@ __global__ void __launch_bounds__(384, 1)
                 ask_next(s);
             }
             __syncwarp();
+            deadline = deadline_after(wait_ns, max(u.n, 0));
             const int hk = u.head * (a.nope + V);
             for (int j = 0; j < u.n; j++)
                 for (int b = 0; b < nb; b++) {

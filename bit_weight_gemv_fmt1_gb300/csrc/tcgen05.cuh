@@ -54,6 +54,11 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
         " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar))
         : "memory");
 }
+// When the waits of a piece of work of so many tiles are given up.  A warp renews it with each piece, since a kernel may run
+// for longer than any limit; a wait bounded from its own start costs 2 to 3 % in the pipelined kernels.
+__device__ __forceinline__ uint64_t deadline_after(long long limit_ns, int tiles) {
+    return global_ns() + (uint64_t)(limit_ns + tiles * (limit_ns >> 8));
+}
 // After a wait has run out: time for every copy and MMA that was issued to end, before the CTA gives up its memory.
 __device__ __forceinline__ void settle() {
     const uint64_t until = global_ns() + 200000000ull;

@@ -527,11 +527,13 @@ void coli_reset_stats(void);
  * load time. */
 void coli_set_fail_after(int64_t n);
 
-/* How long, in nanoseconds, a kernel of the latent attention waits for one of its own
- * steps before it gives up, records COLI_ETIMEOUT for coli_sync_check and returns; its
- * outputs are then unspecified.  ns <= 0: the default, 2 s.  Applies to calls made
- * after it.  A step takes microseconds: the limit is there for a kernel that has
- * gone wrong, and a short one for tests of the error's way back. */
+/* How long, in nanoseconds, a kernel of the latent attention waits in one of its pieces
+ * of work (a head's 256 queries, a CTA's part of a sequence) before it gives up, records
+ * COLI_ETIMEOUT for coli_sync_check and returns; its outputs are then unspecified.  A
+ * piece has 1/256 of it more for each of its tiles of 128 tokens (microseconds each);
+ * a call has no limit.  ns <= 0: the default, 2 s; at most an hour.  Applies to calls
+ * made after it.  The limit is there for a kernel that has gone wrong, and a short one
+ * for tests of the error's way back. */
 void coli_set_wait_limit(int64_t ns);
 
 /* Library version string. */

@@ -73,3 +73,39 @@ def test_prefill_wait_runs_out(limit):
     limit(0)
     assert torch.equal(run(), good)
     coli.sync_check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attend_longer_than_the_limit(limit, e4m3):
+    """The limit is one wait's: a call may take many times as long (here some 3 ms, 512 sequences on the same pages)."""
+    torch, coli = setup()
+    g = gen(torch, 3)
+    c, table = filled(torch, coli, e4m3, 512, 64, 64, [12000], g)
+    B = 512
+    table, n = table.cuda().expand(B, -1).contiguous(), torch.full((B,), 12000, dtype=torch.int32).cuda()
+    ql, qr = torch.randn(B, 1, 128, 512, device="cuda").to(torch.bfloat16), torch.randn(B, 1, 128, 64, device="cuda").to(torch.bfloat16)
+    outs = []
+    for ns in (0, 500000):
+        out = torch.zeros_like(ql)
+        limit(ns)
+        coli.mla_attend(c, ql, qr, table, n, 0.06, out)
+        coli.sync_check()
+        outs.append(out)
+    assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("n_q,n_k,H", [(24000, 24000, 32), (100, 300000, 1)])
+def test_prefill_longer_than_the_limit(limit, n_q, n_k, H):
+    """Likewise: 4 ms of many units, and one unit of 3 ms whose second query tile is empty."""
+    torch, coli = setup()
+    q, kv = torch.randn(n_q, H, 192, device="cuda").to(torch.bfloat16), torch.randn(n_k, H, 256, device="cuda").to(torch.bfloat16)
+    kr = torch.randn(n_k, 64, device="cuda").to(torch.bfloat16)
+    cu_q, cu_k = (torch.tensor([0, n], dtype=torch.int32).cuda() for n in (n_q, n_k))
+    outs = []
+    for ns in (0, 1000000):
+        out = torch.zeros(n_q, H, 128, device="cuda", dtype=torch.bfloat16)
+        limit(ns)
+        coli.mla_prefill(q, kv, kr, cu_q, cu_k, 0.07, out)
+        coli.sync_check()
+        outs.append(out)
+    assert torch.equal(*outs)
