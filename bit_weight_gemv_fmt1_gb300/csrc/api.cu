@@ -10,6 +10,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <map>
+#include <memory>
 #include <mutex>
 #include <unordered_map>
 #include <algorithm>
@@ -76,14 +77,49 @@ void count(int launches, uint64_t wbytes) {
 }
 
 // ------------------------------------------------------------------ device state
-struct Workspace {
-    unsigned *bar = nullptr;      // grid barrier words (kBarrierBytes)
-    void *buf = nullptr;          // scratch
+// While it lives, this thread may allocate and free although some stream is being captured.
+struct Relaxed {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// Device memory that goes with its last holder: the stream's workspace, or a call that another host thread's larger one on
+// the same stream has overtaken.  A stream's work on it ends first; a graph's is gone when the graph is.
+struct Buffer {
+    void *p = nullptr;
     size_t cap = 0;
-    void *rbuf = nullptr;         // router logits (kept apart from buf, which the router matvec may use)
-    size_t rcap = 0;
-    unsigned *cnt = nullptr;      // counters of the streamed decode block (zero between calls)
-    size_t cnt_cap = 0;           // words
+    cudaStream_t st;
+    bool of_graph;
+    Buffer(cudaStream_t st_, bool of_graph_) : st(st_), of_graph(of_graph_) {}
+    Buffer(const Buffer &) = delete;
+    ~Buffer() {
+        if (!p) return;
+        Relaxed r;
+        if (!of_graph) cudaStreamSynchronize(st);
+        cudaFree(p);
+    }
+};
+using Held = std::shared_ptr<Buffer>;
+
+// Library-owned memory of one stream: scratch, which a larger call replaces, and words that kernels leave as they found them
+// and that stay where they are, or at least allocated, as captured graphs keep their addresses.
+// A captured graph may be replayed at any time, on any stream: it has scratch of its own for each stream that was captured
+// into it, shared with no eager call and no other graph; what that outgrows is kept.
+struct Workspace {
+    Held buf;                     // scratch
+    Held rbuf;                    // router logits (kept apart from buf, which the router matvec may use)
+    Held bar;                     // grid barrier words (kBarrierBytes); a stream's alone
+    Held cnt;                     // counters of the streamed decode block (zero between calls); a stream's alone
+    std::vector<Held> outgrown;
+    bool of_graph = false;
+};
+
+// What a call holds of it.
+struct Scratch {
+    Held hold;
+    void *buf = nullptr;
+    unsigned *bar = nullptr;
 };
 
 struct CachedTable {
@@ -98,12 +134,27 @@ struct DeviceState {
     int n_sm = 0, device = 0;
     size_t smem_optin = 0;
     std::map<cudaStream_t, Workspace> ws;
+    std::map<unsigned long long, std::map<cudaStream_t, Workspace>> graphs;   // by capture id
     std::unordered_map<uint64_t, CachedTable> tables;
     uint64_t tick = 0;
+    std::mutex gone_mu;           // no CUDA call is made under it
+    std::vector<unsigned long long> gone;   // captures whose graphs have been destroyed
 };
 
 std::mutex g_dev_mu;
 std::map<int, DeviceState *> g_dev;
+
+// Zeroes fresh memory before any stream can use it.  On a stream of its own: the legacy one would wait for, and may not be
+// used beside, streams under capture.
+cudaError_t zero(void *p, size_t bytes) {
+    cudaStream_t s;
+    cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (e != cudaSuccess) return e;
+    e = cudaMemsetAsync(p, 0, bytes, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    cudaStreamDestroy(s);
+    return e;
+}
 
 int device_state(DeviceState **out) {
     int dev = 0;
@@ -115,8 +166,9 @@ int device_state(DeviceState **out) {
         return COLI_OK;
     }
     DeviceState *d = new DeviceState();
+    Relaxed r;
     CU(cudaMalloc(&d->err, sizeof(int)), "cudaMalloc(error word)");
-    CU(cudaMemset(d->err, 0, sizeof(int)), "cudaMemset(error word)");
+    CU(zero(d->err, sizeof(int)), "clearing the error word");
     CU(cudaDeviceGetAttribute(&d->n_sm, cudaDevAttrMultiProcessorCount, dev), "cudaDeviceGetAttribute");
     int optin = 0;
     CU(cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev), "cudaDeviceGetAttribute");
@@ -127,46 +179,106 @@ int device_state(DeviceState **out) {
     return COLI_OK;
 }
 
-// Router-logit scratch of at least `bytes` for this stream (grown like workspace()).
-int router_scratch(DeviceState *d, cudaStream_t st, size_t bytes, float **out) {
-    std::lock_guard<std::mutex> lk(d->mu);
-    Workspace &w = d->ws[st];
-    if (w.rcap < bytes) {
-        if (w.rbuf) {
-            CU(cudaDeviceSynchronize(), "cudaDeviceSynchronize(router scratch growth)");
-            CU(cudaFree(w.rbuf), "cudaFree(router scratch)");
-            w.rbuf = nullptr;
-            w.rcap = 0;
-        }
-        CU(cudaMalloc(&w.rbuf, bytes), "cudaMalloc(router scratch)");
-        w.rcap = bytes;
+// Told by CUDA, on a thread of its own and where no CUDA call may be made, that a graph and all that was made from it are gone.
+struct Gone {
+    DeviceState *d;
+    unsigned long long id;
+};
+void CUDART_CB graph_gone(void *p) {
+    Gone *g = (Gone *)p;
+    {
+        std::lock_guard<std::mutex> lk(g->d->gone_mu);
+        g->d->gone.push_back(g->id);
     }
-    *out = (float *)w.rbuf;
+    delete g;
+}
+
+// The memory of such graphs (d->mu held).
+void free_gone(DeviceState *d) {
+    std::vector<unsigned long long> gone;
+    {
+        std::lock_guard<std::mutex> lk(d->gone_mu);
+        gone.swap(d->gone);
+    }
+    for (unsigned long long id : gone) d->graphs.erase(id);
+}
+
+// Where a call on this stream has its scratch (d->mu held): the stream's workspace, or, under capture, its part of the graph's.
+// The graph's end is told by a user object, for which a replay takes 2 us longer.
+int workspace_of(DeviceState *d, cudaStream_t st, Workspace **out) {
+    cudaStreamCaptureStatus status;
+    CU(cudaStreamIsCapturing(st, &status), "cudaStreamIsCapturing");
+    if (status == cudaStreamCaptureStatusNone) {
+        *out = &d->ws[st];
+        return COLI_OK;
+    }
+    unsigned long long id = 0;
+    cudaGraph_t graph = nullptr;
+    const cudaGraphNode_t *deps;
+    const cudaGraphEdgeData *edges;
+    size_t n;
+    CU(cudaStreamGetCaptureInfo(st, &status, &id, &graph, &deps, &edges, &n), "cudaStreamGetCaptureInfo");
+    if (status != cudaStreamCaptureStatusActive) return fail(COLI_ECUDA, "the stream's capture has been invalidated");
+    auto it = d->graphs.find(id);
+    if (it == d->graphs.end()) {
+        free_gone(d);
+        Gone *note = new Gone{d, id};
+        cudaUserObject_t obj;
+        const cudaError_t e = cudaUserObjectCreate(&obj, note, graph_gone, 1, cudaUserObjectNoDestructorSync);
+        if (e != cudaSuccess) {
+            delete note;
+            return cuda_fail(e, "cudaUserObjectCreate");
+        }
+        it = d->graphs.emplace(id, std::map<cudaStream_t, Workspace>()).first;
+        const cudaError_t e2 = cudaGraphRetainUserObject(graph, obj, 1, cudaGraphUserObjectMove);
+        if (e2 != cudaSuccess) {
+            cudaUserObjectRelease(obj, 1);
+            return cuda_fail(e2, "cudaGraphRetainUserObject");
+        }
+    }
+    *out = &it->second[st];
+    (*out)->of_graph = true;
     return COLI_OK;
 }
 
-// Scratch of at least `bytes` for this stream (grown on demand; growing waits
-// for the device so that no queued kernel still uses the old buffer).
-int workspace(DeviceState *d, cudaStream_t st, size_t bytes, Workspace **out) {
+// At least `bytes` (`want` when it has to allocate); words: zeroed at allocation, and kept when outgrown (d->mu held).
+int grown(DeviceState *d, Workspace &w, cudaStream_t st, Held &b, size_t bytes, size_t want, bool words, const char *what) {
+    if (b && b->cap >= bytes) return COLI_OK;
+    if (b && (w.of_graph || words)) w.outgrown.push_back(b);
+    if (!w.of_graph && !words) free_gone(d);
+    b.reset();
+    Relaxed r;
+    Held n = std::make_shared<Buffer>(st, w.of_graph);
+    CU(cudaMalloc(&n->p, want), what);
+    if (words) CU(zero(n->p, want), what);
+    n->cap = want;
+    b = std::move(n);
+    return COLI_OK;
+}
+
+// Router-logit scratch of at least `bytes` for this stream.
+int router_scratch(DeviceState *d, cudaStream_t st, size_t bytes, Held *out) {
     std::lock_guard<std::mutex> lk(d->mu);
-    Workspace &w = d->ws[st];
-    if (!w.bar) {
-        // words 0-1: counter and generation of the resetting grid barrier
-        CU(cudaMalloc(&w.bar, kBarrierBytes), "cudaMalloc(barrier)");
-        CU(cudaMemset(w.bar, 0, kBarrierBytes), "cudaMemset(barrier)");
-    }
-    if (w.cap < bytes) {
-        if (w.buf) {
-            CU(cudaDeviceSynchronize(), "cudaDeviceSynchronize(workspace growth)");
-            CU(cudaFree(w.buf), "cudaFree(workspace)");
-            w.buf = nullptr;
-            w.cap = 0;
-        }
-        const size_t want = bytes + bytes / 4;
-        CU(cudaMalloc(&w.buf, want), "cudaMalloc(workspace)");
-        w.cap = want;
-    }
-    *out = &w;
+    Workspace *w = nullptr;
+    if (int rc = workspace_of(d, st, &w)) return rc;
+    if (int rc = grown(d, *w, st, w->rbuf, bytes, bytes, false, "cudaMalloc(router scratch)")) return rc;
+    *out = w->rbuf;
+    return COLI_OK;
+}
+
+// Scratch of at least `bytes` for this stream (grown on demand; growing waits for the stream).
+int workspace(DeviceState *d, cudaStream_t st, size_t bytes, Scratch *out) {
+    std::lock_guard<std::mutex> lk(d->mu);
+    Workspace *w = nullptr;
+    if (int rc = workspace_of(d, st, &w)) return rc;
+    const size_t want = w->of_graph ? bytes : bytes + bytes / 4;
+    if (int rc = grown(d, *w, st, w->buf, bytes, want, false, "cudaMalloc(workspace)")) return rc;
+    // words 0-1: counter and generation of the resetting grid barrier
+    Workspace &own = d->ws[st];
+    if (int rc = grown(d, own, st, own.bar, kBarrierBytes, kBarrierBytes, true, "cudaMalloc(barrier)")) return rc;
+    out->hold = w->buf;
+    out->buf = w->buf->p;
+    out->bar = (unsigned *)own.bar->p;
     return COLI_OK;
 }
 
@@ -175,19 +287,9 @@ int workspace(DeviceState *d, cudaStream_t st, size_t bytes, Workspace **out) {
 int decode_counters(DeviceState *d, cudaStream_t st, size_t words, unsigned **out) {
     std::lock_guard<std::mutex> lk(d->mu);
     Workspace &w = d->ws[st];
-    if (w.cnt_cap < words) {
-        if (w.cnt) {
-            CU(cudaDeviceSynchronize(), "cudaDeviceSynchronize(counter growth)");
-            CU(cudaFree(w.cnt), "cudaFree(counters)");
-            w.cnt = nullptr;
-            w.cnt_cap = 0;
-        }
-        const size_t want = std::max<size_t>(words, 4096);
-        CU(cudaMalloc(&w.cnt, want * sizeof(unsigned)), "cudaMalloc(counters)");
-        CU(cudaMemset(w.cnt, 0, want * sizeof(unsigned)), "cudaMemset(counters)");
-        w.cnt_cap = want;
-    }
-    *out = w.cnt;
+    const size_t want = std::max<size_t>(words, 4096) * sizeof(unsigned);
+    if (int rc = grown(d, w, st, w.cnt, words * sizeof(unsigned), want, true, "cudaMalloc(counters)")) return rc;
+    *out = (unsigned *)w.cnt->p;
     return COLI_OK;
 }
 
@@ -272,9 +374,10 @@ int device_info(DevInfo *out) {
 }
 
 int device_scratch(DevInfo *d, cudaStream_t st, size_t bytes) {
-    Workspace *ws = nullptr;
+    Scratch ws;
     if (int rc = workspace((DeviceState *)d->state, st, bytes, &ws)) return rc;
-    d->scratch = ws->buf;
+    d->scratch = ws.buf;
+    d->hold = ws.hold;
     return COLI_OK;
 }
 }  // namespace coli
@@ -608,11 +711,11 @@ static int run_matmul(int n, const coli_tensor *const *W, const float *x, float 
         if (tc_supported_fmt(W[m]->fmt, W[m]->gs) && W[m]->tmap) {
             const int I = (int)W[m]->I, I_pad = (I + 63) / 64 * 64;
             const int rows_alloc = std::max(S, 64);
-            Workspace *ws = nullptr;
+            Scratch ws;
             const size_t planes = (size_t)3 * rows_alloc * I_pad * 2;
             if (int rc = workspace(ds, st, planes + 256, &ws)) return rc;
-            int *flag = (int *)ws->buf;
-            void *pl = (char *)ws->buf + 256;
+            int *flag = (int *)ws.buf;
+            void *pl = (char *)ws.buf + 256;
             CU(cudaMemsetAsync(flag, 0, sizeof(int), st), "cudaMemsetAsync(flag)");
             cudaError_t e = launch_gather_planes(x, I, nullptr, 1, nullptr, S, I, I_pad, pl, (long long)rows_alloc * I_pad,
                                                  flag, st);
@@ -802,8 +905,9 @@ int coli_moe_router(const float *x, int S, const coli_tensor *router, const floa
     if (int rc = device_state(&ds)) return rc;
     cudaStream_t st = (cudaStream_t)stream;
     // logits go to a scratch buffer of their own (the stream's workspace is used by the matvec)
-    float *logits = nullptr;
-    if (int rc = router_scratch(ds, st, (size_t)S * router->O * sizeof(float), &logits)) return rc;
+    Held held;
+    if (int rc = router_scratch(ds, st, (size_t)S * router->O * sizeof(float), &held)) return rc;
+    float *logits = (float *)held->p;
     float *ys[1] = {logits};
     const coli_tensor *Ws[1] = {router};
     if (int rc = coli_matmul_multi(1, Ws, x, ys, S, stream)) return rc;
@@ -1075,7 +1179,7 @@ static int moe_run(const MoeInfo &mi, const ExpertDesc *table, DeviceState *ds, 
         if (ok && sd_plan(fmt, (int)H, (int)F, K, cpr_gu, cpr_d, (int)g0->rs, (int)d0->rs, g0->ng, d0->ng, ds->n_sm,
                           (size_t)ds->smem_optin, &a, &smem) &&
             sd_occupancy(a, smem, &per_sm) == cudaSuccess && per_sm >= 1) {
-            Workspace *ws = nullptr;
+            Scratch ws;
             if (int rc = workspace(ds, st, sd_scratch_bytes(a), &ws)) return rc;
             unsigned *ctr = nullptr;
             if (int rc = decode_counters(ds, st, sd_counter_words(a), &ctr)) return rc;
@@ -1087,7 +1191,7 @@ static int moe_run(const MoeInfo &mi, const ExpertDesc *table, DeviceState *ds, 
             a.n_experts = n_experts;
             a.gshift_gu = fmt == 4 ? __builtin_ctz(gs_gu / 32) : 0;
             a.gshift_d = fmt == 4 ? __builtin_ctz(gs_d / 32) : 0;
-            a.hbuf = (float *)ws->buf;
+            a.hbuf = (float *)ws.buf;
             a.ctr = ctr;
             a.err = ds->err;
             a.timeout_ns = 2000000000LL;
@@ -1110,7 +1214,7 @@ static int moe_run(const MoeInfo &mi, const ExpertDesc *table, DeviceState *ds, 
         }
         int per_sm = 0;
         if (smem <= ds->smem_optin && slab_decode_occupancy(fmt, smem, &per_sm) == cudaSuccess && per_sm >= 1) {
-            Workspace *ws = nullptr;
+            Scratch ws;
             if (int rc = workspace(ds, st, (size_t)n_slots * F * sizeof(float), &ws)) return rc;
             const int grid = std::min(per_sm, 2) * ds->n_sm;
             MoeDecodeArgs a;
@@ -1127,8 +1231,8 @@ static int moe_run(const MoeInfo &mi, const ExpertDesc *table, DeviceState *ds, 
             a.F = (int)F;
             a.cpr_gu = cpr_gu;
             a.cpr_d = cpr_d;
-            a.hbuf = (float *)ws->buf;
-            a.bar = ws->bar;
+            a.hbuf = (float *)ws.buf;
+            a.bar = ws.bar;
             a.err = ds->err;
             a.sb = sb;
             a.rpc = (int)((H + grid - 1) / grid);
@@ -1157,7 +1261,7 @@ static int moe_run(const MoeInfo &mi, const ExpertDesc *table, DeviceState *ds, 
             cudaError_t e = moe_decode_occupancy(fmt, smem, &per_sm);
             if (e != cudaSuccess) return cuda_fail(e, "decode occupancy");
             if (per_sm >= 1) {
-                Workspace *ws = nullptr;
+                Scratch ws;
                 if (int rc = workspace(ds, st, (size_t)n_slots * F * sizeof(float), &ws)) return rc;
                 const int grid = per_sm * ds->n_sm;
                 MoeDecodeArgs a;
@@ -1174,8 +1278,8 @@ static int moe_run(const MoeInfo &mi, const ExpertDesc *table, DeviceState *ds, 
                 a.F = (int)F;
                 a.cpr_gu = cpr_gu;
                 a.cpr_d = cpr_d;
-                a.hbuf = (float *)ws->buf;
-                a.bar = ws->bar;
+                a.hbuf = (float *)ws.buf;
+                a.bar = ws.bar;
                 a.err = ds->err;
                 a.sb = sb;
                 a.rpc = (int)((H + grid - 1) / grid);
@@ -1211,9 +1315,9 @@ static int moe_run(const MoeInfo &mi, const ExpertDesc *table, DeviceState *ds, 
         const size_t sz_sg = al((size_t)n_slots * 4);
         const size_t total =
             sz_off + 2 * sz_ord + 3 * sz_tile + 256 + sz_px + sz_gu + sz_ph + sz_out + 3 * sz_sg + al(n_slots);
-        Workspace *ws = nullptr;
+        Scratch ws;
         if (int rc = workspace(ds, st, total, &ws)) return rc;
-        char *p = (char *)ws->buf;
+        char *p = (char *)ws.buf;
         int32_t *offsets = (int32_t *)p; p += sz_off;
         int32_t *order = (int32_t *)p; p += sz_ord;
         int32_t *inv = (int32_t *)p; p += sz_ord;
@@ -1323,9 +1427,9 @@ static int moe_run(const MoeInfo &mi, const ExpertDesc *table, DeviceState *ds, 
     const size_t sz_tile = al((size_t)max_tiles * 4), sz_h = al((size_t)n_slots * F * 4);
     const size_t sz_out = al((size_t)n_slots * H * 4);
     const size_t total = sz_off + 2 * sz_ord + 3 * sz_tile + 256 + sz_h + sz_out;
-    Workspace *ws = nullptr;
+    Scratch ws;
     if (int rc = workspace(ds, st, total, &ws)) return rc;
-    char *p = (char *)ws->buf;
+    char *p = (char *)ws.buf;
     int32_t *offsets = (int32_t *)p; p += sz_off;
     int32_t *order = (int32_t *)p; p += sz_ord;
     int32_t *inv = (int32_t *)p; p += sz_ord;
@@ -1406,7 +1510,7 @@ int coli_sync_check(void *stream) {
     if (word == DEV_ERR_TIMEOUT) {
         std::lock_guard<std::mutex> lk(ds->mu);
         for (auto &kv : ds->ws)
-            if (kv.second.bar) cudaMemset(kv.second.bar, 0, kBarrierBytes);
+            if (kv.second.bar) cudaMemset(kv.second.bar->p, 0, kBarrierBytes);
         return fail(COLI_ETIMEOUT, "a bounded device-side wait ran out of time");
     }
     if (word == DEV_ERR_BAD_ID) return fail(COLI_EINVAL, "a routing id was outside [-1, n_experts)");

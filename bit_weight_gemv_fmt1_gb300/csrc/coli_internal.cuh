@@ -24,6 +24,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <memory>
 #include <utility>
 
 #include "coli.h"
@@ -792,6 +793,7 @@ struct DevInfo {
     long long wait_ns;        // bound of the device-side waits (see deadline_after)
     void *scratch;
     void *state;              // the library's own
+    std::shared_ptr<void> hold;   // keeps the scratch until the call has launched its kernels
 };
 int device_info(DevInfo *out);
 int device_scratch(DevInfo *d, cudaStream_t st, size_t bytes);

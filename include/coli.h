@@ -61,6 +61,16 @@
  *     wait that ran out) are reported by the next coli_sync_check(stream).
  *   - Each device has its own library state; tensors live on the device that
  *     was current at upload and must be used with that device current.
+ *   - Some calls use scratch that the library keeps for their stream; it grows when a
+ *     larger call comes, which then waits for the stream.  Calls on one stream are made
+ *     by one host thread at a time.
+ *   - Calls may be captured into a CUDA graph, the first ones too.  A captured call's
+ *     scratch belongs to the graph and is freed after it: the graph can be replayed on
+ *     any stream, whatever is called in the meantime, beside other graphs and calls.
+ *     Two restrictions: what is made from one graph (a clone, a second instance) shares
+ *     its scratch and must not run at the same time; and the decode expert block and the
+ *     S <= 8 products use counters of the stream they were captured on, so that graphs
+ *     with those must not run at the same time as others, or calls, of that stream.
  */
 #ifndef COLI_H
 #define COLI_H
