@@ -174,7 +174,7 @@ int attend(const coli_mla_cache *cache, int dtype_q, const void *q_latent, const
     if ((int64_t)n_seq * n_q * H > (1LL << 31) - 1) return bad(COLI_EINVAL, "n_seq * n_q * n_heads is too large");
     if (pages_stride < 1 || pages_stride > (1LL << 31) - 1)
         return bad(COLI_EINVAL, "pages_stride must be in 1..2^31-1 (got %lld)", (long long)pages_stride);
-    if ((pages_stride * a.c.page / 128 + 1) * n_seq > (1LL << 31) - 1)
+    if (n_seq && pages_stride * a.c.page / 128 + 1 > ((1LL << 31) - 1) / n_seq)   // a product would pass 2^63
         return bad(COLI_EINVAL, "n_seq * pages_stride * page_size is too large");
     if (!(scale == scale)) return bad(COLI_EINVAL, "scale must not be NaN");
     if (n_seq) {
