@@ -40,14 +40,13 @@
 
 #include <algorithm>
 
-#include "mla.cuh"
+#include "mla_units.cuh"
 #include "tcgen05.cuh"
 
 namespace coli {
 
 namespace {
 
-constexpr int kRows = 128;               // rows of a query or key tile
 constexpr uint32_t kBlk = kRows * 128;   // 128 rows x 64 bf16, 128-byte swizzle
 constexpr float kGrow = 8.f;             // log2 of the weight that moves the reference
 constexpr float kNone = -3e38f;          // reference of a row that has seen no key
@@ -57,12 +56,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-
-// One unit of work: a head's pair of query tiles.
-struct Unit {
-    int head, q0, nq, nk, qrow, krow;    // first query of the pair in its sequence, the sequence's sizes and first rows
-    int nt[2], n;                        // key tiles that each query tile sees, the larger of them; n < 0: no more units
-};
 
 struct Shared {
     uint64_t q_full[2], q_empty[2], k_full[5], k_empty[5], v_full[3], v_empty[3], s_full[2], p_full[2], o_full[2], u_full[2], u_empty[2];
@@ -85,115 +78,6 @@ struct Ring {
         }
     }
 };
-
-// Sequence b's offsets (all 0 where they are bad) and its number of pairs.
-__device__ __forceinline__ int pairs_of(const MlaPrefillArgs &a, int b, bool report, int4 &c) {
-    c = make_int4(0, 0, 0, 0);
-    if (b >= a.n_seq) return 0;
-    const int4 d = make_int4(a.cu_q[b], a.cu_q[b + 1], a.cu_k[b], a.cu_k[b + 1]);
-    const bool good = d.x >= 0 && d.y >= d.x && d.y <= a.Tq && d.z >= 0 && d.w >= d.z && d.w <= a.Tk;
-    if (report && !good) mla_bad_index(a.err);
-    if (good) c = d;
-    return (c.y - c.x + 2 * kRows - 1) / (2 * kRows);
-}
-// How many of a sequence's n pairs see v key tiles or more: the last pair sees all nk keys, each one before it 256
-// fewer rows' worth.
-__device__ __forceinline__ int pairs_with(int n, int4 c, int v) {
-    if (v <= 0) return n;
-    const int spare = c.w - c.z - ((v - 1) * kRows + 1);   // rows that may lie behind the pair's last
-    if (spare < 0) return 0;
-    const int need = max(1, (c.y - c.x - spare + 2 * kRows - 1) / (2 * kRows));
-    return min(n, max(0, n - need + 1));
-}
-// Whole warp: the pairs of all sequences, and the most key tiles that one sees.
-__device__ __forceinline__ int all_pairs(const MlaPrefillArgs &a, int lane, bool report, int &most) {
-    int total = 0;
-    most = 0;
-    for (int b = lane; b < a.n_seq; b += 32) {
-        int4 c;
-        total += pairs_of(a, b, report, c);
-        most = max(most, (c.w - c.z + kRows - 1) / kRows);
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    return __reduce_add_sync(0xffffffffu, total);
-}
-// How far a CTA has come in the order of units: the pairs that see v tiles have the numbers below..upto - 1, and those
-// of sequences before b0 end at run.  A CTA's units rise, so most of them are found from here in one look at 32
-// sequences (512 sequences of up to 200 rows x 16 heads: 333 us, with a search from the start each time 853; 8192 x 32 heads,
-// which needs none of it, 459 against 452, or 472 with the count unrolled at five places: it is one loop for its size).
-struct Place {
-    int v, below, upto, b0, run;
-};
-// Whole warp: unit i, in the order of key tiles, most first, all heads of a pair together.
-__device__ __forceinline__ Unit unit_of(const MlaPrefillArgs &a, int i, int pairs, Place &at, int lane) {
-    Unit u;
-    const int p = i / a.H;
-    u.head = i - p * a.H;
-    if (p >= at.upto) {
-        // count(lo) > p >= count(hi), the pairs that see so many tiles or more; first the next number of tiles, then halves
-        int lo = 0, hi = at.v, above = pairs, below = at.upto, v = hi - 1;
-        while (hi - lo > 1) {
-            int t = 0;
-#pragma unroll 2
-            for (int b = lane; b < a.n_seq; b += 32) {
-                int4 c;
-                const int n = pairs_of(a, b, false, c);
-                t += pairs_with(n, c, v);
-            }
-            t = __reduce_add_sync(0xffffffffu, t);
-            if (t > p) {
-                lo = v;
-                above = t;
-            } else {
-                hi = v;
-                below = t;
-            }
-            v = (lo + hi) / 2;
-        }
-        at.v = lo;
-        at.below = below;
-        at.upto = above;
-        at.b0 = 0;
-        at.run = below;
-    }
-    const int v = at.v;
-    int run = at.run;
-    u.q0 = u.nq = u.nk = u.qrow = u.krow = 0;
-    for (int b0 = at.b0; b0 < a.n_seq; b0 += 32) {
-        int4 c;
-        const int n = pairs_of(a, b0 + lane, false, c);
-        const int above = pairs_with(n, c, v + 1), here = pairs_with(n, c, v) - above;
-        int incl = here;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int w = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += w;
-        }
-        const int before = run + incl - here;
-        const uint32_t hit = __ballot_sync(0xffffffffu, before <= p && p < before + here);
-        if (hit) {
-            at.b0 = b0;
-            at.run = run;
-            const int src = __ffs(hit) - 1;
-            u.q0 = __shfl_sync(0xffffffffu, (n - 1 - above - (p - before)) * 2 * kRows, src);
-            u.qrow = __shfl_sync(0xffffffffu, c.x, src);
-            u.nq = __shfl_sync(0xffffffffu, c.y, src) - u.qrow;
-            u.krow = __shfl_sync(0xffffffffu, c.z, src);
-            u.nk = __shfl_sync(0xffffffffu, c.w, src) - u.krow;
-            break;
-        }
-        run += __shfl_sync(0xffffffffu, incl, 31);
-    }
-#pragma unroll
-    for (int x = 0; x < 2; x++) {
-        // the last live row's limit
-        const int rows = min(kRows, u.nq - u.q0 - x * kRows);
-        const int limit = rows > 0 ? u.q0 + x * kRows + rows + u.nk - u.nq : 0;
-        u.nt[x] = limit > 0 ? (min(limit, u.nk) + kRows - 1) / kRows : 0;
-    }
-    u.n = max(u.nt[0], u.nt[1]);
-    return u;
-}
 
 // The same values, all from lane 0: the compiler then keeps them, and the operands of MMAs and copies that derive from
 // them, in uniform registers.
@@ -506,7 +390,7 @@ __global__ void __launch_bounds__(384, 1)
         int most, blocks = 0, i = blockIdx.x, asked = 0;
         Ring c{0, 0};
         const int pairs = all_pairs(a, lane, blockIdx.x == 0, most), units = pairs * a.H;
-        Place at{most + 1, 0, 0, 0, 0};
+        Place at = no_place(most);
         for (int r = 0;; r++) {
             Unit u;
             u.n = -1;
