@@ -105,11 +105,19 @@ _torch = None
 _raw_stream = None
 
 
+def _device() -> int:
+    """The current device, on which the library launches and all of a call's tensors have to be."""
+    _load_torch()
+    return _device()
+
+
 def _load_torch():
     """torch, imported at first use (uploads and the host calls do without it)."""
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _device
     import torch
     _torch = torch
+    # without torch.cuda's look at whether CUDA is initialised, which a call's CUDA tensors have seen to
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     # the handle of the current stream without building a Stream object (3 us a call), where torch has it
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -124,6 +132,8 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
 
 
 def _ptr(t):
@@ -316,27 +326,37 @@ def _dtype(t) -> int:
     return d
 
 
-def _packed(t, kind, name: str) -> int:
-    """Address of t, a contiguous CUDA tensor of torch type `kind`."""
-    if t.dtype is not kind or not t.is_cuda or not t.is_contiguous():
+def _elsewhere(t, dev: int, name: str):
+    if not t.is_cuda:
+        _refuse(f"{name} must be a CUDA tensor")
+    raise ColiError(COLI_EDEVICE, f"{name} lives on device {t.get_device()} but device {dev} is current")
+
+
+def _packed(t, kind, dev: int, name: str) -> int:
+    """Address of t, a contiguous tensor of torch type `kind` on device dev."""
+    if t.get_device() != dev:
+        _elsewhere(t, dev, name)
+    if t.dtype is not kind or not t.is_contiguous():
         _refuse(f"{name} must be a contiguous {kind} CUDA tensor")
     return t.data_ptr()
 
 
-def _rows3(t, name: str) -> int:
+def _rows3(t, dev: int, name: str) -> int:
     """Stride of the rows of t [T, heads, n]: rows of one stride over tokens and heads, elements packed."""
+    if t.get_device() != dev:
+        _elsewhere(t, dev, name)
     T, H, n = t.shape
     s0, s1, s2 = t.stride()
     ld = s1 if H > 1 else s0 if T > 1 else n
-    if not t.is_cuda or (n > 1 and s2 != 1) or (T > 1 and s0 != H * ld):
+    if (n > 1 and s2 != 1) or (T > 1 and s0 != H * ld):
         _refuse(f"{name} must be a CUDA tensor whose [tokens, heads] rows have one stride")
     return ld
 
 
-def _tokens(t, name: str) -> int:
+def _tokens(t, dev: int, name: str) -> int:
     """Token stride of t [T, ...] whose tokens are packed."""
-    if not t.is_cuda:
-        _refuse(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        _elsewhere(t, dev, name)
     shape, stride, n = t.shape, t.stride(), 1
     for i in range(len(shape) - 1, 0, -1):
         if stride[i] != n and shape[i] != 1:
@@ -345,9 +365,11 @@ def _tokens(t, name: str) -> int:
     return stride[0] if shape[0] > 1 else n
 
 
-def _pages(pages, n_seq: int) -> int:
+def _pages(pages, n_seq: int, dev: int) -> int:
     n, width = pages.shape
-    if pages.dtype is not _torch.int32 or not pages.is_cuda or n != n_seq or (width > 1 and pages.stride(1) != 1):
+    if pages.get_device() != dev:
+        _elsewhere(pages, dev, "pages")
+    if pages.dtype is not _torch.int32 or n != n_seq or (width > 1 and pages.stride(1) != 1):
         _refuse("pages must be an int32 CUDA tensor [n_seq, n] with packed rows")
     return pages.stride(0) if n > 1 else width
 
@@ -364,19 +386,21 @@ class MlaCache:
         if d == COLI_E4M3:
             if scales is None or scales.shape != rows.shape[:2]:
                 _refuse("an e4m3 cache needs scales [n_pages, page_size]")
-            _packed(scales, _torch.float32, "scales")
+            _packed(scales, _torch.float32, rows.get_device(), "scales")
         elif scales is not None:
             _refuse("only an e4m3 cache has scales")
-        self.rows, self.scales = rows, scales
+        self.rows, self.scales, self.device = rows, scales, rows.get_device()
         self.latent, self.rope, self.page_size, self.n_pages = int(latent), int(rope), rows.shape[1], rows.shape[0]
         self._c = _MlaCache(d, self.latent, self.rope, self.page_size, self.n_pages, rows.data_ptr(), _ptr(scales))
         self._p = ctypes.addressof(self._c)
+
 
 
 def mla_query(q, pos, rot, out_nope, out_rope, interleaved: bool = False, stream=None):
     """Split q [T, heads, nope + rope] into out_nope [T, heads, nope] and the rotated out_rope [T, heads, rope]
     (f32 or bf16 each, possibly two parts of one tensor; out_nope None: nope = 0).  rot [n_pos, rope] = cos | sin."""
     torch = _torch or _load_torch()
+    dev = _device()
     T, H, n = q.shape
     T2, H2, R = out_rope.shape
     n_pos, R2 = rot.shape
@@ -387,10 +411,10 @@ def mla_query(q, pos, rot, out_nope, out_rope, interleaved: bool = False, stream
     if out_nope is None:
         dn = pn = ln = 0
     else:
-        dn, pn, ln = _dtype(out_nope), out_nope.data_ptr(), _rows3(out_nope, "out_nope")
-    rc = _lib.coli_mla_query(q.data_ptr(), _tokens(q, "q"), T, H, N, R, _packed(pos, torch.int32, "pos"),
-                             _packed(rot, torch.float32, "rot"), n_pos, interleaved, dn, pn, ln, _dtype(out_rope),
-                             out_rope.data_ptr(), _rows3(out_rope, "out_rope"), _stream(stream))
+        dn, pn, ln = _dtype(out_nope), out_nope.data_ptr(), _rows3(out_nope, dev, "out_nope")
+    rc = _lib.coli_mla_query(q.data_ptr(), _tokens(q, dev, "q"), T, H, N, R, _packed(pos, torch.int32, dev, "pos"),
+                             _packed(rot, torch.float32, dev, "rot"), n_pos, interleaved, dn, pn, ln, _dtype(out_rope),
+                             out_rope.data_ptr(), _rows3(out_rope, dev, "out_rope"), _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc)
     return out_nope, out_rope
@@ -399,15 +423,18 @@ def mla_query(q, pos, rot, out_nope, out_rope, interleaved: bool = False, stream
 def mla_append(cache: MlaCache, kv, norm, eps: float, pos, rot, slots, interleaved: bool = False, stream=None):
     """Norm (norm None: none), rotate, quantise and store kv [T, latent + rope] at slots [T] of the cache."""
     torch = _torch or _load_torch()
+    dev = _device()
+    if cache.device != dev:
+        _elsewhere(cache.rows, dev, "the cache")
     T, n = kv.shape
     n_pos, R = rot.shape
     if kv.dtype is not torch.float32 or n != cache.latent + R or R != cache.rope or pos.shape[0] != T or \
             slots.shape[0] != T or (norm is not None and norm.shape[0] != cache.latent):
         _refuse("mla_append: kv must be float32 [T, latent + rope] and the others must match it and the cache")
-    rc = _lib.coli_mla_append(cache._p, kv.data_ptr(), _tokens(kv, "kv"), T,
-                              None if norm is None else _packed(norm, torch.float32, "norm"), eps,
-                              _packed(pos, torch.int32, "pos"), _packed(rot, torch.float32, "rot"), n_pos, interleaved,
-                              _packed(slots, torch.int64, "slots"), _stream(stream))
+    rc = _lib.coli_mla_append(cache._p, kv.data_ptr(), _tokens(kv, dev, "kv"), T,
+                              None if norm is None else _packed(norm, torch.float32, dev, "norm"), eps,
+                              _packed(pos, torch.int32, dev, "pos"), _packed(rot, torch.float32, dev, "rot"), n_pos, interleaved,
+                              _packed(slots, torch.int64, dev, "slots"), _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc)
 
@@ -415,12 +442,15 @@ def mla_append(cache: MlaCache, kv, norm, eps: float, pos, rot, slots, interleav
 def mla_read(cache: MlaCache, pages, cu, out, stream=None):
     """Read the first cu[b+1] - cu[b] tokens of each sequence b back into out [T, latent + rope] (f32 or bf16)."""
     torch = _torch or _load_torch()
+    dev = _device()
+    if cache.device != dev:
+        _elsewhere(cache.rows, dev, "the cache")
     n_seq = cu.shape[0] - 1
     T, n = out.shape
     if n != cache.latent + cache.rope:
         _refuse("mla_read: out must have latent + rope columns")
-    rc = _lib.coli_mla_read(cache._p, pages.data_ptr(), _pages(pages, n_seq), n_seq, _packed(cu, torch.int32, "cu"), T,
-                            _dtype(out), out.data_ptr(), _tokens(out, "out"), _stream(stream))
+    rc = _lib.coli_mla_read(cache._p, pages.data_ptr(), _pages(pages, n_seq, dev), n_seq, _packed(cu, torch.int32, dev, "cu"), T,
+                            _dtype(out), out.data_ptr(), _tokens(out, dev, "out"), _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc)
     return out
@@ -430,15 +460,18 @@ def mla_attend(cache: MlaCache, q_latent, q_rope, pages, lens, scale: float, out
     """Absorbed attention of q_latent [n_seq, n_q, heads, latent] and q_rope [n_seq, n_q, heads, rope] over the cached
     tokens (lens [n_seq] int32, the new ones included) into out [n_seq, n_q, heads, latent]; lse f32 [n_seq, n_q, heads]."""
     torch = _torch or _load_torch()
+    dev = _device()
+    if cache.device != dev:
+        _elsewhere(cache.rows, dev, "the cache")
     B, n_q, H, n = q_latent.shape
     kind = q_latent.dtype
     if n != cache.latent or q_rope.shape != (B, n_q, H, cache.rope) or out.shape != q_latent.shape or \
             lens.shape[0] != B or (lse is not None and lse.shape != (B, n_q, H)):
         _refuse("mla_attend: q_latent, q_rope, lens, out and lse must match one another and the cache")
-    rc = _lib.coli_mla_attend(cache._p, _dtype(q_latent), _packed(q_latent, kind, "q_latent"), _packed(q_rope, kind, "q_rope"),
-                              B, n_q, H, pages.data_ptr(), _pages(pages, B), _packed(lens, torch.int32, "lens"), scale,
-                              _dtype(out), _packed(out, out.dtype, "out"),
-                              None if lse is None else _packed(lse, torch.float32, "lse"), _stream(stream))
+    rc = _lib.coli_mla_attend(cache._p, _dtype(q_latent), _packed(q_latent, kind, dev, "q_latent"), _packed(q_rope, kind, dev, "q_rope"),
+                              B, n_q, H, pages.data_ptr(), _pages(pages, B, dev), _packed(lens, torch.int32, dev, "lens"), scale,
+                              _dtype(out), _packed(out, out.dtype, dev, "out"),
+                              None if lse is None else _packed(lse, torch.float32, dev, "lse"), _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc)
     return out
@@ -448,6 +481,7 @@ def mla_prefill(q, kv, k_rope, cu_q, cu_k, scale: float, out, lse=None, stream=N
     """Causal attention of packed sequences: q [Tq, heads, nope + rope], kv [Tk, heads, nope + v], k_rope [Tk, rope]
     (all bf16 or all f32) into out [Tq, heads, v]; cu_q, cu_k int32 [n_seq + 1]; lse f32 [Tq, heads]."""
     torch = _torch or _load_torch()
+    dev = _device()
     Tq, H, dk = q.shape
     Tk, R = k_rope.shape
     V = out.shape[2]
@@ -455,11 +489,11 @@ def mla_prefill(q, kv, k_rope, cu_q, cu_k, scale: float, out, lse=None, stream=N
     if kv.shape != (Tk, H, N + V) or out.shape != (Tq, H, V) or cu_q.shape != cu_k.shape or kv.dtype is not q.dtype or \
             k_rope.dtype is not q.dtype or (lse is not None and lse.shape != (Tq, H)):
         _refuse("mla_prefill: q, kv, k_rope, cu_q, cu_k, out and lse must match one another")
-    rc = _lib.coli_mla_prefill(_dtype(q), q.data_ptr(), _tokens(q, "q"), kv.data_ptr(), _tokens(kv, "kv"), k_rope.data_ptr(),
-                               _tokens(k_rope, "k_rope"), Tq, Tk, cu_q.shape[0] - 1, _packed(cu_q, torch.int32, "cu_q"),
-                               _packed(cu_k, torch.int32, "cu_k"), H, N, R, V, scale, _dtype(out),
-                               _packed(out, out.dtype, "out"), None if lse is None else _packed(lse, torch.float32, "lse"),
-                               _stream(stream))
+    rc = _lib.coli_mla_prefill(_dtype(q), q.data_ptr(), _tokens(q, dev, "q"), kv.data_ptr(), _tokens(kv, dev, "kv"), k_rope.data_ptr(),
+                               _tokens(k_rope, dev, "k_rope"), Tq, Tk, cu_q.shape[0] - 1, _packed(cu_q, torch.int32, dev, "cu_q"),
+                               _packed(cu_k, torch.int32, dev, "cu_k"), H, N, R, V, scale, _dtype(out),
+                               _packed(out, out.dtype, dev, "out"), None if lse is None else _packed(lse, torch.float32, dev, "lse"),
+                               _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc)
     return out

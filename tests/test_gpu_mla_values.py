@@ -199,3 +199,30 @@ def test_tokens_that_some_queries_do_not_see(e4m3, value, n_q, n):
     check(torch, c, table, [n, 70], ql, qr, 0.06, out, ls, lambda b, j: range(H) if b == 0 and j == n_q - 1 else ())
     if value != value or e4m3:
         assert torch.isnan(out[0, n_q - 1]).all()
+
+
+def test_tensors_of_another_device(monkeypatch):
+    """The library launches on the current device: tensors of another one are refused before that, with COLI_EDEVICE."""
+    torch, coli = setup()
+    c = new_cache(torch, coli, True, 512, 64, 64, 3)
+    z = lambda *s, **k: torch.zeros(*s, device="cuda", **k)  # noqa: E731
+    q, rot, pos, pages, lens = z(2, 4, 192), rotation(torch, 8, 64).cuda(), z(2, dtype=torch.int32), z(2, 1, dtype=torch.int32), z(2, dtype=torch.int32)
+    on, orr, cu = z(2, 4, 128), z(2, 4, 64), z(2, dtype=torch.int32)
+    ql, qr = z(2, 1, 4, 512), z(2, 1, 4, 64)
+    calls = [lambda: coli.mla_query(q, pos, rot, on, orr), lambda: coli.mla_append(c, z(2, 576), None, 1.0, pos, rot, pos.long()),
+             lambda: coli.mla_read(c, pages[:1], cu, z(2, 576)), lambda: coli.mla_attend(c, ql, qr, pages, lens, 1.0, ql.clone()),
+             lambda: coli.mla_prefill(q, z(2, 4, 256), orr[:, 0], cu, cu, 1.0, on)]
+    for f in calls:
+        f()
+    coli.sync_check()
+    monkeypatch.setattr(coli, "_device", lambda: 1, raising=False)
+    for f in calls:
+        with pytest.raises(coli.ColiError) as e:
+            f()
+        assert e.value.code == coli.COLI_EDEVICE
+    monkeypatch.undo()
+    host = lambda t: pytest.raises(coli.ColiError, match="CUDA tensor")  # noqa: E731
+    with host(pos):
+        coli.mla_query(q, pos.cpu(), rot, on, orr)
+    with host(pages):
+        coli.mla_read(c, pages[:1].cpu(), cu, z(2, 576))
