@@ -5,7 +5,7 @@
 //
 // The tensor cores multiply 8-bit floats exactly into f32.  What faces the codes
 // is split into 8-bit terms:
-//   q  (times a power of two per row)  = q0 + 2^-5 q1             E4M3 (a bf16 value exactly)
+//   q  (times a power of two per row)  = q0 + 2^-5 q1             E4M3 (8 bits, but no finer than 2^-22 of the row's largest)
 //   P  = weight * row scale            = p0 + 2^-3 p1 + 2^-7 p2   E5M2 (to 2^-11, as f16 has it)
 // P's terms are E5M2 for its range: the reference starts 6 below the first tile's maximum and
 // weights may grow by 2^8 before it has to move, while those down to 2^-18 of the

@@ -413,7 +413,7 @@ typedef struct {
  * f32 outputs are exact copies / one rounding per operation; bf16 rounds to nearest.
  * f32 outputs may be q itself, part by part (in place).
  * All pointers 16-byte aligned, strides multiples of 8 elements.  T >= 0.  A
- * position out of range is recorded for coli_sync_check and its rows are zero.
+ * position out of range is recorded for coli_sync_check and its rows of out_rope are zero.
  * Errors: COLI_EINVAL, COLI_EFMT (a dtype), COLI_ECUDA, COLI_EINJECTED.
  */
 int coli_mla_query(const float *q, int64_t q_stride, int T, int n_heads, int nope, int rope,
@@ -448,7 +448,8 @@ int coli_mla_append(const coli_mla_cache *cache, const float *kv, int64_t kv_str
  * expand a cached prefix with kv_b): out row cu[b] + i = token i of sequence b,
  * i < cu[b+1] - cu[b].
  *   pages   device int32, sequence b's page ids at pages + b * pages_stride
- *           (pages_stride >= 1 entries; only those its tokens need are read).
+ *           (pages_stride >= 1 entries; only those its tokens need are read, and only
+ *           pages_stride bounds them: shorter lists in wider rows are the caller's care).
  *   cu      device int32 [n_seq + 1], cu[0] = 0, ascending; rows >= cu[n_seq] are left alone.
  *   T       rows of out, >= 0.
  *   dtype   COLI_F32 (exact) or COLI_BF16 (rounded to nearest); out_stride in
@@ -475,11 +476,14 @@ int coli_mla_read(const coli_mla_cache *cache, const int32_t *pages, int64_t pag
  *   lse       device f32 [n_seq][n_q][n_heads], or NULL.
  * The products take operands of the cache's kind: for a COLI_BF16 cache q and
  * the probabilities are rounded to bf16; for a COLI_E4M3 one q becomes two E4M3
- * terms (scaled by a power of two per query row; a bf16 value exactly, others
- * to 2^-8 of them) and the probabilities three E5M2 ones (to 2^-11).  Sums,
- * maxima and the softmax's denominator are f32.  Rows past a sequence's length, and pages
- * past its last, are never used: they may hold anything.  A NaN in a query, or in a row
- * that a query sees, makes its output and lse NaN; a row that it does not see leaves it alone.
+ * terms, scaled by a power of two per query row, and the probabilities three E5M2
+ * ones (to 2^-11).  The terms of a query row whose largest magnitude is m (latent and
+ * rope part together) hold a bf16 element exactly down to 2^-14 m and an f32 one to
+ * 2^-8 of it; below that an element is off by up to 2^-22 m.  Sums, maxima and the
+ * softmax's denominator are f32.
+ * Rows past a sequence's length, and pages past its last, are never used: they may hold
+ * anything.  A NaN or an infinity in a query, or a NaN in a row that a query sees, makes
+ * its output and lse NaN; a row that it does not see leaves it alone.
  * Pointers 16-byte aligned (pages, lens, lse: 4).  n_seq >= 0, n_q >= 1, 1 <= n_heads <= 1024,
  * n_q * n_heads <= 65536.  A page id outside [0, n_pages) among the needed ones, or a length out
  * of range, is recorded for coli_sync_check; that sequence's output is unspecified.

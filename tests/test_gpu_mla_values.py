@@ -226,3 +226,45 @@ def test_tensors_of_another_device(monkeypatch):
         coli.mla_query(q, pos.cpu(), rot, on, orr)
     with host(pages):
         coli.mla_read(c, pages[:1].cpu(), cu, z(2, 576))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_more_query_rows_than_the_device_has_columns(e4m3, bf16):
+    """12800 query rows a sequence: every CTA takes several blocks of rows, each over all sequences."""
+    torch, coli = setup()
+    g = gen(torch, 6)
+    lens, L, R = [150, 300], 128, 16
+    c, table = filled(torch, coli, e4m3, L, R, 16, lens, g)
+    ql, qr = queries(torch, g, 2, 100, 128, L, R, bf16)
+    out, ls = attend(torch, coli, c, table, lens, ql, qr, 0.08, out_bf16=bf16)
+    check(torch, c, table, lens, ql, qr, 0.08, out, ls)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("latent,rope", [(1.0, 1.0), (1.0, 1e-3), (1.0, 1e-5), (1e-3, 1.0), (1e-5, 1.0), (3e4, 1e-30), (1e-30, 1e-30)])
+def test_query_magnitudes(e4m3, bf16, latent, rope):
+    """Parts of a query that differ by orders of magnitude."""
+    torch, coli = setup()
+    g = gen(torch, 7)
+    lens, L, R, H = [700, 33], 512, 64, 20
+    c, table = filled(torch, coli, e4m3, L, R, 64, lens, g)
+    ql, qr = queries(torch, g, 2, 1, H, L, R, False)
+    t = torch.bfloat16 if bf16 else torch.float32
+    ql, qr = (ql * latent).to(t), (qr * rope).to(t)
+    scale = 0.07 / max(1.0, latent)
+    out, ls = attend(torch, coli, c, table, lens, ql, qr, scale)
+    check(torch, c, table, lens, ql, qr, scale, out, ls)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_tables_wider_than_the_lengths(e4m3):
+    """Tables as wide as the longest context that a server allows, short sequences on them, more of them than SMs."""
+    torch, coli = setup()
+    g = gen(torch, 8)
+    lens = [(37 * i) % 300 for i in range(200)]
+    c, table = filled(torch, coli, e4m3, 256, 32, 64, lens, g, columns=4000)
+    ql, qr = queries(torch, g, 200, 1, 16, 256, 32, True)
+    out, ls = attend(torch, coli, c, table, lens, ql, qr, 0.06)
+    check(torch, c, table, lens, ql, qr, 0.06, out, ls)
