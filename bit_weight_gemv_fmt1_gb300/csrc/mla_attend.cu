@@ -216,25 +216,26 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attend_bf16_kernel(const __gr
                 // 0 * NaN is NaN.  Rows past the length may hold anything: zero.  Of the newest tokens' rows, which not every
                 // query sees, what is not finite: the queries that see it have it in their scores.  Every score of such a row
                 // is not finite, so one tells (looking at the rows of 4 x 9000 tokens, 3 queries each, costs 1.1 of 29 us).
-                bool clear = tok >= w.len;
+                bool clear = false;
                 if (a.n_q > 1) {
                     uint32_t v[8];
                     tmem_ld(lanes + col0, v);
                     tmem_ld_wait();
-                    clear = clear || (tok > w.len - a.n_q && !finite_bits(v[0]));
+                    clear = tok > w.len - a.n_q && !finite_bits(v[0]);
                 }
-                if (clear)
+                if (tok >= w.len) {
                     for (int k = grp; k < 2 * npair; k += 2)
 #pragma unroll
-                        for (int u = 0; u < 8; u++) {
-                            uint4 *at = reinterpret_cast<uint4 *>(sm + k * kBlk + t * 128 + 16 * u);
-                            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                            if (tok < w.len) {
-                                x = *at;
-                                for (uint32_t *e : {&x.x, &x.y, &x.z, &x.w}) *e &= ~__vcmpeq2(*e & 0x7F807F80u, 0x7F807F80u);
-                            }
-                            *at = x;
-                        }
+                        for (int u = 0; u < 8; u++) *reinterpret_cast<uint4 *>(sm + k * kBlk + t * 128 + 16 * u) = make_uint4(0u, 0u, 0u, 0u);
+                } else if (clear) {
+#pragma unroll 1
+                    for (int i = 0; i < 8 * npair; i++) {
+                        uint4 *at = reinterpret_cast<uint4 *>(sm + (grp + 2 * (i >> 3)) * kBlk + t * 128 + 16 * (i & 7));
+                        uint4 x = *at;
+                        for (uint32_t *e : {&x.x, &x.y, &x.z, &x.w}) *e &= ~__vcmpeq2(*e & 0x7F807F80u, 0x7F807F80u);
+                        *at = x;
+                    }
+                }
             }
             // Columns in chunks: a thread's 32 scores and 32 sums at once would not fit its registers.
             constexpr int CH = NC < 16 ? NC : 16;

@@ -274,25 +274,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((w.tile() + 1) * kTile > w.len - a.n_q + 1) {
                 // Likewise the codes.  Rows past the length may hold anything: zero.  Of the newest tokens' rows, which not
                 // every query sees, the NaN: the queries that see it have it in their scores, so one score tells.
-                bool clear = tok >= w.len;
+                bool clear = false;
                 if (a.n_q > 1) {
                     uint32_t v[8];
                     tmem_ld(lanes + buf * (2 * NH) + col0, v);
                     tmem_ld_wait();
-                    clear = clear || (tok > w.len - a.n_q && !finite_bits(v[0]));
+                    clear = tok > w.len - a.n_q && !finite_bits(v[0]);
                 }
-                if (clear)
+                if (tok >= w.len) {
                     for (int k = grp; k < np; k += 2)
 #pragma unroll
-                        for (int u = 0; u < 8; u++) {
-                            uint4 *at = reinterpret_cast<uint4 *>(sm + buf * stage + k * kBlk8 + t * 128 + 16 * u);
-                            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                            if (tok < w.len) {
-                                x = *at;
-                                for (uint32_t *e : {&x.x, &x.y, &x.z, &x.w}) *e &= ~__vcmpeq4(*e & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                            }
-                            *at = x;
-                        }
+                        for (int u = 0; u < 8; u++) *reinterpret_cast<uint4 *>(sm + buf * stage + k * kBlk8 + t * 128 + 16 * u) = make_uint4(0u, 0u, 0u, 0u);
+                } else if (clear) {
+#pragma unroll 1
+                    for (int i = 0; grp + 2 * (i >> 3) < np; i++) {
+                        uint4 *at = reinterpret_cast<uint4 *>(sm + buf * stage + (grp + 2 * (i >> 3)) * kBlk8 + t * 128 + 16 * (i & 7));
+                        uint4 x = *at;
+                        for (uint32_t *e : {&x.x, &x.y, &x.z, &x.w}) *e &= ~__vcmpeq4(*e & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                        *at = x;
+                    }
+                }
             }
             // log2 of the row's scale; the floor gives rows of scale 0, which weigh in l alone, a reference too
             const float lg = fmaxf(__log2f(st), kFloor8);
