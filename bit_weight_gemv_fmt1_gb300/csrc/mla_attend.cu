@@ -30,14 +30,15 @@
 // each, but O would fill TMEM and leave no room for S).  One tile is in shared memory at a time (147 KB beside 74 KB of
 // queries), so its scores (2000 cycles), softmax (1240) and outputs (1760) follow one another, 5500 cycles a tile with the
 // hand-overs; the copies are hidden, each block of 64 dims being asked for again when its last product is done.
-// Measured: 48 sequences of up to 12000 tokens (320000 in all), 128 heads: 134 us, 0.66 PFLOP/s, 2.8 TB/s of the cache; 1 x
-// 100000: 55 us with the join's 7; 4 x 9000, 16 heads x 3 queries: 29 us, of which launch, first copies and join are 17.
+// Measured: 48 sequences of up to 12000 tokens (320000 in all), 128 heads: 137 us, 0.65 PFLOP/s, 2.7 TB/s of the cache; 1 x
+// 100000: 55 us with the join's 7; 4 x 9000, 16 heads x 3 queries: 28 us, of which launch, first copies and join are 17.
 //
 // Warps: 0-7 softmax and output (two threads per token, each half the columns), 8
 // MMA issue, 9-11 tiled bulk copies.
 // Every wait for another role is bounded, by a limit that each part of a sequence
-// renews; after one has run out all of them return at once, no further MMA or copy is issued, and the kernel records DEV_ERR_TIMEOUT.  Named
-// barriers join the softmax warps alone, which pass the same ones whatever has run out.
+// renews; after one has run out all of them return at once, no further MMA or copy is
+// issued, and the kernel records DEV_ERR_TIMEOUT.  Named barriers join the softmax warps
+// alone, which pass the same ones whatever has run out.
 #include <cudaTypedefs.h>
 
 #include "mla_attend.cuh"

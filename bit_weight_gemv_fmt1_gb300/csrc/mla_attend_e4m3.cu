@@ -23,7 +23,7 @@
 // 1250, the wait for the other tile's MMAs 1200, outputs 1100 to 1450, release to next copy's arrival 2000 (issue 600,
 // L2 700), 7300 in all, so a tile takes 3650 to 4400.  What shortened it: one barrier for all blocks of a
 // tile and one look at it and at P's (162 -> 157 us), bytes announced ahead of the release (-> 155).
-// Measured: 48 sequences of up to 12000 tokens (320000 in all), 128 heads: 155 us, 0.57 PFLOP/s of the formula's work;
+// Measured: 48 sequences of up to 12000 tokens (320000 in all), 128 heads: 154 us, 0.58 PFLOP/s of the formula's work;
 // 1 x 1000: 13 us, of which two thirds are launch, the first copies and the join.
 //
 // Warps: 0-7 softmax and output (two threads per token, each half the rows), 8 MMA issue, 9-13 bulk

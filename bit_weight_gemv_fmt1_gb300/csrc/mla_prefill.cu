@@ -28,7 +28,8 @@
 // the values lie idle for 770 cycles and the keys for 500, less than a copy takes (1000 to 1500): what the rings hold
 // beyond a tile covers that.  Two whole key tiles and one value tile, of the same size: 474 / 96 / 233 us against
 // 452 / 96 / 231 (8 x 1000 x 16 heads: 40 against 41, the price of more barriers); all blocks of a key tile waited for at once: 471.
-// 8192 tokens x 32 heads: 1.5 PFLOP/s, 0.79 of the measured bf16 rate (0.75 with L2 flushed between calls).
+// (These compare versions of their day on the same inputs again and again.)  8192 tokens x 32 heads now: 435 to 465 us that
+// way, 474 us with new inputs each call, 1.45 PFLOP/s, 0.75 of the measured bf16 rate.
 //
 // Keys past a causal row's limit are masked by selection; value rows past the
 // sequence's end belong to its neighbours and are zeroed in shared memory.
