@@ -186,7 +186,7 @@ struct Gone {
 };
 void CUDART_CB graph_gone(void *p) {
     Gone *g = (Gone *)p;
-    {
+    if (g->d) {
         std::lock_guard<std::mutex> lk(g->d->gone_mu);
         g->d->gone.push_back(g->id);
     }
@@ -222,16 +222,19 @@ int workspace_of(DeviceState *d, cudaStream_t st, Workspace **out) {
     auto it = d->graphs.find(id);
     if (it == d->graphs.end()) {
         free_gone(d);
+        it = d->graphs.emplace(id, std::map<cudaStream_t, Workspace>()).first;
         Gone *note = new Gone{d, id};
         cudaUserObject_t obj;
         const cudaError_t e = cudaUserObjectCreate(&obj, note, graph_gone, 1, cudaUserObjectNoDestructorSync);
         if (e != cudaSuccess) {
             delete note;
+            d->graphs.erase(id);
             return cuda_fail(e, "cudaUserObjectCreate");
         }
-        it = d->graphs.emplace(id, std::map<cudaStream_t, Workspace>()).first;
         const cudaError_t e2 = cudaGraphRetainUserObject(graph, obj, 1, cudaGraphUserObjectMove);
         if (e2 != cudaSuccess) {
+            note->d = nullptr;       // never the graph's: nothing to tell
+            d->graphs.erase(id);
             cudaUserObjectRelease(obj, 1);
             return cuda_fail(e2, "cudaGraphRetainUserObject");
         }
@@ -256,41 +259,55 @@ int grown(DeviceState *d, Workspace &w, cudaStream_t st, Held &b, size_t bytes, 
     return COLI_OK;
 }
 
+// f with the device's state locked; the host memory that it cannot get is an error code, as no C++ exception leaves the library.
+template <class F>
+int locked(DeviceState *d, F f) {
+    try {
+        std::lock_guard<std::mutex> lk(d->mu);
+        return f();
+    } catch (...) {
+        return fail(COLI_ENOMEM, "out of host memory");
+    }
+}
+
 // Router-logit scratch of at least `bytes` for this stream.
 int router_scratch(DeviceState *d, cudaStream_t st, size_t bytes, Held *out) {
-    std::lock_guard<std::mutex> lk(d->mu);
-    Workspace *w = nullptr;
-    if (int rc = workspace_of(d, st, &w)) return rc;
-    if (int rc = grown(d, *w, st, w->rbuf, bytes, bytes, false, "cudaMalloc(router scratch)")) return rc;
-    *out = w->rbuf;
-    return COLI_OK;
+    return locked(d, [&] {
+        Workspace *w = nullptr;
+        if (int rc = workspace_of(d, st, &w)) return rc;
+        if (int rc = grown(d, *w, st, w->rbuf, bytes, bytes, false, "cudaMalloc(router scratch)")) return rc;
+        *out = w->rbuf;
+        return (int)COLI_OK;
+    });
 }
 
 // Scratch of at least `bytes` for this stream (grown on demand; growing waits for the stream).
 int workspace(DeviceState *d, cudaStream_t st, size_t bytes, Scratch *out) {
-    std::lock_guard<std::mutex> lk(d->mu);
-    Workspace *w = nullptr;
-    if (int rc = workspace_of(d, st, &w)) return rc;
-    const size_t want = w->of_graph ? bytes : bytes + bytes / 4;
-    if (int rc = grown(d, *w, st, w->buf, bytes, want, false, "cudaMalloc(workspace)")) return rc;
-    // words 0-1: counter and generation of the resetting grid barrier
-    Workspace &own = d->ws[st];
-    if (int rc = grown(d, own, st, own.bar, kBarrierBytes, kBarrierBytes, true, "cudaMalloc(barrier)")) return rc;
-    out->hold = w->buf;
-    out->buf = w->buf->p;
-    out->bar = (unsigned *)own.bar->p;
-    return COLI_OK;
+    return locked(d, [&] {
+        Workspace *w = nullptr;
+        if (int rc = workspace_of(d, st, &w)) return rc;
+        const size_t want = w->of_graph ? bytes : bytes + bytes / 4;
+        if (int rc = grown(d, *w, st, w->buf, bytes, want, false, "cudaMalloc(workspace)")) return rc;
+        // words 0-1: counter and generation of the resetting grid barrier
+        Workspace &own = d->ws[st];
+        if (int rc = grown(d, own, st, own.bar, kBarrierBytes, kBarrierBytes, true, "cudaMalloc(barrier)")) return rc;
+        out->hold = w->buf;
+        out->buf = w->buf->p;
+        out->bar = (unsigned *)own.bar->p;
+        return (int)COLI_OK;
+    });
 }
 
 // Counter words of the streamed decode block for this stream, zero at
 // allocation; the kernel leaves them zero at the end of every call.
 int decode_counters(DeviceState *d, cudaStream_t st, size_t words, unsigned **out) {
-    std::lock_guard<std::mutex> lk(d->mu);
-    Workspace &w = d->ws[st];
-    const size_t want = std::max<size_t>(words, 4096) * sizeof(unsigned);
-    if (int rc = grown(d, w, st, w.cnt, words * sizeof(unsigned), want, true, "cudaMalloc(counters)")) return rc;
-    *out = (unsigned *)w.cnt->p;
-    return COLI_OK;
+    return locked(d, [&] {
+        Workspace &w = d->ws[st];
+        const size_t want = std::max<size_t>(words, 4096) * sizeof(unsigned);
+        if (int rc = grown(d, w, st, w.cnt, words * sizeof(unsigned), want, true, "cudaMalloc(counters)")) return rc;
+        *out = (unsigned *)w.cnt->p;
+        return (int)COLI_OK;
+    });
 }
 
 int check_tensor(const coli_tensor *t, const char *name) {
