@@ -41,6 +41,11 @@ class _MlaCache(ctypes.Structure):
                 ("rows", _vp), ("scales", _vp)]
 
 
+class _GqaCache(ctypes.Structure):
+    _fields_ = [("n_kv", _int), ("dim", _int), ("gs", _int), ("page_size", _int), ("n_pages", ctypes.c_int64),
+                ("k", _vp), ("v", _vp), ("k_scales", _vp), ("v_scales", _vp), ("weights", _vp)]
+
+
 class _Expert(ctypes.Structure):
     _fields_ = [("gate", _vp), ("up", _vp), ("down", _vp)]
 
@@ -72,6 +77,12 @@ _lib.coli_mla_read.argtypes = [_vp, _vp, _i64, _int, _vp, _int, _int, _vp, _i64,
 _lib.coli_mla_attend.argtypes = [_vp, _int, _vp, _vp, _int, _int, _int, _vp, _i64, _vp, _f, _int, _vp, _vp, _vp]
 _lib.coli_mla_prefill.argtypes = [_int, _vp, _i64, _vp, _i64, _vp, _i64, _int, _int, _int, _vp, _vp, _int, _int, _int, _int, _f,
                                   _int, _vp, _vp, _vp]
+_lib.coli_gqa_prefill.argtypes = [_int, _vp, _i64, _vp, _i64, _vp, _i64, _int, _int, _int, _vp, _vp, _int, _int, _int, _f, _int, _vp,
+                                  _vp, _vp]
+_lib.coli_gqa_append.argtypes = [_vp, _int, _vp, _i64, _vp, _i64, _int, _vp, _vp]
+_lib.coli_gqa_read.argtypes = [_vp, _vp, _i64, _int, _vp, _int, _int, _vp, _i64, _vp, _i64, _vp]
+_lib.coli_gqa_attend.argtypes = [_vp, _int, _vp, _int, _int, _int, _vp, _i64, _vp, _f, _int, _int, _vp, _vp, _vp]
+_lib.coli_gqa_evict.argtypes = [_vp, _vp, _i64, _int, _vp, _int, _int, _vp, _i64, _vp, _vp, _vp]
 _lib.coli_sync_check.argtypes = [_vp]
 _lib.coli_get_stats.argtypes = [ctypes.POINTER(_Stats)]
 _lib.coli_get_stats.restype = None
@@ -86,6 +97,7 @@ EXPORTS = ("coli_tensor_upload", "coli_tensor_upload_host", "coli_tensor_free", 
            "coli_moe_route", "coli_moe_topk", "coli_moe_router", "coli_moe_block", "coli_moe_block_noalloc",
            "coli_expert_table_create", "coli_expert_table_free", "coli_moe_block_t",
            "coli_mla_query", "coli_mla_append", "coli_mla_read", "coli_mla_attend", "coli_mla_prefill",
+           "coli_gqa_prefill", "coli_gqa_append", "coli_gqa_read", "coli_gqa_attend", "coli_gqa_evict",
            "coli_sync_check", "coli_last_error", "coli_get_stats", "coli_reset_stats", "coli_set_fail_after",
            "coli_set_wait_limit", "coli_version")
 
@@ -365,12 +377,12 @@ def _tokens(t, dev: int, name: str) -> int:
     return stride[0] if shape[0] > 1 else n
 
 
-def _pages(pages, n_seq: int, dev: int) -> int:
+def _pages(pages, n_seq: int, dev: int, name: str = "pages") -> int:
     n, width = pages.shape
     if pages.get_device() != dev:
-        _elsewhere(pages, dev, "pages")
+        _elsewhere(pages, dev, name)
     if pages.dtype is not _torch.int32 or n != n_seq or (width > 1 and pages.stride(1) != 1):
-        _refuse("pages must be an int32 CUDA tensor [n_seq, n] with packed rows")
+        _refuse(f"{name} must be an int32 CUDA tensor [n_seq, n] with packed rows")
     return pages.stride(0) if n > 1 else width
 
 
@@ -499,6 +511,119 @@ def mla_prefill(q, kv, k_rope, cu_q, cu_k, scale: float, out, lse=None, stream=N
     return out
 
 
+class GqaCache:
+    """The paged 4-bit cache of coli.h's coli_gqa_cache over the caller's tensors: k and v uint8 [n_pages, n_kv,
+    page_size, dim / 2], k_scales and v_scales bfloat16 [n_pages, n_kv, page_size, dim / gs], weights float32 [n_pages,
+    n_kv, page_size] or None.  Keeps the tensors alive."""
+
+    def __init__(self, k, v, k_scales, v_scales, weights=None):
+        torch = _torch or _load_torch()
+        if k.dim() != 4 or v.shape != k.shape or k_scales.dim() != 4 or k_scales.shape[:3] != k.shape[:3] or \
+                v_scales.shape != k_scales.shape or (weights is not None and weights.shape != k.shape[:3]):
+            _refuse("k, v must be [n_pages, n_kv, page_size, dim / 2], the scales [n_pages, n_kv, page_size, dim / gs], "
+                    "weights [n_pages, n_kv, page_size]")
+        dim, groups = 2 * k.shape[3], k_scales.shape[3]
+        if not k.is_cuda or groups < 1 or dim % groups:
+            _refuse("k must be a CUDA tensor and a row must have whole scale groups")
+        dev = k.get_device()
+        at = [_packed(k, torch.uint8, dev, "k"), _packed(v, torch.uint8, dev, "v"), _packed(k_scales, torch.bfloat16, dev, "k_scales"),
+              _packed(v_scales, torch.bfloat16, dev, "v_scales"), None if weights is None else _packed(weights, torch.float32, dev, "weights")]
+        self.k, self.v, self.k_scales, self.v_scales, self.weights, self.device = k, v, k_scales, v_scales, weights, dev
+        self.n_pages, self.n_kv, self.page_size, self.dim, self.gs = k.shape[0], k.shape[1], k.shape[2], dim, dim // groups
+        self._c = _GqaCache(self.n_kv, self.dim, self.gs, self.page_size, self.n_pages, *at)
+        self._p = ctypes.addressof(self._c)
+
+
+def gqa_prefill(q, k, v, cu_q, cu_k, scale: float, out, lse=None, stream=None):
+    """Causal attention of packed sequences: q [Tq, heads, dim], k and v [Tk, kv heads, dim] (all bf16 or all f32) into
+    out [Tq, heads, dim]; cu_q, cu_k int32 [n_seq + 1]; lse f32 [Tq, heads]."""
+    torch = _torch or _load_torch()
+    dev = _device()
+    Tq, H, D = q.shape
+    Tk, K, D2 = k.shape
+    if D2 != D or v.shape != k.shape or out.shape != q.shape or cu_q.shape != cu_k.shape or k.dtype is not q.dtype or \
+            v.dtype is not q.dtype or (lse is not None and lse.shape != (Tq, H)):
+        _refuse("gqa_prefill: q, k, v, cu_q, cu_k, out and lse must match one another")
+    rc = _lib.coli_gqa_prefill(_dtype(q), q.data_ptr(), _tokens(q, dev, "q"), k.data_ptr(), _tokens(k, dev, "k"), v.data_ptr(),
+                               _tokens(v, dev, "v"), Tq, Tk, cu_q.shape[0] - 1, _packed(cu_q, torch.int32, dev, "cu_q"),
+                               _packed(cu_k, torch.int32, dev, "cu_k"), H, K, D, scale, _dtype(out), _packed(out, out.dtype, dev, "out"),
+                               None if lse is None else _packed(lse, torch.float32, dev, "lse"),
+                               _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
+    return out
+
+
+def gqa_append(cache: GqaCache, k, v, slots, stream=None):
+    """Quantise and store k and v [T, kv heads, dim] (both f32 or both bf16) at slots [T] of the cache."""
+    torch = _torch or _load_torch()
+    dev = _device()
+    if cache.device != dev:
+        _elsewhere(cache.k, dev, "the cache")
+    T = k.shape[0]
+    if k.shape != (T, cache.n_kv, cache.dim) or v.shape != k.shape or v.dtype is not k.dtype or slots.shape != (T,):
+        _refuse("gqa_append: k and v must be [T, kv heads, dim] of one type and match slots [T] and the cache")
+    rc = _lib.coli_gqa_append(cache._p, _dtype(k), k.data_ptr(), _tokens(k, dev, "k"), v.data_ptr(), _tokens(v, dev, "v"), T,
+                              _packed(slots, torch.int64, dev, "slots"), _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def gqa_read(cache: GqaCache, pages, cu, k, v, stream=None):
+    """Read the first cu[b+1] - cu[b] tokens of each sequence b back into k and v [T, kv heads, dim] (both f32 or both bf16)."""
+    torch = _torch or _load_torch()
+    dev = _device()
+    if cache.device != dev:
+        _elsewhere(cache.k, dev, "the cache")
+    n_seq = cu.shape[0] - 1
+    T = k.shape[0]
+    if k.shape != (T, cache.n_kv, cache.dim) or v.shape != k.shape or v.dtype is not k.dtype:
+        _refuse("gqa_read: k and v must be [T, kv heads, dim] of one type and match the cache")
+    rc = _lib.coli_gqa_read(cache._p, pages.data_ptr(), _pages(pages, n_seq, dev), n_seq, _packed(cu, torch.int32, dev, "cu"), T,
+                            _dtype(k), k.data_ptr(), _tokens(k, dev, "k"), v.data_ptr(), _tokens(v, dev, "v"),
+                            _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
+    return k, v
+
+
+def gqa_attend(cache: GqaCache, q, pages, lens, scale: float, out, lse=None, weigh: bool = False, stream=None):
+    """Attention of q [n_seq, n_q, heads, dim] over the cached tokens (lens [n_seq] int32, the new ones included) into out
+    of the same shape; lse f32 [n_seq, n_q, heads].  weigh: each cached row's share is added to the cache's weights."""
+    torch = _torch or _load_torch()
+    dev = _device()
+    if cache.device != dev:
+        _elsewhere(cache.k, dev, "the cache")
+    B, n_q, H, D = q.shape
+    if D != cache.dim or out.shape != q.shape or lens.shape != (B,) or (lse is not None and lse.shape != (B, n_q, H)):
+        _refuse("gqa_attend: q, lens, out and lse must match one another and the cache")
+    rc = _lib.coli_gqa_attend(cache._p, _dtype(q), _packed(q, q.dtype, dev, "q"), B, n_q, H, pages.data_ptr(), _pages(pages, B, dev),
+                              _packed(lens, torch.int32, dev, "lens"), scale, weigh, _dtype(out), _packed(out, out.dtype, dev, "out"),
+                              None if lse is None else _packed(lse, torch.float32, dev, "lse"),
+                              _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
+    return out
+
+
+def gqa_evict(cache: GqaCache, pages, lens, keep: int, recent: int, dst, kept, new_lens, stream=None):
+    """Choose the min(keep, lens[b]) tokens of each sequence and head that stay (the newest `recent` and the most weighted
+    others) and write them to the sequence's new pages dst; kept int32 [n_seq, kv heads, keep], new_lens int32 [n_seq]."""
+    torch = _torch or _load_torch()
+    dev = _device()
+    if cache.device != dev:
+        _elsewhere(cache.k, dev, "the cache")
+    B = lens.shape[0]
+    if kept.shape != (B, cache.n_kv, keep) or new_lens.shape != (B,):
+        _refuse("gqa_evict: kept must be [n_seq, kv heads, keep], new_lens [n_seq]")
+    rc = _lib.coli_gqa_evict(cache._p, pages.data_ptr(), _pages(pages, B, dev), B, _packed(lens, torch.int32, dev, "lens"), keep, recent,
+                             dst.data_ptr(), _pages(dst, B, dev, "dst"), _packed(kept, torch.int32, dev, "kept"),
+                             _packed(new_lens, torch.int32, dev, "new_lens"), _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
+    return kept, new_lens
+
+
 def sync_check(stream=None):
     _check(_lib.coli_sync_check(_stream(stream)))
 
@@ -518,7 +643,7 @@ def set_fail_after(n: int):
 
 
 def set_wait_limit(ns: int):
-    """Bound of each device-side wait of the latent attention's kernels (ns <= 0: the default, 2 s)."""
+    """Bound of each device-side wait of the attention kernels (ns <= 0: the default, 2 s)."""
     _lib.coli_set_wait_limit(int(ns))
 
 

@@ -1,40 +1,11 @@
 // mla_api.cu -- the latent-attention entry points of include/coli.h: argument
 // checks and launches.  Nothing is launched unless every check passed.
-#include <cstdarg>
-#include <cstdio>
-
+#include "api_checks.cuh"
 #include "mla.cuh"
 
 using namespace coli;
 
 namespace {
-
-int bad(int code, const char *fmt, ...) {
-    char buf[256];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    return set_last_error(code, buf);
-}
-
-int launched(cudaError_t e, const char *what, int n) {
-    if (e != cudaSuccess)
-        return bad(e == cudaErrorMemoryAllocation ? COLI_ENOMEM : COLI_ECUDA, "%s: %s", what, cudaGetErrorString(e));
-    count_call(n, 0);
-    return COLI_OK;
-}
-
-int need(const void *p, uintptr_t align, const char *name) {
-    if (!p) return bad(COLI_EINVAL, "%s is NULL", name);
-    if ((uintptr_t)p & (align - 1)) return bad(COLI_EINVAL, "%s is not %d-byte aligned", name, (int)align);
-    return COLI_OK;
-}
-
-int float_type(int dtype, const char *name) {
-    if (dtype != COLI_F32 && dtype != COLI_BF16) return bad(COLI_EFMT, "%s must be COLI_F32 or COLI_BF16 (got %d)", name, dtype);
-    return COLI_OK;
-}
 
 int check_cache(const coli_mla_cache *c, MlaCache *out) {
     if (!c) return bad(COLI_EINVAL, "cache is NULL");
@@ -272,16 +243,6 @@ int prefill(int dtype, const void *q, int64_t q_stride, const void *kv, int64_t 
     int n = 0;
     const cudaError_t e = launch_mla_prefill(a, d, (cudaStream_t)stream, &n);
     return launched(e, "coli_mla_prefill", n);
-}
-
-// No C++ exception leaves the library.
-template <class F>
-int guarded(F f) {
-    try {
-        return f();
-    } catch (...) {
-        return set_last_error(COLI_ENOMEM, "out of host memory");
-    }
 }
 
 }  // namespace

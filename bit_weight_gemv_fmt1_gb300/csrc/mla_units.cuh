@@ -1,39 +1,47 @@
-// mla_units.cuh -- the units of work of the expanded attention (mla_prefill.cu) and the search for one by its number.
+// mla_units.cuh -- the units of work of the prompts' attention (mla_prefill.cu, gqa_prefill.cu) and the search for one by its
+// number.  A query tile is 128 rows: as many tokens of one head, or fewer tokens of several heads that share their keys.
 #pragma once
 
-#include "mla.cuh"
+#include "gqa.cuh"
 
 namespace coli {
 
 constexpr int kRows = 128;               // rows of a query or key tile
 
-// One unit of work: a head's pair of query tiles.
+// Tokens of a query tile.
+__device__ __forceinline__ constexpr int tile_tokens(const MlaPrefillArgs &) { return kRows; }
+__device__ __forceinline__ int tile_tokens(const GqaPrefillArgs &a) { return a.tokens; }
+
+// One unit of work: a head's (or a group of heads') pair of query tiles.
 struct Unit {
-    int head, q0, nq, nk, qrow, krow;    // first query of the pair in its sequence, the sequence's sizes and first rows
+    int head, q0, nq, nk, qrow, krow;    // first token of the pair in its sequence, the sequence's sizes and first rows
     int nt[2], n;                        // key tiles that each query tile sees, the larger of them; n < 0: no more units
 };
 
 // Sequence b's offsets (all 0 where they are bad) and its number of pairs.
-__device__ __forceinline__ int pairs_of(const MlaPrefillArgs &a, int b, bool report, int4 &c) {
+template <class A>
+__device__ __forceinline__ int pairs_of(const A &a, int b, bool report, int4 &c) {
     c = make_int4(0, 0, 0, 0);
     if (b >= a.n_seq) return 0;
     const int4 d = make_int4(a.cu_q[b], a.cu_q[b + 1], a.cu_k[b], a.cu_k[b + 1]);
     const bool good = d.x >= 0 && d.y >= d.x && d.y <= a.Tq && d.z >= 0 && d.w >= d.z && d.w <= a.Tk;
     if (report && !good) mla_bad_index(a.err);
     if (good) c = d;
-    return (c.y - c.x + 2 * kRows - 1) / (2 * kRows);
+    return (c.y - c.x + 2 * tile_tokens(a) - 1) / (2 * tile_tokens(a));
 }
-// How many of a sequence's n pairs see v key tiles or more: the last pair sees all nk keys, each one before it 256
-// fewer rows' worth.
-__device__ __forceinline__ int pairs_with(int n, int4 c, int v) {
+// How many of a sequence's n pairs see v key tiles or more: the last pair sees all nk keys, each one before it a
+// pair's tokens fewer.
+template <class A>
+__device__ __forceinline__ int pairs_with(const A &a, int n, int4 c, int v) {
     if (v <= 0) return n;
     const int spare = c.w - c.z - ((v - 1) * kRows + 1);   // rows that may lie behind the pair's last
     if (spare < 0) return 0;
-    const int need = max(1, (c.y - c.x - spare + 2 * kRows - 1) / (2 * kRows));
+    const int need = max(1, (c.y - c.x - spare + 2 * tile_tokens(a) - 1) / (2 * tile_tokens(a)));
     return min(n, max(0, n - need + 1));
 }
 // Whole warp: the pairs of all sequences, and the most key tiles that one sees.
-__device__ __forceinline__ int all_pairs(const MlaPrefillArgs &a, int lane, bool report, int &most) {
+template <class A>
+__device__ __forceinline__ int all_pairs(const A &a, int lane, bool report, int &most) {
     int total = 0;
     most = 0;
     for (int b = lane; b < a.n_seq; b += 32) {
@@ -55,7 +63,8 @@ struct Place {
 // Before the first unit.
 __device__ __forceinline__ Place no_place(int most) { return Place{most + 1, 0, 0, 0, 0, most}; }
 // Whole warp: unit i, in the order of key tiles, most first, all heads of a pair together.
-__device__ __forceinline__ Unit unit_of(const MlaPrefillArgs &a, int i, int pairs, Place &at, int lane) {
+template <class A>
+__device__ __forceinline__ Unit unit_of(const A &a, int i, int pairs, Place &at, int lane) {
     Unit u;
     const int p = i / a.H;
     u.head = i - p * a.H;
@@ -73,7 +82,7 @@ __device__ __forceinline__ Unit unit_of(const MlaPrefillArgs &a, int i, int pair
             for (int b = lane; b < a.n_seq; b += 32) {
                 int4 c;
                 const int n = pairs_of(a, b, false, c);
-                t += pairs_with(n, c, v);
+                t += pairs_with(a, n, c, v);
             }
             t = __reduce_add_sync(0xffffffffu, t);
             if (t > p) {
@@ -97,7 +106,7 @@ __device__ __forceinline__ Unit unit_of(const MlaPrefillArgs &a, int i, int pair
     for (int b0 = at.b0; b0 < a.n_seq; b0 += 32) {
         int4 c;
         const int n = pairs_of(a, b0 + lane, false, c);
-        const int above = pairs_with(n, c, v + 1), here = pairs_with(n, c, v) - above;
+        const int above = pairs_with(a, n, c, v + 1), here = pairs_with(a, n, c, v) - above;
         int incl = here;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -110,7 +119,7 @@ __device__ __forceinline__ Unit unit_of(const MlaPrefillArgs &a, int i, int pair
             at.b0 = b0;
             at.run = run;
             const int src = __ffs(hit) - 1;
-            u.q0 = __shfl_sync(0xffffffffu, (n - 1 - above - (p - before)) * 2 * kRows, src);
+            u.q0 = __shfl_sync(0xffffffffu, (n - 1 - above - (p - before)) * 2 * tile_tokens(a), src);
             u.qrow = __shfl_sync(0xffffffffu, c.x, src);
             u.nq = __shfl_sync(0xffffffffu, c.y, src) - u.qrow;
             u.krow = __shfl_sync(0xffffffffu, c.z, src);
@@ -122,8 +131,8 @@ __device__ __forceinline__ Unit unit_of(const MlaPrefillArgs &a, int i, int pair
 #pragma unroll
     for (int x = 0; x < 2; x++) {
         // the last live row's limit
-        const int rows = min(kRows, u.nq - u.q0 - x * kRows);
-        const int limit = rows > 0 ? u.q0 + x * kRows + rows + u.nk - u.nq : 0;
+        const int rows = min(tile_tokens(a), u.nq - u.q0 - x * tile_tokens(a));
+        const int limit = rows > 0 ? u.q0 + x * tile_tokens(a) + rows + u.nk - u.nq : 0;
         u.nt[x] = limit > 0 ? (min(limit, u.nk) + kRows - 1) / kRows : 0;
     }
     u.n = max(u.nt[0], u.nt[1]);

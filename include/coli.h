@@ -521,10 +521,155 @@ int coli_mla_prefill(int dtype, const void *q, int64_t q_stride, const void *kv,
                      const int32_t *cu_q, const int32_t *cu_k, int n_heads, int nope, int rope, int v,
                      float scale, int dtype_out, void *out, float *lse, void *stream);
 
+/*
+ * Grouped-head attention (GQA): the attention of decoder layers whose n_heads
+ * query heads share n_kv key / value heads, query head h the head h / (n_heads
+ * / n_kv), for prompts and over a paged cache held in 4 bits.  Queries and keys
+ * come rotated (coli_mla_query with nope = 0 rotates heads of either).
+ */
+
+/*
+ * A paged 4-bit cache of keys and values in the caller's device memory.  The
+ * row of slot page * page_size + offset and head h is row (page * n_kv + h) *
+ * page_size + offset of each array.  A row's element 2j is the low nibble of
+ * byte j, its value (nibble - 8) * scale, one scale for each gs elements.
+ *   n_kv       1..1024.
+ *   dim        64 or 128, of a key and of a value.
+ *   gs         32, 64 or 128, at most dim.
+ *   page_size  tokens per page, a multiple of 16 in 16..65536.
+ *   n_pages    >= 1, n_pages * n_kv * page_size <= 2^31 - 1.
+ *   k, v       device [n_pages][n_kv][page_size][dim / 2] bytes.
+ *   k_scales, v_scales  device bf16 [n_pages][n_kv][page_size][dim / gs].
+ *   weights    device f32 [n_pages][n_kv][page_size]: the attention weight each
+ *              row has got so far, or NULL for a cache without.
+ * All 16-byte aligned.
+ */
+typedef struct {
+    int n_kv, dim, gs, page_size;
+    int64_t n_pages;
+    uint8_t *k, *v;
+    uint16_t *k_scales, *v_scales;
+    float *weights;
+} coli_gqa_cache;
+
+/*
+ * Causal attention of whole prompts, over n_seq sequences packed one after
+ * another.  Sequence b has query rows cu_q[b] .. cu_q[b+1] and key rows cu_k[b]
+ * .. cu_k[b+1]; its last query lines up with its last key: query i sees the
+ * keys j <= i + n_k - n_q (earlier keys: a cached prefix).
+ *   s_ij = scale * q_i . k_j, out_i = sum_j softmax(s_i)_j v_j
+ * A query that sees no key gives zeros and lse = -infinity.
+ *   q       device [Tq][n_heads][dim], token stride q_stride.
+ *   k, v    device [Tk][n_kv][dim], token strides k_stride, v_stride (they may be
+ *           parts of one row).
+ *   dtype   COLI_BF16, or COLI_F32: the three are then rounded to bf16 in scratch first.
+ *   cu_q, cu_k      device int32 [n_seq + 1], ascending from 0 to Tq / Tk.
+ *   out     device [Tq][n_heads][dim], COLI_F32 or COLI_BF16; lse device f32 [Tq][n_heads] or NULL.
+ *           Rows of no sequence are left alone.
+ * Products have bf16 operands (the probabilities are rounded to bf16) and f32
+ * sums; maxima and denominators are f32.  A value of another sequence never
+ * reaches the result; a non-finite v row that a query's own sequence masks may.
+ * Pointers 16-byte aligned (cu, lse: 4); strides in elements, multiples of 8.
+ * dim 64 or 128; n_heads a multiple of n_kv, n_heads / n_kv <= 128.  Tq, Tk >= 0, n_seq >= 0,
+ * 1 <= n_heads <= 1024.  Offsets outside [0, Tq] / [0, Tk] or descending are
+ * recorded for coli_sync_check; those sequences' outputs are unspecified.
+ * Errors: COLI_EINVAL, COLI_EFMT, COLI_ENOMEM, COLI_ECUDA, COLI_EINJECTED.
+ */
+int coli_gqa_prefill(int dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                     const void *v, int64_t v_stride, int Tq, int Tk, int n_seq, const int32_t *cu_q,
+                     const int32_t *cu_k, int n_heads, int n_kv, int dim, float scale, int dtype_out,
+                     void *out, float *lse, void *stream);
+
+/*
+ * Write tokens' keys and values into the cache.  For each group of gs elements
+ *   scale = bf16(max|x| / 7), code = min(7, max(-8, rint(x / scale))),
+ * both to nearest, halves to even; where scale is 0, x / 1 takes the quotient's
+ * place.  A group with a NaN or an infinity gets the scale NaN and codes 0.  The
+ * written rows' weights (if the cache has them) become 0.
+ *   dtype   COLI_F32 or COLI_BF16.
+ *   k, v    device [T][n_kv][dim], token strides k_stride, v_stride in elements.
+ *   slots   device int64 [T]; -1 skips the token.  Equal slots in one call race.
+ * Pointers 16-byte aligned (slots: 8), strides multiples of 8.  T >= 0.
+ * A slot out of range is recorded for coli_sync_check and the token is not written.
+ * Errors: COLI_EINVAL, COLI_EFMT, COLI_ECUDA, COLI_EINJECTED.
+ */
+int coli_gqa_append(const coli_gqa_cache *cache, int dtype, const void *k, int64_t k_stride,
+                    const void *v, int64_t v_stride, int T, const int64_t *slots, void *stream);
+
+/*
+ * Read the first tokens of n_seq sequences back, one after another (e.g. as the
+ * prefix of a prompt's next chunk): row cu[b] + i of k and v = token i of
+ * sequence b, i < cu[b+1] - cu[b].
+ *   pages, cu, T   as in coli_mla_read.
+ *   dtype   COLI_F32 (exact) or COLI_BF16 (rounded to nearest).
+ *   k, v    device [T][n_kv][dim], token strides in elements, multiples of 8; 16-byte aligned.
+ * A page id outside [0, n_pages), or a sequence longer than its page list, is
+ * recorded for coli_sync_check and its rows are zero.
+ * Errors: COLI_EINVAL, COLI_EFMT, COLI_ECUDA, COLI_EINJECTED.
+ */
+int coli_gqa_read(const coli_gqa_cache *cache, const int32_t *pages, int64_t pages_stride, int n_seq,
+                  const int32_t *cu, int T, int dtype, void *k, int64_t k_stride, void *v,
+                  int64_t v_stride, void *stream);
+
+/*
+ * Attention over the cache for the n_q newest tokens of each of n_seq sequences
+ * (n_q = 1: a decode step).  Query token j of sequence b sees the cached tokens
+ * t < lens[b] - (n_q - 1 - j) (lens counts the new tokens, whose rows are in
+ * the cache already).
+ *   s_t = scale * q . k_t, p = softmax(s), out = sum_t p_t v_t, lse = ln sum_t exp(s_t)
+ * With weigh != 0 every row's weight grows by the sum of its p over the n_q
+ * queries of its group's heads.  A query that sees no token gives zeros, lse =
+ * -infinity and no weight.
+ *   q       device [n_seq][n_q][n_heads][dim], COLI_F32 or COLI_BF16 (dtype_q).
+ *   pages   as in coli_mla_read; lens[b] <= pages_stride * page_size.
+ *   lens    device int32 [n_seq], >= 0.
+ *   out     device [n_seq][n_q][n_heads][dim], COLI_F32 or COLI_BF16.
+ *   lse     device f32 [n_seq][n_q][n_heads], or NULL.
+ * The key product takes codes as they are and q in f16, scaled by a power of two
+ * per query row: a bf16 element is exact down to 2^-32 of the row's largest
+ * magnitude, an f32 one is rounded to 11 bits.  For the value product each
+ * probability times its row's scale is rounded to bf16.  Scales are applied and
+ * sums, maxima and the denominator held in f32.
+ * Rows past a sequence's length, and pages past its last, are never used: they may
+ * hold anything.  A NaN or an infinity in a query, or a NaN scale of a key that a query
+ * sees, makes its output, lse and weights NaN; a NaN scale of a value that it sees the
+ * outputs of that group.
+ * Weights of a page that several sequences of the call share are added in no fixed order.
+ * Pointers 16-byte aligned (pages, lens, lse: 4).  n_seq >= 0, n_q >= 1, n_heads a multiple of n_kv,
+ * 1 <= n_heads <= 1024, n_q * n_heads <= 65536.  A page id outside [0, n_pages) among the needed ones, or a
+ * length out of range, is recorded for coli_sync_check; that sequence's output is unspecified.
+ * Errors: COLI_EINVAL (also: weigh with a cache without weights), COLI_EFMT, COLI_ENOMEM (scratch),
+ * COLI_ECUDA, COLI_EINJECTED.
+ */
+int coli_gqa_attend(const coli_gqa_cache *cache, int dtype_q, const void *q, int n_seq, int n_q,
+                    int n_heads, const int32_t *pages, int64_t pages_stride, const int32_t *lens,
+                    float scale, int weigh, int dtype_out, void *out, float *lse, void *stream);
+
+/*
+ * Choose, for each sequence and head by itself, the min(keep, lens[b]) tokens that
+ * stay: the newest `recent` ones and those with the most weight among the others
+ * (equal weights: the earlier token; a NaN counts as the most), and write their
+ * rows, scales and weights, in their order, to the sequence's new pages.  The
+ * sequence's own pages are left as they were.
+ *   pages, lens   as in coli_gqa_attend.
+ *   keep, recent  keep >= 1, 0 <= recent <= keep.
+ *   dst       device int32, sequence b's new page ids at dst + b * dst_stride, for
+ *             min(keep, lens[b]) tokens; pages that no sequence of the call reads.
+ *   kept      device int32 [n_seq][n_kv][keep]: the tokens that stay, ascending, then -1.
+ *   new_lens  device int32 [n_seq]: min(keep, lens[b]); not lens itself.
+ * Pointers 4-byte aligned; dst_stride * page_size >= keep.  A page id out of range, or a
+ * length out of range, is recorded for coli_sync_check; rows of the former are not
+ * written (weights read from it count as 0), a sequence of the latter keeps nothing.
+ * Errors: COLI_EINVAL (also: a cache without weights), COLI_ECUDA, COLI_EINJECTED.
+ */
+int coli_gqa_evict(const coli_gqa_cache *cache, const int32_t *pages, int64_t pages_stride, int n_seq,
+                   const int32_t *lens, int keep, int recent, const int32_t *dst, int64_t dst_stride,
+                   int32_t *kept, int32_t *new_lens, void *stream);
+
 /* Synchronize `stream`, then report (and clear) any error the library's
  * kernels recorded on this device: COLI_ETIMEOUT for a bounded wait that ran
  * out, COLI_EINVAL for an out-of-range routing id or an out-of-range page,
- * slot, position, length or offset of the latent attention, COLI_ECUDA for a
+ * slot, position, length or offset of the attention calls, COLI_ECUDA for a
  * CUDA error.  Returns COLI_OK otherwise. */
 int coli_sync_check(void *stream);
 
@@ -541,7 +686,7 @@ void coli_reset_stats(void);
  * load time. */
 void coli_set_fail_after(int64_t n);
 
-/* How long, in nanoseconds, a kernel of the latent attention waits in one of its pieces
+/* How long, in nanoseconds, a kernel of the attention calls waits in one of its pieces
  * of work (a head's 256 queries, a CTA's part of a sequence) before it gives up, records
  * COLI_ETIMEOUT for coli_sync_check and returns; its outputs are then unspecified.  A
  * piece has 1/256 of it more for each of its tiles of 128 tokens (microseconds each);
