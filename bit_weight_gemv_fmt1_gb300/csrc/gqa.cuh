@@ -83,7 +83,7 @@ struct GqaPrefillArgs {
 
 cudaError_t launch_gqa_append(const GqaAppendArgs &a, bool in_bf16, cudaStream_t st);
 cudaError_t launch_gqa_read(const GqaReadArgs &a, bool out_bf16, cudaStream_t st);
-cudaError_t launch_gqa_evict(const GqaEvictArgs &a, cudaStream_t st, int *n_launch);
+cudaError_t launch_gqa_evict(const GqaEvictArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch);
 // Scratch of a call, and the call (d.scratch: that many bytes, NULL if none).
 size_t gqa_attend_scratch(const GqaAttendArgs &a, int n_sm);
 cudaError_t launch_gqa_attend(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch);

@@ -186,7 +186,7 @@ int evict(const coli_gqa_cache *cache, const int32_t *pages, int64_t pages_strid
     a.new_lens = new_lens;
     a.err = d.err;
     int n = 0;
-    const cudaError_t e = launch_gqa_evict(a, (cudaStream_t)stream, &n);
+    const cudaError_t e = launch_gqa_evict(a, d, (cudaStream_t)stream, &n);
     return launched(e, "coli_gqa_evict", n);
 }
 

@@ -1,21 +1,21 @@
 // gqa_attend.cu -- attention of the newest tokens over the paged 4-bit cache, and
 // the weights that its rows get.
 //
-// A unit of work is a tile of 32 cached tokens of one sequence and key / value
-// head, for 8 or 16 query rows (n_q tokens x the group's heads).  The units of
-// all sequences stand in one row; every CTA takes an equal share of it and walks
-// it by segments (the tiles of one sequence, head and set of rows).  A segment's
-// tiles go round the CTA's 8 warps, each with a running maximum, sum and output of its own
-// and a ring of tiles that bulk copies fill; the warps join at the segment's end.
-// A segment that several CTAs have is joined by a second kernel.
+// A unit of work is a tile of 32 cached tokens of one sequence and key / value head, for 8 query rows (n_q tokens x the
+// group's heads).  The units of all sequences stand in one row; every CTA takes an equal share of it and walks
+// it by segments (the tiles of one sequence, head and set of rows).  A segment's tiles go round the CTA's 8 warps, each
+// with a running maximum, sum and output of its own and a ring of tiles that bulk copies fill; the warps join at the
+// segment's end.  A segment that several CTAs have is joined by a second kernel.
 //
 // Per warp and 16 tokens (mma.sync m16n8k16, tokens or dims as M, query rows as N):
 //   S^T = K q^T   codes AND-ed out of the words are f16 subnormals n 2^-24 (odd nibbles
 //                 16 times that, q a 16th there); accumulators begin at -8 sum q, one
 //                 chain per scale group, whose f32 result takes the scale
-//   O^T += V^T P^T  codes OR-ed into bf16 as 128 + n; p times the row's scale rounded to
-//                 bf16, transposed in registers; -136 sum P comes from one more product
-// so no code is converted one by one and nothing is rounded but q and p * scale.
+//   O^T += V^T P^T  codes OR-ed into bf16 as 128 + n; p rounded to bf16, transposed in registers, its product with the
+//                 row's scale rounded to bf16; -136 sum P comes from one more product
+// so no code is converted one by one.  ldmatrix, transposing for the values, deals the words out as the products want them:
+// its 16-bit elements are 4 codes of one token.  N = 8 is what few query rows need; 5th-generation products would want the codes
+// as bytes in shared memory, M = 128 tokens, and N = 8 as well.
 // Softmax: x = log2(e) scale score, m moves (and O, l with it) only when a tile's
 // maximum passes it by 8.
 //
@@ -35,17 +35,18 @@ namespace coli {
 namespace {
 
 constexpr int kTile = 32, kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kJoin = 512, kGroup = 64;  // threads of the join, parts at a time
 constexpr float kGrow = 8.f;             // log2 of the weight that moves the reference
 constexpr float kNone = -3e38f;          // reference of a row that has seen no key
+constexpr int kRows = 8;                 // query rows of a unit: N of the products
 
-template <int D_, int NG_, int NT_>
+template <int D_, int NG_>
 struct Shape {
-    static constexpr int D = D_, NG = NG_, NT = NT_;    // dims, scale groups of a row, sets of 8 query rows
-    static constexpr int kParts = D / 32, kPer = kParts / NG, kRow = D / 2, kRows = 8 * NT;
+    static constexpr int D = D_, NG = NG_;              // dims, scale groups of a row
+    static constexpr int kParts = D / 32, kPer = kParts / NG, kRow = D / 2;
     static constexpr uint32_t kCodes = kTile * kRow, kScales = kTile * NG * 2;
     static constexpr uint32_t kStage = (2 * kCodes + 2 * kScales + 511) / 512 * 512;
-    static constexpr int kCtas = NT == 1 ? 2 : 1;       // on an SM
-    static constexpr int kDepth = std::min(8u, (kCtas == 2 ? 110u : 222u) * 1024u / (kWarps * kStage));
+    static constexpr int kDepth = std::min(8u, 110u * 1024u / (kWarps * kStage));   // two CTAs on an SM
     static constexpr uint32_t kSmem = kWarps * kDepth * kStage + 1024;
     static_assert(kDepth * kStage >= kRows * D * 4, "a warp's output fits its ring");
 };
@@ -54,6 +55,8 @@ struct AttendPlan {
     int n_cta, rg, boxes;                // CTAs, sets of query rows per head, copies per tile (pages of 16, 48, ... tokens: 2)
     float *part;                         // [n_cta][2][kRows][D + 2]: O, m, l
     float2 *stat;                        // [n_seq][n_kv][rg][kRows]: m and 1 / l, for the weights
+    uint32_t magic;                      // 128 in bf16, twice
+    long long *before;                   // [n_seq + 1]: tiles of the sequences before each, for the join
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -66,13 +69,53 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Four 8 x 8 matrices of 16-bit elements, rows of 16 bytes at the addresses of lanes 0-7, 8-15, ...: of each a thread gets elements
+// 2 (lane % 4) and the next of row lane / 4, or (transposed) of column lane / 4.
+__device__ __forceinline__ void load_matrices(uint32_t at, uint32_t (&x)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
+}
+__device__ __forceinline__ void load_matrices_t(uint32_t at, uint32_t (&x)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+// Two bf16 products, to nearest.
+__device__ __forceinline__ uint32_t mul_bf16(uint32_t a, uint32_t b) {
+    uint32_t c;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+    return c;
+}
+// Fills a stage, or the second half of one: a box of either codes and their scales, counted on `bar`, which the first call tells
+// of all the bytes.  Whole warp, uniform arguments, one thread issues.
+template <bool VALUES, bool FIRST>
+__device__ __forceinline__ void fill(uint32_t dst, uint32_t v_off, uint32_t scales, uint32_t vs_off, const CUtensorMap *k, const CUtensorMap *v, int row,
+                                     const void *ks, const void *vs, uint32_t scale_bytes, uint64_t *bar, uint32_t bytes) {
+    if constexpr (FIRST) expect_bytes(bar, bytes);
+    if constexpr (VALUES)
+        asm volatile(
+            "{\n .reg .pred q;\n .reg .b32 z;\n mov.b32 z, 0;\n elect.sync _|q, 0xffffffff;\n"
+            " @q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%3, {z, %5}], [%0];\n"
+            " @q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%6], [%8], %10, [%0];\n"
+            " @q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%2], [%4, {z, %5}], [%0];\n"
+            " @q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%7], [%9], %10, [%0];\n}\n" ::"r"(smem_addr(bar)),
+            "r"(dst), "r"(dst + v_off), "l"(k), "l"(v), "r"(row), "r"(scales), "r"(scales + vs_off), "l"(ks), "l"(vs), "r"(scale_bytes)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred q;\n .reg .b32 z;\n mov.b32 z, 0;\n elect.sync _|q, 0xffffffff;\n"
+            " @q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%2, {z, %3}], [%0];\n"
+            " @q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%4], [%5], %6, [%0];\n}\n" ::"r"(smem_addr(bar)),
+            "r"(dst), "l"(k), "r"(row), "r"(scales), "l"(ks), "r"(scale_bytes)
+            : "memory");
+}
 __device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// CTAs that have work: fewer than the grid where a CTA's warps would not have a unit each.
+__device__ __forceinline__ long long working(long long units, int grid) { return min((long long)grid, (units + kWarps - 1) / kWarps); }
 
 __device__ __forceinline__ int length_of(const GqaAttendArgs &a, int b, bool report) {
     const int n = a.lens[b];
@@ -82,28 +125,38 @@ __device__ __forceinline__ int length_of(const GqaAttendArgs &a, int b, bool rep
 }
 __device__ __forceinline__ int tiles_of(const GqaAttendArgs &a, int b) { return (length_of(a, b, false) + kTile - 1) / kTile; }
 
-// The whole CTA: the tiles of the sequences before `upto`.
-__device__ __forceinline__ long long tiles_before(const GqaAttendArgs &a, int upto, long long *red) {
-    long long n = 0;
-    for (int b = threadIdx.x; b < upto; b += blockDim.x) n += tiles_of(a, b);
+// Where a CTA's work begins.
+struct Start {
+    long long tiles, u, first;           // tiles of all sequences, the CTA's first unit, the tiles before its sequence
+    int seq;                             // -1: no work
+};
+// The whole CTA: units are tiles * per; CTA i of the n that work has those from units * i / n on.
+// The first CTA writes `before` if there is one.
+__device__ __forceinline__ Start find_start(const GqaAttendArgs &a, int per, long long *before) {
+    __shared__ long long sums[kWarps];
+    __shared__ long long s_first;
+    __shared__ int s_seq;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long mine = tid < a.n_seq ? tiles_of(a, tid) : 0;
+    long long n = mine;
+    for (int b = tid + kThreads; b < a.n_seq; b += kThreads) n += tiles_of(a, b);
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (tid == 0) s_seq = -1;
+    if (lane == 0) sums[warp] = n;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = n;
-    __syncthreads();
-    n = 0;
-    for (int w = 0; w < (int)blockDim.x / 32; w++) n += red[w];
-    return n;
-}
-// The whole CTA: the sequence that holds tile x / per (x < tiles of all * per), and the tiles before it.
-__device__ __forceinline__ int find_sequence(const GqaAttendArgs &a, long long x, int per, long long &first, long long *red) {
-    __shared__ int s_seq;
-    __shared__ long long s_first;
+    Start z;
+    z.tiles = 0;
+    for (int w = 0; w < kWarps; w++) z.tiles += sums[w];
+    const long long units = z.tiles * per, n_cta = working(units, gridDim.x);
+    z.seq = -1;
+    const bool work = blockIdx.x < n_cta, writes = before && blockIdx.x == 0;
+    if (!work && !writes) return z;
+    z.u = work ? units * blockIdx.x / n_cta : 0;
     long long run = 0;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int b0 = 0;; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        const long long n = b < a.n_seq ? tiles_of(a, b) : 0;
+    for (int b0 = 0; b0 < a.n_seq; b0 += kThreads) {
+        const int b = b0 + tid;
+        n = b0 == 0 ? mine : b < a.n_seq ? tiles_of(a, b) : 0;
         long long incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -111,110 +164,111 @@ __device__ __forceinline__ int find_sequence(const GqaAttendArgs &a, long long x
             if (lane >= o) incl += v;
         }
         __syncthreads();
-        if (threadIdx.x == 0) s_seq = -1;
-        if (lane == 31) red[warp] = incl;
+        if (lane == 31) sums[warp] = incl;
         __syncthreads();
-        long long before = run, all = run;
+        long long at = run + incl - n;
         for (int w = 0; w < kWarps; w++) {
-            if (w < warp) before += red[w];
-            all += red[w];
+            if (w < warp) at += sums[w];
+            run += sums[w];
         }
-        before += incl - n;
-        if (before * per <= x && x < (before + n) * per) {
+        if (writes && b < a.n_seq) before[b] = at;
+        if (work && at * per <= z.u && z.u < (at + n) * per) {
             s_seq = b;
-            s_first = before;
+            s_first = at;
         }
         __syncthreads();
-        if (s_seq >= 0 || b0 + kThreads >= a.n_seq) break;
-        run = all;
+        if (s_seq >= 0 && !writes) break;
     }
-    first = s_first;
-    return s_seq;
+    if (writes && tid == 0) before[a.n_seq] = z.tiles;
+    z.seq = s_seq;
+    z.first = s_first;
+    return z;
 }
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // A warp's query rows as the B operand of the key product, and what its scores need.
 template <class S>
 struct Query {
-    uint32_t q[S::NT][S::kParts][4];     // rows lane / 4, dims 8 (lane % 4) + {0,4}, {1,5}/16, {2,6}, {3,7}/16 of each 32
-    float off[S::NT][S::NG][2];          // -8 sum q of rows 2 (lane % 4) + {0, 1}
-    float f[S::NT][2];                   // log2(e) * scale * 2^24 / the row's power of two
+    uint32_t q[S::kParts][4];            // row lane / 4, dims 8 (lane % 4) + {0,4}, {1,5}/16, {2,6}, {3,7}/16 of each 32
+    float f[2];                          // rows 2 (lane % 4) + {0, 1}: log2(e) * |scale| * 2^24 / the row's power of two; q has the scale's sign
 };
 
+// `off`: what the accumulators of lane % 4 begin with, -8 sum q of its two rows, twice.
 template <class S>
-__device__ __forceinline__ void load_query(const GqaAttendArgs &a, int b, int h, int r0, int lane, Query<S> &y) {
-    const int G = a.H / a.c.n_kv, n = a.n_q * G, c = lane & 3;
+__device__ __forceinline__ void load_query(const GqaAttendArgs &a, int b, int h, int r0, int lane, Query<S> &y, float4 (*off)[4]) {
+    const int G = a.H / a.c.n_kv, n = a.n_q * G, c = lane & 3, row = r0 + (lane >> 2);
+    float x[S::kParts][8];
+    if (row < n) {
+        const int j = row / G;
+        const long long e = ((long long)(b * (long long)a.n_q + j) * a.H + h * G + row - j * G) * S::D + 8 * c;
 #pragma unroll
-    for (int t = 0; t < S::NT; t++) {
-        const int row = r0 + 8 * t + (lane >> 2);
-        float x[S::kParts][8];
-        if (row < n) {
-            const int j = row / G;
-            const long long e = ((long long)(b * (long long)a.n_q + j) * a.H + h * G + row - j * G) * S::D + 8 * c;
+        for (int p = 0; p < S::kParts; p++) {
+            if (a.q_bf16) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(a.q) + e + 32 * p);
+                const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int p = 0; p < S::kParts; p++) {
-                if (a.q_bf16) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(a.q) + e + 32 * p);
-                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        x[p][2 * i] = low_bf16(v[i]);
-                        x[p][2 * i + 1] = high_bf16(v[i]);
-                    }
-                } else {
-                    const float4 u = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.q) + e + 32 * p);
-                    const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.q) + e + 32 * p + 4);
-                    x[p][0] = u.x, x[p][1] = u.y, x[p][2] = u.z, x[p][3] = u.w, x[p][4] = v.x, x[p][5] = v.y, x[p][6] = v.z, x[p][7] = v.w;
+                for (int i = 0; i < 4; i++) {
+                    x[p][2 * i] = low_bf16(v[i]);
+                    x[p][2 * i + 1] = high_bf16(v[i]);
                 }
+            } else {
+                const float4 u = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.q) + e + 32 * p);
+                const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.q) + e + 32 * p + 4);
+                x[p][0] = u.x, x[p][1] = u.y, x[p][2] = u.z, x[p][3] = u.w, x[p][4] = v.x, x[p][5] = v.y, x[p][6] = v.z, x[p][7] = v.w;
             }
-        } else {
-#pragma unroll
-            for (int p = 0; p < S::kParts; p++)
-#pragma unroll
-                for (int i = 0; i < 8; i++) x[p][i] = 0.f;
         }
-        float m = 0.f;
+    } else {
 #pragma unroll
         for (int p = 0; p < S::kParts; p++)
 #pragma unroll
-            for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(x[p][i]));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        int e = 0;                                       // the row times 2^e has its largest magnitude in 2^14 .. 2^15
-        if (m > 0.f && m < INFINITY) e = 14 - ilogbf(m);
-        float sum[S::NG];
-#pragma unroll
-        for (int g = 0; g < S::NG; g++) sum[g] = 0.f;
-#pragma unroll
-        for (int p = 0; p < S::kParts; p++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int odd = i & 1;
-                const uint32_t w = pack_f16(ldexpf(x[p][i], e - 4 * odd), ldexpf(x[p][i + 4], e - 4 * odd));
-                y.q[t][p][i] = w;
-                const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-                sum[p / S::kPer] += (back.x + back.y) * (odd ? 16.f : 1.f);
-            }
-        float f = ldexpf(a.scale * 1.4426950408889634f, 24 - e);
-#pragma unroll
-        for (int g = 0; g < S::NG; g++) {
-            sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
-            sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-            sum[g] *= -8.f / 16777216.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const int src = 4 * (2 * c + i);
-            y.f[t][i] = __shfl_sync(0xffffffffu, f, src);
-#pragma unroll
-            for (int g = 0; g < S::NG; g++) y.off[t][g][i] = __shfl_sync(0xffffffffu, sum[g], src);
-        }
+            for (int i = 0; i < 8; i++) x[p][i] = 0.f;
     }
+    float m = 0.f;
+#pragma unroll
+    for (int p = 0; p < S::kParts; p++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            m = fmaxf(m, fabsf(x[p][i]));
+            if (a.scale < 0.f) x[p][i] = -x[p][i];
+        }
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    int e = 0;                                           // the row times 2^e has its largest magnitude in 2^14 .. 2^15
+    if (m > 0.f && m < INFINITY) e = 14 - ilogbf(m);
+    const float up = exp2i(e / 2), even = exp2i(e - e / 2), odd = even * 0.0625f;   // 2^e in two factors: it may pass the range
+    float sum[S::NG];
+#pragma unroll
+    for (int g = 0; g < S::NG; g++) sum[g] = 0.f;
+#pragma unroll
+    for (int p = 0; p < S::kParts; p++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t w = pack_f16(x[p][i] * up * (i & 1 ? odd : even), x[p][i + 4] * up * (i & 1 ? odd : even));
+            y.q[p][i] = w;
+            const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+            sum[p / S::kPer] += (back.x + back.y) * (i & 1 ? 16.f : 1.f);
+        }
+    // a scale of zero must still send masked scores (-infinity) to -infinity
+    const float f = fmaxf(ldexpf(fabsf(a.scale) * 1.4426950408889634f, 24 - e), 1e-37f);
+#pragma unroll
+    for (int i = 0; i < 2; i++) y.f[i] = __shfl_sync(0xffffffffu, f, 4 * (2 * c + i));
+#pragma unroll
+    for (int g = 0; g < S::NG; g++) {
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+        sum[g] *= -8.f / 16777216.f;
+        const float u = __shfl_sync(0xffffffffu, sum[g], 8 * c), v = __shfl_sync(0xffffffffu, sum[g], 8 * c + 4);
+        if (lane < 4) off[g][lane] = make_float4(u, v, u, v);
+    }
+    __syncwarp();
 }
 
-// Byte of part p of row `key` (whose swizzle bits are x) in a tile of codes.
+// Part p of row `key` of a tile of codes stands at 16-byte piece p ^ swizzle(key) of it (64- and 32-byte swizzles of the copies).
 template <class S>
-__device__ __forceinline__ int code_at(int key, int p, int x) {
-    return key * S::kRow + ((p ^ x) << 4);
+__device__ __forceinline__ int swizzle(int key) {
+    return S::D == 128 ? (key >> 1) & 3 : (key >> 2) & 1;
 }
 // The scales of row `key`.
 template <class S>
@@ -230,171 +284,164 @@ __device__ __forceinline__ void load_scales(const uint8_t *sm, int key, float (&
     }
 }
 
-// x of the tile's scores: [k][t][i] is token 16 k + lane / 4 + 8 (i / 2) and row 8 t + 2 (lane % 4) + i % 2.
+// The scales of rows `key` (low halves) and `key` + 1, bf16; key is even.
 template <class S>
-__device__ __forceinline__ void scores(const uint8_t *codes, const uint8_t *scales, const Query<S> &y, int lane, float (&s)[2][S::NT][4]) {
-    const int r = lane >> 2, c = lane & 3, x = S::D == 128 ? (r >> 1) & 3 : r >> 2;
-#pragma unroll
-    for (int k = 0; k < 2; k++) {
-        float lo[S::NG], hi[S::NG];
-        load_scales<S>(scales, 16 * k + r, lo);
-        load_scales<S>(scales, 16 * k + r + 8, hi);
-#pragma unroll
-        for (int t = 0; t < S::NT; t++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) s[k][t][i] = 0.f;
-#pragma unroll
-        for (int g = 0; g < S::NG; g++) {
-            float d[S::NT][4];
-#pragma unroll
-            for (int t = 0; t < S::NT; t++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) d[t][i] = y.off[t][g][i & 1];
-#pragma unroll
-            for (int p = g * S::kPer; p < (g + 1) * S::kPer; p++) {
-                const uint32_t u = *reinterpret_cast<const uint32_t *>(codes + code_at<S>(16 * k + r, p, x) + 4 * c);
-                const uint32_t v = *reinterpret_cast<const uint32_t *>(codes + code_at<S>(16 * k + r + 8, p, x) + 4 * c);
-                const uint32_t u8 = u >> 8, v8 = v >> 8;
-#pragma unroll
-                for (int t = 0; t < S::NT; t++) {
-                    mma_f16(d[t], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u, y.q[t][p][0], y.q[t][p][1]);
-                    mma_f16(d[t], u8 & 0x000F000Fu, v8 & 0x000F000Fu, u8 & 0x00F000F0u, v8 & 0x00F000F0u, y.q[t][p][2], y.q[t][p][3]);
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < S::NT; t++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) s[k][t][i] = fmaf(d[t][i], i < 2 ? lo[g] : hi[g], s[k][t][i]);
-        }
-#pragma unroll
-        for (int t = 0; t < S::NT; t++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) s[k][t][i] *= y.f[t][i & 1];
+__device__ __forceinline__ void pair_scales(const uint8_t *sm, int key, uint32_t (&s)[S::NG]) {
+    if constexpr (S::NG == 4) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(sm + key * 8);
+        s[0] = __byte_perm(w.x, w.z, 0x5410), s[1] = __byte_perm(w.x, w.z, 0x7632);
+        s[2] = __byte_perm(w.y, w.w, 0x5410), s[3] = __byte_perm(w.y, w.w, 0x7632);
+    } else if constexpr (S::NG == 2) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(sm + key * 4);
+        s[0] = __byte_perm(w.x, w.y, 0x5410), s[1] = __byte_perm(w.x, w.y, 0x7632);
+    } else {
+        s[0] = *reinterpret_cast<const uint32_t *>(sm + key * 2);
     }
 }
 
-// What a warp has added up of a segment: rows 8 t + 2 (lane % 4) + i % 2, dims 32 p + 8 (r % 4) + 4 (r / 4) + {0..3} with r = lane / 4
-// ([2 e + i / 2] is dim 2 e + i / 2: m-tile e, its rows r and r + 8).
+// Adds part p of a tile's key product: d[k] is of tokens 16 k + lane / 4 + 8 (i / 2), rows 2 (lane % 4) + i % 2.
 template <class S>
-struct Sums {
-    float o[S::NT][S::kParts][2][4], corr[S::NT][S::NG][4], m[S::NT][2], l[S::NT][2];
-};
-
-template <class S, bool EDGE>
-__device__ __forceinline__ void tile(const GqaAttendArgs &a, const uint8_t *sm, const Query<S> &y, Sums<S> &z, int lane, int r0, int t0, int len) {
-    const int r = lane >> 2, c = lane & 3;
-    float s[2][S::NT][4];
-    scores<S>(sm, sm + 2 * S::kCodes, y, lane, s);
-    uint32_t seen = 0xFFFFFFFFu;                         // bit (k * NT + t) * 4 + i
-    if constexpr (EDGE) {
-        const int G = a.H / a.c.n_kv;
-#pragma unroll
-        for (int t = 0; t < S::NT; t++)
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                const int limit = len - (a.n_q - 1 - (r0 + 8 * t + 2 * c + i) / G);
-#pragma unroll
-                for (int k = 0; k < 2; k++)
-#pragma unroll
-                    for (int e = 0; e < 2; e++)
-                        if (t0 + 16 * k + r + 8 * e >= min(limit, len)) {
-                            s[k][t][2 * e + i] = -INFINITY;
-                            seen &= ~(1u << ((k * S::NT + t) * 4 + 2 * e + i));
-                        }
-            }
-    }
-    bool move = false;
-    float now[S::NT][2];
-#pragma unroll
-    for (int t = 0; t < S::NT; t++)
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            float m = fmaxf(fmaxf(s[0][t][i], s[0][t][2 + i]), fmaxf(s[1][t][i], s[1][t][2 + i]));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            now[t][i] = m;
-            move |= m > z.m[t][i] + kGrow;
-        }
-    if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-        for (int t = 0; t < S::NT; t++)
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                if (!(now[t][i] > z.m[t][i] + kGrow)) continue;
-                const float f = ex2(z.m[t][i] - now[t][i]);
-                z.m[t][i] = now[t][i];
-                z.l[t][i] *= f;
-#pragma unroll
-                for (int p = 0; p < S::kParts; p++)
-#pragma unroll
-                    for (int e = 0; e < 2; e++) z.o[t][p][e][i] *= f, z.o[t][p][e][2 + i] *= f;
-#pragma unroll
-                for (int g = 0; g < S::NG; g++) z.corr[t][g][i] *= f, z.corr[t][g][2 + i] *= f;
-            }
-    }
-    const uint8_t *codes = sm + S::kCodes, *scales = sm + 2 * S::kCodes + S::kScales;
-    const int x = S::D == 128 ? c : c >> 1;
-    const uint32_t sel = r >> 2 ? 0x7632u : 0x5410u;
+__device__ __forceinline__ void key_part(uint32_t at, int p, const Query<S> &y, float (&d)[2][4]) {
+    uint32_t w[4];                                       // 8 codes of tokens r, r + 8, r + 16, r + 24, r = lane / 4
+    load_matrices(at, w);
 #pragma unroll
     for (int k = 0; k < 2; k++) {
+        const uint32_t u = w[2 * k], v = w[2 * k + 1], u8 = u >> 8, v8 = v >> 8;
+        mma_f16(d[k], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u, v & 0x00F000F0u, y.q[p][0], y.q[p][1]);
+        mma_f16(d[k], u8 & 0x000F000Fu, v8 & 0x000F000Fu, u8 & 0x00F000F0u, v8 & 0x00F000F0u, y.q[p][2], y.q[p][3]);
+    }
+}
+// The scores of a scale group: s (+)= d times the tokens' scales.
+template <class S>
+__device__ __forceinline__ void add_scores(const float (&d)[2][4], const float (&sc)[4][S::NG], int g, float (&s)[2][4]) {
 #pragma unroll
-        for (int t = 0; t < S::NT; t++)
+    for (int k = 0; k < 2; k++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float p = ex2(s[k][t][i] - z.m[t][i & 1]);
-                s[k][t][i] = p;
-                z.l[t][i & 1] += p;
+        for (int i = 0; i < 4; i++) {
+            const float by = sc[2 * k + i / 2][g];
+            s[k][i] = g ? fmaf(d[k][i], by, s[k][i]) : d[k][i] * by;
+        }
+}
+__device__ __forceinline__ void begin(const float4 &c, float (&d)[2][4]) {
+#pragma unroll
+    for (int k = 0; k < 2; k++) d[k][0] = c.x, d[k][1] = c.y, d[k][2] = c.z, d[k][3] = c.w;
+}
+
+// What a warp has added up of a segment: rows 2 (lane % 4) + i % 2, dims 32 p + 4 (lane / 4) + 2 e + i / 2 (m-tile e, its rows
+// lane / 4 and 8 more).
+template <class S>
+struct Sums {
+    float o[S::kParts][2][4], corr[S::NG][4], m[2], l[2];
+};
+
+// Adds the outputs of the tile at `sm`, whose scores (before the factor f) are s and which the references have been moved for.
+// EDGE: some row does not see all of the tile's tokens; `seen` is how many of them row lane / 4 sees.
+template <class S, bool EDGE>
+__device__ __forceinline__ void outputs(uint32_t magic, const uint8_t *sm, const Query<S> &y, Sums<S> &z, int lane, int seen, const float (&s)[2][4]) {
+    const int c = lane & 3, x = swizzle<S>(lane);
+    const uint8_t *scales = sm + 2 * S::kCodes + S::kScales;
+    uint32_t b[2][S::NG][2];                             // P^T times the scales: row lane / 4, tokens 16 k + 8 e + 2 c + {0, 1}
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            p[i] = ex2(fmaf(s[k][i], y.f[i & 1], -z.m[i & 1]));
+            z.l[i & 1] += p[i];
+        }
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            const uint32_t pt = transpose8(pack_bf16(p[2 * e], p[2 * e + 1]));
+            uint32_t sc[S::NG], mask = 0xFFFFFFFFu;
+            pair_scales<S>(scales, 16 * k + 8 * e + 2 * c, sc);
+            if constexpr (EDGE) {
+                const int n = seen - (16 * k + 8 * e + 2 * c);   // of this pair
+                mask = (n > 0 ? 0x0000FFFFu : 0u) | (n > 1 ? 0xFFFF0000u : 0u);
             }
-        float lo[S::NG], hi[S::NG];
-        load_scales<S>(scales, 16 * k + r, lo);
-        load_scales<S>(scales, 16 * k + r + 8, hi);
-        const uint8_t *at = codes + (16 * k + 2 * c) * S::kRow + 4 * (r & 3);
 #pragma unroll
-        for (int g = 0; g < S::NG; g++) {
-            uint32_t b[S::NT][2];
+            for (int g = 0; g < S::NG; g++) b[k][g][e] = mul_bf16(pt, sc[g]) & mask;
+        }
+    }
+    const uint32_t at = smem_addr(sm) + S::kCodes + lane * S::kRow;
 #pragma unroll
-            for (int t = 0; t < S::NT; t++) {
-                float v[4];
+    for (int g = 0; g < S::NG; g++) {
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    v[i] = s[k][t][i] * (i < 2 ? lo[g] : hi[g]);
-                    if (EDGE && !(seen >> ((k * S::NT + t) * 4 + i) & 1)) v[i] = 0.f;
-                }
-                b[t][0] = transpose8(pack_bf16(v[0], v[1]));
-                b[t][1] = transpose8(pack_bf16(v[2], v[3]));
-                mma_bf16(z.corr[t][g], 0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u, b[t][0], b[t][1]);
-            }
+        for (int k = 0; k < 2; k++) mma_bf16(z.corr[g], 0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u, b[k][g][0], b[k][g][1]);
 #pragma unroll
-            for (int p = g * S::kPer; p < (g + 1) * S::kPer; p++) {
-                const int o = (p ^ x) << 4;
-                const uint32_t u = __byte_perm(*reinterpret_cast<const uint32_t *>(at + o), *reinterpret_cast<const uint32_t *>(at + S::kRow + o), sel);
-                const uint32_t v = __byte_perm(*reinterpret_cast<const uint32_t *>(at + 8 * S::kRow + o),
-                                               *reinterpret_cast<const uint32_t *>(at + 9 * S::kRow + o), sel);
+        for (int p = g * S::kPer; p < (g + 1) * S::kPer; p++) {
+            uint32_t w[4];                               // 4 codes of tokens 2 c, 2 c + 1 (low and high half), 8, 16 and 24 more
+            load_matrices_t(at + ((p ^ x) << 4), w);
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                const uint32_t u = w[2 * k], v = w[2 * k + 1];
                 uint32_t n[2][4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    n[0][i] = ((u >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-                    n[1][i] = ((v >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+                    n[0][i] = ((u >> (4 * i)) & 0x000F000Fu) | magic;
+                    n[1][i] = ((v >> (4 * i)) & 0x000F000Fu) | magic;
                 }
 #pragma unroll
-                for (int t = 0; t < S::NT; t++)
-#pragma unroll
-                    for (int e = 0; e < 2; e++)
-                        mma_bf16(z.o[t][p][e], n[0][2 * e], n[0][2 * e + 1], n[1][2 * e], n[1][2 * e + 1], b[t][0], b[t][1]);
+                for (int e = 0; e < 2; e++) mma_bf16(z.o[p][e], n[0][2 * e], n[0][2 * e + 1], n[1][2 * e], n[1][2 * e + 1], b[k][g][0], b[k][g][1]);
             }
         }
+    }
+}
+template <class S>
+__device__ __forceinline__ void scores(const uint8_t *sm, const Query<S> &y, const float4 (*off)[4], int lane, float (&s)[2][4]) {
+    float sc[4][S::NG];
+#pragma unroll
+    for (int e = 0; e < 4; e++) load_scales<S>(sm + 2 * S::kCodes, 8 * e + (lane >> 2), sc[e]);
+    const uint32_t at = smem_addr(sm) + lane * S::kRow;
+    const int x = swizzle<S>(lane);
+#pragma unroll
+    for (int g = 0; g < S::NG; g++) {
+        float d[2][4];
+        begin(off[g][lane & 3], d);
+#pragma unroll
+        for (int p = g * S::kPer; p < (g + 1) * S::kPer; p++) key_part<S>(at + ((p ^ x) << 4), p, y, d);
+        add_scores<S>(d, sc, g, s);
+    }
+}
+
+// Moves the references, and what has been added up, if some score of the tile is 8 above: that much is seen without a look at the other
+// lanes.
+template <class S>
+__device__ __forceinline__ void move_references(const Query<S> &y, Sums<S> &z, const float (&s)[2][4]) {
+    bool move = false;
+    float now[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        now[i] = fmaxf(fmaxf(s[0][i], s[0][2 + i]), fmaxf(s[1][i], s[1][2 + i]));
+        move |= fmaf(now[i], y.f[i], -z.m[i]) > kGrow;
+    }
+    if (!__any_sync(0xffffffffu, move)) return;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        float m = now[i];
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16)) * y.f[i];
+        if (!(m - z.m[i] > kGrow)) continue;
+        const float f = ex2(z.m[i] - m);
+        z.m[i] = m;
+        z.l[i] *= f;
+#pragma unroll
+        for (int p = 0; p < S::kParts; p++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) z.o[p][e][i] *= f, z.o[p][e][2 + i] *= f;
+#pragma unroll
+        for (int g = 0; g < S::NG; g++) z.corr[g][i] *= f, z.corr[g][2 + i] *= f;
     }
 }
 
 template <class S, bool WEIGH>
-__global__ void __launch_bounds__(kThreads, S::kCtas)
+__global__ void __launch_bounds__(kThreads, 2)
     gqa_attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const GqaAttendArgs a,
                       const AttendPlan plan, long long wait_ns) {
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[kWarps][S::kDepth];
-    __shared__ long long red[kWarps];
-    __shared__ float2 ml[kWarps][S::kRows];
+    __shared__ float2 ml[kWarps][kRows];
+    __shared__ float4 s_off[kWarps][S::NG][4];
     __shared__ int s_abort;
     uint8_t *base = raw + (((smem_addr(raw) + 1023u) & ~1023u) - smem_addr(raw));
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -409,15 +456,13 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     volatile int *abort = &s_abort;
     const int n_kv = a.c.n_kv, G = a.H / n_kv, n_rows = a.n_q * G;
     const int per = WEIGH ? n_kv : n_kv * plan.rg;       // segments of a sequence
-    const long long units = tiles_before(a, a.n_seq, red) * per;
-    if (blockIdx.x == 0)
-        for (int b = tid; b < a.n_seq; b += kThreads) length_of(a, b, !WEIGH);
-    const long long n_cta = min((long long)gridDim.x, units);   // every one of them has a unit
-    if (blockIdx.x >= n_cta) return;
-    const long long u1 = units * (blockIdx.x + 1) / n_cta;
-    long long u = units * blockIdx.x / n_cta;
-    long long first;
-    int b = find_sequence(a, u, per, first, red);
+    if (!WEIGH && blockIdx.x == 0)
+        for (int b = tid; b < a.n_seq; b += kThreads) length_of(a, b, true);
+    const Start start = find_start(a, per, WEIGH ? nullptr : plan.before);
+    if (start.seq < 0) return;
+    const long long units = start.tiles * per, n_cta = working(units, gridDim.x), u1 = units * (blockIdx.x + 1) / n_cta;
+    long long u = start.u, first = start.first;
+    int b = start.seq;
     int slot = 0, par = 0;                               // next stage to be read, parity of its use
     bool ok = true;
     while (u < u1) {
@@ -429,39 +474,32 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         const int mine = (t1 - t0 - warp + kWarps - 1) / kWarps;   // tiles t0 + warp, t0 + warp + 8, ...
         const uint64_t deadline = deadline_after(wait_ns, max(mine, 0));
         for (int set = WEIGH ? 0 : seg - h * plan.rg, sets = WEIGH ? plan.rg : set + 1; set < sets; set++) {
-            const int r0 = set * S::kRows;
-            // copies: lane i holds the page of the i-th box from `base_tile` on
-            int ids = 0, base_tile = 0;
-            const int per_load = 32 / plan.boxes;
+            const int r0 = set * kRows;
+            // copies: lane i holds the first row of the i-th box from `base_tile` on
+            int first_row = 0, base_tile = 0;
+            const int per_load = 32 / plan.boxes, box_rows = kTile / plan.boxes;
             auto look_up = [&](int i) {                  // whole warp, tiles i, i + 1, ... of this warp
                 base_tile = i;
                 const int t = t0 + warp + kWarps * (i + lane / plan.boxes), tok = t * kTile + (plan.boxes == 2 ? 16 * (lane & 1) : 0);
-                ids = 0;
+                first_row = 0;
                 if (tok < len && i + lane / plan.boxes < mine) {
-                    ids = pages[tok / a.c.page];
-                    if (ids < 0 || ids >= a.c.n_pages) {
-                        mla_bad_index(a.err);
-                        ids = 0;                         // that page's rows: the output is unspecified
-                    }
+                    const int p = tok / a.c.page, id = pages[p];
+                    if (id < 0 || id >= a.c.n_pages) mla_bad_index(a.err);   // the cache's first rows: the output is unspecified
+                    else first_row = (int)gqa_row(a.c, id, h) + tok - p * a.c.page;
                 }
             };
             auto ask = [&](int i, int stage) {           // whole warp
                 if (i - base_tile >= per_load) look_up(i);
-                const int tok = (t0 + warp + kWarps * i) * kTile;
                 const uint32_t dst = smem_addr(ring + stage * S::kStage);
-                uint64_t *bar = &full[warp][stage];
-                const int n = plan.boxes == 1 || tok + 16 < len ? plan.boxes : 1, rows = kTile / plan.boxes;
-                expect_bytes(bar, (uint32_t)(n * rows) * (WEIGH ? S::kRow + S::NG * 2 : 2 * (S::kRow + S::NG * 2)));
-                for (int k = 0; k < n; k++) {
-                    const int id = __shfl_sync(0xffffffffu, ids, (i - base_tile) * plan.boxes + k);
-                    const long long row = gqa_row(a.c, id, h) + (tok + 16 * k) % a.c.page;
-                    const uint32_t o = dst + k * 16 * S::kRow, so = dst + 2 * S::kCodes + k * 16 * S::NG * 2;
-                    tma_box(o, &k_map, 0, (int)row, bar);
-                    bulk_copy(so, a.c.ks + row * S::NG, rows * S::NG * 2, bar);
-                    if (!WEIGH) {
-                        tma_box(o + S::kCodes, &v_map, 0, (int)row, bar);
-                        bulk_copy(so + S::kScales, a.c.vs + row * S::NG, rows * S::NG * 2, bar);
-                    }
+                const bool two = plan.boxes == 2 && (t0 + warp + kWarps * i) * kTile + 16 < len;
+                const uint32_t bytes = (two ? kTile : box_rows) * (WEIGH ? 1 : 2) * (S::kRow + S::NG * 2);
+                const int row = __shfl_sync(0xffffffffu, first_row, (i - base_tile) * plan.boxes);
+                fill<!WEIGH, true>(dst, S::kCodes, dst + 2 * S::kCodes, S::kScales, &k_map, &v_map, row, a.c.ks + (long long)row * S::NG,
+                             a.c.vs + (long long)row * S::NG, box_rows * S::NG * 2, &full[warp][stage], bytes);
+                if (two) {
+                    const int next = __shfl_sync(0xffffffffu, first_row, (i - base_tile) * 2 + 1);
+                    fill<!WEIGH, false>(dst + 16 * S::kRow, S::kCodes, dst + 2 * S::kCodes + 16 * S::NG * 2, S::kScales, &k_map, &v_map, next,
+                                   a.c.ks + (long long)next * S::NG, a.c.vs + (long long)next * S::NG, 16 * S::NG * 2, &full[warp][stage], 0);
                 }
             };
             if (mine > 0) look_up(0);
@@ -471,42 +509,48 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 ask(i, st);
             }
             Query<S> y;
-            load_query<S>(a, b, h, r0, lane, y);
+            float4(*off)[4] = s_off[warp];
+            load_query<S>(a, b, h, r0, lane, y, off);
             Sums<S> z;
-            float2 stat[S::NT][2];
+            float2 stat[2];
             if constexpr (WEIGH) {
 #pragma unroll
-                for (int t = 0; t < S::NT; t++)
-#pragma unroll
-                    for (int i = 0; i < 2; i++)
-                        stat[t][i] = plan.stat[((long long)(b * (long long)n_kv + h) * plan.rg + set) * S::kRows + 8 * t + 2 * (lane & 3) + i];
+                for (int i = 0; i < 2; i++)
+                    stat[i] = plan.stat[((long long)(b * (long long)n_kv + h) * plan.rg + set) * kRows + 2 * (lane & 3) + i];
             } else {
 #pragma unroll
-                for (int t = 0; t < S::NT; t++) {
+                for (int i = 0; i < 2; i++) z.m[i] = kNone, z.l[i] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 2; i++) z.m[t][i] = kNone, z.l[t][i] = 0.f;
+                for (int i = 0; i < 4; i++) {
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
+                    for (int p = 0; p < S::kParts; p++) z.o[p][0][i] = z.o[p][1][i] = 0.f;
 #pragma unroll
-                        for (int p = 0; p < S::kParts; p++) z.o[t][p][0][i] = z.o[t][p][1][i] = 0.f;
-#pragma unroll
-                        for (int g = 0; g < S::NG; g++) z.corr[t][g][i] = 0.f;
-                    }
+                    for (int g = 0; g < S::NG; g++) z.corr[g][i] = 0.f;
                 }
             }
-            for (int i = 0; i < mine; i++) {
+            // the stage that comes next, when it has come
+            auto arrived = [&]() {
                 if (ok && !warp_wait_now(&full[warp][slot], par, deadline, abort, lane)) {
                     ok = false;
                     *abort = 1;
                     atomicCAS(a.err, 0, (int)DEV_ERR_TIMEOUT);
                 }
-                if (!ok) break;
                 const uint8_t *sm = ring + slot * S::kStage;
-                const int tok = (t0 + warp + kWarps * i) * kTile;
-                const bool edge = tok + kTile > len - (a.n_q - 1);
-                if constexpr (WEIGH) {
-                    float s[2][S::NT][4];
-                    scores<S>(sm, sm + 2 * S::kCodes, y, lane, s);
+                if (++slot == S::kDepth) {
+                    slot = 0;
+                    par ^= 1;
+                }
+                return sm;
+            };
+            auto limit_of = [&](int row) { return min(len - (a.n_q - 1 - (r0 + row) / G), len); };   // tokens that a row sees
+            auto token_of = [&](int i) { return (t0 + warp + kWarps * i) * kTile; };
+            if constexpr (WEIGH) {
+                for (int i = 0; i < mine; i++) {
+                    const uint8_t *sm = arrived();
+                    if (!ok) break;
+                    const int tok = token_of(i);
+                    float s[2][4];
+                    scores<S>(sm, y, off, lane, s);
 #pragma unroll
                     for (int k = 0; k < 2; k++)
 #pragma unroll
@@ -514,13 +558,10 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                             const int t = tok + 16 * k + (lane >> 2) + 8 * e;
                             float w = 0.f;
 #pragma unroll
-                            for (int n = 0; n < S::NT; n++)
-#pragma unroll
-                                for (int i = 0; i < 2; i++) {
-                                    const int row = r0 + 8 * n + 2 * (lane & 3) + i;
-                                    if (row < n_rows && t < len - (a.n_q - 1 - row / G))
-                                        w += ex2(s[k][n][2 * e + i] - stat[n][i].x) * stat[n][i].y;
-                                }
+                            for (int j = 0; j < 2; j++) {
+                                const int row = 2 * (lane & 3) + j;
+                                if (r0 + row < n_rows && t < limit_of(row)) w += ex2(fmaf(s[k][2 * e + j], y.f[j], -stat[j].x)) * stat[j].y;
+                            }
                             w += __shfl_xor_sync(0xffffffffu, w, 1);
                             w += __shfl_xor_sync(0xffffffffu, w, 2);
                             if ((lane & 3) == 0 && t < len) {
@@ -528,54 +569,60 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                                 if (page >= 0 && page < a.c.n_pages) atomicAdd(a.c.w + gqa_row(a.c, page, h) + t % a.c.page, w);
                             }
                         }
-                } else if (edge) {
-                    tile<S, true>(a, sm, y, z, lane, r0, tok, len);
-                } else {
-                    tile<S, false>(a, sm, y, z, lane, r0, tok, len);
+                    __syncwarp();
+                    if (i + S::kDepth < mine) ask(i + S::kDepth, (int)(sm - ring) / (int)S::kStage);
                 }
-                __syncwarp();
-                if (i + S::kDepth < mine) ask(i + S::kDepth, slot);
-                if (++slot == S::kDepth) {
-                    slot = 0;
-                    par ^= 1;
+            } else {
+                for (int i = 0; i < mine; i++) {
+                    const uint8_t *sm = arrived();
+                    if (!ok) break;
+                    float s[2][4];
+                    scores<S>(sm, y, off, lane, s);
+                    const bool edge = token_of(i) + kTile > len - (a.n_q - 1);
+                    if (edge)
+#pragma unroll
+                        for (int k = 0; k < 2; k++)
+#pragma unroll
+                            for (int j = 0; j < 4; j++)
+                                if (token_of(i) + 16 * k + (lane >> 2) + 8 * (j / 2) >= limit_of(2 * (lane & 3) + j % 2)) s[k][j] = -INFINITY;
+                    move_references<S>(y, z, s);
+                    if (edge) outputs<S, true>(plan.magic, sm, y, z, lane, limit_of(lane >> 2) - token_of(i), s);
+                    else outputs<S, false>(plan.magic, sm, y, z, lane, kTile, s);
+                    __syncwarp();
+                    if (i + S::kDepth < mine) ask(i + S::kDepth, (int)(sm - ring) / (int)S::kStage);
                 }
             }
             if constexpr (!WEIGH) {
                 // ------------------------------------------------------ the warps' sums become the segment's
 #pragma unroll
-                for (int t = 0; t < S::NT; t++)
-#pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        float l = z.l[t][i];
-                        l += __shfl_xor_sync(0xffffffffu, l, 4);
-                        l += __shfl_xor_sync(0xffffffffu, l, 8);
-                        l += __shfl_xor_sync(0xffffffffu, l, 16);
-                        if (lane < 4) ml[warp][8 * t + 2 * lane + i] = make_float2(z.m[t][i], l);
-                    }
+                for (int i = 0; i < 2; i++) {
+                    float l = z.l[i];
+                    l += __shfl_xor_sync(0xffffffffu, l, 4);
+                    l += __shfl_xor_sync(0xffffffffu, l, 8);
+                    l += __shfl_xor_sync(0xffffffffu, l, 16);
+                    if (lane < 4) ml[warp][2 * lane + i] = make_float2(z.m[i], l);
+                }
                 __syncthreads();
                 float *mine_o = reinterpret_cast<float *>(ring);
 #pragma unroll
-                for (int t = 0; t < S::NT; t++)
+                for (int i = 0; i < 2; i++) {
+                    const int row = 2 * (lane & 3) + i;
+                    float m = ml[0][row].x;
 #pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        const int row = 8 * t + 2 * (lane & 3) + i;
-                        float m = ml[0][row].x;
+                    for (int w = 1; w < kWarps; w++) m = fmaxf(m, ml[w][row].x);
+                    const float f = ex2(z.m[i] - m);
 #pragma unroll
-                        for (int w = 1; w < kWarps; w++) m = fmaxf(m, ml[w][row].x);
-                        const float f = ex2(z.m[t][i] - m);
-#pragma unroll
-                        for (int p = 0; p < S::kParts; p++) {
-                            const float *cr = z.corr[t][p / S::kPer];
-                            const int r = lane >> 2;
-                            *reinterpret_cast<float4 *>(mine_o + row * S::D + 32 * p + 8 * (r & 3) + 4 * (r >> 2)) =
-                                make_float4((z.o[t][p][0][i] + cr[i]) * f, (z.o[t][p][0][2 + i] + cr[2 + i]) * f,
-                                            (z.o[t][p][1][i] + cr[i]) * f, (z.o[t][p][1][2 + i] + cr[2 + i]) * f);
-                        }
+                    for (int p = 0; p < S::kParts; p++) {
+                        const float *cr = z.corr[p / S::kPer];
+                        *reinterpret_cast<float4 *>(mine_o + row * S::D + 32 * p + 4 * (lane >> 2)) =
+                            make_float4((z.o[p][0][i] + cr[i]) * f, (z.o[p][0][2 + i] + cr[2 + i]) * f, (z.o[p][1][i] + cr[i]) * f,
+                                        (z.o[p][1][2 + i] + cr[2 + i]) * f);
                     }
+                }
                 __syncthreads();
                 const bool whole = t0 == 0 && t1 == nt;
-                float *part = plan.part + ((long long)blockIdx.x * 2 + (t0 == 0)) * S::kRows * (S::D + 2);
-                for (int i = tid; i < S::kRows * (S::D / 4); i += kThreads) {
+                float *part = plan.part + ((long long)blockIdx.x * 2 + (t0 == 0)) * kRows * (S::D + 2);
+                for (int i = tid; i < kRows * (S::D / 4); i += kThreads) {
                     const int row = i / (S::D / 4), d = 4 * (i % (S::D / 4));
                     float m = ml[0][row].x, l = 0.f;
 #pragma unroll
@@ -590,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                     }
                     if (!whole) {
                         *reinterpret_cast<float4 *>(part + row * S::D + d) = o;
-                        if (d == 0) *reinterpret_cast<float2 *>(part + S::kRows * S::D + 2 * row) = make_float2(m, l);
+                        if (d == 0) *reinterpret_cast<float2 *>(part + kRows * S::D + 2 * row) = make_float2(m, l);
                         continue;
                     }
                     const int at = r0 + row;
@@ -605,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
                     if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
                     if (d == 0 && a.weigh)
-                        plan.stat[((long long)(b * (long long)n_kv + h) * plan.rg + set) * S::kRows + row] = make_float2(m, inv);
+                        plan.stat[((long long)(b * (long long)n_kv + h) * plan.rg + set) * kRows + row] = make_float2(m, inv);
                 }
                 fence_async_smem();
                 __syncthreads();
@@ -625,37 +672,88 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
 
 // One CTA per segment: joins the parts of one that several CTAs had, fills one without tokens.
 template <class S>
-__global__ void __launch_bounds__(kThreads) gqa_join_kernel(const GqaAttendArgs a, const AttendPlan plan) {
-    __shared__ long long red[kWarps];
+__global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, const AttendPlan plan) {
     const int n_kv = a.c.n_kv, G = a.H / n_kv, n_rows = a.n_q * G, per = n_kv * plan.rg;
     const int b = blockIdx.x / per, seg = blockIdx.x - b * per, h = seg / plan.rg, set = seg - h * plan.rg;
     pdl_wait();
     pdl_trigger();
-    const int nt = tiles_of(a, b);
-    const long long units = tiles_before(a, a.n_seq, red) * per;
-    const long long u0 = tiles_before(a, b, red) * per + (long long)seg * nt;
+    const long long before = plan.before[b], units = plan.before[a.n_seq] * per;
+    const int nt = (int)(plan.before[b + 1] - before);
+    const long long u0 = before * per + (long long)seg * nt;
     int c0 = 0, c1 = -1;
     if (nt > 0) {
         // the CTA of unit u is the largest c with units * c / n <= u, of the n that have units
-        const long long n = min((long long)plan.n_cta, units);
+        const long long n = working(units, plan.n_cta);
         c0 = (int)(((u0 + 1) * n - 1) / units);
         c1 = (int)(((u0 + nt) * n - 1) / units);
         if (c0 == c1) return;
     }
-    constexpr int kPart = S::kRows * (S::D + 2);
-    for (int i = threadIdx.x; i < S::kRows * (S::D / 4); i += kThreads) {
-        const int row = i / (S::D / 4), d = 4 * (i % (S::D / 4)), at = set * S::kRows + row;
-        if (at >= n_rows) continue;
-        float m = kNone, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0; c <= c1; c++) {
-            const float *part = plan.part + ((long long)c * 2 + (c == c0)) * kPart;
-            const float2 ml = *reinterpret_cast<const float2 *>(part + S::kRows * S::D + 2 * row);
-            const float4 x = *reinterpret_cast<const float4 *>(part + row * S::D + d);
-            const float now = fmaxf(m, ml.x), f = ex2(m - now), g = ex2(ml.x - now);
-            m = now;
-            l = l * f + ml.y * g;
-            o = make_float4(o.x * f + x.x * g, o.y * f + x.y * g, o.z * f + x.z * g, o.w * f + x.w * g);
+    // Part c's factor per row in shared memory (parts in groups of kGroup), then the sums: threads of a row's dims take every kSplit-th
+    // part with kAhead of them in flight, in a fixed order.
+    constexpr int kPart = kRows * (S::D + 2), kCols = S::D / 4, kSplit = kJoin / (kRows * kCols), kAhead = 4;
+    __shared__ float factor[kGroup][kRows];
+    __shared__ float4 sum[kSplit][kRows][kCols];
+    __shared__ float s_m[kRows], s_l[kRows];
+    const int tid = threadIdx.x, row = tid / kCols % kRows, d = 4 * (tid % kCols), lot = tid / (kCols * kRows);
+    if (tid < kRows) s_m[tid] = kNone, s_l[tid] = 0.f;
+    auto part = [&](int c) { return plan.part + ((long long)c * 2 + (c == c0)) * kPart; };
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int g0 = c0; g0 <= c1; g0 += kGroup) {
+        const int n = min(kGroup, c1 - g0 + 1);
+        __syncthreads();
+        const float old = s_m[row];
+        __syncthreads();
+        // a warp per row, its lanes the parts
+        for (int r = tid >> 5; r < kRows; r += kJoin / 32) {
+            float m = kNone, l = 0.f;
+            float2 ml[kGroup / 32];
+#pragma unroll
+            for (int k = 0; k < kGroup / 32; k++) {
+                const int c = (tid & 31) + 32 * k;
+                ml[k] = c < n ? *reinterpret_cast<const float2 *>(part(g0 + c) + kRows * S::D + 2 * r) : make_float2(kNone, 0.f);
+                m = fmaxf(m, ml[k].x);
+            }
+            m = fmaxf(m, s_m[r]);
+#pragma unroll
+            for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+#pragma unroll
+            for (int k = 0; k < kGroup / 32; k++) {
+                const float f = ex2(ml[k].x - m);
+                factor[(tid & 31) + 32 * k][r] = f;
+                l += ml[k].y * f;
+            }
+#pragma unroll
+            for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+            __syncwarp();
+            if ((tid & 31) == 0) {
+                s_l[r] = s_l[r] * ex2(s_m[r] - m) + l;
+                s_m[r] = m;
+            }
+        }
+        __syncthreads();
+        const float f0 = ex2(old - s_m[row]);
+        o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+        for (int i = lot; i < n; i += kSplit * kAhead) {
+            float4 x[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; k++)
+                x[k] = i + k * kSplit < n ? *reinterpret_cast<const float4 *>(part(g0 + i + k * kSplit) + row * S::D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kAhead; k++) {
+                const float f = i + k * kSplit < n ? factor[i + k * kSplit][row] : 0.f;
+                o = make_float4(fmaf(x[k].x, f, o.x), fmaf(x[k].y, f, o.y), fmaf(x[k].z, f, o.z), fmaf(x[k].w, f, o.w));
+            }
+        }
+    }
+    sum[lot][row][d / 4] = o;
+    __syncthreads();
+    const int at = set * kRows + row;
+    if (lot == 0 && at < n_rows) {
+        const float m = s_m[row], l = s_l[row];
+#pragma unroll
+        for (int k = 1; k < kSplit; k++) {
+            const float4 x = sum[k][row][d / 4];
+            o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
         }
         const float inv = l != 0.f ? 1.f / l : 0.f;
         const long long orow = (long long)(b * (long long)a.n_q + at / G) * a.H + h * G + at % G;
@@ -665,7 +763,7 @@ __global__ void __launch_bounds__(kThreads) gqa_join_kernel(const GqaAttendArgs 
         else
             *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + orow * S::D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
         if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-        if (d == 0 && a.weigh) plan.stat[(long long)blockIdx.x * S::kRows + row] = make_float2(m, inv);
+        if (d == 0 && a.weigh) plan.stat[(long long)blockIdx.x * kRows + row] = make_float2(m, inv);
     }
 }
 
@@ -684,19 +782,15 @@ cudaError_t code_map(const void *p, int bytes, long long rows, int box_rows, CUt
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Sets of 8 query rows that a CTA has: 2 where the group's rows need them.
-int sets_of(const GqaAttendArgs &a) { return (long long)a.n_q * (a.H / a.c.n_kv) > 8 ? 2 : 1; }
-int row_groups(const GqaAttendArgs &a) {
-    const int rows = a.n_q * (a.H / a.c.n_kv), each = 8 * sets_of(a);
-    return (rows + each - 1) / each;
-}
+// Sets of 8 query rows of a head.
+int row_groups(const GqaAttendArgs &a) { return (a.n_q * (a.H / a.c.n_kv) + kRows - 1) / kRows; }
 // CTAs: all that fit, no more than units that the page tables could hold.
-int grid_of(const GqaAttendArgs &a, int n_sm, int ctas) {
+int grid_of(const GqaAttendArgs &a, int n_sm) {
     const double most = (double)a.n_seq * (a.pages_stride * a.c.page / kTile + 1) * a.c.n_kv * row_groups(a);
-    return (int)std::min((double)(ctas * n_sm), most);
+    return (int)std::min(2.0 * n_sm, most);
 }
 size_t part_bytes(const GqaAttendArgs &a, int n_cta) {
-    return round256((size_t)n_cta * 2 * 8 * sets_of(a) * (a.c.dim + 2) * sizeof(float));
+    return round256((size_t)n_cta * 2 * kRows * (a.c.dim + 2) * sizeof(float));
 }
 
 template <class S>
@@ -704,9 +798,11 @@ cudaError_t run(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *
     AttendPlan plan;
     plan.rg = row_groups(a);
     plan.boxes = a.c.page % kTile ? 2 : 1;
-    plan.n_cta = grid_of(a, d.n_sm, S::kCtas);
+    plan.n_cta = grid_of(a, d.n_sm);
     plan.part = (float *)d.scratch;
-    plan.stat = (float2 *)((char *)d.scratch + part_bytes(a, plan.n_cta));
+    plan.magic = 0x43004300u;
+    plan.before = (long long *)((char *)d.scratch + part_bytes(a, plan.n_cta));
+    plan.stat = (float2 *)((char *)plan.before + round256((size_t)(a.n_seq + 1) * sizeof(long long)));
     CUtensorMap k, v;
     const long long rows = (long long)a.c.n_pages * a.c.n_kv * a.c.page;
     if (cudaError_t e = code_map(a.c.k, S::kRow, rows, kTile / plan.boxes, &k)) return e;
@@ -715,32 +811,27 @@ cudaError_t run(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *
     if (cudaError_t e = allow_smem(gqa_attend_kernel<S, false>, S::kSmem, d.device, done)) return e;
     if (cudaError_t e = launch_pdl(gqa_attend_kernel<S, false>, dim3(plan.n_cta), dim3(kThreads), S::kSmem, st, k, v, a, plan, d.wait_ns)) return e;
     *n_launch = 2;
-    if (cudaError_t e = launch_pdl(gqa_join_kernel<S>, dim3((unsigned)a.n_seq * a.c.n_kv * plan.rg), dim3(kThreads), 0, st, a, plan)) return e;
+    if (cudaError_t e = launch_pdl(gqa_join_kernel<S>, dim3((unsigned)a.n_seq * a.c.n_kv * plan.rg), dim3(kJoin), 0, st, a, plan)) return e;
     if (!a.weigh) return cudaSuccess;
     *n_launch = 3;
     if (cudaError_t e = allow_smem(gqa_attend_kernel<S, true>, S::kSmem, d.device, done_weigh)) return e;
     return launch_pdl(gqa_attend_kernel<S, true>, dim3(plan.n_cta), dim3(kThreads), S::kSmem, st, k, v, a, plan, d.wait_ns);
 }
 
-template <int D, int NG>
-cudaError_t by_rows(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch) {
-    return sets_of(a) == 1 ? run<Shape<D, NG, 1>>(a, d, st, n_launch) : run<Shape<D, NG, 2>>(a, d, st, n_launch);
-}
-
 }  // namespace
 
 size_t gqa_attend_scratch(const GqaAttendArgs &a, int n_sm) {
-    const int n_cta = grid_of(a, n_sm, sets_of(a) == 1 ? 2 : 1);
-    return part_bytes(a, n_cta) + (a.weigh ? (size_t)a.n_seq * a.c.n_kv * row_groups(a) * 8 * sets_of(a) * sizeof(float2) : 0);
+    const int n_cta = grid_of(a, n_sm);
+    return part_bytes(a, n_cta) + round256((size_t)(a.n_seq + 1) * sizeof(long long)) + (a.weigh ? (size_t)a.n_seq * a.c.n_kv * row_groups(a) * kRows * sizeof(float2) : 0);
 }
 
 cudaError_t launch_gqa_attend(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch) {
     switch (a.c.dim * 8 + a.c.dim / a.c.gs) {
-        case 64 * 8 + 1: return by_rows<64, 1>(a, d, st, n_launch);
-        case 64 * 8 + 2: return by_rows<64, 2>(a, d, st, n_launch);
-        case 128 * 8 + 1: return by_rows<128, 1>(a, d, st, n_launch);
-        case 128 * 8 + 2: return by_rows<128, 2>(a, d, st, n_launch);
-        default: return by_rows<128, 4>(a, d, st, n_launch);
+        case 64 * 8 + 1: return run<Shape<64, 1>>(a, d, st, n_launch);
+        case 64 * 8 + 2: return run<Shape<64, 2>>(a, d, st, n_launch);
+        case 128 * 8 + 1: return run<Shape<128, 1>>(a, d, st, n_launch);
+        case 128 * 8 + 2: return run<Shape<128, 2>>(a, d, st, n_launch);
+        default: return run<Shape<128, 4>>(a, d, st, n_launch);
     }
 }
 

@@ -32,74 +32,102 @@ __device__ __forceinline__ void load8(const void *base, long long e, float (&x)[
     }
 }
 
-// One thread per 8 elements of a token's key or value row, gs / 8 neighbouring threads per group.
+// x / b to nearest from r, the reciprocal of b to nearest, by a step with the exact remainder (Markstein, IBM J. Res. Dev. 1990): 3
+// instructions where a division has about 20.  The theorem wants x r within an ulp of the quotient; for b = 7 and every b of 8 bits
+// the result was compared with the quotient for all x of seven binades, as far from overflow and underflow as its caller sees to.
+__device__ __forceinline__ float divide(float x, float b, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(-q, b, x), r, q);
+}
+
+// 8 elements of a group that GS / 8 neighbouring threads have: their codes, and the group's scale.
+template <int GS>
+__device__ __forceinline__ uint32_t quantise(const float (&x)[8], __nv_bfloat16 &stored) {
+    uint32_t m = 0;                                      // max|x| as an integer: above infinity for a NaN
+#pragma unroll
+    for (int i = 0; i < 8; i++) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = 1; o < GS / 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float amax = __uint_as_float(m);
+    uint32_t w = 0;
+    if (amax >= 1e-30f && m < 0x7F800000u) {
+        // max|x| / scale <= 7 (1 + 2^-8): no code needs the clamp.  q + 1.5 2^23 + 8 has rint(q) + 8 in its low bits.
+        stored = __float2bfloat16_rn(divide(amax, 7.f, 1.f / 7.f));
+        const float b = __bfloat162float(stored), r = __frcp_rn(b);
+#pragma unroll
+        for (int i = 7; i >= 0; i--) w = 16 * w + (__float_as_uint(divide(x[i], b, r) + 12582920.f) - 0x4B400000u);
+        return w;
+    }
+    if (m >= 0x7F800000u) {
+        stored = __float2bfloat16_rn(__uint_as_float(0x7FC00000u));
+        return 0x88888888u;
+    }
+    stored = __float2bfloat16_rn(__fdiv_rn(amax, 7.f));
+    const float b = __bfloat162float(stored), by = b > 0.f ? b : 1.f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) w |= (uint32_t)(__float2int_rn(fminf(fmaxf(__fdiv_rn(x[i], by), -8.f), 7.f)) + 8) << (4 * i);
+    return w;
+}
+
+// One thread per 8 elements of a token's key and of its value.
 template <bool BF16, int GS>
 __global__ void __launch_bounds__(kThreads) gqa_append_kernel(const GqaAppendArgs a) {
     const int upr = a.c.dim / 8;                         // 8 or 16
-    const uint32_t row = blockIdx.x * (kThreads / upr) + threadIdx.x / upr, heads = 2 * a.c.n_kv;
+    const uint32_t row = blockIdx.x * (kThreads / upr) + threadIdx.x / upr;
     const int u = threadIdx.x & (upr - 1);
-    const uint32_t t = row / heads, h2 = row - t * heads;
-    const bool value = h2 >= (uint32_t)a.c.n_kv;
-    const int h = value ? h2 - a.c.n_kv : h2;
+    const uint32_t t = row / a.c.n_kv;
+    const int h = row - t * a.c.n_kv;
     const bool live = t < (uint32_t)a.T;
     pdl_wait();
     pdl_trigger();
-    float x[8];
+    float k[8], v[8];
     long long slot = -1;
     if (live) {
         slot = a.slots[t];
-        load8<BF16>(value ? a.v : a.k, t * (value ? a.v_stride : a.k_stride) + h * a.c.dim + 8 * u, x);
+        load8<BF16>(a.k, t * a.k_stride + h * a.c.dim + 8 * u, k);
+        load8<BF16>(a.v, t * a.v_stride + h * a.c.dim + 8 * u, v);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = 0.f;
+        for (int i = 0; i < 8; i++) k[i] = v[i] = 0.f;
     }
-    float m = 0.f;
-    bool fine = true;
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        m = fmaxf(m, fabsf(x[i]));
-        fine = fine && fabsf(x[i]) <= 3.402823466e38f;   // neither NaN nor infinite
-    }
-    if (!fine) m = INFINITY;
-#pragma unroll
-    for (int o = 1; o < GS / 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    __nv_bfloat16 ks, vs;
+    const uint32_t kw = quantise<GS>(k, ks), vw = quantise<GS>(v, vs);
     if (!live || slot == -1) return;
     if (slot < 0 || slot >= (long long)a.c.n_pages * a.c.page) {
         mla_bad_index(a.err);
         return;
     }
-    fine = m < INFINITY;
-    const __nv_bfloat16 stored = __float2bfloat16_rn(fine ? __fdiv_rn(m, 7.f) : __uint_as_float(0x7FC00000u));
-    const float scale = __bfloat162float(stored), by = scale > 0.f ? scale : 1.f;
-    uint32_t w = 0x88888888u;
-    if (fine) {
-        w = 0;
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int c = __float2int_rn(fminf(fmaxf(__fdiv_rn(x[i], by), -8.f), 7.f)) + 8;
-            w |= (uint32_t)c << (4 * i);
-        }
+    const int at = (int)slot, page = at / a.c.page;      // n_pages * page_size < 2^31
+    const long long r = gqa_row(a.c, page, h) + (at - page * a.c.page);
+    reinterpret_cast<uint32_t *>(a.c.k)[r * upr + u] = kw;
+    reinterpret_cast<uint32_t *>(a.c.v)[r * upr + u] = vw;
+    if (u % (GS / 8) == 0) {
+        a.c.ks[r * (a.c.dim / GS) + u / (GS / 8)] = ks;
+        a.c.vs[r * (a.c.dim / GS) + u / (GS / 8)] = vs;
     }
-    const int page = (int)(slot / a.c.page);
-    const long long r = gqa_row(a.c, page, h) + (slot - (long long)page * a.c.page);
-    reinterpret_cast<uint32_t *>(value ? a.c.v : a.c.k)[r * upr + u] = w;
-    if (u % (GS / 8) == 0) (value ? a.c.vs : a.c.ks)[r * (a.c.dim / GS) + u / (GS / 8)] = stored;
-    if (u == 0 && !value && a.c.w) a.c.w[r] = 0.f;
+    if (u == 0 && a.c.w) a.c.w[r] = 0.f;
 }
 
-// kReadRows tokens of one head per CTA: as many threads find the tokens' rows, then every thread moves units of 8 elements,
-// keys first.
+// kReadRows tokens of one head per CTA: as many threads find the tokens' rows, then every thread moves units of 8 elements.
 constexpr int kReadRows = 32;
 
+// The values of a word of codes.  bf16: 128 + code by an OR, minus 136 exactly, times the scale to nearest: the same as the f32
+// product, which is exact, rounded.
 template <bool OB>
-__device__ __forceinline__ void store8(void *base, long long e, uint32_t w, float scale) {
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) x[i] = (__uint_as_float(0x4B000000u | ((w >> (4 * i)) & 15u)) - 8388616.f) * scale;   // 2^23 + code
+__device__ __forceinline__ void store8(void *base, long long e, uint32_t w, uint32_t scale) {
     if constexpr (OB) {
-        *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(base) + e) =
-            make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        const uint32_t up = w >> 4;
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            x[i] = (__byte_perm(w, up, (4 + i) << 8 | i) & 0x000F000Fu) | 0x43004300u;   // codes 2 i, 2 i + 1
+            asm("sub.rn.bf16x2 %0, %0, %1;\n mul.rn.bf16x2 %0, %0, %2;" : "+r"(x[i]) : "r"(0x43084308u), "r"(scale * 0x10001u));
+        }
+        *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(base) + e) = make_uint4(x[0], x[1], x[2], x[3]);
     } else {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] = (__uint_as_float(0x4B000000u | ((w >> (4 * i)) & 15u)) - 8388616.f) * __uint_as_float(scale << 16);
         float4 *d = reinterpret_cast<float4 *>(reinterpret_cast<float *>(base) + e);
         d[0] = make_float4(x[0], x[1], x[2], x[3]);
         d[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -108,14 +136,14 @@ __device__ __forceinline__ void store8(void *base, long long e, uint32_t w, floa
 
 template <bool OB, int D>
 __global__ void __launch_bounds__(kThreads) gqa_read_kernel(const GqaReadArgs a) {
-    constexpr int kUnits = D / 8, kEach = 2 * kReadRows * kUnits / kThreads;
-    __shared__ long long s_row[kReadRows];    // -1: a zero row, -2: not to be written
+    constexpr int kUnits = D / 8, kStep = kThreads / kUnits, kEach = kReadRows / kStep;   // a thread's unit, every kStep-th row
+    __shared__ int s_row[kReadRows];          // -1: a zero row, -2: not to be written
     const int r0 = blockIdx.x * kReadRows, h = blockIdx.y;
     pdl_wait();
     pdl_trigger();
     if (threadIdx.x < kReadRows) {
         const int r = r0 + threadIdx.x;
-        long long row = -2;
+        int row = -2;
         if (r < a.T && r < a.cu[a.n_seq] && r >= a.cu[0]) {
             int lo = 0, hi = a.n_seq;         // cu[lo] <= r < cu[hi]
             while (hi - lo > 1) {
@@ -130,39 +158,38 @@ __global__ void __launch_bounds__(kThreads) gqa_read_kernel(const GqaReadArgs a)
                 mla_bad_index(a.err);
                 row = -1;
             } else {
-                row = gqa_row(a.c, id, h) + (i - pi * a.c.page);
+                row = (int)gqa_row(a.c, id, h) + (i - pi * a.c.page);
             }
         }
         s_row[threadIdx.x] = row;
     }
     __syncthreads();
-    const int ng = D / a.c.gs, per = a.c.gs / 8;
-    uint32_t w[kEach];
-    float sc[kEach];
+    const int u = threadIdx.x % kUnits, r1 = threadIdx.x / kUnits, ng = D / a.c.gs, g = 8 * u / a.c.gs;
+    uint32_t kw[kEach], vw[kEach], ks[kEach], vs[kEach];
 #pragma unroll
-    for (int k = 0; k < kEach; k++) {
-        const int i = threadIdx.x + k * kThreads, u = i % kUnits, r = i / kUnits % kReadRows;
-        const bool value = i >= kReadRows * kUnits;
-        const long long row = s_row[r];
-        w[k] = 0x88888888u;
-        sc[k] = 0.f;
+    for (int i = 0; i < kEach; i++) {
+        const int row = s_row[r1 + i * kStep];
+        kw[i] = vw[i] = 0x88888888u;
+        ks[i] = vs[i] = 0;
         if (row >= 0) {
-            w[k] = reinterpret_cast<const uint32_t *>(value ? a.c.v : a.c.k)[row * kUnits + u];
-            sc[k] = __bfloat162float((value ? a.c.vs : a.c.ks)[row * ng + u / per]);
+            kw[i] = reinterpret_cast<const uint32_t *>(a.c.k)[(long long)row * kUnits + u];
+            vw[i] = reinterpret_cast<const uint32_t *>(a.c.v)[(long long)row * kUnits + u];
+            ks[i] = reinterpret_cast<const uint16_t *>(a.c.ks)[(long long)row * ng + g];
+            vs[i] = reinterpret_cast<const uint16_t *>(a.c.vs)[(long long)row * ng + g];
         }
     }
 #pragma unroll
-    for (int k = 0; k < kEach; k++) {
-        const int i = threadIdx.x + k * kThreads, u = i % kUnits, r = i / kUnits % kReadRows;
-        const bool value = i >= kReadRows * kUnits;
+    for (int i = 0; i < kEach; i++) {
+        const int r = r1 + i * kStep;
         if (s_row[r] == -2) continue;
-        store8<OB>(value ? a.v : a.k, (r0 + r) * (value ? a.v_stride : a.k_stride) + h * D + 8 * u, w[k], sc[k]);
+        store8<OB>(a.k, (r0 + r) * a.k_stride + h * D + 8 * u, kw[i], ks[i]);
+        store8<OB>(a.v, (r0 + r) * a.v_stride + h * D + 8 * u, vw[i], vs[i]);
     }
 }
 
 template <bool BF16>
 cudaError_t append(const GqaAppendArgs &a, cudaStream_t st) {
-    const long long rows = 2LL * a.T * a.c.n_kv, per = kThreads / (a.c.dim / 8);
+    const long long rows = (long long)a.T * a.c.n_kv, per = kThreads / (a.c.dim / 8);
     const dim3 grid((unsigned)((rows + per - 1) / per)), block(kThreads);
     switch (a.c.gs) {
         case 32: return launch_pdl(gqa_append_kernel<BF16, 32>, grid, block, 0, st, a);

@@ -6,13 +6,15 @@
 // counts in shared memory) give the smallest one that stays and how many equal to it
 // do; one more pass writes the tokens that stay in their order.  The move is a
 // kernel of its own, so that few sequences use every SM.
+#include <algorithm>
+
 #include "gqa.cuh"
 
 namespace coli {
 
 namespace {
 
-constexpr int kSelect = 1024, kBins = 2048;
+constexpr int kSelect = 1024, kBins = 2048, kRoom = 52000;   // kRoom keys of 4 bytes in shared memory
 
 // Integers ordered as the weights; +0 and -0 alike, every NaN the largest.
 __device__ __forceinline__ uint32_t ordered(float w) {
@@ -29,11 +31,35 @@ __device__ __forceinline__ int length_of(const GqaEvictArgs &a, int b, bool repo
     return 0;
 }
 
-__global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs a) {
+// Inclusive sums over the CTA's threads of x and y; x_all and y_all get the totals.
+__device__ __forceinline__ void scan(int &x, int &y, int &x_all, int &y_all, int2 *sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) x += u, y += v;
+    }
+    if (lane == 31) sums[warp] = make_int2(x, y);
+    __syncthreads();
+    int2 s = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, s.x, o), v = __shfl_up_sync(0xffffffffu, s.y, o);
+        if (lane >= o) s.x += u, s.y += v;
+    }
+    x_all = __shfl_sync(0xffffffffu, s.x, 31);
+    y_all = __shfl_sync(0xffffffffu, s.y, 31);
+    const int u = __shfl_sync(0xffffffffu, s.x, max(warp - 1, 0)), v = __shfl_sync(0xffffffffu, s.y, max(warp - 1, 0));
+    if (warp) x += u, y += v;
+    __syncthreads();                                     // sums is free again
+}
+
+__global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs a, int room) {
+    extern __shared__ uint32_t keys[];                   // the first `room` candidates'; more are read again each time
     __shared__ int count[kBins];
-    __shared__ int sums[kSelect / 32], above[kSelect / 32];
+    __shared__ int2 sums[kSelect / 32];
     __shared__ int s_bin, s_left;
-    const int b = blockIdx.x / a.c.n_kv, h = blockIdx.x - b * a.c.n_kv, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int b = blockIdx.x / a.c.n_kv, h = blockIdx.x - b * a.c.n_kv, tid = threadIdx.x;
     pdl_wait();
     pdl_trigger();
     const int n = length_of(a, b, tid == 0 && h == 0);
@@ -49,7 +75,7 @@ __global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs 
     for (int i = tid; i < a.recent; i += kSelect) kept[want + i] = old + i;
     if (want == 0) return;
     const int32_t *pages = a.pages + b * a.pages_stride;
-    auto key = [&](int t) {
+    auto read_key = [&](int t) {
         const int p = t / a.c.page, id = pages[p];
         if (id < 0 || id >= a.c.n_pages) {
             mla_bad_index(a.err);
@@ -57,118 +83,126 @@ __global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs 
         }
         return ordered(a.c.w[gqa_row(a.c, id, h) + t - p * a.c.page]);
     };
+    auto key = [&](int t) { return t < room ? keys[t] : read_key(t); };
+    for (int i = tid; i < kBins; i += kSelect) count[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int t = tid; t < old; t += kSelect) {
+        const uint32_t k = read_key(t);
+        if (t < room) keys[t] = k;
+        atomicAdd(&count[k >> 21], 1);
+    }
     uint32_t prefix = 0;
     int left = want;                                     // of the keys that begin with the prefix, how many stay
     for (int pass = 0; pass < 3; pass++) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11, known = shift + bits;
-        for (int i = tid; i < kBins; i += kSelect) count[i] = 0;
-        __syncthreads();
-        for (int t = tid; t < old; t += kSelect) {
-            const uint32_t k = key(t);
-            if (pass == 0 || (k >> known) == (prefix >> known)) atomicAdd(&count[(k >> shift) & ((1 << bits) - 1)], 1);
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+        if (pass > 0) {
+            const int known = shift + bits;
+            for (int i = tid; i < kBins; i += kSelect) count[i] = 0;
+            __syncthreads();
+            for (int t = tid; t < old; t += kSelect) {
+                const uint32_t k = key(t);
+                if ((k >> known) == (prefix >> known)) atomicAdd(&count[(k >> shift) & ((1 << bits) - 1)], 1);
+            }
         }
         __syncthreads();
         // counts from the top: thread i has the bins 2047 - 2i and 2046 - 2i
-        const int c0 = count[kBins - 1 - 2 * tid], c1 = count[kBins - 2 - 2 * tid];
-        int incl = c0 + c1;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) sums[warp] = incl;
-        __syncthreads();
-        if (warp == 0) {
-            int v = sums[lane];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int w = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += w;
-            }
-            sums[lane] = v;
-        }
-        __syncthreads();
-        const int before = incl - c0 - c1 + (warp ? sums[warp - 1] : 0);
-        if (before < left && left <= before + c0) {
+        const int2 c = *reinterpret_cast<const int2 *>(&count[kBins - 2 - 2 * tid]);
+        int incl = c.x + c.y, none = 0, all, all2;
+        scan(incl, none, all, all2, sums);
+        const int before = incl - c.x - c.y;
+        if (before < left && left <= before + c.y) {
             s_bin = kBins - 1 - 2 * tid;
             s_left = left - before;
-        } else if (before + c0 < left && left <= before + c0 + c1) {
+        } else if (before + c.y < left && left <= incl) {
             s_bin = kBins - 2 - 2 * tid;
-            s_left = left - before - c0;
+            s_left = left - before - c.y;
         }
         __syncthreads();
         prefix |= (uint32_t)s_bin << shift;
         left = s_left;
     }
-    // in order: every key above the last one that stays, and the first `left` equal ones
-    int done = 0, equal = 0;                             // written so far, equal ones met so far
-    for (int t0 = 0; t0 < old; t0 += kSelect) {
-        const int t = t0 + tid;
-        const uint32_t k = t < old ? key(t) : 0;
-        const bool over = t < old && k > prefix, same = t < old && k == prefix;
-        const uint32_t mo = __ballot_sync(0xffffffffu, over), ms = __ballot_sync(0xffffffffu, same);
-        __syncthreads();
-        if (lane == 0) {
-            above[warp] = __popc(mo);
-            sums[warp] = __popc(ms);
-        }
-        __syncthreads();
-        int o0 = 0, e0 = 0, o_all = 0, e_all = 0;
-        for (int w = 0; w < kSelect / 32; w++) {
-            if (w == warp) o0 = o_all, e0 = e_all;
-            o_all += above[w];
-            e_all += sums[w];
-        }
-        const uint32_t lower = (1u << lane) - 1;
-        const int my_over = o0 + __popc(mo & lower), my_equal = e0 + __popc(ms & lower);
-        const int room = max(0, left - equal);           // equal ones that still stay
-        if (over || (same && my_equal < room)) kept[done + my_over + min(my_equal, room)] = t;
-        done += o_all + min(e_all, room);
-        equal += e_all;
+    // In order: every key above the last one that stays, and the first `left` equal ones.  A thread has as many neighbours as the
+    // next one, an odd number: its lane's words lie in banks of their own.
+    const int each = ((old + kSelect - 1) / kSelect) | 1, t0 = min((long long)tid * each, (long long)old), t1 = min(t0 + each, old);
+    int over = 0, same = 0, all, all2;
+    for (int t = t0; t < t1; t++) {
+        const uint32_t k = key(t);
+        over += k > prefix;
+        same += k == prefix;
+    }
+    const int over_here = over, same_here = same;
+    scan(over, same, all, all2, sums);
+    int equal = same - same_here, at = over - over_here + min(equal, left);
+    for (int t = t0; t < t1; t++) {
+        const uint32_t k = key(t);
+        if (k > prefix || (k == prefix && equal++ < left)) kept[at++] = t;
     }
 }
 
-// dim / 16 neighbouring threads per row that stays: 16 bytes of the key's codes or of the value's each, the first of either half the
-// scales too, the second one the weight.
+// A warp has 32 rows that stay: each lane finds one's old and new place and moves its scales and weight, then the lanes move all their
+// codes, 16 bytes each, keys first.
+template <int D>
 __global__ void __launch_bounds__(256) gqa_move_kernel(const GqaEvictArgs a) {
-    const int half = a.c.dim / 32, tpr = 2 * half, rows = 256 / tpr;
-    const int blocks = (a.keep + rows - 1) / rows, pair = blockIdx.x / blocks;
-    const int i = (blockIdx.x - pair * blocks) * rows + threadIdx.x / tpr, c = threadIdx.x & (tpr - 1);
-    const int b = pair / a.c.n_kv, h = pair - b * a.c.n_kv;
+    constexpr int kHalf = D / 32, kEach = 2 * kHalf;     // 16-byte pieces of a row's key, of a row
+    const int lane = threadIdx.x & 31, per = (a.keep + 31) / 32;
+    const long long w = blockIdx.x * 8LL + (threadIdx.x >> 5);
+    const int pair = (int)(w / per), i = (int)(w - (long long)pair * per) * 32 + lane;
     pdl_wait();
     pdl_trigger();
-    if (i >= a.keep) return;
-    const int t = a.kept[(long long)pair * a.keep + i];
-    if (t < 0) return;
-    const int sp = t / a.c.page, dp = i / a.c.page;
-    const int from = a.pages[b * a.pages_stride + sp], to = a.dst[b * a.dst_stride + dp];
-    if (from < 0 || from >= a.c.n_pages || to < 0 || to >= a.c.n_pages) {
-        mla_bad_index(a.err);
-        return;
+    if (pair >= a.n_seq * a.c.n_kv) return;
+    const int b = pair / a.c.n_kv, h = pair - b * a.c.n_kv;
+    const int t = i < a.keep ? a.kept[(long long)pair * a.keep + i] : -1;
+    int s = -1, d = -1;
+    if (t >= 0) {
+        const int sp = t / a.c.page, dp = i / a.c.page;
+        const int from = a.pages[b * a.pages_stride + sp], to = a.dst[b * a.dst_stride + dp];
+        if (from < 0 || from >= a.c.n_pages || to < 0 || to >= a.c.n_pages) {
+            mla_bad_index(a.err);
+        } else {
+            s = (int)gqa_row(a.c, from, h) + t - sp * a.c.page;
+            d = (int)gqa_row(a.c, to, h) + i - dp * a.c.page;
+        }
     }
-    const long long s = gqa_row(a.c, from, h) + t - sp * a.c.page, d = gqa_row(a.c, to, h) + i - dp * a.c.page;
-    const bool value = c >= half;
-    uint8_t *codes = value ? a.c.v : a.c.k;
-    const int u = value ? c - half : c, ng = a.c.dim / a.c.gs;
-    const uint4 x = reinterpret_cast<const uint4 *>(codes)[s * half + u];
-    if (u == 0) {
-        __nv_bfloat16 *sc = value ? a.c.vs : a.c.ks;
-        if (ng == 4) reinterpret_cast<uint2 *>(sc)[d] = reinterpret_cast<const uint2 *>(sc)[s];
-        else if (ng == 2) reinterpret_cast<uint32_t *>(sc)[d] = reinterpret_cast<const uint32_t *>(sc)[s];
-        else sc[d] = sc[s];
+    uint4 x[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; k++) {
+        const int piece = (k % kHalf) * 32 + lane;
+        const int row = __shfl_sync(0xffffffffu, s, piece / kHalf);
+        if (row >= 0) x[k] = reinterpret_cast<const uint4 *>(k < kHalf ? a.c.k : a.c.v)[(long long)row * kHalf + piece % kHalf];
     }
-    if (c == 1) a.c.w[d] = a.c.w[s];
-    reinterpret_cast<uint4 *>(codes)[d * half + u] = x;
+    if (s >= 0) {
+        const float weight = a.c.w[s];
+        auto scales = [&](auto *ks, auto *vs) {
+            const auto p = ks[s], q = vs[s];
+            ks[d] = p;
+            vs[d] = q;
+        };
+        const int ng = D / a.c.gs;
+        if (ng == 4) scales(reinterpret_cast<uint2 *>(a.c.ks), reinterpret_cast<uint2 *>(a.c.vs));
+        else if (ng == 2) scales(reinterpret_cast<uint32_t *>(a.c.ks), reinterpret_cast<uint32_t *>(a.c.vs));
+        else scales(reinterpret_cast<uint16_t *>(a.c.ks), reinterpret_cast<uint16_t *>(a.c.vs));
+        a.c.w[d] = weight;
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; k++) {
+        const int piece = (k % kHalf) * 32 + lane;
+        const int row = __shfl_sync(0xffffffffu, d, piece / kHalf);
+        if (row >= 0) reinterpret_cast<uint4 *>(k < kHalf ? a.c.k : a.c.v)[(long long)row * kHalf + piece % kHalf] = x[k];
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_gqa_evict(const GqaEvictArgs &a, cudaStream_t st, int *n_launch) {
-    const unsigned pairs = (unsigned)a.n_seq * a.c.n_kv;
+cudaError_t launch_gqa_evict(const GqaEvictArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch) {
+    const long long pairs = (long long)a.n_seq * a.c.n_kv;
+    const int room = (int)std::min(a.pages_stride * a.c.page, (long long)kRoom);
+    static std::atomic<uint64_t> done{0};
+    if (cudaError_t e = allow_smem(gqa_select_kernel, kRoom * sizeof(uint32_t), d.device, done)) return e;
     *n_launch = 2;
-    if (cudaError_t e = launch_pdl(gqa_select_kernel, dim3(pairs), dim3(kSelect), 0, st, a)) return e;
-    const int rows = 256 / (a.c.dim / 16);
-    return launch_pdl(gqa_move_kernel, dim3((a.keep + rows - 1) / rows * pairs), dim3(256), 0, st, a);
+    if (cudaError_t e = launch_pdl(gqa_select_kernel, dim3((unsigned)pairs), dim3(kSelect), room * sizeof(uint32_t), st, a, room)) return e;
+    const dim3 grid((unsigned)((pairs * ((a.keep + 31) / 32) + 7) / 8));
+    return a.c.dim == 64 ? launch_pdl(gqa_move_kernel<64>, grid, dim3(256), 0, st, a) : launch_pdl(gqa_move_kernel<128>, grid, dim3(256), 0, st, a);
 }
 
 }  // namespace coli

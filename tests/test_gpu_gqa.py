@@ -2,8 +2,8 @@
 back, attention of prompts and over the cache, the rows' weights, the eviction.
 
 Tolerances.  Codes, scales, kept tokens and moved rows are exact.  An attention output is sum_t p_t v_t.  Prompts: rounding
-every p_t to bf16 moves it by at most 2^-8 sum_t p_t |v_t|.  Over the cache p_t times the row's scale is rounded to bf16, the
-same bound, and sum_t p_t s_t (128 + n_t) - 136 sum_t p_t s_t is added up in f32: each of at most len / 16 + 8 additions
+every p_t to bf16 moves it by at most 2^-8 sum_t p_t |v_t|.  Over the cache p_t is rounded to bf16 and its product with the
+row's scale once more, (1 + 2^-8)^2 - 1 = 2^-7 + 2^-16 in all, and sum_t p_t s_t (128 + n_t) - 136 sum_t p_t s_t is added up in f32: each of at most len / 16 + 8 additions
 may be off by 2^-23 of 136 max_t s_t.  f32 scores, exp and sums move the p_t by less than 1e-4 of themselves for these
 lengths, and a bf16 output rounds once more (2^-8).  An f32 query becomes f16 (2^-11 of each element), which moves a score by at
 most d = 2^-11 scale sum_i |q_i| |k_ti| and p_t by a factor exp(2 d)."""
@@ -363,7 +363,7 @@ def reference_step(torch, s, table, lens, q, scale, kind_q, kind_out):
                 d = (k[kh, :m].abs() @ x[b, j, h].abs()).max() * abs(scale)    # no score is larger, nor its terms together
                 r = math.expm1(2 * UF16 * d) if kind_q == "f32" else 0.0
                 out[b, j, h] = p @ v[kh, :m]
-                tol[b, j, h] = (U16 + 1e-4 + r) * (p @ v[kh, :m].abs()) + r * out[b, j, h].abs() + (n / 16 + 8) * 2.0 ** -23 * 136 * vs[kh, :m].max()
+                tol[b, j, h] = (2 * U16 + U16 * U16 + 1e-4 + r) * (p @ v[kh, :m].abs()) + r * out[b, j, h].abs() + (n / 16 + 8) * 2.0 ** -23 * 136 * vs[kh, :m].max()
                 lse[b, j, h] = torch.logsumexp(a, -1)
                 got[kh, :m] += p
                 # scores: f32 sums of codes 0..15 (2 d at most) in some 20 additions; x and m in units of log2; exp; 1 / l
