@@ -78,6 +78,7 @@ struct GqaPrefillArgs {
     float scale;
     void *out;
     float *lse;
+    const int *q_exponent, *exponent;   // f16 inputs made from f32: powers of two of each row of q, of k and of v
     int *err;
 };
 

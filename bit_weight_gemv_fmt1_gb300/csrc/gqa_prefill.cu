@@ -17,6 +17,10 @@
 // maximum passes it by 8: weights up to 2^8 lose nothing in bf16.  m, l and O are
 // f32; rounding P to bf16 is within 2^-8 of each weight, as the values' own.
 //
+// f32 inputs become f16, which keeps 3 bits more than bf16: every row of q times a power of two of its own, k and v times one each,
+// so that the largest magnitudes lie in 2^14 .. 2^15 and all down to 2^-28 of them keep their 11 bits.  P is f16 then too.  The
+// powers come out again in the scores' factor, a thread's own, and with 1 / l.  (bf16 without the powers: twice the error.)
+//
 // Keys past a causal row's limit are masked by selection; value rows past the
 // sequence's end belong to its neighbours and are zeroed in shared memory.
 // Warps: 0-3 and 4-7 softmax of A and B, 8 MMA issue, 9 units and copies of keys, 10 and 11 of queries and values.
@@ -33,7 +37,7 @@ namespace {
 constexpr int kKeys = 6, kValues = 4;    // ring slots: key blocks of 64 dims, value halves of 64 keys
 
 struct Shared {
-    uint64_t q_full[2], q_empty[2], k_full[kKeys], k_empty[kKeys], v_full[kValues], v_empty[kValues], s_full[2], p_full[2], o_full[2],
+    uint64_t q_full[2], q_empty[2], k_full[kKeys], k_empty[kKeys], v_full[kValues], v_empty[kValues], s_full[2], p_full[2][2], o_full[2],
         u_full[2], u_empty[2];
     uint64_t next_full;
     Unit unit[2];
@@ -41,6 +45,25 @@ struct Shared {
     uint32_t tmem;
     int abort;
 };
+
+// (x, y) = (x, y) * f + m, and s += (x, y): two f32 operations in one instruction.
+__device__ __forceinline__ void fma2(float &x, float &y, uint32_t u, uint32_t v, float f, float m) {
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 d, {%5, %5};\n fma.rn.f32x2 a, a, b, d;\n"
+        " mov.b64 {%0, %1}, a;\n}"
+        : "=f"(x), "=f"(y)
+        : "r"(u), "r"(v), "f"(f), "f"(m));
+}
+__device__ __forceinline__ void add2(float &s, float &t, float x, float y) {
+    asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%0, %1};\n add.rn.f32x2 b, b, a;\n mov.b64 {%0, %1}, b;\n}"
+        : "+f"(s), "+f"(t)
+        : "f"(x), "f"(y));
+}
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// x 2^e for the exponents that f16_exponent gives: in two factors, since 2^e may pass the range.
+__device__ __forceinline__ float scaled(float x, int e) { return x * exp2i(e / 2) * exp2i(e - e / 2); }
+// The power of two that takes a largest magnitude to 2^14 .. 2^15.
+__device__ __forceinline__ int f16_exponent(uint32_t bits) { return bits ? 14 - ilogbf(__uint_as_float(bits)) : 0; }
 
 // A box of a 3-D tensor map, as tma_box.
 __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
@@ -51,7 +74,7 @@ __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, i
         : "memory");
 }
 
-template <int D>
+template <int D, bool F16>
 __global__ void __launch_bounds__(384, 1)
     gqa_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                        const __grid_constant__ CUtensorMap v_map, const GqaPrefillArgs a, long long wait_ns) {
@@ -71,7 +94,8 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&s.q_full[i], 1);
             mbar_init(&s.q_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_full[i], 4);
+            mbar_init(&s.p_full[i][0], 4);
+            mbar_init(&s.p_full[i][1], 4);
             mbar_init(&s.o_full[i], 1);
             mbar_init(&s.u_full[i], 1);
             mbar_init(&s.u_empty[i], 11);
@@ -120,9 +144,10 @@ __global__ void __launch_bounds__(384, 1)
         // ---------------------------------------------------------- softmax and output
         const int x = warp >> 2, t = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), S = lanes + x * 128, O = lanes + 256 + x * D;
-        // a negative scale turns the scores' sign; a zero one must still send masked scores (-inf) to -inf
+        // a negative scale turns the scores' sign; a factor of zero must still send masked scores (-inf) to -inf
         const bool negative = a.scale < 0.f;
-        const float f = a.scale == 0.f ? 1e-37f : fabsf(a.scale) * 1.4426950408889634f;
+        const float scale2 = fabsf(a.scale) * 1.4426950408889634f;
+        const int ek = F16 ? a.exponent[0] : 0, ev = F16 ? a.exponent[1] : 0;
         const int tok = t / a.group, g = t - tok * a.group;  // this thread's row: token of the tile, head of the group
         int tiles = 0, s_tiles = 0, outs = 0;            // key tiles, this tile's score tiles and outputs so far
         for (int r = 0;; r++) {
@@ -132,6 +157,8 @@ __global__ void __launch_bounds__(384, 1)
             const int limit = min(row + nk - u.nq + 1, nk);     // keys this row sees
             const int all = min(first + nk - u.nq + 1, nk);     // keys every row of the tile sees
             const long long orow = tok < a.tokens && row < u.nq ? (long long)(u.qrow + row) * a.heads + u.head * a.group + g : -1;
+            const int eq = F16 && orow >= 0 ? a.q_exponent[orow] : 0;
+            const float f = fmaxf(F16 ? scaled(scaled(scale2, -eq), -ek) : scale2, 1e-37f);
             float m = kNone;
             float l4[4] = {0.f, 0.f, 0.f, 0.f};
             for (int j = 0; j < nt; j++) {
@@ -180,19 +207,6 @@ __global__ void __launch_bounds__(384, 1)
                         }
                     }
                 }
-                const float m0 = -m;
-#pragma unroll
-                for (int c0 = 0; c0 < kRows; c0 += 32) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        const float x = ex2(fmaf(__uint_as_float(v[c0 + c]), f, m0)), y = ex2(fmaf(__uint_as_float(v[c0 + c + 1]), f, m0));
-                        l4[c & 3] += x;
-                        l4[(c + 1) & 3] += y;
-                        p[c / 2] = pack_bf16(x, y);
-                    }
-                    tmem_st(S + c0 / 2, p);                  // over scores that have been read
-                }
                 if (k0 + kRows > nk) {
                     // value rows of other sequences may hold anything, and 0 * NaN is NaN
                     const int half = 2 * (tiles + j) + (t >> 6), slot = half % kValues;
@@ -205,10 +219,27 @@ __global__ void __launch_bounds__(384, 1)
                                 *reinterpret_cast<uint4 *>(sm + v_off + slot * kHalf + k * (kBlk / 2) + (t & 63) * 128 + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
                     fence_async_smem();
                 }
-                tmem_st_wait();
-                tc_before_sync();
-                __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(&s.p_full[x]);
+                const float m0 = -m;
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+#pragma unroll
+                    for (int c0 = 64 * h; c0 < 64 * h + 64; c0 += 32) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            float x, y;
+                            fma2(x, y, v[c0 + c], v[c0 + c + 1], f, m0);
+                            x = ex2(x), y = ex2(y);
+                            add2(l4[c & 2], l4[(c & 2) + 1], x, y);
+                            p[c / 2] = F16 ? pack_f16(x, y) : pack_bf16(x, y);
+                        }
+                        tmem_st(S + c0 / 2, p);              // over scores that have been read
+                    }
+                    tmem_st_wait();
+                    tc_before_sync();
+                    __syncwarp();
+                    if (lane == 0 && ok) mbar_arrive(&s.p_full[x][h]);
+                }
             }
             tiles += u.n;
             const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
@@ -229,7 +260,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 if (orow < 0) continue;
 #pragma unroll
-                for (int c = 0; c < 32; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
+                for (int c = 0; c < 32; c++) o[c] = __float_as_uint(F16 ? scaled(__uint_as_float(o[c]) * inv, -ev) : __uint_as_float(o[c]) * inv);
                 if (a.out_bf16) {
                     uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * D + c0);
 #pragma unroll
@@ -250,7 +281,7 @@ __global__ void __launch_bounds__(384, 1)
         }
     } else if (warp == 8) {
         // ---------------------------------------------------------- MMA issue
-        constexpr uint32_t id_s = f16_idesc(1, false, false, kRows, kRows), id_o = f16_idesc(1, false, true, kRows, D);
+        constexpr uint32_t id_s = f16_idesc(!F16, false, false, kRows, kRows), id_o = f16_idesc(!F16, false, true, kRows, D);
         const uint64_t dq = sw128_desc(base, 16, 1024), dk = sw128_desc(base + k_off, 16, 1024), dv = sw128_desc(base + v_off, kBlk / 2, 1024);
         // scores of query tile x with the keys at c; fresh: nobody has waited for them yet, last: nobody uses them after
         auto scores = [&](int x, Ring c, bool fresh, bool last) {
@@ -271,13 +302,12 @@ __global__ void __launch_bounds__(384, 1)
             tc_commit(&s.s_full[x]);
         };
         // the products of query tile x with the values at c, in halves of 64 keys
-        auto output = [&](int x, bool more, Ring c, bool fresh, bool last) {
+        auto output = [&](int x, int tile, bool more, Ring c, bool fresh, bool last) {
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-                if (fresh) {
-                    wait(&s.v_full[c.slot], c.par);
-                    tc_after_sync();
-                }
+                wait(&s.p_full[x][h], tile & 1);
+                if (fresh) wait(&s.v_full[c.slot], c.par);
+                tc_after_sync();
                 if (!ok) return;
                 const uint64_t va = dv + ((c.slot * kHalf) >> 4);
 #pragma unroll
@@ -305,9 +335,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                 for (int x = 0; x < 2; x++) {
                     if (j >= u.nt[x]) continue;
-                    wait(&s.p_full[x], (st[x] + j) & 1);
-                    tc_after_sync();
-                    output(x, j > 0, vr, x == 0 || j >= u.nt[0], x == 1 || j >= u.nt[1]);
+                    output(x, st[x] + j, j > 0, vr, x == 0 || j >= u.nt[0], x == 1 || j >= u.nt[1]);
                     if (j + 1 < u.nt[x]) {
                         scores(x, kr, x == 0 || j + 1 >= u.nt[0], x == 1 || j + 1 >= u.nt[1]);
                         if (ok && j + 2 == u.nt[x]) tc_commit(&s.q_empty[x]);
@@ -409,7 +437,135 @@ cudaError_t query_map(const GqaPrefillArgs &a, CUtensorMap *out) {
                : cudaErrorInvalidValue;
 }
 
+// f32 -> f16, first step: each row of q times a power of two of its own (whose exponent goes to q_exponent), and the largest finite
+// magnitudes of k and v, one for each of the first `ranges` CTAs.  One thread per 8 elements.
 template <int D>
+__global__ void __launch_bounds__(256) gqa_round_q_kernel(const GqaPrefillArgs a, __half *q16, int *q_exponent, uint2 *range, int ranges) {
+    constexpr int kUnits = D / 8;
+    __shared__ uint32_t most[2];
+    pdl_wait();
+    pdl_trigger();
+    auto finite = [](float x) {
+        const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+        return b < 0x7F800000u ? b : 0u;
+    };
+    auto largest = [&](const float4 &x, const float4 &y) {
+        return max(max(max(finite(x.x), finite(x.y)), max(finite(x.z), finite(x.w))), max(max(finite(y.x), finite(y.y)), max(finite(y.z), finite(y.w))));
+    };
+    if ((int)blockIdx.x < ranges) {
+        if (threadIdx.x < 2) most[threadIdx.x] = 0;
+        __syncthreads();
+        const long long units = (long long)a.Tk * a.H * kUnits;
+        const int upt = a.H * kUnits;
+        uint32_t m[2] = {0, 0};
+        for (long long i = blockIdx.x * 256LL + threadIdx.x; i < units; i += ranges * 256LL) {
+            const long long t = i / upt;
+            const int u = (int)(i - t * upt);
+            const float *k = (const float *)a.k + t * a.k_stride + 8 * u, *v = (const float *)a.v + t * a.v_stride + 8 * u;
+            m[0] = max(m[0], largest(*reinterpret_cast<const float4 *>(k), *reinterpret_cast<const float4 *>(k + 4)));
+            m[1] = max(m[1], largest(*reinterpret_cast<const float4 *>(v), *reinterpret_cast<const float4 *>(v + 4)));
+        }
+        for (int j = 0; j < 2; j++) {
+            m[j] = __reduce_max_sync(0xffffffffu, m[j]);
+            if ((threadIdx.x & 31) == 0) atomicMax(&most[j], m[j]);
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) range[blockIdx.x] = make_uint2(most[0], most[1]);
+    }
+    const long long rows = (long long)a.Tq * a.heads;
+    const int u = threadIdx.x % kUnits;
+    for (long long r0 = blockIdx.x * (256LL / kUnits); r0 < rows; r0 += gridDim.x * (256LL / kUnits)) {   // the CTA stays together
+        const long long r = r0 + threadIdx.x / kUnits;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (r < rows) {
+            const long long t = r / a.heads;
+            const float *q = (const float *)a.q + t * a.q_stride + (r - t * a.heads) * D + 8 * u;
+            x = *reinterpret_cast<const float4 *>(q);
+            y = *reinterpret_cast<const float4 *>(q + 4);
+        }
+        uint32_t m = largest(x, y);
+#pragma unroll
+        for (int o = 1; o < kUnits; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int e = f16_exponent(m);
+        if (r >= rows) continue;
+        if (u == 0) q_exponent[r] = e;
+        reinterpret_cast<uint4 *>(q16)[r * kUnits + u] = make_uint4(pack_f16(scaled(x.x, e), scaled(x.y, e)), pack_f16(scaled(x.z, e), scaled(x.w, e)),
+                                                                  pack_f16(scaled(y.x, e), scaled(y.y, e)), pack_f16(scaled(y.z, e), scaled(y.w, e)));
+    }
+}
+// Second step: k and v, each times one power of two.
+template <int D>
+__global__ void __launch_bounds__(256) gqa_round_kv_kernel(const GqaPrefillArgs a, __half *k16, __half *v16, int *exponent, const uint2 *range, int ranges) {
+    constexpr int kUnits = D / 8;
+    __shared__ uint32_t most[2];
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x < 2) most[threadIdx.x] = 0;
+    __syncthreads();
+    uint2 m = make_uint2(0, 0);
+    for (int i = threadIdx.x; i < ranges; i += 256) m = make_uint2(max(m.x, range[i].x), max(m.y, range[i].y));
+    m = make_uint2(__reduce_max_sync(0xffffffffu, m.x), __reduce_max_sync(0xffffffffu, m.y));
+    if ((threadIdx.x & 31) == 0) {
+        atomicMax(&most[0], m.x);
+        atomicMax(&most[1], m.y);
+    }
+    __syncthreads();
+    const int ek = f16_exponent(most[0]), ev = f16_exponent(most[1]), upt = a.H * kUnits;
+    if (blockIdx.x == 0 && threadIdx.x == 0) exponent[0] = ek, exponent[1] = ev;
+    const long long units = (long long)a.Tk * upt;
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < 2 * units; i += gridDim.x * 256LL) {
+        const bool value = i >= units;
+        const long long j = value ? i - units : i, t = j / upt;
+        const int u = (int)(j - t * upt), e = value ? ev : ek;
+        const float *p = (const float *)(value ? a.v : a.k) + t * (value ? a.v_stride : a.k_stride) + 8 * u;
+        const float4 x = *reinterpret_cast<const float4 *>(p), y = *reinterpret_cast<const float4 *>(p + 4);
+        reinterpret_cast<uint4 *>(value ? v16 : k16)[j] = make_uint4(pack_f16(scaled(x.x, e), scaled(x.y, e)), pack_f16(scaled(x.z, e), scaled(x.w, e)),
+                                                                     pack_f16(scaled(y.x, e), scaled(y.y, e)), pack_f16(scaled(y.z, e), scaled(y.w, e)));
+    }
+}
+
+// What a call with f32 inputs keeps in scratch.
+struct Rounded {
+    size_t q, k, v, q_exponent, exponent, range, end;
+};
+constexpr int kRanges = 152;             // CTAs that look for the largest magnitudes, at most
+Rounded rounded(const GqaPrefillArgs &a) {
+    Rounded z;
+    z.q = 0;
+    z.k = z.q + round256((size_t)a.Tq * a.heads * a.dim * 2);
+    z.v = z.k + round256((size_t)a.Tk * a.H * a.dim * 2);
+    z.q_exponent = z.v + round256((size_t)a.Tk * a.H * a.dim * 2);
+    z.exponent = z.q_exponent + round256((size_t)a.Tq * a.heads * sizeof(int));
+    z.range = z.exponent + 256;
+    z.end = z.range + round256(kRanges * sizeof(uint2));
+    return z;
+}
+
+template <int D>
+cudaError_t round_inputs(GqaPrefillArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch) {
+    const Rounded z = rounded(a);
+    char *at = (char *)d.scratch;
+    const long long q_ctas = ((long long)a.Tq * a.heads * (D / 8) + 255) / 256, kv_ctas = ((long long)a.Tk * a.H * (D / 8) + 255) / 256;
+    const int ranges = (int)std::max(1LL, std::min((long long)kRanges, kv_ctas));
+    auto grid = [&](long long n) { return dim3((unsigned)std::max(1LL, std::min(n, 16LL * d.n_sm))); };
+    if (cudaError_t e = launch_pdl(gqa_round_q_kernel<D>, grid(std::max(q_ctas, (long long)ranges)), dim3(256), 0, st, a, (__half *)(at + z.q),
+                                   (int *)(at + z.q_exponent), (uint2 *)(at + z.range), ranges))
+        return e;
+    if (cudaError_t e = launch_pdl(gqa_round_kv_kernel<D>, grid(2 * kv_ctas), dim3(256), 0, st, a, (__half *)(at + z.k), (__half *)(at + z.v),
+                                   (int *)(at + z.exponent), (const uint2 *)(at + z.range), ranges))
+        return e;
+    *n_launch += 2;
+    a.q = at + z.q;
+    a.k = at + z.k;
+    a.v = at + z.v;
+    a.q_stride = a.heads * a.dim;
+    a.k_stride = a.v_stride = a.H * a.dim;
+    a.q_exponent = (const int *)(at + z.q_exponent);
+    a.exponent = (const int *)(at + z.exponent);
+    return cudaSuccess;
+}
+
+template <int D, bool F16>
 cudaError_t run(const GqaPrefillArgs &a, const DevInfo &d, cudaStream_t st) {
     CUtensorMap q, k, v;
     if (cudaError_t e = query_map(a, &q)) return e;
@@ -422,43 +578,24 @@ cudaError_t run(const GqaPrefillArgs &a, const DevInfo &d, cudaStream_t st) {
     const long long units = std::min((long long)a.Tq, ((long long)a.Tq + 2 * a.tokens - 1) / (2 * a.tokens) + a.n_seq - 1) * a.H;
     constexpr size_t smem = (2 * (D / 64) + kKeys) * kBlk + kValues * (D / 64) * (kBlk / 2) + 1024;
     static std::atomic<uint64_t> done{0};
-    if (cudaError_t e = allow_smem(gqa_prefill_kernel<D>, smem, d.device, done)) return e;
-    return launch_pdl(gqa_prefill_kernel<D>, dim3((unsigned)units), dim3(384), smem, st, q, k, v, a, d.wait_ns);
+    if (cudaError_t e = allow_smem(gqa_prefill_kernel<D, F16>, smem, d.device, done)) return e;
+    return launch_pdl(gqa_prefill_kernel<D, F16>, dim3((unsigned)units), dim3(384), smem, st, q, k, v, a, d.wait_ns);
+}
+
+template <int D>
+cudaError_t launch(GqaPrefillArgs a, const DevInfo &d, cudaStream_t st, int *n_launch) {
+    *n_launch = 1;
+    if (!a.in_f32) return run<D, false>(a, d, st);
+    if (cudaError_t e = round_inputs<D>(a, d, st, n_launch)) return e;
+    return run<D, true>(a, d, st);
 }
 
 }  // namespace
 
-size_t gqa_prefill_scratch(const GqaPrefillArgs &a) {
-    if (!a.in_f32) return 0;
-    return round256((size_t)a.Tq * a.heads * a.dim * 2) + 2 * round256((size_t)a.Tk * a.H * a.dim * 2);
-}
+size_t gqa_prefill_scratch(const GqaPrefillArgs &a) { return a.in_f32 ? rounded(a).end : 0; }
 
-cudaError_t launch_gqa_prefill(const GqaPrefillArgs &a0, const DevInfo &d, cudaStream_t st, int *n_launch) {
-    GqaPrefillArgs a = a0;
-    *n_launch = 1;
-    if (a.in_f32) {
-        const int cols[3] = {a.heads * a.dim, a.H * a.dim, a.H * a.dim};
-        const long long rows[3] = {a.Tq, a.Tk, a.Tk}, strides[3] = {a.q_stride, a.k_stride, a.v_stride};
-        const void *src[3] = {a.q, a.k, a.v};
-        __nv_bfloat16 *dst[3];
-        char *at = (char *)d.scratch;
-        for (int i = 0; i < 3; i++) {
-            dst[i] = (__nv_bfloat16 *)at;
-            at += round256((size_t)rows[i] * cols[i] * 2);
-            const long long want = (rows[i] * (cols[i] / 8) + 255) / 256;
-            if (want == 0) continue;
-            if (cudaError_t e = launch_pdl(round_kernel, dim3((unsigned)(want < 32LL * d.n_sm ? want : 32LL * d.n_sm)), dim3(256), 0, st,
-                                           (const float *)src[i], strides[i], rows[i], cols[i], dst[i]))
-                return e;
-            ++*n_launch;
-        }
-        a.q = dst[0];
-        a.k = dst[1];
-        a.v = dst[2];
-        a.q_stride = cols[0];
-        a.k_stride = a.v_stride = cols[1];
-    }
-    return a.dim == 64 ? run<64>(a, d, st) : run<128>(a, d, st);
+cudaError_t launch_gqa_prefill(const GqaPrefillArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch) {
+    return a.dim == 64 ? launch<64>(a, d, st, n_launch) : launch<128>(a, d, st, n_launch);
 }
 
 }  // namespace coli

@@ -409,6 +409,20 @@ __global__ void __launch_bounds__(384, 1)
     }
 }
 
+// f32 -> bf16, rows of `cols` (a multiple of 8) at `stride` to packed ones.
+__global__ void __launch_bounds__(256) mla_round_kernel(const float *src, long long stride, long long rows, int cols, __nv_bfloat16 *dst) {
+    pdl_wait();
+    pdl_trigger();
+    const int units = cols / 8;
+    const long long n = rows * units;
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
+        const long long r = i / units;
+        const int u = (int)(i - r * units);
+        const float4 x = *reinterpret_cast<const float4 *>(src + r * stride + 8 * u), y = *reinterpret_cast<const float4 *>(src + r * stride + 8 * u + 4);
+        reinterpret_cast<uint4 *>(dst)[i] = make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+    }
+}
+
 template <int V>
 cudaError_t run(const MlaPrefillArgs &a, const DevInfo &d, cudaStream_t st) {
     CUtensorMap q, kv, kr, vm;
@@ -453,7 +467,7 @@ cudaError_t launch_mla_prefill(const MlaPrefillArgs &a0, const DevInfo &d, cudaS
             at += round256((size_t)rows[i] * cols[i] * 2);
             const long long want = (rows[i] * (cols[i] / 8) + 255) / 256;
             if (want == 0) continue;
-            if (cudaError_t e = launch_pdl(round_kernel, dim3((unsigned)(want < 32LL * d.n_sm ? want : 32LL * d.n_sm)), dim3(256), 0, st,
+            if (cudaError_t e = launch_pdl(mla_round_kernel, dim3((unsigned)(want < 32LL * d.n_sm ? want : 32LL * d.n_sm)), dim3(256), 0, st,
                                            (const float *)src[i], strides[i], rows[i], cols[i], dst[i]))
                 return e;
             ++*n_launch;

@@ -1,5 +1,5 @@
 // prefill.cuh -- what the prompts' attention kernels (mla_prefill.cu, gqa_prefill.cu) share: rings, the take-over of
-// CTAs that have not started, tensor maps, the rounding of f32 inputs.
+// CTAs that have not started, tensor maps.
 #pragma once
 
 #include "encode_tiled.cuh"
@@ -59,20 +59,6 @@ __device__ __forceinline__ int read_next(S &s) {
         : "r"(smem_addr(s.next))
         : "memory");
     return i;
-}
-
-// f32 -> bf16, rows of `cols` (a multiple of 8) at `stride` to packed ones.
-__global__ void __launch_bounds__(256) round_kernel(const float *src, long long stride, long long rows, int cols, __nv_bfloat16 *dst) {
-    pdl_wait();
-    pdl_trigger();
-    const int units = cols / 8;
-    const long long n = rows * units;
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
-        const long long r = i / units;
-        const int u = (int)(i - r * units);
-        const float4 x = *reinterpret_cast<const float4 *>(src + r * stride + 8 * u), y = *reinterpret_cast<const float4 *>(src + r * stride + 8 * u + 4);
-        reinterpret_cast<uint4 *>(dst)[i] = make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
-    }
 }
 
 cudaError_t matrix_map(const void *p, long long cols, long long rows, long long stride, int box_rows, CUtensorMap *out) {

@@ -562,11 +562,13 @@ typedef struct {
  *   q       device [Tq][n_heads][dim], token stride q_stride.
  *   k, v    device [Tk][n_kv][dim], token strides k_stride, v_stride (they may be
  *           parts of one row).
- *   dtype   COLI_BF16, or COLI_F32: the three are then rounded to bf16 in scratch first.
+ *   dtype   COLI_BF16, or COLI_F32: the three are then rounded to f16 in scratch first, each row
+ *           (token and head) of q times a power of two, k and v times one each, so that any range of
+ *           magnitudes fits; elements below 2^-28 of the largest lose bits.
  *   cu_q, cu_k      device int32 [n_seq + 1], ascending from 0 to Tq / Tk.
  *   out     device [Tq][n_heads][dim], COLI_F32 or COLI_BF16; lse device f32 [Tq][n_heads] or NULL.
  *           Rows of no sequence are left alone.
- * Products have bf16 operands (the probabilities are rounded to bf16) and f32
+ * Products have bf16 (f32 inputs: f16) operands, to which the probabilities are rounded, and f32
  * sums; maxima and denominators are f32.  A value of another sequence never
  * reaches the result; a non-finite v row that a query's own sequence masks may.
  * Pointers 16-byte aligned (cu, lse: 4); strides in elements, multiples of 8.

@@ -2,7 +2,7 @@
 back, attention of prompts and over the cache, the rows' weights, the eviction.
 
 Tolerances.  Codes, scales, kept tokens and moved rows are exact.  An attention output is sum_t p_t v_t.  Prompts: rounding
-every p_t to bf16 moves it by at most 2^-8 sum_t p_t |v_t|.  Over the cache p_t is rounded to bf16 and its product with the
+every p_t to bf16 moves it by at most 2^-8 sum_t p_t |v_t|, to f16 (f32 inputs) by 2^-11 of that.  Over the cache p_t is rounded to bf16 and its product with the
 row's scale once more, (1 + 2^-8)^2 - 1 = 2^-7 + 2^-16 in all, and sum_t p_t s_t (128 + n_t) - 136 sum_t p_t s_t is added up in f32: each of at most len / 16 + 8 additions
 may be off by 2^-23 of 136 max_t s_t.  f32 scores, exp and sums move the p_t by less than 1e-4 of themselves for these
 lengths, and a bf16 output rounds once more (2^-8).  An f32 query becomes f16 (2^-11 of each element), which moves a score by at
@@ -198,10 +198,12 @@ def test_read_bad_pages():
 
 # ------------------------------------------------------------------ prompts
 def reference_prompt(torch, q, k, v, cu_q, cu_k, scale, kind):
-    """Outputs, tolerances and lse in 64 bits; q, k, v as rounded to bf16."""
+    """Outputs, tolerances and lse in 64 bits; q, k, v as they are (bf16) or rounded to f16 (f32 inputs; a power of two that goes
+    with them changes no bit of values above 2^-14, and below they are off by 2^-25)."""
     Tq, H, D = q.shape
     group = H // k.shape[1]
-    q, k, v = (x.to(torch.bfloat16).double() for x in (q, k, v))
+    u = UF16 if q.dtype is torch.float32 else U16
+    q, k, v = ((x.to(torch.float16) if x.dtype is torch.float32 else x).double() for x in (q, k, v))
     out, tol = torch.zeros(Tq, H, D, dtype=torch.float64), torch.zeros(Tq, H, D, dtype=torch.float64)
     lse = torch.full((Tq, H), -math.inf, dtype=torch.float64)
     for b in range(len(cu_q) - 1):
@@ -216,7 +218,7 @@ def reference_prompt(torch, q, k, v, cu_q, cu_k, scale, kind):
             p = torch.zeros_like(a)
             p[some] = torch.softmax(a[some], -1)
             out[q0:q1, h] = p @ v[k0:k1, h // group]
-            tol[q0:q1, h] = (U16 + 1e-4) * (p @ v[k0:k1, h // group].abs())
+            tol[q0:q1, h] = (u + 1e-4) * (p @ v[k0:k1, h // group].abs())
             lse[q0:q1, h] = torch.logsumexp(a, -1)
     if kind == "bf16":
         tol += U16 * out.abs()
@@ -259,6 +261,28 @@ def test_prompt(lens_q, lens_k, H, K, D, kind_in, kind_out):
     none = torch.isinf(ref_lse)
     assert torch.equal(torch.isinf(got), none)
     assert ((got - ref_lse)[~none].abs() <= 1e-4 * (1 + ref_lse[~none].abs())).all()
+
+
+@pytest.mark.parametrize("size_q,size_k,size_v", [(1e-30, 1e20, 1.0), (1e25, 1e-25, 1e30), (1.0, 1.0, 1e-30), (1e-5, 1e-5, 1e-5)])
+def test_prompt_f32_magnitudes(size_q, size_k, size_v):
+    """f32 inputs of any size: the powers of two that come with f16 leave every score and output in its place."""
+    torch, coli = setup()
+    g = gen(torch, 8)
+    q, kv = packed_qkv(torch, [70], [90], 4, 2, 64, g, torch.float32)
+    q[::3] *= 2.0 ** -20                                  # each row of q has a power of its own
+    scale = 0.125 / size_q / size_k
+    out = torch.empty(70, 4, 64, device="cuda")
+    cu = [torch.tensor([0, n], dtype=torch.int32, device="cuda") for n in (70, 90)]
+    coli.gqa_prefill((q * size_q).cuda(), (kv[:, :2] * size_k).contiguous().cuda(), (kv[:, 2:4] * size_v).contiguous().cuda(), *cu, scale, out)
+    coli.sync_check()
+    q[::3] *= 2.0 ** 20                                   # the reference rounds to f16 where all rows are in range: a row's
+    ref, tol, _ = reference_prompt(torch, q, kv[:, :2], kv[:, 2:4], [0, 70], [0, 90], 0.125, "f32")
+    small, small_tol, _ = reference_prompt(torch, q, kv[:, :2], kv[:, 2:4], [0, 70], [0, 90], 0.125 * 2.0 ** -20, "f32")
+    ref[::3], tol[::3] = small[::3], small_tol[::3]
+    # q * size_q, k * size_k and v * size_v are f32 products: off by 2^-24 before the kernel sees them, and may round the other way
+    # to f16: one more 2^-11 of each q and k in the scores (|s| <= 12, 2 x 2^-11 x 12), of each v in the output
+    some = ref.abs() * 0 + kv[:, 2:4].abs().max().double()
+    assert ((out.cpu().double() / size_v - ref).abs() <= tol + (UF16 + 4 * UF16 * 12) * some).all()
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
