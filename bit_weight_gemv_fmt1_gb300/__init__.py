@@ -370,6 +370,8 @@ def _tokens(t, dev: int, name: str) -> int:
     if t.get_device() != dev:
         _elsewhere(t, dev, name)
     shape, stride, n = t.shape, t.stride(), 1
+    if len(shape) == 3 and stride[2] == 1 and stride[1] == shape[2]:     # the usual case, without the loop
+        return stride[0] if shape[0] > 1 else shape[1] * shape[2]
     for i in range(len(shape) - 1, 0, -1):
         if stride[i] != n and shape[i] != 1:
             _refuse(f"a token of {name} must be packed")

@@ -35,7 +35,7 @@ namespace coli {
 namespace {
 
 constexpr int kTile = 32, kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kJoin = 512, kGroup = 64;  // threads of the join, parts at a time
+constexpr int kJoin = 256, kGroup = 64;  // threads of the join, parts at a time
 constexpr float kGrow = 8.f;             // log2 of the weight that moves the reference
 constexpr float kNone = -3e38f;          // reference of a row that has seen no key
 constexpr int kRows = 8;                 // query rows of a unit: N of the products
@@ -442,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __shared__ uint64_t full[kWarps][S::kDepth];
     __shared__ float2 ml[kWarps][kRows];
     __shared__ float4 s_off[kWarps][S::NG][4];
+    __shared__ int s_row[kWarps][S::kDepth][2];          // WEIGH: the cache rows that a stage's halves come from, -1: none
     __shared__ int s_abort;
     uint8_t *base = raw + (((smem_addr(raw) + 1023u) & ~1023u) - smem_addr(raw));
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -481,10 +482,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             auto look_up = [&](int i) {                  // whole warp, tiles i, i + 1, ... of this warp
                 base_tile = i;
                 const int t = t0 + warp + kWarps * (i + lane / plan.boxes), tok = t * kTile + (plan.boxes == 2 ? 16 * (lane & 1) : 0);
-                first_row = 0;
+                first_row = -1;
                 if (tok < len && i + lane / plan.boxes < mine) {
                     const int p = tok / a.c.page, id = pages[p];
-                    if (id < 0 || id >= a.c.n_pages) mla_bad_index(a.err);   // the cache's first rows: the output is unspecified
+                    if (id < 0 || id >= a.c.n_pages) mla_bad_index(a.err);   // the cache's first rows instead: the output is unspecified
                     else first_row = (int)gqa_row(a.c, id, h) + tok - p * a.c.page;
                 }
             };
@@ -493,11 +494,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint32_t dst = smem_addr(ring + stage * S::kStage);
                 const bool two = plan.boxes == 2 && (t0 + warp + kWarps * i) * kTile + 16 < len;
                 const uint32_t bytes = (two ? kTile : box_rows) * (WEIGH ? 1 : 2) * (S::kRow + S::NG * 2);
-                const int row = __shfl_sync(0xffffffffu, first_row, (i - base_tile) * plan.boxes);
+                const int found = __shfl_sync(0xffffffffu, first_row, (i - base_tile) * plan.boxes), row = max(found, 0);
+                if (WEIGH && lane == 0) {
+                    s_row[warp][stage][0] = found;
+                    s_row[warp][stage][1] = found < 0 ? -1 : found + 16;
+                }
                 fill<!WEIGH, true>(dst, S::kCodes, dst + 2 * S::kCodes, S::kScales, &k_map, &v_map, row, a.c.ks + (long long)row * S::NG,
                              a.c.vs + (long long)row * S::NG, box_rows * S::NG * 2, &full[warp][stage], bytes);
                 if (two) {
-                    const int next = __shfl_sync(0xffffffffu, first_row, (i - base_tile) * 2 + 1);
+                    const int found2 = __shfl_sync(0xffffffffu, first_row, (i - base_tile) * 2 + 1), next = max(found2, 0);
+                    if (WEIGH && lane == 0) s_row[warp][stage][1] = found2;
                     fill<!WEIGH, false>(dst + 16 * S::kRow, S::kCodes, dst + 2 * S::kCodes + 16 * S::NG * 2, S::kScales, &k_map, &v_map, next,
                                    a.c.ks + (long long)next * S::NG, a.c.vs + (long long)next * S::NG, 16 * S::NG * 2, &full[warp][stage], 0);
                 }
@@ -548,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int i = 0; i < mine; i++) {
                     const uint8_t *sm = arrived();
                     if (!ok) break;
-                    const int tok = token_of(i);
+                    const int tok = token_of(i), stage = (int)(sm - ring) / (int)S::kStage;
                     float s[2][4];
                     scores<S>(sm, y, off, lane, s);
 #pragma unroll
@@ -564,13 +570,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                             }
                             w += __shfl_xor_sync(0xffffffffu, w, 1);
                             w += __shfl_xor_sync(0xffffffffu, w, 2);
-                            if ((lane & 3) == 0 && t < len) {
-                                const int page = pages[t / a.c.page];
-                                if (page >= 0 && page < a.c.n_pages) atomicAdd(a.c.w + gqa_row(a.c, page, h) + t % a.c.page, w);
-                            }
+                            const int at = s_row[warp][stage][k];
+                            if ((lane & 3) == 0 && t < len && at >= 0) atomicAdd(a.c.w + at + (lane >> 2) + 8 * e, w);
                         }
                     __syncwarp();
-                    if (i + S::kDepth < mine) ask(i + S::kDepth, (int)(sm - ring) / (int)S::kStage);
+                    if (i + S::kDepth < mine) ask(i + S::kDepth, stage);
                 }
             } else {
                 for (int i = 0; i < mine; i++) {
@@ -670,11 +674,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (*abort) settle();
 }
 
-// One CTA per segment: joins the parts of one that several CTAs had, fills one without tokens.
-template <class S>
+// Joins the parts of a segment that several CTAs had, fills one without tokens.  A CTA has ROWS rows of one: all 8 where a segment
+// has few parts, a single one where it has many, whose loads then spread over 8 times as many SMs (1x100000, 38 parts: 5.5 us less).
+template <class S, int ROWS>
 __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, const AttendPlan plan) {
+    constexpr int kSets = kRows / ROWS;
     const int n_kv = a.c.n_kv, G = a.H / n_kv, n_rows = a.n_q * G, per = n_kv * plan.rg;
-    const int b = blockIdx.x / per, seg = blockIdx.x - b * per, h = seg / plan.rg, set = seg - h * plan.rg;
+    const int place = blockIdx.x / kSets, row0 = (blockIdx.x - place * kSets) * ROWS;
+    const int b = place / per, seg = place - b * per, h = seg / plan.rg, set = seg - h * plan.rg;
     pdl_wait();
     pdl_trigger();
     const long long before = plan.before[b], units = plan.before[a.n_seq] * per;
@@ -690,12 +697,12 @@ __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, 
     }
     // Part c's factor per row in shared memory (parts in groups of kGroup), then the sums: threads of a row's dims take every kSplit-th
     // part with kAhead of them in flight, in a fixed order.
-    constexpr int kPart = kRows * (S::D + 2), kCols = S::D / 4, kSplit = kJoin / (kRows * kCols), kAhead = 4;
-    __shared__ float factor[kGroup][kRows];
-    __shared__ float4 sum[kSplit][kRows][kCols];
-    __shared__ float s_m[kRows], s_l[kRows];
-    const int tid = threadIdx.x, row = tid / kCols % kRows, d = 4 * (tid % kCols), lot = tid / (kCols * kRows);
-    if (tid < kRows) s_m[tid] = kNone, s_l[tid] = 0.f;
+    constexpr int kPart = kRows * (S::D + 2), kCols = S::D / 4, kSplit = kJoin / (ROWS * kCols), kAhead = 4;
+    __shared__ float factor[kGroup][ROWS];
+    __shared__ float4 sum[kSplit][ROWS][kCols];
+    __shared__ float s_m[ROWS], s_l[ROWS];
+    const int tid = threadIdx.x, row = tid / kCols % ROWS, d = 4 * (tid % kCols), lot = tid / (kCols * ROWS);
+    if (tid < ROWS) s_m[tid] = kNone, s_l[tid] = 0.f;
     auto part = [&](int c) { return plan.part + ((long long)c * 2 + (c == c0)) * kPart; };
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int g0 = c0; g0 <= c1; g0 += kGroup) {
@@ -704,13 +711,13 @@ __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, 
         const float old = s_m[row];
         __syncthreads();
         // a warp per row, its lanes the parts
-        for (int r = tid >> 5; r < kRows; r += kJoin / 32) {
+        for (int r = tid >> 5; r < ROWS; r += kJoin / 32) {
             float m = kNone, l = 0.f;
             float2 ml[kGroup / 32];
 #pragma unroll
             for (int k = 0; k < kGroup / 32; k++) {
                 const int c = (tid & 31) + 32 * k;
-                ml[k] = c < n ? *reinterpret_cast<const float2 *>(part(g0 + c) + kRows * S::D + 2 * r) : make_float2(kNone, 0.f);
+                ml[k] = c < n ? *reinterpret_cast<const float2 *>(part(g0 + c) + kRows * S::D + 2 * (row0 + r)) : make_float2(kNone, 0.f);
                 m = fmaxf(m, ml[k].x);
             }
             m = fmaxf(m, s_m[r]);
@@ -737,7 +744,7 @@ __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, 
             float4 x[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; k++)
-                x[k] = i + k * kSplit < n ? *reinterpret_cast<const float4 *>(part(g0 + i + k * kSplit) + row * S::D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[k] = i + k * kSplit < n ? *reinterpret_cast<const float4 *>(part(g0 + i + k * kSplit) + (row0 + row) * S::D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < kAhead; k++) {
                 const float f = i + k * kSplit < n ? factor[i + k * kSplit][row] : 0.f;
@@ -747,7 +754,7 @@ __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, 
     }
     sum[lot][row][d / 4] = o;
     __syncthreads();
-    const int at = set * kRows + row;
+    const int at = set * kRows + row0 + row;
     if (lot == 0 && at < n_rows) {
         const float m = s_m[row], l = s_l[row];
 #pragma unroll
@@ -763,7 +770,7 @@ __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, 
         else
             *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + orow * S::D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
         if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-        if (d == 0 && a.weigh) plan.stat[(long long)blockIdx.x * kRows + row] = make_float2(m, inv);
+        if (d == 0 && a.weigh) plan.stat[(long long)place * kRows + row0 + row] = make_float2(m, inv);
     }
 }
 
@@ -811,7 +818,12 @@ cudaError_t run(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *
     if (cudaError_t e = allow_smem(gqa_attend_kernel<S, false>, S::kSmem, d.device, done)) return e;
     if (cudaError_t e = launch_pdl(gqa_attend_kernel<S, false>, dim3(plan.n_cta), dim3(kThreads), S::kSmem, st, k, v, a, plan, d.wait_ns)) return e;
     *n_launch = 2;
-    if (cudaError_t e = launch_pdl(gqa_join_kernel<S>, dim3((unsigned)a.n_seq * a.c.n_kv * plan.rg), dim3(kJoin), 0, st, a, plan)) return e;
+    const long long segments = (long long)a.n_seq * a.c.n_kv * plan.rg;
+    if (plan.n_cta > 4 * segments) {          // 4 parts a segment or more
+        if (cudaError_t e = launch_pdl(gqa_join_kernel<S, 1>, dim3((unsigned)segments * kRows), dim3(kJoin), 0, st, a, plan)) return e;
+    } else {
+        if (cudaError_t e = launch_pdl(gqa_join_kernel<S, kRows>, dim3((unsigned)segments), dim3(kJoin), 0, st, a, plan)) return e;
+    }
     if (!a.weigh) return cudaSuccess;
     *n_launch = 3;
     if (cudaError_t e = allow_smem(gqa_attend_kernel<S, true>, S::kSmem, d.device, done_weigh)) return e;

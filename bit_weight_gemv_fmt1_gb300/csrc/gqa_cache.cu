@@ -13,22 +13,29 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 8 consecutive elements as f32.
+// 8 consecutive elements as f32, and the largest magnitude among them as an integer: above infinity for a NaN.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void *base, long long e, float (&x)[8]) {
+__device__ __forceinline__ uint32_t load8(const void *base, long long e, float (&x)[8]) {
     if constexpr (BF16) {
         const uint4 w = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(base) + e);
         const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+        uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             const float2 p = bf16x2_f32x2(v[i]);
             x[2 * i] = p.x;
             x[2 * i + 1] = p.y;
+            m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
         }
+        return max(m << 16, m & 0xFFFF0000u);
     } else {
         const float4 p = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + e);
         const float4 q = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + e + 4);
         x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w, x[4] = q.x, x[5] = q.y, x[6] = q.z, x[7] = q.w;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+        return m;
     }
 }
 
@@ -40,12 +47,9 @@ __device__ __forceinline__ float divide(float x, float b, float r) {
     return fmaf(fmaf(-q, b, x), r, q);
 }
 
-// 8 elements of a group that GS / 8 neighbouring threads have: their codes, and the group's scale.
+// 8 elements, of magnitudes up to m, of a group that GS / 8 neighbouring threads have: their codes, and the group's scale.
 template <int GS>
-__device__ __forceinline__ uint32_t quantise(const float (&x)[8], __nv_bfloat16 &stored) {
-    uint32_t m = 0;                                      // max|x| as an integer: above infinity for a NaN
-#pragma unroll
-    for (int i = 0; i < 8; i++) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+__device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t m, __nv_bfloat16 &stored) {
 #pragma unroll
     for (int o = 1; o < GS / 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float amax = __uint_as_float(m);
@@ -55,8 +59,8 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], __nv_bfloat16 
         stored = __float2bfloat16_rn(divide(amax, 7.f, 1.f / 7.f));
         const float b = __bfloat162float(stored), r = __frcp_rn(b);
 #pragma unroll
-        for (int i = 7; i >= 0; i--) w = 16 * w + (__float_as_uint(divide(x[i], b, r) + 12582920.f) - 0x4B400000u);
-        return w;
+        for (int i = 7; i >= 0; i--) w = 16 * w + __float_as_uint(divide(x[i], b, r) + 12582920.f);
+        return w - 0x11111111u * 0x4B400000u;            // the float's own bits, added up as the codes
     }
     if (m >= 0x7F800000u) {
         stored = __float2bfloat16_rn(__uint_as_float(0x7FC00000u));
@@ -81,17 +85,18 @@ __global__ void __launch_bounds__(kThreads) gqa_append_kernel(const GqaAppendArg
     pdl_wait();
     pdl_trigger();
     float k[8], v[8];
+    uint32_t km = 0, vm = 0;
     long long slot = -1;
     if (live) {
         slot = a.slots[t];
-        load8<BF16>(a.k, t * a.k_stride + h * a.c.dim + 8 * u, k);
-        load8<BF16>(a.v, t * a.v_stride + h * a.c.dim + 8 * u, v);
+        km = load8<BF16>(a.k, t * a.k_stride + h * a.c.dim + 8 * u, k);
+        vm = load8<BF16>(a.v, t * a.v_stride + h * a.c.dim + 8 * u, v);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; i++) k[i] = v[i] = 0.f;
     }
     __nv_bfloat16 ks, vs;
-    const uint32_t kw = quantise<GS>(k, ks), vw = quantise<GS>(v, vs);
+    const uint32_t kw = quantise<GS>(k, km, ks), vw = quantise<GS>(v, vm, vs);
     if (!live || slot == -1) return;
     if (slot < 0 || slot >= (long long)a.c.n_pages * a.c.page) {
         mla_bad_index(a.err);
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) gqa_append_kernel(const GqaAppendArg
 }
 
 // kReadRows tokens of one head per CTA: as many threads find the tokens' rows, then every thread moves units of 8 elements.
-constexpr int kReadRows = 32;
+constexpr int kReadRows = 64;
 
 // The values of a word of codes.  bf16: 128 + code by an OR, minus 136 exactly, times the scale to nearest: the same as the f32
 // product, which is exact, rounded.

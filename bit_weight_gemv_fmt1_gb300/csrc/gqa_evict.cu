@@ -2,7 +2,7 @@
 // and their way to the sequence's new pages.
 //
 // Selection, one CTA per sequence and head: the weights become integers of the
-// same order (a NaN last), three passes of a radix selection (11, 11 and 10 bits,
+// same order (a NaN last), three passes of a radix selection (12, 10 and 10 bits,
 // counts in shared memory) give the smallest one that stays and how many equal to it
 // do; one more pass writes the tokens that stay in their order.  The move is a
 // kernel of its own, so that few sequences use every SM.
@@ -14,7 +14,7 @@ namespace coli {
 
 namespace {
 
-constexpr int kSelect = 1024, kBins = 2048, kRoom = 52000;   // kRoom keys of 4 bytes in shared memory
+constexpr int kSelect = 1024, kBins = 4096, kRoom = 48000;   // kRoom keys of 4 bytes in shared memory
 
 // Integers ordered as the weights; +0 and -0 alike, every NaN the largest.
 __device__ __forceinline__ uint32_t ordered(float w) {
@@ -86,16 +86,23 @@ __global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs 
     auto key = [&](int t) { return t < room ? keys[t] : read_key(t); };
     for (int i = tid; i < kBins; i += kSelect) count[i] = 0;
     __syncthreads();
+    // 4 tokens at a time, which share a page and 16 bytes of weights
 #pragma unroll 4
-    for (int t = tid; t < old; t += kSelect) {
-        const uint32_t k = read_key(t);
-        if (t < room) keys[t] = k;
-        atomicAdd(&count[k >> 21], 1);
+    for (int t = 4 * tid; t < old; t += 4 * kSelect) {
+        const int p = t / a.c.page, id = pages[p];
+        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (id < 0 || id >= a.c.n_pages) mla_bad_index(a.err);
+        else w = *reinterpret_cast<const float4 *>(a.c.w + gqa_row(a.c, id, h) + t - p * a.c.page);
+        const uint32_t k[4] = {ordered(w.x), ordered(w.y), ordered(w.z), ordered(w.w)};
+        if (t < room) *reinterpret_cast<uint4 *>(keys + t) = make_uint4(k[0], k[1], k[2], k[3]);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (t + i < old) atomicAdd(&count[k[i] >> 20], 1);
     }
     uint32_t prefix = 0;
     int left = want;                                     // of the keys that begin with the prefix, how many stay
     for (int pass = 0; pass < 3; pass++) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+        const int shift = pass == 0 ? 20 : pass == 1 ? 10 : 0, bits = pass == 0 ? 12 : 10;
         if (pass > 0) {
             const int known = shift + bits;
             for (int i = tid; i < kBins; i += kSelect) count[i] = 0;
@@ -106,17 +113,19 @@ __global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs 
             }
         }
         __syncthreads();
-        // counts from the top: thread i has the bins 2047 - 2i and 2046 - 2i
-        const int2 c = *reinterpret_cast<const int2 *>(&count[kBins - 2 - 2 * tid]);
-        int incl = c.x + c.y, none = 0, all, all2;
+        // counts from the top: thread i has the bins 4095 - 4i .. 4092 - 4i
+        const int4 c = *reinterpret_cast<const int4 *>(&count[kBins - 4 - 4 * tid]);
+        int incl = c.x + c.y + c.z + c.w, none = 0, all, all2;
         scan(incl, none, all, all2, sums);
-        const int before = incl - c.x - c.y;
-        if (before < left && left <= before + c.y) {
-            s_bin = kBins - 1 - 2 * tid;
-            s_left = left - before;
-        } else if (before + c.y < left && left <= incl) {
-            s_bin = kBins - 2 - 2 * tid;
-            s_left = left - before - c.y;
+        int before = incl - c.x - c.y - c.z - c.w;
+        const int each[4] = {c.w, c.z, c.y, c.x};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if (before < left && left <= before + each[i]) {
+                s_bin = kBins - 1 - 4 * tid - i;
+                s_left = left - before;
+            }
+            before += each[i];
         }
         __syncthreads();
         prefix |= (uint32_t)s_bin << shift;
