@@ -82,7 +82,7 @@ struct GqaPrefillArgs {
     int *err;
 };
 
-cudaError_t launch_gqa_append(const GqaAppendArgs &a, bool in_bf16, cudaStream_t st);
+cudaError_t launch_gqa_append(const GqaAppendArgs &a, bool in_bf16, int n_sm, cudaStream_t st);
 cudaError_t launch_gqa_read(const GqaReadArgs &a, bool out_bf16, cudaStream_t st);
 cudaError_t launch_gqa_evict(const GqaEvictArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch);
 // Scratch of a call, and the call (d.scratch: that many bytes, NULL if none).

@@ -62,7 +62,7 @@ int append(const coli_gqa_cache *cache, int dtype, const void *k, int64_t k_stri
     a.T = T;
     a.slots = slots;
     a.err = d.err;
-    return launched(launch_gqa_append(a, dtype == COLI_BF16, (cudaStream_t)stream), "coli_gqa_append", 1);
+    return launched(launch_gqa_append(a, dtype == COLI_BF16, d.n_sm, (cudaStream_t)stream), "coli_gqa_append", 1);
 }
 
 int read(const coli_gqa_cache *cache, const int32_t *pages, int64_t pages_stride, int n_seq, const int32_t *cu, int T, int dtype,

@@ -13,31 +13,39 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 8 consecutive elements as f32, and the largest magnitude among them as an integer: above infinity for a NaN.
+// 8 consecutive elements as they stand in memory.
 template <bool BF16>
-__device__ __forceinline__ uint32_t load8(const void *base, long long e, float (&x)[8]) {
-    if constexpr (BF16) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(base) + e);
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-        uint32_t m = 0;
+struct Raw {
+    uint4 w[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void *base, long long e) {
+        const uint4 *at = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(base) + e * (BF16 ? 2 : 4));
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const float2 p = bf16x2_f32x2(v[i]);
-            x[2 * i] = p.x;
-            x[2 * i + 1] = p.y;
-            m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
-        }
-        return max(m << 16, m & 0xFFFF0000u);
-    } else {
-        const float4 p = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + e);
-        const float4 q = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + e + 4);
-        x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w, x[4] = q.x, x[5] = q.y, x[6] = q.z, x[7] = q.w;
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; i++) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-        return m;
+        for (int i = 0; i < (BF16 ? 1 : 2); i++) w[i] = at[i];
     }
-}
+    // The values in f32, and the largest magnitude among them as an integer: above infinity for a NaN.
+    __device__ __forceinline__ uint32_t values(float (&x)[8]) const {
+        uint32_t m = 0;
+        if constexpr (BF16) {
+            const uint32_t v[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float2 two = bf16x2_f32x2(v[i]);
+                x[2 * i] = two.x;
+                x[2 * i + 1] = two.y;
+                m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
+            }
+            return max(m << 16, m & 0xFFFF0000u);
+        } else {
+            const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                x[i] = __uint_as_float(v[i]);
+                m = max(m, v[i] & 0x7FFFFFFFu);
+            }
+            return m;
+        }
+    }
+};
 
 // x / b to nearest from r, the reciprocal of b to nearest, by a step with the exact remainder (Markstein, IBM J. Res. Dev. 1990): 3
 // instructions where a division has about 20.  The theorem wants x r within an ulp of the quotient; for b = 7 and every b of 8 bits
@@ -69,52 +77,52 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t m, __
     stored = __float2bfloat16_rn(__fdiv_rn(amax, 7.f));
     const float b = __bfloat162float(stored), by = b > 0.f ? b : 1.f;
 #pragma unroll
-    for (int i = 0; i < 8; i++) w |= (uint32_t)(__float2int_rn(fminf(fmaxf(__fdiv_rn(x[i], by), -8.f), 7.f)) + 8) << (4 * i);
+    for (int i = 7; i >= 0; i--) w = 16 * w + (uint32_t)(__float2int_rn(fminf(fmaxf(__fdiv_rn(x[i], by), -8.f), 7.f)) + 8);
     return w;
 }
 
-// One thread per 8 elements of a token's key and of its value.
-template <bool BF16, int GS>
+// One thread per 8 elements of a token's key and of its value; a CTA has tokens of one head, and asks for the next ones before it works
+// on those that have come.
+template <bool BF16, int D, int GS>
 __global__ void __launch_bounds__(kThreads) gqa_append_kernel(const GqaAppendArgs a) {
-    const int upr = a.c.dim / 8;                         // 8 or 16
-    const uint32_t row = blockIdx.x * (kThreads / upr) + threadIdx.x / upr;
-    const int u = threadIdx.x & (upr - 1);
-    const uint32_t t = row / a.c.n_kv;
-    const int h = row - t * a.c.n_kv;
-    const bool live = t < (uint32_t)a.T;
+    constexpr int kUnits = D / 8, kTokens = kThreads / kUnits;
+    const int h = blockIdx.y, u = threadIdx.x % kUnits, step = gridDim.x * kTokens;
+    int t = blockIdx.x * kTokens + threadIdx.x / kUnits;
     pdl_wait();
     pdl_trigger();
-    float k[8], v[8];
-    uint32_t km = 0, vm = 0;
+    Raw<BF16> k, v;
     long long slot = -1;
-    if (live) {
-        slot = a.slots[t];
-        km = load8<BF16>(a.k, t * a.k_stride + h * a.c.dim + 8 * u, k);
-        vm = load8<BF16>(a.v, t * a.v_stride + h * a.c.dim + 8 * u, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i++) k[i] = v[i] = 0.f;
+    auto load = [&](int t) {
+        if (t < a.T) {
+            slot = a.slots[t];
+            k.load(a.k, t * a.k_stride + h * D + 8 * u);
+            v.load(a.v, t * a.v_stride + h * D + 8 * u);
+        }
+    };
+    load(t);
+    for (int t0 = blockIdx.x * kTokens; t0 < a.T; t0 += step, t += step) {   // the warp stays together
+        float kx[8], vx[8];
+        const uint32_t km = k.values(kx), vm = v.values(vx);
+        const long long at = t < a.T ? slot : -1;
+        if (t0 + step < a.T) load(t + step);
+        __nv_bfloat16 ks, vs;
+        const uint32_t kw = quantise<GS>(kx, km, ks), vw = quantise<GS>(vx, vm, vs);
+        if (at == -1) continue;
+        if (at < 0 || at >= (long long)a.c.n_pages * a.c.page) {
+            mla_bad_index(a.err);
+            continue;
+        }
+        const int place = (int)at, page = place / a.c.page;   // n_pages * page_size < 2^31, rows too
+        const int r = (page * a.c.n_kv + h) * a.c.page + (place - page * a.c.page);
+        reinterpret_cast<uint32_t *>(a.c.k)[(long long)r * kUnits + u] = kw;
+        reinterpret_cast<uint32_t *>(a.c.v)[(long long)r * kUnits + u] = vw;
+        if (u % (GS / 8) == 0) {
+            a.c.ks[(long long)r * (D / GS) + u / (GS / 8)] = ks;
+            a.c.vs[(long long)r * (D / GS) + u / (GS / 8)] = vs;
+        }
+        if (u == 0 && a.c.w) a.c.w[r] = 0.f;
     }
-    __nv_bfloat16 ks, vs;
-    const uint32_t kw = quantise<GS>(k, km, ks), vw = quantise<GS>(v, vm, vs);
-    if (!live || slot == -1) return;
-    if (slot < 0 || slot >= (long long)a.c.n_pages * a.c.page) {
-        mla_bad_index(a.err);
-        return;
-    }
-    const int at = (int)slot, page = at / a.c.page;      // n_pages * page_size < 2^31
-    const long long r = gqa_row(a.c, page, h) + (at - page * a.c.page);
-    reinterpret_cast<uint32_t *>(a.c.k)[r * upr + u] = kw;
-    reinterpret_cast<uint32_t *>(a.c.v)[r * upr + u] = vw;
-    if (u % (GS / 8) == 0) {
-        a.c.ks[r * (a.c.dim / GS) + u / (GS / 8)] = ks;
-        a.c.vs[r * (a.c.dim / GS) + u / (GS / 8)] = vs;
-    }
-    if (u == 0 && a.c.w) a.c.w[r] = 0.f;
 }
-
-// kReadRows tokens of one head per CTA: as many threads find the tokens' rows, then every thread moves units of 8 elements.
-constexpr int kReadRows = 64;
 
 // The values of a word of codes.  bf16: 128 + code by an OR, minus 136 exactly, times the scale to nearest: the same as the f32
 // product, which is exact, rounded.
@@ -138,6 +146,10 @@ __device__ __forceinline__ void store8(void *base, long long e, uint32_t w, uint
         d[1] = make_float4(x[4], x[5], x[6], x[7]);
     }
 }
+
+// kReadRows tokens of one head per CTA: as many threads find the tokens' rows, then every thread moves units of 8 elements.  (Every
+// thread of a row finding it by itself, without the barrier: slower, 21 us where this takes 16.5.)
+constexpr int kReadRows = 32;
 
 template <bool OB, int D>
 __global__ void __launch_bounds__(kThreads) gqa_read_kernel(const GqaReadArgs a) {
@@ -163,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) gqa_read_kernel(const GqaReadArgs a)
                 mla_bad_index(a.err);
                 row = -1;
             } else {
-                row = (int)gqa_row(a.c, id, h) + (i - pi * a.c.page);
+                row = (id * a.c.n_kv + h) * a.c.page + (i - pi * a.c.page);
             }
         }
         s_row[threadIdx.x] = row;
@@ -192,30 +204,33 @@ __global__ void __launch_bounds__(kThreads) gqa_read_kernel(const GqaReadArgs a)
     }
 }
 
-template <bool BF16>
-cudaError_t append(const GqaAppendArgs &a, cudaStream_t st) {
-    const long long rows = (long long)a.T * a.c.n_kv, per = kThreads / (a.c.dim / 8);
-    const dim3 grid((unsigned)((rows + per - 1) / per)), block(kThreads);
-    switch (a.c.gs) {
-        case 32: return launch_pdl(gqa_append_kernel<BF16, 32>, grid, block, 0, st, a);
-        case 64: return launch_pdl(gqa_append_kernel<BF16, 64>, grid, block, 0, st, a);
-        default: return launch_pdl(gqa_append_kernel<BF16, 128>, grid, block, 0, st, a);
-    }
+template <bool BF16, int D, int GS>
+cudaError_t append_by(const GqaAppendArgs &a, int n_sm, cudaStream_t st) {
+    constexpr int kTokens = kThreads / (D / 8);
+    const int want = (a.T + kTokens - 1) / kTokens, most = (4 * n_sm + a.c.n_kv - 1) / a.c.n_kv;   // 4 CTAs an SM
+    return launch_pdl(gqa_append_kernel<BF16, D, GS>, dim3(want < most ? want : most, a.c.n_kv), dim3(kThreads), 0, st, a);
+}
+template <bool BF16, int D>
+cudaError_t append(const GqaAppendArgs &a, int n_sm, cudaStream_t st) {
+    if (a.c.gs == 32) return append_by<BF16, D, 32>(a, n_sm, st);
+    if (a.c.gs == 64) return append_by<BF16, D, 64>(a, n_sm, st);
+    return append_by<BF16, D, D>(a, n_sm, st);           // 128: dim is 128 then
+}
+template <bool OB, int D>
+cudaError_t read(const GqaReadArgs &a, cudaStream_t st) {
+    return launch_pdl(gqa_read_kernel<OB, D>, dim3((a.T + kReadRows - 1) / kReadRows, a.c.n_kv), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace
 
-cudaError_t launch_gqa_append(const GqaAppendArgs &a, bool in_bf16, cudaStream_t st) {
-    return in_bf16 ? append<true>(a, st) : append<false>(a, st);
+cudaError_t launch_gqa_append(const GqaAppendArgs &a, bool in_bf16, int n_sm, cudaStream_t st) {
+    if (a.c.dim == 64) return in_bf16 ? append<true, 64>(a, n_sm, st) : append<false, 64>(a, n_sm, st);
+    return in_bf16 ? append<true, 128>(a, n_sm, st) : append<false, 128>(a, n_sm, st);
 }
 
 cudaError_t launch_gqa_read(const GqaReadArgs &a, bool out_bf16, cudaStream_t st) {
-    const dim3 grid((a.T + kReadRows - 1) / kReadRows, a.c.n_kv), block(kThreads);
-    if (a.c.dim == 64)
-        return out_bf16 ? launch_pdl(gqa_read_kernel<true, 64>, grid, block, 0, st, a)
-                        : launch_pdl(gqa_read_kernel<false, 64>, grid, block, 0, st, a);
-    return out_bf16 ? launch_pdl(gqa_read_kernel<true, 128>, grid, block, 0, st, a)
-                    : launch_pdl(gqa_read_kernel<false, 128>, grid, block, 0, st, a);
+    if (a.c.dim == 64) return out_bf16 ? read<true, 64>(a, st) : read<false, 64>(a, st);
+    return out_bf16 ? read<true, 128>(a, st) : read<false, 128>(a, st);
 }
 
 }  // namespace coli

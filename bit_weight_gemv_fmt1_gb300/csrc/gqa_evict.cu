@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs 
 // A warp has 32 rows that stay: each lane finds one's old and new place and moves its scales and weight, then the lanes move all their
 // codes, 16 bytes each, keys first.
 template <int D>
-__global__ void __launch_bounds__(256) gqa_move_kernel(const GqaEvictArgs a) {
-    constexpr int kHalf = D / 32, kEach = 2 * kHalf;     // 16-byte pieces of a row's key, of a row
+__global__ void __launch_bounds__(256, 6) gqa_move_kernel(const GqaEvictArgs a) {
+    constexpr int kHalf = D / 32;        // 16-byte pieces of a row's key, and of its value
     const int lane = threadIdx.x & 31, per = (a.keep + 31) / 32;
     const long long w = blockIdx.x * 8LL + (threadIdx.x >> 5);
     const int pair = (int)(w / per), i = (int)(w - (long long)pair * per) * 32 + lane;
@@ -173,31 +173,29 @@ __global__ void __launch_bounds__(256) gqa_move_kernel(const GqaEvictArgs a) {
             d = (int)gqa_row(a.c, to, h) + i - dp * a.c.page;
         }
     }
-    uint4 x[kEach];
+    // keys, then values: half the registers of both at once, and more warps
+#pragma unroll 1
+    for (int value = 0; value < 2; value++) {
+        uint4 *codes = reinterpret_cast<uint4 *>(value ? a.c.v : a.c.k);
+        uint4 x[kHalf];
 #pragma unroll
-    for (int k = 0; k < kEach; k++) {
-        const int piece = (k % kHalf) * 32 + lane;
-        const int row = __shfl_sync(0xffffffffu, s, piece / kHalf);
-        if (row >= 0) x[k] = reinterpret_cast<const uint4 *>(k < kHalf ? a.c.k : a.c.v)[(long long)row * kHalf + piece % kHalf];
-    }
-    if (s >= 0) {
-        const float weight = a.c.w[s];
-        auto scales = [&](auto *ks, auto *vs) {
-            const auto p = ks[s], q = vs[s];
-            ks[d] = p;
-            vs[d] = q;
-        };
-        const int ng = D / a.c.gs;
-        if (ng == 4) scales(reinterpret_cast<uint2 *>(a.c.ks), reinterpret_cast<uint2 *>(a.c.vs));
-        else if (ng == 2) scales(reinterpret_cast<uint32_t *>(a.c.ks), reinterpret_cast<uint32_t *>(a.c.vs));
-        else scales(reinterpret_cast<uint16_t *>(a.c.ks), reinterpret_cast<uint16_t *>(a.c.vs));
-        a.c.w[d] = weight;
-    }
+        for (int k = 0; k < kHalf; k++) {
+            const int piece = k * 32 + lane, row = __shfl_sync(0xffffffffu, s, piece / kHalf);
+            if (row >= 0) x[k] = codes[(long long)row * kHalf + piece % kHalf];
+        }
+        if (s >= 0) {
+            void *sc = value ? a.c.vs : a.c.ks;
+            const int ng = D / a.c.gs;
+            if (ng == 4) reinterpret_cast<uint2 *>(sc)[d] = reinterpret_cast<const uint2 *>(sc)[s];
+            else if (ng == 2) reinterpret_cast<uint32_t *>(sc)[d] = reinterpret_cast<const uint32_t *>(sc)[s];
+            else reinterpret_cast<uint16_t *>(sc)[d] = reinterpret_cast<const uint16_t *>(sc)[s];
+            if (value) a.c.w[d] = a.c.w[s];
+        }
 #pragma unroll
-    for (int k = 0; k < kEach; k++) {
-        const int piece = (k % kHalf) * 32 + lane;
-        const int row = __shfl_sync(0xffffffffu, d, piece / kHalf);
-        if (row >= 0) reinterpret_cast<uint4 *>(k < kHalf ? a.c.k : a.c.v)[(long long)row * kHalf + piece % kHalf] = x[k];
+        for (int k = 0; k < kHalf; k++) {
+            const int piece = k * 32 + lane, row = __shfl_sync(0xffffffffu, d, piece / kHalf);
+            if (row >= 0) codes[(long long)row * kHalf + piece % kHalf] = x[k];
+        }
     }
 }
 
