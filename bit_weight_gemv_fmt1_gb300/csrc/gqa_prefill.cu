@@ -6,7 +6,8 @@
 // down), brought by one box over (dims, heads, tokens): a sequence of few tokens fills a tile with its heads, and a group's
 // keys and values are read once for all of them.  The grid has a CTA per unit, longest first; a CTA that nears its
 // unit's end takes over one that has not started (cluster launch control), so that the next queries, keys and
-// scores come while the last output is written.
+// scores come while the last output is written.  (A CTA per SM and units dealt out there and back
+// measures the same within 2 %.)
 //   S = Q K^T   M = 128 queries, N = 128 keys, K = dim (K-major operands in shared memory)
 //   O += P V    M = 128 queries, N = dim, K = 128 keys (P in TMEM, V as stored: N-major)
 // The two tiles alternate: while the softmax of one runs, the tensor cores work
@@ -34,7 +35,8 @@ namespace coli {
 
 namespace {
 
-constexpr int kKeys = 6, kValues = 4;    // ring slots: key blocks of 64 dims, value halves of 64 keys
+constexpr int kKeys = 5, kValues = 4;    // ring slots: key blocks of 64 dims, value halves of 64 keys
+constexpr uint32_t kOut = 32 * 64;       // bytes of a warp's outputs on their way: 64 of each row
 
 struct Shared {
     uint64_t q_full[2], q_empty[2], k_full[kKeys], k_empty[kKeys], v_full[kValues], v_empty[kValues], s_full[2], p_full[2][2], o_full[2],
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(384, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     constexpr int nb = D / 64;                           // blocks of a query or key tile
     constexpr uint32_t kHalf = nb * (kBlk / 2);          // 64 value rows
-    constexpr uint32_t k_off = 2 * nb * kBlk, v_off = k_off + kKeys * kBlk;
+    constexpr uint32_t k_off = 2 * nb * kBlk, v_off = k_off + kKeys * kBlk, o_off = v_off + kValues * kHalf;
     pdl_wait();
     pdl_trigger();
     if (warp == 0) tmem_alloc(&s.tmem, 512);
@@ -127,8 +129,7 @@ __global__ void __launch_bounds__(384, 1)
             atomicCAS(a.err, 0, (int)DEV_ERR_TIMEOUT);
         }
     };
-    // Unit r of this CTA as the key warp has found it; the warp that has read it says so.  It comes when the keys of the unit
-    // before have been asked for: a warp with no tile in that one waits for all of its time.
+    // Unit r of this CTA as the key warp has found it; the warp that has read it says so.
     auto take = [&](int r) {
         wait(&s.u_full[r & 1], (r >> 1) & 1);
         Unit u = s.unit[r & 1];
@@ -175,10 +176,15 @@ __global__ void __launch_bounds__(384, 1)
                 if (negative)
 #pragma unroll
                     for (int c = 0; c < kRows; c++) v[c] ^= 0x80000000u;
+                // Rows of a warp see ever more keys: blocks of 32 keys before `least` are seen by all, from `most` on by none.
+                const int least = full ? kRows : __shfl_sync(0xffffffffu, seen, 0), most = full ? kRows : __shfl_sync(0xffffffffu, seen, 31);
                 if (!full)
 #pragma unroll
-                    for (int c = 0; c < kRows; c++)
-                        if (c >= seen) v[c] = 0xFF800000u;
+                    for (int c0 = 0; c0 < kRows; c0 += 32)
+                        if (c0 + 32 > least)
+#pragma unroll
+                            for (int c = c0; c < c0 + 32; c++)
+                                if (c >= seen) v[c] = 0xFF800000u;
                 float t4[4];
 #pragma unroll
                 for (int k = 0; k < 4; k++) t4[k] = max3(__uint_as_float(v[k]), __uint_as_float(v[4 + k]), __uint_as_float(v[8 + k]));
@@ -225,6 +231,12 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                     for (int c0 = 64 * h; c0 < 64 * h + 64; c0 += 32) {
                         uint32_t p[16];
+                        if (c0 >= most) {
+#pragma unroll
+                            for (int c = 0; c < 16; c++) p[c] = 0;
+                            tmem_st(S + c0 / 2, p);
+                            continue;
+                        }
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
                             float x, y;
@@ -248,6 +260,27 @@ __global__ void __launch_bounds__(384, 1)
                 wait(&s.o_full[x], outs++ & 1);
                 tc_after_sync();
             }
+            // Rows go out through shared memory, 64 bytes of each at a time: 4 threads then write a row's piece together, where a thread's
+            // own 16 bytes of 32 different rows cost 2.5 us a unit.
+            uint8_t *stage = sm + o_off + warp * kOut;
+            int dst[4];                                  // the output rows of this thread's pieces
+#pragma unroll
+            for (int i = 0; i < 4; i++) dst[i] = __shfl_sync(0xffffffffu, (int)orow, 8 * i + (lane >> 2));
+            auto send = [&](const uint32_t (&w)[16], int byte) {   // 64 bytes of this thread's row
+                const int x = lane >> 1 & 3;             // pieces of 16 bytes in an order of the row's own: no bank twice
+#pragma unroll
+                for (int c = 0; c < 4; c++)
+                    *reinterpret_cast<uint4 *>(stage + lane * 64 + ((c ^ x) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int row = 8 * i + (lane >> 2), piece = lane & 3;
+                    const uint4 y = *reinterpret_cast<const uint4 *>(stage + row * 64 + ((piece ^ (row >> 1 & 3)) << 4));
+                    if (dst[i] >= 0)
+                        *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(a.out) + (long long)dst[i] * (D * (a.out_bf16 ? 2 : 4)) + byte + 16 * piece) = y;
+                }
+                __syncwarp();
+            };
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t o[32];
@@ -258,22 +291,20 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                     for (int c = 0; c < 32; c++) o[c] = 0u;
                 }
-                if (orow < 0) continue;
 #pragma unroll
                 for (int c = 0; c < 32; c++) o[c] = __float_as_uint(F16 ? scaled(__uint_as_float(o[c]) * inv, -ev) : __uint_as_float(o[c]) * inv);
+                uint32_t w[16];
                 if (a.out_bf16) {
-                    uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * D + c0);
 #pragma unroll
-                    for (int c = 0; c < 32; c += 8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; k++) w[k] = pack_bf16(__uint_as_float(o[c + 2 * k]), __uint_as_float(o[c + 2 * k + 1]));
-                        d[c / 8] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int c = 0; c < 16; c++) w[c] = pack_bf16(__uint_as_float(o[2 * c]), __uint_as_float(o[2 * c + 1]));
+                    send(w, 2 * c0);
                 } else {
-                    uint4 *d = reinterpret_cast<uint4 *>(reinterpret_cast<float *>(a.out) + orow * D + c0);
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) d[c / 4] = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    for (int k = 0; k < 2; k++) {
+#pragma unroll
+                        for (int c = 0; c < 16; c++) w[c] = o[16 * k + c];
+                        send(w, 4 * c0 + 64 * k);
+                    }
                 }
             }
             if (orow >= 0 && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -583,7 +614,7 @@ cudaError_t run(const GqaPrefillArgs &a, const DevInfo &d, cudaStream_t st) {
     }
     // at most; every unit that is not empty has a row of its own
     const long long units = std::min((long long)a.Tq, ((long long)a.Tq + 2 * a.tokens - 1) / (2 * a.tokens) + a.n_seq - 1) * a.H;
-    constexpr size_t smem = (2 * (D / 64) + kKeys) * kBlk + kValues * (D / 64) * (kBlk / 2) + 1024;
+    constexpr size_t smem = (2 * (D / 64) + kKeys) * kBlk + kValues * (D / 64) * (kBlk / 2) + 8 * kOut + 1024;
     static std::atomic<uint64_t> done{0};
     if (cudaError_t e = allow_smem(gqa_prefill_kernel<D, F16>, smem, d.device, done)) return e;
     return launch_pdl(gqa_prefill_kernel<D, F16>, dim3((unsigned)units), dim3(384), smem, st, q, k, v, a, d.wait_ns);
