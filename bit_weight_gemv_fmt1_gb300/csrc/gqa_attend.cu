@@ -23,7 +23,7 @@
 // always finite numbers, their scales need not be.
 // Weights need the final maximum and sum, so a third kernel goes over the keys again: keeping the
 // scores instead would need scratch for every token that the page tables could hold.
-// Every wait is bounded, by a limit that each segment renews.
+// Every wait is bounded, by a limit that each segment and set of rows renews.
 #include <algorithm>
 
 #include "encode_tiled.cuh"
@@ -473,9 +473,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int h = WEIGH ? seg : seg / plan.rg;
         const int32_t *pages = a.pages + b * a.pages_stride;
         const int mine = (t1 - t0 - warp + kWarps - 1) / kWarps;   // tiles t0 + warp, t0 + warp + 8, ...
-        const uint64_t deadline = deadline_after(wait_ns, max(mine, 0));
         for (int set = WEIGH ? 0 : seg - h * plan.rg, sets = WEIGH ? plan.rg : set + 1; set < sets; set++) {
             const int r0 = set * kRows;
+            const uint64_t deadline = deadline_after(wait_ns, max(mine, 0));
             // copies: lane i holds the first row of the i-th box from `base_tile` on
             int first_row = 0, base_tile = 0;
             const int per_load = 32 / plan.boxes, box_rows = kTile / plan.boxes;
