@@ -2,8 +2,8 @@
 // the weights that its rows get.
 //
 // A unit of work is a tile of 32 cached tokens of one sequence and key / value head, for 8 query rows (n_q tokens x the
-// group's heads).  The units of all sequences stand in one row; every CTA takes an equal share of it and walks
-// it by segments (the tiles of one sequence, head and set of rows).  A segment's tiles go round the CTA's 8 warps, each
+// group's heads).  A segment is the tiles of one sequence, head and set of rows; CTAs have a piece of one each, or, where segments
+// are many, an equal share of all units in a row, which they walk by segments.  A segment's tiles go round the CTA's 8 warps, each
 // with a running maximum, sum and output of its own and a ring of tiles that bulk copies fill; the warps join at the
 // segment's end.  A segment that several CTAs have is joined by a second kernel.
 //
@@ -56,7 +56,7 @@ struct AttendPlan {
     float *part;                         // [n_cta][2][kRows][D + 2]: O, m, l
     float2 *stat;                        // [n_seq][n_kv][rg][kRows]: m and 1 / l, for the weights
     uint32_t magic;                      // 128 in bf16, twice
-    long long *before;                   // [n_seq + 1]: tiles of the sequences before each, for the join
+    long long *before;                   // [n_seq + 2]: tiles (or pieces) of the sequences before each and of all, tiles of a piece
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -114,9 +114,6 @@ __device__ __forceinline__ void fill(uint32_t dst, uint32_t v_off, uint32_t scal
 __device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// CTAs that have work: fewer than the grid where a CTA's warps would not have a unit each.
-__device__ __forceinline__ long long working(long long units, int grid) { return min((long long)grid, (units + kWarps - 1) / kWarps); }
-
 __device__ __forceinline__ int length_of(const GqaAttendArgs &a, int b, bool report) {
     const int n = a.lens[b];
     if (n >= 0 && n <= a.pages_stride * a.c.page) return n;
@@ -125,19 +122,25 @@ __device__ __forceinline__ int length_of(const GqaAttendArgs &a, int b, bool rep
 }
 __device__ __forceinline__ int tiles_of(const GqaAttendArgs &a, int b) { return (length_of(a, b, false) + kTile - 1) / kTile; }
 
-// Where a CTA's work begins.
-struct Start {
-    long long tiles, u, first;           // tiles of all sequences, the CTA's first unit, the tiles before its sequence
+// A CTA's work.
+struct Share {
+    int piece;                           // tiles of a piece at most; 0: a share of the row of units
+    long long u, u1;                     // the CTA's units, or its own number
+    long long first;                     // units (or pieces) of the sequences before `seq`, by segment
     int seq;                             // -1: no work
 };
-// The whole CTA: units are tiles * per; CTA i of the n that work has those from units * i / n on.
-// The first CTA writes `before` if there is one.
-__device__ __forceinline__ Start find_start(const GqaAttendArgs &a, int per, long long *before) {
+// The whole CTA: how the tiles of all sequences, `per` segments each, are dealt out.
+// Pieces: every segment is cut into pieces of at most 8 r tiles, r for each warp, a CTA each.  r is the rounds of an even
+// share, or up to 2 more: what a CTA pays whose share spans two segments (look-ups, first copies, two joins: 3 to 4 us, a round takes
+// 1.7).  Where no such pieces fit the grid, every CTA has an even share of the units in a row.
+// The first CTA writes `before`, if there is one: the sums, and `piece`.
+__device__ __forceinline__ Share find_share(const GqaAttendArgs &a, int per, long long *before) {
     __shared__ long long sums[kWarps];
+    __shared__ int counts[kWarps][3];
     __shared__ long long s_first;
     __shared__ int s_seq;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long mine = tid < a.n_seq ? tiles_of(a, tid) : 0;
+    const int mine = tid < a.n_seq ? tiles_of(a, tid) : 0;
     long long n = mine;
     for (int b = tid + kThreads; b < a.n_seq; b += kThreads) n += tiles_of(a, b);
 #pragma unroll
@@ -145,18 +148,47 @@ __device__ __forceinline__ Start find_start(const GqaAttendArgs &a, int per, lon
     if (tid == 0) s_seq = -1;
     if (lane == 0) sums[warp] = n;
     __syncthreads();
-    Start z;
-    z.tiles = 0;
-    for (int w = 0; w < kWarps; w++) z.tiles += sums[w];
-    const long long units = z.tiles * per, n_cta = working(units, gridDim.x);
+    long long tiles = 0;
+    for (int w = 0; w < kWarps; w++) tiles += sums[w];
+    const long long units = tiles * per;
+    const int grid = gridDim.x;
+    // pieces of 8 r, 8 (r + 1) and 8 (r + 2) tiles
+    const int least = (int)min((units + 8LL * grid - 1) / (8LL * grid), 1LL << 27) * 8;
+    int k[3] = {0, 0, 0};
+    for (int b = tid; b < a.n_seq; b += kThreads) {
+        const int t = b == tid ? mine : tiles_of(a, b);
+#pragma unroll
+        for (int i = 0; i < 3; i++) k[i] += t ? (t - 1) / max(least + 8 * i, 1) + 1 : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 3; i++) {
+        k[i] = __reduce_add_sync(0xffffffffu, k[i]);
+        if (lane == 0) counts[warp][i] = k[i];
+    }
+    __syncthreads();
+    Share z;
+    z.piece = 0;
+    long long pieces = 0;
+#pragma unroll
+    for (int i = 2; i >= 0; i--) {
+        long long all = 0;
+        for (int w = 0; w < kWarps; w++) all += counts[w][i];
+        if (all * per <= grid) {
+            z.piece = max(least + 8 * i, 1);
+            pieces = all * per;
+        }
+    }
     z.seq = -1;
-    const bool work = blockIdx.x < n_cta, writes = before && blockIdx.x == 0;
+    const bool work = z.piece ? blockIdx.x < pieces : blockIdx.x < units, writes = before && blockIdx.x == 0;
     if (!work && !writes) return z;
-    z.u = work ? units * blockIdx.x / n_cta : 0;
+    const long long n_cta = min((long long)grid, units);
+    z.u = z.piece ? (long long)blockIdx.x : work ? units * blockIdx.x / n_cta : 0;
+    z.u1 = z.piece ? z.u + 1 : work ? units * (blockIdx.x + 1) / n_cta : 0;
     long long run = 0;
     for (int b0 = 0; b0 < a.n_seq; b0 += kThreads) {
         const int b = b0 + tid;
         n = b0 == 0 ? mine : b < a.n_seq ? tiles_of(a, b) : 0;
+        if (z.piece && n) n = ((int)n - 1) / z.piece + 1;
         long long incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -179,7 +211,10 @@ __device__ __forceinline__ Start find_start(const GqaAttendArgs &a, int per, lon
         __syncthreads();
         if (s_seq >= 0 && !writes) break;
     }
-    if (writes && tid == 0) before[a.n_seq] = z.tiles;
+    if (writes && tid == 0) {
+        before[a.n_seq] = run;
+        before[a.n_seq + 1] = z.piece;
+    }
     z.seq = s_seq;
     z.first = s_first;
     return z;
@@ -459,17 +494,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int per = WEIGH ? n_kv : n_kv * plan.rg;       // segments of a sequence
     if (!WEIGH && blockIdx.x == 0)
         for (int b = tid; b < a.n_seq; b += kThreads) length_of(a, b, true);
-    const Start start = find_start(a, per, WEIGH ? nullptr : plan.before);
-    if (start.seq < 0) return;
-    const long long units = start.tiles * per, n_cta = working(units, gridDim.x), u1 = units * (blockIdx.x + 1) / n_cta;
-    long long u = start.u, first = start.first;
-    int b = start.seq;
+    const Share share = find_share(a, per, WEIGH ? nullptr : plan.before);
+    if (share.seq < 0) return;
+    const long long u1 = share.u1;
+    long long u = share.u, first = share.first;
+    int b = share.seq;
     int slot = 0, par = 0;                               // next stage to be read, parity of its use
     bool ok = true;
     while (u < u1) {
         const int len = length_of(a, b, false), nt = (len + kTile - 1) / kTile;
         const long long at = u - first * per;
-        const int seg = (int)(at / nt), t0 = (int)(at - (long long)seg * nt), t1 = (int)min((long long)nt, t0 + (u1 - u));
+        const int each = share.piece ? (nt - 1) / share.piece + 1 : nt;   // pieces or tiles of a segment
+        const int seg = (int)(at / each), k = (int)(at - (long long)seg * each);
+        const int t0 = share.piece ? (int)((long long)nt * k / each) : k;
+        const int t1 = share.piece ? (int)((long long)nt * (k + 1) / each) : (int)min((long long)nt, t0 + (u1 - u));
         const int h = WEIGH ? seg : seg / plan.rg;
         const int32_t *pages = a.pages + b * a.pages_stride;
         const int mine = (t1 - t0 - warp + kWarps - 1) / kWarps;   // tiles t0 + warp, t0 + warp + 8, ...
@@ -663,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 ok = ok && !*abort;
             }
         }
-        u += t1 - t0;
+        u += share.piece ? 1 : t1 - t0;
         if (u < u1 && at + (t1 - t0) == (long long)nt * per) {
             first += nt;
             do b++;
@@ -685,12 +723,16 @@ __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, 
     pdl_wait();
     pdl_trigger();
     const long long before = plan.before[b], units = plan.before[a.n_seq] * per;
-    const int nt = (int)(plan.before[b + 1] - before);
+    const int nt = (int)(plan.before[b + 1] - before);   // tiles, or pieces
     const long long u0 = before * per + (long long)seg * nt;
     int c0 = 0, c1 = -1;
-    if (nt > 0) {
+    if (plan.before[a.n_seq + 1]) {                      // a CTA per piece
+        c0 = (int)u0;
+        c1 = c0 + nt - 1;
+        if (nt == 1) return;
+    } else if (nt > 0) {
         // the CTA of unit u is the largest c with units * c / n <= u, of the n that have units
-        const long long n = working(units, plan.n_cta);
+        const long long n = min((long long)plan.n_cta, units);
         c0 = (int)(((u0 + 1) * n - 1) / units);
         c1 = (int)(((u0 + nt) * n - 1) / units);
         if (c0 == c1) return;
@@ -809,7 +851,7 @@ cudaError_t run(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *
     plan.part = (float *)d.scratch;
     plan.magic = 0x43004300u;
     plan.before = (long long *)((char *)d.scratch + part_bytes(a, plan.n_cta));
-    plan.stat = (float2 *)((char *)plan.before + round256((size_t)(a.n_seq + 1) * sizeof(long long)));
+    plan.stat = (float2 *)((char *)plan.before + round256((size_t)(a.n_seq + 2) * sizeof(long long)));
     CUtensorMap k, v;
     const long long rows = (long long)a.c.n_pages * a.c.n_kv * a.c.page;
     if (cudaError_t e = code_map(a.c.k, S::kRow, rows, kTile / plan.boxes, &k)) return e;
@@ -834,7 +876,7 @@ cudaError_t run(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *
 
 size_t gqa_attend_scratch(const GqaAttendArgs &a, int n_sm) {
     const int n_cta = grid_of(a, n_sm);
-    return part_bytes(a, n_cta) + round256((size_t)(a.n_seq + 1) * sizeof(long long)) + (a.weigh ? (size_t)a.n_seq * a.c.n_kv * row_groups(a) * kRows * sizeof(float2) : 0);
+    return part_bytes(a, n_cta) + round256((size_t)(a.n_seq + 2) * sizeof(long long)) + (a.weigh ? (size_t)a.n_seq * a.c.n_kv * row_groups(a) * kRows * sizeof(float2) : 0);
 }
 
 cudaError_t launch_gqa_attend(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch) {
