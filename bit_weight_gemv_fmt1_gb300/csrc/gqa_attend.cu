@@ -45,10 +45,15 @@ struct Shape {
     static constexpr int D = D_, NG = NG_;              // dims, scale groups of a row
     static constexpr int kParts = D / 32, kPer = kParts / NG, kRow = D / 2;
     static constexpr uint32_t kCodes = kTile * kRow, kScales = kTile * NG * 2;
-    static constexpr uint32_t kStage = (2 * kCodes + 2 * kScales + 511) / 512 * 512;
+};
+// A warp's ring of tiles: keys' codes, values' codes, keys' scales, values' scales; the keys' alone for the weights.
+template <class S, bool WEIGH>
+struct Ring {
+    static constexpr uint32_t kScaleAt = (WEIGH ? 1 : 2) * S::kCodes;
+    static constexpr uint32_t kStage = (kScaleAt + (WEIGH ? 1 : 2) * S::kScales + 511) / 512 * 512;
     static constexpr int kDepth = std::min(8u, 110u * 1024u / (kWarps * kStage));   // two CTAs on an SM
     static constexpr uint32_t kSmem = kWarps * kDepth * kStage + 1024;
-    static_assert(kDepth * kStage >= kRows * D * 4, "a warp's output fits its ring");
+    static_assert(WEIGH || kDepth * kStage >= kRows * S::D * 4, "a warp's output fits its ring");
 };
 
 struct AttendPlan {
@@ -422,10 +427,10 @@ __device__ __forceinline__ void outputs(uint32_t magic, const uint8_t *sm, const
     }
 }
 template <class S>
-__device__ __forceinline__ void scores(const uint8_t *sm, const Query<S> &y, const float4 (*off)[4], int lane, float (&s)[2][4]) {
+__device__ __forceinline__ void scores(const uint8_t *sm, const uint8_t *scales, const Query<S> &y, const float4 (*off)[4], int lane, float (&s)[2][4]) {
     float sc[4][S::NG];
 #pragma unroll
-    for (int e = 0; e < 4; e++) load_scales<S>(sm + 2 * S::kCodes, 8 * e + (lane >> 2), sc[e]);
+    for (int e = 0; e < 4; e++) load_scales<S>(scales, 8 * e + (lane >> 2), sc[e]);
     const uint32_t at = smem_addr(sm) + lane * S::kRow;
     const int x = swizzle<S>(lane);
 #pragma unroll
@@ -473,17 +478,18 @@ template <class S, bool WEIGH>
 __global__ void __launch_bounds__(kThreads, 2)
     gqa_attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const GqaAttendArgs a,
                       const AttendPlan plan, long long wait_ns) {
+    using R = Ring<S, WEIGH>;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[kWarps][S::kDepth];
+    __shared__ uint64_t full[kWarps][R::kDepth];
     __shared__ float2 ml[kWarps][kRows];
     __shared__ float4 s_off[kWarps][S::NG][4];
-    __shared__ int s_row[kWarps][S::kDepth][2];          // WEIGH: the cache rows that a stage's halves come from, -1: none
+    __shared__ int s_row[kWarps][R::kDepth][2];          // WEIGH: the cache rows that a stage's halves come from, -1: none
     __shared__ int s_abort;
     uint8_t *base = raw + (((smem_addr(raw) + 1023u) & ~1023u) - smem_addr(raw));
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    uint8_t *ring = base + warp * S::kDepth * S::kStage;
+    uint8_t *ring = base + warp * R::kDepth * R::kStage;
     if (lane == 0)
-        for (int i = 0; i < S::kDepth; i++) mbar_init(&full[warp][i], 1);
+        for (int i = 0; i < R::kDepth; i++) mbar_init(&full[warp][i], 1);
     if (tid == 0) s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_wait();
@@ -529,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             };
             auto ask = [&](int i, int stage) {           // whole warp
                 if (i - base_tile >= per_load) look_up(i);
-                const uint32_t dst = smem_addr(ring + stage * S::kStage);
+                const uint32_t dst = smem_addr(ring + stage * R::kStage);
                 const bool two = plan.boxes == 2 && (t0 + warp + kWarps * i) * kTile + 16 < len;
                 const uint32_t bytes = (two ? kTile : box_rows) * (WEIGH ? 1 : 2) * (S::kRow + S::NG * 2);
                 const int found = __shfl_sync(0xffffffffu, first_row, (i - base_tile) * plan.boxes), row = max(found, 0);
@@ -537,19 +543,19 @@ __global__ void __launch_bounds__(kThreads, 2)
                     s_row[warp][stage][0] = found;
                     s_row[warp][stage][1] = found < 0 ? -1 : found + 16;
                 }
-                fill<!WEIGH, true>(dst, S::kCodes, dst + 2 * S::kCodes, S::kScales, &k_map, &v_map, row, a.c.ks + (long long)row * S::NG,
+                fill<!WEIGH, true>(dst, S::kCodes, dst + R::kScaleAt, S::kScales, &k_map, &v_map, row, a.c.ks + (long long)row * S::NG,
                              a.c.vs + (long long)row * S::NG, box_rows * S::NG * 2, &full[warp][stage], bytes);
                 if (two) {
                     const int found2 = __shfl_sync(0xffffffffu, first_row, (i - base_tile) * 2 + 1), next = max(found2, 0);
                     if (WEIGH && lane == 0) s_row[warp][stage][1] = found2;
-                    fill<!WEIGH, false>(dst + 16 * S::kRow, S::kCodes, dst + 2 * S::kCodes + 16 * S::NG * 2, S::kScales, &k_map, &v_map, next,
+                    fill<!WEIGH, false>(dst + 16 * S::kRow, S::kCodes, dst + R::kScaleAt + 16 * S::NG * 2, S::kScales, &k_map, &v_map, next,
                                    a.c.ks + (long long)next * S::NG, a.c.vs + (long long)next * S::NG, 16 * S::NG * 2, &full[warp][stage], 0);
                 }
             };
             if (mine > 0) look_up(0);
-            for (int i = 0; i < S::kDepth && i < mine; i++) {
+            for (int i = 0; i < R::kDepth && i < mine; i++) {
                 int st = slot + i;
-                if (st >= S::kDepth) st -= S::kDepth;
+                if (st >= R::kDepth) st -= R::kDepth;
                 ask(i, st);
             }
             Query<S> y;
@@ -558,9 +564,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             Sums<S> z;
             float2 stat[2];
             if constexpr (WEIGH) {
+                // a row that is none has scores of 0 and no weight
 #pragma unroll
-                for (int i = 0; i < 2; i++)
-                    stat[i] = plan.stat[((long long)(b * (long long)n_kv + h) * plan.rg + set) * kRows + 2 * (lane & 3) + i];
+                for (int i = 0; i < 2; i++) {
+                    const int row = 2 * (lane & 3) + i;
+                    stat[i] = make_float2(0.f, 0.f);
+                    if (r0 + row < n_rows) stat[i] = plan.stat[((long long)(b * (long long)n_kv + h) * plan.rg + set) * kRows + row];
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < 2; i++) z.m[i] = kNone, z.l[i] = 0.f;
@@ -579,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     *abort = 1;
                     atomicCAS(a.err, 0, (int)DEV_ERR_TIMEOUT);
                 }
-                const uint8_t *sm = ring + slot * S::kStage;
-                if (++slot == S::kDepth) {
+                const uint8_t *sm = ring + slot * R::kStage;
+                if (++slot == R::kDepth) {
                     slot = 0;
                     par ^= 1;
                 }
@@ -589,37 +599,48 @@ __global__ void __launch_bounds__(kThreads, 2)
             auto limit_of = [&](int row) { return min(len - (a.n_q - 1 - (r0 + row) / G), len); };   // tokens that a row sees
             auto token_of = [&](int i) { return (t0 + warp + kWarps * i) * kTile; };
             if constexpr (WEIGH) {
+                const int limit[2] = {limit_of(2 * (lane & 3)), limit_of(2 * (lane & 3) + 1)};
                 for (int i = 0; i < mine; i++) {
                     const uint8_t *sm = arrived();
                     if (!ok) break;
-                    const int tok = token_of(i), stage = (int)(sm - ring) / (int)S::kStage;
+                    const int tok = token_of(i), stage = (int)(sm - ring) / (int)R::kStage;
                     float s[2][4];
-                    scores<S>(sm, y, off, lane, s);
+                    scores<S>(sm, sm + R::kScaleAt, y, off, lane, s);
+                    if (tok + kTile > len - (a.n_q - 1))
+#pragma unroll
+                        for (int k = 0; k < 2; k++)
+#pragma unroll
+                            for (int j = 0; j < 4; j++)
+                                if (tok + 16 * k + (lane >> 2) + 8 * (j / 2) >= limit[j & 1]) s[k][j] = -INFINITY;
+                    // of token 16 k + 8 e + lane / 4: this thread's two rows, then all eight
+                    float w[2][2];
 #pragma unroll
                     for (int k = 0; k < 2; k++)
 #pragma unroll
                         for (int e = 0; e < 2; e++) {
-                            const int t = tok + 16 * k + (lane >> 2) + 8 * e;
-                            float w = 0.f;
+                            w[k][e] = 0.f;
 #pragma unroll
                             for (int j = 0; j < 2; j++) {
-                                const int row = 2 * (lane & 3) + j;
-                                if (r0 + row < n_rows && t < limit_of(row)) w += ex2(fmaf(s[k][2 * e + j], y.f[j], -stat[j].x)) * stat[j].y;
+                                const float x = s[k][2 * e + j];
+                                const float p = ex2(fmaf(x, y.f[j], -stat[j].x)) * stat[j].y;
+                                w[k][e] += x == -INFINITY ? 0.f : p;   // a row that sees nothing has no reference
                             }
-                            w += __shfl_xor_sync(0xffffffffu, w, 1);
-                            w += __shfl_xor_sync(0xffffffffu, w, 2);
-                            const int at = s_row[warp][stage][k];
-                            if ((lane & 3) == 0 && t < len && at >= 0) atomicAdd(a.c.w + at + (lane >> 2) + 8 * e, w);
+                            w[k][e] += __shfl_xor_sync(0xffffffffu, w[k][e], 1);
+                            w[k][e] += __shfl_xor_sync(0xffffffffu, w[k][e], 2);
                         }
+                    // lane 4 r + c adds token 8 c + r
+                    const int c = lane & 3, t = 8 * c + (lane >> 2), at = s_row[warp][stage][c >> 1];
+                    const float mine_w = c & 2 ? (c & 1 ? w[1][1] : w[1][0]) : (c & 1 ? w[0][1] : w[0][0]);
+                    if (tok + t < len && at >= 0) atomicAdd(a.c.w + at + (t & 15), mine_w);
                     __syncwarp();
-                    if (i + S::kDepth < mine) ask(i + S::kDepth, stage);
+                    if (i + R::kDepth < mine) ask(i + R::kDepth, stage);
                 }
             } else {
                 for (int i = 0; i < mine; i++) {
                     const uint8_t *sm = arrived();
                     if (!ok) break;
                     float s[2][4];
-                    scores<S>(sm, y, off, lane, s);
+                    scores<S>(sm, sm + R::kScaleAt, y, off, lane, s);
                     const bool edge = token_of(i) + kTile > len - (a.n_q - 1);
                     if (edge)
 #pragma unroll
@@ -631,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (edge) outputs<S, true>(plan.magic, sm, y, z, lane, limit_of(lane >> 2) - token_of(i), s);
                     else outputs<S, false>(plan.magic, sm, y, z, lane, kTile, s);
                     __syncwarp();
-                    if (i + S::kDepth < mine) ask(i + S::kDepth, (int)(sm - ring) / (int)S::kStage);
+                    if (i + R::kDepth < mine) ask(i + R::kDepth, (int)(sm - ring) / (int)R::kStage);
                 }
             }
             if constexpr (!WEIGH) {
@@ -674,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int w = 0; w < kWarps; w++) {
-                        const float4 x = *reinterpret_cast<const float4 *>(base + w * S::kDepth * S::kStage + (row * S::D + d) * 4);
+                        const float4 x = *reinterpret_cast<const float4 *>(base + w * R::kDepth * R::kStage + (row * S::D + d) * 4);
                         o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
                     }
                     if (!whole) {
@@ -857,8 +878,9 @@ cudaError_t run(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *
     if (cudaError_t e = code_map(a.c.k, S::kRow, rows, kTile / plan.boxes, &k)) return e;
     if (cudaError_t e = code_map(a.c.v, S::kRow, rows, kTile / plan.boxes, &v)) return e;
     static std::atomic<uint64_t> done{0}, done_weigh{0};
-    if (cudaError_t e = allow_smem(gqa_attend_kernel<S, false>, S::kSmem, d.device, done)) return e;
-    if (cudaError_t e = launch_pdl(gqa_attend_kernel<S, false>, dim3(plan.n_cta), dim3(kThreads), S::kSmem, st, k, v, a, plan, d.wait_ns)) return e;
+    if (cudaError_t e = allow_smem(gqa_attend_kernel<S, false>, Ring<S, false>::kSmem, d.device, done)) return e;
+    if (cudaError_t e = launch_pdl(gqa_attend_kernel<S, false>, dim3(plan.n_cta), dim3(kThreads), Ring<S, false>::kSmem, st, k, v, a, plan, d.wait_ns))
+        return e;
     *n_launch = 2;
     const long long segments = (long long)a.n_seq * a.c.n_kv * plan.rg;
     if (plan.n_cta > 4 * segments) {          // 4 parts a segment or more
@@ -868,8 +890,8 @@ cudaError_t run(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *
     }
     if (!a.weigh) return cudaSuccess;
     *n_launch = 3;
-    if (cudaError_t e = allow_smem(gqa_attend_kernel<S, true>, S::kSmem, d.device, done_weigh)) return e;
-    return launch_pdl(gqa_attend_kernel<S, true>, dim3(plan.n_cta), dim3(kThreads), S::kSmem, st, k, v, a, plan, d.wait_ns);
+    if (cudaError_t e = allow_smem(gqa_attend_kernel<S, true>, Ring<S, true>::kSmem, d.device, done_weigh)) return e;
+    return launch_pdl(gqa_attend_kernel<S, true>, dim3(plan.n_cta), dim3(kThreads), Ring<S, true>::kSmem, st, k, v, a, plan, d.wait_ns);
 }
 
 }  // namespace
