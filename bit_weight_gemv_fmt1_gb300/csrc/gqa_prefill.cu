@@ -76,6 +76,55 @@ __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, i
         : "memory");
 }
 
+// One element of an operand, whose address is a 16-bit type's.
+template <bool F16>
+__device__ __forceinline__ float operand(const void *base, long long e) {
+    const uint16_t b = reinterpret_cast<const uint16_t *>(base)[e];
+    return F16 ? __half2float(__ushort_as_half(b)) : __uint_as_float((uint32_t)b << 16);
+}
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// A query row whose last tile holds keys that it does not see: their weights are 0, but 0 times an infinity or a NaN is NaN.  Called by
+// a row's thread for an output that is not finite, after it has been stored: the columns where such a value is among
+// the keys seen .. end - 1 are computed once more from the keys before, one by one, until they are NaN.  (The keys' other tiles are
+// seen by all of a tile's rows.)  A row of n keys takes some n / 4 us for each 32 columns; nothing comes here unless a value is not finite.
+template <int D, bool F16>
+__device__ __noinline__ void repair(const GqaPrefillArgs &a, long long orow, long long token, int q_head, int head, int krow, int seen, int end,
+                                    float f, float m, float inv, int ev) {
+    const long long q = token * a.q_stride + (long long)q_head * D;
+    auto key = [&](int j) { return (krow + j) * a.k_stride + (long long)head * D; };
+    auto value = [&](int j) { return (krow + j) * a.v_stride + (long long)head * D; };
+    for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t cols = 0;
+        for (int j = seen; j < end; j++)
+            for (int c = 0; c < 32; c++)
+                if (!finite(operand<F16>(a.v, value(j) + c0 + c))) cols |= 1u << c;
+        if (!cols) continue;
+        float sum[32];
+#pragma unroll
+        for (int c = 0; c < 32; c++) sum[c] = 0.f;
+        bool open = true;                    // some column is not NaN yet
+        for (int j = 0; j < seen && open; j++) {
+            float s = 0.f;
+            for (int i = 0; i < D; i++) s = fmaf(operand<F16>(a.q, q + i), operand<F16>(a.k, key(j) + i), s);
+            const float p = ex2(fmaf(a.scale < 0.f ? -s : s, f, -m));
+            open = false;
+#pragma unroll
+            for (int c = 0; c < 32; c++) {
+                sum[c] = fmaf(p, operand<F16>(a.v, value(j) + c0 + c), sum[c]);
+                open |= (cols >> c & 1) && sum[c] == sum[c];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c++)
+            if (cols >> c & 1) {
+                const float x = F16 ? scaled(sum[c] * inv, -ev) : sum[c] * inv;
+                if (a.out_bf16) reinterpret_cast<__nv_bfloat16 *>(a.out)[orow * D + c0 + c] = __float2bfloat16_rn(x);
+                else reinterpret_cast<float *>(a.out)[orow * D + c0 + c] = x;
+            }
+    }
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(384, 1)
     gqa_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -281,6 +330,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 __syncwarp();
             };
+            float odd = 0.f;                             // NaN once an output is not finite
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t o[32];
@@ -293,6 +343,8 @@ __global__ void __launch_bounds__(384, 1)
                 }
 #pragma unroll
                 for (int c = 0; c < 32; c++) o[c] = __float_as_uint(F16 ? scaled(__uint_as_float(o[c]) * inv, -ev) : __uint_as_float(o[c]) * inv);
+#pragma unroll
+                for (int c = 0; c < 32; c++) odd = fmaf(__uint_as_float(o[c]), 0.f, odd);
                 uint32_t w[16];
                 if (a.out_bf16) {
 #pragma unroll
@@ -307,6 +359,9 @@ __global__ void __launch_bounds__(384, 1)
                     }
                 }
             }
+            const int end = min(nt * kRows, nk);
+            if (odd != odd && orow >= 0 && limit > 0 && limit < end)
+                repair<D, F16>(a, orow, u.qrow + row, u.head * a.group + g, u.head, u.krow, limit, end, f, m, inv, ev);
             if (orow >= 0 && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
             tc_before_sync();
         }

@@ -569,8 +569,9 @@ typedef struct {
  *   out     device [Tq][n_heads][dim], COLI_F32 or COLI_BF16; lse device f32 [Tq][n_heads] or NULL.
  *           Rows of no sequence are left alone.
  * Products have bf16 (f32 inputs: f16) operands, to which the probabilities are rounded, and f32
- * sums; maxima and denominators are f32.  A value of another sequence never
- * reaches the result; a non-finite v row that a query's own sequence masks may.
+ * sums; maxima and denominators are f32.  A key or value that a query does not see, of another
+ * sequence or its own, may be anything, NaN included.  A NaN or an infinity in a query, or a NaN in a key that
+ * it sees, makes its row NaN.
  * Pointers 16-byte aligned (cu, lse: 4); strides in elements, multiples of 8.
  * dim 64 or 128; n_heads a multiple of n_kv, n_heads / n_kv <= 128.  Tq, Tk >= 0, n_seq >= 0,
  * 1 <= n_heads <= 1024.  Offsets outside [0, Tq] / [0, Tk] or descending are

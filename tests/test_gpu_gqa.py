@@ -349,6 +349,53 @@ def test_prompt_nan_rows():
     assert torch.equal(got[:90], want[:90]) and torch.equal(got[:, :2], want[:, :2]) and torch.isnan(got[90:, 2:]).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("lens_q,lens_k,H,K,D", [([150, 40], [150, 90], 4, 2, 64), ([70], [300], 14, 2, 128), ([300], [300], 2, 2, 128)])
+def test_prompt_masked_values(lens_q, lens_k, H, K, D, kind):
+    """Values that are not finite reach the rows that see them and no others: infinities keep their sign, and where a row sees
+    infinities of both signs or a NaN it is NaN."""
+    torch, coli = setup()
+    g = gen(torch, H + D)
+    dtype = torch.bfloat16 if kind == "bf16" else torch.float32
+    q, kv = packed_qkv(torch, lens_q, lens_k, H, K, D, g, dtype)
+    cu_q, cu_k = ([0] + [int(x) for x in np.cumsum(v)] for v in (lens_q, lens_k))
+    bad = {}                                              # (key, head, column): value
+    for b in range(len(lens_k)):
+        n = lens_k[b]
+        for back, col, x in ((1, 0, "nan"), (3, 1, "inf"), (3, 5, "-inf"), (9, 5, "inf"), (9, 40, "nan"), (20, 41, "inf"), (33, D - 1, "-inf")):
+            if back <= n:
+                bad[(cu_k[b] + n - back, b % K, col)] = float(x)
+    dirty = kv.clone()
+    for (t, h, col), x in bad.items():
+        dirty[t, K + h, col] = x
+
+    def run(kv):
+        out = torch.empty(cu_q[-1], H, D, device="cuda", dtype=torch.float32)
+        d = kv.cuda()
+        coli.gqa_prefill(q.cuda(), d[:, :K], d[:, K:2 * K], torch.tensor(cu_q, dtype=torch.int32, device="cuda"),
+                         torch.tensor(cu_k, dtype=torch.int32, device="cuda"), 0.09, out)
+        coli.sync_check()
+        return out.cpu().double()
+
+    got = run(dirty)
+    # what a row sees: finite values as they are, then the others added
+    clean = kv.clone()
+    for (t, h, col), x in bad.items():
+        clean[t, K + h, col] = 0.0
+    ref, tol, _ = reference_prompt(torch, q, clean[:, :K], clean[:, K:2 * K], cu_q, cu_k, 0.09, "f32")
+    for b in range(len(lens_q)):
+        for i in range(lens_q[b]):
+            seen = cu_k[b] + i + lens_k[b] - lens_q[b]
+            for (t, h, col), x in bad.items():
+                if cu_k[b] <= t <= seen:
+                    ref[cu_q[b] + i, h * H // K:(h + 1) * H // K, col] += x
+    fine = torch.isfinite(ref)
+    assert torch.equal(torch.isfinite(got), fine)
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    assert torch.equal(got[~fine & ~torch.isnan(ref)], ref[~fine & ~torch.isnan(ref)])
+    assert ((got - ref).abs()[fine] <= tol[fine]).all()
+
+
 def test_prompt_bad_offsets():
     torch, coli = setup()
     q, k = torch.zeros(10, 2, 64, device="cuda", dtype=torch.bfloat16), torch.zeros(10, 1, 64, device="cuda", dtype=torch.bfloat16)
