@@ -11,8 +11,10 @@
 //   S^T = K q^T   codes AND-ed out of the words are f16 subnormals n 2^-24 (odd nibbles
 //                 16 times that, q a 16th there); accumulators begin at -8 sum q, one
 //                 chain per scale group, whose f32 result takes the scale
-//   O^T += V^T P^T  codes OR-ed into bf16 as 128 + n; p rounded to bf16, transposed in registers, its product with the
-//                 row's scale rounded to bf16; -136 sum P comes from one more product
+//   O^T += V^T P^T  codes AND-ed out are bf16 subnormals n 2^-133 (odd nibbles 16 times that, taken back at the end); p times
+//                 2^80 rounded to bf16, transposed in registers, its product with the row's scale rounded to bf16; -8 sum P comes from
+//                 one more product.  2^80 keeps products and sums within f32 for scales from 2^-60 to 2^38.  (Codes as
+//                 128 + n need an OR and two more shifts a word: 48x12000 87.3 us, this way 84.4.)
 // so no code is converted one by one.  ldmatrix, transposing for the values, deals the words out as the products want them:
 // its 16-bit elements are 4 codes of one token.  N = 8 is what few query rows need; 5th-generation products would want the codes
 // as bytes in shared memory, M = 128 tokens, and N = 8 as well.
@@ -37,6 +39,8 @@ namespace {
 constexpr int kTile = 32, kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kJoin = 256, kGroup = 64;  // threads of the join, parts at a time
 constexpr float kGrow = 8.f;             // log2 of the weight that moves the reference
+constexpr float kUp = 80.f, kScale = 0x1p80f;   // log2 of what p is held times, and that: references are lower by it
+constexpr float kDown = 0x1p53f;         // codes' 2^133 without it: outputs without factors
 constexpr float kNone = -3e38f;          // reference of a row that has seen no key
 constexpr int kRows = 8;                 // query rows of a unit: N of the products
 
@@ -60,7 +64,6 @@ struct AttendPlan {
     int n_cta, rg, boxes;                // CTAs, sets of query rows per head, copies per tile (pages of 16, 48, ... tokens: 2)
     float *part;                         // [n_cta][2][kRows][D + 2]: O, m, l
     float2 *stat;                        // [n_seq][n_kv][rg][kRows]: m and 1 / l, for the weights
-    uint32_t magic;                      // 128 in bf16, twice
     long long *before;                   // [n_seq + 2]: tiles (or pieces) of the sequences before each and of all, tiles of a piece
 };
 
@@ -377,7 +380,7 @@ struct Sums {
 // Adds the outputs of the tile at `sm`, whose scores (before the factor f) are s and which the references have been moved for.
 // EDGE: some row does not see all of the tile's tokens; `seen` is how many of them row lane / 4 sees.
 template <class S, bool EDGE>
-__device__ __forceinline__ void outputs(uint32_t magic, const uint8_t *sm, const Query<S> &y, Sums<S> &z, int lane, int seen, const float (&s)[2][4]) {
+__device__ __forceinline__ void outputs(const uint8_t *sm, const Query<S> &y, Sums<S> &z, int lane, int seen, const float (&s)[2][4]) {
     const int c = lane & 3, x = swizzle<S>(lane);
     const uint8_t *scales = sm + 2 * S::kCodes + S::kScales;
     uint32_t b[2][S::NG][2];                             // P^T times the scales: row lane / 4, tokens 16 k + 8 e + 2 c + {0, 1}
@@ -406,7 +409,7 @@ __device__ __forceinline__ void outputs(uint32_t magic, const uint8_t *sm, const
 #pragma unroll
     for (int g = 0; g < S::NG; g++) {
 #pragma unroll
-        for (int k = 0; k < 2; k++) mma_bf16(z.corr[g], 0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u, b[k][g][0], b[k][g][1]);
+        for (int k = 0; k < 2; k++) mma_bf16(z.corr[g], 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, b[k][g][0], b[k][g][1]);
 #pragma unroll
         for (int p = g * S::kPer; p < (g + 1) * S::kPer; p++) {
             uint32_t w[4];                               // 4 codes of tokens 2 c, 2 c + 1 (low and high half), 8, 16 and 24 more
@@ -414,12 +417,9 @@ __device__ __forceinline__ void outputs(uint32_t magic, const uint8_t *sm, const
 #pragma unroll
             for (int k = 0; k < 2; k++) {
                 const uint32_t u = w[2 * k], v = w[2 * k + 1];
-                uint32_t n[2][4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    n[0][i] = ((u >> (4 * i)) & 0x000F000Fu) | magic;
-                    n[1][i] = ((v >> (4 * i)) & 0x000F000Fu) | magic;
-                }
+                const uint32_t u8 = u >> 8, v8 = v >> 8;
+                const uint32_t n[2][4] = {{u & 0x000F000Fu, u & 0x00F000F0u, u8 & 0x000F000Fu, u8 & 0x00F000F0u},
+                                          {v & 0x000F000Fu, v & 0x00F000F0u, v8 & 0x000F000Fu, v8 & 0x00F000F0u}};
 #pragma unroll
                 for (int e = 0; e < 2; e++) mma_bf16(z.o[p][e], n[0][2 * e], n[0][2 * e + 1], n[1][2 * e], n[1][2 * e + 1], b[k][g][0], b[k][g][1]);
             }
@@ -452,7 +452,7 @@ __device__ __forceinline__ void move_references(const Query<S> &y, Sums<S> &z, c
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         now[i] = fmaxf(fmaxf(s[0][i], s[0][2 + i]), fmaxf(s[1][i], s[1][2 + i]));
-        move |= fmaf(now[i], y.f[i], -z.m[i]) > kGrow;
+        move |= fmaf(now[i], y.f[i], -z.m[i]) > kUp + kGrow;
     }
     if (!__any_sync(0xffffffffu, move)) return;
 #pragma unroll
@@ -461,7 +461,8 @@ __device__ __forceinline__ void move_references(const Query<S> &y, Sums<S> &z, c
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16)) * y.f[i];
-        if (!(m - z.m[i] > kGrow)) continue;
+        if (!(m - z.m[i] > kUp + kGrow)) continue;
+        m -= kUp;
         const float f = ex2(z.m[i] - m);
         z.m[i] = m;
         z.l[i] *= f;
@@ -649,8 +650,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                             for (int j = 0; j < 4; j++)
                                 if (token_of(i) + 16 * k + (lane >> 2) + 8 * (j / 2) >= limit_of(2 * (lane & 3) + j % 2)) s[k][j] = -INFINITY;
                     move_references<S>(y, z, s);
-                    if (edge) outputs<S, true>(plan.magic, sm, y, z, lane, limit_of(lane >> 2) - token_of(i), s);
-                    else outputs<S, false>(plan.magic, sm, y, z, lane, kTile, s);
+                    if (edge) outputs<S, true>(sm, y, z, lane, limit_of(lane >> 2) - token_of(i), s);
+                    else outputs<S, false>(sm, y, z, lane, kTile, s);
                     __syncwarp();
                     if (i + R::kDepth < mine) ask(i + R::kDepth, (int)(sm - ring) / (int)R::kStage);
                 }
@@ -678,8 +679,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     for (int p = 0; p < S::kParts; p++) {
                         const float *cr = z.corr[p / S::kPer];
                         *reinterpret_cast<float4 *>(mine_o + row * S::D + 32 * p + 4 * (lane >> 2)) =
-                            make_float4((z.o[p][0][i] + cr[i]) * f, (z.o[p][0][2 + i] + cr[2 + i]) * f, (z.o[p][1][i] + cr[i]) * f,
-                                        (z.o[p][1][2 + i] + cr[2 + i]) * f);
+                            make_float4((z.o[p][0][i] + cr[i]) * kDown * f, fmaf(z.o[p][0][2 + i], 0.0625f, cr[2 + i]) * kDown * f, (z.o[p][1][i] + cr[i]) * kDown * f,
+                                        fmaf(z.o[p][1][2 + i], 0.0625f, cr[2 + i]) * kDown * f);
                     }
                 }
                 __syncthreads();
@@ -705,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     const int at = r0 + row;
                     if (at >= n_rows) continue;
-                    const float inv = l != 0.f ? 1.f / l : 0.f;
+                    const float inv1 = l != 0.f ? 1.f / l : 0.f, inv = inv1 * kScale;
                     const long long orow = (long long)(b * (long long)a.n_q + at / G) * a.H + h * G + at % G;
                     if (a.out_bf16)
                         *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * S::D + d) =
@@ -715,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
                     if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
                     if (d == 0 && a.weigh)
-                        plan.stat[((long long)(b * (long long)n_kv + h) * plan.rg + set) * kRows + row] = make_float2(m, inv);
+                        plan.stat[((long long)(b * (long long)n_kv + h) * plan.rg + set) * kRows + row] = make_float2(m, inv1);
                 }
                 fence_async_smem();
                 __syncthreads();
@@ -825,7 +826,7 @@ __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, 
             const float4 x = sum[k][row][d / 4];
             o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
         }
-        const float inv = l != 0.f ? 1.f / l : 0.f;
+        const float inv1 = l != 0.f ? 1.f / l : 0.f, inv = inv1 * kScale;
         const long long orow = (long long)(b * (long long)a.n_q + at / G) * a.H + h * G + at % G;
         if (a.out_bf16)
             *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * S::D + d) =
@@ -833,7 +834,7 @@ __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, 
         else
             *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + orow * S::D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
         if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-        if (d == 0 && a.weigh) plan.stat[(long long)place * kRows + row0 + row] = make_float2(m, inv);
+        if (d == 0 && a.weigh) plan.stat[(long long)place * kRows + row0 + row] = make_float2(m, inv1);
     }
 }
 
@@ -870,7 +871,6 @@ cudaError_t run(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *
     plan.boxes = a.c.page % kTile ? 2 : 1;
     plan.n_cta = grid_of(a, d.n_sm);
     plan.part = (float *)d.scratch;
-    plan.magic = 0x43004300u;
     plan.before = (long long *)((char *)d.scratch + part_bytes(a, plan.n_cta));
     plan.stat = (float2 *)((char *)plan.before + round256((size_t)(a.n_seq + 2) * sizeof(long long)));
     CUtensorMap k, v;

@@ -631,7 +631,8 @@ int coli_gqa_read(const coli_gqa_cache *cache, const int32_t *pages, int64_t pag
  * The key product takes codes as they are and q in f16, scaled by a power of two
  * per query row: a bf16 element is exact down to 2^-32 of the row's largest
  * magnitude, an f32 one is rounded to 11 bits.  For the value product each
- * probability, and its product with its row's scale, is rounded to bf16.  Scales are applied and
+ * probability, and its product with its row's scale, is rounded to bf16; scales of values from 2^-60 to
+ * 2^38 stay within the products' range (values of 1e-17 to 1e12).  Scales are applied and
  * sums, maxima and the denominator held in f32.
  * Rows past a sequence's length, and pages past its last, are never used: they may
  * hold anything.  A NaN or an infinity in a query, or a NaN scale of a key that a query

@@ -506,6 +506,19 @@ def test_step_magnitudes(magnitude):
     assert ((out.cpu().double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("size", [2.0 ** -55, 2.0 ** 36])
+def test_step_value_sizes(size):
+    """Values' scales at both ends of their range: the powers of two of the products take nothing away."""
+    torch, coli = setup()
+    g = gen(torch, 4)
+    s, table, _ = filled(torch, coli, [300, 40], 2, 16, 128, 32, g, spread=1.0)
+    q = torch.randn(2, 1, 8, 128, generator=g).to(torch.bfloat16)
+    want, lse = run_step(torch, coli, s, table, [300, 40], q, 0.1, "f32")
+    s.vs.mul_(size)
+    got, lse2 = run_step(torch, coli, s, table, [300, 40], q, 0.1, "f32")
+    assert torch.equal(got, want * size) and torch.equal(lse, lse2)      # every step of the sum is that power of two larger
+
+
 def test_step_strangers_do_not_matter():
     """Rows past a length (any scale, infinities too), pages past the last one and other heads' rows change no bit."""
     torch, coli = setup()
