@@ -370,13 +370,24 @@ def _tokens(t, dev: int, name: str) -> int:
     if t.get_device() != dev:
         _elsewhere(t, dev, name)
     shape, stride, n = t.shape, t.stride(), 1
-    if len(shape) == 3 and stride[2] == 1 and stride[1] == shape[2]:     # the usual case, without the loop
-        return stride[0] if shape[0] > 1 else shape[1] * shape[2]
     for i in range(len(shape) - 1, 0, -1):
         if stride[i] != n and shape[i] != 1:
             _refuse(f"a token of {name} must be packed")
         n *= shape[i]
     return stride[0] if shape[0] > 1 else n
+
+
+def _heads(t, shape, kind, dev: int, name: str) -> int:
+    """Token stride of t, of this shape [T, heads, dim] and type, whose tokens are packed."""
+    if t.shape != shape or t.dtype is not kind:
+        _refuse(f"{name} must be a {kind} tensor of shape {tuple(shape)}")
+    if t.get_device() != dev:
+        _elsewhere(t, dev, name)
+    T, H, D = shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or s1 != D:
+        return _tokens(t, dev, name)         # single heads or tokens, whose strides mean nothing, or a refusal
+    return s0 if T > 1 else H * D
 
 
 def _pages(pages, n_seq: int, dev: int, name: str = "pages") -> int:
@@ -541,13 +552,14 @@ def gqa_prefill(q, k, v, cu_q, cu_k, scale: float, out, lse=None, stream=None):
     out [Tq, heads, dim]; cu_q, cu_k int32 [n_seq + 1]; lse f32 [Tq, heads]."""
     torch = _torch or _load_torch()
     dev = _device()
-    Tq, H, D = q.shape
-    Tk, K, D2 = k.shape
-    if D2 != D or v.shape != k.shape or out.shape != q.shape or cu_q.shape != cu_k.shape or k.dtype is not q.dtype or \
-            v.dtype is not q.dtype or (lse is not None and lse.shape != (Tq, H)):
+    kind, shape, kv_shape = q.dtype, q.shape, k.shape
+    Tq, H, D = shape
+    Tk, K, D2 = kv_shape
+    n = cu_q.shape
+    if D2 != D or out.shape != shape or cu_k.shape != n or (lse is not None and lse.shape != (Tq, H)):
         _refuse("gqa_prefill: q, k, v, cu_q, cu_k, out and lse must match one another")
-    rc = _lib.coli_gqa_prefill(_dtype(q), q.data_ptr(), _tokens(q, dev, "q"), k.data_ptr(), _tokens(k, dev, "k"), v.data_ptr(),
-                               _tokens(v, dev, "v"), Tq, Tk, cu_q.shape[0] - 1, _packed(cu_q, torch.int32, dev, "cu_q"),
+    rc = _lib.coli_gqa_prefill(_dtype(q), q.data_ptr(), _heads(q, shape, kind, dev, "q"), k.data_ptr(), _heads(k, kv_shape, kind, dev, "k"),
+                               v.data_ptr(), _heads(v, kv_shape, kind, dev, "v"), Tq, Tk, n[0] - 1, _packed(cu_q, torch.int32, dev, "cu_q"),
                                _packed(cu_k, torch.int32, dev, "cu_k"), H, K, D, scale, _dtype(out), _packed(out, out.dtype, dev, "out"),
                                None if lse is None else _packed(lse, torch.float32, dev, "lse"),
                                _raw_stream(dev) if stream is None else _stream(stream))
@@ -562,11 +574,11 @@ def gqa_append(cache: GqaCache, k, v, slots, stream=None):
     dev = _device()
     if cache.device != dev:
         _elsewhere(cache.k, dev, "the cache")
-    T = k.shape[0]
-    if k.shape != (T, cache.n_kv, cache.dim) or v.shape != k.shape or v.dtype is not k.dtype or slots.shape != (T,):
-        _refuse("gqa_append: k and v must be [T, kv heads, dim] of one type and match slots [T] and the cache")
-    rc = _lib.coli_gqa_append(cache._p, _dtype(k), k.data_ptr(), _tokens(k, dev, "k"), v.data_ptr(), _tokens(v, dev, "v"), T,
-                              _packed(slots, torch.int64, dev, "slots"), _raw_stream(dev) if stream is None else _stream(stream))
+    kind, (T,) = k.dtype, slots.shape
+    shape = (T, cache.n_kv, cache.dim)
+    rc = _lib.coli_gqa_append(cache._p, _dtype(k), k.data_ptr(), _heads(k, shape, kind, dev, "k"), v.data_ptr(),
+                              _heads(v, shape, kind, dev, "v"), T, _packed(slots, torch.int64, dev, "slots"),
+                              _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc)
 
@@ -577,12 +589,10 @@ def gqa_read(cache: GqaCache, pages, cu, k, v, stream=None):
     dev = _device()
     if cache.device != dev:
         _elsewhere(cache.k, dev, "the cache")
-    n_seq = cu.shape[0] - 1
-    T = k.shape[0]
-    if k.shape != (T, cache.n_kv, cache.dim) or v.shape != k.shape or v.dtype is not k.dtype:
-        _refuse("gqa_read: k and v must be [T, kv heads, dim] of one type and match the cache")
+    n_seq, kind, T = cu.shape[0] - 1, k.dtype, k.shape[0]
+    shape = (T, cache.n_kv, cache.dim)
     rc = _lib.coli_gqa_read(cache._p, pages.data_ptr(), _pages(pages, n_seq, dev), n_seq, _packed(cu, torch.int32, dev, "cu"), T,
-                            _dtype(k), k.data_ptr(), _tokens(k, dev, "k"), v.data_ptr(), _tokens(v, dev, "v"),
+                            _dtype(k), k.data_ptr(), _heads(k, shape, kind, dev, "k"), v.data_ptr(), _heads(v, shape, kind, dev, "v"),
                             _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(rc)
@@ -596,8 +606,9 @@ def gqa_attend(cache: GqaCache, q, pages, lens, scale: float, out, lse=None, wei
     dev = _device()
     if cache.device != dev:
         _elsewhere(cache.k, dev, "the cache")
-    B, n_q, H, D = q.shape
-    if D != cache.dim or out.shape != q.shape or lens.shape != (B,) or (lse is not None and lse.shape != (B, n_q, H)):
+    shape = q.shape
+    B, n_q, H, D = shape
+    if D != cache.dim or out.shape != shape or lens.shape != (B,) or (lse is not None and lse.shape != (B, n_q, H)):
         _refuse("gqa_attend: q, lens, out and lse must match one another and the cache")
     rc = _lib.coli_gqa_attend(cache._p, _dtype(q), _packed(q, q.dtype, dev, "q"), B, n_q, H, pages.data_ptr(), _pages(pages, B, dev),
                               _packed(lens, torch.int32, dev, "lens"), scale, weigh, _dtype(out), _packed(out, out.dtype, dev, "out"),
