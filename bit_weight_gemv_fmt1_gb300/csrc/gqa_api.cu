@@ -72,6 +72,7 @@ int read(const coli_gqa_cache *cache, const int32_t *pages, int64_t pages_stride
     if (int rc = check_cache(cache, &a.c)) return rc;
     if (int rc = float_type(dtype, "dtype")) return rc;
     if (T < 0 || n_seq < 0) return bad(COLI_EINVAL, "T and n_seq must be >= 0 (got %d, %d)", T, n_seq);
+    if ((int64_t)T * a.c.n_kv > kIntMax / 2) return bad(COLI_EINVAL, "T * n_kv is too large (got %d, %d)", T, a.c.n_kv);
     if (pages_stride < 1 || pages_stride > kIntMax)
         return bad(COLI_EINVAL, "pages_stride must be in 1..2^31-1 (got %lld)", (long long)pages_stride);
     if (int rc = check_stride(k_stride, T, a.c.n_kv, a.c.dim, "k_stride")) return rc;
@@ -201,8 +202,8 @@ int prefill(int dtype, const void *q, int64_t q_stride, const void *k, int64_t k
         return bad(COLI_EINVAL, "need 1 <= n_heads <= 1024, a multiple of n_kv and at most 128 times it (got %d, %d)", heads, n_kv);
     if (Tq < 0 || Tk < 0 || n_seq < 0) return bad(COLI_EINVAL, "need Tq, Tk, n_seq >= 0 (got %d, %d, %d)", Tq, Tk, n_seq);
     const int group = heads / n_kv, tokens = 128 / group;
-    if ((int64_t)Tq * heads > kIntMax || ((int64_t)Tq / (2 * tokens) + 1 + n_seq) * n_kv > kIntMax)
-        return bad(COLI_EINVAL, "Tq * n_heads or n_seq * n_kv is too large");
+    if ((int64_t)Tq * heads > kIntMax || (int64_t)Tk * n_kv > kIntMax || ((int64_t)Tq / (2 * tokens) + 1 + n_seq) * n_kv > kIntMax)
+        return bad(COLI_EINVAL, "Tq * n_heads, Tk * n_kv or n_seq * n_kv is too large");
     if (int rc = check_stride(q_stride, Tq, heads, dim, "q_stride")) return rc;
     if (int rc = check_stride(k_stride, Tk, n_kv, dim, "k_stride")) return rc;
     if (int rc = check_stride(v_stride, Tk, n_kv, dim, "v_stride")) return rc;

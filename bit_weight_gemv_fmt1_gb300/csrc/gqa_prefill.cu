@@ -18,9 +18,17 @@
 // maximum passes it by 8: weights up to 2^8 lose nothing in bf16.  m, l and O are
 // f32; rounding P to bf16 is within 2^-8 of each weight, as the values' own.
 //
+// Bound: the chain of a tile.  A round (128 keys for both tiles) is 32 MMAs of 64 cycles, 2048; measured 2860: either tile's softmax
+// takes about 1250 (scores out of TMEM 200, maxima 180, 128 exponentials at 4 cycles and what goes with them 600, P and the
+// hand-overs 250), longer than the 1024 of the other tile's products.  P is handed over in halves of 64 keys and the arithmetic on
+// pairs is packed (1x8192, 32 heads on 8: 376 us, 370 with halves, 366 packed, 355 once the next unit is asked for late); half a row per
+// thread, two warps a tile and SM quarter, is slower (384).  1.54 PFLOP/s, 0.80 of the measured bf16 rate; 1x2048 33 us, 6 ragged up
+// to 700 behind 333 cached 45.5, 24 of up to 301 (D 64) 17.
+//
 // f32 inputs become f16, which keeps 3 bits more than bf16: every row of q times a power of two of its own, k and v times one each,
 // so that the largest magnitudes lie in 2^14 .. 2^15 and all down to 2^-28 of them keep their 11 bits.  P is f16 then too.  The
-// powers come out again in the scores' factor, a thread's own, and with 1 / l.  (bf16 without the powers: twice the error.)
+// powers come out again in the scores' factor, a thread's own, and with 1 / l.  (bf16 without the powers: twice the error.)  The
+// two launches that make them take 9 us of the 29 of 24 short prompts.
 //
 // Keys past a causal row's limit are masked by selection; value rows past the
 // sequence's end belong to its neighbours and are zeroed in shared memory.
@@ -76,51 +84,94 @@ __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// One element of an operand, whose address is a 16-bit type's.
+// Two neighbouring elements of an operand.
 template <bool F16>
-__device__ __forceinline__ float operand(const void *base, long long e) {
-    const uint16_t b = reinterpret_cast<const uint16_t *>(base)[e];
-    return F16 ? __half2float(__ushort_as_half(b)) : __uint_as_float((uint32_t)b << 16);
+__device__ __forceinline__ float2 operands(uint32_t w) {
+    return F16 ? __half22float2(*reinterpret_cast<const __half2 *>(&w)) : bf16x2_f32x2(w);
 }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
-// A query row whose last tile holds keys that it does not see: their weights are 0, but 0 times an infinity or a NaN is NaN.  Called by
-// a row's thread for an output that is not finite, after it has been stored: the columns where such a value is among
-// the keys seen .. end - 1 are computed once more from the keys before, one by one, until they are NaN.  (The keys' other tiles are
-// seen by all of a tile's rows.)  A row of n keys takes some n / 4 us for each 32 columns; nothing comes here unless a value is not finite.
+// Query rows whose last tile holds keys that they do not see: those keys' weights are 0, but 0 times an infinity or a NaN is NaN.  A
+// whole warp calls this after its rows have been stored, for the rows (`mine`) with an output that is not finite: the columns where such a
+// value is among the keys seen .. end - 1 are computed once more from the keys before, 32 at a time, until they are NaN.  (The
+// other tiles are seen by all of a tile's rows.)  Nothing comes here unless a value or a result is not finite; a warp of 32 such rows of
+// 8192 keys then takes 53 ms, which its unit's limit of waits (2.5 s) leaves room for.
 template <int D, bool F16>
-__device__ __noinline__ void repair(const GqaPrefillArgs &a, long long orow, long long token, int q_head, int head, int krow, int seen, int end,
+__device__ __noinline__ void repair(const GqaPrefillArgs &a, bool mine, int orow, int token, int q_head, int head, int krow, int seen, int end,
                                     float f, float m, float inv, int ev) {
-    const long long q = token * a.q_stride + (long long)q_head * D;
-    auto key = [&](int j) { return (krow + j) * a.k_stride + (long long)head * D; };
-    auto value = [&](int j) { return (krow + j) * a.v_stride + (long long)head * D; };
-    for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t cols = 0;
-        for (int j = seen; j < end; j++)
-            for (int c = 0; c < 32; c++)
-                if (!finite(operand<F16>(a.v, value(j) + c0 + c))) cols |= 1u << c;
-        if (!cols) continue;
-        float sum[32];
+    constexpr int kCols = D / 32;            // columns of a lane
+    const int lane = threadIdx.x & 31;
+    const uint16_t *k = reinterpret_cast<const uint16_t *>(a.k) + krow * a.k_stride + head * D;
+    const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v) + krow * a.v_stride + head * D + lane * kCols;
+    auto value = [&](int j, float (&x)[kCols]) {
 #pragma unroll
-        for (int c = 0; c < 32; c++) sum[c] = 0.f;
-        bool open = true;                    // some column is not NaN yet
-        for (int j = 0; j < seen && open; j++) {
-            float s = 0.f;
-            for (int i = 0; i < D; i++) s = fmaf(operand<F16>(a.q, q + i), operand<F16>(a.k, key(j) + i), s);
-            const float p = ex2(fmaf(a.scale < 0.f ? -s : s, f, -m));
-            open = false;
+        for (int c = 0; c < kCols; c += 2) {
+            const float2 two = operands<F16>(*reinterpret_cast<const uint32_t *>(v + j * a.v_stride + c));
+            x[c] = two.x, x[c + 1] = two.y;
+        }
+    };
+    for (uint32_t left = __ballot_sync(0xffffffffu, mine); left; left &= left - 1) {
+        const int src = __ffs(left) - 1;
+        const int n = __shfl_sync(0xffffffffu, seen, src), stop = __shfl_sync(0xffffffffu, end, src), to = __shfl_sync(0xffffffffu, orow, src);
+        const float f1 = __shfl_sync(0xffffffffu, f, src), m1 = __shfl_sync(0xffffffffu, m, src), inv1 = __shfl_sync(0xffffffffu, inv, src);
+        const uint16_t *q = reinterpret_cast<const uint16_t *>(a.q) + __shfl_sync(0xffffffffu, token, src) * a.q_stride +
+                            __shfl_sync(0xffffffffu, q_head, src) * D;
+        bool bad[kCols], some = false;
+        float x[kCols], sum[kCols];
 #pragma unroll
-            for (int c = 0; c < 32; c++) {
-                sum[c] = fmaf(p, operand<F16>(a.v, value(j) + c0 + c), sum[c]);
-                open |= (cols >> c & 1) && sum[c] == sum[c];
-            }
+        for (int c = 0; c < kCols; c++) bad[c] = false, sum[c] = 0.f;
+        for (int j = n; j < stop; j++) {
+            value(j, x);
+#pragma unroll
+            for (int c = 0; c < kCols; c++) bad[c] = bad[c] || !finite(x[c]);
         }
 #pragma unroll
-        for (int c = 0; c < 32; c++)
-            if (cols >> c & 1) {
-                const float x = F16 ? scaled(sum[c] * inv, -ev) : sum[c] * inv;
-                if (a.out_bf16) reinterpret_cast<__nv_bfloat16 *>(a.out)[orow * D + c0 + c] = __float2bfloat16_rn(x);
-                else reinterpret_cast<float *>(a.out)[orow * D + c0 + c] = x;
+        for (int c = 0; c < kCols; c++) some = some || bad[c];
+        if (!__any_sync(0xffffffffu, some)) continue;
+        for (int j0 = 0; j0 < n; j0 += 32) {
+            float p = 0.f;
+            if (j0 + lane < n) {
+                const uint16_t *kj = k + (j0 + lane) * a.k_stride;
+                float s = 0.f;
+#pragma unroll 4
+                for (int i = 0; i < D; i += 8) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(q + i), w = *reinterpret_cast<const uint4 *>(kj + i);
+                    const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const float2 y = operands<F16>(us[e]), z = operands<F16>(ws[e]);
+                        s = fmaf(y.y, z.y, fmaf(y.x, z.x, s));
+                    }
+                }
+                p = ex2(fmaf(a.scale < 0.f ? -s : s, f1, -m1));
+            }
+            bool open = false;               // some column is not NaN yet
+            for (int j = 0; j < 32; j += 8) {
+                float ahead[8][kCols];
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c++) ahead[e][c] = 0.f;   // past the row's keys: p is 0, too
+                    if (j0 + j + e < n) value(j0 + j + e, ahead[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const float pj = __shfl_sync(0xffffffffu, p, j + e);
+#pragma unroll
+                    for (int c = 0; c < kCols; c++) sum[c] = fmaf(pj, ahead[e][c], sum[c]);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < kCols; c++) open = open || (bad[c] && sum[c] == sum[c]);
+            if (!__any_sync(0xffffffffu, open)) break;
+        }
+#pragma unroll
+        for (int c = 0; c < kCols; c++)
+            if (bad[c]) {
+                const float y = F16 ? scaled(sum[c] * inv1, -ev) : sum[c] * inv1;
+                const long long at = (long long)to * D + lane * kCols + c;
+                if (a.out_bf16) reinterpret_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(y);
+                else reinterpret_cast<float *>(a.out)[at] = y;
             }
     }
 }
@@ -360,8 +411,9 @@ __global__ void __launch_bounds__(384, 1)
                 }
             }
             const int end = min(nt * kRows, nk);
-            if (odd != odd && orow >= 0 && limit > 0 && limit < end)
-                repair<D, F16>(a, orow, u.qrow + row, u.head * a.group + g, u.head, u.krow, limit, end, f, m, inv, ev);
+            const bool again = odd != odd && orow >= 0 && limit > 0 && limit < end;
+            if (__any_sync(0xffffffffu, again))
+                repair<D, F16>(a, again, (int)orow, u.qrow + row, u.head * a.group + g, u.head, u.krow, limit, end, f, m, inv, ev);
             if (orow >= 0 && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
             tc_before_sync();
         }

@@ -77,7 +77,7 @@ def test_append(lib, kw, code):  # noqa: F811
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dt=E4M3), EFMT), (dict(T=-1), EINVAL), (dict(n=-1), EINVAL), (dict(ps=0), EINVAL), (dict(ps=1 << 31), EINVAL), (dict(ks=504), EINVAL),
-    (dict(vs=516), EINVAL), (dict(pages=None), EINVAL), (dict(cu=A + 2), EINVAL), (dict(k=A + 8), EINVAL), (dict(v=None), EINVAL)])
+    (dict(vs=516), EINVAL), (dict(T=1 << 29), EINVAL), (dict(pages=None), EINVAL), (dict(cu=A + 2), EINVAL), (dict(k=A + 8), EINVAL), (dict(v=None), EINVAL)])
 def test_read(lib, kw, code):  # noqa: F811
     assert read(lib, **kw) == code
 
@@ -113,7 +113,7 @@ def test_evict(lib, kw):  # noqa: F811
     (dict(H=1028), EINVAL), (dict(H=258, K=2, qs=258 * 128), EINVAL), (dict(Tq=-1), EINVAL), (dict(Tk=-1), EINVAL), (dict(n=-1), EINVAL),
     (dict(qs=2040), EINVAL), (dict(ks=516), EINVAL), (dict(vs=504), EINVAL), (dict(scale=float("nan")), EINVAL), (dict(q=None), EINVAL),
     (dict(k=A + 8), EINVAL), (dict(v=None), EINVAL), (dict(cuq=None), EINVAL), (dict(cuk=A + 1), EINVAL), (dict(out=None), EINVAL),
-    (dict(lse=A + 2), EINVAL), (dict(Tq=1 << 28), EINVAL)])
+    (dict(lse=A + 2), EINVAL), (dict(Tq=1 << 28), EINVAL), (dict(Tk=1 << 29), EINVAL)])
 def test_prefill(lib, kw, code):  # noqa: F811
     assert prefill(lib, **kw) == code
 
