@@ -61,7 +61,9 @@ template <class S, bool WEIGH>
 struct Ring {
     static constexpr uint32_t kScaleAt = (WEIGH ? 1 : 2) * S::kCodes;
     static constexpr uint32_t kStage = (kScaleAt + (WEIGH ? 1 : 2) * S::kScales + 511) / 512 * 512;
-    static constexpr int kDepth = std::min(8u, 110u * 1024u / (kWarps * kStage));   // two CTAs on an SM
+    // Two CTAs on an SM, 74 KB each for 128 dims: what the rings hold when the last copies have come is worked on with HBM idle (3 tiles a
+    // warp: 48x12000 84.2 us, 2: 82.4).
+    static constexpr int kDepth = WEIGH ? 4 : 2;
     static constexpr uint32_t kSmem = kWarps * kDepth * kStage + 1024;
     static_assert(WEIGH || kDepth * kStage >= kRows * S::D * 4, "a warp's output fits its ring");
 };
@@ -500,7 +502,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (tid == 0) s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_wait();
-    pdl_trigger();
     __syncthreads();
     volatile int *abort = &s_abort;
     const int n_kv = a.c.n_kv, G = a.H / n_kv, n_rows = a.n_q * G;
@@ -737,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (!ok) break;
     }
+    pdl_trigger();                       // not before: the next kernel's CTAs would take room that these want (4x9000: 21 us, this way 19)
     if (*abort) settle();
 }
 

@@ -90,7 +90,6 @@ __global__ void __launch_bounds__(kThreads) gqa_append_kernel(const GqaAppendArg
     const int h = blockIdx.y, u = threadIdx.x % kUnits, step = gridDim.x * kTokens;
     int t = blockIdx.x * kTokens + threadIdx.x / kUnits;
     pdl_wait();
-    pdl_trigger();
     Raw<BF16> k, v;
     long long slot = -1;
     auto load = [&](int t) {
@@ -123,6 +122,7 @@ __global__ void __launch_bounds__(kThreads) gqa_append_kernel(const GqaAppendArg
         }
         if (u == 0 && a.c.w) a.c.w[r] = 0.f;
     }
+    pdl_trigger();
 }
 
 // The values of a word of codes.  bf16: 128 + code by an OR, minus 136 exactly, times the scale to nearest: the same as the f32
@@ -158,7 +158,6 @@ __global__ void __launch_bounds__(kThreads) gqa_read_kernel(const GqaReadArgs a)
     __shared__ int s_row[kReadRows];          // -1: a zero row, -2: not to be written
     const int r0 = blockIdx.x * kReadRows, h = blockIdx.y;
     pdl_wait();
-    pdl_trigger();
     if (threadIdx.x < kReadRows) {
         const int r = r0 + threadIdx.x;
         int row = -2;
@@ -203,6 +202,7 @@ __global__ void __launch_bounds__(kThreads) gqa_read_kernel(const GqaReadArgs a)
         store8<OB>(a.k, (r0 + r) * a.k_stride + h * D + 8 * u, kw[i], ks[i]);
         store8<OB>(a.v, (r0 + r) * a.v_stride + h * D + 8 * u, vw[i], vs[i]);
     }
+    pdl_trigger();
 }
 
 template <bool BF16, int D, int GS>

@@ -65,7 +65,6 @@ __global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs 
     __shared__ int s_bin, s_left;
     const int b = blockIdx.x / a.c.n_kv, h = blockIdx.x - b * a.c.n_kv, tid = threadIdx.x;
     pdl_wait();
-    pdl_trigger();
     const int n = length_of(a, b, tid == 0 && h == 0);
     const int stay = min(n, a.keep);
     int32_t *kept = a.kept + (long long)blockIdx.x * a.keep;
@@ -151,6 +150,7 @@ __global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs 
         const uint32_t k = key(t);
         if (k > prefix || (k == prefix && equal++ < left)) kept[at++] = t;
     }
+    pdl_trigger();
 }
 
 // A warp has 32 rows that stay: each lane finds one's old and new place and moves its scales and weight, then the lanes move all their
@@ -162,7 +162,6 @@ __global__ void __launch_bounds__(256, 6) gqa_move_kernel(const GqaEvictArgs a) 
     const long long w = blockIdx.x * 8LL + (threadIdx.x >> 5);
     const int pair = (int)(w / per), i = (int)(w - (long long)pair * per) * 32 + lane;
     pdl_wait();
-    pdl_trigger();
     if (pair >= a.n_seq * a.c.n_kv) return;
     const int b = pair / a.c.n_kv, h = pair - b * a.c.n_kv;
     const int t = i < a.keep ? a.kept[(long long)pair * a.keep + i] : -1;
@@ -201,6 +200,7 @@ __global__ void __launch_bounds__(256, 6) gqa_move_kernel(const GqaEvictArgs a) 
             if (row >= 0) codes[(long long)row * kHalf + piece % kHalf] = x[k];
         }
     }
+    pdl_trigger();
 }
 
 }  // namespace

@@ -189,7 +189,6 @@ __global__ void __launch_bounds__(384, 1)
     constexpr uint32_t kHalf = nb * (kBlk / 2);          // 64 value rows
     constexpr uint32_t k_off = 2 * nb * kBlk, v_off = k_off + kKeys * kBlk, o_off = v_off + kValues * kHalf;
     pdl_wait();
-    pdl_trigger();
     if (warp == 0) tmem_alloc(&s.tmem, 512);
     if (tid == 0) {
         for (int i = 0; i < 2; i++) {
@@ -560,6 +559,7 @@ __global__ void __launch_bounds__(384, 1)
             }
         }
     }
+    pdl_trigger();
     tc_before_sync();
     __syncthreads();
     if (warp == 0) {
@@ -589,7 +589,6 @@ __global__ void __launch_bounds__(256) gqa_round_q_kernel(const GqaPrefillArgs a
     constexpr int kUnits = D / 8;
     __shared__ uint32_t most[2];
     pdl_wait();
-    pdl_trigger();
     auto finite = [](float x) {
         const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
         return b < 0x7F800000u ? b : 0u;
@@ -637,6 +636,7 @@ __global__ void __launch_bounds__(256) gqa_round_q_kernel(const GqaPrefillArgs a
         reinterpret_cast<uint4 *>(q16)[r * kUnits + u] = make_uint4(pack_f16(scaled(x.x, e), scaled(x.y, e)), pack_f16(scaled(x.z, e), scaled(x.w, e)),
                                                                   pack_f16(scaled(y.x, e), scaled(y.y, e)), pack_f16(scaled(y.z, e), scaled(y.w, e)));
     }
+    pdl_trigger();
 }
 // Second step: k and v, each times one power of two.
 template <int D>
@@ -644,7 +644,6 @@ __global__ void __launch_bounds__(256) gqa_round_kv_kernel(const GqaPrefillArgs 
     constexpr int kUnits = D / 8;
     __shared__ uint32_t most[2];
     pdl_wait();
-    pdl_trigger();
     if (threadIdx.x < 2) most[threadIdx.x] = 0;
     __syncthreads();
     uint2 m = make_uint2(0, 0);
@@ -667,6 +666,7 @@ __global__ void __launch_bounds__(256) gqa_round_kv_kernel(const GqaPrefillArgs 
         reinterpret_cast<uint4 *>(value ? v16 : k16)[j] = make_uint4(pack_f16(scaled(x.x, e), scaled(x.y, e)), pack_f16(scaled(x.z, e), scaled(x.w, e)),
                                                                      pack_f16(scaled(y.x, e), scaled(y.y, e)), pack_f16(scaled(y.z, e), scaled(y.w, e)));
     }
+    pdl_trigger();
 }
 
 // What a call with f32 inputs keeps in scratch.
