@@ -751,7 +751,6 @@ __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, 
     const int place = blockIdx.x / kSets, row0 = (blockIdx.x - place * kSets) * ROWS;
     const int b = place / per, seg = place - b * per, h = seg / plan.rg, set = seg - h * plan.rg;
     pdl_wait();
-    pdl_trigger();
     const long long before = plan.before[b], units = plan.before[a.n_seq] * per;
     const int nt = (int)(plan.before[b + 1] - before);   // tiles, or pieces
     const long long u0 = before * per + (long long)seg * nt;
@@ -844,6 +843,7 @@ __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, 
         if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         if (d == 0 && a.weigh) plan.stat[(long long)place * kRows + row0 + row] = make_float2(m, inv1);
     }
+    pdl_trigger();
 }
 
 // Rows of `bytes` codes; boxes of box_rows of them, swizzled by their length.

@@ -643,28 +643,39 @@ template <int D>
 __global__ void __launch_bounds__(256) gqa_round_kv_kernel(const GqaPrefillArgs a, __half *k16, __half *v16, int *exponent, const uint2 *range, int ranges) {
     constexpr int kUnits = D / 8;
     __shared__ uint32_t most[2];
+    const int upt = a.H * kUnits;
+    const long long units = (long long)a.Tk * upt, step = gridDim.x * 256LL;
+    float4 x, y;
+    auto load = [&](long long i) {
+        const bool value = i >= units;
+        const long long j = value ? i - units : i, t = j / upt;
+        const float *p = (const float *)(value ? a.v : a.k) + t * (value ? a.v_stride : a.k_stride) + 8 * (j - t * upt);
+        x = *reinterpret_cast<const float4 *>(p);
+        y = *reinterpret_cast<const float4 *>(p + 4);
+    };
     pdl_wait();
+    // the first elements are on their way while the largest magnitudes are looked up
+    long long i = blockIdx.x * 256LL + threadIdx.x;
+    if (i < 2 * units) load(i);
     if (threadIdx.x < 2) most[threadIdx.x] = 0;
     __syncthreads();
     uint2 m = make_uint2(0, 0);
-    for (int i = threadIdx.x; i < ranges; i += 256) m = make_uint2(max(m.x, range[i].x), max(m.y, range[i].y));
+    for (int r = threadIdx.x; r < ranges; r += 256) m = make_uint2(max(m.x, range[r].x), max(m.y, range[r].y));
     m = make_uint2(__reduce_max_sync(0xffffffffu, m.x), __reduce_max_sync(0xffffffffu, m.y));
     if ((threadIdx.x & 31) == 0) {
         atomicMax(&most[0], m.x);
         atomicMax(&most[1], m.y);
     }
     __syncthreads();
-    const int ek = f16_exponent(most[0]), ev = f16_exponent(most[1]), upt = a.H * kUnits;
+    const int ek = f16_exponent(most[0]), ev = f16_exponent(most[1]);
     if (blockIdx.x == 0 && threadIdx.x == 0) exponent[0] = ek, exponent[1] = ev;
-    const long long units = (long long)a.Tk * upt;
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < 2 * units; i += gridDim.x * 256LL) {
+    for (; i < 2 * units; i += step) {
         const bool value = i >= units;
-        const long long j = value ? i - units : i, t = j / upt;
-        const int u = (int)(j - t * upt), e = value ? ev : ek;
-        const float *p = (const float *)(value ? a.v : a.k) + t * (value ? a.v_stride : a.k_stride) + 8 * u;
-        const float4 x = *reinterpret_cast<const float4 *>(p), y = *reinterpret_cast<const float4 *>(p + 4);
-        reinterpret_cast<uint4 *>(value ? v16 : k16)[j] = make_uint4(pack_f16(scaled(x.x, e), scaled(x.y, e)), pack_f16(scaled(x.z, e), scaled(x.w, e)),
-                                                                     pack_f16(scaled(y.x, e), scaled(y.y, e)), pack_f16(scaled(y.z, e), scaled(y.w, e)));
+        const int e = value ? ev : ek;
+        reinterpret_cast<uint4 *>(value ? v16 : k16)[value ? i - units : i] =
+            make_uint4(pack_f16(scaled(x.x, e), scaled(x.y, e)), pack_f16(scaled(x.z, e), scaled(x.w, e)),
+                       pack_f16(scaled(y.x, e), scaled(y.y, e)), pack_f16(scaled(y.z, e), scaled(y.w, e)));
+        if (i + step < 2 * units) load(i + step);
     }
     pdl_trigger();
 }
@@ -673,7 +684,7 @@ __global__ void __launch_bounds__(256) gqa_round_kv_kernel(const GqaPrefillArgs 
 struct Rounded {
     size_t q, k, v, q_exponent, exponent, range, end;
 };
-constexpr int kRanges = 152;             // CTAs that look for the largest magnitudes, at most
+constexpr int kRanges = 608;             // CTAs that look for the largest magnitudes, at most
 Rounded rounded(const GqaPrefillArgs &a) {
     Rounded z;
     z.q = 0;
