@@ -14,7 +14,7 @@
 //   O^T += V^T P^T  codes AND-ed out are bf16 subnormals n 2^-133 (odd nibbles 16 times that, taken back at the end); p times
 //                 2^80 rounded to bf16, transposed in registers, its product with the row's scale rounded to bf16; -8 sum P comes from
 //                 one more product.  2^80 keeps products and sums within f32 for scales from 2^-60 to 2^38.  (Codes as
-//                 128 + n need an OR and two more shifts a word: 48x12000 87.3 us, this way 84.4.)
+//                 128 + n need an OR and two more shifts a word: 48x12000 3 us more.)
 // so no code is converted one by one.  ldmatrix, transposing for the values, deals the words out as the products want them:
 // its 16-bit elements are 4 codes of one token.  N = 8 is what few query rows need; 5th-generation products would want the codes
 // as bytes in shared memory, M = 128 tokens, and N = 8 as well.
@@ -27,10 +27,10 @@
 // scores instead would need scratch for every token that the page tables could hold.
 // Every wait is bounded, by a limit that each segment and set of rows renews.
 //
-// Bound: a tile takes 480 instructions of a warp, 215 of them ANDs, shifts and the like on the ALU pipe, which has an SM's four
-// warps' worth of tiles in 430 cycles at best where HBM delivers them in 690; measured, 100000 more tokens of 8 heads, gs 32, take 17 us,
-// 6.7 TB/s.  About 10 us of a call are start (lengths, pages, first copies), last tiles and join: 1x1000 10.3 us on the device,
-// 1x100000 (32 heads on 8, gs 128) 30.3, 48x12000 (64 on 8) 84.4 = 4.4 TB/s, 4x9000 of 3 tokens (28 on 4) 21, 16x8000 with weights 52.7.
+// Bound: HBM once a call is long.  A tile takes 480 instructions of a warp, 215 of them ANDs, shifts and the like on the ALU pipe (430
+// cycles of a quarter of an SM, which HBM gives a tile in 790); measured, 100000 more tokens of 8 heads, gs 32, take 17 us,
+// 6.7 TB/s.  Some 14 us of a call that fills the GPU are start (lengths, pages, first copies), last tiles and join: 48x12000 (64 heads on
+// 8) 80.9 us = 4.6 TB/s, 1x100000 (32 on 8, gs 128) 28.6, 4x9000 of 3 tokens (28 on 4) 18.4, 16x8000 with weights 49; 1x1000 9.8.
 // 16 warps an SM with 128 registers each; 12 with 168 or 20 with 96 are 14 to 17 % slower.
 #include <algorithm>
 

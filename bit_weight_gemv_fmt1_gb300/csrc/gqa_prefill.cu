@@ -23,12 +23,12 @@
 // hand-overs 250), longer than the 1024 of the other tile's products.  P is handed over in halves of 64 keys and the arithmetic on
 // pairs is packed (1x8192, 32 heads on 8: 376 us, 370 with halves, 366 packed, 355 once the next unit is asked for late); half a row per
 // thread, two warps a tile and SM quarter, is slower (384).  1.54 PFLOP/s, 0.80 of the measured bf16 rate; 1x2048 33 us, 6 ragged up
-// to 700 behind 333 cached 45.5, 24 of up to 301 (D 64) 17.
+// to 700 behind 333 cached 46, 24 of up to 301 (D 64) 17.
 //
 // f32 inputs become f16, which keeps 3 bits more than bf16: every row of q times a power of two of its own, k and v times one each,
 // so that the largest magnitudes lie in 2^14 .. 2^15 and all down to 2^-28 of them keep their 11 bits.  P is f16 then too.  The
 // powers come out again in the scores' factor, a thread's own, and with 1 / l.  (bf16 without the powers: twice the error.)  The
-// two launches that make them take 9 us of the 29 of 24 short prompts.
+// two launches that make them take 9 us of the 28 of 24 short prompts.
 //
 // Keys past a causal row's limit are masked by selection; value rows past the
 // sequence's end belong to its neighbours and are zeroed in shared memory.
