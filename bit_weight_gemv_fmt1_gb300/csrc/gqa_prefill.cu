@@ -387,7 +387,8 @@ __global__ void __launch_bounds__(384, 1)
                 if (nt > 0) {
                     tmem_ld(O + c0, o);
                     tmem_ld_wait();
-                } else {
+                }
+                if (nt == 0 || limit <= 0) {             // a row without keys beside ones that have some: 0 times their values may be NaN
 #pragma unroll
                     for (int c = 0; c < 32; c++) o[c] = 0u;
                 }

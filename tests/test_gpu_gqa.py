@@ -396,6 +396,26 @@ def test_prompt_masked_values(lens_q, lens_k, H, K, D, kind):
     assert ((got - ref).abs()[fine] <= tol[fine]).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_prompt_rows_without_keys_beside_infinite_values(kind):
+    """More queries than keys, and values that are not finite: the first queries, which share a tile with some that see
+    those, give zeros."""
+    torch, coli = setup()
+    g = gen(torch, 21)
+    q, kv = packed_qkv(torch, [100, 9], [70, 3], 4, 2, 64, g, torch.bfloat16 if kind == "bf16" else torch.float32)
+    kv[0, 2, 3] = kv[70, 3, 5] = float("nan")
+    kv[1, 3, 7], kv[69, 2, 9], kv[72, 2, 0] = float("inf"), float("-inf"), float("inf")
+    out, lse = torch.full((109, 4, 64), -5.0, device="cuda"), torch.full((109, 4), -5.0, device="cuda")
+    dev = kv.cuda()
+    coli.gqa_prefill(q.cuda(), dev[:, :2], dev[:, 2:4], torch.tensor([0, 100, 109], dtype=torch.int32, device="cuda"),
+                     torch.tensor([0, 70, 73], dtype=torch.int32, device="cuda"), 0.12, out, lse)
+    coli.sync_check()
+    for first, last in ((0, 30), (100, 106)):
+        assert (out[first:last] == 0).all() and (lse[first:last] == -math.inf).all()
+    assert torch.isnan(out[30:100, :2, 3]).all() and torch.isnan(out[106:, 2:, 5]).all()
+    assert torch.isfinite(out[30:100, :2, 10:]).all() and torch.isfinite(lse[30:100]).all()
+
+
 def test_prompt_bad_offsets():
     torch, coli = setup()
     q, k = torch.zeros(10, 2, 64, device="cuda", dtype=torch.bfloat16), torch.zeros(10, 1, 64, device="cuda", dtype=torch.bfloat16)
