@@ -39,6 +39,7 @@ struct GqaReadArgs {
 
 struct GqaAttendArgs {
     GqaCache c;
+    int longest;            // length allowed
     const void *q;
     int q_bf16, out_bf16, weigh;
     int n_seq, n_q, H;
@@ -53,6 +54,7 @@ struct GqaAttendArgs {
 
 struct GqaEvictArgs {
     GqaCache c;
+    int longest;            // length allowed
     const int32_t *pages;
     long long pages_stride;
     int n_seq;

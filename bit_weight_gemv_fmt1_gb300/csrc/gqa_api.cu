@@ -1,5 +1,7 @@
 // gqa_api.cu -- the grouped-head attention entry points of include/coli.h:
 // argument checks and launches.  Nothing is launched unless every check passed.
+#include <algorithm>
+
 #include "api_checks.cuh"
 #include "gqa.cuh"
 
@@ -8,6 +10,9 @@ using namespace coli;
 namespace {
 
 constexpr long long kIntMax = (1LL << 31) - 1;
+constexpr long long kLongest = 1LL << 30;    // tokens of a sequence: the kernels' places, some tiles past its end too, fit an int
+
+int longest(int64_t pages_stride, const GqaCache &c) { return (int)std::min((long long)pages_stride * c.page, kLongest); }
 
 int check_cache(const coli_gqa_cache *c, GqaCache *out) {
     if (!c) return bad(COLI_EINVAL, "cache is NULL");
@@ -137,6 +142,7 @@ int attend(const coli_gqa_cache *cache, int dtype_q, const void *q, int n_seq, i
     a.pages = pages;
     a.pages_stride = pages_stride;
     a.lens = lens;
+    a.longest = longest(pages_stride, a.c);
     a.scale = scale;
     a.out = out;
     a.lse = lse;
@@ -157,7 +163,8 @@ int evict(const coli_gqa_cache *cache, const int32_t *pages, int64_t pages_strid
     if (int rc = check_cache(cache, &a.c)) return rc;
     if (!a.c.w) return bad(COLI_EINVAL, "an eviction needs a cache with weights");
     if (n_seq < 0) return bad(COLI_EINVAL, "n_seq must be >= 0 (got %d)", n_seq);
-    if (keep < 1 || recent < 0 || recent > keep) return bad(COLI_EINVAL, "need keep >= 1 and 0 <= recent <= keep (got %d, %d)", keep, recent);
+    if (keep < 1 || keep > kLongest || recent < 0 || recent > keep)
+        return bad(COLI_EINVAL, "need 1 <= keep <= 2^30 and 0 <= recent <= keep (got %d, %d)", keep, recent);
     if (pages_stride < 1 || pages_stride > kIntMax || dst_stride < 1 || dst_stride > kIntMax)
         return bad(COLI_EINVAL, "pages_stride and dst_stride must be in 1..2^31-1 (got %lld, %lld)", (long long)pages_stride, (long long)dst_stride);
     if (dst_stride * a.c.page < keep) return bad(COLI_EINVAL, "dst_stride pages must hold keep tokens (got %lld, %d)", (long long)dst_stride, keep);
@@ -179,6 +186,7 @@ int evict(const coli_gqa_cache *cache, const int32_t *pages, int64_t pages_strid
     a.pages_stride = pages_stride;
     a.n_seq = n_seq;
     a.lens = lens;
+    a.longest = longest(pages_stride, a.c);
     a.keep = keep;
     a.recent = recent;
     a.dst = dst;

@@ -132,7 +132,7 @@ __device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(
 
 __device__ __forceinline__ int length_of(const GqaAttendArgs &a, int b, bool report) {
     const int n = a.lens[b];
-    if (n >= 0 && n <= a.pages_stride * a.c.page) return n;
+    if (n >= 0 && n <= a.longest) return n;
     if (report) mla_bad_index(a.err);
     return 0;
 }

@@ -30,7 +30,7 @@ __device__ __forceinline__ uint32_t ordered(float w) {
 // A sequence's length; 0 (and a record) where it is out of range.
 __device__ __forceinline__ int length_of(const GqaEvictArgs &a, int b, bool report) {
     const int n = a.lens[b];
-    if (n >= 0 && n <= a.pages_stride * a.c.page) return n;
+    if (n >= 0 && n <= a.longest) return n;
     if (report) mla_bad_index(a.err);
     return 0;
 }

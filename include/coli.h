@@ -624,7 +624,7 @@ int coli_gqa_read(const coli_gqa_cache *cache, const int32_t *pages, int64_t pag
  * queries of its group's heads.  A query that sees no token gives zeros, lse =
  * -infinity and no weight.
  *   q       device [n_seq][n_q][n_heads][dim], COLI_F32 or COLI_BF16 (dtype_q).
- *   pages   as in coli_mla_read; lens[b] <= pages_stride * page_size.
+ *   pages   as in coli_mla_read; lens[b] <= pages_stride * page_size and <= 2^30.
  *   lens    device int32 [n_seq], >= 0.
  *   out     device [n_seq][n_q][n_heads][dim], COLI_F32 or COLI_BF16.
  *   lse     device f32 [n_seq][n_q][n_heads], or NULL.
@@ -656,7 +656,7 @@ int coli_gqa_attend(const coli_gqa_cache *cache, int dtype_q, const void *q, int
  * rows, scales and weights, in their order, to the sequence's new pages.  The
  * sequence's own pages are left as they were.
  *   pages, lens   as in coli_gqa_attend.
- *   keep, recent  keep >= 1, 0 <= recent <= keep.
+ *   keep, recent  1 <= keep <= 2^30, 0 <= recent <= keep.
  *   dst       device int32, sequence b's new page ids at dst + b * dst_stride, for
  *             min(keep, lens[b]) tokens; pages that no sequence of the call reads.
  *   kept      device int32 [n_seq][n_kv][keep]: the tokens that stay, ascending, then -1.

@@ -273,6 +273,34 @@ def test_prompt_many_units(dtype):
     assert ((outs[0].cpu().double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("n", [(1 << 30) + 1, (1 << 31) - 32, (1 << 31) - 1])
+def test_lengths_past_what_a_sequence_may_have(n):
+    """Page tables that repeat a page can hold more than 2^30 tokens; such a length is recorded, as others out of range are, and the
+    sequence beside it is served."""
+    torch, coli = setup()
+    page = 65536
+    k, v = (torch.randint(0, 256, (2, 1, page, 32), dtype=torch.uint8, device="cuda") for _ in "kv")
+    ks, vs = (torch.full((2, 1, page, 1), 0.1, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    w = torch.rand(2, 1, page, device="cuda")
+    c = coli.GqaCache(k, v, ks, vs, w)
+    table = torch.zeros(2, 32768, dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 1, 2, 64, device="cuda")
+
+    def call(lens):
+        out, kept, new = torch.zeros(2, 1, 2, 64, device="cuda"), i32(torch, [[[9] * 40]] * 2), i32(torch, [9, 9])
+        coli.gqa_attend(c, q, table, i32(torch, lens), 0.1, out)
+        coli.gqa_evict(c, table, i32(torch, lens), 40, 8, i32(torch, [[1], [1]]), kept, new)
+        return out, kept, new
+
+    good = call([0, 300])
+    coli.sync_check()
+    out, kept, new = call([n, 300])
+    with pytest.raises(coli.ColiError) as e:
+        coli.sync_check()
+    assert e.value.code == coli.COLI_EINVAL
+    assert torch.equal(out[1], good[0][1]) and torch.equal(kept, good[1]) and new.tolist() == [0, 40]
+
+
 # ------------------------------------------------------------------ waits
 @pytest.fixture
 def limit():

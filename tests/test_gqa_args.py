@@ -108,6 +108,12 @@ def test_evict(lib, kw):  # noqa: F811
     assert evict(lib, **kw) == EINVAL
 
 
+@pytest.mark.parametrize("keep,code", [((1 << 30) + 1, EINVAL), ((1 << 31) - 1, EINVAL)])
+def test_evict_keeps_no_more_than_a_sequence_may_have(lib, keep, code):  # noqa: F811
+    assert evict(lib, cache(page_size=65536, n_pages=1), keep=keep, ds=1 << 15, n=1) == code
+    assert b"2^30" in lib.coli_last_error()
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(dt=E4M3), EFMT), (dict(do=-1), EFMT), (dict(D=96), EINVAL), (dict(K=3), EINVAL), (dict(K=0), EINVAL), (dict(H=0), EINVAL),
     (dict(H=1028), EINVAL), (dict(H=258, K=2, qs=258 * 128), EINVAL), (dict(Tq=-1), EINVAL), (dict(Tk=-1), EINVAL), (dict(n=-1), EINVAL),
