@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int h = WEIGH ? seg : seg / plan.rg;
         const int32_t *pages = a.pages + b * a.pages_stride;
         const int mine = (t1 - t0 - warp + kWarps - 1) / kWarps;   // tiles t0 + warp, t0 + warp + 8, ...
-        for (int set = WEIGH ? 0 : seg - h * plan.rg, sets = WEIGH ? plan.rg : set + 1; set < sets; set++) {
+        for (int set = WEIGH ? 0 : seg - h * plan.rg, sets = WEIGH ? plan.rg : set + 1; set < sets && (!WEIGH || ok); set++) {   // after a wait that ran out, no copies into a stage that has some
             const int r0 = set * kRows;
             const uint64_t deadline = deadline_after(wait_ns, max(mine, 0));
             // copies: lane i holds the first row of the i-th box from `base_tile` on

@@ -343,6 +343,41 @@ def test_step_wait_runs_out(limit):
     coli.sync_check()
 
 
+def test_weighed_step_of_several_sets_wait_runs_out(limit):
+    """As above for the pass that adds the weights, which goes over a head's keys once for each 8 of its 16 query rows."""
+    torch, coli = setup()
+    n, kv, page, seqs = 4096, 8, 64, 16
+    per = n // page
+    k, v = (torch.randint(0, 256, (seqs * per, kv, page, 64), dtype=torch.uint8, device="cuda") for _ in "kv")
+    vs = torch.full((seqs * per, kv, page, 4), 0.1, dtype=torch.bfloat16, device="cuda")
+    ks = vs.cpu().pin_memory()
+    w = torch.zeros(seqs * per, kv, page, device="cuda")
+    c = coli._GqaCache(kv, 128, 32, page, seqs * per, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), w.data_ptr())
+    table, lens = torch.arange(seqs * per, dtype=torch.int32, device="cuda").view(seqs, per), i32(torch, [n] * seqs)
+    q = torch.randn(seqs, 2, 64, 128, device="cuda")
+
+    def call():
+        out = torch.zeros(seqs, 2, 64, 128, device="cuda")
+        w.zero_()
+        rc = coli._lib.coli_gqa_attend(ctypes.byref(c), coli.COLI_F32, q.data_ptr(), seqs, 2, 64, table.data_ptr(), per, lens.data_ptr(), 0.09,
+                                       1, coli.COLI_F32, out.data_ptr(), None, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        return out
+
+    good = call()
+    coli.sync_check()
+    assert abs(float(w.double().sum()) - seqs * 2 * 64) < 1e-3 * seqs * 2 * 64
+    limit(1)
+    call()
+    with pytest.raises(coli.ColiError) as e:
+        coli.sync_check()
+    assert e.value.code == coli.COLI_ETIMEOUT
+    limit(0)
+    assert torch.equal(call(), good)
+    assert abs(float(w.double().sum()) - seqs * 2 * 64) < 1e-3 * seqs * 2 * 64
+    coli.sync_check()
+
+
 def test_prompt_wait_runs_out(limit):
     """Finding the first unit among 20000 sequences takes long enough."""
     torch, coli = setup()
