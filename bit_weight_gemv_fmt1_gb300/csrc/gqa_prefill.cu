@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 __syncwarp();
             };
+            const uint32_t some = limit > 0 ? 0xFFFFFFFFu : 0u;   // a row without keys beside ones that have some: 0 times their values may be NaN
             float odd = 0.f;                             // NaN once an output is not finite
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
@@ -387,13 +388,12 @@ __global__ void __launch_bounds__(384, 1)
                 if (nt > 0) {
                     tmem_ld(O + c0, o);
                     tmem_ld_wait();
-                }
-                if (nt == 0 || limit <= 0) {             // a row without keys beside ones that have some: 0 times their values may be NaN
+                } else {
 #pragma unroll
                     for (int c = 0; c < 32; c++) o[c] = 0u;
                 }
 #pragma unroll
-                for (int c = 0; c < 32; c++) o[c] = __float_as_uint(F16 ? scaled(__uint_as_float(o[c]) * inv, -ev) : __uint_as_float(o[c]) * inv);
+                for (int c = 0; c < 32; c++) o[c] = __float_as_uint(F16 ? scaled(__uint_as_float(o[c]) * inv, -ev) : __uint_as_float(o[c]) * inv) & some;
 #pragma unroll
                 for (int c = 0; c < 32; c++) odd = fmaf(__uint_as_float(o[c]), 0.f, odd);
                 uint32_t w[16];
