@@ -2,14 +2,14 @@
 // and their way to the sequence's new pages.
 //
 // Selection, one CTA per sequence and head: the weights become integers of the
-// same order (a NaN last), three passes of a radix selection (12, 10 and 10 bits,
-// counts in shared memory) give the smallest one that stays and how many equal to it
+// same order (a NaN last), up to three passes of a radix selection (12, 10 and 10 bits,
+// counts in shared memory; none after one whose last bin stays whole) give the smallest one that stays and how many equal to it
 // do; one more pass writes the tokens that stay in their order.  The move is a
 // kernel of its own, so that few sequences use every SM.
 //
-// 12 sequences up to 16000 to 4001 tokens, 8 heads: selection 19 us (96 CTAs: barriers and latency of a few passes over 16 keys a
+// 12 sequences up to 16000 to 4001 tokens, 8 heads: selection 18 us (96 CTAs: barriers and latency of a few passes over 16 keys a
 // thread), move 22 us: of a scattered row's 64 + 64 bytes of codes, 16 of scales and 4 of weight each piece costs DRAM an access of its
-// own, 97 MB for 58 MB.  One sequence of 4096 to 1024: 13 us on the device with the read back.
+// own, 97 MB for 58 MB.  One sequence of 4096 to 1024: 12 us on the device with the read back (13 with always three passes).
 #include <algorithm>
 
 #include "gqa.cuh"
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs 
     extern __shared__ __align__(16) uint32_t keys[];     // the first `room` candidates'; more are read again each time
     __shared__ __align__(16) int count[kBins];
     __shared__ int2 sums[kSelect / 32];
-    __shared__ int s_bin, s_left;
+    __shared__ int s_bin, s_left, s_in;
     const int b = blockIdx.x / a.c.n_kv, h = blockIdx.x - b * a.c.n_kv, tid = threadIdx.x;
     pdl_wait();
     const int n = length_of(a, b, tid == 0 && h == 0);
@@ -108,8 +108,6 @@ __global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs 
         const int shift = pass == 0 ? 20 : pass == 1 ? 10 : 0, bits = pass == 0 ? 12 : 10;
         if (pass > 0) {
             const int known = shift + bits;
-            for (int i = tid; i < kBins; i += kSelect) count[i] = 0;
-            __syncthreads();
             for (int t = tid; t < old; t += kSelect) {
                 const uint32_t k = key(t);
                 if ((k >> known) == (prefix >> known)) atomicAdd(&count[(k >> shift) & ((1 << bits) - 1)], 1);
@@ -117,7 +115,9 @@ __global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs 
         }
         __syncthreads();
         // counts from the top: thread i has the bins 4095 - 4i .. 4092 - 4i
-        const int4 c = *reinterpret_cast<const int4 *>(&count[kBins - 4 - 4 * tid]);
+        int4 *bins = reinterpret_cast<int4 *>(&count[kBins - 4 - 4 * tid]);
+        const int4 c = *bins;
+        *bins = make_int4(0, 0, 0, 0);                   // for the next pass
         int incl = c.x + c.y + c.z + c.w, none = 0, all, all2;
         scan(incl, none, all, all2, sums);
         int before = incl - c.x - c.y - c.z - c.w;
@@ -127,12 +127,14 @@ __global__ void __launch_bounds__(kSelect) gqa_select_kernel(const GqaEvictArgs 
             if (before < left && left <= before + each[i]) {
                 s_bin = kBins - 1 - 4 * tid - i;
                 s_left = left - before;
+                s_in = each[i];
             }
             before += each[i];
         }
         __syncthreads();
         prefix |= (uint32_t)s_bin << shift;
         left = s_left;
+        if (left == s_in) break;                         // all of the bin stay: those above the prefix and those equal to it
     }
     // In order: every key above the last one that stays, and the first `left` equal ones.  A thread has as many neighbours as the
     // next one, an odd number: its lane's words lie in banks of their own.
