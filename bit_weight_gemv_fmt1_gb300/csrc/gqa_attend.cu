@@ -71,7 +71,8 @@ struct Ring {
 struct AttendPlan {
     int n_cta, rg, boxes;                // CTAs, sets of query rows per head, copies per tile (pages of 16, 48, ... tokens: 2)
     float *part;                         // [n_cta][2][kRows][D + 2]: O, m, l
-    float2 *stat;                        // [n_seq][n_kv][rg][kRows]: m and 1 / l, for the weights
+    float2 *stat;                        // [n_seq][n_kv][rg][kRows]: m and 1 / l without 2^80, for the weights: exponents near 80 would
+                                         // be rounded to 2^-18, 1e-6 of a weight
     long long *before;                   // [n_seq + 2]: tiles (or pieces) of the sequences before each and of all, tiles of a piece
 };
 
@@ -721,9 +722,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                     else
                         *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + orow * S::D + d) =
                             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-                    if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                    if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + kUp + log2f(l * 0x1p-80f)) * 0.6931471805599453f : -INFINITY;
                     if (d == 0 && a.weigh)
-                        plan.stat[((long long)(b * (long long)n_kv + h) * plan.rg + set) * kRows + row] = make_float2(m, inv1);
+                        plan.stat[((long long)(b * (long long)n_kv + h) * plan.rg + set) * kRows + row] = make_float2(m + kUp, inv);
                 }
                 fence_async_smem();
                 __syncthreads();
@@ -840,8 +841,8 @@ __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, 
                 make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         else
             *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + orow * S::D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-        if (d == 0 && a.weigh) plan.stat[(long long)place * kRows + row0 + row] = make_float2(m, inv1);
+        if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + kUp + log2f(l * 0x1p-80f)) * 0.6931471805599453f : -INFINITY;
+        if (d == 0 && a.weigh) plan.stat[(long long)place * kRows + row0 + row] = make_float2(m + kUp, inv);
     }
     pdl_trigger();
 }
