@@ -5,7 +5,8 @@
 // group's heads).  A segment is the tiles of one sequence, head and set of rows; CTAs have a piece of one each, or, where segments
 // are many, an equal share of all units in a row, which they walk by segments.  A segment's tiles go round the CTA's 8 warps, each
 // with a running maximum, sum and output of its own and a ring of tiles that bulk copies fill; the warps join at the
-// segment's end.  A segment that several CTAs have is joined by a second kernel.
+// segment's end.  A segment that several CTAs have is joined by a second kernel.  Short calls (cluster_of) have a cluster of 8, 4, 2 or
+// 1 CTAs for each segment instead, which hand one another their sums through shared memory: one kernel in all.
 //
 // Per warp and 16 tokens (mma.sync m16n8k16, tokens or dims as M, query rows as N):
 //   S^T = K q^T   codes AND-ed out of the words are f16 subnormals n 2^-24 (odd nibbles
@@ -30,7 +31,7 @@
 // Bound: HBM once a call is long.  A tile takes 480 instructions of a warp, 215 of them ANDs, shifts and the like on the ALU pipe (430
 // cycles of a quarter of an SM, which HBM gives a tile in 790); measured, 100000 more tokens of 8 heads, gs 32, take 17 us,
 // 6.7 TB/s.  Some 14 us of a call that fills the GPU are start (lengths, pages, first copies), last tiles and join: 48x12000 (64 heads on
-// 8) 80.9 us = 4.6 TB/s, 1x100000 (32 on 8, gs 128) 28.6, 4x9000 of 3 tokens (28 on 4) 18.4, 16x8000 with weights 49; 1x1000 9.8.
+// 8) 80.9 us = 4.6 TB/s, 1x100000 (32 on 8, gs 128) 28.6, 4x9000 of 3 tokens (28 on 4) 18.4, 16x8000 with weights 49; 1x1000, a cluster a head, 7.2.
 // 16 warps an SM with 128 registers each; 12 with 168 or 20 with 96 are 14 to 17 % slower.
 #include <algorithm>
 
@@ -49,6 +50,7 @@ constexpr float kUp = 80.f, kScale = 0x1p80f;   // log2 of what p is held times,
 constexpr float kDown = 0x1p53f;         // codes' 2^133 without it: outputs without factors
 constexpr float kNone = -3e38f;          // reference of a row that has seen no key
 constexpr int kRows = 8;                 // query rows of a unit: N of the products
+constexpr int kRounds = 4;               // tiles of a warp, at the most that page tables could hold, for which clusters are taken
 
 template <int D_, int NG_>
 struct Shape {
@@ -70,6 +72,7 @@ struct Ring {
 
 struct AttendPlan {
     int n_cta, rg, boxes;                // CTAs, sets of query rows per head, copies per tile (pages of 16, 48, ... tokens: 2)
+    int cluster;                         // CTAs of a cluster, which share a segment; 0: no clusters
     float *part;                         // [n_cta][2][kRows][D + 2]: O, m, l
     float2 *stat;                        // [n_seq][n_kv][rg][kRows]: m and 1 / l without 2^80, for the weights: exponents near 80 would
                                          // be rounded to 2^-18, 1e-6 of a weight
@@ -452,6 +455,30 @@ __device__ __forceinline__ void scores(const uint8_t *sm, const uint8_t *scales,
     }
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// The address of a place in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t of_rank(const void *p, int rank) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+    return at;
+}
+
+// Output, lse and what the weights need, of a row of set `set` and its dims d .. d + 3.
+__device__ __forceinline__ void finish(const GqaAttendArgs &a, const AttendPlan &plan, int b, int h, int set, int row, int d, int D, const float4 &o, float m,
+                                       float l) {
+    const int n_kv = a.c.n_kv, G = a.H / n_kv, at = set * kRows + row;
+    if (at >= a.n_q * G) return;
+    const float inv = l != 0.f ? 1.f / l * kScale : 0.f;
+    const long long orow = (long long)(b * (long long)a.n_q + at / G) * a.H + h * G + at % G;
+    if (a.out_bf16)
+        *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * D + d) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    else
+        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + orow * D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + kUp + log2f(l * 0x1p-80f)) * 0.6931471805599453f : -INFINITY;
+    if (d == 0 && a.weigh) plan.stat[((long long)(b * (long long)n_kv + h) * plan.rg + set) * kRows + row] = make_float2(m + kUp, inv);
+}
+
 // Moves the references, and what has been added up, if some score of the tile is 8 above: that much is seen without a look at the other
 // lanes.
 template <class S>
@@ -484,7 +511,7 @@ __device__ __forceinline__ void move_references(const Query<S> &y, Sums<S> &z, c
     }
 }
 
-template <class S, bool WEIGH>
+template <class S, bool WEIGH, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 2)
     gqa_attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const GqaAttendArgs a,
                       const AttendPlan plan, long long wait_ns) {
@@ -502,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = 0; i < R::kDepth; i++) mbar_init(&full[warp][i], 1);
     if (tid == 0) s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if constexpr (CLUSTER) cluster_arrive();             // the CTAs have begun
     pdl_wait();
     __syncthreads();
     volatile int *abort = &s_abort;
@@ -509,8 +537,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int per = WEIGH ? n_kv : n_kv * plan.rg;       // segments of a sequence
     if (!WEIGH && blockIdx.x == 0)
         for (int b = tid; b < a.n_seq; b += kThreads) length_of(a, b, true);
-    const Share share = find_share(a, per, WEIGH ? nullptr : plan.before);
-    if (share.seq < 0) return;
+    Share share;
+    int rank = 0;
+    if constexpr (CLUSTER) {
+        const int place = blockIdx.x / plan.cluster;     // a segment each
+        rank = blockIdx.x - place * plan.cluster;
+        share.seq = place / per;
+        share.first = 0;
+        share.u = place - share.seq * per;
+        share.u1 = share.u + 1;
+        share.piece = 1;
+    } else {
+        share = find_share(a, per, WEIGH ? nullptr : plan.before);
+        if (share.seq < 0) return;
+    }
     const long long u1 = share.u1;
     long long u = share.u, first = share.first;
     int b = share.seq;
@@ -519,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     while (u < u1) {
         const int len = length_of(a, b, false), nt = (len + kTile - 1) / kTile;
         const long long at = u - first * per;
-        const int each = share.piece ? (nt - 1) / share.piece + 1 : nt;   // pieces or tiles of a segment
-        const int seg = (int)(at / each), k = (int)(at - (long long)seg * each);
+        const int each = CLUSTER ? plan.cluster : share.piece ? (nt - 1) / share.piece + 1 : nt;   // pieces or tiles of a segment
+        const int seg = CLUSTER ? (int)at : (int)(at / each), k = CLUSTER ? rank : (int)(at - (long long)seg * each);
         const int t0 = share.piece ? (int)((long long)nt * k / each) : k;
         const int t1 = share.piece ? (int)((long long)nt * (k + 1) / each) : (int)min((long long)nt, t0 + (u1 - u));
         const int h = WEIGH ? seg : seg / plan.rg;
@@ -692,6 +732,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 }
                 __syncthreads();
+                __shared__ float4 c_o[CLUSTER ? kRows : 1][S::D / 4];   // of each CTA of the cluster, the rows that this one joins
+                __shared__ float2 c_ml[kRows];
+                const int rows = CLUSTER ? kRows / plan.cluster : kRows;
+                if constexpr (CLUSTER) cluster_wait();
                 const bool whole = t0 == 0 && t1 == nt;
                 float *part = plan.part + ((long long)blockIdx.x * 2 + (t0 == 0)) * kRows * (S::D + 2);
                 for (int i = tid; i < kRows * (S::D / 4); i += kThreads) {
@@ -707,24 +751,42 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const float4 x = *reinterpret_cast<const float4 *>(base + w * R::kDepth * R::kStage + (row * S::D + d) * 4);
                         o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
                     }
+                    if constexpr (CLUSTER) {
+                        const int to = row / rows, place = rank * rows + row - to * rows;
+                        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(of_rank(&c_o[place][d / 4], to)), "f"(o.x), "f"(o.y), "f"(o.z),
+                                     "f"(o.w)
+                                     : "memory");
+                        if (d == 0) asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(of_rank(&c_ml[place], to)), "f"(m), "f"(l) : "memory");
+                        continue;
+                    }
                     if (!whole) {
                         *reinterpret_cast<float4 *>(part + row * S::D + d) = o;
                         if (d == 0) *reinterpret_cast<float2 *>(part + kRows * S::D + 2 * row) = make_float2(m, l);
                         continue;
                     }
-                    const int at = r0 + row;
-                    if (at >= n_rows) continue;
-                    const float inv1 = l != 0.f ? 1.f / l : 0.f, inv = inv1 * kScale;
-                    const long long orow = (long long)(b * (long long)a.n_q + at / G) * a.H + h * G + at % G;
-                    if (a.out_bf16)
-                        *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * S::D + d) =
-                            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-                    else
-                        *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + orow * S::D + d) =
-                            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-                    if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + kUp + log2f(l * 0x1p-80f)) * 0.6931471805599453f : -INFINITY;
-                    if (d == 0 && a.weigh)
-                        plan.stat[((long long)(b * (long long)n_kv + h) * plan.rg + set) * kRows + row] = make_float2(m + kUp, inv);
+                    finish(a, plan, b, h, set, row, d, S::D, o, m, l);
+                }
+                if constexpr (CLUSTER) {
+                    cluster_arrive();
+                    cluster_wait();
+                    if (tid < rows * (S::D / 4)) {
+                        const int row = tid / (S::D / 4), col = tid % (S::D / 4);
+                        float m = kNone, l = 0.f;
+                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int c = 0; c < kRows; c++)
+                            if (c < plan.cluster) m = fmaxf(m, c_ml[c * rows + row].x);
+#pragma unroll
+                        for (int c = 0; c < kRows; c++)
+                            if (c < plan.cluster) {
+                                const float2 ml1 = c_ml[c * rows + row];
+                                const float4 x = c_o[c * rows + row][col];
+                                const float f = ex2(ml1.x - m);
+                                l = fmaf(ml1.y, f, l);
+                                o = make_float4(fmaf(x.x, f, o.x), fmaf(x.y, f, o.y), fmaf(x.z, f, o.z), fmaf(x.w, f, o.w));
+                            }
+                        finish(a, plan, b, h, set, rank * rows + row, 4 * col, S::D, o, m, l);
+                    }
                 }
                 fence_async_smem();
                 __syncthreads();
@@ -748,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <class S, int ROWS>
 __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, const AttendPlan plan) {
     constexpr int kSets = kRows / ROWS;
-    const int n_kv = a.c.n_kv, G = a.H / n_kv, n_rows = a.n_q * G, per = n_kv * plan.rg;
+    const int n_kv = a.c.n_kv, per = n_kv * plan.rg;
     const int place = blockIdx.x / kSets, row0 = (blockIdx.x - place * kSets) * ROWS;
     const int b = place / per, seg = place - b * per, h = seg / plan.rg, set = seg - h * plan.rg;
     pdl_wait();
@@ -826,23 +888,14 @@ __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, 
     }
     sum[lot][row][d / 4] = o;
     __syncthreads();
-    const int at = set * kRows + row0 + row;
-    if (lot == 0 && at < n_rows) {
+    if (lot == 0) {
         const float m = s_m[row], l = s_l[row];
 #pragma unroll
         for (int k = 1; k < kSplit; k++) {
             const float4 x = sum[k][row][d / 4];
             o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
         }
-        const float inv1 = l != 0.f ? 1.f / l : 0.f, inv = inv1 * kScale;
-        const long long orow = (long long)(b * (long long)a.n_q + at / G) * a.H + h * G + at % G;
-        if (a.out_bf16)
-            *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + orow * S::D + d) =
-                make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        else
-            *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + orow * S::D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + kUp + log2f(l * 0x1p-80f)) * 0.6931471805599453f : -INFINITY;
-        if (d == 0 && a.weigh) plan.stat[(long long)place * kRows + row0 + row] = make_float2(m + kUp, inv);
+        finish(a, plan, b, h, set, row0 + row, d, S::D, o, m, l);
     }
     pdl_trigger();
 }
@@ -873,6 +926,36 @@ size_t part_bytes(const GqaAttendArgs &a, int n_cta) {
     return round256((size_t)n_cta * 2 * kRows * (a.c.dim + 2) * sizeof(float));
 }
 
+// CTAs of a cluster that shares a segment, 0: segments are dealt out by find_share and joined by a second kernel.  Clusters
+// need neither the one nor the other, but leave SMs idle where 8 CTAs a segment do not fill the GPU, and go by the longest sequence: what
+// counts is the rounds of tiles a warp would go through, by the page tables' width, since lengths are known on the device alone.
+// Device time, this way / that: 1x1000 (8 heads) 7.3 / 10.0 us, 4x4000 11.4 / 14.0, 16x500 9.8 / 12.5, at 4 rounds 1x8000 11.9 / 12.5, 32x1000
+// 14.8 / 15.2; at 5 4x10000 17.7 / 17.6, at 6 to 8 8x6000 18.7 / 17.6, 1x16000 16.5 / 14.8.
+int cluster_of(const GqaAttendArgs &a, int n_sm) {
+    const long long segments = (long long)a.n_seq * a.c.n_kv * row_groups(a), tiles = (a.longest + kTile - 1) / kTile;
+    for (int c = kRows; c; c /= 2)
+        if (segments * c <= 2 * n_sm) return (tiles + c - 1) / c <= kRounds * kWarps ? c : 0;
+    return 0;
+}
+
+template <class... P, class... A>
+cudaError_t launch_clusters(void (*kern)(P...), int n_cta, int size, size_t smem, cudaStream_t st, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n_cta);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = size;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
+}
+
 template <class S>
 cudaError_t run(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch) {
     AttendPlan plan;
@@ -886,21 +969,29 @@ cudaError_t run(const GqaAttendArgs &a, const DevInfo &d, cudaStream_t st, int *
     const long long rows = (long long)a.c.n_pages * a.c.n_kv * a.c.page;
     if (cudaError_t e = code_map(a.c.k, S::kRow, rows, kTile / plan.boxes, &k)) return e;
     if (cudaError_t e = code_map(a.c.v, S::kRow, rows, kTile / plan.boxes, &v)) return e;
-    static std::atomic<uint64_t> done{0}, done_weigh{0};
-    if (cudaError_t e = allow_smem(gqa_attend_kernel<S, false>, Ring<S, false>::kSmem, d.device, done)) return e;
-    if (cudaError_t e = launch_pdl(gqa_attend_kernel<S, false>, dim3(plan.n_cta), dim3(kThreads), Ring<S, false>::kSmem, st, k, v, a, plan, d.wait_ns))
-        return e;
-    *n_launch = 2;
+    static std::atomic<uint64_t> done{0}, done_cluster{0}, done_weigh{0};
     const long long segments = (long long)a.n_seq * a.c.n_kv * plan.rg;
-    if (plan.n_cta > 4 * segments) {          // 4 parts a segment or more
-        if (cudaError_t e = launch_pdl(gqa_join_kernel<S, 1>, dim3((unsigned)segments * kRows), dim3(kJoin), 0, st, a, plan)) return e;
+    plan.cluster = cluster_of(a, d.n_sm);
+    if (plan.cluster) {
+        if (cudaError_t e = allow_smem(gqa_attend_kernel<S, false, true>, Ring<S, false>::kSmem, d.device, done_cluster)) return e;
+        if (cudaError_t e = launch_clusters(gqa_attend_kernel<S, false, true>, (int)segments * plan.cluster, plan.cluster, Ring<S, false>::kSmem, st, k, v, a, plan, d.wait_ns))
+            return e;
+        *n_launch = 1;
     } else {
-        if (cudaError_t e = launch_pdl(gqa_join_kernel<S, kRows>, dim3((unsigned)segments), dim3(kJoin), 0, st, a, plan)) return e;
+        if (cudaError_t e = allow_smem(gqa_attend_kernel<S, false, false>, Ring<S, false>::kSmem, d.device, done)) return e;
+        if (cudaError_t e = launch_pdl(gqa_attend_kernel<S, false, false>, dim3(plan.n_cta), dim3(kThreads), Ring<S, false>::kSmem, st, k, v, a, plan, d.wait_ns))
+            return e;
+        *n_launch = 2;
+        if (plan.n_cta > 4 * segments) {      // 4 parts a segment or more
+            if (cudaError_t e = launch_pdl(gqa_join_kernel<S, 1>, dim3((unsigned)segments * kRows), dim3(kJoin), 0, st, a, plan)) return e;
+        } else {
+            if (cudaError_t e = launch_pdl(gqa_join_kernel<S, kRows>, dim3((unsigned)segments), dim3(kJoin), 0, st, a, plan)) return e;
+        }
     }
     if (!a.weigh) return cudaSuccess;
-    *n_launch = 3;
-    if (cudaError_t e = allow_smem(gqa_attend_kernel<S, true>, Ring<S, true>::kSmem, d.device, done_weigh)) return e;
-    return launch_pdl(gqa_attend_kernel<S, true>, dim3(plan.n_cta), dim3(kThreads), Ring<S, true>::kSmem, st, k, v, a, plan, d.wait_ns);
+    ++*n_launch;
+    if (cudaError_t e = allow_smem(gqa_attend_kernel<S, true, false>, Ring<S, true>::kSmem, d.device, done_weigh)) return e;
+    return launch_pdl(gqa_attend_kernel<S, true, false>, dim3(plan.n_cta), dim3(kThreads), Ring<S, true>::kSmem, st, k, v, a, plan, d.wait_ns);
 }
 
 }  // namespace

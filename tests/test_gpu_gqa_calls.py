@@ -202,6 +202,36 @@ def test_wide_page_tables():
     assert ((got.cpu().double() - ref).abs() <= tol).all() and ((want.cpu().double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("seqs,K,H,n_q,D,gs", [(1, 8, 32, 1, 128, 32), (2, 8, 24, 2, 64, 64), (9, 4, 28, 1, 128, 64), (8, 8, 16, 2, 128, 128), (20, 5, 5, 1, 64, 32),
+                                               (38, 8, 16, 1, 128, 32), (39, 8, 16, 1, 64, 32)])
+def test_clusters_and_shares(seqs, K, H, n_q, D, gs):
+    """Segments shared by clusters of 8, 4, 2 CTAs and by none, and the same dealt out as a wide table has them, against 64 bits: outputs,
+    lse, weights."""
+    torch, coli = setup()
+    g = gen(torch, seqs + D)
+    lens = [int(x) for x in torch.randint(0, 230, (seqs,), generator=g)]
+    lens[0] = 231
+    s, table, _ = filled(torch, coli, lens, K, 16, D, gs, g)
+    q = torch.randn(seqs, n_q, H, D, generator=g).to(torch.bfloat16)
+    ref, tol, ref_lse, weights, w_tol = reference_step(torch, s, table, lens, q, 0.1, "bf16", "f32")
+    wide = torch.full((seqs, 5000), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    none = torch.isinf(ref_lse)
+    for t in (table, wide):
+        before = s.w.cpu().double()
+        out, lse = run_step(torch, coli, s, t, lens, q, 0.1, "f32", weigh=True)
+        assert ((out.cpu().double() - ref).abs() <= tol).all()
+        got = lse.cpu().double()
+        assert torch.equal(torch.isinf(got), none) and ((got - ref_lse)[~none].abs() <= 1e-4 * (1 + ref_lse[~none].abs())).all()
+        after = s.w.cpu().double()
+        for b, m in enumerate(lens):
+            for i in range(-(-m // 16)):
+                k, p = min(16, m - 16 * i), int(table[b, i])
+                off = (after[p, :, :k] - before[p, :, :k] - weights[b][:, 16 * i:16 * i + k]).abs()
+                # f32 additions to what the first call has left
+                assert (off <= w_tol[b][:, 16 * i:16 * i + k] + 2.0 ** -23 * (1 + before[p, :, :k].abs() + weights[b][:, 16 * i:16 * i + k])).all()
+
+
 def test_far_pages():
     """Codes past 2^32 bytes, rows past 2^26: writes, reads, steps with weights and an eviction at both ends of the cache."""
     torch, coli = setup()
@@ -343,6 +373,37 @@ def test_step_wait_runs_out(limit):
     coli.sync_check()
 
 
+def test_cluster_step_wait_runs_out(limit):
+    """As above where two CTAs share a sequence's head, with the values' scales there, too."""
+    torch, coli = setup()
+    n, kv, page, seqs = 2048, 8, 64, 16
+    per = n // page
+    k, v = (torch.randint(0, 256, (seqs * per, kv, page, 64), dtype=torch.uint8, device="cuda") for _ in "kv")
+    ks, vs = (torch.full((seqs * per, kv, page, 4), 0.1, dtype=torch.bfloat16).pin_memory() for _ in "kv")
+    c = coli._GqaCache(kv, 128, 32, page, seqs * per, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), None)
+    table, lens = torch.arange(seqs * per, dtype=torch.int32, device="cuda").view(seqs, per), i32(torch, [n] * seqs)
+    q = torch.randn(seqs, 1, 64, 128, device="cuda")
+
+    def call():
+        out = torch.zeros(seqs, 1, 64, 128, device="cuda")
+        rc = coli._lib.coli_gqa_attend(ctypes.byref(c), coli.COLI_F32, q.data_ptr(), seqs, 1, 64, table.data_ptr(), per, lens.data_ptr(), 0.09,
+                                       0, coli.COLI_F32, out.data_ptr(), None, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        return out
+
+    good = call()
+    coli.sync_check()
+    limit(1)
+    for _ in range(30):                                  # in any of them
+        call()
+    with pytest.raises(coli.ColiError) as e:
+        coli.sync_check()
+    assert e.value.code == coli.COLI_ETIMEOUT
+    limit(0)
+    assert torch.equal(call(), good)
+    coli.sync_check()
+
+
 def test_weighed_step_of_several_sets_wait_runs_out(limit):
     """As above for the pass that adds the weights, which goes over a head's keys once for each 8 of its 16 query rows."""
     torch, coli = setup()
@@ -368,7 +429,8 @@ def test_weighed_step_of_several_sets_wait_runs_out(limit):
     coli.sync_check()
     assert abs(float(w.double().sum()) - seqs * 2 * 64) < 1e-3 * seqs * 2 * 64
     limit(1)
-    call()
+    for _ in range(30):                                  # in any of them
+        call()
     with pytest.raises(coli.ColiError) as e:
         coli.sync_check()
     assert e.value.code == coli.COLI_ETIMEOUT
