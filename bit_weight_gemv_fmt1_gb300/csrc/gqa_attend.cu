@@ -464,11 +464,9 @@ __device__ __forceinline__ uint32_t of_rank(const void *p, int rank) {
     return at;
 }
 
-// Output, lse and what the weights need, of a row of set `set` and its dims d .. d + 3.
-__device__ __forceinline__ void finish(const GqaAttendArgs &a, const AttendPlan &plan, int b, int h, int set, int row, int d, int D, const float4 &o, float m,
-                                       float l) {
-    const int n_kv = a.c.n_kv, G = a.H / n_kv, at = set * kRows + row;
-    if (at >= a.n_q * G) return;
+// Output, lse and what the weights need (`stat`), of a head's row `at` = token * G + head of the group and its dims d .. d + 3.
+template <int D>
+__device__ __forceinline__ void finish(const GqaAttendArgs &a, float2 *stat, int b, int h, int G, int at, int d, const float4 &o, float m, float l) {
     const float inv = l != 0.f ? 1.f / l * kScale : 0.f;
     const long long orow = (long long)(b * (long long)a.n_q + at / G) * a.H + h * G + at % G;
     if (a.out_bf16)
@@ -476,7 +474,7 @@ __device__ __forceinline__ void finish(const GqaAttendArgs &a, const AttendPlan 
     else
         *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + orow * D + d) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     if (d == 0 && a.lse) a.lse[orow] = l != 0.f ? (m + kUp + log2f(l * 0x1p-80f)) * 0.6931471805599453f : -INFINITY;
-    if (d == 0 && a.weigh) plan.stat[((long long)(b * (long long)n_kv + h) * plan.rg + set) * kRows + row] = make_float2(m + kUp, inv);
+    if (d == 0 && a.weigh) *stat = make_float2(m + kUp, inv);
 }
 
 // Moves the references, and what has been added up, if some score of the tile is 8 above: that much is seen without a look at the other
@@ -764,7 +762,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                         if (d == 0) *reinterpret_cast<float2 *>(part + kRows * S::D + 2 * row) = make_float2(m, l);
                         continue;
                     }
-                    finish(a, plan, b, h, set, row, d, S::D, o, m, l);
+                    if (r0 + row < n_rows)
+                        finish<S::D>(a, plan.stat + ((long long)(b * (long long)n_kv + h) * plan.rg + set) * kRows + row, b, h, G, r0 + row, d, o, m, l);
                 }
                 if constexpr (CLUSTER) {
                     cluster_arrive();
@@ -785,7 +784,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                                 l = fmaf(ml1.y, f, l);
                                 o = make_float4(fmaf(x.x, f, o.x), fmaf(x.y, f, o.y), fmaf(x.z, f, o.z), fmaf(x.w, f, o.w));
                             }
-                        finish(a, plan, b, h, set, rank * rows + row, 4 * col, S::D, o, m, l);
+                        if (const int r = rank * rows + row; r0 + r < n_rows)
+                            finish<S::D>(a, plan.stat + ((long long)(b * (long long)n_kv + h) * plan.rg + set) * kRows + r, b, h, G, r0 + r, 4 * col, o, m, l);
                     }
                 }
                 fence_async_smem();
@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <class S, int ROWS>
 __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, const AttendPlan plan) {
     constexpr int kSets = kRows / ROWS;
-    const int n_kv = a.c.n_kv, per = n_kv * plan.rg;
+    const int n_kv = a.c.n_kv, G = a.H / n_kv, n_rows = a.n_q * G, per = n_kv * plan.rg;
     const int place = blockIdx.x / kSets, row0 = (blockIdx.x - place * kSets) * ROWS;
     const int b = place / per, seg = place - b * per, h = seg / plan.rg, set = seg - h * plan.rg;
     pdl_wait();
@@ -888,14 +888,15 @@ __global__ void __launch_bounds__(kJoin) gqa_join_kernel(const GqaAttendArgs a, 
     }
     sum[lot][row][d / 4] = o;
     __syncthreads();
-    if (lot == 0) {
+    const int at = set * kRows + row0 + row;
+    if (lot == 0 && at < n_rows) {
         const float m = s_m[row], l = s_l[row];
 #pragma unroll
         for (int k = 1; k < kSplit; k++) {
             const float4 x = sum[k][row][d / 4];
             o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
         }
-        finish(a, plan, b, h, set, row0 + row, d, S::D, o, m, l);
+        finish<S::D>(a, plan.stat + (long long)place * kRows + row0 + row, b, h, G, at, d, o, m, l);
     }
     pdl_trigger();
 }
