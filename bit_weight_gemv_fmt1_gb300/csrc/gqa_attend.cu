@@ -931,11 +931,12 @@ size_t part_bytes(const GqaAttendArgs &a, int n_cta) {
 // need neither the one nor the other, but leave SMs idle where 8 CTAs a segment do not fill the GPU, and go by the longest sequence: what
 // counts is the rounds of tiles a warp would go through, by the page tables' width, since lengths are known on the device alone.
 // Device time, this way / that: 1x1000 (8 heads) 7.3 / 10.0 us, 4x4000 11.4 / 14.0, 16x500 9.8 / 12.5, at 4 rounds 1x8000 11.9 / 12.5, 32x1000
-// 14.8 / 15.2; at 5 4x10000 17.7 / 17.6, at 6 to 8 8x6000 18.7 / 17.6, 1x16000 16.5 / 14.8.
+// 14.8 / 15.2; at 5 4x10000 17.7 / 17.6, at 6 to 8 8x6000 18.7 / 17.6, 1x16000 16.5 / 14.8.  More segments than CTAs fit at once come one
+// after another, two on an SM beside each other: 48x300 17.7 / 25.5, 100x1000 39.6 / 48.9, 45x165 of 5 tokens (96 heads on 8) 61 / 77.
 int cluster_of(const GqaAttendArgs &a, int n_sm) {
     const long long segments = (long long)a.n_seq * a.c.n_kv * row_groups(a), tiles = (a.longest + kTile - 1) / kTile;
     for (int c = kRows; c; c /= 2)
-        if (segments * c <= 2 * n_sm) return (tiles + c - 1) / c <= kRounds * kWarps ? c : 0;
+        if (segments * c <= 2 * n_sm || c == 1) return (tiles + c - 1) / c <= kRounds * kWarps ? c : 0;
     return 0;
 }
 
