@@ -569,7 +569,8 @@ typedef struct {
  *   out     device [Tq][n_heads][dim], COLI_F32 or COLI_BF16; lse device f32 [Tq][n_heads] or NULL.
  *           Rows of no sequence are left alone.
  * Products have bf16 (f32 inputs: f16) operands, to which the probabilities are rounded, and f32
- * sums; maxima and denominators are f32.  A key or value that a query does not see, of another
+ * sums; maxima and denominators are f32.  f16 probabilities below 2^-21 of a row's largest one are off by up
+ * to 2^-32 of that.  A key or value that a query does not see, of another
  * sequence or its own, may be anything, NaN included.  A NaN or an infinity in a query, or a NaN in a key that
  * it sees, makes its row NaN.
  * Pointers 16-byte aligned (cu, lse: 4); strides in elements, multiples of 8.
