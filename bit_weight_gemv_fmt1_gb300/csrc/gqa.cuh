@@ -80,7 +80,9 @@ struct GqaPrefillArgs {
     float scale;
     void *out;
     float *lse;
-    const int *q_exponent, *exponent;   // f16 inputs made from f32: powers of two of each row of q, of k and of v
+    // f16 inputs made from f32: what takes each row of q back [Tq][heads], and two bf16 factors for each key and its value [H][Tk]
+    const float *q_power;
+    const uint32_t *kv_power;
     int *err;
 };
 

@@ -25,10 +25,16 @@
 // thread, two warps a tile and SM quarter, is slower (384).  1.54 PFLOP/s, 0.80 of the measured bf16 rate; 1x2048 33 us, 6 ragged up
 // to 700 behind 333 cached 46, 24 of up to 301 (D 64) 17.
 //
-// f32 inputs become f16, which keeps 3 bits more than bf16: every row of q times a power of two of its own, k and v times one each,
-// so that the largest magnitudes lie in 2^14 .. 2^15 and all down to 2^-28 of them keep their 11 bits.  P is f16 then too.  The
-// powers come out again in the scores' factor, a thread's own, and with 1 / l.  (bf16 without the powers: twice the error.)  The
-// two launches that make them take 9 us of the 28 of 24 short prompts.
+// f32 inputs become f16, which keeps 3 bits more than bf16: every row (token and head) of q, k and v times a power of two that follows
+// from that row alone, so that what a query does not see cannot change its result.  Rows of ordinary size (the largest magnitude of a
+// key in 2^-5 .. 2^11, of a value in 2^-4 .. 2^6) share one; others get the one that takes their largest magnitude to 2^14 .. 2^15.  The
+// powers come out again by a factor of the scores, a thread's own for q, and two factors per key, which every softmax warp copies to
+// shared memory a tile ahead: the scores', and that of a key's weight in P, which is f16 then, too.  With U the largest weight times
+// factor of a row so far, P is held times a power of two B that keeps B U in 2^7 .. 2^15; O is rescaled when B moves.  A tile of
+// ordinary rows in a warp whose B are the usual one needs neither multiplication, and the bits are the same: 1x8192, 32 heads on 8, 457 us
+// (D 64: 365), with rows of other sizes 850 (715).  Exponents rather than tf32 operands: those would be twice the bytes in shared memory, which
+// two query tiles of 128 dims fill, and twice the products' cycles.  24 short prompts 24 us, one launch of
+// which makes f16 (7.7 us by the profiler, its inputs from DRAM).
 //
 // Keys past a causal row's limit are masked by selection; value rows past the
 // sequence's end belong to its neighbours and are zeroed in shared memory.
@@ -45,6 +51,14 @@ namespace {
 
 constexpr int kKeys = 5, kValues = 4;    // ring slots: key blocks of 64 dims, value halves of 64 keys
 constexpr uint32_t kOut = 32 * 64;       // bytes of a warp's outputs on their way: 64 of each row
+constexpr float kLog2e = 1.4426950408889634f;
+// f16 inputs made from f32, log2 of their powers: those of ordinary keys and values, and shifts of the factors that are kept, so that these
+// and their products with scores (up to 2^37) and weights (up to 2^15) are numbers for rows of any size.
+constexpr int kKeyPower = 4, kValuePower = 9, kKeyShift = 32, kValueShift = 4;
+constexpr int kUp = 7;                   // log2 of what f16 weights are held times
+constexpr int kUsual = kValueShift + kValuePower, kMostUp = 126;   // log2 of B for ordinary values, and at the most
+// A key's factors are two bf16 in a word, its scores' in the low half: powers of two, of ordinary rows these.
+constexpr uint32_t kPlain = (uint32_t)(127 - kUsual) << 23 | (uint32_t)(127 - kKeyShift) << 7;
 
 struct Shared {
     uint64_t q_full[2], q_empty[2], k_full[kKeys], k_empty[kKeys], v_full[kValues], v_empty[kValues], s_full[2], p_full[2][2], o_full[2],
@@ -56,7 +70,7 @@ struct Shared {
     int abort;
 };
 
-// (x, y) = (x, y) * f + m, and s += (x, y): two f32 operations in one instruction.
+// (x, y) = (x, y) * f + m, s += (x, y), and products: two f32 operations in one instruction.
 __device__ __forceinline__ void fma2(float &x, float &y, uint32_t u, uint32_t v, float f, float m) {
     asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 d, {%5, %5};\n fma.rn.f32x2 a, a, b, d;\n"
         " mov.b64 {%0, %1}, a;\n}"
@@ -68,12 +82,19 @@ __device__ __forceinline__ void add2(float &s, float &t, float x, float y) {
         : "+f"(s), "+f"(t)
         : "f"(x), "f"(y));
 }
+__device__ __forceinline__ void mul2(float &x, float &y, float u, float v) {
+    asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
+        : "+f"(x), "+f"(y)
+        : "f"(u), "f"(v));
+}
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-// x 2^e for the exponents that f16_exponent gives: in two factors, since 2^e may pass the range.
-__device__ __forceinline__ float scaled(float x, int e) { return x * exp2i(e / 2) * exp2i(e - e / 2); }
-// The power of two that takes a largest magnitude to 2^14 .. 2^15.
-__device__ __forceinline__ int f16_exponent(uint32_t bits) { return bits ? 14 - ilogbf(__uint_as_float(bits)) : 0; }
+// 4 bytes from global to shared memory without a register, zeros instead where `some` is false; and the wait for all such copies of this
+// thread.
+__device__ __forceinline__ void copy4(uint32_t *dst, const uint32_t *src, bool some) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(some ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // A box of a 3-D tensor map, as tma_box.
 __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
@@ -98,16 +119,18 @@ __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466
 // 8192 keys then takes 53 ms, which its unit's limit of waits (2.5 s) leaves room for.
 template <int D, bool F16>
 __device__ __noinline__ void repair(const GqaPrefillArgs &a, bool mine, int orow, int token, int q_head, int head, int krow, int seen, int end,
-                                    float f, float m, float inv, int ev) {
+                                    float f, float m, float inv) {
     constexpr int kCols = D / 32;            // columns of a lane
     const int lane = threadIdx.x & 31;
     const uint16_t *k = reinterpret_cast<const uint16_t *>(a.k) + krow * a.k_stride + head * D;
     const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v) + krow * a.v_stride + head * D + lane * kCols;
+    const uint32_t *factors = F16 ? a.kv_power + ((long long)head * a.Tk + krow) : nullptr;
     auto value = [&](int j, float (&x)[kCols]) {
+        const float by = F16 ? bf16x2_f32x2(factors[j]).y : 1.f;   // times 2^kValueShift
 #pragma unroll
         for (int c = 0; c < kCols; c += 2) {
             const float2 two = operands<F16>(*reinterpret_cast<const uint32_t *>(v + j * a.v_stride + c));
-            x[c] = two.x, x[c + 1] = two.y;
+            x[c] = F16 ? two.x * by * exp2i(kValueShift) : two.x, x[c + 1] = F16 ? two.y * by * exp2i(kValueShift) : two.y;
         }
     };
     for (uint32_t left = __ballot_sync(0xffffffffu, mine); left; left &= left - 1) {
@@ -143,7 +166,9 @@ __device__ __noinline__ void repair(const GqaPrefillArgs &a, bool mine, int orow
                         s = fmaf(y.y, z.y, fmaf(y.x, z.x, s));
                     }
                 }
-                p = ex2(fmaf(a.scale < 0.f ? -s : s, f1, -m1));
+                if (a.scale < 0.f) s = -s;
+                if constexpr (F16) s *= bf16x2_f32x2(factors[j0 + lane]).x;
+                p = ex2(fmaf(s, f1, -m1)) * inv1;
             }
             bool open = false;               // some column is not NaN yet
             for (int j = 0; j < 32; j += 8) {
@@ -168,7 +193,7 @@ __device__ __noinline__ void repair(const GqaPrefillArgs &a, bool mine, int orow
 #pragma unroll
         for (int c = 0; c < kCols; c++)
             if (bad[c]) {
-                const float y = F16 ? scaled(sum[c] * inv1, -ev) : sum[c] * inv1;
+                const float y = sum[c];
                 const long long at = (long long)to * D + lane * kCols + c;
                 if (a.out_bf16) reinterpret_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(y);
                 else reinterpret_cast<float *>(a.out)[at] = y;
@@ -246,11 +271,11 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), S = lanes + x * 128, O = lanes + 256 + x * D;
         // a negative scale turns the scores' sign; a factor of zero must still send masked scores (-inf) to -inf
         const bool negative = a.scale < 0.f;
-        const float scale2 = fabsf(a.scale) * 1.4426950408889634f;
-        // f16 weights are held times 2^7, so that they reach 2^15 (kGrow above the reference): one keeps its 11 bits down to 2^-21 of the
-        // largest score's and loses no more than 2^-32 of that below.  Without, 20000 keys e^-17 below another lost 0.4 of themselves.
-        constexpr float kUp = F16 ? 7.f : 0.f;
-        const int ek = F16 ? a.exponent[0] : 0, ev = F16 ? a.exponent[1] : 0;
+        const float scale2 = fabsf(a.scale) * kLog2e;
+        // f16 inputs: the factors of a tile's keys, [parity of the tile][key], in the warp's place for outputs
+        uint8_t *stage = sm + o_off + warp * kOut;
+        uint32_t(*power)[kRows] = reinterpret_cast<uint32_t(*)[kRows]>(stage);
+        static_assert(sizeof(uint32_t[2][kRows]) <= kOut, "two tiles' factors fit");
         const int tok = t / a.group, g = t - tok * a.group;  // this thread's row: token of the tile, head of the group
         int tiles = 0, s_tiles = 0, outs = 0;            // key tiles, this tile's score tiles and outputs so far
         for (int r = 0;; r++) {
@@ -260,11 +285,32 @@ __global__ void __launch_bounds__(384, 1)
             const int limit = min(row + nk - u.nq + 1, nk);     // keys this row sees
             const int all = min(first + nk - u.nq + 1, nk);     // keys every row of the tile sees
             const long long orow = tok < a.tokens && row < u.nq ? (long long)(u.qrow + row) * a.heads + u.head * a.group + g : -1;
-            const int eq = F16 && orow >= 0 ? a.q_exponent[orow] : 0;
-            const float f = fmaxf(F16 ? scaled(scaled(scale2, -eq), -ek) : scale2, 1e-37f);
+            const float f = fmaxf(F16 ? scale2 * (orow >= 0 ? a.q_power[orow] : 0.f) * exp2i(-kKeyPower) : scale2, 1e-37f);
+            auto fetch = [&](int j) {                    // whole warp
+                const uint32_t *at = a.kv_power + ((long long)u.head * a.Tk + u.krow);
+#pragma unroll
+                for (int i = 0; i < kRows; i += 32) {
+                    const int key = j * kRows + i + lane;
+                    copy4(&power[j & 1][i + lane], at + (key < nk ? key : 0), key < nk);
+                }
+            };
+            if (F16 && nt > 0) fetch(0);
             float m = kNone;
+            float share = 0.f;                           // U
+            int up = kUsual;                             // log2 B
             float l4[4] = {0.f, 0.f, 0.f, 0.f};
             for (int j = 0; j < nt; j++) {
+                bool plain = true;                       // the tile's keys and values are ordinary rows
+                if constexpr (F16) {
+                    copies_done();
+                    __syncwarp();                        // every lane's have come, and the last tile's factors are read
+#pragma unroll
+                    for (int i = 0; i < kRows; i += 32)
+                        plain = plain && (j * kRows + i + lane >= nk || power[j & 1][i + lane] == kPlain);
+                    plain = __all_sync(0xffffffffu, plain && up == kUsual);
+                    if (j + 1 < nt) fetch(j + 1);
+                }
+                const float ft = F16 && !plain ? f * exp2i(kKeyShift) : f;
                 wait(&s.s_full[x], s_tiles++ & 1);
                 tc_after_sync();
                 const int k0 = j * kRows;
@@ -278,6 +324,18 @@ __global__ void __launch_bounds__(384, 1)
                 if (negative)
 #pragma unroll
                     for (int c = 0; c < kRows; c++) v[c] ^= 0x80000000u;
+                if (F16 && !plain)
+#pragma unroll
+                    for (int c = 0; c < kRows; c += 4) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(&power[j & 1][c]);
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int k = 0; k < 4; k += 2) {
+                            float y = __uint_as_float(v[c + k]), z = __uint_as_float(v[c + k + 1]);
+                            mul2(y, z, bf16x2_f32x2(ws[k]).x, bf16x2_f32x2(ws[k + 1]).x);
+                            v[c + k] = __float_as_uint(y), v[c + k + 1] = __float_as_uint(z);
+                        }
+                    }
                 // Rows of a warp see ever more keys: blocks of 32 keys before `least` are seen by all, from `most` on by none.
                 const int least = full ? kRows : __shfl_sync(0xffffffffu, seen, 0), most = full ? kRows : __shfl_sync(0xffffffffu, seen, 31);
                 if (!full)
@@ -296,24 +354,27 @@ __global__ void __launch_bounds__(384, 1)
                     for (int k = 0; k < 4; k++) t4[k] = max3(t4[k], __uint_as_float(v[c + k]), __uint_as_float(v[c + 4 + k]));
 #pragma unroll
                 for (int k = 0; k < 4; k++) t4[k] = fmaxf(t4[k], __uint_as_float(v[kRows - 4 + k]));
-                const float now = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f;
+                const float now = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * ft;
                 const bool move = now > m + kGrow;
+                auto rescale = [&](float r) {            // O times r; whole warp
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 8) {
+                        uint32_t o[8];
+                        tmem_ld(O + c0, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 8; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * r);
+                        tmem_st(O + c0, o);
+                    }
+                };
+                float r = 1.f;
                 if (__any_sync(0xffffffffu, move)) {
-                    const float r = move ? ex2(m - now) : 1.f;
+                    r = move ? ex2(m - now) : 1.f;
+                    if (F16 && r < 0x1p-116f) r = 0.f;   // what it leaves of U can be held times B again
                     if (move) m = now;
 #pragma unroll
                     for (int k = 0; k < 4; k++) l4[k] *= r;
-                    if (j > 0) {
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 8) {
-                            uint32_t o[8];
-                            tmem_ld(O + c0, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int c = 0; c < 8; c++) o[c] = __float_as_uint(__uint_as_float(o[c]) * r);
-                            tmem_st(O + c0, o);
-                        }
-                    }
+                    if (j > 0) rescale(r);
                 }
                 if (k0 + kRows > nk) {
                     // value rows of other sequences may hold anything, and 0 * NaN is NaN
@@ -327,7 +388,48 @@ __global__ void __launch_bounds__(384, 1)
                                 *reinterpret_cast<uint4 *>(sm + v_off + slot * kHalf + k * (kBlk / 2) + (t & 63) * 128 + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
                     fence_async_smem();
                 }
-                const float m0 = kUp - m;
+                const float m0 = (F16 ? (float)kUp : 0.f) - m;
+                if constexpr (F16) share *= r;
+                if (F16 && plain) {
+                    share = fmaxf(share, ex2(now + m0) * exp2i(-kUsual));
+                } else if constexpr (F16) {
+                    // weights, times their keys' factors, times B
+                    float u4[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int c0 = 0; c0 < kRows; c0 += 32)
+                        if (c0 < most)
+#pragma unroll
+                            for (int c = c0; c < c0 + 32; c += 4) {
+                                const uint4 w = *reinterpret_cast<const uint4 *>(&power[j & 1][c]);
+                                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                                float e[4];
+                                fma2(e[0], e[1], v[c], v[c + 1], ft, m0);
+                                fma2(e[2], e[3], v[c + 2], v[c + 3], ft, m0);
+#pragma unroll
+                                for (int k = 0; k < 4; k++) e[k] = ex2(e[k]);
+                                add2(l4[0], l4[1], e[0], e[1]);
+                                add2(l4[2], l4[3], e[2], e[3]);
+#pragma unroll
+                                for (int k = 0; k < 4; k += 2) {
+                                    mul2(e[k], e[k + 1], bf16x2_f32x2(ws[k]).y, bf16x2_f32x2(ws[k + 1]).y);
+                                    u4[k / 2] = max3(u4[k / 2], e[k], e[k + 1]);
+                                    v[c + k] = __float_as_uint(e[k]), v[c + k + 1] = __float_as_uint(e[k + 1]);
+                                }
+                            }
+                    share = max3(share, u4[0], u4[1]);
+                    const float held = share * exp2i(up);
+                    // an exponent field of 0 gives more than kMostUp, the largest one (2^15 times 2^109) -114
+                    const int next = share > 0.f && (held > 32768.f || held < 128.f) ? min(kMostUp, 10 + 127 - (int)(__float_as_uint(share) >> 23)) : up;
+                    if (__any_sync(0xffffffffu, next != up) && j > 0) rescale(exp2i(max(-126, min(next - up, 126))));   // past that O is 0, or next to it
+                    up = next;
+                    const float by = exp2i(up);
+#pragma unroll
+                    for (int c = 0; c < kRows; c += 2) {
+                        float y = __uint_as_float(v[c]), z = __uint_as_float(v[c + 1]);
+                        mul2(y, z, by, by);
+                        v[c] = __float_as_uint(y), v[c + 1] = __float_as_uint(z);
+                    }
+                }
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
 #pragma unroll
@@ -342,9 +444,13 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
                             float x, y;
-                            fma2(x, y, v[c0 + c], v[c0 + c + 1], f, m0);
-                            x = ex2(x), y = ex2(y);
-                            add2(l4[c & 2], l4[(c & 2) + 1], x, y);
+                            if (F16 && !plain) {
+                                x = __uint_as_float(v[c0 + c]), y = __uint_as_float(v[c0 + c + 1]);
+                            } else {
+                                fma2(x, y, v[c0 + c], v[c0 + c + 1], f, m0);
+                                x = ex2(x), y = ex2(y);
+                                add2(l4[c & 2], l4[(c & 2) + 1], x, y);
+                            }
                             p[c / 2] = F16 ? pack_f16(x, y) : pack_bf16(x, y);
                         }
                         tmem_st(S + c0 / 2, p);              // over scores that have been read
@@ -364,7 +470,7 @@ __global__ void __launch_bounds__(384, 1)
             }
             // Rows go out through shared memory, 64 bytes of each at a time: 4 threads then write a row's piece together, where a thread's
             // own 16 bytes of 32 different rows cost 2.5 us a unit.
-            uint8_t *stage = sm + o_off + warp * kOut;
+            if constexpr (F16) __syncwarp();             // the last tile's factors are read
             int dst[4];                                  // the output rows of this thread's pieces
 #pragma unroll
             for (int i = 0; i < 4; i++) dst[i] = __shfl_sync(0xffffffffu, (int)orow, 8 * i + (lane >> 2));
@@ -384,6 +490,7 @@ __global__ void __launch_bounds__(384, 1)
                 __syncwarp();
             };
             const uint32_t some = limit > 0 ? 0xFFFFFFFFu : 0u;   // a row without keys beside ones that have some: 0 times their values may be NaN
+            const float down = exp2i(kValueShift - up);  // what P and the values are held times, taken back
             float odd = 0.f;                             // NaN once an output is not finite
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
@@ -396,7 +503,7 @@ __global__ void __launch_bounds__(384, 1)
                     for (int c = 0; c < 32; c++) o[c] = 0u;
                 }
 #pragma unroll
-                for (int c = 0; c < 32; c++) o[c] = __float_as_uint(F16 ? scaled(__uint_as_float(o[c]) * inv, -ev) : __uint_as_float(o[c]) * inv) & some;
+                for (int c = 0; c < 32; c++) o[c] = __float_as_uint(F16 ? __uint_as_float(o[c]) * inv * down : __uint_as_float(o[c]) * inv) & some;
 #pragma unroll
                 for (int c = 0; c < 32; c++) odd = fmaf(__uint_as_float(o[c]), 0.f, odd);
                 uint32_t w[16];
@@ -416,8 +523,8 @@ __global__ void __launch_bounds__(384, 1)
             const int end = min(nt * kRows, nk);
             const bool again = odd != odd && orow >= 0 && limit > 0 && limit < end;
             if (__any_sync(0xffffffffu, again))
-                repair<D, F16>(a, again, (int)orow, u.qrow + row, u.head * a.group + g, u.head, u.krow, limit, end, f, m - kUp, inv, ev);
-            if (orow >= 0 && a.lse) a.lse[orow] = l != 0.f ? (m - kUp + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                repair<D, F16>(a, again, (int)orow, u.qrow + row, u.head * a.group + g, u.head, u.krow, limit, end, F16 ? f * exp2i(kKeyShift) : f, F16 ? m - kUp : m, inv);
+            if (orow >= 0 && a.lse) a.lse[orow] = l != 0.f ? (m - (F16 ? kUp : 0) + log2f(l)) * 0.6931471805599453f : -INFINITY;
             tc_before_sync();
         }
     } else if (warp == 8) {
@@ -586,118 +693,62 @@ cudaError_t query_map(const GqaPrefillArgs &a, CUtensorMap *out) {
                : cudaErrorInvalidValue;
 }
 
-// f32 -> f16, first step: each row of q times a power of two of its own (whose exponent goes to q_exponent), and the largest finite
-// magnitudes of k and v, one for each of the first `ranges` CTAs.  One thread per 8 elements.
+// f32 -> f16: each row of q, k and v times a power of two of its own, whose factor goes to q_power (by rows) or, by heads and tokens,
+// to kv_power.  Rows of q, then of k, then of v; one thread per 8 elements.
 template <int D>
-__global__ void __launch_bounds__(256) gqa_round_q_kernel(const GqaPrefillArgs a, __half *q16, int *q_exponent, uint2 *range, int ranges) {
+__global__ void __launch_bounds__(256) gqa_round_kernel(const GqaPrefillArgs a, __half *q16, __half *k16, __half *v16, float *q_power,
+                                                        __nv_bfloat16 *kv_power) {
     constexpr int kUnits = D / 8;
-    __shared__ uint32_t most[2];
-    pdl_wait();
     auto finite = [](float x) {
         const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
         return b < 0x7F800000u ? b : 0u;
     };
-    auto largest = [&](const float4 &x, const float4 &y) {
-        return max(max(max(finite(x.x), finite(x.y)), max(finite(x.z), finite(x.w))), max(max(finite(y.x), finite(y.y)), max(finite(y.z), finite(y.w))));
-    };
-    if ((int)blockIdx.x < ranges) {
-        if (threadIdx.x < 2) most[threadIdx.x] = 0;
-        __syncthreads();
-        const long long units = (long long)a.Tk * a.H * kUnits;
-        const int upt = a.H * kUnits;
-        uint32_t m[2] = {0, 0};
-        for (long long i = blockIdx.x * 256LL + threadIdx.x; i < units; i += ranges * 256LL) {
-            const long long t = i / upt;
-            const int u = (int)(i - t * upt);
-            const float *k = (const float *)a.k + t * a.k_stride + 8 * u, *v = (const float *)a.v + t * a.v_stride + 8 * u;
-            m[0] = max(m[0], largest(*reinterpret_cast<const float4 *>(k), *reinterpret_cast<const float4 *>(k + 4)));
-            m[1] = max(m[1], largest(*reinterpret_cast<const float4 *>(v), *reinterpret_cast<const float4 *>(v + 4)));
-        }
-        for (int j = 0; j < 2; j++) {
-            m[j] = __reduce_max_sync(0xffffffffu, m[j]);
-            if ((threadIdx.x & 31) == 0) atomicMax(&most[j], m[j]);
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) range[blockIdx.x] = make_uint2(most[0], most[1]);
-    }
-    const long long rows = (long long)a.Tq * a.heads;
+    const long long n_q = (long long)a.Tq * a.heads, n_k = (long long)a.Tk * a.H, rows = n_q + 2 * n_k;
     const int u = threadIdx.x % kUnits;
+    // Factors are numbers, at 2^-126 the smallest: rows that would need a smaller one get a power that is less.
+    const int most_q = min(126, 118 + max(-230, min(8, ilogbf(a.scale * kLog2e)))), most_k = 126 + kKeyPower - kKeyShift, most_v = 126 - kValueShift;
+    pdl_wait();
     for (long long r0 = blockIdx.x * (256LL / kUnits); r0 < rows; r0 += gridDim.x * (256LL / kUnits)) {   // the CTA stays together
         const long long r = r0 + threadIdx.x / kUnits;
+        const bool query = r < n_q, value = r >= n_q + n_k;
+        const uint32_t i = (uint32_t)(query ? r : value ? r - n_q - n_k : r - n_q), heads = query ? a.heads : a.H, t = i / heads, h = i - t * heads;   // rows of each < 2^31
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
         if (r < rows) {
-            const long long t = r / a.heads;
-            const float *q = (const float *)a.q + t * a.q_stride + (r - t * a.heads) * D + 8 * u;
-            x = *reinterpret_cast<const float4 *>(q);
-            y = *reinterpret_cast<const float4 *>(q + 4);
+            const float *p = (const float *)(query ? a.q : value ? a.v : a.k) + t * (query ? a.q_stride : value ? a.v_stride : a.k_stride) + h * D + 8 * u;
+            x = *reinterpret_cast<const float4 *>(p);
+            y = *reinterpret_cast<const float4 *>(p + 4);
         }
-        uint32_t m = largest(x, y);
+        uint32_t m = max(max(max(finite(x.x), finite(x.y)), max(finite(x.z), finite(x.w))), max(max(finite(y.x), finite(y.y)), max(finite(y.z), finite(y.w))));
 #pragma unroll
         for (int o = 1; o < kUnits; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int e = f16_exponent(m);
         if (r >= rows) continue;
-        if (u == 0) q_exponent[r] = e;
-        reinterpret_cast<uint4 *>(q16)[r * kUnits + u] = make_uint4(pack_f16(scaled(x.x, e), scaled(x.y, e)), pack_f16(scaled(x.z, e), scaled(x.w, e)),
-                                                                  pack_f16(scaled(y.x, e), scaled(y.y, e)), pack_f16(scaled(y.z, e), scaled(y.w, e)));
-    }
-    pdl_trigger();
-}
-// Second step: k and v, each times one power of two.
-template <int D>
-__global__ void __launch_bounds__(256) gqa_round_kv_kernel(const GqaPrefillArgs a, __half *k16, __half *v16, int *exponent, const uint2 *range, int ranges) {
-    constexpr int kUnits = D / 8;
-    __shared__ uint32_t most[2];
-    const int upt = a.H * kUnits;
-    const long long units = (long long)a.Tk * upt, step = gridDim.x * 256LL;
-    float4 x, y;
-    auto load = [&](long long i) {
-        const bool value = i >= units;
-        const long long j = value ? i - units : i, t = j / upt;
-        const float *p = (const float *)(value ? a.v : a.k) + t * (value ? a.v_stride : a.k_stride) + 8 * (j - t * upt);
-        x = *reinterpret_cast<const float4 *>(p);
-        y = *reinterpret_cast<const float4 *>(p + 4);
-    };
-    pdl_wait();
-    // the first elements are on their way while the largest magnitudes are looked up
-    long long i = blockIdx.x * 256LL + threadIdx.x;
-    if (i < 2 * units) load(i);
-    if (threadIdx.x < 2) most[threadIdx.x] = 0;
-    __syncthreads();
-    uint2 m = make_uint2(0, 0);
-    for (int r = threadIdx.x; r < ranges; r += 256) m = make_uint2(max(m.x, range[r].x), max(m.y, range[r].y));
-    m = make_uint2(__reduce_max_sync(0xffffffffu, m.x), __reduce_max_sync(0xffffffffu, m.y));
-    if ((threadIdx.x & 31) == 0) {
-        atomicMax(&most[0], m.x);
-        atomicMax(&most[1], m.y);
-    }
-    __syncthreads();
-    const int ek = f16_exponent(most[0]), ev = f16_exponent(most[1]);
-    if (blockIdx.x == 0 && threadIdx.x == 0) exponent[0] = ek, exponent[1] = ev;
-    for (; i < 2 * units; i += step) {
-        const bool value = i >= units;
-        const int e = value ? ev : ek;
-        reinterpret_cast<uint4 *>(value ? v16 : k16)[value ? i - units : i] =
-            make_uint4(pack_f16(scaled(x.x, e), scaled(x.y, e)), pack_f16(scaled(x.z, e), scaled(x.w, e)),
-                       pack_f16(scaled(y.x, e), scaled(y.y, e)), pack_f16(scaled(y.z, e), scaled(y.w, e)));
-        if (i + step < 2 * units) load(i + step);
+        const int size = m ? ilogbf(__uint_as_float(m)) : 0;
+        int e = min(14 - size, query ? most_q : value ? most_v : most_k);
+        if (!query && !value && size >= -5 && size <= 10) e = kKeyPower;
+        if (value && size >= -4 && size <= 5) e = kValuePower;
+        const float by = query && a.scale == 0.f ? 0.f : exp2i(e);
+        if (u == 0) {
+            if (query) q_power[i] = exp2i(-e);
+            else kv_power[2 * (h * (long long)a.Tk + t) + value] = __float2bfloat16_rn(exp2i(value ? -kValueShift - e : kKeyPower - kKeyShift - e));
+        }
+        reinterpret_cast<uint4 *>(query ? q16 : value ? v16 : k16)[i * (long long)kUnits + u] =
+            make_uint4(pack_f16(x.x * by, x.y * by), pack_f16(x.z * by, x.w * by), pack_f16(y.x * by, y.y * by), pack_f16(y.z * by, y.w * by));
     }
     pdl_trigger();
 }
 
 // What a call with f32 inputs keeps in scratch.
 struct Rounded {
-    size_t q, k, v, q_exponent, exponent, range, end;
+    size_t q, k, v, q_power, kv_power, end;
 };
-constexpr int kRanges = 608;             // CTAs that look for the largest magnitudes, at most
 Rounded rounded(const GqaPrefillArgs &a) {
     Rounded z;
     z.q = 0;
     z.k = z.q + round256((size_t)a.Tq * a.heads * a.dim * 2);
     z.v = z.k + round256((size_t)a.Tk * a.H * a.dim * 2);
-    z.q_exponent = z.v + round256((size_t)a.Tk * a.H * a.dim * 2);
-    z.exponent = z.q_exponent + round256((size_t)a.Tq * a.heads * sizeof(int));
-    z.range = z.exponent + 256;
-    z.end = z.range + round256(kRanges * sizeof(uint2));
+    z.q_power = z.v + round256((size_t)a.Tk * a.H * a.dim * 2);
+    z.kv_power = z.q_power + round256((size_t)a.Tq * a.heads * sizeof(float));
+    z.end = z.kv_power + round256((size_t)a.Tk * a.H * sizeof(uint32_t));
     return z;
 }
 
@@ -705,23 +756,18 @@ template <int D>
 cudaError_t round_inputs(GqaPrefillArgs &a, const DevInfo &d, cudaStream_t st, int *n_launch) {
     const Rounded z = rounded(a);
     char *at = (char *)d.scratch;
-    const long long q_ctas = ((long long)a.Tq * a.heads * (D / 8) + 255) / 256, kv_ctas = ((long long)a.Tk * a.H * (D / 8) + 255) / 256;
-    const int ranges = (int)std::max(1LL, std::min((long long)kRanges, kv_ctas));
-    auto grid = [&](long long n) { return dim3((unsigned)std::max(1LL, std::min(n, 16LL * d.n_sm))); };
-    if (cudaError_t e = launch_pdl(gqa_round_q_kernel<D>, grid(std::max(q_ctas, (long long)ranges)), dim3(256), 0, st, a, (__half *)(at + z.q),
-                                   (int *)(at + z.q_exponent), (uint2 *)(at + z.range), ranges))
+    const long long rows = (long long)a.Tq * a.heads + 2LL * a.Tk * a.H, ctas = (rows * (D / 8) + 255) / 256;
+    if (cudaError_t e = launch_pdl(gqa_round_kernel<D>, dim3((unsigned)std::min(ctas, 16LL * d.n_sm)), dim3(256), 0, st, a, (__half *)(at + z.q),
+                                   (__half *)(at + z.k), (__half *)(at + z.v), (float *)(at + z.q_power), (__nv_bfloat16 *)(at + z.kv_power)))
         return e;
-    if (cudaError_t e = launch_pdl(gqa_round_kv_kernel<D>, grid(2 * kv_ctas), dim3(256), 0, st, a, (__half *)(at + z.k), (__half *)(at + z.v),
-                                   (int *)(at + z.exponent), (const uint2 *)(at + z.range), ranges))
-        return e;
-    *n_launch += 2;
+    ++*n_launch;
     a.q = at + z.q;
     a.k = at + z.k;
     a.v = at + z.v;
     a.q_stride = a.heads * a.dim;
     a.k_stride = a.v_stride = a.H * a.dim;
-    a.q_exponent = (const int *)(at + z.q_exponent);
-    a.exponent = (const int *)(at + z.exponent);
+    a.q_power = (const float *)(at + z.q_power);
+    a.kv_power = (const uint32_t *)(at + z.kv_power);
     return cudaSuccess;
 }
 

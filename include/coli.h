@@ -563,16 +563,17 @@ typedef struct {
  *   k, v    device [Tk][n_kv][dim], token strides k_stride, v_stride (they may be
  *           parts of one row).
  *   dtype   COLI_BF16, or COLI_F32: the three are then rounded to f16 in scratch first, each row
- *           (token and head) of q times a power of two, k and v times one each, so that any range of
- *           magnitudes fits; elements below 2^-28 of the largest lose bits.
+ *           (token and head) times a power of two that depends on that row alone, so that any range of
+ *           magnitudes fits; elements below 2^-13 of their row's largest are off by up to 2^-24 of that.
  *   cu_q, cu_k      device int32 [n_seq + 1], ascending from 0 to Tq / Tk.
  *   out     device [Tq][n_heads][dim], COLI_F32 or COLI_BF16; lse device f32 [Tq][n_heads] or NULL.
  *           Rows of no sequence are left alone.
  * Products have bf16 (f32 inputs: f16) operands, to which the probabilities are rounded, and f32
- * sums; maxima and denominators are f32.  f16 probabilities below 2^-21 of a row's largest one are off by up
- * to 2^-32 of that.  A key or value that a query does not see, of another
- * sequence or its own, may be anything, NaN included.  A NaN or an infinity in a query, or a NaN in a key that
- * it sees, makes its row NaN.
+ * sums; maxima and denominators are f32.  f16 probabilities below 2^-21 of a query's largest one are off by
+ * up to 2^-32 of that (beside values whose row's largest magnitude lies outside 2^-4 .. 2^6, a probability counts
+ * times that magnitude, or 2^6, and is off by up to 2^-31 of the largest such product).  A key or value that a
+ * query does not see, of another sequence or its own, may be anything, NaN included; what is finite there changes
+ * no bit of the output.  A NaN or an infinity in a query, or a NaN in a key that it sees, makes its row NaN.
  * Pointers 16-byte aligned (cu, lse: 4); strides in elements, multiples of 8.
  * dim 64 or 128; n_heads a multiple of n_kv, n_heads / n_kv <= 128.  Tq, Tk >= 0, n_seq >= 0,
  * 1 <= n_heads <= 1024.  Offsets outside [0, Tq] / [0, Tk] or descending are
