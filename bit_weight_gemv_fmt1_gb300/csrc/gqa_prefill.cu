@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(384, 1)
             }
             tiles += u.n;
             const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
-            const float inv = l != 0.f ? 1.f / l : 0.f;
+            // no weight at all: a row without keys, or one whose scores are all -infinity, which is NaN
+            const float none = limit > 0 ? __uint_as_float(0x7FC00000u) : 0.f, inv = l != 0.f ? 1.f / l : none;
             if (nt > 0) {
                 wait(&s.o_full[x], outs++ & 1);
                 tc_after_sync();
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(384, 1)
             const bool again = odd != odd && orow >= 0 && limit > 0 && limit < end;
             if (__any_sync(0xffffffffu, again))
                 repair<D, F16>(a, again, (int)orow, u.qrow + row, u.head * a.group + g, u.head, u.krow, limit, end, F16 ? f * exp2i(kKeyShift) : f, F16 ? m - kUp : m, inv);
-            if (orow >= 0 && a.lse) a.lse[orow] = l != 0.f ? (m - (F16 ? kUp : 0) + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            if (orow >= 0 && a.lse) a.lse[orow] = l != 0.f ? (m - (F16 ? kUp : 0) + log2f(l)) * 0.6931471805599453f : none - INFINITY;
             tc_before_sync();
         }
     } else if (warp == 8) {

@@ -573,7 +573,8 @@ typedef struct {
  * up to 2^-32 of that (beside values whose row's largest magnitude lies outside 2^-4 .. 2^6, a probability counts
  * times that magnitude, or 2^6, and is off by up to 2^-31 of the largest such product).  A key or value that a
  * query does not see, of another sequence or its own, may be anything, NaN included; what is finite there changes
- * no bit of the output.  A NaN or an infinity in a query, or a NaN in a key that it sees, makes its row NaN.
+ * no bit of the output.  A NaN or an infinity in a query, a NaN in a key that it sees, or scores that are
+ * all -infinity make its row NaN.
  * Pointers 16-byte aligned (cu, lse: 4); strides in elements, multiples of 8.
  * dim 64 or 128; n_heads a multiple of n_kv, n_heads / n_kv <= 128.  Tq, Tk >= 0, n_seq >= 0,
  * 1 <= n_heads <= 1024.  Offsets outside [0, Tq] / [0, Tk] or descending are
