@@ -41,6 +41,11 @@ int check_stride(long long stride, int T, int heads, int dim, const char *name) 
     return COLI_OK;
 }
 
+bool overlap(const void *a, int64_t bytes_a, const void *b, int64_t bytes_b) {
+    const char *x = (const char *)a, *y = (const char *)b;
+    return x < y + bytes_b && y < x + bytes_a;
+}
+
 int append(const coli_gqa_cache *cache, int dtype, const void *k, int64_t k_stride, const void *v, int64_t v_stride, int T,
            const int64_t *slots, void *stream) {
     clear_last_error();
@@ -129,6 +134,11 @@ int attend(const coli_gqa_cache *cache, int dtype_q, const void *q, int n_seq, i
         if (int rc = need(out, 16, "out")) return rc;
         if (lse)
             if (int rc = need(lse, 4, "lse")) return rc;
+        // A segment's queries are read before its outputs are written, but not before other segments', and again for the weights.
+        const int64_t rows = (int64_t)n_seq * n_q * H, bytes_q = rows * a.c.dim * (dtype_q == COLI_BF16 ? 2 : 4);
+        if (overlap(out, rows * a.c.dim * (dtype_out == COLI_BF16 ? 2 : 4), q, bytes_q) && (weigh || out != q || dtype_out != dtype_q))
+            return bad(COLI_EINVAL, "out may be q itself, of its type and without weigh, and must not overlap it otherwise");
+        if (lse && overlap(lse, rows * 4, q, bytes_q)) return bad(COLI_EINVAL, "lse must not overlap q");
     }
     if (int rc = injected_gate()) return rc;
     if (!n_seq) return COLI_OK;

@@ -567,7 +567,7 @@ typedef struct {
  *           magnitudes fits; elements below 2^-13 of their row's largest are off by up to 2^-24 of that.
  *   cu_q, cu_k      device int32 [n_seq + 1], ascending from 0 to Tq / Tk.
  *   out     device [Tq][n_heads][dim], COLI_F32 or COLI_BF16; lse device f32 [Tq][n_heads] or NULL.
- *           Rows of no sequence are left alone.
+ *           Rows of no sequence are left alone.  out and lse overlap no input.
  * Products have bf16 (f32 inputs: f16) operands, to which the probabilities are rounded, and f32
  * sums; maxima and denominators are f32.  f16 probabilities below 2^-21 of a query's largest one are off by
  * up to 2^-32 of that (beside values whose row's largest magnitude lies outside 2^-4 .. 2^6, a probability counts
@@ -629,8 +629,9 @@ int coli_gqa_read(const coli_gqa_cache *cache, const int32_t *pages, int64_t pag
  *   q       device [n_seq][n_q][n_heads][dim], COLI_F32 or COLI_BF16 (dtype_q).
  *   pages   as in coli_mla_read; lens[b] <= pages_stride * page_size and <= 2^30.
  *   lens    device int32 [n_seq], >= 0.
- *   out     device [n_seq][n_q][n_heads][dim], COLI_F32 or COLI_BF16.
- *   lse     device f32 [n_seq][n_q][n_heads], or NULL.
+ *   out     device [n_seq][n_q][n_heads][dim], COLI_F32 or COLI_BF16; it may be q itself where the types
+ *           are the same and weigh is 0, and overlaps no input otherwise.
+ *   lse     device f32 [n_seq][n_q][n_heads], or NULL; overlaps no input.
  * The key product takes codes as they are and q in f16, scaled by a power of two
  * per query row: a bf16 element is exact down to 2^-32 of the row's largest
  * magnitude, an f32 one is rounded to 11 bits.  For the value product each
