@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (tok < len && i + lane / plan.boxes < mine) {
                     const int p = tok / a.c.page, id = pages[p];
                     if (id < 0 || id >= a.c.n_pages) mla_bad_index(a.err);   // the cache's first rows instead: the output is unspecified
-                    else first_row = (int)gqa_row(a.c, id, h) + tok - p * a.c.page;
+                    else first_row = (int)gqa_row(a.c, id, h) + (tok - p * a.c.page);   // rows < 2^31, a row plus a token need not be
                 }
             };
             auto ask = [&](int i, int stage) {           // whole warp

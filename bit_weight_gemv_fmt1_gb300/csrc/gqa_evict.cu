@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(256, 6) gqa_move_kernel(const GqaEvictArgs a) 
         if (from < 0 || from >= a.c.n_pages || to < 0 || to >= a.c.n_pages) {
             mla_bad_index(a.err);
         } else {
-            s = (int)gqa_row(a.c, from, h) + t - sp * a.c.page;
-            d = (int)gqa_row(a.c, to, h) + i - dp * a.c.page;
+            s = (int)gqa_row(a.c, from, h) + (t - sp * a.c.page);   // rows < 2^31, a row plus a token need not be
+            d = (int)gqa_row(a.c, to, h) + (i - dp * a.c.page);
         }
     }
     // keys, then values: half the registers of both at once, and more warps
