@@ -26,13 +26,13 @@
 // to 700 behind 333 cached 46, 24 of up to 301 (D 64) 17.
 //
 // f32 inputs become f16, which keeps 3 bits more than bf16: every row (token and head) of q, k and v times a power of two that follows
-// from that row alone, so that what a query does not see cannot change its result.  Rows of ordinary size (the largest magnitude of a
-// key in 2^-5 .. 2^11, of a value in 2^-4 .. 2^6) share one; others get the one that takes their largest magnitude to 2^14 .. 2^15.  The
-// powers come out again by a factor of the scores, a thread's own for q, and two factors per key, which every softmax warp copies to
+// from that row alone, so that what a query does not see cannot change its result.  Keys of ordinary size (the largest magnitude in
+// 2^-5 .. 2^11) share one, others and queries get the one that takes their largest magnitude to 2^14 .. 2^15; values whose largest
+// magnitudes lie between the same two of 2^-4, 2^6, 2^16 and so on share one, which takes the upper end to 2^15.  The powers come out again by a factor of the scores, a thread's own for q, and two factors per key, which every softmax warp copies to
 // shared memory a tile ahead: the scores', and that of a key's weight in P, which is f16 then, too.  With U the largest weight times
-// factor of a row so far, P is held times a power of two B that keeps B U in 2^7 .. 2^15; O is rescaled when B moves.  A tile of
-// ordinary rows in a warp whose B are the usual one needs neither multiplication, and the bits are the same: 1x8192, 32 heads on 8, 457 us
-// (D 64: 365), with rows of other sizes 850 (715).  Exponents rather than tf32 operands: those would be twice the bytes in shared memory, which
+// factor of a row so far, P is held times a power of two B that keeps B U in 100 .. 2^15; O is rescaled when B moves.  A tile of
+// ordinary keys and values of one size, 1 / B, needs neither multiplication, and the bits are the same: 1x8192, 32 heads on 8, 453 us
+// (D 64: 369), with values of many sizes 769 (621), keys, too, 869 (743).  Exponents rather than tf32 operands: those would be twice the bytes in shared memory, which
 // two query tiles of 128 dims fill, and twice the products' cycles.  24 short prompts 24 us, one launch of
 // which makes f16 (7.7 us by the profiler, its inputs from DRAM).
 //
@@ -54,11 +54,11 @@ constexpr uint32_t kOut = 32 * 64;       // bytes of a warp's outputs on their w
 constexpr float kLog2e = 1.4426950408889634f;
 // f16 inputs made from f32, log2 of their powers: those of ordinary keys and values, and shifts of the factors that are kept, so that these
 // and their products with scores (up to 2^37) and weights (up to 2^15) are numbers for rows of any size.
-constexpr int kKeyPower = 4, kValuePower = 9, kKeyShift = 32, kValueShift = 4;
+constexpr int kKeyPower = 4, kValuePower = 9, kKeyShift = 32, kValueShift = 10;
 constexpr int kUp = 7;                   // log2 of what f16 weights are held times
-constexpr int kUsual = kValueShift + kValuePower, kMostUp = 126;   // log2 of B for ordinary values, and at the most
-// A key's factors are two bf16 in a word, its scores' in the low half: powers of two, of ordinary rows these.
-constexpr uint32_t kPlain = (uint32_t)(127 - kUsual) << 23 | (uint32_t)(127 - kKeyShift) << 7;
+constexpr int kMostUp = 126;             // log2 of B at the most
+// A key's factors are two bf16 in a word, its scores' in the low half: powers of two, an ordinary key's this one.
+constexpr uint32_t kPlainKey = (uint32_t)(127 - kKeyShift) << 7;
 
 struct Shared {
     uint64_t q_full[2], q_empty[2], k_full[kKeys], k_empty[kKeys], v_full[kValues], v_empty[kValues], s_full[2], p_full[2][2], o_full[2],
@@ -297,20 +297,28 @@ __global__ void __launch_bounds__(384, 1)
             if (F16 && nt > 0) fetch(0);
             float m = kNone;
             float share = 0.f;                           // U
-            int up = kUsual;                             // log2 B
+            int up = 0;                                  // log2 B
             float l4[4] = {0.f, 0.f, 0.f, 0.f};
             for (int j = 0; j < nt; j++) {
-                bool plain = true;                       // the tile's keys and values are ordinary rows
+                bool keys_plain = true, plain = true;    // ordinary keys; and every value's factor is 1 / B
                 if constexpr (F16) {
                     copies_done();
                     __syncwarp();                        // every lane's have come, and the last tile's factors are read
+                    if (j == 0) up = 127 - (int)(power[0][0] >> 23);   // the first key, which all rows that see any see
+                    const int up0 = __shfl_sync(0xffffffffu, up, 0);
+                    plain = up == up0;
 #pragma unroll
-                    for (int i = 0; i < kRows; i += 32)
-                        plain = plain && (j * kRows + i + lane >= nk || power[j & 1][i + lane] == kPlain);
-                    plain = __all_sync(0xffffffffu, plain && up == kUsual);
+                    for (int i = 0; i < kRows; i += 32) {
+                        const uint32_t w = power[j & 1][i + lane];
+                        const bool none = j * kRows + i + lane >= nk;
+                        keys_plain = keys_plain && (none || (w & 0xFFFFu) == kPlainKey);
+                        plain = plain && (none || w == ((uint32_t)(127 - up0) << 23 | kPlainKey));
+                    }
+                    keys_plain = __all_sync(0xffffffffu, keys_plain);
+                    plain = __all_sync(0xffffffffu, plain);
                     if (j + 1 < nt) fetch(j + 1);
                 }
-                const float ft = F16 && !plain ? f * exp2i(kKeyShift) : f;
+                const float ft = F16 && !keys_plain ? f * exp2i(kKeyShift) : f;
                 wait(&s.s_full[x], s_tiles++ & 1);
                 tc_after_sync();
                 const int k0 = j * kRows;
@@ -324,7 +332,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (negative)
 #pragma unroll
                     for (int c = 0; c < kRows; c++) v[c] ^= 0x80000000u;
-                if (F16 && !plain)
+                if (F16 && !keys_plain)
 #pragma unroll
                     for (int c = 0; c < kRows; c += 4) {
                         const uint4 w = *reinterpret_cast<const uint4 *>(&power[j & 1][c]);
@@ -391,7 +399,7 @@ __global__ void __launch_bounds__(384, 1)
                 const float m0 = (F16 ? (float)kUp : 0.f) - m;
                 if constexpr (F16) share *= r;
                 if (F16 && plain) {
-                    share = fmaxf(share, ex2(now + m0) * exp2i(-kUsual));
+                    share = fmaxf(share, ex2(now + m0) * exp2i(-up));
                 } else if constexpr (F16) {
                     // weights, times their keys' factors, times B
                     float u4[2] = {0.f, 0.f};
@@ -418,8 +426,9 @@ __global__ void __launch_bounds__(384, 1)
                             }
                     share = max3(share, u4[0], u4[1]);
                     const float held = share * exp2i(up);
-                    // an exponent field of 0 gives more than kMostUp, the largest one (2^15 times 2^109) -114
-                    const int next = share > 0.f && (held > 32768.f || held < 128.f) ? min(kMostUp, 10 + 127 - (int)(__float_as_uint(share) >> 23)) : up;
+                    // to about 2^7, which for values of one size is 1 / their factor (2^7 less an ulp, too); an exponent field of 0
+                    // gives more than kMostUp, the largest one (2^15 times 2^111) -119
+                    const int next = share > 0.f && (held > 32768.f || held < 100.f) ? min(kMostUp, kUp + 127 - (int)(__float_as_uint(share * 1.5f) >> 23)) : up;
                     if (__any_sync(0xffffffffu, next != up) && j > 0) rescale(exp2i(max(-126, min(next - up, 126))));   // past that O is 0, or next to it
                     up = next;
                     const float by = exp2i(up);
@@ -491,7 +500,7 @@ __global__ void __launch_bounds__(384, 1)
                 __syncwarp();
             };
             const uint32_t some = limit > 0 ? 0xFFFFFFFFu : 0u;   // a row without keys beside ones that have some: 0 times their values may be NaN
-            const float down = exp2i(kValueShift - up);  // what P and the values are held times, taken back
+            const float out_inv = F16 ? inv * exp2i(kValueShift) : inv, down = exp2i(-up);   // what P and the values are held times, taken back
             float odd = 0.f;                             // NaN once an output is not finite
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
@@ -504,7 +513,7 @@ __global__ void __launch_bounds__(384, 1)
                     for (int c = 0; c < 32; c++) o[c] = 0u;
                 }
 #pragma unroll
-                for (int c = 0; c < 32; c++) o[c] = __float_as_uint(F16 ? __uint_as_float(o[c]) * inv * down : __uint_as_float(o[c]) * inv) & some;
+                for (int c = 0; c < 32; c++) o[c] = __float_as_uint(F16 ? __uint_as_float(o[c]) * out_inv * down : __uint_as_float(o[c]) * inv) & some;
 #pragma unroll
                 for (int c = 0; c < 32; c++) odd = fmaf(__uint_as_float(o[c]), 0.f, odd);
                 uint32_t w[16];
@@ -723,10 +732,10 @@ __global__ void __launch_bounds__(256) gqa_round_kernel(const GqaPrefillArgs a, 
 #pragma unroll
         for (int o = 1; o < kUnits; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (r >= rows) continue;
-        const int size = m ? ilogbf(__uint_as_float(m)) : 0;
-        int e = min(14 - size, query ? most_q : value ? most_v : most_k);
+        const int size = m ? (int)(m >> 23) - 127 : 0;   // below 2^-126 any small number will do
+        int e = min(14 - size, query ? most_q : most_k);
         if (!query && !value && size >= -5 && size <= 10) e = kKeyPower;
-        if (value && size >= -4 && size <= 5) e = kValuePower;
+        if (value) e = min(kValuePower - 10 * ((size + 204) / 10 - 20), most_v);
         const float by = query && a.scale == 0.f ? 0.f : exp2i(e);
         if (u == 0) {
             if (query) q_power[i] = exp2i(-e);

@@ -570,11 +570,11 @@ typedef struct {
  *           Rows of no sequence are left alone.  out and lse overlap no input.
  * Products have bf16 (f32 inputs: f16) operands, to which the probabilities are rounded, and f32
  * sums; maxima and denominators are f32.  f16 probabilities below 2^-21 of a query's largest one are off by
- * up to 2^-32 of that (beside values whose row's largest magnitude lies outside 2^-4 .. 2^6, a probability counts
- * times that magnitude, or 2^6, and is off by up to 2^-31 of the largest such product).  A key or value that a
- * query does not see, of another sequence or its own, may be anything, NaN included; what is finite there changes
- * no bit of the output.  A NaN or an infinity in a query, a NaN in a key that it sees, or scores that are
- * all -infinity make its row NaN.
+ * up to 2^-31 of that, where the magnitudes of the values' rows (the largest of each) lie between the same two
+ * of 2^-4, 2^6, 2^16 and so on either way; else it is the products of probabilities and the upper of these two that
+ * are.  A key or value that a query does not see, of another sequence or its own, may be anything, NaN included;
+ * what is finite there changes no bit of the output.  A NaN or an infinity in a query, a NaN in a key that it
+ * sees, or scores that are all -infinity make its row NaN.
  * Pointers 16-byte aligned (cu, lse: 4); strides in elements, multiples of 8.
  * dim 64 or 128; n_heads a multiple of n_kv, n_heads / n_kv <= 128.  Tq, Tk >= 0, n_seq >= 0,
  * 1 <= n_heads <= 1024.  Offsets outside [0, Tq] / [0, Tk] or descending are

@@ -2,14 +2,15 @@
 what a query does not see: whatever it holds, no bit of the query's output changes.
 
 Tolerance.  An element of q, k or v becomes f16 with its row's power of two: off by u = 2^-11 of itself, or, where it is small, by half an
-f16 step of 2^-24: 2^-39 of the row's largest magnitude, which goes to 2^14 .. 2^15, or 2^-29 for a key's row of ordinary size (its largest
-magnitude in 2^-5 .. 2^11; a power of 2^4) and 2^-34 for a value's (2^-4 .. 2^6; 2^9).  A score s_ij = scale q_i . k_j is then off by at most
+f16 step of 2^-24: 2^-39 of the row's largest magnitude, which goes to 2^14 .. 2^15; 2^-29 for a key's row of ordinary size (its largest
+magnitude in 2^-5 .. 2^11; a power of 2^4); 2^-40 size for a value's, size the upper end of the place of its largest magnitude between
+2^-4, 2^6, 2^16 and so on, which goes to 2^15.  A score s_ij = scale q_i . k_j is then off by at most
     d_ij = scale ((2 u + u^2 + 128 x 2^-24) sum |q| |k| + sum (|q| of k's small step, |k| of q's)),
 the third term for the f32 sum of up to 128 products.  With e^d weights around, out' - out = sum p_j (e^(delta_j) - 1) (v_j - out) /
 sum p_j e^(delta_j), at most e^(max d) sum p_j (e^(d_j) - 1) |v_j - out|.  Values and probabilities are off by u each: 2 u + u^2 of
 sum p |v|; exp, sums and the division by 1e-4 of it.  Small f16 weights of the product are off by half a step of 2^-24.  They are
-p_j size_j times something that takes the largest of a query's to 2^7 or more, size_j a power of two at most twice the largest magnitude of the
-value's row, for ordinary ones 64: n 2^-25 2^-7 of the largest p size, twice for the power's place."""
+p_j size_j times something that takes the largest of a query's to 100 or more, with values of 2^15 |v_j| / size_j: n 2^-25 / 100 of the largest
+p size, less than n 2^-31."""
 import math
 
 import pytest
@@ -69,9 +70,9 @@ def definition(torch, q, k, v, cu_q, cu_k, scale):
             for i in range(0, n, 16):
                 move[i:i + 16] = (w[i:i + 16, :, None] * (z[None] - o[i:i + 16, None]).abs()).sum(1)
             out[q0:q1, h] = o
-            step = small(torch, z, 2.0 ** -4, 2.0 ** 6, 2.0 ** -34)
-            size = torch.where(step == 2.0 ** -34, 64.0, z.abs().amax(-1))
-            tol[q0:q1, h] = most * move + (2 * U + U * U + 1e-4) * (p @ z.abs()) + (p @ step)[:, None] + m * 2.0 ** -31 * (p * size).amax(-1, keepdim=True)
+            size = z.abs().amax(-1)
+            size = torch.where(size == 0, 64.0, 2.0 ** (6 + 10 * ((size.log2().floor() + 4) / 10).floor()))
+            tol[q0:q1, h] = most * move + (2 * U + U * U + 1e-4) * (p @ z.abs()) + 2.0 ** -40 * (p @ size)[:, None] + m * 2.0 ** -31 * (p * size).amax(-1, keepdim=True)
             lse[q0:q1, h] = torch.logsumexp(a, -1)
             lse_tol[q0:q1, h] = d.amax(-1) + 1e-5 * (1 + a.masked_fill(~seen, 0).abs().amax(-1))
     return out, tol, lse, lse_tol
@@ -188,3 +189,23 @@ def test_large_values_that_are_seen(dim):
     got = call(torch, coli, q, k, v, [0, 200], [0, 200], 0.1).double()
     ref, tol, *_ = definition(torch, q, k, v, [0, 200], [0, 200], 0.1)
     assert torch.isfinite(got).all() and ((got - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("size", [-70, -37, -9, 12, 31, 90])
+def test_values_of_another_size_beside_junk(size):
+    """Values that are all large or all small, ordinary ones in between, junk where nobody looks: the same bits, the definition's values."""
+    torch, coli = setup()
+    g = gen(torch, 17)
+    q, kv = packed_qkv(torch, [300, 20], [500, 20], 4, 1, 64, g, torch.float32)
+    k, v = kv[:, :1].contiguous(), kv[:, 1:2] * 2.0 ** size
+    v[100:200] *= 2.0 ** -size                            # a few tiles of ordinary ones
+    want = call(torch, coli, q, k, v, [0, 300, 320], [0, 500, 520], 0.1)
+    ref, tol, *_ = definition(torch, q, k, v, [0, 300, 320], [0, 500, 520], 0.1)
+    assert ((want.double() - ref).abs() <= tol).all()
+    for junk in JUNK:
+        v2, k2 = v.clone(), k.clone()
+        k2[450:500], k2[510:] = junk, junk
+        if math.isfinite(junk):
+            v2[450:500], v2[510:] = junk, junk
+        got = call(torch, coli, q, k2, v2, [0, 300, 320], [0, 500, 520], 0.1)
+        assert torch.equal(got[:250], want[:250]) and torch.equal(got[300:310], want[300:310]), junk
