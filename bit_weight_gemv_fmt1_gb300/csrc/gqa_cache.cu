@@ -1,7 +1,8 @@
 // gqa_cache.cu -- writing keys and values into the paged 4-bit cache and reading
-// them back.  Both touch every input and output once and are bound by HBM on
-// long inputs, by launch and two memory round trips on short ones.  16384 tokens x 8 heads of 128, gs 32, in bf16: write 23 us (5.8
-// TB/s, 0.85 of the measured copy rate), read 16.4 us (5.2); 48000 tokens read 45 us (5.6).  8 tokens, both: 3.3 us on the device.
+// them back.  Both touch every input and output once.  16384 tokens x 8 heads of 128, gs 32, inputs and outputs rotated through four sets:
+// write of f32 25 us (153 MB: 6.1 TB/s, 0.90 of the measured copy rate: HBM), of bf16 25 us, too (86 MB: 3.5 TB/s, 0.51: the issue slots,
+// 70 % of them taken, some 17 instructions an element); read to bf16 18 us (4.8 TB/s), to f32 38 (4.1); 48000 tokens to bf16 45 (5.6).
+// Short inputs are bound by launch and two memory round trips: 8 tokens, both, 3.3 us on the device.
 //
 // Group of gs elements: scale = bf16(max|x| / 7), code = clamp(rint(x / scale)).
 // Codes are taken against the scale as it is stored, so its rounding to 8 bits

@@ -23,18 +23,19 @@
 // hand-overs 250), longer than the 1024 of the other tile's products.  P is handed over in halves of 64 keys and the arithmetic on
 // pairs is packed (1x8192, 32 heads on 8: 376 us, 370 with halves, 366 packed, 355 once the next unit is asked for late); half a row per
 // thread, two warps a tile and SM quarter, is slower (384).  1.54 PFLOP/s, 0.80 of the measured bf16 rate; 1x2048 33 us, 6 ragged up
-// to 700 behind 333 cached 46, 24 of up to 301 (D 64) 17.
+// to 700 behind 333 cached 47.
 //
 // f32 inputs become f16, which keeps 3 bits more than bf16: every row (token and head) of q, k and v times a power of two that follows
 // from that row alone, so that what a query does not see cannot change its result.  Keys of ordinary size (the largest magnitude in
 // 2^-5 .. 2^11) share one, others and queries get the one that takes their largest magnitude to 2^14 .. 2^15; values whose largest
-// magnitudes lie between the same two of 2^-4, 2^6, 2^16 and so on share one, which takes the upper end to 2^15.  The powers come out again by a factor of the scores, a thread's own for q, and two factors per key, which every softmax warp copies to
-// shared memory a tile ahead: the scores', and that of a key's weight in P, which is f16 then, too.  With U the largest weight times
-// factor of a row so far, P is held times a power of two B that keeps B U in 100 .. 2^15; O is rescaled when B moves.  A tile of
-// ordinary keys and values of one size, 1 / B, needs neither multiplication, and the bits are the same: 1x8192, 32 heads on 8, 453 us
-// (D 64: 369), with values of many sizes 769 (621), keys, too, 869 (743).  Exponents rather than tf32 operands: those would be twice the bytes in shared memory, which
-// two query tiles of 128 dims fill, and twice the products' cycles.  24 short prompts 24 us, one launch of
-// which makes f16 (7.7 us by the profiler, its inputs from DRAM).
+// magnitudes lie between the same two of 2^-4, 2^6, 2^16 and so on share one, which takes the upper end to 2^15.  The powers come out
+// again by a factor of the scores, a thread's own for q, and two factors per key, which every softmax warp copies to shared memory a
+// tile ahead: the scores', and that of a key's weight in P, which is f16 then, too.  With U the largest weight times factor of a row so
+// far, P is held times a power of two B that keeps B U in 100 .. 2^15; O is rescaled when B moves.  A tile of ordinary keys whose
+// values' factors are all 1 / B needs neither multiplication, and the bits are the same: 1x8192, 32 heads on 8, 453 us (D 64: 369), with
+// values of many sizes 769 (621), keys, too, 869 (743).  Exponents rather than tf32 operands: those would be twice the bytes in
+// shared memory, which two query tiles of 128 dims fill, and twice the products' cycles.  24 prompts of up to 301 tokens (16 heads on 2,
+// D 64) 24 us, with the launch that makes f16 (10 us by the profiler, its inputs from DRAM: 21 MB and what it works out for each row).
 //
 // Keys past a causal row's limit are masked by selection; value rows past the
 // sequence's end belong to its neighbours and are zeroed in shared memory.
@@ -112,10 +113,11 @@ __device__ __forceinline__ float2 operands(uint32_t w) {
 }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
-// Query rows whose last tile holds keys that they do not see: those keys' weights are 0, but 0 times an infinity or a NaN is NaN.  A
+// Query rows whose tiles hold keys that they do not see (up to two tiles: a tile's rows have limits up to 127 apart, whose border with
+// the next keys may lie anywhere): those keys' weights are 0, but 0 times an infinity or a NaN is NaN.  A
 // whole warp calls this after its rows have been stored, for the rows (`mine`) with an output that is not finite: the columns where such a
 // value is among the keys seen .. end - 1 are computed once more from the keys before, 32 at a time, until they are NaN.  (The
-// other tiles are seen by all of a tile's rows.)  Nothing comes here unless a value or a result is not finite; a warp of 32 such rows of
+// tiles before are seen by all of a tile's rows.)  Nothing comes here unless a value or a result is not finite; a warp of 32 such rows of
 // 8192 keys then takes 53 ms, which its unit's limit of waits (2.5 s) leaves room for.
 template <int D, bool F16>
 __device__ __noinline__ void repair(const GqaPrefillArgs &a, bool mine, int orow, int token, int q_head, int head, int krow, int seen, int end,

@@ -563,13 +563,15 @@ typedef struct {
  *   k, v    device [Tk][n_kv][dim], token strides k_stride, v_stride (they may be
  *           parts of one row).
  *   dtype   COLI_BF16, or COLI_F32: the three are then rounded to f16 in scratch first, each row
- *           (token and head) times a power of two that depends on that row alone, so that any range of
- *           magnitudes fits; elements below 2^-13 of their row's largest are off by up to 2^-24 of that.
+ *           (token and head) times a power of two that depends on that row alone, so that magnitudes from
+ *           2^-99 on fit; elements below 2^-13 of their row's largest are off by up to 2^-24 of that.
+ *           |scale| times a query's magnitudes must be below 2^112: past that its row may be NaN.
  *   cu_q, cu_k      device int32 [n_seq + 1], ascending from 0 to Tq / Tk.
  *   out     device [Tq][n_heads][dim], COLI_F32 or COLI_BF16; lse device f32 [Tq][n_heads] or NULL.
  *           Rows of no sequence are left alone.  out and lse overlap no input.
  * Products have bf16 (f32 inputs: f16) operands, to which the probabilities are rounded, and f32
- * sums; maxima and denominators are f32.  f16 probabilities below 2^-21 of a query's largest one are off by
+ * sums; maxima and denominators are f32.  bf16 values times the number of keys must be below 2^120, since
+ * sums hold probabilities times up to 2^8.  f16 probabilities below 2^-21 of a query's largest one are off by
  * up to 2^-31 of that, where the magnitudes of the values' rows (the largest of each) lie between the same two
  * of 2^-4, 2^6, 2^16 and so on either way; else it is the products of probabilities and the upper of these two that
  * are.  A key or value that a query does not see, of another sequence or its own, may be anything, NaN included;
@@ -633,15 +635,17 @@ int coli_gqa_read(const coli_gqa_cache *cache, const int32_t *pages, int64_t pag
  *           are the same and weigh is 0, and overlaps no input otherwise.
  *   lse     device f32 [n_seq][n_q][n_heads], or NULL; overlaps no input.
  * The key product takes codes as they are and q in f16, scaled by a power of two
- * per query row: a bf16 element is exact down to 2^-32 of the row's largest
- * magnitude, an f32 one is rounded to 11 bits.  For the value product each
+ * per query row: a bf16 element is exact down to 2^-27 of the row's largest
+ * magnitude, an f32 one is rounded to 11 bits down to 2^-24 of it.  |scale| times a query's magnitudes must be
+ * below 2^116: past that its row may be NaN.  For the value product each
  * probability, and its product with its row's scale, is rounded to bf16; scales of values from 2^-60 to
  * 2^38 stay within the products' range (values of 1e-17 to 1e12).  Scales are applied and
  * sums, maxima and the denominator held in f32.
  * Rows past a sequence's length, and pages past its last, are never used: they may
  * hold anything.  A NaN or an infinity in a query, or a NaN scale of a key that a query
  * sees, makes its output, lse and weights NaN; a NaN scale of a value that it sees the
- * outputs of that group.
+ * outputs of that group.  Keys that score -infinity (infinite scales, which coli_gqa_append does not write)
+ * count as not seen.
  * Weights of a page that several sequences of the call share are added in no fixed order.
  * Pointers 16-byte aligned (pages, lens, lse: 4).  n_seq >= 0, n_q >= 1, n_heads a multiple of n_kv,
  * 1 <= n_heads <= 1024, n_q * n_heads <= 65536.  A page id outside [0, n_pages) among the needed ones, or a
